@@ -398,6 +398,51 @@ NM_API nm_status nm_sddmm(const uint32_t* meta, int n, int m, int64_t R, int64_t
                           const uint16_t* dY, int64_t lddy, const uint16_t* X, int64_t ldx, int64_t T, void* dV,
                           nm_out_dtype dtype, void* stream);
 
+/* ----------------------------------------------------------- layer norm */
+/*
+ * nm_layer_norm -- layer norm over the K features of each token, in the
+ * layout of the GEMMs, so that its output is the X of nm_spmm:
+ *   mean[t] = sum_k X[k][t] / K,  var[t] = sum_k (X[k][t] - mean[t])^2 / K,
+ *   rstd[t] = 1 / sqrt(var[t] + eps),
+ *   Y[k][t] = (X[k][t] - mean[t]) * rstd[t] * gamma[k] + beta[k].
+ * The pages name the networks (the ViT-B linears) but not this step; it is
+ * what stands in front of their projections.  Statistics and arithmetic are
+ * fp32 (the variance from squares about the mean), Y is rounded once.
+ *   X      [in]  K x T, bf16 or fp32 (x_dtype), row stride ldx >= T, 16-byte rows
+ *   gamma, beta [in] K fp32 each, or NULL for 1 and 0 (either by itself)
+ *   eps    finite, >= 0
+ *   Y      [out] K x T, bf16 or fp32 (y_dtype), row stride ldy >= T, 16-byte
+ *          rows; must not overlap X
+ *   mean, rstd [out, optional] T fp32 each, as nm_layer_norm_grad reads them
+ * One launch, no staging.  K = 0 is refused (there is no mean); T = 0 writes
+ * nothing.
+ * Errors: NM_ERR_INVALID_ARG, NM_ERR_MISALIGNED, NM_ERR_UNSUPPORTED (a
+ * dimension >= 2^31), NM_ERR_CUDA.
+ */
+NM_API nm_status nm_layer_norm(const void* X, int64_t ldx, nm_out_dtype x_dtype, int64_t K, int64_t T,
+                               const float* gamma, const float* beta, float eps, void* Y, int64_t ldy,
+                               nm_out_dtype y_dtype, float* mean, float* rstd, void* stream);
+
+/*
+ * nm_layer_norm_grad -- gradients of nm_layer_norm, with xh = (X - mean) rstd
+ * and g = gamma dY:
+ *   dX = rstd * (g - (sum_k g + xh * sum_k g xh) / K),
+ *   dgamma[k] = sum_t dY[k][t] xh[k][t],  dbeta[k] = sum_t dY[k][t].
+ *   dY     [in]  K x T, bf16 or fp32 (dy_dtype), row stride lddy >= T, 16-byte rows
+ *   X, gamma     as given to nm_layer_norm; mean, rstd as it wrote them
+ *   dX     [out] K x T of X's type, row stride lddx >= T, 16-byte rows; must
+ *          not overlap dY or X
+ *   dgamma, dbeta [out, optional] K fp32 each, overwritten (zeros when T = 0)
+ * With dgamma or dbeta, ceil(T/w)*2*K*4 bytes of row sums (one pair per strip
+ * of w = 8 to 64 tokens) are staged from the library's pool, and a second
+ * launch adds them in a fixed order, so that results repeat bit for bit.
+ * Errors: as nm_layer_norm.
+ */
+NM_API nm_status nm_layer_norm_grad(const void* dY, int64_t lddy, nm_out_dtype dy_dtype, const void* X, int64_t ldx,
+                                    nm_out_dtype x_dtype, int64_t K, int64_t T, const float* gamma,
+                                    const float* mean, const float* rstd, void* dX, int64_t lddx, float* dgamma,
+                                    float* dbeta, void* stream);
+
 /*
  * nm_spmm_algo --nm_spmm / nm_spmm_permuted (idx may be NULL) with the kernel
  * design chosen explicitly, to compare the sparse tensor-core path with the

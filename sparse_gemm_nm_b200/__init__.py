@@ -16,6 +16,7 @@ the same bits).  Matrices are row-major: W is R x K, X is K x T, Y is R x T.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -39,7 +40,7 @@ NM_ALGO_SPARSE_TC = 1
 NM_ALGO_DENSE_TC = 2
 
 # Every symbol include/nm.h declares, with its ctypes signature.
-_P, _I64, _I, _U64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
+_P, _I64, _I, _U64, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64, ctypes.c_float
 SIGNATURES = {
     "nm_index_bits": ([_I], _I),
     "nm_value_cols": ([_I64, _I, _I], _I64),
@@ -61,6 +62,8 @@ SIGNATURES = {
     "nm_decompress_tf32": ([_P, _P, _I64, _I64, _P, _I64, _P], _I),
     "nm_spmm_tf32": ([_P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I, _P], _I),
     "nm_sddmm": ([_P, _I, _I, _I64, _I64, _P, _P, _I64, _P, _I64, _I64, _P, _I, _P], _I),
+    "nm_layer_norm": ([_P, _I64, _I, _I64, _I64, _P, _P, _F, _P, _I64, _I, _P, _P, _P], _I),
+    "nm_layer_norm_grad": ([_P, _I64, _I, _P, _I64, _I, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _P], _I),
     "nm_spmm_algo": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I, _I, _P], _I),
     "nm_spmm_permuted_noalloc": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I, _P], _I),
     "nm_release_staging": ([], _I),
@@ -229,6 +232,19 @@ def nm_diag_spmm(values, offsets, D, R, K, idx, X, ldx, T, Y, ldy, y_dtype=NM_OU
                               y_dtype, _stream(stream)), "nm_diag_spmm")
 
 
+def nm_layer_norm(X, ldx, x_dtype, K, T, gamma, beta, eps, Y, ldy, y_dtype, mean=None, rstd=None,
+                  stream=None) -> None:
+    _check(lib().nm_layer_norm(_ptr(X), ldx, x_dtype, K, T, _ptr(gamma), _ptr(beta), eps, _ptr(Y), ldy, y_dtype,
+                               _ptr(mean), _ptr(rstd), _stream(stream)), "nm_layer_norm")
+
+
+def nm_layer_norm_grad(dY, lddy, dy_dtype, X, ldx, x_dtype, K, T, gamma, mean, rstd, dX, lddx, dgamma=None,
+                       dbeta=None, stream=None) -> None:
+    _check(lib().nm_layer_norm_grad(_ptr(dY), lddy, dy_dtype, _ptr(X), ldx, x_dtype, K, T, _ptr(gamma), _ptr(mean),
+                                    _ptr(rstd), _ptr(dX), lddx, _ptr(dgamma), _ptr(dbeta), _stream(stream)),
+           "nm_layer_norm_grad")
+
+
 def nm_spmm_algo(values, meta, n, m, R, K, idx, X, ldx, T, Y, ldy, y_dtype=NM_OUT_BF16, algo=NM_ALGO_AUTO,
                  stream=None) -> None:
     _check(lib().nm_spmm_algo(_ptr(values), _ptr(meta), n, m, R, K, _ptr(idx), _ptr(X), ldx, T, _ptr(Y), ldy,
@@ -268,6 +284,101 @@ def _require_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
             raise ValueError("tensors must live on a CUDA device")
+
+
+def _same_device(first, *others):
+    """Every tensor is on first's CUDA device."""
+    _require_cuda(first, *others)
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors must share one device, got {first.device} and {t.device}")
+
+
+@contextlib.contextmanager
+def _on(X, stream):
+    """X's device made current and, when given, `stream` too (outputs are then allocated in that stream's order);
+    yields the stream handle for the call."""
+    import torch
+    if stream is None:
+        if X.device.index == torch.cuda.current_device():
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            with torch.cuda.device(X.device):
+                yield torch.cuda.current_stream().cuda_stream
+        return
+    s = torch.cuda.ExternalStream(stream, device=X.device) if isinstance(stream, int) else stream
+    with torch.cuda.device(X.device), torch.cuda.stream(s):
+        yield s.cuda_stream
+
+
+def _rows(X, name: str, *dtypes):
+    """Row stride (elements) of a matrix whose columns are adjacent."""
+    if X.dim() != 2 or X.dtype not in dtypes:
+        raise ValueError(f"{name} must be a matrix of {' or '.join(str(d) for d in dtypes)}, got {X.dim()}-d {X.dtype}")
+    rows, cols = X.shape
+    if cols > 1 and X.stride(1) != 1:
+        raise ValueError(f"{name}: the columns of a row must be adjacent (stride 1), got {X.stride(1)}")
+    return X.stride(0) if rows > 1 else (cols + 7) // 8 * 8
+
+
+def _vector(v, name: str, size: int, dtype):
+    if v is not None and (tuple(v.shape) != (size,) or v.dtype != dtype or not v.is_contiguous()):
+        raise ValueError(f"{name} must be {size} contiguous values of {dtype}, got {tuple(v.shape)} {v.dtype}")
+
+
+def _out_rows(rows: int, cols: int, dtype, device):
+    """rows x cols with rows padded to 16 bytes: (the view, its row stride)."""
+    import torch
+    per = 4 if dtype == torch.float32 else 8
+    ld = max((cols + per - 1) // per * per, per)
+    return torch.empty((rows, ld), dtype=dtype, device=device)[:, :cols], ld
+
+
+def _out_type(dtype):
+    import torch
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"output type must be bfloat16 or float32, got {dtype}")
+    return NM_OUT_F32 if dtype == torch.float32 else NM_OUT_BF16
+
+
+def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, out_dtype=None, stream=None):
+    """(Y, mean, rstd): layer norm over the K features of each token of X (K x T bf16 or float32).
+
+    Y (K x T, X's type unless out_dtype says otherwise) has rows padded to 16 bytes, ready to be the X of spmm;
+    mean and rstd (T float32) are what layer_norm_grad reads.
+    """
+    import torch
+    _same_device(X, gamma, beta)
+    ldx = _rows(X, "X", torch.bfloat16, torch.float32)
+    K, T = X.shape
+    _vector(gamma, "gamma", K, torch.float32)
+    _vector(beta, "beta", K, torch.float32)
+    out_dtype = out_dtype or X.dtype
+    yt = _out_type(out_dtype)
+    with _on(X, stream) as s:
+        Y, ldy = _out_rows(K, T, out_dtype, X.device)
+        stats = torch.empty((2, T), dtype=torch.float32, device=X.device)
+        nm_layer_norm(X, ldx, _out_type(X.dtype), K, T, gamma, beta, eps, Y, ldy, yt, stats[0], stats[1], s)
+    return Y, stats[0], stats[1]
+
+
+def layer_norm_grad(dY, X, mean, rstd, gamma=None, stream=None):
+    """(dX of X's type, dgamma, dbeta float32) of layer_norm, from its input and the mean and rstd it returned."""
+    import torch
+    _same_device(X, dY, mean, rstd, gamma)
+    ldx = _rows(X, "X", torch.bfloat16, torch.float32)
+    lddy = _rows(dY, "dY", torch.bfloat16, torch.float32)
+    if dY.shape != X.shape:
+        raise ValueError(f"dY {tuple(dY.shape)} and X {tuple(X.shape)} differ in shape")
+    K, T = X.shape
+    for v, name, size in ((mean, "mean", T), (rstd, "rstd", T), (gamma, "gamma", K)):
+        _vector(v, name, size, torch.float32)
+    with _on(X, stream) as s:
+        dX, lddx = _out_rows(K, T, X.dtype, X.device)
+        sums = torch.empty((2, K), dtype=torch.float32, device=X.device)
+        nm_layer_norm_grad(dY, lddy, _out_type(dY.dtype), X, ldx, _out_type(X.dtype), K, T, gamma, mean, rstd, dX,
+                           lddx, sums[0], sums[1], s)
+    return dX, sums[0], sums[1]
 
 
 def prune_compress(W, n: int, m: int, stream=None):

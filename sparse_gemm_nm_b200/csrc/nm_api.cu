@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/nm.h"
+#include "nm_host.h"
 #include "nm_internal.h"
 #include "nm_spmm.h"
 
@@ -22,8 +23,7 @@ void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 static thread_local std::string t_last_error;
 
-static nm_status fail(nm_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-static nm_status fail(nm_status s, const char* fmt, ...) {
+nm_status fail(nm_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -33,7 +33,7 @@ static nm_status fail(nm_status s, const char* fmt, ...) {
   return s;
 }
 
-static nm_status cuda_fail(cudaError_t e, const char* what) {
+nm_status cuda_fail(cudaError_t e, const char* what) {
   return fail(NM_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
@@ -63,7 +63,7 @@ int sm_count_current() {
   return d ? d->sms : 148;
 }
 
-static nm_status require_device() {
+nm_status require_device() {
   const DeviceInfo* d = device_info();
   if (!d) return fail(NM_ERR_NO_DEVICE, "no CUDA device is current");
   if (d->major != 10) return fail(NM_ERR_NO_DEVICE, "device is sm_%d0, this library is built for sm_100a", d->major);
@@ -97,7 +97,7 @@ static EncodeTiledFn encode_fn() {
 static std::mutex g_pool_mu;
 static cudaMemPool_t g_pool[64];
 
-static cudaError_t staging_pool(cudaMemPool_t* out) {
+cudaError_t staging_pool(cudaMemPool_t* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -162,9 +162,9 @@ static thread_local TmapCache t_tmaps;
 // swizzle_bytes code of the 128-byte swizzle with 32-byte units (MN-major tf32 operands of the MMA).
 constexpr int kSwizzle128Atom32B = -32;
 
-static nm_status make_tmap(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,
-                           uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, int swizzle_bytes,
-                           const char* what, CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
+nm_status make_tmap(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
+                    uint32_t box_inner, uint32_t box_outer, int swizzle_bytes, const char* what,
+                    CUtensorMapDataType dtype) {
   const TmapKey key{base, inner, outer, 0, row_bytes, 0, box_inner, box_outer, 0, swizzle_bytes, (int)dtype, 2};
   if (t_tmaps.find(key, tm)) return NM_OK;
   EncodeTiledFn fn = encode_fn();
@@ -212,8 +212,6 @@ static nm_status make_meta_tmap(CUtensorMap* tm, const void* meta, int64_t rbloc
   t_tmaps.put(key, *tm);
   return NM_OK;
 }
-
-static bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Tile order of the SM-pair kernel: column tiles fastest when the compressed weights (R x vcols) exceed
 // 1.5x the dense input (K x T; same element size), so that the weights stream from HBM about once.
@@ -999,7 +997,6 @@ static nm_status run_sddmm(const uint32_t* meta, int n, int m, int64_t R, int64_
 
 
 // INT8 2:4 (compress, decompress, GEMM on the decompressed operand).
-static bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 static nm_status check_i8_shape(int64_t R, int64_t K) {
   if (R < 0 || K < 0) return fail(NM_ERR_INVALID_ARG, "negative dimension");

@@ -1,0 +1,67 @@
+// nm_host.h -- host helpers of the C entry points that live in several files
+// (internal): error reporting, the staging pool, tensor maps, argument checks
+// and the GEMM routines that other entry points build on.  Defined in nm_api.cu.
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "../../include/nm.h"
+#include "nm_internal.h"
+#include "nm_spmm.h"
+
+namespace nmk {
+
+// Records the text of nm_last_error() and returns the status.
+nm_status fail(nm_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+nm_status cuda_fail(cudaError_t e, const char* what);
+void set_last_error(const char* msg);
+nm_status require_device();
+cudaError_t staging_pool(cudaMemPool_t* out);
+nm_status make_tmap(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
+                    uint32_t box_inner, uint32_t box_outer, int swizzle_bytes, const char* what,
+                    CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+
+inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool dtype_ok(int d) { return d == NM_OUT_BF16 || d == NM_OUT_F32; }
+inline int64_t dtype_bytes(int d) { return d == NM_OUT_F32 ? 4 : 2; }
+constexpr int64_t kMaxDim = 1ll << 31;
+
+// A strided matrix of rows x T elements: pointer set, row stride at least T, rows on 16 bytes.
+inline nm_status check_matrix(const void* p, int64_t ld, int64_t T, int64_t esize, const char* name) {
+  if (!p) return fail(NM_ERR_INVALID_ARG, "%s is null", name);
+  if (ld < T) return fail(NM_ERR_INVALID_ARG, "ld of %s < T", name);
+  if (!al16(p) || (ld * esize) % 16 != 0) return fail(NM_ERR_MISALIGNED, "%s rows must be 16-byte aligned", name);
+  return NM_OK;
+}
+
+// A staging buffer from the library's pool, handed back on its stream when it goes out of scope.
+class Staged {
+ public:
+  explicit Staged(cudaStream_t s) : stream_(s) {}
+  ~Staged() { release(); }
+  Staged(const Staged&) = delete;
+  Staged& operator=(const Staged&) = delete;
+  cudaError_t get(size_t bytes) {
+    cudaMemPool_t pool = nullptr;
+    cudaError_t e = staging_pool(&pool);
+    if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&p_, bytes, pool, stream_);
+    if (e != cudaSuccess) p_ = nullptr;
+    return e;
+  }
+  void release() {
+    if (p_) cudaFreeAsync(p_, stream_);
+    p_ = nullptr;
+  }
+  template <typename T>
+  T* as() const {
+    return static_cast<T*>(p_);
+  }
+
+ private:
+  cudaStream_t stream_;
+  void* p_ = nullptr;
+};
+
+}  // namespace nmk

@@ -116,3 +116,28 @@ def test_host_argument_checks_of_the_format_calls(lib):
     assert L.nm_diag_spmm(None, None, 2, 4, 8, None, None, 8, 8, None, 4, 0, None) == I  # ldy < T
     assert L.nm_prune_compress_i8(None, 4, 16, 8, None, None, None) == I           # ldw < K
     assert L.nm_spmm_i8(None, None, 4, 16, None, 16, 16, None, 8, None) == I       # ldy < T
+
+
+def test_host_argument_checks_of_layer_norm(lib):
+    """Refused before any launch: sizes, types, eps, nulls, strides and alignment."""
+    L, I = lib, nm.NM_ERR_INVALID_ARG
+
+    def fwd(X=16, ldx=8, xt=0, K=4, T=8, eps=1e-5, Y=16, ldy=8, yt=0):
+        return L.nm_layer_norm(X, ldx, xt, K, T, None, None, eps, Y, ldy, yt, None, None, None)
+
+    def bwd(dY=16, lddy=8, dt=0, X=16, ldx=8, xt=0, K=4, T=8, mean=16, rstd=16, dX=16, lddx=8):
+        return L.nm_layer_norm_grad(dY, lddy, dt, X, ldx, xt, K, T, None, mean, rstd, dX, lddx, None, None, None)
+
+    for bad in (dict(K=-1), dict(T=-1), dict(K=0), dict(xt=2), dict(yt=-1), dict(eps=-1.0), dict(eps=float("nan")),
+                dict(eps=float("inf")), dict(X=None), dict(Y=None), dict(ldx=7), dict(ldy=7)):
+        assert fwd(**bad) == I, bad
+    for bad in (dict(X=8), dict(Y=2), dict(ldx=12), dict(ldy=9), dict(xt=1, ldx=9)):
+        assert fwd(**bad) == nm.NM_ERR_MISALIGNED, bad
+    assert fwd(K=1 << 31) == fwd(T=1 << 31) == nm.NM_ERR_UNSUPPORTED
+    assert fwd(T=0) == nm.NM_OK
+    for bad in (dict(K=-1), dict(T=-1), dict(K=0), dict(xt=2), dict(dt=9), dict(X=None), dict(dY=None),
+                dict(dX=None), dict(mean=None), dict(rstd=None), dict(lddy=7), dict(ldx=7), dict(lddx=7)):
+        assert bwd(**bad) == I, bad
+    for bad in (dict(dY=8), dict(X=8), dict(dX=8), dict(lddy=12), dict(lddx=12)):
+        assert bwd(**bad) == nm.NM_ERR_MISALIGNED, bad
+    assert bwd(T=0) == nm.NM_OK

@@ -1,0 +1,36 @@
+"""64-bit definitions of the operators around a pruned projection, for the GPU parity tests.
+
+Plain torch.float64 on the CPU, written from the formulas; gradients come from
+autograd on these definitions, so that a gradient kernel is checked against
+the derivative of the forward formula and not against a copy of its own.
+"""
+import torch
+
+U32 = 2.0 ** -24    # half a step of float32
+UBF16 = 2.0 ** -8   # half a step of bf16
+
+
+def layer_norm(x, gamma=None, beta=None, eps=1e-5):
+    """(y, mean, rstd) over dim 0 of x (features x tokens, float64)."""
+    mean = x.mean(0)
+    rstd = 1.0 / torch.sqrt(((x - mean) ** 2).mean(0) + eps)
+    y = (x - mean) * rstd
+    if gamma is not None:
+        y = y * gamma[:, None]
+    if beta is not None:
+        y = y + beta[:, None]
+    return y, mean, rstd
+
+
+def layer_norm_grad(dy, x, gamma=None, beta=None, eps=1e-5):
+    """(dx, dgamma, dbeta) by autograd; gamma and beta default to ones and zeros."""
+    K = x.shape[0]
+    x = x.detach().clone().requires_grad_()
+    g = (torch.ones(K, dtype=torch.float64) if gamma is None else gamma.detach().clone()).requires_grad_()
+    b = (torch.zeros(K, dtype=torch.float64) if beta is None else beta.detach().clone()).requires_grad_()
+    return torch.autograd.grad(layer_norm(x, g, b, eps)[0], (x, g, b), dy)
+
+
+def chain(n):
+    """Relative bound of a float32 sum whose longest chain has n additions: n u / (1 - n u)."""
+    return n * U32 / (1 - n * U32)
