@@ -300,11 +300,12 @@ def _on(X, stream):
     yields the stream handle for the call."""
     import torch
     if stream is None:
-        if X.device.index == torch.cuda.current_device():
-            yield torch.cuda.current_stream().cuda_stream
+        at = X.device.index
+        if at == torch.cuda.current_device():
+            yield torch.cuda.current_stream(at).cuda_stream
         else:
-            with torch.cuda.device(X.device):
-                yield torch.cuda.current_stream().cuda_stream
+            with torch.cuda.device(at):
+                yield torch.cuda.current_stream(at).cuda_stream
         return
     s = torch.cuda.ExternalStream(stream, device=X.device) if isinstance(stream, int) else stream
     with torch.cuda.device(X.device), torch.cuda.stream(s):

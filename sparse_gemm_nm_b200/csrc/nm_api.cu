@@ -109,10 +109,17 @@ cudaError_t staging_pool(cudaMemPool_t* out) {
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
     cudaMemPool_t pool = nullptr;
+    // The pool is made at the first call that stages; that call may be under a stream capture, which
+    // refuses pool creation in the capturing thread unless its capture mode is relaxed meanwhile.
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
     e = cudaMemPoolCreate(&pool, &props);
-    if (e != cudaSuccess) return e;
     uint64_t keep = ~0ull;
-    e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    cudaError_t set = e;
+    if (e == cudaSuccess) set = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    e = set;
     if (e != cudaSuccess) {
       cudaMemPoolDestroy(pool);
       return e;

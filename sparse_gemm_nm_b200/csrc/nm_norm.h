@@ -1,11 +1,13 @@
 // nm_norm.h -- parameter block and launchers of the layer norm kernels (internal).
 #pragma once
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace nmk {
 
 struct NormParams {
+  CUtensorMap tm_x, tm_d;  // cached: X and dY in boxes of one strip
   const void* X;
   int64_t ldx;
   const void* dY;  // backward
@@ -17,16 +19,17 @@ struct NormParams {
   float eps;
   float *mean, *rstd;  // forward: outputs (may be null); backward: inputs
   float* part;         // backward: tiles x 2 x K row sums (dgamma, dbeta), or null
+  uint32_t* status;
   int x_f32, y_f32;    // type of X (and dX), type of Y (forward) or dY (backward)
-  // set by the launcher
-  int lpr, cluster;
-  int64_t tiles;
+  // set by norm_shape
+  int lpr, cluster, cached;
+  int64_t tiles, rows;  // strips; rows of a CTA's slab
+  uint32_t smem;
 };
 
-cudaError_t launch_norm(NormParams& p, cudaStream_t s);
-// Fills p.lpr, p.cluster and p.tiles (the rows of p.part) and the rows per thread.
-void norm_grad_shape(NormParams& p, int* rpt);
-cudaError_t launch_norm_grad(NormParams& p, int rpt, cudaStream_t s);
+void norm_shape(NormParams& p, int64_t bytes);
+cudaError_t launch_norm(const NormParams& p, cudaStream_t s);
+cudaError_t launch_norm_grad(const NormParams& p, cudaStream_t s);
 cudaError_t launch_norm_grad_reduce(const float* part, int64_t tiles, int64_t K, float* dgamma, float* dbeta,
                                     cudaStream_t s);
 

@@ -17,10 +17,10 @@ pytestmark = pytest.mark.gpu
 
 BF, F32 = torch.bfloat16, torch.float32
 
-# (K, T): one token, one feature, ragged strips, every strip width, the register limits of the kernel (rows a
-# thread keeps times the threads of a cluster) and K past them, where the strip is read again
+# (K, T): one token, one feature, ragged strips, every strip width and cluster size, slabs above a quarter of an SM,
+# and a K too large for a cluster's shared memory, where the strip is read again in every pass
 SHAPES = [(1, 1), (5, 1), (1, 9), (24, 17), (768, 197), (257, 64), (4096, 40), (5120, 16), (4097, 72), (8200, 33),
-          (33000, 9), (9, 5000)]
+          (33000, 9), (9, 5000), (500, 20000), (40000, 50), (113000, 3)]
 
 
 def rows(A, dtype):
@@ -135,7 +135,7 @@ def test_equal_features_give_beta():
     assert torch.equal(y, beta[:, None].expand(512, 24)) and torch.equal(mean, torch.full((24,), 0.75, device=DEV))
 
 
-@pytest.mark.parametrize("K,T", [(768, 100), (33000, 9), (40, 3)])
+@pytest.mark.parametrize("K,T", [(768, 100), (113000, 9), (40, 3)])
 def test_a_bad_token_stays_alone(K, T):
     """NaN and Inf of one token reach no other token's output."""
     x, gamma, beta = case(K, T, BF)
