@@ -443,6 +443,51 @@ NM_API nm_status nm_layer_norm_grad(const void* dY, int64_t lddy, nm_out_dtype d
                                     const float* mean, const float* rstd, void* dX, int64_t lddx, float* dgamma,
                                     float* dbeta, void* stream);
 
+/* -------------------------------------------------------- cross entropy */
+/*
+ * nm_spmm_xent -- softmax cross entropy of a pruned output head: with the
+ * logits z = (W' Pi) X (R rows, the vocabulary or classes; R x T),
+ *   lse[t]  = log sum_v exp(z[v][t]),
+ *   loss[t] = lse[t] - z[target[t]][t], and 0 where target[t] is outside
+ *             [0, R) (a token without a loss; its lse is still written).
+ * The logits are never all in memory: the vocabulary is taken in pieces of
+ * rows, and every 256 rows leave one (max, sum of exponentials) pair per token.
+ * The pages train and fine-tune pruned networks without giving this step; it
+ * is the loss behind the last projection.  Logits, exponentials and sums are fp32.
+ *   values, meta, n, m, idx, X  as nm_spmm_permuted (idx may be NULL); R, K >= 1
+ *   target    [in]  T int32
+ *   loss, lse [out] T fp32 each
+ * Staged from the library's pool: 8 bytes per token and 256 rows of W, and a
+ * piece of fp32 logits (at most 8192 rows, about 64 MB; 256 rows at least),
+ * Xp with idx, and what nm_spmm stages for a piece.
+ * Errors: as nm_spmm_permuted.
+ */
+NM_API nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                              const int32_t* idx, const uint16_t* X, int64_t ldx, int64_t T, const int32_t* target,
+                              float* loss, float* lse, void* stream);
+
+/*
+ * nm_spmm_xent_grad -- gradients of sum_t dloss[t] loss[t]: with
+ *   G[v][t] = dloss[t] (exp(z[v][t] - lse[t]) - [v == target[t]])
+ * (0 for a token without a loss), dX = (W' Pi)^T G as nm_spmm_t gives it and
+ * dV = the survivors' entries of G Xp^T as nm_sddmm gives them.  The logits
+ * of a piece of the vocabulary are computed again; G is rounded to bf16, as
+ * the dY of those calls is; dX adds up in fp32 over the pieces.
+ *   target, lse, dloss [in] T each (int32, fp32, fp32); lse from nm_spmm_xent
+ *   dX  [out] K x T bf16, row stride lddx >= T, 16-byte rows, or NULL.  With
+ *       idx, rows as in nm_spmm_t (repeated entries are not supported, rows
+ *       that no entry names are not written)
+ *   dV  [out] R x nm_value_cols(K,n,m) bf16, or NULL (a frozen head); not both
+ * Results repeat bit for bit.  Staged from the library's pool: a piece of
+ * logits and of G, and with dX the piece's decompressed weights and a K x T
+ * fp32 accumulator.
+ * Errors: as nm_spmm_t.
+ */
+NM_API nm_status nm_spmm_xent_grad(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                                   const int32_t* idx, const uint16_t* X, int64_t ldx, int64_t T,
+                                   const int32_t* target, const float* lse, const float* dloss, uint16_t* dX,
+                                   int64_t lddx, uint16_t* dV, void* stream);
+
 /*
  * nm_spmm_algo --nm_spmm / nm_spmm_permuted (idx may be NULL) with the kernel
  * design chosen explicitly, to compare the sparse tensor-core path with the

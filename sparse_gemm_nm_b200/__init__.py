@@ -64,6 +64,8 @@ SIGNATURES = {
     "nm_sddmm": ([_P, _I, _I, _I64, _I64, _P, _P, _I64, _P, _I64, _I64, _P, _I, _P], _I),
     "nm_layer_norm": ([_P, _I64, _I, _I64, _I64, _P, _P, _F, _P, _I64, _I, _P, _P, _P], _I),
     "nm_layer_norm_grad": ([_P, _I64, _I, _P, _I64, _I, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _P], _I),
+    "nm_spmm_xent": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P], _I),
+    "nm_spmm_xent_grad": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P], _I),
     "nm_spmm_algo": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I, _I, _P], _I),
     "nm_spmm_permuted_noalloc": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I, _P], _I),
     "nm_release_staging": ([], _I),
@@ -245,6 +247,18 @@ def nm_layer_norm_grad(dY, lddy, dy_dtype, X, ldx, x_dtype, K, T, gamma, mean, r
            "nm_layer_norm_grad")
 
 
+def nm_spmm_xent(values, meta, n, m, R, K, idx, X, ldx, T, target, loss, lse, stream=None) -> None:
+    _check(lib().nm_spmm_xent(_ptr(values), _ptr(meta), n, m, R, K, _ptr(idx), _ptr(X), ldx, T, _ptr(target),
+                              _ptr(loss), _ptr(lse), _stream(stream)), "nm_spmm_xent")
+
+
+def nm_spmm_xent_grad(values, meta, n, m, R, K, idx, X, ldx, T, target, lse, dloss, dX, lddx, dV=None,
+                      stream=None) -> None:
+    _check(lib().nm_spmm_xent_grad(_ptr(values), _ptr(meta), n, m, R, K, _ptr(idx), _ptr(X), ldx, T, _ptr(target),
+                                   _ptr(lse), _ptr(dloss), _ptr(dX), lddx, _ptr(dV), _stream(stream)),
+           "nm_spmm_xent_grad")
+
+
 def nm_spmm_algo(values, meta, n, m, R, K, idx, X, ldx, T, Y, ldy, y_dtype=NM_OUT_BF16, algo=NM_ALGO_AUTO,
                  stream=None) -> None:
     _check(lib().nm_spmm_algo(_ptr(values), _ptr(meta), n, m, R, K, _ptr(idx), _ptr(X), ldx, T, _ptr(Y), ldy,
@@ -380,6 +394,67 @@ def layer_norm_grad(dY, X, mean, rstd, gamma=None, stream=None):
         nm_layer_norm_grad(dY, lddy, _out_type(dY.dtype), X, ldx, _out_type(X.dtype), K, T, gamma, mean, rstd, dX,
                            lddx, sums[0], sums[1], s)
     return dX, sums[0], sums[1]
+
+
+def _compressed(values, meta, n: int, m: int, K: int, idx=None) -> int:
+    """Checks a compressed R x K operand (and its index map) and returns R."""
+    import torch
+    if values.dim() != 2 or values.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise ValueError(f"values must be a matrix of bfloat16, got {values.dim()}-d {values.dtype}")
+    R = values.shape[0]
+    cols = nm_value_cols(K, n, m)
+    if cols < 0:  # let the library name the bad argument
+        _check(lib().nm_prune_compress(None, R, K, K, n, m, None, None, None), "nm_prune_compress")
+    if values.shape[1] != cols or not values.is_contiguous():
+        raise ValueError(f"values must be {R} x {cols} contiguous for K={K} at {n}:{m}, got {tuple(values.shape)}")
+    words = nm_meta_words(R, K, n, m)
+    if meta.numel() != words or meta.element_size() != 4 or not meta.is_contiguous():
+        raise ValueError(f"meta must be {words} contiguous 32-bit words, got {meta.numel()} of {meta.dtype}")
+    _vector(idx, "idx", K, torch.int32)
+    return R
+
+
+def spmm_xent(values, meta, n: int, m: int, K: int, X, target, idx=None, stream=None):
+    """(loss, lse), T float32 each: cross entropy of the pruned head W' Pi (R x K compressed) at the int32 targets.
+
+    X is K x T bf16; a target outside [0, R) gives its token a loss of 0.
+    """
+    import torch
+    _same_device(X, values, meta, target, idx)
+    R = _compressed(values, meta, n, m, K, idx)
+    ldx = _rows(X, "X", torch.bfloat16)
+    T = X.shape[1]
+    if X.shape[0] != K:
+        raise ValueError(f"X has {X.shape[0]} rows, K is {K}")
+    _vector(target, "target", T, torch.int32)
+    with _on(X, stream) as s:
+        out = torch.empty((2, T), dtype=torch.float32, device=X.device)
+        loss, lse = out[0], out[1]
+        nm_spmm_xent(values, meta, n, m, R, K, idx, X, ldx, T, target, loss, lse, s)
+    return loss, lse
+
+
+def spmm_xent_grad(values, meta, n: int, m: int, K: int, X, target, lse, dloss, idx=None, need_dx: bool = True,
+                   need_dv: bool = True, stream=None):
+    """(dX K x T, dV like values), bf16: gradients of sum(dloss * loss) of spmm_xent; None for one not needed."""
+    import torch
+    _same_device(X, values, meta, target, lse, dloss, idx)
+    R = _compressed(values, meta, n, m, K, idx)
+    ldx = _rows(X, "X", torch.bfloat16)
+    T = X.shape[1]
+    if X.shape[0] != K:
+        raise ValueError(f"X has {X.shape[0]} rows, K is {K}")
+    _vector(target, "target", T, torch.int32)
+    _vector(lse, "lse", T, torch.float32)
+    _vector(dloss, "dloss", T, torch.float32)
+    dX, dV, lddx = None, None, 0
+    with _on(X, stream) as s:
+        if need_dx:
+            dX, lddx = _out_rows(K, T, torch.bfloat16, X.device)
+        if need_dv:
+            dV = torch.empty((R, nm_value_cols(K, n, m)), dtype=torch.bfloat16, device=X.device)
+        nm_spmm_xent_grad(values, meta, n, m, R, K, idx, X, ldx, T, target, lse, dloss, dX, lddx, dV, s)
+    return dX, dV
 
 
 def prune_compress(W, n: int, m: int, stream=None):

@@ -877,6 +877,52 @@ static nm_status check_bwd_common(int n, int m, int64_t R, int64_t K, int64_t T,
   return NM_OK;
 }
 
+nm_status spmm_rows(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                    const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, nm_out_dtype y_dtype,
+                    cudaStream_t stream) {
+  GemmRequest q{};
+  q.values = values;
+  q.meta = meta;
+  q.n = n;
+  q.m = m;
+  q.R = R;
+  q.K = K;
+  q.T = T;
+  q.X = X;
+  q.ldx = ldx;
+  q.Y = Y;
+  q.ldy = ldy;
+  q.y_dtype = (int)y_dtype;
+  q.algo = NM_ALGO_AUTO;
+  return run_gemm(q, stream);
+}
+
+nm_status dense_t_accumulate(const uint16_t* W, int64_t ldw, int64_t R, int64_t K, const uint16_t* D, int64_t ldd,
+                             int64_t T, float* C, int64_t ldc, bool add, cudaStream_t stream) {
+  DenseParams p;
+  std::memset(&p, 0, sizeof p);
+  p.M = K;
+  p.N = T;
+  p.Kr = R;
+  p.k_tiles = (R + 127) / 128;
+  p.tiles_m = (int)((K + 255) / 256);
+  p.tiles_n = (int)((T + 255) / 256);
+  if ((int64_t)p.tiles_m * p.tiles_n >= (1ll << 31)) return fail(NM_ERR_UNSUPPORTED, "too many tiles");
+  p.num_tiles = p.tiles_m * p.tiles_n;
+  p.status = status_word_ptr();
+  if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
+  p.out = C;
+  p.ldo = ldc;
+  p.out_f32 = 1;
+  p.add = add ? 1 : 0;
+  nm_status st = make_tmap(&p.tm_a, W, (uint64_t)K, (uint64_t)R, (uint64_t)ldw * 2, 64, 64, 128, "W' (dense)");
+  if (st == NM_OK) st = make_tmap(&p.tm_b, D, (uint64_t)T, (uint64_t)R, (uint64_t)ldd * 2, 64, 64, 128, "dY");
+  if (st == NM_OK) st = set_store_map(p, C, K, T, ldc, true);
+  if (st != NM_OK) return st;
+  cudaError_t e = launch_dense_pair(p, true, true, EPI_STORE, stream);
+  return e == cudaSuccess ? NM_OK : cuda_fail(e, "transposed GEMM launch");
+}
+
 static nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
                             const int32_t* idx, const uint16_t* dY, int64_t lddy, int64_t T, void* dX, int64_t lddx,
                             nm_out_dtype dtype, cudaStream_t stream) {
@@ -934,7 +980,7 @@ static nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n,
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "transposed GEMM launch");
 }
 
-static nm_status run_sddmm(const uint32_t* meta, int n, int m, int64_t R, int64_t K, const int32_t* idx,
+nm_status run_sddmm(const uint32_t* meta, int n, int m, int64_t R, int64_t K, const int32_t* idx,
                            const uint16_t* dY, int64_t lddy, const uint16_t* X, int64_t ldx, int64_t T, void* dV,
                            nm_out_dtype dtype, cudaStream_t stream) {
   t_last_error.clear();

@@ -301,7 +301,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && col0 < p.N && (int64_t)wrow0 < p.M) {
-            tma_store_2d(&p.tm_out, sbuf, (int32_t)col0, wrow0);
+            if (p.add)
+              tma_reduce_add_2d(&p.tm_out, sbuf, (int32_t)col0, wrow0);
+            else
+              tma_store_2d(&p.tm_out, sbuf, (int32_t)col0, wrow0);
             bulk_commit_group();
           }
         }

@@ -22,6 +22,19 @@ nm_status make_tmap(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t 
                     uint32_t box_inner, uint32_t box_outer, int swizzle_bytes, const char* what,
                     CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 
+// Y = W' X (nm_spmm).
+nm_status spmm_rows(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                    const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, nm_out_dtype y_dtype,
+                    cudaStream_t stream);
+// nm_sddmm.
+nm_status run_sddmm(const uint32_t* meta, int n, int m, int64_t R, int64_t K, const int32_t* idx, const uint16_t* dY,
+                    int64_t lddy, const uint16_t* X, int64_t ldx, int64_t T, void* dV, nm_out_dtype dtype,
+                    cudaStream_t stream);
+// C (K x T fp32, row stride ldc) = or += W^T D for a dense R x K bf16 W (row stride ldw) and an R x T bf16 D, by
+// the SM-pair GEMM; every element takes one addition.
+nm_status dense_t_accumulate(const uint16_t* W, int64_t ldw, int64_t R, int64_t K, const uint16_t* D, int64_t ldd,
+                             int64_t T, float* C, int64_t ldc, bool add, cudaStream_t stream);
+
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool dtype_ok(int d) { return d == NM_OUT_BF16 || d == NM_OUT_F32; }

@@ -85,6 +85,7 @@ struct DenseParams {
   void* out;
   int64_t ldo;
   int out_f32;
+  int add;  // epilogue 0 with tma_store and out_f32: C += (a TMA reduction per chunk) instead of C =
   const int32_t* row_map;
   int64_t rows_out;
   const uint32_t* meta;

@@ -1,0 +1,319 @@
+// nm_xent.cu -- softmax cross entropy of a pruned output head, forward and
+// backward, without the logits of the whole vocabulary in memory.
+//
+// With the logits z = (W' Pi) X (R x T, R the vocabulary):
+//   lse[t] = log sum_v exp z[v][t],  loss[t] = lse[t] - z[target[t]][t],
+//   G[v][t] = dloss[t] (exp(z[v][t] - lse[t]) - [v == target[t]]),
+//   dX = (W' Pi)^T G,  dV = the survivors' entries of G Xp^T.
+// The vocabulary is taken in pieces of rows: a piece's logits are multiplied
+// out, used and overwritten by the next piece's.
+//
+// Forward: every 256 rows leave a pair (max, sum of exp(z - max)) per token,
+// and the token's target row its logit; one last pass joins the pairs.
+// Backward: the logits of a piece are computed again, become G (bf16, rounded
+// once: it is an operand of the tensor cores like the dY of nm_spmm_t), and G
+// meets the decompressed piece of W' in a product that adds to a K x T fp32
+// accumulator, and Xp in the survivor-sampled product for dV.  The accumulator
+// takes one addition per piece, in the order of the pieces; it is rounded to
+// dX at the end.
+#include <cstdint>
+#include <cstring>
+#include <cuda_runtime.h>
+
+#include "nm_host.h"
+#include "nm_internal.h"
+#include "nm_ptx.cuh"
+#include "nm_spmm.h"
+
+namespace nmk {
+
+namespace xent {
+constexpr int kPairRows = 256;  // logits rows joined into one (max, sum) pair
+constexpr float kLog2e = 1.4426950408889634f;
+}  // namespace xent
+
+// part[pair][t] = (max, sum exp(z - max)) over one pair's rows of the logits
+// piece; the rows of targets write their logit.  One block: 32 tokens, one pair.
+__global__ void __launch_bounds__(256) xent_pairs_kernel(const float* Z, int64_t ldz, int64_t rows, int64_t T,
+                                                         int64_t v0, const int32_t* target, float2* part,
+                                                         float* z_target) {
+  using namespace xent;
+  __shared__ float s_max[8][32], s_sum[8][32];
+  pdl_gate();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t r0 = (int64_t)blockIdx.y * kPairRows;
+  const int64_t r1 = r0 + kPairRows < rows ? r0 + kPairRows : rows;
+  float top = -INFINITY, sum = 0.f;
+  if (t < T) {
+    const int64_t want = (int64_t)__ldg(target + t) - v0;
+    for (int64_t r = r0 + warp; r < r1; r += 8) {
+      const float z = __ldcg(Z + r * ldz + t);
+      if (r == want) z_target[t] = z;
+      if (z > top) {
+        sum = sum * exp2f((top - z) * kLog2e) + 1.f;
+        top = z;
+      } else {
+        sum += exp2f((z - top) * kLog2e);
+      }
+    }
+  }
+  s_max[warp][lane] = top;
+  s_sum[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && t < T) {
+    float m = s_max[0][lane];
+    for (int w = 1; w < 8; ++w) m = fmaxf(m, s_max[w][lane]);
+    float s = 0.f;
+    for (int w = 0; w < 8; ++w)
+      if (s_sum[w][lane] != 0.f) s += s_sum[w][lane] * exp2f((s_max[w][lane] - m) * kLog2e);
+    part[(v0 / kPairRows + blockIdx.y) * T + t] = make_float2(m, s);
+  }
+}
+
+// Joins a token's pairs: lse = M + log sum_p s_p exp(m_p - M), M the largest max.
+__global__ void __launch_bounds__(256) xent_join_kernel(const float2* part, int64_t pairs, int64_t R, int64_t T,
+                                                        const int32_t* target, const float* z_target, float* loss,
+                                                        float* lse) {
+  using namespace xent;
+  __shared__ float s_max[8][32], s_sum[8][32];
+  pdl_gate();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * 32 + lane;
+  float m = -INFINITY, s = 0.f;
+  if (t < T) {
+    for (int64_t p = warp; p < pairs; p += 8) {
+      const float2 q = __ldcg(part + p * T + t);
+      const float top = fmaxf(m, q.x);
+      if (s != 0.f) s *= exp2f((m - top) * kLog2e);
+      if (q.y != 0.f) s += q.y * exp2f((q.x - top) * kLog2e);  // not 0: a NaN logit's NaN is passed on
+      m = top;
+    }
+  }
+  s_max[warp][lane] = m;
+  s_sum[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && t < T) {
+    float top = s_max[0][lane];
+    for (int w = 1; w < 8; ++w) top = fmaxf(top, s_max[w][lane]);
+    float sum = 0.f;
+    for (int w = 0; w < 8; ++w)
+      if (s_sum[w][lane] != 0.f) sum += s_sum[w][lane] * exp2f((s_max[w][lane] - top) * kLog2e);
+    const float l = top + logf(sum);
+    const int32_t want = __ldg(target + t);
+    lse[t] = l;
+    loss[t] = want >= 0 && (int64_t)want < R ? l - __ldcg(z_target + t) : 0.f;
+  }
+}
+
+// G = dloss (exp(z - lse) - [row == target]) of a logits piece, bf16; 0 where the target is outside [0, R).
+// Columns T .. ldg - 1 (padding to whole 16-byte pieces) are written as 0.
+__global__ void __launch_bounds__(256) xent_g_kernel(const float* Z, int64_t ldz, int64_t rows, int64_t T, int64_t R,
+                                                     int64_t v0, const int32_t* target, const float* lse,
+                                                     const float* dloss, uint16_t* G, int64_t ldg) {
+  using namespace xent;
+  pdl_gate();
+  const int64_t t = ((int64_t)blockIdx.x * 32 + (threadIdx.x & 31)) * 2;
+  if (t >= ldg) return;
+  float l[2], d[2];
+  int64_t want[2];
+  for (int j = 0; j < 2; ++j) {
+    const int64_t tj = t + j;
+    const int32_t w = tj < T ? __ldg(target + tj) : -1;
+    const bool has = w >= 0 && (int64_t)w < R;
+    want[j] = (int64_t)w - v0;
+    l[j] = has ? __ldg(lse + tj) : 0.f;
+    d[j] = has ? __ldg(dloss + tj) : 0.f;
+  }
+  const bool has0 = t < T && want[0] + v0 >= 0 && want[0] + v0 < R, has1 = t + 1 < T && want[1] + v0 >= 0 && want[1] + v0 < R;
+  for (int64_t r = (int64_t)blockIdx.y * 64 + (threadIdx.x >> 5); r < rows && r < ((int64_t)blockIdx.y + 1) * 64; r += 8) {
+    float g[2] = {0.f, 0.f};
+    if (has0) g[0] = d[0] * (exp2f((__ldcg(Z + r * ldz + t) - l[0]) * kLog2e) - (r == want[0] ? 1.f : 0.f));
+    if (has1) g[1] = d[1] * (exp2f((__ldcg(Z + r * ldz + t + 1) - l[1]) * kLog2e) - (r == want[1] ? 1.f : 0.f));
+    *reinterpret_cast<uint32_t*>(G + r * ldg + t) = pack_bf16x2(g[0], g[1]);
+  }
+}
+
+// dX[idx[k]] (dX[k] without idx) = the accumulator's row k, rounded to bf16; rows mapped outside [0, K) are dropped.
+__global__ void __launch_bounds__(256) xent_round_kernel(const float* acc, int64_t lda, int64_t K, int64_t T,
+                                                         const int32_t* idx, uint16_t* dX, int64_t lddx) {
+  pdl_gate();
+  const int64_t pieces = (T + 7) / 8, total = K * pieces;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t k = i / pieces, t = (i - k * pieces) * 8;
+    const int64_t row = idx ? (int64_t)__ldg(idx + k) : k;
+    if (row < 0 || row >= K) continue;
+    const float* a = acc + k * lda + t;
+    uint16_t* d = dX + row * lddx + t;
+    if (t + 8 <= T) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(a)), y = __ldcg(reinterpret_cast<const float4*>(a) + 1);
+      *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
+                                                pack_bf16x2(y.z, y.w));
+    } else {
+      for (int j = 0; t + j < T; ++j) d[j] = (uint16_t)(pack_bf16x2(__ldcg(a + j), 0.f) & 0xFFFFu);
+    }
+  }
+}
+
+namespace {
+
+struct Head {  // the compressed head and its input (permuted rows already gathered)
+  const uint16_t* values;
+  const uint32_t* meta;
+  int n, m;
+  int64_t R, K, T;
+  const uint16_t* X;
+  int64_t ldx;
+  const uint16_t* row_values(int64_t v) const { return values + v * value_cols(K, n, m); }
+  const uint32_t* row_meta(int64_t v) const {  // v a multiple of 16 for the tiled metadata
+    return meta + (tiled_meta(n, m) ? v / 16 * meta_col_blocks(K) * 64 : v * meta_cols(K, n, m));
+  }
+};
+
+nm_status check_head(int n, int m, int64_t R, int64_t K, int64_t T) {
+  if (R < 0 || K < 0 || T < 0) return fail(NM_ERR_INVALID_ARG, "negative dimension");
+  if (!pattern_ok(n, m)) return fail(NM_ERR_INVALID_ARG, "pattern %d:%d not supported (M in 2,4,8,16; 1<=N<M)", n, m);
+  if (K % m != 0) return fail(NM_ERR_INVALID_ARG, "K=%lld is not a multiple of M=%d", (long long)K, m);
+  if (R == 0 || K == 0) return fail(NM_ERR_INVALID_ARG, "an output head needs at least one row and one column");
+  if (R >= kMaxDim || K >= kMaxDim || T >= kMaxDim) return fail(NM_ERR_UNSUPPORTED, "dimensions must stay below 2^31");
+  return NM_OK;
+}
+
+// Rows of one piece: a multiple of 256 whose logits take about 64 MB, so that they stay in L2.
+int64_t piece_rows(int64_t R, int64_t T) {
+  int64_t rows = (16ll << 20) / (T > 0 ? T : 1) / 256 * 256;
+  if (rows < 256) rows = 256;
+  if (rows > 8192) rows = 8192;
+  return rows < R ? rows : R;
+}
+
+// Xp[k] = X[idx[k]] when there is an index map.
+nm_status gather_input(Head& h, const int32_t* idx, Staged& staged, cudaStream_t s) {
+  if (!idx) return NM_OK;
+  const int64_t ldp = (h.T + 7) / 8 * 8;
+  cudaError_t e = staged.get((size_t)(h.K * ldp * 2));
+  if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the permuted input");
+  e = launch_gather_rows(h.X, h.ldx, idx, h.K, h.T, staged.as<uint16_t>(), ldp, s);
+  if (e != cudaSuccess) return cuda_fail(e, "gather launch");
+  h.X = staged.as<uint16_t>();
+  h.ldx = ldp;
+  return NM_OK;
+}
+
+nm_status run_xent(Head h, const int32_t* idx, const int32_t* target, float* loss, float* lse, cudaStream_t s) {
+  Staged xp(s), work(s), z(s);
+  nm_status st = gather_input(h, idx, xp, s);
+  if (st != NM_OK) return st;
+  const int64_t pairs = (h.R + xent::kPairRows - 1) / xent::kPairRows;
+  const int64_t rows = piece_rows(h.R, h.T), ldz = (h.T + 3) / 4 * 4;
+  cudaError_t e = work.get((size_t)(pairs * h.T * 8 + h.T * 4));
+  if (e == cudaSuccess) e = z.get((size_t)(rows * ldz * 4));
+  if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the logits piece");
+  float2* part = work.as<float2>();
+  float* z_target = reinterpret_cast<float*>(part + pairs * h.T);
+  const unsigned tb = (unsigned)((h.T + 31) / 32);
+  for (int64_t v0 = 0; v0 < h.R; v0 += rows) {
+    const int64_t n = h.R - v0 < rows ? h.R - v0 : rows;
+    st = spmm_rows(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, z.as<float>(), ldz, NM_OUT_F32, s);
+    if (st != NM_OK) return st;
+    e = launch_pdl(xent_pairs_kernel, dim3(tb, (unsigned)((n + xent::kPairRows - 1) / xent::kPairRows)), dim3(256), 0,
+                   s, (const float*)z.as<float>(), ldz, n, h.T, v0, target, part, z_target);
+    count_launch();
+    if (e != cudaSuccess) return cuda_fail(e, "cross-entropy launch");
+  }
+  e = launch_pdl(xent_join_kernel, dim3(tb), dim3(256), 0, s, (const float2*)part, pairs, h.R, h.T, target,
+                 (const float*)z_target, loss, lse);
+  count_launch();
+  return e == cudaSuccess ? NM_OK : cuda_fail(e, "cross-entropy launch");
+}
+
+nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const float* lse, const float* dloss,
+                        uint16_t* dX, int64_t lddx, uint16_t* dV, cudaStream_t s) {
+  Staged xp(s), z(s), g(s), wd(s), acc(s);
+  nm_status st = gather_input(h, idx, xp, s);
+  if (st != NM_OK) return st;
+  const int64_t rows = piece_rows(h.R, h.T), ldz = (h.T + 3) / 4 * 4, ldg = (h.T + 7) / 8 * 8;
+  const int64_t ldk = (h.K + 7) / 8 * 8;
+  cudaError_t e = z.get((size_t)(rows * ldz * 4));
+  if (e == cudaSuccess) e = g.get((size_t)(rows * ldg * 2));
+  if (e == cudaSuccess && dX) e = wd.get((size_t)(rows * ldk * 2));
+  if (e == cudaSuccess && dX) e = acc.get((size_t)(h.K * ldz * 4));
+  if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gradient piece");
+  for (int64_t v0 = 0; v0 < h.R; v0 += rows) {
+    const int64_t n = h.R - v0 < rows ? h.R - v0 : rows;
+    st = spmm_rows(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, z.as<float>(), ldz, NM_OUT_F32, s);
+    if (st != NM_OK) return st;
+    e = launch_pdl(xent_g_kernel, dim3((unsigned)((ldg / 2 + 31) / 32), (unsigned)((n + 63) / 64)), dim3(256), 0, s,
+                   (const float*)z.as<float>(), ldz, n, h.T, h.R, v0, target, lse, dloss, g.as<uint16_t>(), ldg);
+    count_launch();
+    if (e != cudaSuccess) return cuda_fail(e, "cross-entropy gradient launch");
+    if (dX) {
+      e = launch_decompress(h.row_values(v0), h.row_meta(v0), n, h.K, h.n, h.m, wd.as<uint16_t>(), ldk, s);
+      if (e != cudaSuccess) return cuda_fail(e, "decompress launch");
+      st = dense_t_accumulate(wd.as<uint16_t>(), ldk, n, h.K, g.as<uint16_t>(), ldg, h.T, acc.as<float>(), ldz, v0 > 0, s);
+      if (st != NM_OK) return st;
+    }
+    if (dV) {
+      st = run_sddmm(h.row_meta(v0), h.n, h.m, n, h.K, nullptr, g.as<uint16_t>(), ldg, h.X, h.ldx, h.T,
+                     dV + v0 * value_cols(h.K, h.n, h.m), NM_OUT_BF16, s);
+      if (st != NM_OK) return st;
+    }
+  }
+  if (dX) {
+    const int64_t want = (h.K * ((h.T + 7) / 8) + 255) / 256, cap = (int64_t)sm_count_current() * 16;
+    e = launch_pdl(xent_round_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, s,
+                   (const float*)acc.as<float>(), ldz, h.K, h.T, idx, dX, lddx);
+    count_launch();
+    if (e != cudaSuccess) return cuda_fail(e, "gradient rounding launch");
+  }
+  return NM_OK;
+}
+
+}  // namespace
+}  // namespace nmk
+
+using namespace nmk;
+
+extern "C" {
+
+nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                       const int32_t* idx, const uint16_t* X, int64_t ldx, int64_t T, const int32_t* target,
+                       float* loss, float* lse, void* stream) {
+  set_last_error("");
+  nm_status st = check_head(n, m, R, K, T);
+  if (st != NM_OK || T == 0) return st;
+  if (!values || !meta || !target || !loss || !lse) return fail(NM_ERR_INVALID_ARG, "null operand");
+  st = check_matrix(X, ldx, T, 2, "X");
+  if (st == NM_OK) st = require_device();
+  if (st != NM_OK) return st;
+  return run_xent(Head{values, meta, n, m, R, K, T, X, ldx}, idx, target, loss, lse,
+                  static_cast<cudaStream_t>(stream));
+}
+
+nm_status nm_spmm_xent_grad(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                            const int32_t* idx, const uint16_t* X, int64_t ldx, int64_t T, const int32_t* target,
+                            const float* lse, const float* dloss, uint16_t* dX, int64_t lddx, uint16_t* dV,
+                            void* stream) {
+  set_last_error("");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  nm_status st = check_head(n, m, R, K, T);
+  if (st != NM_OK) return st;
+  if (!dX && !dV) return fail(NM_ERR_INVALID_ARG, "dX and dV are both null");
+  if (dV && !aligned_to(dV, 2)) return fail(NM_ERR_MISALIGNED, "dV misaligned");
+  if (T == 0) {  // no tokens: dX has no elements, dV is an empty sum
+    if (!dV) return NM_OK;
+    st = require_device();
+    if (st != NM_OK) return st;
+    const int64_t vcols = value_cols(K, n, m);
+    cudaError_t e = launch_fill_zero(dV, R, vcols, vcols, 2, s);
+    return e == cudaSuccess ? NM_OK : cuda_fail(e, "zero fill");
+  }
+  if (!values || !meta || !target || !lse || !dloss) return fail(NM_ERR_INVALID_ARG, "null operand");
+  st = check_matrix(X, ldx, T, 2, "X");
+  if (st == NM_OK && dX) st = check_matrix(dX, lddx, T, 2, "dX");
+  if (st == NM_OK) st = require_device();
+  if (st != NM_OK) return st;
+  return run_xent_grad(Head{values, meta, n, m, R, K, T, X, ldx}, idx, target, lse, dloss, dX, lddx, dV, s);
+}
+
+}  // extern "C"

@@ -141,3 +141,26 @@ def test_host_argument_checks_of_layer_norm(lib):
     for bad in (dict(dY=8), dict(X=8), dict(dX=8), dict(lddy=12), dict(lddx=12)):
         assert bwd(**bad) == nm.NM_ERR_MISALIGNED, bad
     assert bwd(T=0) == nm.NM_OK
+
+
+def test_host_argument_checks_of_cross_entropy(lib):
+    """Refused before any launch: pattern, sizes, nulls, strides and alignment."""
+    L, I = lib, nm.NM_ERR_INVALID_ARG
+
+    def loss(n=2, m=4, R=8, K=32, X=16, ldx=8, T=8, target=16, out=16, lse=16, values=16):
+        return L.nm_spmm_xent(values, 16, n, m, R, K, None, X, ldx, T, target, out, lse, None)
+
+    def grad(n=2, m=4, R=8, K=32, X=16, ldx=8, T=8, target=16, lse=16, dloss=16, dX=16, lddx=8, dV=16):
+        return L.nm_spmm_xent_grad(16, 16, n, m, R, K, None, X, ldx, T, target, lse, dloss, dX, lddx, dV, None)
+
+    for bad in (dict(n=4), dict(m=5), dict(K=30), dict(R=0), dict(K=0), dict(R=-1), dict(T=-1), dict(X=None),
+                dict(target=None), dict(out=None), dict(lse=None), dict(values=None), dict(ldx=7)):
+        assert loss(**bad) == I, bad
+    assert loss(X=8) == loss(ldx=12) == nm.NM_ERR_MISALIGNED
+    assert loss(T=1 << 31) == loss(R=1 << 31) == nm.NM_ERR_UNSUPPORTED
+    assert loss(T=0) == nm.NM_OK
+    for bad in (dict(n=4), dict(K=30), dict(R=0), dict(T=-1), dict(X=None), dict(target=None), dict(lse=None),
+                dict(dloss=None), dict(dX=None, dV=None), dict(lddx=7), dict(ldx=7)):
+        assert grad(**bad) == I, bad
+    assert grad(dX=8) == grad(lddx=12) == grad(dV=17) == nm.NM_ERR_MISALIGNED
+    assert grad(T=0, dV=None) == nm.NM_OK

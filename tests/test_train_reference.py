@@ -41,3 +41,18 @@ def test_layer_norm_gradient_against_the_closed_form():
     assert torch.allclose(got[0], dx, rtol=1e-12, atol=1e-12)
     assert torch.allclose(got[1], (dy * h).sum(1), rtol=1e-12, atol=1e-12)
     assert torch.allclose(got[2], dy.sum(1), rtol=1e-12, atol=1e-12)
+
+
+def test_cross_entropy_gradient_against_differences():
+    w, x = rand(6, 5, seed=8), rand(5, 4, seed=9)
+    target, dloss = torch.tensor([3, -100, 5, 6]), rand(4, seed=10)
+    loss = lambda: (ref.cross_entropy(w @ x, target)[0] * dloss).sum()  # noqa: E731
+    G, dX, dW = ref.cross_entropy_grad(w, x, target, dloss)
+    assert torch.allclose(dX, differences(loss, x), rtol=1e-6, atol=1e-7)
+    assert torch.allclose(dW, differences(loss, w), rtol=1e-6, atol=1e-7)
+    p = torch.softmax(w @ x, 0)
+    want = p.clone()
+    want[3, 0] -= 1
+    want[5, 2] -= 1
+    want *= torch.where((target >= 0) & (target < 6), dloss, 0.0)
+    assert torch.allclose(G, want, rtol=1e-12, atol=1e-14)

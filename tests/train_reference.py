@@ -34,3 +34,19 @@ def layer_norm_grad(dy, x, gamma=None, beta=None, eps=1e-5):
 def chain(n):
     """Relative bound of a float32 sum whose longest chain has n additions: n u / (1 - n u)."""
     return n * U32 / (1 - n * U32)
+
+
+def cross_entropy(z, target):
+    """(loss, lse) per column of the logits z (R x T, float64); a target outside [0, R) gives a loss of 0."""
+    lse = torch.logsumexp(z, 0)
+    has = (target >= 0) & (target < z.shape[0])
+    at = torch.where(has, target, 0).long()
+    return torch.where(has, lse - z.gather(0, at[None, :])[0], torch.zeros_like(lse)), lse
+
+
+def cross_entropy_grad(w, x, target, dloss):
+    """(G, dX, dW) of sum(dloss * loss) with z = w x, by autograd."""
+    w, x = w.detach().clone().requires_grad_(), x.detach().clone().requires_grad_()
+    z = w @ x
+    loss, _ = cross_entropy(z, target)
+    return torch.autograd.grad((loss * dloss).sum(), (z, x, w))
