@@ -488,6 +488,58 @@ NM_API nm_status nm_spmm_xent_grad(const uint16_t* values, const uint32_t* meta,
                                    const int32_t* target, const float* lse, const float* dloss, uint16_t* dX,
                                    int64_t lddx, uint16_t* dV, void* stream);
 
+/* ------------------------------------------------------------- adapters */
+/*
+ * Low-rank adapters of many requests beside one shared pruned projection:
+ *   y_t = (W' Pi) x_t + s_a B_a (A_a x_t),   a = adapter[t],
+ * for columns t of any mix of adapters; a token whose entry of `adapter` is
+ * outside [0, num_adapters) has none.  A_a acts on X itself, not on the
+ * permuted input.  The pages prune one shared network; its fine-tuned variants
+ * next to it are what these calls add.  Arguments shared by the three calls:
+ *   A       num_adapters x rank x K bf16, contiguous
+ *   B       num_adapters x R x rank bf16, contiguous
+ *   rank    1..128 (NM_ERR_UNSUPPORTED above); adapters of a smaller rank are
+ *           padded with zero rows of A and columns of B
+ *   num_adapters  0..32767
+ *   scale   num_adapters fp32, or NULL for 1
+ *   adapter T int32
+ * A and B are aligned to their elements; rows that start on 16 bytes (K % 8 ==
+ * 0, rank % 8 == 0) are read faster.  A_a x_t and B_a^T dy_t stay fp32 between
+ * the products (read by the tensor cores as two or three bf16 terms), and the
+ * projection's fp32 sum takes the adapter's before the one rounding to the
+ * output.  No column depends on another column's data: an Inf or NaN in one
+ * request's tokens or adapter stays in its columns.  Results repeat bit for
+ * bit.  At most 4194240 tokens a call (NM_ERR_UNSUPPORTED).
+ *
+ * nm_spmm_lora: Y as above; other arguments as nm_spmm_permuted (idx may be
+ *   NULL).  Staged from the library's pool: T x rank (padded to 16) fp32, the
+ *   projection's R x T fp32 sum, and what nm_spmm_permuted stages.
+ * nm_spmm_lora_t: the input gradient dX = (W' Pi)^T dY + s_a A_a^T (B_a^T dY).
+ *   Arguments as nm_spmm_t, but with idx every row of dX is written: rows that
+ *   no entry names get the adapters' part alone.  Staged: T x rank fp32, a K x T
+ *   fp32 sum, with idx K*4 bytes, and what nm_spmm_t stages.
+ * nm_lora_grad: the adapters' gradients, summed over each adapter's tokens,
+ *     dA_a = s_a sum_t (B_a^T dy_t) x_t^T   (num_adapters x rank x K),
+ *     dB_a = s_a sum_t dy_t (A_a x_t)^T     (num_adapters x R x rank),
+ *   both bf16 or both fp32 (dtype), contiguous, either may be NULL (not
+ *   both); zeros for an adapter without tokens.  dY R x T and X K x T as in
+ *   nm_sddmm.  Staged: T x rank fp32 for each of the two, and 4 bytes per
+ *   adapter and 64 tokens.
+ * Errors: as nm_spmm_permuted, nm_spmm_t and nm_sddmm.
+ */
+NM_API nm_status nm_spmm_lora(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                              const int32_t* idx, const uint16_t* X, int64_t ldx, int64_t T, const uint16_t* A,
+                              const uint16_t* B, int rank, int64_t num_adapters, const float* scale,
+                              const int32_t* adapter, void* Y, int64_t ldy, nm_out_dtype y_dtype, void* stream);
+NM_API nm_status nm_spmm_lora_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                                const int32_t* idx, const uint16_t* dY, int64_t lddy, int64_t T, const uint16_t* A,
+                                const uint16_t* B, int rank, int64_t num_adapters, const float* scale,
+                                const int32_t* adapter, void* dX, int64_t lddx, nm_out_dtype dtype, void* stream);
+NM_API nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t lddy, const uint16_t* X, int64_t ldx,
+                              int64_t T, const uint16_t* A, const uint16_t* B, int rank, int64_t num_adapters,
+                              const float* scale, const int32_t* adapter, void* dA, void* dB, nm_out_dtype dtype,
+                              void* stream);
+
 /*
  * nm_spmm_algo --nm_spmm / nm_spmm_permuted (idx may be NULL) with the kernel
  * design chosen explicitly, to compare the sparse tensor-core path with the

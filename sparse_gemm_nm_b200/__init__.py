@@ -66,6 +66,9 @@ SIGNATURES = {
     "nm_layer_norm_grad": ([_P, _I64, _I, _P, _I64, _I, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _P], _I),
     "nm_spmm_xent": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P], _I),
     "nm_spmm_xent_grad": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P], _I),
+    "nm_spmm_lora": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I, _I64, _P, _P, _P, _I64, _I, _P], _I),
+    "nm_spmm_lora_t": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I, _I64, _P, _P, _P, _I64, _I, _P], _I),
+    "nm_lora_grad": ([_I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I, _I64, _P, _P, _P, _P, _I, _P], _I),
     "nm_spmm_algo": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I, _I, _P], _I),
     "nm_spmm_permuted_noalloc": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I, _P], _I),
     "nm_release_staging": ([], _I),
@@ -257,6 +260,26 @@ def nm_spmm_xent_grad(values, meta, n, m, R, K, idx, X, ldx, T, target, lse, dlo
     _check(lib().nm_spmm_xent_grad(_ptr(values), _ptr(meta), n, m, R, K, _ptr(idx), _ptr(X), ldx, T, _ptr(target),
                                    _ptr(lse), _ptr(dloss), _ptr(dX), lddx, _ptr(dV), _stream(stream)),
            "nm_spmm_xent_grad")
+
+
+def nm_spmm_lora(values, meta, n, m, R, K, idx, X, ldx, T, A, B, rank, num_adapters, scale, adapter, Y, ldy,
+                 y_dtype=NM_OUT_BF16, stream=None) -> None:
+    _check(lib().nm_spmm_lora(_ptr(values), _ptr(meta), n, m, R, K, _ptr(idx), _ptr(X), ldx, T, _ptr(A), _ptr(B), rank,
+                              num_adapters, _ptr(scale), _ptr(adapter), _ptr(Y), ldy, y_dtype, _stream(stream)),
+           "nm_spmm_lora")
+
+
+def nm_spmm_lora_t(values, meta, n, m, R, K, idx, dY, lddy, T, A, B, rank, num_adapters, scale, adapter, dX, lddx,
+                   dtype=NM_OUT_BF16, stream=None) -> None:
+    _check(lib().nm_spmm_lora_t(_ptr(values), _ptr(meta), n, m, R, K, _ptr(idx), _ptr(dY), lddy, T, _ptr(A), _ptr(B),
+                                rank, num_adapters, _ptr(scale), _ptr(adapter), _ptr(dX), lddx, dtype,
+                                _stream(stream)), "nm_spmm_lora_t")
+
+
+def nm_lora_grad(R, K, dY, lddy, X, ldx, T, A, B, rank, num_adapters, scale, adapter, dA, dB, dtype=NM_OUT_BF16,
+                 stream=None) -> None:
+    _check(lib().nm_lora_grad(R, K, _ptr(dY), lddy, _ptr(X), ldx, T, _ptr(A), _ptr(B), rank, num_adapters, _ptr(scale),
+                              _ptr(adapter), _ptr(dA), _ptr(dB), dtype, _stream(stream)), "nm_lora_grad")
 
 
 def nm_spmm_algo(values, meta, n, m, R, K, idx, X, ldx, T, Y, ldy, y_dtype=NM_OUT_BF16, algo=NM_ALGO_AUTO,
@@ -455,6 +478,80 @@ def spmm_xent_grad(values, meta, n: int, m: int, K: int, X, target, lse, dloss, 
             dV = torch.empty((R, nm_value_cols(K, n, m)), dtype=torch.bfloat16, device=X.device)
         nm_spmm_xent_grad(values, meta, n, m, R, K, idx, X, ldx, T, target, lse, dloss, dX, lddx, dV, s)
     return dX, dV
+
+
+def _adapters(A, B, R: int, K: int, T: int, adapter, scale):
+    """Checks the adapters' tensors and returns (num_adapters, rank)."""
+    import torch
+    for M, name in ((A, "A"), (B, "B")):
+        if M.dim() != 3 or M.dtype != torch.bfloat16 or not M.is_contiguous():
+            raise ValueError(f"{name} must be three contiguous dimensions of bfloat16, got {tuple(M.shape)} {M.dtype}")
+    n, rank = A.shape[0], A.shape[1]
+    if tuple(A.shape) != (n, rank, K) or tuple(B.shape) != (n, R, rank):
+        raise ValueError(f"A must be n x rank x {K} and B n x {R} x rank, got {tuple(A.shape)} and {tuple(B.shape)}")
+    _vector(adapter, "adapter", T, torch.int32)
+    _vector(scale, "scale", n, torch.float32)
+    return n, rank
+
+
+def spmm_lora(values, meta, n: int, m: int, K: int, X, A, B, adapter, scale=None, idx=None, out_dtype=None,
+              stream=None):
+    """Y = (W' Pi) X with every token's low-rank adapter beside it: y_t += scale[a] B[a] (A[a] x_t), a = adapter[t].
+
+    A is num_adapters x rank x K, B num_adapters x R x rank (bf16), adapter T int32 (outside [0, num_adapters): no
+    adapter), scale num_adapters float32 or None.  Y's rows are padded to 16 bytes.
+    """
+    import torch
+    _same_device(X, values, meta, A, B, adapter, scale, idx)
+    R = _compressed(values, meta, n, m, K, idx)
+    ldx = _rows(X, "X", torch.bfloat16)
+    T = X.shape[1]
+    if X.shape[0] != K:
+        raise ValueError(f"X has {X.shape[0]} rows, K is {K}")
+    num, rank = _adapters(A, B, R, K, T, adapter, scale)
+    out_dtype = out_dtype or torch.bfloat16
+    yt = _out_type(out_dtype)
+    with _on(X, stream) as s:
+        Y, ldy = _out_rows(R, T, out_dtype, X.device)
+        nm_spmm_lora(values, meta, n, m, R, K, idx, X, ldx, T, A, B, rank, num, scale, adapter, Y, ldy, yt, s)
+    return Y
+
+
+def spmm_lora_t(values, meta, n: int, m: int, K: int, dY, A, B, adapter, scale=None, idx=None, out_dtype=None,
+                stream=None):
+    """dX = (W' Pi)^T dY + scale[a] A[a]^T (B[a]^T dY) (K x T), the input gradient of spmm_lora."""
+    import torch
+    _same_device(dY, values, meta, A, B, adapter, scale, idx)
+    R = _compressed(values, meta, n, m, K, idx)
+    lddy = _rows(dY, "dY", torch.bfloat16)
+    T = dY.shape[1]
+    if dY.shape[0] != R:
+        raise ValueError(f"dY has {dY.shape[0]} rows, values {R}")
+    num, rank = _adapters(A, B, R, K, T, adapter, scale)
+    out_dtype = out_dtype or torch.bfloat16
+    yt = _out_type(out_dtype)
+    with _on(dY, stream) as s:
+        dX, lddx = _out_rows(K, T, out_dtype, dY.device)
+        nm_spmm_lora_t(values, meta, n, m, R, K, idx, dY, lddy, T, A, B, rank, num, scale, adapter, dX, lddx, yt, s)
+    return dX
+
+
+def lora_grad(dY, X, A, B, adapter, scale=None, out_dtype=None, stream=None):
+    """(dA, dB) of spmm_lora, shaped like A and B (bf16 unless out_dtype says float32)."""
+    import torch
+    _same_device(X, dY, A, B, adapter, scale)
+    ldx, lddy = _rows(X, "X", torch.bfloat16), _rows(dY, "dY", torch.bfloat16)
+    (K, T), R = X.shape, dY.shape[0]
+    if dY.shape[1] != T:
+        raise ValueError(f"dY has {dY.shape[1]} tokens, X {T}")
+    num, rank = _adapters(A, B, R, K, T, adapter, scale)
+    out_dtype = out_dtype or torch.bfloat16
+    yt = _out_type(out_dtype)
+    with _on(X, stream) as s:
+        dA = torch.empty((num, rank, K), dtype=out_dtype, device=X.device)
+        dB = torch.empty((num, R, rank), dtype=out_dtype, device=X.device)
+        nm_lora_grad(R, K, dY, lddy, X, ldx, T, A, B, rank, num, scale, adapter, dA, dB, yt, s)
+    return dA, dB
 
 
 def prune_compress(W, n: int, m: int, stream=None):

@@ -275,6 +275,7 @@ struct GemmRequest {
   // false: never stage anything (no re-encoded operand); used by the
   // allocation-free entry point for shapes it does not chunk itself
   bool allow_staging = true;
+  GemmPartials* partials = nullptr;  // set: a split-K GEMM leaves its partial sums there
 };
 
 // Split of the K stages for the skinny kernel: the number of ranges that
@@ -530,14 +531,25 @@ static nm_status run_gemm(const GemmRequest& q, cudaStream_t stream) {
       p.tiles_n = 1;
       p.num_tiles = p.tiles_m;
       if (p.splits > 1) {
-        if (!pool) e = staging_pool(&pool);
-        if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&ws, (size_t)p.splits * q.R * p.bn * 4, pool, stream);
+        const size_t ws_bytes = (size_t)p.splits * q.R * p.bn * 4;
+        if (q.partials) {
+          e = q.partials->ws->get(ws_bytes);
+        } else {
+          if (!pool) e = staging_pool(&pool);
+          if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&ws, ws_bytes, pool, stream);
+        }
         if (e != cudaSuccess) {
           ws = nullptr;
           release();
           return cuda_fail(e, "split-K workspace");
         }
-        p.ws = static_cast<float*>(ws);
+        p.ws = q.partials ? q.partials->ws->as<float>() : static_cast<float*>(ws);
+        if (q.partials) {
+          p.keep_partials = 1;
+          q.partials->splits = p.splits;
+          q.partials->split_stride = q.R * p.bn;
+          q.partials->ld = p.bn;
+        }
       }
       st = make_tmap(&p.tm_x, xsrc, (uint64_t)q.T, (uint64_t)q.K, (uint64_t)ldsrc * 2, (uint32_t)p.bn,
                      (uint32_t)p.kd, p.bn * 2, "X");
@@ -877,9 +889,9 @@ static nm_status check_bwd_common(int n, int m, int64_t R, int64_t K, int64_t T,
   return NM_OK;
 }
 
-nm_status spmm_rows(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
-                    const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, nm_out_dtype y_dtype,
-                    cudaStream_t stream) {
+static GemmRequest gemm_request(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                                const int32_t* idx, const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy,
+                                nm_out_dtype y_dtype) {
   GemmRequest q{};
   q.values = values;
   q.meta = meta;
@@ -888,13 +900,38 @@ nm_status spmm_rows(const uint16_t* values, const uint32_t* meta, int n, int m, 
   q.R = R;
   q.K = K;
   q.T = T;
+  q.idx = idx;
   q.X = X;
   q.ldx = ldx;
   q.Y = Y;
   q.ldy = ldy;
   q.y_dtype = (int)y_dtype;
   q.algo = NM_ALGO_AUTO;
+  return q;
+}
+
+nm_status check_spmm(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                     const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, nm_out_dtype y_dtype) {
+  const GemmRequest q = gemm_request(values, meta, n, m, R, K, nullptr, X, ldx, T, Y, ldy, y_dtype);
+  nm_status st = check_gemm_shape(q);
+  if (st != NM_OK || R == 0 || T == 0) return st;
+  st = check_gemm_output(q);
+  if (st == NM_OK && K > 0) st = check_gemm_operands(q);
+  return st;
+}
+
+nm_status run_spmm(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                   const int32_t* idx, const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy,
+                   nm_out_dtype y_dtype, GemmPartials* partials, cudaStream_t stream) {
+  GemmRequest q = gemm_request(values, meta, n, m, R, K, idx, X, ldx, T, Y, ldy, y_dtype);
+  q.partials = partials;
   return run_gemm(q, stream);
+}
+
+nm_status spmm_rows(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                    const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, nm_out_dtype y_dtype,
+                    cudaStream_t stream) {
+  return run_gemm(gemm_request(values, meta, n, m, R, K, nullptr, X, ldx, T, Y, ldy, y_dtype), stream);
 }
 
 nm_status dense_t_accumulate(const uint16_t* W, int64_t ldw, int64_t R, int64_t K, const uint16_t* D, int64_t ldd,
@@ -923,10 +960,8 @@ nm_status dense_t_accumulate(const uint16_t* W, int64_t ldw, int64_t R, int64_t 
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "transposed GEMM launch");
 }
 
-static nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
-                            const int32_t* idx, const uint16_t* dY, int64_t lddy, int64_t T, void* dX, int64_t lddx,
-                            nm_out_dtype dtype, cudaStream_t stream) {
-  t_last_error.clear();
+nm_status check_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                       const uint16_t* dY, int64_t lddy, int64_t T, void* dX, int64_t lddx, nm_out_dtype dtype) {
   nm_status st = check_bwd_common(n, m, R, K, T, dtype);
   if (st != NM_OK) return st;
   if (K == 0 || T == 0) return NM_OK;
@@ -935,14 +970,23 @@ static nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n,
   const int esize = dtype == NM_OUT_F32 ? 4 : 2;
   if (!al16(dX) || (lddx * esize) % 16 != 0) return fail(NM_ERR_MISALIGNED, "dX rows must be 16-byte aligned");
   st = require_device();
-  if (st != NM_OK) return st;
-  if (R == 0) {  // no rows of W': the gradient is zero
-    cudaError_t e = launch_fill_zero(dX, K, T, lddx, esize, stream);
-    return e == cudaSuccess ? NM_OK : cuda_fail(e, "zero fill");
-  }
+  if (st != NM_OK || R == 0) return st;
   if (!values || !meta || !dY) return fail(NM_ERR_INVALID_ARG, "null operand");
   if (lddy < T) return fail(NM_ERR_INVALID_ARG, "lddy < T");
   if (!al16(dY) || lddy % 8 != 0) return fail(NM_ERR_MISALIGNED, "dY rows must be 16-byte aligned");
+  return NM_OK;
+}
+
+nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                            const int32_t* idx, const uint16_t* dY, int64_t lddy, int64_t T, void* dX, int64_t lddx,
+                            nm_out_dtype dtype, cudaStream_t stream) {
+  t_last_error.clear();
+  nm_status st = check_spmm_t(values, meta, n, m, R, K, dY, lddy, T, dX, lddx, dtype);
+  if (st != NM_OK || K == 0 || T == 0) return st;
+  if (R == 0) {  // no rows of W': the gradient is zero
+    cudaError_t e = launch_fill_zero(dX, K, T, lddx, dtype == NM_OUT_F32 ? 4 : 2, stream);
+    return e == cudaSuccess ? NM_OK : cuda_fail(e, "zero fill");
+  }
   // W' written out densely (R x ldk bf16, rows padded to 16 bytes) in a staging buffer
   cudaMemPool_t pool = nullptr;
   cudaError_t e = staging_pool(&pool);

@@ -22,6 +22,28 @@ nm_status make_tmap(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t 
                     uint32_t box_inner, uint32_t box_outer, int swizzle_bytes, const char* what,
                     CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 
+class Staged;
+
+// Where a split-K GEMM may leave its fp32 partial sums instead of adding them up: `splits` matrices (1: the result
+// is in Y as usual), `split_stride` elements apart, rows of `ld`.
+struct GemmPartials {
+  Staged* ws;
+  int splits;
+  int64_t split_stride, ld;
+};
+
+// nm_spmm / nm_spmm_permuted (idx may be null): the argument checks alone, and the call.
+nm_status check_spmm(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                     const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, nm_out_dtype y_dtype);
+nm_status run_spmm(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                   const int32_t* idx, const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy,
+                   nm_out_dtype y_dtype, GemmPartials* partials, cudaStream_t stream);
+// nm_spmm_t: the argument checks alone, and the call.
+nm_status check_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                       const uint16_t* dY, int64_t lddy, int64_t T, void* dX, int64_t lddx, nm_out_dtype dtype);
+nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                     const int32_t* idx, const uint16_t* dY, int64_t lddy, int64_t T, void* dX, int64_t lddx,
+                     nm_out_dtype dtype, cudaStream_t stream);
 // Y = W' X (nm_spmm).
 nm_status spmm_rows(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
                     const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, nm_out_dtype y_dtype,

@@ -60,6 +60,7 @@ struct SpmmParams {
   int bn;
   int kd;  // skinny stage depth (logical K per stage: 128 or 256)
   float* ws;
+  int keep_partials;  // leave the ranges' sums in ws (no reduction launch)
   // fused prune + compress + GEMM: optional outputs of the compressed operand
   uint16_t* out_vals;
   uint32_t* out_meta;

@@ -307,7 +307,7 @@ static cudaError_t launch_bn(SpmmParams& p, cudaStream_t stream) {
                              stream, p);
   count_launch();
   if (e == cudaSuccess) e = cudaGetLastError();
-  if (e != cudaSuccess || p.splits == 1) return e;
+  if (e != cudaSuccess || p.splits == 1 || p.keep_partials) return e;
   return launch_skinny_reduce(p, stream);
 }
 

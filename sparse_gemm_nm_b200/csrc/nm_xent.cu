@@ -298,7 +298,7 @@ nm_status nm_spmm_xent_grad(const uint16_t* values, const uint32_t* meta, int n,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   nm_status st = check_head(n, m, R, K, T);
   if (st != NM_OK) return st;
-  if (!dX && !dV) return fail(NM_ERR_INVALID_ARG, "dX and dV are both null");
+  if (!dX && !dV && T > 0) return fail(NM_ERR_INVALID_ARG, "dX and dV are both null");
   if (dV && !aligned_to(dV, 2)) return fail(NM_ERR_MISALIGNED, "dV misaligned");
   if (T == 0) {  // no tokens: dX has no elements, dV is an empty sum
     if (!dV) return NM_OK;

@@ -164,3 +164,29 @@ def test_host_argument_checks_of_cross_entropy(lib):
         assert grad(**bad) == I, bad
     assert grad(dX=8) == grad(lddx=12) == grad(dV=17) == nm.NM_ERR_MISALIGNED
     assert grad(T=0, dV=None) == nm.NM_OK
+
+
+def test_host_argument_checks_of_the_adapters(lib):
+    """Refused before any launch: pattern, sizes, rank, number of adapters, nulls, strides and alignment."""
+    L, I, A16, U = lib, nm.NM_ERR_INVALID_ARG, nm.NM_ERR_MISALIGNED, nm.NM_ERR_UNSUPPORTED
+
+    def fwd(fn="nm_spmm_lora", n=2, m=4, R=8, K=32, X=16, ldx=8, T=8, A=16, B=16, rank=4, num=2, adapter=16, Y=16, ldy=8,
+            yt=0, values=16):
+        return getattr(L, fn)(values, 16, n, m, R, K, None, X, ldx, T, A, B, rank, num, None, adapter, Y, ldy, yt, None)
+
+    def grad(R=8, K=32, dY=16, lddy=8, X=16, ldx=8, T=8, A=16, B=16, rank=4, num=2, adapter=16, dA=16, dB=16, dt=0):
+        return L.nm_lora_grad(R, K, dY, lddy, X, ldx, T, A, B, rank, num, None, adapter, dA, dB, dt, None)
+
+    for fn in ("nm_spmm_lora", "nm_spmm_lora_t"):
+        for bad in (dict(n=4), dict(K=30), dict(R=-1), dict(T=-1), dict(rank=0), dict(num=-1), dict(yt=3), dict(Y=None),
+                    dict(ldy=7)):
+            assert fwd(fn, **bad) == I, (fn, bad)
+        assert fwd(fn, rank=129) == fwd(fn, num=32768) == U
+        assert fwd(fn, Y=8) == fwd(fn, ldy=12) == A16
+        assert fwd(fn, T=0) == nm.NM_OK
+    for bad in (dict(R=-1), dict(K=-1), dict(T=-1), dict(rank=0), dict(num=-1), dict(dt=2), dict(dA=None, dB=None),
+                dict(A=None), dict(B=None), dict(adapter=None), dict(dY=None), dict(X=None), dict(ldx=7), dict(lddy=7)):
+        assert grad(**bad) == I, bad
+    assert grad(rank=129) == grad(num=32768) == grad(T=1 << 31) == U
+    assert grad(dA=17) == grad(dt=1, dB=18) == grad(X=8) == grad(lddy=12) == grad(A=17) == A16
+    assert grad(num=0) == nm.NM_OK

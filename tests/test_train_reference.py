@@ -56,3 +56,15 @@ def test_cross_entropy_gradient_against_differences():
     want[5, 2] -= 1
     want *= torch.where((target >= 0) & (target < 6), dloss, 0.0)
     assert torch.allclose(G, want, rtol=1e-12, atol=1e-14)
+
+
+def test_adapter_gradients_against_differences():
+    w, x, dy = rand(5, 6, seed=11), rand(6, 4, seed=12), rand(5, 4, seed=13)
+    A, B, scale = rand(3, 2, 6, seed=14), rand(3, 5, 2, seed=15), rand(3, seed=16)
+    adapter, idx = torch.tensor([2, 0, -1, 2]), torch.tensor([3, 0, 5, 1, 2, 4])
+    f = lambda: (ref.lora(w, x[idx], A, B, adapter, scale, x) * dy).sum()  # noqa: E731
+    for grad, at in zip(ref.lora_grad(dy, w, x, A, B, adapter, scale, idx), (x, A, B)):
+        assert torch.allclose(grad, differences(f, at), rtol=1e-6, atol=1e-7)
+    t = 0  # one token written out
+    want = w @ x[idx][:, t] + scale[2] * B[2] @ (A[2] @ x[:, t])
+    assert torch.allclose(ref.lora(w, x[idx], A, B, adapter, scale, x)[:, t], want, rtol=1e-13, atol=1e-13)

@@ -50,3 +50,19 @@ def cross_entropy_grad(w, x, target, dloss):
     z = w @ x
     loss, _ = cross_entropy(z, target)
     return torch.autograd.grad((loss * dloss).sum(), (z, x, w))
+
+
+def lora(w, x, A, B, adapter, scale=None, low_x=None):
+    """w x + scale_a B_a A_a low_x column by column (float64); low_x: the adapters' input, x by default."""
+    y, z = w @ x, x if low_x is None else low_x
+    for a in range(A.shape[0]):
+        serves = (adapter == a).to(torch.float64)
+        y = y + (1.0 if scale is None else scale[a]) * (B[a] @ (A[a] @ z)) * serves
+    return y
+
+
+def lora_grad(dy, w, x, A, B, adapter, scale=None, idx=None):
+    """(dX, dA, dB) of <dy, lora> by autograd, x before the index map."""
+    x, A, B = (v.detach().clone().requires_grad_() for v in (x, A, B))
+    y = lora(w, x if idx is None else x[idx], A, B, adapter, scale, x)
+    return torch.autograd.grad((y * dy).sum(), (x, A, B), allow_unused=True, materialize_grads=True)
