@@ -276,6 +276,7 @@ struct GemmRequest {
   // allocation-free entry point for shapes it does not chunk itself
   bool allow_staging = true;
   GemmPartials* partials = nullptr;  // set: a split-K GEMM leaves its partial sums there
+  const PairEpiData* epi = nullptr;  // set: the SM-pair kernel's epilogue (on a shape that kernel serves)
 };
 
 // Split of the K stages for the skinny kernel: the number of ranges that
@@ -570,7 +571,9 @@ static nm_status run_gemm(const GemmRequest& q, cudaStream_t stream) {
       st = make_tmap(&p.tm_vals, vals, (uint64_t)p.vcols, (uint64_t)q.R, (uint64_t)p.vcols * 2, 64, kPairBoxRows,
                      128, "values");
     if (st == NM_OK && !dense_pair) st = make_meta_tmap(&p.tm_meta, meta, p.meta_rblocks, p.meta_cblocks);
-    if (st == NM_OK && !use_skinny) st = make_pair_store_maps(p, q.Y, q.R, q.T, q.ldy, p.out_f32 != 0);
+    if (q.epi) p.epi = *q.epi;
+    if (st == NM_OK && !use_skinny && p.epi.mode != PAIR_EPI_LSE)
+      st = make_pair_store_maps(p, q.Y, q.R, q.T, q.ldy, p.out_f32 != 0);
     if (!use_skinny && !dense_pair) p.n_major = pair_n_major(q.R, p.vcols, q.K, q.T);
     if (st == NM_OK)
       e = use_skinny   ? launch_spmm_skinny(p, stream)
@@ -932,6 +935,20 @@ nm_status spmm_rows(const uint16_t* values, const uint32_t* meta, int n, int m, 
                     const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, nm_out_dtype y_dtype,
                     cudaStream_t stream) {
   return run_gemm(gemm_request(values, meta, n, m, R, K, nullptr, X, ldx, T, Y, ldy, y_dtype), stream);
+}
+
+bool spmm_pair_serves(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t K, int64_t T) {
+  return K % 128 == 0 && T >= 192 && T % 8 == 0 && ((n == 2 && m == 4) ? al16(values) && al16(meta) : fits_2of4(n, m));
+}
+
+nm_status run_spmm_epilogue(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                            const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, const PairEpiData& epi,
+                            cudaStream_t stream) {
+  // no Y: the checks want a pointer, which nothing is written to
+  GemmRequest q = gemm_request(values, meta, n, m, R, K, nullptr, X, ldx, T, Y ? Y : epi.part, Y ? ldy : (T + 7) / 8 * 8,
+                               NM_OUT_BF16);
+  q.epi = &epi;
+  return run_gemm(q, stream);
 }
 
 nm_status dense_t_accumulate(const uint16_t* W, int64_t ldw, int64_t R, int64_t K, const uint16_t* D, int64_t ldd,

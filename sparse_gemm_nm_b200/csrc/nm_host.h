@@ -48,6 +48,12 @@ nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m,
 nm_status spmm_rows(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
                     const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, nm_out_dtype y_dtype,
                     cudaStream_t stream);
+// Does the SM-pair 2:4 kernel serve the shape (directly, or after re-encoding)?  Only then run_spmm_epilogue: the
+// product with one of that kernel's epilogues (Y null where the epilogue stores none).
+bool spmm_pair_serves(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t K, int64_t T);
+nm_status run_spmm_epilogue(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
+                            const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, const PairEpiData& epi,
+                            cudaStream_t stream);
 // nm_sddmm.
 nm_status run_sddmm(const uint32_t* meta, int n, int m, int64_t R, int64_t K, const int32_t* idx, const uint16_t* dY,
                     int64_t lddy, const uint16_t* X, int64_t ldx, int64_t T, void* dV, nm_out_dtype dtype,

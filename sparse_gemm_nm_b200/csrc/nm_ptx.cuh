@@ -409,6 +409,26 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "memory");
 }
 
+// 16 lanes x 32 consecutive 32-bit columns, laid out like the accumulator of a warp-level m16n8 MMA: for each 8
+// columns, thread i gets lane i / 4 (then lane i / 4 + 8) at columns 2 (i % 4) and 2 (i % 4) + 1.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 2^x by the special-function unit (relative error about 2^-22; results below the normal range become 0).
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Shared-memory matrix descriptor (sm_100 layout): start, leading and stride
 // byte offsets (16-byte units), descriptor version 1, swizzle mode in [61,64).
 // Layout type of a shared-memory matrix descriptor (bits 61-63).  SWZ_128B_BASE32B is the 128-byte

@@ -21,6 +21,23 @@ constexpr uint32_t kPairBoxRows = 64;
 
 enum Pattern : int { PAT_2_4 = 0, PAT_1_2 = 1, PAT_1_4 = 2, PAT_1_8 = 3, PAT_2_8 = 4, PAT_OTHER = 5 };
 
+// What the SM-pair 2:4 kernel does with a tile of Y = W' X.
+enum PairEpi : int {
+  PAIR_EPI_Y = 0,      // stores it
+  PAIR_EPI_LSE = 1,    // Y are logits (rows: the vocabulary): one (max, sum of exponentials) pair per 32 rows and column
+  PAIR_EPI_XGRAD = 2   // Y are logits: stores the gradient d (exp(y - lse) - [row == target]) as bf16
+};
+// Per-column data of the last two, each padded with anything to a whole number of tiles and on 16 bytes.
+struct PairEpiData {
+  int mode;
+  float2* part;         // LSE: [ceil(R / 32)][T], (max, sum 2^(y log2 e - max)), the max times log2 e
+  float* z_target;      // LSE: y[target] of the columns whose target lies in the rows
+  const int32_t* target;  // the column's row (relative to the whole vocabulary), negative for none
+  const float* lse2;    // XGRAD: lse times log2 e
+  const float* d;       // XGRAD: the column's factor, 0 for a column without a target
+  int64_t row0;         // row 0 of Y within the vocabulary
+};
+
 struct SpmmParams {
   CUtensorMap tm_vals;  // compressed values R x K*n/m, box {32, 128} 64B swizzle (one SM) or {64, kPairBoxRows} 128B (SM pair)
   CUtensorMap tm_w;     // dense W R x K, box {64, 128}, 128B swizzle (hybrid)
@@ -59,6 +76,7 @@ struct SpmmParams {
   int kt_per_split;
   int bn;
   int kd;  // skinny stage depth (logical K per stage: 128 or 256)
+  PairEpiData epi;
   float* ws;
   int keep_partials;  // leave the ranges' sums in ws (no reduction launch)
   // fused prune + compress + GEMM: optional outputs of the compressed operand

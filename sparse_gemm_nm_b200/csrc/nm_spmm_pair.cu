@@ -112,7 +112,119 @@ struct Cfg {
 };
 }  // namespace pair
 
-template <bool HYB, bool DB, bool I8, bool TF32>
+// (max, sum) of two sets of terms as one; maxima and exponents in powers of two.
+__device__ __forceinline__ void join_pair(float& m, float& s, float m2, float s2) {
+  const float top = fmaxf(m, m2);
+  s = s * exp2_fast(m - top) + s2 * exp2_fast(m2 - top);
+  m = top;
+}
+
+// Log-sum-exp epilogue of one warp's 32 rows x NB * 32 columns of logits in TMEM.  The 16-lane TMEM load gives a
+// thread four rows of eight columns of each 32-column block, so a column's pair is four exponentials against the
+// thread's own maximum, then three exchanges between lanes that halve the columns a lane keeps (7 joins a block);
+// a butterfly over the 32 rows of the one-row-per-lane layout would take 31.  `release` is called after the last TMEM load.
+template <int NB, typename Release>
+__device__ __forceinline__ void lse_epilogue(const SpmmParams& p, uint32_t t_addr, int64_t wrow0, int64_t n0, int lane,
+                                             Release release) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const bool ragged = wrow0 + 32 > p.R;
+#pragma unroll 1
+  for (int c = 0; c < NB; ++c) {
+    uint32_t lo[16], hi[16];
+    tmem_ld_16x256b_x4(t_addr + c * 32, lo);
+    tmem_ld_16x256b_x4(t_addr + (16u << 16) + c * 32, hi);
+    const int64_t t0 = n0 + 32 * c;
+    const int32_t want = t0 < p.T ? __ldg(p.epi.target + t0 + lane) : -1;
+    tc_wait_ld();
+    if (c == NB - 1) release();
+    if (t0 >= p.T || wrow0 >= p.R) continue;
+    if (ragged) {  // rows past R are no logits
+      const int64_t left = p.R - wrow0 - (lane >> 2);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (left <= ((i & 2) ? 8 : 0)) lo[i] = 0xFF800000u;
+        if (left <= ((i & 2) ? 24 : 16)) hi[i] = 0xFF800000u;
+      }
+    }
+    // a column whose target is one of the 32 rows: rare, so found by a vote
+    const uint32_t at = (uint32_t)(want - p.epi.row0 - wrow0);
+    unsigned votes = __ballot_sync(0xFFFFFFFFu, want >= 0 && at < 32u && t0 + lane < p.T);
+    while (votes) {
+      const int col = __ffs(votes) - 1;
+      votes &= votes - 1;
+      const int row = (int)__shfl_sync(0xFFFFFFFFu, at, col);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int ccol = 8 * (i >> 2) + 2 * (lane & 3) + (i & 1), crow = (lane >> 2) + 8 * ((i >> 1) & 1);
+        if (ccol == col && crow == row) p.epi.z_target[t0 + col] = __uint_as_float(lo[i]);
+        if (ccol == col && crow + 16 == row) p.epi.z_target[t0 + col] = __uint_as_float(hi[i]);
+      }
+    }
+    float m[8], s[8];  // column v: block of eight v / 2, parity v % 2
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const int i = 4 * (v >> 1) + (v & 1);
+      const float z0 = __uint_as_float(lo[i]), z1 = __uint_as_float(lo[i + 2]);
+      const float z2 = __uint_as_float(hi[i]), z3 = __uint_as_float(hi[i + 2]);
+      m[v] = fmaxf(fmaxf(fmaxf(z0, z1), fmaxf(z2, z3)), -3.0e38f) * kLog2e;
+      m[v] = fmaxf(m[v], -3.0e38f);  // finite: (-inf) - (-inf) must not arise
+      s[v] = (exp2_fast(fmaf(z0, kLog2e, -m[v])) + exp2_fast(fmaf(z1, kLog2e, -m[v]))) +
+             (exp2_fast(fmaf(z2, kLog2e, -m[v])) + exp2_fast(fmaf(z3, kLog2e, -m[v])));
+    }
+#pragma unroll
+    for (int half = 4; half > 0; half >>= 1) {
+      const bool up = (lane & (half * 4)) != 0;  // keeps the upper half of the columns
+#pragma unroll
+      for (int v = 0; v < half; ++v) {
+        const float send_m = up ? m[v] : m[v + half], send_s = up ? s[v] : s[v + half];
+        const float got_m = __shfl_xor_sync(0xFFFFFFFFu, send_m, half * 4);
+        const float got_s = __shfl_xor_sync(0xFFFFFFFFu, send_s, half * 4);
+        float km = up ? m[v + half] : m[v], ks = up ? s[v + half] : s[v];
+        join_pair(km, ks, got_m, got_s);
+        m[v] = km;
+        s[v] = ks;
+      }
+    }
+    const int v = ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+    const int64_t t = t0 + 8 * (v >> 1) + 2 * (lane & 3) + (v & 1);
+    if (t < p.T) p.epi.part[(wrow0 >> 5) * p.T + t] = make_float2(m[0], s[0]);
+  }
+}
+
+// The gradient of 32 columns of one logits row per lane: v becomes d (exp(v - lse) - [row == target]).
+__device__ __forceinline__ void xgrad_block(const SpmmParams& p, uint32_t (&v)[32], int64_t wrow0, int64_t t0, int lane) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const int32_t want = __ldg(p.epi.target + t0 + lane);
+  const uint32_t at = (uint32_t)(want - p.epi.row0 - wrow0);
+  const float4* l4 = reinterpret_cast<const float4*>(p.epi.lse2 + t0);
+  const float4* d4 = reinterpret_cast<const float4*>(p.epi.d + t0);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float4 l = __ldg(l4 + q);
+    v[4 * q] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(v[4 * q]), kLog2e, -l.x)));
+    v[4 * q + 1] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(v[4 * q + 1]), kLog2e, -l.y)));
+    v[4 * q + 2] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(v[4 * q + 2]), kLog2e, -l.z)));
+    v[4 * q + 3] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(v[4 * q + 3]), kLog2e, -l.w)));
+  }
+  if (__ballot_sync(0xFFFFFFFFu, want >= 0 && at < 32u)) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const int32_t w = __shfl_sync(0xFFFFFFFFu, want, j);
+      const uint32_t row = __shfl_sync(0xFFFFFFFFu, at, j);
+      if (w >= 0 && row == (uint32_t)lane) v[j] = __float_as_uint(__uint_as_float(v[j]) - 1.f);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float4 d = __ldg(d4 + q);  // 0 for a column without a target, whatever its logits are
+    v[4 * q] = d.x == 0.f ? 0u : __float_as_uint(__uint_as_float(v[4 * q]) * d.x);
+    v[4 * q + 1] = d.y == 0.f ? 0u : __float_as_uint(__uint_as_float(v[4 * q + 1]) * d.y);
+    v[4 * q + 2] = d.z == 0.f ? 0u : __float_as_uint(__uint_as_float(v[4 * q + 2]) * d.z);
+    v[4 * q + 3] = d.w == 0.f ? 0u : __float_as_uint(__uint_as_float(v[4 * q + 3]) * d.w);
+  }
+}
+
+template <bool HYB, bool DB, bool I8, bool TF32, int EPI = PAIR_EPI_Y>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     spmm_pair_kernel(const __grid_constant__ SpmmParams p) {
   using namespace pair;
@@ -317,7 +429,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       tc_fence_after();
       const uint32_t t_addr = tmem_base + 256u * (uint32_t)acc + ((uint32_t)(quarter * 32) << 16);
       const uint32_t lead_acc_empty = lead_acc_empty0 + 8u * (uint32_t)acc;
-      if (DB && !p.out_f32) {
+      if constexpr (EPI == PAIR_EPI_LSE) {
+        lse_epilogue<(int)(C::kN / 32)>(p, t_addr, (int64_t)tm * 256 + 128 * rank + quarter * 32, n0, lane, [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead_acc_empty);
+        });
+      } else if constexpr (EPI == PAIR_EPI_XGRAD) {
+        // Chunks of 64 columns (a last one of 32 in the 224-column form) become gradients in registers and leave
+        // through the staging buffer.  The last two stay packed in registers until the accumulator is released,
+        // so that only one earlier store's read of the buffer is waited for before that.
+        constexpr int kChunks = (int)((C::kN + 63) / 64);
+        const int32_t wrow0 = (int32_t)(tm * 256 + 128 * rank + quarter * 32);
+        uint8_t* ebuf = smem + L.epi + quarter * (C::kEpiBufs * kEpi);
+        uint32_t w[2][32];
+        auto take = [&](int c, uint32_t (&out)[32]) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (C::kN == 224u && c == kChunks - 1 && h == 1) break;
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(t_addr + c * 64 + 32 * h, v);
+            tc_wait_ld();
+            if (n0 + 64 * c + 32 * h < p.T) xgrad_block(p, v, wrow0, n0 + 64 * c + 32 * h, lane);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              out[16 * h + j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+          }
+        };
+        auto put = [&](int c, const uint32_t (&out)[32]) {
+          if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the buffer
+          __syncwarp();
+          const bool narrow = C::kN == 224u && c == kChunks - 1;  // 32 columns: 64-byte rows, unswizzled
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (narrow && j >= 4) break;
+            *reinterpret_cast<uint4*>(narrow ? ebuf + lane * 64 + (j << 4) : ebuf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && n0 + 64 * c < p.T && wrow0 < p.R) {
+            tma_store_2d(narrow ? &p.tm_y32 : &p.tm_y, ebuf, (int32_t)(n0 + 64 * c), wrow0);
+            bulk_commit_group();
+          }
+        };
+#pragma unroll
+        for (int c = 0; c < kChunks - 2; ++c) {
+          take(c, w[0]);
+          put(c, w[0]);
+        }
+        take(kChunks - 2, w[0]);
+        take(kChunks - 1, w[1]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead_acc_empty);
+        put(kChunks - 2, w[0]);
+        put(kChunks - 1, w[1]);
+      } else if (DB && !p.out_f32) {
         // Column chunks of 64, 64, 64 and 32 through the warp's staging buffer,
         // one TMA store each (the last through the 32-column map tm_y32).  The
         // accumulator is released after the last TMEM load; the next tile's MMAs
@@ -465,7 +633,7 @@ bool pair_kernel_fits(const SpmmParams& p) {
   return p.a_mode == A_TMA_SPARSE && p.K % 128 == 0 && p.K > 0 && p.T >= 192 && p.R >= 1 && p.T % 8 == 0;
 }
 
-template <bool HYB, bool DB, bool I8 = false, bool TF32 = false>
+template <bool HYB, bool DB, bool I8 = false, bool TF32 = false, int EPI = PAIR_EPI_Y>
 static cudaError_t launch_pair(SpmmParams& p, cudaStream_t stream) {
   constexpr pair::Layout L = pair::Cfg<HYB, DB, I8, TF32>::layout();
   const size_t bytes = L.total + 1024;
@@ -473,7 +641,7 @@ static cudaError_t launch_pair(SpmmParams& p, cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !configured[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(spmm_pair_kernel<HYB, DB, I8, TF32>,
+    cudaError_t e = cudaFuncSetAttribute(spmm_pair_kernel<HYB, DB, I8, TF32, EPI>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
@@ -481,7 +649,7 @@ static cudaError_t launch_pair(SpmmParams& p, cudaStream_t stream) {
   const int pairs_avail = sm_count_current() / 2;
   const int pairs = p.num_tiles < pairs_avail ? p.num_tiles : pairs_avail;
   cudaError_t e =
-      launch_pdl(spmm_pair_kernel<HYB, DB, I8, TF32>, dim3(2 * pairs), dim3(pair::kThreads), bytes, stream, p);
+      launch_pdl(spmm_pair_kernel<HYB, DB, I8, TF32, EPI>, dim3(2 * pairs), dim3(pair::kThreads), bytes, stream, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -499,8 +667,12 @@ cudaError_t launch_spmm_pair(SpmmParams& p, cudaStream_t stream) {
   if (p.k_tiles <= kDbMaxStages) {
     p.tiles_n = (int)((p.T + 223) / 224);
     p.num_tiles = p.tiles_m * p.tiles_n;
+    if (p.epi.mode == PAIR_EPI_LSE) return launch_pair<false, true, false, false, PAIR_EPI_LSE>(p, stream);
+    if (p.epi.mode == PAIR_EPI_XGRAD) return launch_pair<false, true, false, false, PAIR_EPI_XGRAD>(p, stream);
     return launch_pair<false, true>(p, stream);
   }
+  if (p.epi.mode == PAIR_EPI_LSE) return launch_pair<false, false, false, false, PAIR_EPI_LSE>(p, stream);
+  if (p.epi.mode == PAIR_EPI_XGRAD) return launch_pair<false, false, false, false, PAIR_EPI_XGRAD>(p, stream);
   return launch_pair<false, false>(p, stream);
 }
 

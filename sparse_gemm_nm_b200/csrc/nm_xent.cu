@@ -28,36 +28,43 @@
 namespace nmk {
 
 namespace xent {
-constexpr int kPairRows = 256;  // logits rows joined into one (max, sum) pair
+constexpr int kPairRows = 256;  // logits rows joined into one (max, sum) pair by xent_pairs_kernel
 constexpr float kLog2e = 1.4426950408889634f;
 }  // namespace xent
 
-// part[pair][t] = (max, sum exp(z - max)) over one pair's rows of the logits
-// piece; the rows of targets write their logit.  One block: 32 tokens, one pair.
-__global__ void __launch_bounds__(256) xent_pairs_kernel(const float* Z, int64_t ldz, int64_t rows, int64_t T,
-                                                         int64_t v0, const int32_t* target, float2* part,
-                                                         float* z_target) {
+// part[pair][t] = (max, sum 2^(z log2 e - max)) over one pair's kPairRows rows of the logits piece, the max times log2 e;
+// the rows of targets write their logit.  Z is the sum of `splits` matrices.  One block: 32 tokens, one pair.
+__global__ void __launch_bounds__(256) xent_pairs_kernel(const float* Z, int splits, int64_t split_stride, int64_t ldz,
+                                                         int64_t rows, int64_t T, int64_t v0, const int32_t* target,
+                                                         float2* part, float* z_target) {
   using namespace xent;
   __shared__ float s_max[8][32], s_sum[8][32];
   pdl_gate();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * 32 + lane;
-  const int64_t r0 = (int64_t)blockIdx.y * kPairRows;
-  const int64_t r1 = r0 + kPairRows < rows ? r0 + kPairRows : rows;
-  float top = -INFINITY, sum = 0.f;
-  if (t < T) {
-    const int64_t want = (int64_t)__ldg(target + t) - v0;
-    for (int64_t r = r0 + warp; r < r1; r += 8) {
-      const float z = __ldcg(Z + r * ldz + t);
-      if (r == want) z_target[t] = z;
-      if (z > top) {
-        sum = sum * exp2f((top - z) * kLog2e) + 1.f;
-        top = z;
-      } else {
-        sum += exp2f((z - top) * kLog2e);
-      }
-    }
+  const int64_t r0 = (int64_t)blockIdx.y * kPairRows + warp;
+  constexpr int kEach = kPairRows / 8;  // rows of a warp, all loaded before the first exponential
+  float z[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int64_t r = r0 + 8 * i;
+    z[i] = t < T && r < rows ? __ldcg(Z + r * ldz + t) : -INFINITY;
   }
+  for (int q = 1; q < splits; ++q) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (t < T && r0 + 8 * i < rows) z[i] += __ldcg(Z + q * split_stride + (r0 + 8 * i) * ldz + t);
+  }
+  const int64_t want = t < T ? (int64_t)__ldg(target + t) - v0 - r0 : -1;
+  float top = -3.0e38f, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    top = fmaxf(top, z[i]);
+    if (want == 8 * i) z_target[t] = z[i];
+  }
+  top = fmaxf(top * kLog2e, -3.0e38f);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) sum += exp2_fast(fmaf(z[i], kLog2e, -top));
   s_max[warp][lane] = top;
   s_sum[warp][lane] = sum;
   __syncthreads();
@@ -65,28 +72,33 @@ __global__ void __launch_bounds__(256) xent_pairs_kernel(const float* Z, int64_t
     float m = s_max[0][lane];
     for (int w = 1; w < 8; ++w) m = fmaxf(m, s_max[w][lane]);
     float s = 0.f;
-    for (int w = 0; w < 8; ++w)
-      if (s_sum[w][lane] != 0.f) s += s_sum[w][lane] * exp2f((s_max[w][lane] - m) * kLog2e);
+    for (int w = 0; w < 8; ++w) s += s_sum[w][lane] * exp2_fast(s_max[w][lane] - m);
     part[(v0 / kPairRows + blockIdx.y) * T + t] = make_float2(m, s);
   }
 }
 
-// Joins a token's pairs: lse = M + log sum_p s_p exp(m_p - M), M the largest max.
-__global__ void __launch_bounds__(256) xent_join_kernel(const float2* part, int64_t pairs, int64_t R, int64_t T,
-                                                        const int32_t* target, const float* z_target, float* loss,
-                                                        float* lse) {
+// Joins a token's pairs: lse = (M + log2 sum_p s_p 2^(m_p - M)) log 2, M the largest max.
+__global__ void __launch_bounds__(1024) xent_join_kernel(const float2* part, int64_t pairs, int64_t R, int64_t T,
+                                                         const int32_t* target, const float* z_target, float* loss,
+                                                         float* lse) {
   using namespace xent;
-  __shared__ float s_max[8][32], s_sum[8][32];
+  __shared__ float s_max[32][33], s_sum[32][33];
   pdl_gate();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * 32 + lane;
-  float m = -INFINITY, s = 0.f;
+  float m = -3.0e38f, s = 0.f;
   if (t < T) {
-    for (int64_t p = warp; p < pairs; p += 8) {
-      const float2 q = __ldcg(part + p * T + t);
-      const float top = fmaxf(m, q.x);
-      if (s != 0.f) s *= exp2f((m - top) * kLog2e);
-      if (q.y != 0.f) s += q.y * exp2f((q.x - top) * kLog2e);  // not 0: a NaN logit's NaN is passed on
+    for (int64_t p0 = warp; p0 < pairs; p0 += 32 * 8) {  // eight pairs in flight
+      float2 q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        q[i] = p0 + 32 * i < pairs ? __ldcg(part + (p0 + 32 * i) * T + t) : make_float2(-3.0e38f, 0.f);
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, q[i].x);
+      s *= exp2_fast(m - top);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += q[i].y * exp2_fast(q[i].x - top);
       m = top;
     }
   }
@@ -95,14 +107,32 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2* part, int6
   __syncthreads();
   if (warp == 0 && t < T) {
     float top = s_max[0][lane];
-    for (int w = 1; w < 8; ++w) top = fmaxf(top, s_max[w][lane]);
+#pragma unroll
+    for (int w = 1; w < 32; ++w) top = fmaxf(top, s_max[w][lane]);
     float sum = 0.f;
-    for (int w = 0; w < 8; ++w)
-      if (s_sum[w][lane] != 0.f) sum += s_sum[w][lane] * exp2f((s_max[w][lane] - top) * kLog2e);
-    const float l = top + logf(sum);
+#pragma unroll
+    for (int w = 0; w < 32; ++w) sum += s_sum[w][lane] * exp2_fast(s_max[w][lane] - top);
+    const float l = (top + log2f(sum)) * 0.6931471805599453f;
     const int32_t want = __ldg(target + t);
     lse[t] = l;
     loss[t] = want >= 0 && (int64_t)want < R ? l - __ldcg(z_target + t) : 0.f;
+  }
+}
+
+// The SM-pair epilogues' per-token data, on 16 bytes and padded to `padded` tokens (no target, factor 0).
+__global__ void __launch_bounds__(256) xent_columns_kernel(const int32_t* target, const float* lse, const float* dloss,
+                                                           int64_t R, int64_t T, int64_t padded, int32_t* tgt,
+                                                           float* lse2, float* d) {
+  using namespace xent;
+  pdl_gate();
+  const int64_t t = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+  if (t >= padded) return;
+  const int32_t w = t < T ? __ldg(target + t) : -1;
+  const bool has = w >= 0 && (int64_t)w < R;
+  tgt[t] = has ? w : -1;
+  if (lse) {
+    lse2[t] = has ? __ldg(lse + t) * kLog2e : 0.f;
+    d[t] = has ? __ldg(dloss + t) : 0.f;
   }
 }
 
@@ -179,11 +209,11 @@ nm_status check_head(int n, int m, int64_t R, int64_t K, int64_t T) {
   return NM_OK;
 }
 
-// Rows of one piece: a multiple of 256 whose logits take about 64 MB, so that they stay in L2.
+// Rows of one piece: a multiple of 256 whose fp32 logits take about 64 MB (bf16 gradients 32 MB), so that they stay in L2.
 int64_t piece_rows(int64_t R, int64_t T) {
   int64_t rows = (16ll << 20) / (T > 0 ? T : 1) / 256 * 256;
   if (rows < 256) rows = 256;
-  if (rows > 8192) rows = 8192;
+  if (rows > (1 << 21)) rows = 1 << 21;  // the element-wise kernels' grids: 64 rows a block, 65535 blocks
   return rows < R ? rows : R;
 }
 
@@ -200,28 +230,65 @@ nm_status gather_input(Head& h, const int32_t* idx, Staged& staged, cudaStream_t
   return NM_OK;
 }
 
+// Per-token data of the SM-pair epilogues: [target | lse2 | d], each padded to whole tiles (256 and 224 columns).
+int64_t padded_tokens(int64_t T) { return (T + 255) / 256 * 256 + 256; }
+nm_status column_data(const Head& h, const int32_t* target, const float* lse, const float* dloss, PairEpiData& epi,
+                      Staged& staged, cudaStream_t s) {
+  const int64_t n = padded_tokens(h.T);
+  cudaError_t e = staged.get((size_t)(n * 4 * (lse ? 3 : 1)));
+  if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the token data");
+  int32_t* tgt = staged.as<int32_t>();
+  float* lse2 = staged.as<float>() + n;
+  e = launch_pdl(xent_columns_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, target, lse, dloss, h.R, h.T, n,
+                 tgt, lse2, lse2 + n);
+  count_launch();
+  epi.target = tgt;
+  epi.lse2 = lse2;
+  epi.d = lse2 + n;
+  return e == cudaSuccess ? NM_OK : cuda_fail(e, "token data launch");
+}
+
 nm_status run_xent(Head h, const int32_t* idx, const int32_t* target, float* loss, float* lse, cudaStream_t s) {
-  Staged xp(s), work(s), z(s);
+  Staged xp(s), work(s), z(s), ws(s), cols(s);
   nm_status st = gather_input(h, idx, xp, s);
   if (st != NM_OK) return st;
-  const int64_t pairs = (h.R + xent::kPairRows - 1) / xent::kPairRows;
-  const int64_t rows = piece_rows(h.R, h.T), ldz = (h.T + 3) / 4 * 4;
+  const bool fused = spmm_pair_serves(h.values, h.meta, h.n, h.m, h.K, h.T);
+  const int64_t per = fused ? 32 : xent::kPairRows;
+  const int64_t pairs = (h.R + per - 1) / per;
   cudaError_t e = work.get((size_t)(pairs * h.T * 8 + h.T * 4));
-  if (e == cudaSuccess) e = z.get((size_t)(rows * ldz * 4));
-  if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the logits piece");
+  if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the sums");
   float2* part = work.as<float2>();
   float* z_target = reinterpret_cast<float*>(part + pairs * h.T);
   const unsigned tb = (unsigned)((h.T + 31) / 32);
-  for (int64_t v0 = 0; v0 < h.R; v0 += rows) {
-    const int64_t n = h.R - v0 < rows ? h.R - v0 : rows;
-    st = spmm_rows(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, z.as<float>(), ldz, NM_OUT_F32, s);
+  if (fused) {  // the GEMM's epilogue leaves the pairs: no logits are written at all
+    PairEpiData epi = {};
+    epi.mode = PAIR_EPI_LSE;
+    epi.part = part;
+    epi.z_target = z_target;
+    st = column_data(h, target, nullptr, nullptr, epi, cols, s);
+    if (st == NM_OK)
+      st = run_spmm_epilogue(h.values, h.meta, h.n, h.m, h.R, h.K, h.X, h.ldx, h.T, nullptr, 0, epi, s);
     if (st != NM_OK) return st;
-    e = launch_pdl(xent_pairs_kernel, dim3(tb, (unsigned)((n + xent::kPairRows - 1) / xent::kPairRows)), dim3(256), 0,
-                   s, (const float*)z.as<float>(), ldz, n, h.T, v0, target, part, z_target);
-    count_launch();
-    if (e != cudaSuccess) return cuda_fail(e, "cross-entropy launch");
+  } else {
+    const int64_t rows = piece_rows(h.R, h.T), ldz = (h.T + 3) / 4 * 4;
+    e = z.get((size_t)(rows * ldz * 4));
+    if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the logits piece");
+    for (int64_t v0 = 0; v0 < h.R; v0 += rows) {
+      const int64_t n = h.R - v0 < rows ? h.R - v0 : rows;
+      ws.release();
+      GemmPartials raw{&ws, 1, 0, 0};
+      st = run_spmm(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, nullptr, h.X, h.ldx, h.T, z.as<float>(), ldz,
+                    NM_OUT_F32, &raw, s);
+      if (st != NM_OK) return st;
+      const bool split = raw.splits > 1;
+      e = launch_pdl(xent_pairs_kernel, dim3(tb, (unsigned)((n + per - 1) / per)), dim3(256), 0, s,
+                     (const float*)(split ? ws.as<float>() : z.as<float>()), raw.splits, raw.split_stride,
+                     split ? raw.ld : ldz, n, h.T, v0, target, part, z_target);
+      count_launch();
+      if (e != cudaSuccess) return cuda_fail(e, "cross-entropy launch");
+    }
   }
-  e = launch_pdl(xent_join_kernel, dim3(tb), dim3(256), 0, s, (const float2*)part, pairs, h.R, h.T, target,
+  e = launch_pdl(xent_join_kernel, dim3(tb), dim3(1024), 0, s, (const float2*)part, pairs, h.R, h.T, target,
                  (const float*)z_target, loss, lse);
   count_launch();
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "cross-entropy launch");
@@ -229,24 +296,37 @@ nm_status run_xent(Head h, const int32_t* idx, const int32_t* target, float* los
 
 nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const float* lse, const float* dloss,
                         uint16_t* dX, int64_t lddx, uint16_t* dV, cudaStream_t s) {
-  Staged xp(s), z(s), g(s), wd(s), acc(s);
+  Staged xp(s), z(s), g(s), wd(s), acc(s), cols(s);
   nm_status st = gather_input(h, idx, xp, s);
   if (st != NM_OK) return st;
   const int64_t rows = piece_rows(h.R, h.T), ldz = (h.T + 3) / 4 * 4, ldg = (h.T + 7) / 8 * 8;
   const int64_t ldk = (h.K + 7) / 8 * 8;
-  cudaError_t e = z.get((size_t)(rows * ldz * 4));
-  if (e == cudaSuccess) e = g.get((size_t)(rows * ldg * 2));
+  const bool fused = spmm_pair_serves(h.values, h.meta, h.n, h.m, h.K, h.T);
+  PairEpiData epi = {};
+  epi.mode = PAIR_EPI_XGRAD;
+  if (fused) st = column_data(h, target, lse, dloss, epi, cols, s);
+  if (st != NM_OK) return st;
+  cudaError_t e = g.get((size_t)(rows * ldg * 2));
+  if (e == cudaSuccess && !fused) e = z.get((size_t)(rows * ldz * 4));
   if (e == cudaSuccess && dX) e = wd.get((size_t)(rows * ldk * 2));
   if (e == cudaSuccess && dX) e = acc.get((size_t)(h.K * ldz * 4));
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gradient piece");
   for (int64_t v0 = 0; v0 < h.R; v0 += rows) {
     const int64_t n = h.R - v0 < rows ? h.R - v0 : rows;
-    st = spmm_rows(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, z.as<float>(), ldz, NM_OUT_F32, s);
-    if (st != NM_OK) return st;
-    e = launch_pdl(xent_g_kernel, dim3((unsigned)((ldg / 2 + 31) / 32), (unsigned)((n + 63) / 64)), dim3(256), 0, s,
-                   (const float*)z.as<float>(), ldz, n, h.T, h.R, v0, target, lse, dloss, g.as<uint16_t>(), ldg);
-    count_launch();
-    if (e != cudaSuccess) return cuda_fail(e, "cross-entropy gradient launch");
+    if (fused) {  // the GEMM's epilogue turns the logits into G
+      epi.row0 = v0;
+      st = run_spmm_epilogue(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, g.as<uint16_t>(), ldg,
+                             epi, s);
+      if (st != NM_OK) return st;
+    } else {
+      st = spmm_rows(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, z.as<float>(), ldz, NM_OUT_F32,
+                     s);
+      if (st != NM_OK) return st;
+      e = launch_pdl(xent_g_kernel, dim3((unsigned)((ldg / 2 + 31) / 32), (unsigned)((n + 63) / 64)), dim3(256), 0, s,
+                     (const float*)z.as<float>(), ldz, n, h.T, h.R, v0, target, lse, dloss, g.as<uint16_t>(), ldg);
+      count_launch();
+      if (e != cudaSuccess) return cuda_fail(e, "cross-entropy gradient launch");
+    }
     if (dX) {
       e = launch_decompress(h.row_values(v0), h.row_meta(v0), n, h.K, h.n, h.m, wd.as<uint16_t>(), ldk, s);
       if (e != cudaSuccess) return cuda_fail(e, "decompress launch");
