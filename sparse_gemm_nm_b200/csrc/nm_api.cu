@@ -303,6 +303,28 @@ static void choose_splits(SpmmParams& p, int sms) {
   p.kt_per_split = best_kps;
 }
 
+// The same when the caller reads the ranges' sums itself: every range then costs R * bn fp32 written and read, which
+// for many rows is more than an idle tail (32000 rows at bn = 64: 16 MB a range, against 148 MB of weights).  Takes
+// the least sum of weight bytes over the balance and bytes of sums.
+static void choose_splits_partials(SpmmParams& p, int sms) {
+  const int64_t kt = p.k_tiles;
+  const double weights = (double)p.R * (double)p.K * 1.125;
+  double best = 0.0;
+  for (int s = 1; s <= 16 && s <= kt; ++s) {
+    const int64_t kps = (kt + s - 1) / s;
+    if (kps < 2 && s > 1) break;
+    const int64_t se = (kt + kps - 1) / kps;
+    const int64_t units = (int64_t)p.tiles_m * se;
+    const int64_t waves = (units + sms - 1) / sms;
+    const double cost = weights * (double)(waves * sms) / (double)units + (double)se * (double)p.R * p.bn * 8.0;
+    if (s == 1 || cost < best) {
+      best = cost;
+      p.splits = (int)se;
+      p.kt_per_split = (int)kps;
+    }
+  }
+}
+
 // Argument checks of the sparse GEMM calls, in three steps so that every
 // entry point reports the same status and text for the same mistake:
 // shape/pattern/dtype, then the output (and a usable device), then the operands.
@@ -528,7 +550,10 @@ static nm_status run_gemm(const GemmRequest& q, cudaStream_t stream) {
         release();
         return fail(NM_ERR_UNSUPPORTED, "too many tiles");
       }
-      choose_splits(p, sm_count_current());
+      if (q.partials)
+        choose_splits_partials(p, sm_count_current());
+      else
+        choose_splits(p, sm_count_current());
       p.tiles_n = 1;
       p.num_tiles = p.tiles_m;
       if (p.splits > 1) {

@@ -664,15 +664,13 @@ static cudaError_t launch_pair(SpmmParams& p, cudaStream_t stream) {
 constexpr int64_t kDbMaxStages = 8;
 
 cudaError_t launch_spmm_pair(SpmmParams& p, cudaStream_t stream) {
-  if (p.k_tiles <= kDbMaxStages) {
+  if (p.k_tiles <= kDbMaxStages || p.epi.mode != PAIR_EPI_Y) {
     p.tiles_n = (int)((p.T + 223) / 224);
     p.num_tiles = p.tiles_m * p.tiles_n;
     if (p.epi.mode == PAIR_EPI_LSE) return launch_pair<false, true, false, false, PAIR_EPI_LSE>(p, stream);
     if (p.epi.mode == PAIR_EPI_XGRAD) return launch_pair<false, true, false, false, PAIR_EPI_XGRAD>(p, stream);
     return launch_pair<false, true>(p, stream);
   }
-  if (p.epi.mode == PAIR_EPI_LSE) return launch_pair<false, false, false, false, PAIR_EPI_LSE>(p, stream);
-  if (p.epi.mode == PAIR_EPI_XGRAD) return launch_pair<false, false, false, false, PAIR_EPI_XGRAD>(p, stream);
   return launch_pair<false, false>(p, stream);
 }
 

@@ -209,9 +209,10 @@ nm_status check_head(int n, int m, int64_t R, int64_t K, int64_t T) {
   return NM_OK;
 }
 
-// Rows of one piece: a multiple of 256 whose fp32 logits take about 64 MB (bf16 gradients 32 MB), so that they stay in L2.
-int64_t piece_rows(int64_t R, int64_t T) {
-  int64_t rows = (16ll << 20) / (T > 0 ? T : 1) / 256 * 256;
+// Rows of one piece: a multiple of 256 that takes about 64 MB (fp32 logits, or bf16 gradients where no logits are
+// written), so that it stays in L2.
+int64_t piece_rows(int64_t R, int64_t T, int64_t bytes = 4) {
+  int64_t rows = (64ll << 20) / bytes / (T > 0 ? T : 1) / 256 * 256;
   if (rows < 256) rows = 256;
   if (rows > (1 << 21)) rows = 1 << 21;  // the element-wise kernels' grids: 64 rows a block, 65535 blocks
   return rows < R ? rows : R;
@@ -299,9 +300,9 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
   Staged xp(s), z(s), g(s), wd(s), acc(s), cols(s);
   nm_status st = gather_input(h, idx, xp, s);
   if (st != NM_OK) return st;
-  const int64_t rows = piece_rows(h.R, h.T), ldz = (h.T + 3) / 4 * 4, ldg = (h.T + 7) / 8 * 8;
-  const int64_t ldk = (h.K + 7) / 8 * 8;
   const bool fused = spmm_pair_serves(h.values, h.meta, h.n, h.m, h.K, h.T);
+  const int64_t rows = piece_rows(h.R, h.T, fused ? 2 : 4), ldz = (h.T + 3) / 4 * 4, ldg = (h.T + 7) / 8 * 8;
+  const int64_t ldk = (h.K + 7) / 8 * 8;
   PairEpiData epi = {};
   epi.mode = PAIR_EPI_XGRAD;
   if (fused) st = column_data(h, target, lse, dloss, epi, cols, s);
