@@ -192,10 +192,49 @@ nm_status make_tmap(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t 
   return NM_OK;
 }
 
+nm_status make_tmap3(CUtensorMap* tm, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
+                     uint32_t b0, uint32_t b1, int swizzle_bytes, const char* what) {
+  const TmapKey key{base, d0, d1, d2, s1, s2, b0, b1, 1, swizzle_bytes, (int)CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3};
+  if (t_tmaps.find(key, tm)) return NM_OK;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(NM_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[3] = {d0, d1, d2};
+  cuuint64_t strides[2] = {s1, s2};
+  cuuint32_t box[3] = {b0, b1, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUtensorMapSwizzle swz = swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                           : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                           : swizzle_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                 : CU_TENSOR_MAP_SWIZZLE_NONE;
+  CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(NM_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", what, (int)r);
+  t_tmaps.put(key, *tm);
+  return NM_OK;
+}
+
+// Maps of a GEMM's further reduction steps (boxes of 64 x 64).
+template <typename Params>
+static nm_status set_ext(Params& p, const GemmExt& x, int64_t T) {
+  p.ext_planes = x.planes;
+  p.ext_cat = x.cat;
+  p.ext_masks = x.masks;
+  nm_status st = make_tmap(&p.tm_xa, x.left, (uint64_t)x.cols, (uint64_t)x.rows, (uint64_t)x.ldl * 2, 64, 64, 128,
+                           "adapter matrix");
+  if (st == NM_OK)
+    st = make_tmap(&p.tm_xs, x.terms, (uint64_t)T, (uint64_t)(x.planes * x.cat), (uint64_t)x.ldp * 2, 64, 64, 128,
+                   "adapter blocks");
+  return st;
+}
+
 // Whole-line TMA stores for the dense pair kernel's plain epilogue: C is rows x cols with row stride ldo
-// elements (bf16, or four-byte values when wide); the caller has checked 16-byte rows.
+// elements (bf16, or four-byte values when wide); the caller has checked 16-byte rows.  A TMA store writes whole
+// 16-byte units, so rows that end inside one would lose what the caller keeps behind their last column: those are
+// stored element by element from registers.
 static nm_status set_store_map(DenseParams& p, void* out, int64_t rows, int64_t cols, int64_t ldo, bool wide) {
-  p.tma_store = 1;
+  p.tma_store = cols % (wide ? 4 : 8) == 0 ? 1 : 0;
+  if (!p.tma_store) return NM_OK;
   return wide ? make_tmap(&p.tm_out, out, (uint64_t)cols, (uint64_t)rows, (uint64_t)ldo * 4, 32, 32, 128,
                           "C (four-byte)", CU_TENSOR_MAP_DATA_TYPE_FLOAT32)
               : make_tmap(&p.tm_out, out, (uint64_t)cols, (uint64_t)rows, (uint64_t)ldo * 2, 64, 32, 128, "C (bf16)");
@@ -276,6 +315,7 @@ struct GemmRequest {
   // allocation-free entry point for shapes it does not chunk itself
   bool allow_staging = true;
   GemmPartials* partials = nullptr;  // set: a split-K GEMM leaves its partial sums there
+  const GemmExt* ext = nullptr;      // set: further reduction steps (on a shape the SM-pair kernel serves)
   const PairEpiData* epi = nullptr;  // set: the SM-pair kernel's epilogue (on a shape that kernel serves)
 };
 
@@ -597,6 +637,7 @@ static nm_status run_gemm(const GemmRequest& q, cudaStream_t stream) {
                      128, "values");
     if (st == NM_OK && !dense_pair) st = make_meta_tmap(&p.tm_meta, meta, p.meta_rblocks, p.meta_cblocks);
     if (q.epi) p.epi = *q.epi;
+    if (st == NM_OK && q.ext) st = set_ext(p, *q.ext, q.T);
     if (st == NM_OK && !use_skinny && p.epi.mode != PAIR_EPI_LSE)
       st = make_pair_store_maps(p, q.Y, q.R, q.T, q.ldy, p.out_f32 != 0);
     if (!use_skinny && !dense_pair) p.n_major = pair_n_major(q.R, p.vcols, q.K, q.T);
@@ -950,9 +991,10 @@ nm_status check_spmm(const uint16_t* values, const uint32_t* meta, int n, int m,
 
 nm_status run_spmm(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
                    const int32_t* idx, const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy,
-                   nm_out_dtype y_dtype, GemmPartials* partials, cudaStream_t stream) {
+                   nm_out_dtype y_dtype, GemmPartials* partials, cudaStream_t stream, const GemmExt* ext) {
   GemmRequest q = gemm_request(values, meta, n, m, R, K, idx, X, ldx, T, Y, ldy, y_dtype);
   q.partials = partials;
+  q.ext = ext;
   return run_gemm(q, stream);
 }
 
@@ -996,7 +1038,7 @@ nm_status dense_t_accumulate(const uint16_t* W, int64_t ldw, int64_t R, int64_t 
   p.add = add ? 1 : 0;
   nm_status st = make_tmap(&p.tm_a, W, (uint64_t)K, (uint64_t)R, (uint64_t)ldw * 2, 64, 64, 128, "W' (dense)");
   if (st == NM_OK) st = make_tmap(&p.tm_b, D, (uint64_t)T, (uint64_t)R, (uint64_t)ldd * 2, 64, 64, 128, "dY");
-  if (st == NM_OK) st = set_store_map(p, C, K, T, ldc, true);
+  if (st == NM_OK) st = set_store_map(p, C, K, ldc, ldc, true);  // ldc % 4 == 0; columns past T add zeros
   if (st != NM_OK) return st;
   cudaError_t e = launch_dense_pair(p, true, true, EPI_STORE, stream);
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "transposed GEMM launch");
@@ -1021,7 +1063,7 @@ nm_status check_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int 
 
 nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
                             const int32_t* idx, const uint16_t* dY, int64_t lddy, int64_t T, void* dX, int64_t lddx,
-                            nm_out_dtype dtype, cudaStream_t stream) {
+                            nm_out_dtype dtype, cudaStream_t stream, const GemmExt* ext) {
   t_last_error.clear();
   nm_status st = check_spmm_t(values, meta, n, m, R, K, dY, lddy, T, dX, lddx, dtype);
   if (st != NM_OK || K == 0 || T == 0) return st;
@@ -1060,6 +1102,7 @@ nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m,
   if (e == cudaSuccess && st == NM_OK)
     st = make_tmap(&p.tm_b, dY, (uint64_t)T, (uint64_t)R, (uint64_t)lddy * 2, 64, 64, 128, "dY");
   if (e == cudaSuccess && st == NM_OK && !idx) st = set_store_map(p, dX, K, T, lddx, p.out_f32 != 0);
+  if (e == cudaSuccess && st == NM_OK && ext) st = set_ext(p, *ext, T);
   if (e == cudaSuccess && st == NM_OK) e = launch_dense_pair(p, true, true, EPI_STORE, stream);
   cudaFreeAsync(wd, stream);
   if (st != NM_OK) return st;

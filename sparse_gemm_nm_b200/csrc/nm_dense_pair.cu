@@ -71,12 +71,15 @@ __device__ __forceinline__ int64_t survivor_col(const DenseParams& p, int64_t r,
 
 // I8: signed int8 operands and int32 accumulation (kind::i8).  A stage then holds 256 reduction steps in
 // the same bytes: A K-major as two 128-byte halves, B MN-major as one 128-column strip of 256 rows.
-template <bool A_MN, bool B_MN, int EPI, bool I8 = false, bool TF32 = false>
+// EXT (both operands MN-major): a tile's last stages are further reduction steps, a block of 64 rows of tm_xa against
+// that block of two planes of tm_xs (a plane past the last reads as zeros), for the blocks that its columns use.
+template <bool A_MN, bool B_MN, int EPI, bool I8 = false, bool TF32 = false, bool EXT = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
     dense_pair_kernel(const __grid_constant__ DenseParams p) {
   using namespace dpair;
   static_assert(!I8 || (!A_MN && B_MN), "int8: K-major A and MN-major B");
   static_assert(!TF32 || (!A_MN && B_MN && !I8), "tf32: K-major A and MN-major B");
+  static_assert(!EXT || (A_MN && B_MN && !I8 && !TF32), "further reduction steps: MN-major bf16 operands");
   constexpr uint32_t kIdesc = I8     ? idesc_s8_major(256, 256, A_MN, B_MN)
                               : TF32 ? idesc_tf32_major(256, 256, A_MN, B_MN)
                                      : idesc_bf16_major(256, 256, A_MN, B_MN);
@@ -129,6 +132,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
   const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
   const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
   bool ok = true;
+  auto ext_blocks = [&](int tn) -> uint32_t {  // the blocks that column tile tn's four 64-token tiles use
+    uint32_t m = 0;
+    for (int64_t i = (int64_t)tn * 4; i < (int64_t)tn * 4 + 4 && i * 64 < p.N; ++i) m |= __ldg(p.ext_masks + i);
+    return m;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------- copies
@@ -193,6 +201,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
           }
           if (++s == kStages) { s = 0; ph ^= 1u; }
         }
+        if (EXT && ok) {
+          for (uint32_t left = ext_blocks(tn); left && ok; left &= left - 1) {
+            const int32_t k0 = 64 * (__ffs(left) - 1);
+            for (int pl = 0; pl < p.ext_planes; pl += 2) {
+              ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
+              if (!ok) break;
+              const uint32_t bar = lead_full0 + 8u * s;
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], kTx);
+              uint8_t* a = smem + s * (kA + kB);
+              uint8_t* b = a + kA;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int32_t plane0 = (int32_t)((pl + h < p.ext_planes ? pl + h : p.ext_planes) * p.ext_cat);
+                  tma_load_2d_pair(a + i * 16384 + h * 8192, &p.tm_xa, bar, m0 + 64 * i, k0);
+                  tma_load_2d_pair(b + i * 16384 + h * 8192, &p.tm_xs, bar, n0 + 64 * i,
+                                   pl + h < p.ext_planes ? plane0 + k0 : plane0);
+                }
+              }
+              if (++s == kStages) { s = 0; ph ^= 1u; }
+            }
+          }
+        }
       }
     }
   } else if (warp == 1) {
@@ -207,7 +239,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + 256u * (uint32_t)ab;
-        for (int64_t kt = 0; kt < p.k_tiles; ++kt) {
+        int64_t k_tiles = p.k_tiles;
+        if (EXT)
+          k_tiles += (int64_t)__popc(ext_blocks(p.n_major ? tile % p.tiles_n : tile / p.tiles_m)) * ((p.ext_planes + 1) / 2);
+        for (int64_t kt = 0; kt < k_tiles; ++kt) {
           ok = mbar_wait(&full[s], ph, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           tc_fence_after();
@@ -414,13 +449,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
   }
 }
 
-template <bool A_MN, bool B_MN, int EPI, bool I8 = false, bool TF32 = false>
+template <bool A_MN, bool B_MN, int EPI, bool I8 = false, bool TF32 = false, bool EXT = false>
 static cudaError_t launch_dp(const DenseParams& p, cudaStream_t stream) {
   static std::atomic<bool> configured[64];  // zero-initialised: false
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !configured[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(dense_pair_kernel<A_MN, B_MN, EPI, I8, TF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(dense_pair_kernel<A_MN, B_MN, EPI, I8, TF32, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)dpair::kSmemBytes);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
@@ -432,7 +467,7 @@ static cudaError_t launch_dp(const DenseParams& p, cudaStream_t stream) {
   // HBM about once (a float32 W' of 11008 x 4096 is 180 MB, above the 126 MB L2); otherwise row tiles.
   DenseParams q = p;
   q.n_major = p.M > p.N ? 1 : 0;
-  cudaError_t e = launch_pdl(dense_pair_kernel<A_MN, B_MN, EPI, I8, TF32>, dim3(2 * pairs), dim3(dpair::kThreads),
+  cudaError_t e = launch_pdl(dense_pair_kernel<A_MN, B_MN, EPI, I8, TF32, EXT>, dim3(2 * pairs), dim3(dpair::kThreads),
                              (size_t)dpair::kSmemBytes, stream, q);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -440,6 +475,10 @@ static cudaError_t launch_dp(const DenseParams& p, cudaStream_t stream) {
 
 cudaError_t launch_dense_pair(const DenseParams& p, bool a_mn, bool b_mn, int epi, cudaStream_t stream) {
   if (p.num_tiles <= 0) return cudaSuccess;
+  if (p.ext_planes) {
+    if (!a_mn || !b_mn || epi != EPI_STORE) return cudaErrorInvalidValue;
+    return launch_dp<true, true, EPI_STORE, false, false, true>(p, stream);
+  }
   if (a_mn && b_mn && epi == EPI_STORE) return launch_dp<true, true, EPI_STORE>(p, stream);
   if (!a_mn && !b_mn && epi == EPI_SURVIVORS) return launch_dp<false, false, EPI_SURVIVORS>(p, stream);
   if (!a_mn && b_mn && epi == EPI_STORE) return launch_dp<false, true, EPI_STORE>(p, stream);

@@ -22,7 +22,23 @@ nm_status make_tmap(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t 
                     uint32_t box_inner, uint32_t box_outer, int swizzle_bytes, const char* what,
                     CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 
+// 3-D map of {d0, d1, d2} bf16 with strides s1 and s2 bytes, boxes {b0, b1, 1}.
+nm_status make_tmap3(CUtensorMap* tm, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
+                     uint32_t b0, uint32_t b1, int swizzle_bytes, const char* what);
+
 class Staged;
+
+// Further dense reduction steps of a GEMM: blocks of 64 rows of `terms` (planes x cat rows x T, row stride ldp) against
+// the same 64 columns of `left` (forward: R x cat, K-major) or rows (input gradient: cat x K); a column tile takes the
+// blocks in the masks of its 64-token tiles.  left: rows x cols, row stride ldl.
+struct GemmExt {
+  const uint16_t* left;
+  int64_t rows, cols, ldl;
+  const uint16_t* terms;
+  int64_t cat, ldp;
+  int planes;
+  const uint32_t* masks;
+};
 
 // Where a split-K GEMM may leave its fp32 partial sums instead of adding them up: `splits` matrices (1: the result
 // is in Y as usual), `split_stride` elements apart, rows of `ld`.
@@ -37,13 +53,13 @@ nm_status check_spmm(const uint16_t* values, const uint32_t* meta, int n, int m,
                      const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, nm_out_dtype y_dtype);
 nm_status run_spmm(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
                    const int32_t* idx, const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy,
-                   nm_out_dtype y_dtype, GemmPartials* partials, cudaStream_t stream);
+                   nm_out_dtype y_dtype, GemmPartials* partials, cudaStream_t stream, const GemmExt* ext = nullptr);
 // nm_spmm_t: the argument checks alone, and the call.
 nm_status check_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
                        const uint16_t* dY, int64_t lddy, int64_t T, void* dX, int64_t lddx, nm_out_dtype dtype);
 nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
                      const int32_t* idx, const uint16_t* dY, int64_t lddy, int64_t T, void* dX, int64_t lddx,
-                     nm_out_dtype dtype, cudaStream_t stream);
+                     nm_out_dtype dtype, cudaStream_t stream, const GemmExt* ext = nullptr);
 // Y = W' X (nm_spmm).
 nm_status spmm_rows(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
                     const uint16_t* X, int64_t ldx, int64_t T, void* Y, int64_t ldy, nm_out_dtype y_dtype,

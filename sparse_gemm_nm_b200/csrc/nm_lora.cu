@@ -12,9 +12,14 @@
 // select, not a multiplication by 0), so an Inf or NaN of one request reaches no
 // other request.  Requests side by side have one or two adapters in a tile;
 // tokens in any order, up to 64.
-// S and U stay fp32 in memory.  As MMA operands they are split into two bf16
-// terms (three for fp32 results): 2^-17 (2^-25) of a value is lost instead of
-// the 2^-9 of one rounding.  Sums over a reduction leave the MMA accumulator
+// Where the SM-pair GEMM serves the projection (and for every input gradient),
+// the expand product is not a pass of its own: the adapters' second factors
+// stand side by side in one matrix, shrink leaves s_a S as blocks that are 0
+// outside an adapter's tokens, and the GEMM takes the blocks that a column tile
+// uses as further reduction steps, so Y is rounded once and written once.
+// S and U are fp32 sums.  As MMA operands they are split into two bf16 terms
+// (three for fp32 results): 2^-17 (2^-25) of a value is lost instead of the 2^-9
+// of one rounding.  Sums over a reduction leave the MMA accumulator
 // every 128 steps and add up in fp32 registers, since the accumulator
 // truncates; the CTAs of a cluster share a reduction and join in rank order, so
 // results repeat bit for bit.
@@ -36,14 +41,18 @@ constexpr int kStages = 3;
 constexpr uint32_t kZBytes = kDepth * kTok * 2;
 constexpr uint32_t kMBytes = kRankBlock * kDepth * 2;
 constexpr uint32_t kShrinkPart = 2 * kRankBlock * (kTok + 1) * 4;
-constexpr uint32_t kShrinkSmem = kStages * (kZBytes + kMBytes) + kShrinkPart;
+constexpr uint32_t kShrinkSmem = kStages * (kZBytes + kMBytes) + kShrinkPart + 1024;
 constexpr int kRows = 128;       // rows of an expand or outer tile
+constexpr int kExpandStages = 4; // adapters in flight
 constexpr int kOuterRank = 64;   // rank columns of an outer work item
-constexpr int kOuterStages = 4;
+constexpr int kOuterStages = 3;
 constexpr uint32_t kOuterM = kRows * kTok * 2;
 constexpr uint32_t kOuterV = kTok * kOuterRank * 2;  // one bf16 term
-constexpr uint32_t kOuterSmem = kOuterStages * kOuterM + 3 * kOuterV;
+__host__ __device__ constexpr uint32_t outer_smem(int planes) {
+  return kOuterStages * (kOuterM + (uint32_t)planes * kOuterV) + 1024;
+}
 static_assert(kRows * (kOuterRank + 1) * 4 <= kOuterStages * kOuterM, "the joined sums reuse the stages");
+constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -90,30 +99,36 @@ __device__ __forceinline__ void stage16(uint8_t* dst, const uint16_t* src, int64
   }
 }
 
-// The tile's token adapters (-1: none) and the distinct ones in order of first appearance; all threads call it.
+// The tile's token adapters (-1: none) and the distinct ones, the first half's before the second's; all threads call
+// it, the first warp works: matches within each half, then the first half's adapters are struck from the second's.
 __device__ __forceinline__ int tile_adapters(const int32_t* adapter, int64_t n, int64_t t0, int64_t T, int32_t* s_id,
                                              int32_t* s_list, int* s_count) {
-  const int tid = threadIdx.x;
-  int32_t id = -1;
-  if (tid < kTok) {
-    if (adapter && t0 + tid < T) id = __ldg(adapter + t0 + tid);
-    if (id < 0 || (int64_t)id >= n) id = -1;
-    s_id[tid] = id;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int32_t id[2];
+    bool first[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      id[h] = adapter && t0 + 32 * h + lane < T ? __ldg(adapter + t0 + 32 * h + lane) : -1;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (id[h] < 0 || (int64_t)id[h] >= n) id[h] = -1;
+      s_id[32 * h + lane] = id[h];
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, id[h]);  // every lane takes part, those without an adapter too
+      first[h] = id[h] >= 0 && __ffs(same) - 1 == lane;
+    }
+    const unsigned f0 = __ballot_sync(0xFFFFFFFFu, first[0]);
+    for (unsigned left = f0; left; left &= left - 1)
+      if (__shfl_sync(0xFFFFFFFFu, id[0], __ffs(left) - 1) == id[1]) first[1] = false;
+    const unsigned f1 = __ballot_sync(0xFFFFFFFFu, first[1]);
+    const unsigned below = (1u << lane) - 1u;
+    if (first[0]) s_list[__popc(f0 & below)] = id[0];
+    if (first[1]) s_list[__popc(f0) + __popc(f1 & below)] = id[1];
+    if (lane == 0) *s_count = __popc(f0) + __popc(f1);
   }
   __syncthreads();
-  unsigned firsts = 0;
-  bool first = false;
-  if (tid < kTok) {
-    first = id >= 0;
-    for (int j = 0; j < tid; ++j)
-      if (s_id[j] == id) first = false;
-    firsts = __ballot_sync(0xFFFFFFFFu, first);
-    if ((tid & 31) == 0) s_count[tid >> 5] = __popc(firsts);
-  }
-  __syncthreads();
-  if (first) s_list[(tid >= 32 ? s_count[0] : 0) + __popc(firsts & ((1u << (tid & 31)) - 1u))] = id;
-  __syncthreads();
-  return s_count[0] + s_count[1];
+  return *s_count;
 }
 
 // The bf16 terms of v: term p is the rounding of what the terms before it left over.
@@ -123,98 +138,126 @@ __device__ __forceinline__ void split_terms(float v, uint16_t (&term)[P]) {
   for (int p = 0; p < P; ++p) {
     const uint32_t b = pack_bf16x2(v, 0.f) & 0xFFFFu;
     term[p] = (uint16_t)b;
-    v -= __uint_as_float(b << 16);
+    v = (b & 0x7F80u) == 0x7F80u ? 0.f : v - __uint_as_float(b << 16);  // nothing is left over of an Inf or NaN
   }
 }
 }  // namespace lora
 
-template <bool TRANS>
-__global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const LoraShrink p) {
+template <bool TRANS, int OUT, int P>
+__global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __grid_constant__ LoraShrink p) {
   using namespace lora;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ int32_t s_id[kTok], s_list[kTok];
-  __shared__ int s_count[2];
+  __shared__ int s_count, s_abort;
+  __shared__ uint32_t s_present[kMaxCat / 32];
+  __shared__ uint64_t s_full[kStages];
   float* s_part = reinterpret_cast<float*>(smem + kStages * (kZBytes + kMBytes));  // [K half][32 ranks][65]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&s_full[i], 1);
+    s_abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    if (p.D > 0) tma_prefetch_desc(&p.tm_z);
+    if (p.vec) tma_prefetch_desc(&p.tm_m);
+  }
   pdl_gate();
+  if (p.inv) {
+    const int64_t all = (int64_t)gridDim.x * gridDim.y * kThreads;
+    for (int64_t k = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + tid; k < p.idx_n; k += all) {
+      const int32_t j = __ldg(p.idx + k);
+      if (j >= 0 && (int64_t)j < p.idx_n) atomicMax(p.inv + j, (int32_t)k);
+    }
+  }
   const uint32_t rank = cluster_ctarank();
   const int C = p.cluster;
-  const int64_t t0 = (int64_t)(blockIdx.x / C) * kTok;
-  const int distinct = tile_adapters(p.adapter, p.n, t0, p.T, s_id, s_list, s_count);
+  const int64_t tile = blockIdx.x / C;
+  const int64_t t0 = tile * kTok;
+  const int distinct = tile_adapters(p.adapter, p.n, t0, p.T, s_id, s_list, &s_count);
   const int rblocks = (p.rank + kRankBlock - 1) / kRankBlock;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int half = warp & 1, group = warp >> 1;  // K half of a stage, group of 16 tokens
   const int rs = (p.rank + 15) / 16 * 16;
-  const int64_t chunks = (p.D + kDepth - 1) / kDepth;
-  const int64_t mine = chunks > rank ? (chunks - rank + C - 1) / C : 0;  // chunks rank, rank + C, ...
+  const int chunks = (int)((p.D + kDepth - 1) / kDepth);
+  const int mine = chunks > (int)rank ? (chunks - (int)rank + C - 1) / C : 0;  // chunks rank, rank + C, ...
+  int use = 0;  // stages taken so far: ring slot use % kStages, phase use / kStages
 
   for (int item = blockIdx.y; item < distinct * rblocks; item += gridDim.y) {
     const int32_t a = s_list[item / rblocks];
     const int j0 = (item % rblocks) * kRankBlock;
-    auto load = [&](int64_t i) {
-      uint8_t* z = smem + (i % kStages) * (kZBytes + kMBytes);
+    const int live = p.rank - j0 < kRankBlock ? p.rank - j0 : kRankBlock;
+    auto load = [&](int i) {  // all threads; chunk i of this CTA into ring slot (use + i) % kStages
+      const int slot = (use + i) % kStages;
+      uint8_t* z = smem + slot * (kZBytes + kMBytes);
       uint8_t* m = z + kZBytes;
-      const int64_t d0 = (rank + i * C) * kDepth;
-#pragma unroll
-      for (int u = tid; u < kDepth * 8; u += kThreads) {  // 128 rows of eight 16-byte units
-        const int row = u >> 3, c = u & 7;
-        const int64_t d = d0 + row;
-        const int64_t valid = d < p.D ? p.T - (t0 + 8 * c) : 0;
-        cp_async_16(z + row * 128 + ((c ^ (row & 7)) << 4), valid > 0 ? p.Z + d * p.ldz + t0 + 8 * c : p.Z,
-                    (uint32_t)(2 * (valid < 0 ? 0 : valid > 8 ? 8 : valid)));
+      const int d0 = ((int)rank + i * C) * kDepth;
+      if (tid == 0) {
+        mbar_arrive_expect_tx(&s_full[slot], kZBytes + (p.vec ? kMBytes : 0u));
+        tma_load_2d(z, &p.tm_z, &s_full[slot], (int32_t)t0, d0);
+        if (p.vec) {
+          if (TRANS) {
+            tma_load_3d(m, &p.tm_m, &s_full[slot], j0, d0, a);
+          } else {
+            tma_load_3d(m, &p.tm_m, &s_full[slot], d0, j0, a);
+            tma_load_3d(m + kMBytes / 2, &p.tm_m, &s_full[slot], d0 + kDepth / 2, j0, a);
+          }
+        }
       }
-#pragma unroll
-      for (int u = tid; u < kRankBlock * 16; u += kThreads) {
-        if (!TRANS) {  // 32 rank rows of sixteen units
-          const int j = u >> 4, c = u & 15;
-          const int64_t valid = j0 + j < p.rank ? p.D - (d0 + 8 * c) : 0;
-          const uint16_t* src = p.M + ((int64_t)a * p.rank + j0 + j) * p.D + d0 + 8 * c;
-          stage16(m + j * 256 + ((c ^ (j & 7)) << 4), valid > 0 ? src : p.M, valid, p.vec);
-        } else {  // 128 reduction rows of four units
-          const int row = u >> 2, c = u & 3;
-          const int64_t valid = d0 + row < p.D ? p.rank - (j0 + 8 * c) : 0;
-          const uint16_t* src = p.M + ((int64_t)a * p.D + d0 + row) * p.rank + j0 + 8 * c;
-          stage16(m + row * 64 + ((c ^ ((row >> 1) & 3)) << 4), valid > 0 ? src : p.M, valid, p.vec);
+      if (!p.vec) {  // rows off 16 bytes: element by element; read at the earliest after two more barriers
+        for (int u = tid; u < kRankBlock * 16; u += kThreads) {
+          if (!TRANS) {
+            const int j = u >> 4, c = u & 15;
+            const int64_t valid = j < live ? p.D - (d0 + 8 * c) : 0;
+            stage16(m + (c >> 3) * (kMBytes / 2) + j * 128 + (((c & 7) ^ (j & 7)) << 4),
+                    p.M + ((int64_t)a * p.rank + j0 + j) * p.D + d0 + 8 * c, valid, 0);
+          } else {
+            const int row = u >> 2, c = u & 3;
+            const int64_t valid = d0 + row < p.D ? p.rank - (j0 + 8 * c) : 0;
+            stage16(m + row * 64 + ((c ^ ((row >> 1) & 3)) << 4),
+                    p.M + ((int64_t)a * p.D + d0 + row) * p.rank + j0 + 8 * c, valid, 0);
+          }
         }
       }
     };
-    bool active = false;  // does any of this warp's 16 tokens use the adapter?
-    for (int j = 0; j < 16; ++j) active |= s_id[16 * group + j] == a;
-
-    float sum[2][2][4] = {};
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (i < mine) load(i);
-      cp_commit();
+    unsigned serves;  // does any of this warp's 16 tokens use the adapter?
+    {
+      const unsigned lo = __ballot_sync(0xFFFFFFFFu, s_id[lane] == a), hi = __ballot_sync(0xFFFFFFFFu, s_id[32 + lane] == a);
+      serves = ((group & 2 ? hi : lo) >> (16 * (group & 1))) & 0xFFFFu;
     }
-    for (int64_t i = 0; i < mine; ++i) {
-      cp_wait<kStages - 2>();
-      __syncthreads();
+    float sum[2][2][4] = {};
+    for (int i = 0; i < kStages - 1 && i < mine; ++i) load(i);
+    for (int i = 0; i < mine; ++i) {
+      const int slot = (use + i) % kStages;
+      mbar_wait(&s_full[slot], (uint32_t)((use + i) / kStages) & 1u, &s_abort, p.status, kWaitNs);
+      __syncthreads();  // the slot of chunk i - 1 is free, and element-wise loads have landed
       if (i + kStages - 1 < mine) load(i + kStages - 1);
-      cp_commit();
-      if (!active) continue;
-      const uint32_t z = smem_u32(smem + (i % kStages) * (kZBytes + kMBytes)), m = z + kZBytes;
+      if (!serves) continue;
+      const uint32_t z = smem_u32(smem + slot * (kZBytes + kMBytes)), m = z + kZBytes;
       float acc[2][2][4] = {};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int ks = 4 * half + q, mi = lane >> 3, l8 = lane & 7;
-        uint32_t b[4], w[2][4];
+        uint32_t b[4], w[4];
         const int zr = 16 * ks + 8 * (mi & 1) + l8;
         ldmatrix_x4_trans(b, z + zr * 128 + (((2 * group + (mi >> 1)) ^ (zr & 7)) << 4));
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
+          if (16 * mt >= live) continue;
           if (!TRANS) {
             const int j = 16 * mt + 8 * (mi & 1) + l8;
-            ldmatrix_x4(w[mt], m + j * 256 + (((2 * ks + (mi >> 1)) ^ (j & 7)) << 4));
+            ldmatrix_x4(w, m + half * (kMBytes / 2) + j * 128 + (((2 * q + (mi >> 1)) ^ (j & 7)) << 4));
           } else {
             const int row = 16 * ks + 8 * (mi >> 1) + l8;
-            ldmatrix_x4_trans(w[mt], m + row * 64 + (((2 * mt + (mi & 1)) ^ ((row >> 1) & 3)) << 4));
+            ldmatrix_x4_trans(w, m + row * 64 + (((2 * mt + (mi & 1)) ^ ((row >> 1) & 3)) << 4));
           }
-          mma_bf16(acc[mt][0], w[mt], b[0], b[1]);
-          mma_bf16(acc[mt][1], w[mt], b[2], b[3]);
+          mma_bf16(acc[mt][0], w, b[0], b[1]);
+          mma_bf16(acc[mt][1], w, b[2], b[3]);
         }
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) sum[e >> 3][(e >> 2) & 1][e & 3] += acc[e >> 3][(e >> 2) & 1][e & 3];
     }
+    use += mine;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -226,18 +269,67 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const LoraS
         }
     __syncthreads();
     if (C > 1) cluster_sync();  // every CTA's sums are written
+    // The token-major forms take the ranks of a token side by side, the block form the tokens of a rank row.
     for (int e = tid + kThreads * (int)rank; e < kRankBlock * kTok; e += kThreads * C) {
-      const int j = e & (kRankBlock - 1), t = e / kRankBlock;
-      if (s_id[t] != a || j0 + j >= rs) continue;
-      float v = 0.f;
-      for (int c = 0; c < C; ++c) {
+      const int j = OUT == SHRINK_BLOCKS ? e / kTok : e % kRankBlock, t = OUT == SHRINK_BLOCKS ? e % kTok : e / kRankBlock;
+      const bool own = s_id[t] == a;
+      if (OUT == SHRINK_BLOCKS ? (j >= live || t0 + t >= p.ldp) : (!own || j0 + j >= rs)) continue;
+      float part[8][2];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        if (c >= C) continue;
         const uint32_t at = map_to_cta(smem_u32(s_part + j * (kTok + 1) + t), c);
-        v += ld_cluster_f32(at) + ld_cluster_f32(at + kRankBlock * (kTok + 1) * 4);
+        part[c][0] = ld_cluster_f32(at);
+        part[c][1] = ld_cluster_f32(at + kRankBlock * (kTok + 1) * 4);
       }
-      p.S[(t0 + t) * rs + j0 + j] = v;
+      float v = 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < C) v += part[c][0] + part[c][1];
+      if (OUT == SHRINK_F32) {
+        p.S[(t0 + t) * rs + j0 + j] = v;
+      } else {
+        if (OUT == SHRINK_BLOCKS && p.scale) v *= __ldg(p.scale + a);
+        uint16_t term[P];
+        split_terms<P>(v, term);
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+          if (OUT == SHRINK_TERMS)
+            p.terms[((int64_t)q * p.T + t0 + t) * rs + j0 + j] = term[q];
+          else
+            p.terms[((int64_t)q * p.cat + (int64_t)a * p.rank + j0 + j) * p.ldp + t0 + t] = own ? term[q] : (uint16_t)0;
+        }
+      }
     }
     if (C > 1) cluster_sync();  // the sums may be overwritten, and a CTA may leave
     __syncthreads();
+  }
+
+  if (OUT == SHRINK_BLOCKS && blockIdx.y == 0) {  // the rows of adapters that the tile does not use, and the tile's mask
+    if (tid < kMaxCat / 32) s_present[tid] = 0;
+    __syncthreads();
+    if (tid < distinct) {
+      const int32_t a = s_list[tid];
+      if (a < kMaxCat) atomicOr(&s_present[a >> 5], 1u << (a & 31));
+    }
+    __syncthreads();
+    for (int64_t u = tid + kThreads * (int64_t)rank; u < p.cat * 8; u += (int64_t)kThreads * C) {
+      const int row = (int)(u >> 3), c = (int)(u & 7);
+      const int a = row / p.rank;
+      if (a < p.n && ((s_present[a >> 5] >> (a & 31)) & 1u)) continue;
+      if (t0 + 8 * c >= p.ldp) continue;
+#pragma unroll
+      for (int q = 0; q < P; ++q)
+        *reinterpret_cast<uint4*>(p.terms + ((int64_t)q * p.cat + row) * p.ldp + t0 + 8 * c) = make_uint4(0, 0, 0, 0);
+    }
+    if (rank == 0 && tid == 0) {
+      uint32_t mask = 0;
+      for (int i = 0; i < distinct; ++i) {
+        const int first = (int)s_list[i] * p.rank / 64, last = ((int)s_list[i] * p.rank + p.rank - 1) / 64;
+        for (int b = first; b <= last; ++b) mask |= 1u << b;
+      }
+      p.masks[tile] = mask;
+    }
   }
 }
 
@@ -246,19 +338,48 @@ __global__ void __launch_bounds__(lora::kThreads) lora_expand_kernel(const LoraE
   using namespace lora;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int32_t s_id[kTok], s_list[kTok];
-  __shared__ int s_count[2];
+  __shared__ int s_count;
   pdl_gate();
   const int rs = (p.rank + 15) / 16 * 16;
   const uint32_t pitch = (uint32_t)rs * 2 + 16;  // an odd number of 16-byte units: eight rows miss each other's banks
   const uint32_t m_bytes = TRANS ? (uint32_t)rs * 256u : kRows * pitch;
-  uint8_t* s_m = smem;                // two buffers of one adapter's tile
-  uint8_t* s_s = smem + 2 * m_bytes;  // P terms of 64 tokens x rs
+  uint8_t* s_m = smem;                            // kExpandStages adapters' tiles
+  uint8_t* s_s = smem + kExpandStages * m_bytes;  // P terms of 64 tokens x rs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t r0 = (int64_t)blockIdx.x * kRows, t0 = (int64_t)blockIdx.y * kTok;
-  const int distinct = tile_adapters(p.adapter, p.n, t0, p.T, s_id, s_list, s_count);
+
+  // The base first: it needs nothing else, and its loads are in flight behind the rest.
+  float acc[8][4];
+  const int tokens = p.T - t0 < kTok ? (int)(p.T - t0) : kTok;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t row = r0 + 16 * warp + (lane >> 2) + 8 * h;
+    int64_t brow = row < p.rows ? row : -1;
+    if (p.base_row && brow >= 0) brow = __ldg(p.base_row + row);
+    const float* src = p.base + brow * p.ldb + t0 + 2 * (lane & 3);
+#pragma unroll
+    for (int nb = 0; nb < 8; ++nb) {
+      const bool in = brow >= 0 && 8 * nb + 2 * (lane & 3) < tokens;
+      const float2 v = in ? __ldcg(reinterpret_cast<const float2*>(src + 8 * nb)) : make_float2(0.f, 0.f);
+      acc[nb][2 * h] = v.x;
+      acc[nb][2 * h + 1] = v.y;
+    }
+    for (int q = 1; q < p.splits; ++q) {
+      src += p.split_stride;
+#pragma unroll
+      for (int nb = 0; nb < 8; ++nb) {
+        if (brow >= 0 && 8 * nb + 2 * (lane & 3) < tokens) {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(src + 8 * nb));
+          acc[nb][2 * h] += v.x;
+          acc[nb][2 * h + 1] += v.y;
+        }
+      }
+    }
+  }
+  const int distinct = tile_adapters(p.adapter, p.n, t0, p.T, s_id, s_list, &s_count);
 
   auto load = [&](int i) {
-    uint8_t* m = s_m + (i & 1) * m_bytes;
+    uint8_t* m = s_m + (i % kExpandStages) * m_bytes;
     const int64_t a = s_list[i];
     if (!TRANS) {
       const int units = rs / 8;
@@ -276,40 +397,46 @@ __global__ void __launch_bounds__(lora::kThreads) lora_expand_kernel(const LoraE
       }
     }
   };
-  if (distinct > 0) load(0);
-  cp_commit();
+#pragma unroll
+  for (int i = 0; i < kExpandStages - 1; ++i) {
+    if (i < distinct) load(i);
+    cp_commit();
+  }
   // s_a S of the tile's tokens as P bf16 terms (0 for a token without an adapter, whose S is not written)
-  for (int u = tid; u < kTok * rs; u += kThreads) {
-    const int t = u / rs, j = u - t * rs;
+  for (int u = tid; u < tokens * (rs / 4); u += kThreads) {
+    const int t = u / (rs / 4), j = 4 * (u - t * (rs / 4));
     const int32_t id = s_id[t];
-    const float v = id >= 0 ? __ldcg(p.S + (t0 + t) * rs + j) * (p.scale ? __ldg(p.scale + id) : 1.f) : 0.f;
-    uint16_t term[P];
-    split_terms<P>(v, term);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (id >= 0) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(p.S + (t0 + t) * rs + j));
+      const float sc = p.scale ? __ldg(p.scale + id) : 1.f;
+      v[0] = x.x * sc;
+      v[1] = x.y * sc;
+      v[2] = x.z * sc;
+      v[3] = x.w * sc;
+    }
+    uint16_t term[4][P];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_terms<P>(v[e], term[e]);
 #pragma unroll
     for (int q = 0; q < P; ++q)
-      *reinterpret_cast<uint16_t*>(s_s + ((uint32_t)q * kTok + t) * pitch + 2 * j) = term[q];
+      *reinterpret_cast<uint2*>(s_s + ((uint32_t)q * kTok + t) * pitch + 2 * j) =
+          make_uint2((uint32_t)term[0][q] | (uint32_t)term[1][q] << 16, (uint32_t)term[2][q] | (uint32_t)term[3][q] << 16);
   }
 
-  float acc[8][4] = {};
   for (int i = 0; i < distinct; ++i) {
-    if (i + 1 < distinct) load(i + 1);
+    cp_wait<kExpandStages - 2>();
+    __syncthreads();  // the tile of adapter i has landed (and S, at first); that of adapter i - 1 is free
+    if (i + kExpandStages - 1 < distinct) load(i + kExpandStages - 1);
     cp_commit();
-    cp_wait<1>();
-    __syncthreads();
     const int32_t a = s_list[i];
-    const uint32_t m = smem_u32(s_m + (i & 1) * m_bytes);
-    uint32_t used = 0;  // pairs of 8-token blocks with a token of the adapter
-    {
-      const unsigned lo = __ballot_sync(0xFFFFFFFFu, s_id[lane] == a), hi = __ballot_sync(0xFFFFFFFFu, s_id[32 + lane] == a);
-      for (int b = 0; b < 2; ++b) {
-        if (lo & (0xFFFFu << (16 * b))) used |= 1u << b;
-        if (hi & (0xFFFFu << (16 * b))) used |= 4u << b;
-      }
-    }
+    const uint32_t m = smem_u32(s_m + (i % kExpandStages) * m_bytes);
+    const unsigned lo = __ballot_sync(0xFFFFFFFFu, s_id[lane] == a), hi = __ballot_sync(0xFFFFFFFFu, s_id[32 + lane] == a);
     const int mi = lane >> 3, l8 = lane & 7;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      if (!(used & (1u << b))) continue;
+      const unsigned used = ((b & 2 ? hi : lo) >> (16 * (b & 1))) & 0xFFFFu;  // this block's tokens of the adapter
+      if (!used) continue;
       float d[2][4] = {};
       for (int ks = 0; ks < rs / 16; ++ks) {
         uint32_t w[4];
@@ -331,40 +458,29 @@ __global__ void __launch_bounds__(lora::kThreads) lora_expand_kernel(const LoraE
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (s_id[16 * b + 8 * h + 2 * (lane & 3) + (e & 1)] == a) acc[2 * b + h][e] += d[h][e];
+          if ((used >> (8 * h + 2 * (lane & 3) + (e & 1))) & 1u) acc[2 * b + h][e] += d[h][e];
     }
-    __syncthreads();
   }
 
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int64_t row = r0 + 16 * warp + (lane >> 2) + 8 * h;
     if (row >= p.rows) continue;
-    const int64_t brow = p.base_row ? (int64_t)__ldg(p.base_row + row) : row;
+    const int64_t at = row * p.ldy + t0 + 2 * (lane & 3);
 #pragma unroll
     for (int nb = 0; nb < 8; ++nb) {
-      const int64_t t = t0 + 8 * nb + 2 * (lane & 3);
-      if (t >= p.T) continue;
-      float2 v = make_float2(0.f, 0.f);
-      if (brow >= 0) {
-        for (int q = 0; q < p.splits; ++q) {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(p.base + q * p.split_stride + brow * p.ldb + t));
-          v.x += x.x;
-          v.y += x.y;
-        }
-      }
-      v.x += acc[nb][2 * h];
-      v.y += acc[nb][2 * h + 1];
+      const int t = 8 * nb + 2 * (lane & 3);
+      if (t >= tokens) continue;
       if (p.out_f32) {
-        float* y = static_cast<float*>(p.Y) + row * p.ldy + t;
-        if (t + 1 < p.T)
-          *reinterpret_cast<float2*>(y) = v;
+        float* y = static_cast<float*>(p.Y) + at + 8 * nb;
+        if (t + 1 < tokens)
+          *reinterpret_cast<float2*>(y) = make_float2(acc[nb][2 * h], acc[nb][2 * h + 1]);
         else
-          *y = v.x;
+          *y = acc[nb][2 * h];
       } else {
-        uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.ldy + t;
-        const uint32_t w = pack_bf16x2(v.x, v.y);
-        if (t + 1 < p.T)
+        uint16_t* y = static_cast<uint16_t*>(p.Y) + at + 8 * nb;
+        const uint32_t w = pack_bf16x2(acc[nb][2 * h], acc[nb][2 * h + 1]);
+        if (t + 1 < tokens)
           *reinterpret_cast<uint32_t*>(y) = w;
         else
           *y = (uint16_t)(w & 0xFFFFu);
@@ -373,31 +489,124 @@ __global__ void __launch_bounds__(lora::kThreads) lora_expand_kernel(const LoraE
   }
 }
 
-// The tiles that hold tokens of adapter blockIdx.x, ascending, and their number.
-__global__ void __launch_bounds__(256) lora_plan_kernel(const int32_t* adapter, int64_t T, int32_t* tiles,
-                                                        int32_t* counts) {
+// The second factors of all adapters side by side (see LoraCat).
+template <bool BY_RANK>
+__global__ void __launch_bounds__(256) lora_cat_kernel(const LoraCat p) {
+  pdl_gate();
+  const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, all = (int64_t)gridDim.x * blockDim.x;
+  if (p.inv)
+    for (int64_t k = first; k < p.rows; k += all) p.inv[k] = -1;
+  const int live = (int)p.n * p.rank;
+  const int64_t lines = BY_RANK ? live : p.rows, units = p.ldc / 8;
+  bool bad = false;
+  for (int64_t u = first; u < lines * units; u += all) {
+    const int64_t line = u / units;
+    const int64_t c = (u - line * units) * 8;
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint32_t v = 0;
+      if (BY_RANK) {
+        if (c + e < p.rows) {
+          const int64_t k = p.idx ? (int64_t)__ldg(p.idx + c + e) : c + e;
+          if (k >= 0 && k < p.rows) v = __ldg(p.M + line * p.rows + k);
+        }
+      } else if (c + e < live) {
+        const int col = (int)c + e, a = col / p.rank;
+        v = __ldg(p.M + ((int64_t)a * p.rows + line) * p.rank + col - a * p.rank);
+      }
+      if ((v & 0x7F80u) == 0x7F80u) {
+        bad = true;
+        v = 0;
+      }
+      w[e >> 1] |= v << (16 * (e & 1));
+    }
+    *reinterpret_cast<uint4*>(p.out + line * p.ldc + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  const int any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) p.flags[blockIdx.x] = any ? 1u : 0u;
+}
+
+template <bool TRANS>
+__global__ void __launch_bounds__(256) lora_mend_kernel(const LoraMend p) {
+  pdl_gate();
+  bool set = false;
+  for (int i = threadIdx.x; i < p.nflags; i += 256) set |= __ldcg(p.flags + i) != 0;
+  const int64_t r0 = (int64_t)blockIdx.x * 128;
+  bool orphan = false;
+  if (p.inv && threadIdx.x < 128 && r0 + threadIdx.x < p.rows) orphan = __ldcg(p.inv + r0 + threadIdx.x) < 0;
+  const int flagged = __syncthreads_or(set), orphans = __syncthreads_or(orphan);
+  if (!flagged && !orphans) return;
+  for (int64_t row = r0 + (threadIdx.x >> 5); row < r0 + 128 && row < p.rows; row += 8) {
+    const bool whole = p.inv && __ldcg(p.inv + row) < 0;
+    if (!whole && !flagged) continue;
+    for (int64_t t = threadIdx.x & 31; t < p.T; t += 32) {
+      const int32_t a = __ldg(p.adapter + t);
+      float v = 0.f;
+      bool any = whole;
+      if (a >= 0 && (int64_t)a < p.n) {
+        for (int j = 0; j < p.rank; ++j) {
+          const uint32_t b = TRANS ? __ldg(p.M + ((int64_t)a * p.rank + j) * p.rows + row)
+                                   : __ldg(p.M + ((int64_t)a * p.rows + row) * p.rank + j);
+          if (!whole && (b & 0x7F80u) != 0x7F80u) continue;
+          any = true;
+          float s = 0.f;
+          for (int q = 0; q < p.planes; ++q)
+            s += __uint_as_float((uint32_t)__ldcg(p.blocks + ((int64_t)q * p.cat + (int64_t)a * p.rank + j) * p.ldp + t) << 16);
+          v += __uint_as_float(b << 16) * s;
+        }
+      }
+      if (!any) continue;
+      if (p.out_f32) {
+        float* y = static_cast<float*>(p.Y) + row * p.ldy + t;
+        *y = whole ? v : *y + v;
+      } else {
+        uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.ldy + t;
+        const float f = whole ? v : __uint_as_float((uint32_t)*y << 16) + v;
+        *y = (uint16_t)(pack_bf16x2(f, 0.f) & 0xFFFFu);
+      }
+    }
+  }
+}
+
+// The tiles that hold tokens of adapter blockIdx.x, ascending, and their number.  A warp votes on four tiles at a time.
+__global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* adapter, int64_t T, int32_t* tiles,
+                                                         int32_t* counts) {
   using namespace lora;
-  __shared__ int s_warp[8];
+  __shared__ int s_has[128], s_votes[4];
   pdl_gate();
   const int32_t a = (int32_t)blockIdx.x;
   const int64_t all = (T + kTok - 1) / kTok;
   int32_t* out = tiles + (int64_t)a * all;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int found = 0;
-  for (int64_t base = 0; base < all; base += 256) {
-    const int64_t tile = base + threadIdx.x;
+  for (int64_t base = 0; base < all; base += 128) {
+    int32_t id[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t t = (base + 4 * warp) * kTok + 32 * i + lane;
+      id[i] = t < T ? __ldg(adapter + t) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool has = __any_sync(0xFFFFFFFFu, id[2 * i] == a || id[2 * i + 1] == a);
+      if (lane == 0) s_has[4 * warp + i] = has;
+    }
+    __syncthreads();
     bool has = false;
-    if (tile < all)
-      for (int64_t t = tile * kTok; t < (tile + 1) * kTok && t < T; ++t) has |= __ldg(adapter + t) == a;
-    const unsigned votes = __ballot_sync(0xFFFFFFFFu, has);
-    if (lane == 0) s_warp[warp] = __popc(votes);
+    unsigned votes = 0;
+    if (threadIdx.x < 128) {
+      has = s_has[threadIdx.x] != 0;
+      votes = __ballot_sync(0xFFFFFFFFu, has);
+      if (lane == 0) s_votes[warp] = __popc(votes);
+    }
     __syncthreads();
     int before = found, total = 0;
-    for (int w = 0; w < 8; ++w) {
-      if (w < warp) before += s_warp[w];
-      total += s_warp[w];
+    for (int w = 0; w < 4; ++w) {
+      if (w < warp) before += s_votes[w];
+      total += s_votes[w];
     }
-    if (has) out[before + __popc(votes & ((1u << lane) - 1u))] = (int32_t)tile;
+    if (has) out[before + __popc(votes & ((1u << lane) - 1u))] = (int32_t)(base + threadIdx.x);
     found += total;
     __syncthreads();
   }
@@ -405,11 +614,23 @@ __global__ void __launch_bounds__(256) lora_plan_kernel(const int32_t* adapter, 
 }
 
 template <bool BY_RANK, int P>
-__global__ void __launch_bounds__(lora::kThreads) lora_outer_kernel(const LoraOuter p) {
+__global__ void __launch_bounds__(lora::kThreads) lora_outer_kernel(const __grid_constant__ LoraOuter p) {
   using namespace lora;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int32_t s_id[2][kTok];
-  uint8_t* s_v = smem + kOuterStages * kOuterM;  // P terms of [64 tokens][64 ranks], swizzled 128-byte rows
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr uint32_t kStage = kOuterM + P * kOuterV;  // Z tile, then P terms of [64 tokens][up to 64 ranks]
+  __shared__ int32_t s_id[kOuterStages][kTok];
+  __shared__ uint64_t s_full[kOuterStages];
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < kOuterStages; ++i) mbar_init(&s_full[i], 1);
+    s_abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&p.tm_z);
+    tma_prefetch_desc(&p.tm_v);
+  }
   pdl_gate();
   const uint32_t rank = cluster_ctarank();
   const int C = p.cluster;
@@ -418,71 +639,66 @@ __global__ void __launch_bounds__(lora::kThreads) lora_outer_kernel(const LoraOu
   const int32_t a = (int32_t)(blockIdx.y / rblocks);
   const int j0 = (int)(blockIdx.y % rblocks) * kOuterRank;
   const int rs = (p.rank + 15) / 16 * 16;
-  const int cols = rs - j0 < kOuterRank ? rs - j0 : kOuterRank;  // rank columns of this item, a multiple of 16
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int box = rs < kOuterRank ? rs : kOuterRank;            // rank columns that a box brings
+  const int cols = rs - j0 < kOuterRank ? rs - j0 : kOuterRank;  // of which this item has (a multiple of 16)
   const int32_t* list = p.tiles + (int64_t)a * ((p.T + kTok - 1) / kTok);
   const int count = __ldcg(p.counts + a);
   const int mine = count > (int)rank ? (count - (int)rank + C - 1) / C : 0;  // tiles rank, rank + C, ... of the list
+  __syncthreads();
 
-  auto load = [&](int i) {
-    uint8_t* m = smem + (i % kOuterStages) * kOuterM;
-    const int64_t t0 = (int64_t)__ldcg(list + rank + (int64_t)i * C) * kTok;
+  // Ring slot i % kOuterStages: the tile's boxes by one thread, its tokens' adapters by 64 others.  `tile` comes from
+  // the list one turn earlier, so that no load waits for the list.
+  auto load = [&](int i, int32_t tile) {
+    const int slot = i % kOuterStages;
+    const int64_t t0 = (int64_t)tile * kTok;
+    if (tid == 0) {
+      mbar_arrive_expect_tx(&s_full[slot], kOuterM + (uint32_t)(P * kTok * box * 2));
+      uint8_t* m = smem + slot * kStage;
+      tma_load_2d(m, &p.tm_z, &s_full[slot], (int32_t)t0, (int32_t)r0);
 #pragma unroll
-    for (int u = tid; u < kRows * 8; u += kThreads) {
-      const int row = u >> 3, c = u & 7;
-      const int64_t valid = r0 + row < p.rows ? p.T - (t0 + 8 * c) : 0;
-      cp_async_16(m + row * 128 + ((c ^ (row & 7)) << 4), valid > 0 ? p.Z + (r0 + row) * p.ldz + t0 + 8 * c : p.Z,
-                  (uint32_t)(2 * (valid < 0 ? 0 : valid > 8 ? 8 : valid)));
+      for (int q = 0; q < P; ++q) tma_load_3d(m + kOuterM + q * kOuterV, &p.tm_v, &s_full[slot], j0, (int32_t)t0, q);
+    } else if (tid >= 64 && tid < 64 + kTok) {
+      const int t = tid - 64;
+      s_id[slot][t] = t0 + t < p.T ? __ldg(p.adapter + t0 + t) : -1;
     }
   };
+  auto tile_at = [&](int i) { return i < mine ? __ldcg(list + rank + (int64_t)i * C) : 0; };
   float sum[8][4] = {};
-  for (int i = 0; i < kOuterStages - 1; ++i) {
-    if (i < mine) load(i);
-    cp_commit();
-  }
+  for (int i = 0; i < kOuterStages - 1; ++i)
+    if (i < mine) load(i, tile_at(i));
+  int32_t next = tile_at(kOuterStages - 1);
+  // Swizzle of the term boxes: rows of 32, 64 or 128 bytes.
+  const uint32_t vrow = (uint32_t)box * 2;
+  const int vshift = box >= 64 ? 0 : box >= 32 ? 1 : 2;
+  const uint32_t vmask = box >= 64 ? 7u : box >= 32 ? 3u : 1u;
+  const bool plain = box != 16 && box != 32 && box != 64;  // other widths come unswizzled
   for (int i = 0; i < mine; ++i) {
-    const int64_t t0 = (int64_t)__ldcg(list + rank + (int64_t)i * C) * kTok;
-    if (tid < kTok) s_id[i & 1][tid] = t0 + tid < p.T ? __ldg(p.adapter + t0 + tid) : -1;
-    cp_wait<kOuterStages - 2>();
-    __syncthreads();  // the stage has landed, the ids are there, and the products of the tile before are done
-    if (i + kOuterStages - 1 < mine) load(i + kOuterStages - 1);
-    cp_commit();
-    for (int u = tid; u < kTok * (cols / 8); u += kThreads) {  // eight ranks of one token at a time
-      const int t = u / (cols / 8), c = u - t * (cols / 8);
-      uint32_t w[P][4] = {};
-      if (s_id[i & 1][t] == a) {
-        const float4* src = reinterpret_cast<const float4*>(p.V + (t0 + t) * rs + j0 + 8 * c);
-        const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
-        const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          uint16_t term[P];
-          split_terms<P>(v[e], term);
-#pragma unroll
-          for (int q = 0; q < P; ++q) w[q][e >> 1] |= (uint32_t)term[q] << (16 * (e & 1));
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < P; ++q)
-        *reinterpret_cast<uint4*>(s_v + q * kOuterV + t * 128 + ((c ^ (t & 7)) << 4)) =
-            make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
-    }
-    __syncthreads();
-    const uint32_t m = smem_u32(smem + (i % kOuterStages) * kOuterM), v = smem_u32(s_v);
+    const int slot = i % kOuterStages;
+    mbar_wait(&s_full[slot], (uint32_t)(i / kOuterStages) & 1u, &s_abort, p.status, kWaitNs);
+    __syncthreads();  // the ids are there, and the slot of tile i - 1 is free
+    if (i + kOuterStages - 1 < mine) load(i + kOuterStages - 1, next);
+    next = tile_at(i + kOuterStages);
+    const uint32_t m = smem_u32(smem + slot * kStage), v = m + kOuterM;
     const int mi = lane >> 3, l8 = lane & 7;
+    const unsigned lo = __ballot_sync(0xFFFFFFFFu, s_id[slot][lane] == a);
+    const unsigned hi = __ballot_sync(0xFFFFFFFFu, s_id[slot][32 + lane] == a);
     float acc[8][4] = {};
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
+      const unsigned used = ((ks & 2 ? hi : lo) >> (16 * (ks & 1))) & 0xFFFFu;  // this step's tokens of the adapter
+      if (!used) continue;
       uint32_t z[4];
       const int row = 16 * warp + 8 * (mi & 1) + l8;
       ldmatrix_x4(z, m + row * 128 + (((2 * ks + (mi >> 1)) ^ (row & 7)) << 4));
-      // other requests' tokens leave the product as zeros of Z too: their Inf or NaN times a 0 of V would stay
+      // Other tokens leave both operands: their Inf or NaN in one would survive a 0 in the other, and S of a token
+      // without an adapter is not written at all.
+      uint32_t keep[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int t = 16 * ks + 8 * h + 2 * (lane & 3);
-        const uint32_t keep = (s_id[i & 1][t] == a ? 0xFFFFu : 0u) | (s_id[i & 1][t + 1] == a ? 0xFFFF0000u : 0u);
-        z[2 * h] &= keep;
-        z[2 * h + 1] &= keep;
+        const unsigned two = used >> (8 * h + 2 * (lane & 3));
+        keep[h] = (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+        z[2 * h] &= keep[h];
+        z[2 * h + 1] &= keep[h];
       }
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
@@ -491,16 +707,17 @@ __global__ void __launch_bounds__(lora::kThreads) lora_outer_kernel(const LoraOu
         for (int q = 0; q < P; ++q) {
           uint32_t f[4];
           const int t = 16 * ks + 8 * (mi & 1) + l8;
-          ldmatrix_x4_trans(f, v + q * kOuterV + t * 128 + (((2 * b + (mi >> 1)) ^ (t & 7)) << 4));
-          mma_bf16(acc[2 * b], z, f[0], f[1]);
-          mma_bf16(acc[2 * b + 1], z, f[2], f[3]);
+          const uint32_t unit = (uint32_t)(2 * b + (mi >> 1));
+          const uint32_t sw = plain ? unit : unit ^ (((uint32_t)t >> vshift) & vmask);
+          ldmatrix_x4_trans(f, v + q * kOuterV + t * vrow + (sw << 4));
+          mma_bf16(acc[2 * b], z, f[0] & keep[0], f[1] & keep[1]);
+          mma_bf16(acc[2 * b + 1], z, f[2] & keep[0], f[3] & keep[1]);
         }
       }
     }
 #pragma unroll
     for (int e = 0; e < 32; ++e) sum[e >> 2][e & 3] += acc[e >> 2][e & 3];
   }
-  cp_wait<0>();
   __syncthreads();
   float* s_sum = reinterpret_cast<float*>(smem);  // [128 rows][65], over the stages
 #pragma unroll
@@ -516,8 +733,13 @@ __global__ void __launch_bounds__(lora::kThreads) lora_outer_kernel(const LoraOu
   for (int e = tid; e < part * live; e += kThreads) {
     const int row = (BY_RANK ? e % part : e / live) + (int)rank * part, j = BY_RANK ? e / part : e % live;
     if (r0 + row >= p.rows) continue;
-    float v = 0.f;
-    for (int c = 0; c < C; ++c) v += ld_cluster_f32(map_to_cta(smem_u32(s_sum + row * (kOuterRank + 1) + j), c));
+    float got[8], v = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < C) got[c] = ld_cluster_f32(map_to_cta(smem_u32(s_sum + row * (kOuterRank + 1) + j), c));
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < C) v += got[c];
     v *= scale;
     const int64_t at = BY_RANK ? ((int64_t)a * p.rank + j0 + j) * p.rows + r0 + row
                                : ((int64_t)a * p.rows + r0 + row) * p.rank + j0 + j;
@@ -567,6 +789,18 @@ static cudaError_t launch_clustered(Kern kernel, dim3 grid, int cluster, uint32_
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <bool TRANS>
+static cudaError_t launch_shrink_out(const LoraShrink& p, dim3 grid, cudaStream_t s) {
+  using namespace lora;
+  const uint32_t b = kShrinkSmem;
+  if (p.out == SHRINK_F32) return launch_clustered(lora_shrink_kernel<TRANS, SHRINK_F32, 1>, grid, p.cluster, b, b, p, s);
+  if (p.out == SHRINK_TERMS)
+    return p.planes == 3 ? launch_clustered(lora_shrink_kernel<TRANS, SHRINK_TERMS, 3>, grid, p.cluster, b, b, p, s)
+                         : launch_clustered(lora_shrink_kernel<TRANS, SHRINK_TERMS, 2>, grid, p.cluster, b, b, p, s);
+  return p.planes == 3 ? launch_clustered(lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 3>, grid, p.cluster, b, b, p, s)
+                       : launch_clustered(lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 2>, grid, p.cluster, b, b, p, s);
+}
+
 cudaError_t launch_lora_shrink(LoraShrink& p, bool trans, cudaStream_t s) {
   using namespace lora;
   const int64_t tiles = tiles_of(p.T), chunks = (p.D + kDepth - 1) / kDepth;
@@ -581,19 +815,19 @@ cudaError_t launch_lora_shrink(LoraShrink& p, bool trans, cudaStream_t s) {
   if (y < 1) y = 1;
   if (tiles * p.cluster >= (1ll << 31)) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(tiles * p.cluster), (unsigned)y);
-  return trans ? launch_clustered(lora_shrink_kernel<true>, grid, p.cluster, kShrinkSmem, kShrinkSmem, p, s)
-               : launch_clustered(lora_shrink_kernel<false>, grid, p.cluster, kShrinkSmem, kShrinkSmem, p, s);
+  return trans ? launch_shrink_out<true>(p, grid, s) : launch_shrink_out<false>(p, grid, s);
 }
 
 cudaError_t launch_lora_expand(const LoraExpand& p, bool trans, cudaStream_t s) {
   using namespace lora;
   const int64_t tiles = tiles_of(p.T), blocks = (p.rows + kRows - 1) / kRows;
   if (tiles > 65535) return cudaErrorInvalidValue;
-  const uint32_t rs = (uint32_t)rank_stride(p.rank);
   const uint32_t terms = p.out_f32 ? 3 : 2;
-  auto bytes = [&](uint32_t r) { return 2 * (trans ? r * 256u : kRows * (r * 2 + 16)) + terms * kTok * (r * 2 + 16); };
+  auto bytes = [&](uint32_t r) {
+    return kExpandStages * (trans ? r * 256u : kRows * (r * 2 + 16)) + terms * kTok * (r * 2 + 16);
+  };
   const dim3 grid((unsigned)blocks, (unsigned)tiles);
-  const uint32_t b = bytes(rs), most = bytes(kMaxRank);
+  const uint32_t b = bytes((uint32_t)rank_stride(p.rank)), most = bytes(kMaxRank);
   if (trans)
     return p.out_f32 ? launch_clustered(lora_expand_kernel<true, 3>, grid, 1, b, most, p, s)
                      : launch_clustered(lora_expand_kernel<true, 2>, grid, 1, b, most, p, s);
@@ -601,9 +835,27 @@ cudaError_t launch_lora_expand(const LoraExpand& p, bool trans, cudaStream_t s) 
                    : launch_clustered(lora_expand_kernel<false, 2>, grid, 1, b, most, p, s);
 }
 
+int lora_cat_blocks() { return 2 * sm_count_current(); }
+
+cudaError_t launch_lora_cat(LoraCat& p, bool by_rank, cudaStream_t s) {
+  p.blocks = lora_cat_blocks();
+  cudaError_t e = by_rank ? launch_pdl(lora_cat_kernel<true>, dim3((unsigned)p.blocks), dim3(256), 0, s, p)
+                          : launch_pdl(lora_cat_kernel<false>, dim3((unsigned)p.blocks), dim3(256), 0, s, p);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_lora_mend(const LoraMend& p, bool trans, cudaStream_t s) {
+  const dim3 grid((unsigned)((p.rows + 127) / 128));
+  cudaError_t e = trans ? launch_pdl(lora_mend_kernel<true>, grid, dim3(256), 0, s, p)
+                        : launch_pdl(lora_mend_kernel<false>, grid, dim3(256), 0, s, p);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 cudaError_t launch_lora_plan(const int32_t* adapter, int64_t T, int64_t n, int32_t* tiles, int32_t* counts,
                              cudaStream_t s) {
-  cudaError_t e = launch_pdl(lora_plan_kernel, dim3((unsigned)n), dim3(256), 0, s, adapter, T, tiles, counts);
+  cudaError_t e = launch_pdl(lora_plan_kernel, dim3((unsigned)n), dim3(1024), 0, s, adapter, T, tiles, counts);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -620,7 +872,7 @@ cudaError_t launch_lora_outer(LoraOuter& p, bool by_rank, cudaStream_t s) {
     p.cluster <<= 1;
   if (blocks * p.cluster >= (1ll << 31)) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(blocks * p.cluster), (unsigned)items);
-  const uint32_t b = kOuterSmem;
+  const uint32_t b = outer_smem(p.out_f32 ? 3 : 2);
   if (by_rank)
     return p.out_f32 ? launch_clustered(lora_outer_kernel<true, 3>, grid, p.cluster, b, b, p, s)
                      : launch_clustered(lora_outer_kernel<true, 2>, grid, p.cluster, b, b, p, s);
@@ -662,21 +914,96 @@ nm_status check_adapter_pointers(const Adapters& ad, int64_t R, int64_t K, int64
   return NM_OK;
 }
 
-nm_status shrink(const Adapters& ad, bool trans, int64_t D, const uint16_t* Z, int64_t ldz, int64_t T, float* S,
+// The shrink product of Z (D x T) into the form that `p` asks for.
+nm_status shrink(const Adapters& ad, bool trans, int64_t D, const uint16_t* Z, int64_t ldz, int64_t T, LoraShrink& p,
                  cudaStream_t s) {
-  LoraShrink p = {};
+  using namespace lora;
   p.M = trans ? ad.B : ad.A;
-  p.Z = Z;
-  p.ldz = ldz;
   p.adapter = ad.adapter;
+  p.scale = ad.scale;
   p.n = ad.n;
   p.D = D;
   p.T = T;
   p.rank = ad.rank;
-  p.vec = al16(p.M) && (trans ? ad.rank : D) % 8 == 0;
-  p.S = S;
+  p.vec = D > 0 && al16(p.M) && (trans ? ad.rank : D) % 8 == 0;
+  p.status = status_word_ptr();
+  if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
+  nm_status st = NM_OK;
+  if (D > 0) st = make_tmap(&p.tm_z, Z, (uint64_t)T, (uint64_t)D, (uint64_t)ldz * 2, kTok, kDepth, 128, "tokens");
+  if (st == NM_OK && p.vec) {
+    const uint64_t inner = trans ? (uint64_t)ad.rank : (uint64_t)D, rows = trans ? (uint64_t)D : (uint64_t)ad.rank;
+    st = make_tmap3(&p.tm_m, p.M, inner, rows, (uint64_t)ad.n, inner * 2, inner * rows * 2, trans ? kRankBlock : 64,
+                    trans ? kDepth : kRankBlock, trans ? 64 : 128, "adapters");
+  }
+  if (st != NM_OK) return st;
   cudaError_t e = launch_lora_shrink(p, trans, s);
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "adapter shrink launch");
+}
+
+// The adapters in the projection's own reduction: a GEMM that serves the shape takes, after its own steps, the blocks
+// of 64 rank rows that a column tile's tokens use.  Returns what that GEMM and the mending pass need.
+struct InGemm {
+  Staged cat, blocks, small;
+  GemmExt ext{};
+  LoraMend mend{};
+  InGemm(cudaStream_t s) : cat(s), blocks(s), small(s) {}
+};
+bool adapters_fit_gemm(const Adapters& ad) { return ad.n > 0 && ad.n * ad.rank <= lora::kMaxCat; }
+nm_status adapters_for_gemm(const Adapters& ad, bool trans, int64_t D, int64_t rows, const uint16_t* Z, int64_t ldz,
+                            int64_t T, const int32_t* idx, bool f32, InGemm& g, cudaStream_t s) {
+  using namespace lora;
+  const int64_t cat = (ad.n * ad.rank + 63) / 64 * 64, ldp = (T + 7) / 8 * 8, ldc = trans ? (rows + 7) / 8 * 8 : cat;
+  const int planes = f32 ? 3 : 2, nflags = lora_cat_blocks();
+  cudaError_t e = g.cat.get((size_t)((trans ? ad.n * ad.rank : rows) * ldc * 2));
+  if (e == cudaSuccess) e = g.blocks.get((size_t)(planes * cat * ldp * 2));
+  if (e == cudaSuccess) e = g.small.get((size_t)(nflags + tiles_of(T) + (idx ? rows : 0)) * 4);
+  if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the adapters");
+  uint32_t* flags = g.small.as<uint32_t>();
+  uint32_t* masks = flags + nflags;
+  int32_t* inv = idx ? reinterpret_cast<int32_t*>(masks + tiles_of(T)) : nullptr;
+  LoraCat c = {};
+  c.M = trans ? ad.A : ad.B;
+  c.n = ad.n;
+  c.rows = rows;
+  c.rank = ad.rank;
+  c.cat = cat;
+  c.ldc = ldc;
+  c.idx = idx;
+  c.out = g.cat.as<uint16_t>();
+  c.flags = flags;
+  c.inv = inv;
+  e = launch_lora_cat(c, trans, s);
+  if (e != cudaSuccess) return cuda_fail(e, "adapter layout launch");
+  LoraShrink p = {};
+  p.out = SHRINK_BLOCKS;
+  p.planes = planes;
+  p.terms = g.blocks.as<uint16_t>();
+  p.cat = cat;
+  p.ldp = ldp;
+  p.masks = masks;
+  p.idx = idx;
+  p.idx_n = rows;
+  p.inv = inv;
+  nm_status st = shrink(ad, trans, D, Z, ldz, T, p, s);
+  if (st != NM_OK) return st;
+  g.ext = GemmExt{g.cat.as<uint16_t>(), trans ? ad.n * ad.rank : rows, trans ? rows : cat, ldc, g.blocks.as<uint16_t>(), cat,
+                  ldp, planes, masks};
+  LoraMend& m = g.mend;
+  m.M = c.M;
+  m.adapter = ad.adapter;
+  m.n = ad.n;
+  m.rows = rows;
+  m.T = T;
+  m.rank = ad.rank;
+  m.blocks = p.terms;
+  m.planes = planes;
+  m.cat = cat;
+  m.ldp = ldp;
+  m.flags = flags;
+  m.nflags = nflags;
+  m.inv = inv;
+  m.out_f32 = f32;
+  return NM_OK;
 }
 
 }  // namespace
@@ -700,12 +1027,25 @@ nm_status nm_spmm_lora(const uint16_t* values, const uint32_t* meta, int n, int 
     return run_spmm(values, meta, n, m, R, K, idx, X, ldx, T, Y, ldy, y_dtype, nullptr, s);
   st = check_adapter_pointers(ad, R, K, T);
   if (st != NM_OK) return st;
+  if (spmm_pair_serves(values, meta, n, m, K, T) && adapters_fit_gemm(ad)) {
+    InGemm g(s);
+    st = adapters_for_gemm(ad, false, K, R, X, ldx, T, nullptr, y_dtype == NM_OUT_F32, g, s);
+    if (st == NM_OK) st = run_spmm(values, meta, n, m, R, K, idx, X, ldx, T, Y, ldy, y_dtype, nullptr, s, &g.ext);
+    if (st != NM_OK) return st;
+    g.mend.Y = Y;
+    g.mend.ldy = ldy;
+    cudaError_t e = launch_lora_mend(g.mend, false, s);
+    return e == cudaSuccess ? NM_OK : cuda_fail(e, "adapter mending launch");
+  }
   Staged low(s), sum(s), partials(s);
   const int64_t ldb = (T + 3) / 4 * 4;
   cudaError_t e = low.get((size_t)(T * lora::rank_stride(rank) * 4));
   if (e == cudaSuccess) e = sum.get((size_t)(R * ldb * 4));
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the projection");
-  st = shrink(ad, false, K, X, ldx, T, low.as<float>(), s);
+  LoraShrink sh = {};
+  sh.out = SHRINK_F32;
+  sh.S = low.as<float>();
+  st = shrink(ad, false, K, X, ldx, T, sh, s);
   GemmPartials raw{&partials, 1, 0, 0};
   if (st == NM_OK) st = run_spmm(values, meta, n, m, R, K, idx, X, ldx, T, sum.as<float>(), ldb, NM_OUT_F32, &raw, s);
   if (st != NM_OK) return st;
@@ -743,6 +1083,16 @@ nm_status nm_spmm_lora_t(const uint16_t* values, const uint32_t* meta, int n, in
   if (R == 0) return run_spmm_t(values, meta, n, m, R, K, nullptr, dY, lddy, T, dX, lddx, dtype, s);
   if (num_adapters > 0) st = check_adapter_pointers(ad, R, K, T);
   if (st != NM_OK) return st;
+  if (adapters_fit_gemm(ad)) {
+    InGemm g(s);
+    st = adapters_for_gemm(ad, true, R, K, dY, lddy, T, idx, dtype == NM_OUT_F32, g, s);
+    if (st == NM_OK) st = run_spmm_t(values, meta, n, m, R, K, idx, dY, lddy, T, dX, lddx, dtype, s, &g.ext);
+    if (st != NM_OK) return st;
+    g.mend.Y = dX;
+    g.mend.ldy = lddx;
+    cudaError_t e = launch_lora_mend(g.mend, true, s);
+    return e == cudaSuccess ? NM_OK : cuda_fail(e, "adapter mending launch");
+  }
   Staged low(s), sum(s), inverse(s);
   const int64_t ldb = (T + 3) / 4 * 4;
   cudaError_t e = low.get((size_t)(T * lora::rank_stride(rank) * 4));
@@ -753,7 +1103,10 @@ nm_status nm_spmm_lora_t(const uint16_t* values, const uint32_t* meta, int n, in
     e = launch_invert_map(idx, K, inverse.as<int32_t>(), s);
     if (e != cudaSuccess) return cuda_fail(e, "index map launch");
   }
-  if (num_adapters > 0) st = shrink(ad, true, R, dY, lddy, T, low.as<float>(), s);
+  LoraShrink sh = {};
+  sh.out = SHRINK_F32;
+  sh.S = low.as<float>();
+  if (num_adapters > 0) st = shrink(ad, true, R, dY, lddy, T, sh, s);
   if (st == NM_OK) st = run_spmm_t(values, meta, n, m, R, K, nullptr, dY, lddy, T, sum.as<float>(), ldb, NM_OUT_F32, s);
   if (st != NM_OK) return st;
   LoraExpand p = {};
@@ -806,12 +1159,11 @@ nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t lddy, c
   if (st == NM_OK && K > 0) st = check_matrix(X, ldx, T, 2, "X");
   if (st == NM_OK) st = require_device();
   if (st != NM_OK) return st;
-  Staged low(s), up(s), plan(s);
-  const size_t bytes = (size_t)(T * lora::rank_stride(rank) * 4);
-  const int64_t tiles = lora::tiles_of(T);
+  Staged terms(s), plan(s);
+  const int planes = dtype == NM_OUT_F32 ? 3 : 2;
+  const int64_t rs = lora::rank_stride(rank), tiles = lora::tiles_of(T);
   cudaError_t e = plan.get((size_t)((tiles + 1) * num_adapters * 4));
-  if (e == cudaSuccess && dB) e = low.get(bytes);
-  if (e == cudaSuccess && dA) e = up.get(bytes);
+  if (e == cudaSuccess) e = terms.get((size_t)(planes * T * rs * 2));
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the adapter gradients");
   LoraOuter p = {};
   p.adapter = adapter;
@@ -822,28 +1174,32 @@ nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t lddy, c
   p.counts = plan.as<int32_t>();
   p.tiles = plan.as<int32_t>() + num_adapters;
   p.out_f32 = dtype == NM_OUT_F32;
+  p.status = status_word_ptr();
+  if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
   e = launch_lora_plan(adapter, T, num_adapters, plan.as<int32_t>() + num_adapters, plan.as<int32_t>(), s);
   if (e != cudaSuccess) return cuda_fail(e, "adapter plan launch");
-  if (dB && R > 0) {
-    st = shrink(ad, false, K, X, ldx, T, low.as<float>(), s);
+  const uint32_t box = (uint32_t)(rs < lora::kOuterRank ? rs : lora::kOuterRank);
+  st = make_tmap3(&p.tm_v, terms.as<uint16_t>(), (uint64_t)rs, (uint64_t)T, (uint64_t)planes, (uint64_t)rs * 2,
+                  (uint64_t)(T * rs) * 2, box, lora::kTok, box == 64 ? 128 : box == 32 ? 64 : box == 16 ? 32 : 0,
+                  "adapter terms");
+  if (st != NM_OK) return st;
+  for (int which = 0; which < 2; ++which) {  // dB from S = A X and dY, then dA from U = B^T dY and X
+    const int64_t rows = which ? K : R;
+    void* out = which ? dA : dB;
+    if (!out || rows == 0) continue;
+    LoraShrink sh = {};
+    sh.out = SHRINK_TERMS;
+    sh.planes = planes;
+    sh.terms = terms.as<uint16_t>();
+    st = which ? shrink(ad, true, R, dY, lddy, T, sh, s) : shrink(ad, false, K, X, ldx, T, sh, s);
+    const uint16_t* Z = which ? X : dY;
+    const int64_t ldz = which ? ldx : lddy;
+    if (st == NM_OK)
+      st = make_tmap(&p.tm_z, Z, (uint64_t)T, (uint64_t)rows, (uint64_t)ldz * 2, lora::kTok, lora::kRows, 128, "tokens");
     if (st != NM_OK) return st;
-    p.Z = dY;
-    p.ldz = lddy;
-    p.V = low.as<float>();
-    p.rows = R;
-    p.out = dB;
-    e = launch_lora_outer(p, false, s);
-    if (e != cudaSuccess) return cuda_fail(e, "adapter gradient launch");
-  }
-  if (dA && K > 0) {
-    st = shrink(ad, true, R, dY, lddy, T, up.as<float>(), s);
-    if (st != NM_OK) return st;
-    p.Z = X;
-    p.ldz = ldx;
-    p.V = up.as<float>();
-    p.rows = K;
-    p.out = dA;
-    e = launch_lora_outer(p, true, s);
+    p.rows = rows;
+    p.out = out;
+    e = launch_lora_outer(p, which != 0, s);
     if (e != cudaSuccess) return cuda_fail(e, "adapter gradient launch");
   }
   return NM_OK;

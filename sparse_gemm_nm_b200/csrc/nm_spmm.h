@@ -77,6 +77,12 @@ struct SpmmParams {
   int bn;
   int kd;  // skinny stage depth (logical K per stage: 128 or 256)
   PairEpiData epi;
+  // further dense reduction steps (SM pair): 64-row blocks of tm_xs (ext_planes planes of ext_cat rows) against 64-column
+  // blocks of tm_xa, for the blocks set in the masks of a column tile's 64-token tiles
+  CUtensorMap tm_xa, tm_xs;
+  const uint32_t* ext_masks;
+  int ext_planes;
+  int64_t ext_cat;
   float* ws;
   int keep_partials;  // leave the ranges' sums in ws (no reduction launch)
   // fused prune + compress + GEMM: optional outputs of the compressed operand
@@ -92,6 +98,10 @@ struct SpmmParams {
 // M x N weight (meta), as out[m][j] for survivor j of row m.
 struct DenseParams {
   CUtensorMap tm_a, tm_b;
+  CUtensorMap tm_xa, tm_xs;  // further reduction steps: 64-row blocks of tm_xa (MN-major) and tm_xs, as in SpmmParams
+  const uint32_t* ext_masks;
+  int ext_planes;
+  int64_t ext_cat;
   CUtensorMap tm_b_alt;     // read instead of tm_b when use_alt is set and *use_alt is nonzero at run time
   CUtensorMap tm_out;       // epilogue 0 with tma_store: C (M x N), box {64 bf16 | 32 four-byte, 32 rows}, 128B swizzle
   const uint32_t* use_alt;

@@ -224,7 +224,17 @@ __device__ __forceinline__ void xgrad_block(const SpmmParams& p, uint32_t (&v)[3
   }
 }
 
-template <bool HYB, bool DB, bool I8, bool TF32, int EPI = PAIR_EPI_Y>
+// Blocks of the further reduction steps that the columns [n0, n0 + width) use.
+__device__ __forceinline__ uint32_t ext_mask(const uint32_t* masks, int64_t n0, int64_t width, int64_t T) {
+  const int64_t last = (n0 + width < T ? n0 + width : T) - 1;
+  uint32_t m = 0;
+  for (int64_t i = n0 >> 6; i <= last >> 6; ++i) m |= __ldg(masks + i);
+  return m;
+}
+
+// EXT: after its K stages a tile takes half stages (64 dense reduction steps: A 16 KB, B the first 8 KB of each strip)
+// for the adapter blocks that its columns use, one for each bf16 term.
+template <bool HYB, bool DB, bool I8, bool TF32, int EPI = PAIR_EPI_Y, bool EXT = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     spmm_pair_kernel(const __grid_constant__ SpmmParams p) {
   using namespace pair;
@@ -302,6 +312,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
         uint32_t ph = 0, aph = 0;  // aph bit a: phase of accumulator a
         for (int tile = pair_id; tile < p.num_tiles && ok; tile += npairs) {
           const int tm = p.n_major ? tile / p.tiles_n : tile % p.tiles_m;
+          uint32_t ext = 0;
+          if (EXT) {
+            const int tn = p.n_major ? tile % p.tiles_n : tile / p.tiles_m;
+            ext = ext_mask(p.ext_masks, (int64_t)tn * C::kN, C::kN, p.T);
+          }
           ok = mbar_wait(&acc_empty[acc], ((aph >> acc) & 1u) ^ 1u, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           tc_fence_after();
@@ -350,6 +365,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
             }
             tc_commit_pair(&empty[s], 0x3);
             if (++s == kStages) { s = 0; ph ^= 1u; }
+          }
+          if (EXT && ok) {
+            constexpr uint32_t kIdescExt = idesc_bf16(C::kN, false, 256);
+            for (uint32_t left = ext; left && ok; left &= left - 1) {
+              for (int pl = 0; pl < p.ext_planes; ++pl) {
+                ok = mbar_wait(&full[s], ph, abort_flag, p.status, kWaitNs);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t a_addr = smem_u32(smem + L.a + s * kA);
+                const uint32_t b_addr = smem_u32(smem + L.b + s * kB);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  tc_mma_pair(d_tmem, smem_desc(a_addr + kk * 32, 16, 1024, SWZ_128B),
+                              smem_desc(b_addr + kk * 2048, 16384, 1024, SWZ_128B), kIdescExt, 1u);
+                tc_commit_pair(&empty[s], 0x3);
+                if (++s == kStages) { s = 0; ph ^= 1u; }
+              }
+            }
           }
           if (!ok) break;
           tc_commit_pair(&acc_full[acc], 0x3);
@@ -411,6 +444,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
               tma_load_3d_pair(smem + L.e + s * kE, &p.tm_meta, lead_full, 0, (int32_t)kt, row0 / 16);
             }
             if (++s == kStages) { s = 0; ph ^= 1u; }
+          }
+          if (EXT && ok) {
+            uint32_t left = ext_mask(p.ext_masks, (int64_t)tn * C::kN, C::kN, p.T);
+            for (; left && ok; left &= left - 1) {
+              const int32_t k0 = 64 * (__ffs(left) - 1);
+              for (int pl = 0; pl < p.ext_planes; ++pl) {
+                ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
+                if (!ok) break;
+                const uint32_t lead_full = lead_full0 + 8u * s;
+                if (warp == 0 || warp == 10) {
+                  const int h = warp == 10;
+                  if (rank == 0 && h == 0) mbar_arrive_expect_tx(&full[s], 2u * (16384u + 16384u));
+                  tma_load_2d_pair(smem + L.a + s * kA + h * 8192, &p.tm_xa, lead_full, k0, row0 + 64 * h);
+                } else if (warp == 2 || warp == 4) {
+                  const int j = (warp - 2) >> 1;
+                  tma_load_2d_pair(smem + L.b + s * kB + j * 16384, &p.tm_xs, lead_full, col0 + 64 * j,
+                                   (int32_t)(pl * p.ext_cat) + k0);
+                }
+                if (++s == kStages) { s = 0; ph ^= 1u; }
+              }
+            }
           }
         }
       }
@@ -633,7 +687,7 @@ bool pair_kernel_fits(const SpmmParams& p) {
   return p.a_mode == A_TMA_SPARSE && p.K % 128 == 0 && p.K > 0 && p.T >= 192 && p.R >= 1 && p.T % 8 == 0;
 }
 
-template <bool HYB, bool DB, bool I8 = false, bool TF32 = false, int EPI = PAIR_EPI_Y>
+template <bool HYB, bool DB, bool I8 = false, bool TF32 = false, int EPI = PAIR_EPI_Y, bool EXT = false>
 static cudaError_t launch_pair(SpmmParams& p, cudaStream_t stream) {
   constexpr pair::Layout L = pair::Cfg<HYB, DB, I8, TF32>::layout();
   const size_t bytes = L.total + 1024;
@@ -641,7 +695,7 @@ static cudaError_t launch_pair(SpmmParams& p, cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !configured[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(spmm_pair_kernel<HYB, DB, I8, TF32, EPI>,
+    cudaError_t e = cudaFuncSetAttribute(spmm_pair_kernel<HYB, DB, I8, TF32, EPI, EXT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
@@ -649,7 +703,7 @@ static cudaError_t launch_pair(SpmmParams& p, cudaStream_t stream) {
   const int pairs_avail = sm_count_current() / 2;
   const int pairs = p.num_tiles < pairs_avail ? p.num_tiles : pairs_avail;
   cudaError_t e =
-      launch_pdl(spmm_pair_kernel<HYB, DB, I8, TF32, EPI>, dim3(2 * pairs), dim3(pair::kThreads), bytes, stream, p);
+      launch_pdl(spmm_pair_kernel<HYB, DB, I8, TF32, EPI, EXT>, dim3(2 * pairs), dim3(pair::kThreads), bytes, stream, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -669,8 +723,10 @@ cudaError_t launch_spmm_pair(SpmmParams& p, cudaStream_t stream) {
     p.num_tiles = p.tiles_m * p.tiles_n;
     if (p.epi.mode == PAIR_EPI_LSE) return launch_pair<false, true, false, false, PAIR_EPI_LSE>(p, stream);
     if (p.epi.mode == PAIR_EPI_XGRAD) return launch_pair<false, true, false, false, PAIR_EPI_XGRAD>(p, stream);
+    if (p.ext_planes) return launch_pair<false, true, false, false, PAIR_EPI_Y, true>(p, stream);
     return launch_pair<false, true>(p, stream);
   }
+  if (p.ext_planes) return launch_pair<false, false, false, false, PAIR_EPI_Y, true>(p, stream);
   return launch_pair<false, false>(p, stream);
 }
 
