@@ -24,6 +24,7 @@
 // truncates; the CTAs of a cluster share a reduction and join in rank order, so
 // results repeat bit for bit.
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "nm_host.h"
@@ -40,18 +41,19 @@ constexpr int kRankBlock = 32;   // rank rows of a shrink work item
 constexpr int kStages = 3;
 constexpr uint32_t kZBytes = kDepth * kTok * 2;
 constexpr uint32_t kMBytes = kRankBlock * kDepth * 2;
-constexpr uint32_t kShrinkPart = 2 * kRankBlock * (kTok + 1) * 4;
+constexpr uint32_t kShrinkPart = 2 * kTok * (kRankBlock + 1) * 4;  // the wider of the two layouts of the joined sums
 constexpr uint32_t kShrinkSmem = kStages * (kZBytes + kMBytes) + kShrinkPart + 1024;
 constexpr int kRows = 128;       // rows of an expand or outer tile
 constexpr int kExpandStages = 4; // adapters in flight
 constexpr int kOuterRank = 64;   // rank columns of an outer work item
-constexpr int kOuterStages = 3;
 constexpr uint32_t kOuterM = kRows * kTok * 2;
 constexpr uint32_t kOuterV = kTok * kOuterRank * 2;  // one bf16 term
+// Two CTAs to an SM: their warps cover for one another's MMA latency (one CTA left the issue slots 59 % idle).
+__host__ __device__ constexpr int outer_stages(int planes) { return planes == 3 ? 2 : 3; }
 __host__ __device__ constexpr uint32_t outer_smem(int planes) {
-  return kOuterStages * (kOuterM + (uint32_t)planes * kOuterV) + 1024;
+  return outer_stages(planes) * (kOuterM + (uint32_t)planes * kOuterV) + 1024;
 }
-static_assert(kRows * (kOuterRank + 1) * 4 <= kOuterStages * kOuterM, "the joined sums reuse the stages");
+static_assert(kRows * (kOuterRank + 1) * 4 <= 2 * (kOuterM + 2 * kOuterV), "the joined sums reuse the stages");
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
@@ -78,6 +80,8 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
   __shared__ int s_count, s_abort;
   __shared__ uint32_t s_present[kMaxCat / 32];
   __shared__ uint64_t s_full[kStages];
-  float* s_part = reinterpret_cast<float*>(smem + kStages * (kZBytes + kMBytes));  // [K half][32 ranks][65]
+  float* s_part = reinterpret_cast<float*>(smem + kStages * (kZBytes + kMBytes));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&s_full[i], 1);
@@ -258,6 +262,11 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
       for (int e = 0; e < 16; ++e) sum[e >> 3][(e >> 2) & 1][e & 3] += acc[e >> 3][(e >> 2) & 1][e & 3];
     }
     use += mine;
+    // The sums of both K halves, in the order of the output (ranks of a token, or tokens of a rank row, side by side):
+    // lanes that read another CTA's shared memory at neighbouring addresses share a transfer (reading it across rows
+    // took 14 us of a 25 us item).
+    auto at = [](int j, int t) { return OUT == SHRINK_BLOCKS ? j * (kTok + 1) + t : t * (kRankBlock + 1) + j; };
+    constexpr int kHalf = kShrinkPart / 8;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -265,33 +274,45 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = 16 * mt + (lane >> 2) + 8 * (e >> 1), t = 16 * group + 8 * nb + 2 * (lane & 3) + (e & 1);
-          s_part[(half * kRankBlock + j) * (kTok + 1) + t] = sum[mt][nb][e];
+          s_part[half * kHalf + at(j, t)] = sum[mt][nb][e];
         }
     __syncthreads();
     if (C > 1) cluster_sync();  // every CTA's sums are written
-    // The token-major forms take the ranks of a token side by side, the block form the tokens of a rank row.
-    for (int e = tid + kThreads * (int)rank; e < kRankBlock * kTok; e += kThreads * C) {
+    constexpr int kOwn = kRankBlock * kTok / kThreads;  // outputs of a thread when it is alone
+    float v[kOwn];
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+      const int e = tid + kThreads * ((int)rank + o * C);
+      v[o] = 0.f;
+      if (e >= kRankBlock * kTok) continue;
       const int j = OUT == SHRINK_BLOCKS ? e / kTok : e % kRankBlock, t = OUT == SHRINK_BLOCKS ? e % kTok : e / kRankBlock;
-      const bool own = s_id[t] == a;
-      if (OUT == SHRINK_BLOCKS ? (j >= live || t0 + t >= p.ldp) : (!own || j0 + j >= rs)) continue;
+      const uint32_t mine_at = smem_u32(s_part + at(j, t));
       float part[8][2];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         if (c >= C) continue;
-        const uint32_t at = map_to_cta(smem_u32(s_part + j * (kTok + 1) + t), c);
-        part[c][0] = ld_cluster_f32(at);
-        part[c][1] = ld_cluster_f32(at + kRankBlock * (kTok + 1) * 4);
+        const uint32_t there = map_to_cta(mine_at, c);
+        part[c][0] = ld_cluster_f32(there);
+        part[c][1] = ld_cluster_f32(there + kHalf * 4);
       }
-      float v = 0.f;
 #pragma unroll
       for (int c = 0; c < 8; ++c)
-        if (c < C) v += part[c][0] + part[c][1];
+        if (c < C) v[o] += part[c][0] + part[c][1];
+    }
+    if (C > 1) cluster_arrive();  // done with the other CTAs' sums; the stores below need not be waited for
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+      const int e = tid + kThreads * ((int)rank + o * C);
+      if (e >= kRankBlock * kTok) continue;
+      const int j = OUT == SHRINK_BLOCKS ? e / kTok : e % kRankBlock, t = OUT == SHRINK_BLOCKS ? e % kTok : e / kRankBlock;
+      const bool own = s_id[t] == a;
+      if (OUT == SHRINK_BLOCKS ? (j >= live || t0 + t >= p.ldp) : (!own || j0 + j >= rs)) continue;
       if (OUT == SHRINK_F32) {
-        p.S[(t0 + t) * rs + j0 + j] = v;
+        p.S[(t0 + t) * rs + j0 + j] = v[o];
       } else {
-        if (OUT == SHRINK_BLOCKS && p.scale) v *= __ldg(p.scale + a);
+        if (OUT == SHRINK_BLOCKS && p.scale) v[o] *= __ldg(p.scale + a);
         uint16_t term[P];
-        split_terms<P>(v, term);
+        split_terms<P>(v[o], term);
 #pragma unroll
         for (int q = 0; q < P; ++q) {
           if (OUT == SHRINK_TERMS)
@@ -301,7 +322,7 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
         }
       }
     }
-    if (C > 1) cluster_sync();  // the sums may be overwritten, and a CTA may leave
+    if (C > 1) cluster_wait();  // the sums may be overwritten, and a CTA may leave
     __syncthreads();
   }
 
@@ -614,10 +635,11 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* adapter,
 }
 
 template <bool BY_RANK, int P>
-__global__ void __launch_bounds__(lora::kThreads) lora_outer_kernel(const __grid_constant__ LoraOuter p) {
+__global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __grid_constant__ LoraOuter p) {
   using namespace lora;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kOuterStages = outer_stages(P);
   constexpr uint32_t kStage = kOuterM + P * kOuterV;  // Z tile, then P terms of [64 tokens][up to 64 ranks]
   __shared__ int32_t s_id[kOuterStages][kTok];
   __shared__ uint64_t s_full[kOuterStages];
@@ -667,38 +689,38 @@ __global__ void __launch_bounds__(lora::kThreads) lora_outer_kernel(const __grid
   for (int i = 0; i < kOuterStages - 1; ++i)
     if (i < mine) load(i, tile_at(i));
   int32_t next = tile_at(kOuterStages - 1);
-  // Swizzle of the term boxes: rows of 32, 64 or 128 bytes.
-  const uint32_t vrow = (uint32_t)box * 2;
-  const int vshift = box >= 64 ? 0 : box >= 32 ? 1 : 2;
-  const uint32_t vmask = box >= 64 ? 7u : box >= 32 ? 3u : 1u;
-  const bool plain = box != 16 && box != 32 && box != 64;  // other widths come unswizzled
-  for (int i = 0; i < mine; ++i) {
-    const int slot = i % kOuterStages;
-    mbar_wait(&s_full[slot], (uint32_t)(i / kOuterStages) & 1u, &s_abort, p.status, kWaitNs);
-    __syncthreads();  // the ids are there, and the slot of tile i - 1 is free
-    if (i + kOuterStages - 1 < mine) load(i + kOuterStages - 1, next);
-    next = tile_at(i + kOuterStages);
-    const uint32_t m = smem_u32(smem + slot * kStage), v = m + kOuterM;
-    const int mi = lane >> 3, l8 = lane & 7;
-    const unsigned lo = __ballot_sync(0xFFFFFFFFu, s_id[slot][lane] == a);
-    const unsigned hi = __ballot_sync(0xFFFFFFFFu, s_id[slot][32 + lane] == a);
-    float acc[8][4] = {};
+  // Addresses within a stage.  The swizzles XOR row bits that a step of 16 rows leaves alone, so a lane's offsets are
+  // the same in every step: Z in units of the K step, the terms' four 16-rank blocks (rows of 32, 64 or 128 bytes
+  // swizzled within themselves, rows of 96 bytes not).
+  const int mi = lane >> 3, l8 = lane & 7;
+  const uint32_t z_row = (uint32_t)(16 * warp + 8 * (mi & 1) + l8);
+  const uint32_t z_off = z_row * 128, z_sw = z_row & 7u, z_unit = (uint32_t)(mi >> 1);
+  const uint32_t v_step = 16u * (uint32_t)box * 2u;
+  uint32_t v_off[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint32_t unit = (uint32_t)(2 * b + (mi >> 1));
+    const uint32_t sw = box == 64 ? (uint32_t)l8 : box == 32 ? (uint32_t)(l8 >> 1) & 3u : box == 16 ? (uint32_t)(l8 >> 2) : 0u;
+    v_off[b] = kOuterM + (uint32_t)(8 * (mi & 1) + l8) * (uint32_t)box * 2u + ((unit ^ sw) << 4);
+  }
+  // One tile's products.  MASKED: some of its tokens are not the adapter's and leave both operands: their Inf or NaN in
+  // one would survive a 0 in the other, and S of a token without an adapter is not written at all.
+  auto products = [&](uint32_t m, unsigned lo, unsigned hi, float (&acc)[8][4], auto masked) {
+    constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       const unsigned used = ((ks & 2 ? hi : lo) >> (16 * (ks & 1))) & 0xFFFFu;  // this step's tokens of the adapter
-      if (!used) continue;
-      uint32_t z[4];
-      const int row = 16 * warp + 8 * (mi & 1) + l8;
-      ldmatrix_x4(z, m + row * 128 + (((2 * ks + (mi >> 1)) ^ (row & 7)) << 4));
-      // Other tokens leave both operands: their Inf or NaN in one would survive a 0 in the other, and S of a token
-      // without an adapter is not written at all.
-      uint32_t keep[2];
+      if (MASKED && !used) continue;
+      uint32_t z[4], keep[2] = {~0u, ~0u};
+      ldmatrix_x4(z, m + z_off + (((2 * ks + z_unit) ^ z_sw) << 4));
+      if (MASKED) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const unsigned two = used >> (8 * h + 2 * (lane & 3));
-        keep[h] = (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
-        z[2 * h] &= keep[h];
-        z[2 * h + 1] &= keep[h];
+        for (int h = 0; h < 2; ++h) {
+          const unsigned two = used >> (8 * h + 2 * (lane & 3));
+          keep[h] = (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+          z[2 * h] &= keep[h];
+          z[2 * h + 1] &= keep[h];
+        }
       }
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
@@ -706,15 +728,33 @@ __global__ void __launch_bounds__(lora::kThreads) lora_outer_kernel(const __grid
 #pragma unroll
         for (int q = 0; q < P; ++q) {
           uint32_t f[4];
-          const int t = 16 * ks + 8 * (mi & 1) + l8;
-          const uint32_t unit = (uint32_t)(2 * b + (mi >> 1));
-          const uint32_t sw = plain ? unit : unit ^ (((uint32_t)t >> vshift) & vmask);
-          ldmatrix_x4_trans(f, v + q * kOuterV + t * vrow + (sw << 4));
-          mma_bf16(acc[2 * b], z, f[0] & keep[0], f[1] & keep[1]);
-          mma_bf16(acc[2 * b + 1], z, f[2] & keep[0], f[3] & keep[1]);
+          ldmatrix_x4_trans(f, m + q * kOuterV + ks * v_step + v_off[b]);
+          if (MASKED) {
+            f[0] &= keep[0];
+            f[1] &= keep[1];
+            f[2] &= keep[0];
+            f[3] &= keep[1];
+          }
+          mma_bf16(acc[2 * b], z, f[0], f[1]);
+          mma_bf16(acc[2 * b + 1], z, f[2], f[3]);
         }
       }
     }
+  };
+  for (int i = 0; i < mine; ++i) {
+    const int slot = i % kOuterStages;
+    mbar_wait(&s_full[slot], (uint32_t)(i / kOuterStages) & 1u, &s_abort, p.status, kWaitNs);
+    __syncthreads();  // the ids are there, and the slot of tile i - 1 is free
+    if (i + kOuterStages - 1 < mine) load(i + kOuterStages - 1, next);
+    next = tile_at(i + kOuterStages);
+    const uint32_t m = smem_u32(smem + slot * kStage);
+    const unsigned lo = __ballot_sync(0xFFFFFFFFu, s_id[slot][lane] == a);
+    const unsigned hi = __ballot_sync(0xFFFFFFFFu, s_id[slot][32 + lane] == a);
+    float acc[8][4] = {};
+    if ((lo & hi) == 0xFFFFFFFFu)
+      products(m, lo, hi, acc, std::false_type());
+    else
+      products(m, lo, hi, acc, std::true_type());
 #pragma unroll
     for (int e = 0; e < 32; ++e) sum[e >> 2][e & 3] += acc[e >> 2][e & 3];
   }
@@ -730,25 +770,34 @@ __global__ void __launch_bounds__(lora::kThreads) lora_outer_kernel(const __grid
   const float scale = p.scale ? __ldg(p.scale + a) : 1.f;
   const int part = kRows / C;  // rows that this CTA joins and stores
   const int live = p.rank - j0 < kOuterRank ? p.rank - j0 : kOuterRank;
-  for (int e = tid; e < part * live; e += kThreads) {
-    const int row = (BY_RANK ? e % part : e / live) + (int)rank * part, j = BY_RANK ? e / part : e % live;
-    if (r0 + row >= p.rows) continue;
+  // Neighbouring lanes take neighbouring ranks of a row, for the reads across the cluster; this CTA's rows of its own
+  // sums are read by nobody else, so the joined values go back there and leave in the order of the output.
+  float* own = s_sum + (int)rank * part * (kOuterRank + 1);
+  for (int e = tid; e < part * kOuterRank; e += kThreads) {
+    const int at = (e / kOuterRank) * (kOuterRank + 1) + e % kOuterRank;
     float got[8], v = 0.f;
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-      if (c < C) got[c] = ld_cluster_f32(map_to_cta(smem_u32(s_sum + row * (kOuterRank + 1) + j), c));
+      if (c < C) got[c] = ld_cluster_f32(map_to_cta(smem_u32(own + at), c));
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       if (c < C) v += got[c];
-    v *= scale;
-    const int64_t at = BY_RANK ? ((int64_t)a * p.rank + j0 + j) * p.rows + r0 + row
-                               : ((int64_t)a * p.rows + r0 + row) * p.rank + j0 + j;
+    own[at] = v * scale;
+  }
+  if (C > 1) cluster_arrive();  // done with the other CTAs' sums
+  __syncthreads();
+  for (int e = tid; e < part * live; e += kThreads) {
+    const int row = BY_RANK ? e % part : e / live, j = BY_RANK ? e / part : e % live;
+    const int64_t r = r0 + (int)rank * part + row;
+    if (r >= p.rows) continue;
+    const float v = own[row * (kOuterRank + 1) + j];
+    const int64_t at = BY_RANK ? ((int64_t)a * p.rank + j0 + j) * p.rows + r : ((int64_t)a * p.rows + r) * p.rank + j0 + j;
     if (p.out_f32)
       static_cast<float*>(p.out)[at] = v;
     else
       static_cast<uint16_t*>(p.out)[at] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
   }
-  if (C > 1) cluster_sync();  // no CTA leaves while another still reads its sums
+  if (C > 1) cluster_wait();  // no CTA leaves while another still reads its sums
 }
 
 __global__ void __launch_bounds__(256) invert_clear_kernel(int64_t K, int32_t* inv) {
