@@ -315,6 +315,9 @@ struct GemmRequest {
   // allocation-free entry point for shapes it does not chunk itself
   bool allow_staging = true;
   GemmPartials* partials = nullptr;  // set: a split-K GEMM leaves its partial sums there
+  // the launch before this call began with pdl_gate() or ended with pdl_leave() and writes nothing that the call's
+  // first launch reads (adapters): that launch may run beside it
+  bool beside = false;
   const GemmExt* ext = nullptr;      // set: further reduction steps (on a shape the SM-pair kernel serves)
   const PairEpiData* epi = nullptr;  // set: the SM-pair kernel's epilogue (on a shape that kernel serves)
 };
@@ -570,7 +573,7 @@ static nm_status run_gemm(const GemmRequest& q, cudaStream_t stream) {
         release();
         return cuda_fail(e, "staging buffer for the permuted input");
       }
-      e = launch_gather_rows(q.X, q.ldx, q.idx, q.K, q.T, static_cast<uint16_t*>(staged), ldp, stream);
+      e = launch_gather_rows(q.X, q.ldx, q.idx, q.K, q.T, static_cast<uint16_t*>(staged), ldp, stream, nullptr, q.beside);
       if (e != cudaSuccess) {
         release();
         return cuda_fail(e, "gather launch");
@@ -609,6 +612,7 @@ static nm_status run_gemm(const GemmRequest& q, cudaStream_t stream) {
           release();
           return cuda_fail(e, "split-K workspace");
         }
+        p.early = q.beside && !staged && !staged_a;
         p.ws = q.partials ? q.partials->ws->as<float>() : static_cast<float*>(ws);
         if (q.partials) {
           p.keep_partials = 1;
@@ -995,6 +999,7 @@ nm_status run_spmm(const uint16_t* values, const uint32_t* meta, int n, int m, i
   GemmRequest q = gemm_request(values, meta, n, m, R, K, idx, X, ldx, T, Y, ldy, y_dtype);
   q.partials = partials;
   q.ext = ext;
+  q.beside = ext || partials;
   return run_gemm(q, stream);
 }
 
@@ -1079,7 +1084,7 @@ nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m,
   void* wd = nullptr;
   e = cudaMallocFromPoolAsync(&wd, (size_t)(R * ldk * 2), pool, stream);
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the decompressed weights");
-  e = launch_decompress(values, meta, R, K, n, m, static_cast<uint16_t*>(wd), ldk, stream);
+  e = launch_decompress(values, meta, R, K, n, m, static_cast<uint16_t*>(wd), ldk, stream, ext != nullptr);
   DenseParams p;
   std::memset(&p, 0, sizeof p);
   p.M = K;

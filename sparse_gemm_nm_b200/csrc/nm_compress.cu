@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(256) decompress_2of4_tiled_kernel(const uint16
                                                                     uint32_t K, uint16_t* __restrict__ W,
                                                                     int64_t ldw, uint32_t cblocks, uint32_t total,
                                                                     bool vec, const uint8_t* __restrict__ tile_map,
-                                                                    uint32_t rtiles) {
-  pdl_gate();
+                                                                    uint32_t rtiles, bool early) {
+  pdl_enter(early);
   for (uint32_t w = blockIdx.x * blockDim.x + threadIdx.x; w < total; w += gridDim.x * blockDim.x) {
     const uint32_t blk = w >> 6, wi = w & 63u;
     const uint32_t l = wi >> 2, q = wi & 3u;
@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(256) decompress_2of4_tiled_kernel(const uint16
     if (r_lo + 8 < R)
       decompress_half16(V + (int64_t)(r_lo + 8) * (K >> 1), W + (int64_t)(r_lo + 8) * ldw, word >> 16, k0, K, vec);
   }
+  pdl_leave(early);
 }
 
 // Generic decompress: one thread per group.
@@ -335,8 +336,8 @@ template <int M>
 __global__ void __launch_bounds__(256) decompress_generic_kernel(const uint16_t* __restrict__ V,
                                                                  const uint32_t* __restrict__ meta, int64_t R,
                                                                  int64_t K, int n, uint16_t* __restrict__ W,
-                                                                 int64_t ldw) {
-  pdl_gate();
+                                                                 int64_t ldw, bool early) {
+  pdl_enter(early);
   constexpr int B = M == 2 ? 1 : M == 4 ? 2 : M == 8 ? 3 : 4;
   constexpr int S = 32 / B;
   const int64_t groups = K / M;
@@ -363,6 +364,7 @@ __global__ void __launch_bounds__(256) decompress_generic_kernel(const uint16_t*
 #pragma unroll
     for (int i = 0; i < M; ++i) dst[i] = e[i];
   }
+  pdl_leave(early);
 }
 
 __global__ void fill_zero_kernel(uint8_t* Y, int64_t R, int64_t row_bytes, int64_t ld_bytes) {
@@ -387,11 +389,12 @@ constexpr int kGatherCtasPerSm = 4;
 constexpr size_t kGatherSmemCap = 56 * 1024;
 
 __global__ void __launch_bounds__(256) gather_rows_kernel(const GatherJob g) {
-  pdl_gate();
-  if (g.skip_if && *reinterpret_cast<const volatile uint32_t*>(g.skip_if)) return;
+  pdl_enter(g.early);
+  if (g.skip_if && *reinterpret_cast<const volatile uint32_t*>(g.skip_if)) return;  // never together with early
   const int64_t warp = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
   const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
   gather_rows_items(g, warp, nwarps, threadIdx.x & 31);
+  pdl_leave(g.early);
 }
 
 // Re-encoding of an N:M operand whose survivors never exceed two per aligned
@@ -506,22 +509,22 @@ cudaError_t launch_compress(const uint16_t* W, int64_t R, int64_t K, int64_t ldw
 }
 
 cudaError_t launch_decompress(const uint16_t* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
-                              uint16_t* W_out, int64_t ldw, cudaStream_t s) {
+                              uint16_t* W_out, int64_t ldw, cudaStream_t s, bool early) {
   const int threads = 256;
   if (tiled_meta(n, m)) {
     const int64_t total = meta_words(R, K, n, m);
     const bool vec = K % 16 == 0 && ldw % 8 == 0 && aligned16(W_out) && aligned16(values);
     launch_pdl(decompress_2of4_tiled_kernel, grid_for(total, threads), threads, 0, s,
         values, meta, (uint32_t)R, (uint32_t)K, W_out, ldw, (uint32_t)meta_col_blocks(K), (uint32_t)total, vec,
-        nullptr, 0u);
+        nullptr, 0u, early);
   } else {
     const int64_t work = R * (K / m);
     const int grid = grid_for(work, threads);
     switch (m) {
-      case 2: launch_pdl(decompress_generic_kernel<2>, grid, threads, 0, s, values, meta, R, K, n, W_out, ldw); break;
-      case 4: launch_pdl(decompress_generic_kernel<4>, grid, threads, 0, s, values, meta, R, K, n, W_out, ldw); break;
-      case 8: launch_pdl(decompress_generic_kernel<8>, grid, threads, 0, s, values, meta, R, K, n, W_out, ldw); break;
-      default: launch_pdl(decompress_generic_kernel<16>, grid, threads, 0, s, values, meta, R, K, n, W_out, ldw); break;
+      case 2: launch_pdl(decompress_generic_kernel<2>, grid, threads, 0, s, values, meta, R, K, n, W_out, ldw, early); break;
+      case 4: launch_pdl(decompress_generic_kernel<4>, grid, threads, 0, s, values, meta, R, K, n, W_out, ldw, early); break;
+      case 8: launch_pdl(decompress_generic_kernel<8>, grid, threads, 0, s, values, meta, R, K, n, W_out, ldw, early); break;
+      default: launch_pdl(decompress_generic_kernel<16>, grid, threads, 0, s, values, meta, R, K, n, W_out, ldw, early); break;
     }
   }
   count_launch();
@@ -535,13 +538,14 @@ cudaError_t launch_decompress_tiles(const uint16_t* values, const uint32_t* meta
   const bool vec = K % 16 == 0 && ldw % 8 == 0 && aligned16(W_out) && aligned16(values);
   launch_pdl(decompress_2of4_tiled_kernel, grid_for(total, threads), threads, 0, s,
       values, meta, (uint32_t)R, (uint32_t)K, W_out, ldw, (uint32_t)meta_col_blocks(K), (uint32_t)total, vec,
-      tile_map, (uint32_t)((R + 127) / 128));
+      tile_map, (uint32_t)((R + 127) / 128), false);
   count_launch();
   return cudaGetLastError();
 }
 
 cudaError_t launch_gather_rows(const uint16_t* X, int64_t ldx, const int32_t* idx, int64_t K, int64_t T,
-                               uint16_t* Xp, int64_t ldp, cudaStream_t s, const uint32_t* skip_if) {
+                               uint16_t* Xp, int64_t ldp, cudaStream_t s, const uint32_t* skip_if,
+                               bool early) {
   const int threads = 256;
   static std::atomic<bool> configured[64];  // zero-initialised: false
   int dev = 0;
@@ -556,7 +560,7 @@ cudaError_t launch_gather_rows(const uint16_t* X, int64_t ldx, const int32_t* id
   const int64_t want = (items + 7) / 8;  // 8 warps per CTA
   const int64_t cap = (int64_t)sm_count_current() * kGatherCtasPerSm;
   const int grid = (int)(want < cap ? (want > 0 ? want : 1) : cap);
-  const GatherJob g{X, ldx, idx, K, T, Xp, ldp, skip_if};
+  const GatherJob g{X, ldx, idx, K, T, Xp, ldp, skip_if, early};
   cudaError_t e = launch_pdl(gather_rows_kernel, grid, threads, kGatherSmemCap, s, g);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();

@@ -45,12 +45,24 @@ struct GatherJob {
   uint16_t* Xp;
   int64_t ldp;
   const uint32_t* skip_if;  // gather_rows_kernel does nothing when this word is set and nonzero at run time
+  bool early;               // gather_rows_kernel runs beside its predecessor (pdl_enter)
 };
 
 #ifdef __CUDACC__
 __device__ __forceinline__ void pdl_gate() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// A kernel that reads nothing its predecessor in the stream writes (and whose predecessor itself began with pdl_gate())
+// may run beside it: with early set, pdl_enter() does not wait, and pdl_leave(), the last thing of every thread, does,
+// so that this kernel too completes only after everything before it, as its successors assume.
+__device__ __forceinline__ void pdl_enter(bool early) {
+  if (!early) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_leave(bool early) {
+  if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Items warp, warp + nwarps, ... of a gather: each lane moves 16-byte pieces of
@@ -110,7 +122,7 @@ void count_launch();
 cudaError_t launch_compress(const uint16_t* W, int64_t R, int64_t K, int64_t ldw, int n, int m, uint16_t* values,
                             uint32_t* meta, cudaStream_t s);
 cudaError_t launch_decompress(const uint16_t* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
-                              uint16_t* W_out, int64_t ldw, cudaStream_t s);
+                              uint16_t* W_out, int64_t ldw, cudaStream_t s, bool early = false);
 // 2:4 decompress of the 128 x 128 tiles that the SM-pair hybrid kernel reads as
 // dense tiles: tile_map entry non-zero (tile map ceil(R/128) x ceil(K/128)) and
 // the partner row tile (row tile index ^ 1) present and zero in the same column;
@@ -120,7 +132,8 @@ cudaError_t launch_decompress_tiles(const uint16_t* values, const uint32_t* meta
 // Xp[k] = X[idx[k]] (zero rows for idx outside [0, K)); with skip_if set, the
 // launch does nothing when that device word is nonzero when it runs.
 cudaError_t launch_gather_rows(const uint16_t* X, int64_t ldx, const int32_t* idx, int64_t K, int64_t T,
-                               uint16_t* Xp, int64_t ldp, cudaStream_t s, const uint32_t* skip_if = nullptr);
+                               uint16_t* Xp, int64_t ldp, cudaStream_t s, const uint32_t* skip_if = nullptr,
+                               bool early = false);
 cudaError_t launch_reencode_2of4(const uint16_t* values, const uint32_t* meta, int64_t R, int64_t K, int n, int m,
                                  uint16_t* values2, uint32_t* meta2, cudaStream_t s);
 cudaError_t launch_fill_zero(void* Y, int64_t R, int64_t T, int64_t ldy, int esize, cudaStream_t s);

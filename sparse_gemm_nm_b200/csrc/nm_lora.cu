@@ -38,13 +38,14 @@ namespace lora {
 constexpr int kThreads = 256;
 constexpr int kDepth = 128;      // reduction steps of a shrink stage
 constexpr int kRankBlock = 32;   // rank rows of a shrink work item
-constexpr int kStages = 3;
+constexpr int kMaxStages = 6;
 constexpr uint32_t kZBytes = kDepth * kTok * 2;
 constexpr uint32_t kMBytes = kRankBlock * kDepth * 2;
 constexpr uint32_t kShrinkPart = 2 * kTok * (kRankBlock + 1) * 4;  // the wider of the two layouts of the joined sums
-constexpr uint32_t kShrinkSmem = kStages * (kZBytes + kMBytes) + kShrinkPart + 1024;
+__host__ __device__ constexpr uint32_t shrink_smem(int stages) { return (uint32_t)stages * (kZBytes + kMBytes) + 1024; }
+static_assert(kShrinkPart <= kZBytes + kMBytes, "the joined sums reuse the first stage");
 constexpr int kRows = 128;       // rows of an expand or outer tile
-constexpr int kExpandStages = 4; // adapters in flight
+constexpr uint32_t kExpandBatch = 96 * 1024;  // bytes of adapters' tiles in flight
 constexpr int kOuterRank = 64;   // rank columns of an outer work item
 constexpr uint32_t kOuterM = kRows * kTok * 2;
 constexpr uint32_t kOuterV = kTok * kOuterRank * 2;  // one bf16 term
@@ -155,25 +156,19 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
   __shared__ int32_t s_id[kTok], s_list[kTok];
   __shared__ int s_count, s_abort;
   __shared__ uint32_t s_present[kMaxCat / 32];
-  __shared__ uint64_t s_full[kStages];
-  float* s_part = reinterpret_cast<float*>(smem + kStages * (kZBytes + kMBytes));
+  __shared__ uint64_t s_full[kMaxStages];
+  float* s_part = reinterpret_cast<float*>(smem);  // joined sums, over the first stages
+  const int stages = p.stages;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&s_full[i], 1);
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(&s_full[i], 1);
     s_abort = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
     if (p.D > 0) tma_prefetch_desc(&p.tm_z);
     if (p.vec) tma_prefetch_desc(&p.tm_m);
   }
-  pdl_gate();
-  if (p.inv) {
-    const int64_t all = (int64_t)gridDim.x * gridDim.y * kThreads;
-    for (int64_t k = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + tid; k < p.idx_n; k += all) {
-      const int32_t j = __ldg(p.idx + k);
-      if (j >= 0 && (int64_t)j < p.idx_n) atomicMax(p.inv + j, (int32_t)k);
-    }
-  }
+  pdl_enter(p.early != 0);
   const uint32_t rank = cluster_ctarank();
   const int C = p.cluster;
   const int64_t tile = blockIdx.x / C;
@@ -184,26 +179,28 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
   const int rs = (p.rank + 15) / 16 * 16;
   const int chunks = (int)((p.D + kDepth - 1) / kDepth);
   const int mine = chunks > (int)rank ? (chunks - (int)rank + C - 1) / C : 0;  // chunks rank, rank + C, ...
-  int use = 0;  // stages taken so far: ring slot use % kStages, phase use / kStages
+  int next_slot = 0, slot = 0;  // ring slots of the next load and of the next chunk to be read
+  uint32_t phase = 0;           // of that chunk
 
   for (int item = blockIdx.y; item < distinct * rblocks; item += gridDim.y) {
     const int32_t a = s_list[item / rblocks];
     const int j0 = (item % rblocks) * kRankBlock;
     const int live = p.rank - j0 < kRankBlock ? p.rank - j0 : kRankBlock;
-    auto load = [&](int i) {  // all threads; chunk i of this CTA into ring slot (use + i) % kStages
-      const int slot = (use + i) % kStages;
-      uint8_t* z = smem + slot * (kZBytes + kMBytes);
+    auto load = [&](int i) {  // all threads; chunk i of this CTA into the next ring slot
+      const int at = next_slot;
+      if (++next_slot == stages) next_slot = 0;
+      uint8_t* z = smem + at * (kZBytes + kMBytes);
       uint8_t* m = z + kZBytes;
       const int d0 = ((int)rank + i * C) * kDepth;
       if (tid == 0) {
-        mbar_arrive_expect_tx(&s_full[slot], kZBytes + (p.vec ? kMBytes : 0u));
-        tma_load_2d(z, &p.tm_z, &s_full[slot], (int32_t)t0, d0);
+        mbar_arrive_expect_tx(&s_full[at], kZBytes + (p.vec ? kMBytes : 0u));
+        tma_load_2d(z, &p.tm_z, &s_full[at], (int32_t)t0, d0);
         if (p.vec) {
           if (TRANS) {
-            tma_load_3d(m, &p.tm_m, &s_full[slot], j0, d0, a);
+            tma_load_3d(m, &p.tm_m, &s_full[at], j0, d0, a);
           } else {
-            tma_load_3d(m, &p.tm_m, &s_full[slot], d0, j0, a);
-            tma_load_3d(m + kMBytes / 2, &p.tm_m, &s_full[slot], d0 + kDepth / 2, j0, a);
+            tma_load_3d(m, &p.tm_m, &s_full[at], d0, j0, a);
+            tma_load_3d(m + kMBytes / 2, &p.tm_m, &s_full[at], d0 + kDepth / 2, j0, a);
           }
         }
       }
@@ -229,14 +226,17 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
       serves = ((group & 2 ? hi : lo) >> (16 * (group & 1))) & 0xFFFFu;
     }
     float sum[2][2][4] = {};
-    for (int i = 0; i < kStages - 1 && i < mine; ++i) load(i);
+    for (int i = 0; i < stages - 1 && i < mine; ++i) load(i);
     for (int i = 0; i < mine; ++i) {
-      const int slot = (use + i) % kStages;
-      mbar_wait(&s_full[slot], (uint32_t)((use + i) / kStages) & 1u, &s_abort, p.status, kWaitNs);
+      mbar_wait(&s_full[slot], phase, &s_abort, p.status, kWaitNs);
       __syncthreads();  // the slot of chunk i - 1 is free, and element-wise loads have landed
-      if (i + kStages - 1 < mine) load(i + kStages - 1);
-      if (!serves) continue;
+      if (i + stages - 1 < mine) load(i + stages - 1);
       const uint32_t z = smem_u32(smem + slot * (kZBytes + kMBytes)), m = z + kZBytes;
+      if (++slot == stages) {
+        slot = 0;
+        phase ^= 1u;
+      }
+      if (!serves) continue;
       float acc[2][2][4] = {};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -261,11 +261,11 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
 #pragma unroll
       for (int e = 0; e < 16; ++e) sum[e >> 3][(e >> 2) & 1][e & 3] += acc[e >> 3][(e >> 2) & 1][e & 3];
     }
-    use += mine;
+    __syncthreads();  // every warp is done with the stages
     // The sums of both K halves, in the order of the output (ranks of a token, or tokens of a rank row, side by side):
     // lanes that read another CTA's shared memory at neighbouring addresses share a transfer (reading it across rows
     // took 14 us of a 25 us item).
-    auto at = [](int j, int t) { return OUT == SHRINK_BLOCKS ? j * (kTok + 1) + t : t * (kRankBlock + 1) + j; };
+    auto part_at = [](int j, int t) { return OUT == SHRINK_BLOCKS ? j * (kTok + 1) + t : t * (kRankBlock + 1) + j; };
     constexpr int kHalf = kShrinkPart / 8;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = 16 * mt + (lane >> 2) + 8 * (e >> 1), t = 16 * group + 8 * nb + 2 * (lane & 3) + (e & 1);
-          s_part[half * kHalf + at(j, t)] = sum[mt][nb][e];
+          s_part[half * kHalf + part_at(j, t)] = sum[mt][nb][e];
         }
     __syncthreads();
     if (C > 1) cluster_sync();  // every CTA's sums are written
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
       v[o] = 0.f;
       if (e >= kRankBlock * kTok) continue;
       const int j = OUT == SHRINK_BLOCKS ? e / kTok : e % kRankBlock, t = OUT == SHRINK_BLOCKS ? e % kTok : e / kRankBlock;
-      const uint32_t mine_at = smem_u32(s_part + at(j, t));
+      const uint32_t mine_at = smem_u32(s_part + part_at(j, t));
       float part[8][2];
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -352,6 +352,14 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
       p.masks[tile] = mask;
     }
   }
+  pdl_leave(p.early != 0);
+  if (p.inv) {  // after the wait: the launch before presets inv
+    const int64_t all = (int64_t)gridDim.x * gridDim.y * kThreads;
+    for (int64_t k = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + tid; k < p.idx_n; k += all) {
+      const int32_t j = __ldg(p.idx + k);
+      if (j >= 0 && (int64_t)j < p.idx_n) atomicMax(p.inv + j, (int32_t)k);
+    }
+  }
 }
 
 template <bool TRANS, int P>
@@ -364,16 +372,56 @@ __global__ void __launch_bounds__(lora::kThreads) lora_expand_kernel(const LoraE
   const int rs = (p.rank + 15) / 16 * 16;
   const uint32_t pitch = (uint32_t)rs * 2 + 16;  // an odd number of 16-byte units: eight rows miss each other's banks
   const uint32_t m_bytes = TRANS ? (uint32_t)rs * 256u : kRows * pitch;
-  uint8_t* s_m = smem;                            // kExpandStages adapters' tiles
-  uint8_t* s_s = smem + kExpandStages * m_bytes;  // P terms of 64 tokens x rs
+  uint8_t* s_m = smem;                      // p.batch adapters' tiles
+  uint8_t* s_s = smem + p.batch * m_bytes;  // P terms of 64 tokens x rs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t r0 = (int64_t)blockIdx.x * kRows, t0 = (int64_t)blockIdx.y * kTok;
 
-  // The base first: it needs nothing else, and its loads are in flight behind the rest.
+  // The base first: it needs nothing else, and its loads are in flight behind the rest.  Several K ranges' sums are
+  // added on the way into shared memory, four ranges in flight for every 16 bytes.
   float acc[8][4];
   const int tokens = p.T - t0 < kTok ? (int)(p.T - t0) : kTok;
+  if (p.splits > 1) {
+    float* s_base = reinterpret_cast<float*>(smem + p.base_off);
+    const int quads = (int)p.ldb / 4;  // rows of a K range's sums: 16, 32 or 64 columns (one tile of tokens)
+    for (int u = tid; u < kRows * quads; u += kThreads) {
+      const int row = u / quads, c = u - row * quads;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r0 + row < p.rows) {
+        const float* src = p.base + (r0 + row) * p.ldb + 4 * c;
+        for (int q0 = 0; q0 < p.splits; q0 += 4) {
+          float4 x[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            x[q] = q0 + q < p.splits ? __ldcg(reinterpret_cast<const float4*>(src + (q0 + q) * p.split_stride))
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v.x += x[q].x;
+            v.y += x[q].y;
+            v.z += x[q].z;
+            v.w += x[q].w;
+          }
+        }
+      }
+      *reinterpret_cast<float4*>(s_base + row * (p.ldb + 4) + 4 * c) = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int nb = 0; nb < 8; ++nb) {
+        const int t = 8 * nb + 2 * (lane & 3);
+        float2 v = make_float2(0.f, 0.f);
+        if (t < tokens)
+          v = *reinterpret_cast<const float2*>(s_base + (16 * warp + (lane >> 2) + 8 * h) * (p.ldb + 4) + t);
+        acc[nb][2 * h] = v.x;
+        acc[nb][2 * h + 1] = v.y;
+      }
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    if (p.splits > 1) break;
     const int64_t row = r0 + 16 * warp + (lane >> 2) + 8 * h;
     int64_t brow = row < p.rows ? row : -1;
     if (p.base_row && brow >= 0) brow = __ldg(p.base_row + row);
@@ -385,22 +433,11 @@ __global__ void __launch_bounds__(lora::kThreads) lora_expand_kernel(const LoraE
       acc[nb][2 * h] = v.x;
       acc[nb][2 * h + 1] = v.y;
     }
-    for (int q = 1; q < p.splits; ++q) {
-      src += p.split_stride;
-#pragma unroll
-      for (int nb = 0; nb < 8; ++nb) {
-        if (brow >= 0 && 8 * nb + 2 * (lane & 3) < tokens) {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(src + 8 * nb));
-          acc[nb][2 * h] += v.x;
-          acc[nb][2 * h + 1] += v.y;
-        }
-      }
-    }
   }
   const int distinct = tile_adapters(p.adapter, p.n, t0, p.T, s_id, s_list, &s_count);
 
-  auto load = [&](int i) {
-    uint8_t* m = s_m + (i % kExpandStages) * m_bytes;
+  auto load = [&](int i, int at) {
+    uint8_t* m = s_m + at * m_bytes;
     const int64_t a = s_list[i];
     if (!TRANS) {
       const int units = rs / 8;
@@ -418,11 +455,7 @@ __global__ void __launch_bounds__(lora::kThreads) lora_expand_kernel(const LoraE
       }
     }
   };
-#pragma unroll
-  for (int i = 0; i < kExpandStages - 1; ++i) {
-    if (i < distinct) load(i);
-    cp_commit();
-  }
+  for (int i = 0; i < p.batch && i < distinct; ++i) load(i, i);
   // s_a S of the tile's tokens as P bf16 terms (0 for a token without an adapter, whose S is not written)
   for (int u = tid; u < tokens * (rs / 4); u += kThreads) {
     const int t = u / (rs / 4), j = 4 * (u - t * (rs / 4));
@@ -445,13 +478,19 @@ __global__ void __launch_bounds__(lora::kThreads) lora_expand_kernel(const LoraE
           make_uint2((uint32_t)term[0][q] | (uint32_t)term[1][q] << 16, (uint32_t)term[2][q] | (uint32_t)term[3][q] << 16);
   }
 
-  for (int i = 0; i < distinct; ++i) {
-    cp_wait<kExpandStages - 2>();
-    __syncthreads();  // the tile of adapter i has landed (and S, at first); that of adapter i - 1 is free
-    if (i + kExpandStages - 1 < distinct) load(i + kExpandStages - 1);
-    cp_commit();
+  for (int i = 0, at = 0; i < distinct; ++i, ++at) {
+    if (at == p.batch) {  // the next batch of adapters' tiles, all in flight together
+      __syncthreads();
+      at = 0;
+      for (int u = 0; u < p.batch && i + u < distinct; ++u) load(i + u, u);
+    }
+    if (at == 0) {
+      cp_commit();
+      cp_wait<0>();
+      __syncthreads();  // the batch has landed (and S, at first)
+    }
     const int32_t a = s_list[i];
-    const uint32_t m = smem_u32(s_m + (i % kExpandStages) * m_bytes);
+    const uint32_t m = smem_u32(s_m + at * m_bytes);
     const unsigned lo = __ballot_sync(0xFFFFFFFFu, s_id[lane] == a), hi = __ballot_sync(0xFFFFFFFFu, s_id[32 + lane] == a);
     const int mi = lane >> 3, l8 = lane & 7;
 #pragma unroll
@@ -653,7 +692,7 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
     tma_prefetch_desc(&p.tm_z);
     tma_prefetch_desc(&p.tm_v);
   }
-  pdl_gate();
+  pdl_enter(p.early != 0);
   const uint32_t rank = cluster_ctarank();
   const int C = p.cluster;
   const int64_t r0 = (int64_t)(blockIdx.x / C) * kRows;
@@ -798,6 +837,7 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
       static_cast<uint16_t*>(p.out)[at] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
   }
   if (C > 1) cluster_wait();  // no CTA leaves while another still reads its sums
+  pdl_leave(p.early != 0);
 }
 
 __global__ void __launch_bounds__(256) invert_clear_kernel(int64_t K, int32_t* inv) {
@@ -841,13 +881,13 @@ static cudaError_t launch_clustered(Kern kernel, dim3 grid, int cluster, uint32_
 template <bool TRANS>
 static cudaError_t launch_shrink_out(const LoraShrink& p, dim3 grid, cudaStream_t s) {
   using namespace lora;
-  const uint32_t b = kShrinkSmem;
-  if (p.out == SHRINK_F32) return launch_clustered(lora_shrink_kernel<TRANS, SHRINK_F32, 1>, grid, p.cluster, b, b, p, s);
+  const uint32_t b = shrink_smem(p.stages), most = shrink_smem(kMaxStages);
+  if (p.out == SHRINK_F32) return launch_clustered(lora_shrink_kernel<TRANS, SHRINK_F32, 1>, grid, p.cluster, b, most, p, s);
   if (p.out == SHRINK_TERMS)
-    return p.planes == 3 ? launch_clustered(lora_shrink_kernel<TRANS, SHRINK_TERMS, 3>, grid, p.cluster, b, b, p, s)
-                         : launch_clustered(lora_shrink_kernel<TRANS, SHRINK_TERMS, 2>, grid, p.cluster, b, b, p, s);
-  return p.planes == 3 ? launch_clustered(lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 3>, grid, p.cluster, b, b, p, s)
-                       : launch_clustered(lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 2>, grid, p.cluster, b, b, p, s);
+    return p.planes == 3 ? launch_clustered(lora_shrink_kernel<TRANS, SHRINK_TERMS, 3>, grid, p.cluster, b, most, p, s)
+                         : launch_clustered(lora_shrink_kernel<TRANS, SHRINK_TERMS, 2>, grid, p.cluster, b, most, p, s);
+  return p.planes == 3 ? launch_clustered(lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 3>, grid, p.cluster, b, most, p, s)
+                       : launch_clustered(lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 2>, grid, p.cluster, b, most, p, s);
 }
 
 cudaError_t launch_lora_shrink(LoraShrink& p, bool trans, cudaStream_t s) {
@@ -859,24 +899,31 @@ cudaError_t launch_lora_shrink(LoraShrink& p, bool trans, cudaStream_t s) {
   while (p.cluster < 8 && tiles * p.cluster < target && chunks / (2 * p.cluster) >= 2) p.cluster <<= 1;
   // ... and further CTAs take the tile's adapters side by side when the tiles are few
   const int64_t items = (p.n < kTok ? p.n : kTok) * ((p.rank + kRankBlock - 1) / kRankBlock);
+  const int64_t rblocks = (p.rank + kRankBlock - 1) / kRankBlock;
   int64_t y = (target + tiles * p.cluster - 1) / (tiles * p.cluster);
+  if (y < rblocks) y = rblocks;
   if (y > items) y = items;
-  if (y < 1) y = 1;
   if (tiles * p.cluster >= (1ll << 31)) return cudaErrorInvalidValue;
+  // Three CTAs to an SM in a full grid (three stages); with an SM to itself a CTA has all its chunks in flight.
+  p.stages = tiles * p.cluster * y <= sm_count_current() ? kMaxStages : 3;
   const dim3 grid((unsigned)(tiles * p.cluster), (unsigned)y);
   return trans ? launch_shrink_out<true>(p, grid, s) : launch_shrink_out<false>(p, grid, s);
 }
 
-cudaError_t launch_lora_expand(const LoraExpand& p, bool trans, cudaStream_t s) {
+cudaError_t launch_lora_expand(LoraExpand& p, bool trans, cudaStream_t s) {
   using namespace lora;
   const int64_t tiles = tiles_of(p.T), blocks = (p.rows + kRows - 1) / kRows;
   if (tiles > 65535) return cudaErrorInvalidValue;
   const uint32_t terms = p.out_f32 ? 3 : 2;
-  auto bytes = [&](uint32_t r) {
-    return kExpandStages * (trans ? r * 256u : kRows * (r * 2 + 16)) + terms * kTok * (r * 2 + 16);
-  };
+  const uint32_t r = (uint32_t)rank_stride(p.rank), tile = trans ? r * 256u : kRows * (r * 2 + 16);
+  int64_t batch = kExpandBatch / tile;  // at least 2
+  if (batch > p.n) batch = p.n > 0 ? p.n : 1;
+  if (batch > kTok) batch = kTok;
+  p.batch = (int)batch;
   const dim3 grid((unsigned)blocks, (unsigned)tiles);
-  const uint32_t b = bytes((uint32_t)rank_stride(p.rank)), most = bytes(kMaxRank);
+  p.base_off = (uint32_t)batch * tile + terms * kTok * (r * 2 + 16);
+  const uint32_t b = p.base_off + (p.splits > 1 ? (uint32_t)(kRows * (p.ldb + 4) * 4) : 0u);
+  const uint32_t most = kExpandBatch + 3 * kTok * (kMaxRank * 2 + 16) + kRows * (kTok + 4) * 4;
   if (trans)
     return p.out_f32 ? launch_clustered(lora_expand_kernel<true, 3>, grid, 1, b, most, p, s)
                      : launch_clustered(lora_expand_kernel<true, 2>, grid, 1, b, most, p, s);
@@ -1033,6 +1080,7 @@ nm_status adapters_for_gemm(const Adapters& ad, bool trans, int64_t D, int64_t r
   p.idx = idx;
   p.idx_n = rows;
   p.inv = inv;
+  p.early = 1;  // reads nothing of the layout launch (inv is taken at its end)
   nm_status st = shrink(ad, trans, D, Z, ldz, T, p, s);
   if (st != NM_OK) return st;
   g.ext = GemmExt{g.cat.as<uint16_t>(), trans ? ad.n * ad.rank : rows, trans ? rows : cat, ldc, g.blocks.as<uint16_t>(), cat,
@@ -1208,11 +1256,12 @@ nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t lddy, c
   if (st == NM_OK && K > 0) st = check_matrix(X, ldx, T, 2, "X");
   if (st == NM_OK) st = require_device();
   if (st != NM_OK) return st;
-  Staged terms(s), plan(s);
+  Staged terms(s), more(s), plan(s);
   const int planes = dtype == NM_OUT_F32 ? 3 : 2;
   const int64_t rs = lora::rank_stride(rank), tiles = lora::tiles_of(T);
   cudaError_t e = plan.get((size_t)((tiles + 1) * num_adapters * 4));
   if (e == cudaSuccess) e = terms.get((size_t)(planes * T * rs * 2));
+  if (e == cudaSuccess) e = more.get((size_t)(planes * T * rs * 2));
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the adapter gradients");
   LoraOuter p = {};
   p.adapter = adapter;
@@ -1228,26 +1277,32 @@ nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t lddy, c
   e = launch_lora_plan(adapter, T, num_adapters, plan.as<int32_t>() + num_adapters, plan.as<int32_t>(), s);
   if (e != cudaSuccess) return cuda_fail(e, "adapter plan launch");
   const uint32_t box = (uint32_t)(rs < lora::kOuterRank ? rs : lora::kOuterRank);
-  st = make_tmap3(&p.tm_v, terms.as<uint16_t>(), (uint64_t)rs, (uint64_t)T, (uint64_t)planes, (uint64_t)rs * 2,
-                  (uint64_t)(T * rs) * 2, box, lora::kTok, box == 64 ? 128 : box == 32 ? 64 : box == 16 ? 32 : 0,
-                  "adapter terms");
-  if (st != NM_OK) return st;
-  for (int which = 0; which < 2; ++which) {  // dB from S = A X and dY, then dA from U = B^T dY and X
-    const int64_t rows = which ? K : R;
-    void* out = which ? dA : dB;
-    if (!out || rows == 0) continue;
+  // S = A X for dB and U = B^T dY for dA, then the two gradients: within each pair the second launch needs nothing of
+  // the first and runs beside it.
+  const bool want[2] = {dB && R > 0, dA && K > 0};
+  for (int which = 0; which < 2; ++which) {
+    if (!want[which]) continue;
     LoraShrink sh = {};
     sh.out = SHRINK_TERMS;
     sh.planes = planes;
-    sh.terms = terms.as<uint16_t>();
+    sh.terms = which ? more.as<uint16_t>() : terms.as<uint16_t>();
+    sh.early = 1;
     st = which ? shrink(ad, true, R, dY, lddy, T, sh, s) : shrink(ad, false, K, X, ldx, T, sh, s);
-    const uint16_t* Z = which ? X : dY;
-    const int64_t ldz = which ? ldx : lddy;
+    if (st != NM_OK) return st;
+  }
+  for (int which = 0; which < 2; ++which) {
+    if (!want[which]) continue;
+    const int64_t rows = which ? K : R;
+    st = make_tmap(&p.tm_z, which ? X : dY, (uint64_t)T, (uint64_t)rows, (uint64_t)(which ? ldx : lddy) * 2, lora::kTok,
+                   lora::kRows, 128, "tokens");
     if (st == NM_OK)
-      st = make_tmap(&p.tm_z, Z, (uint64_t)T, (uint64_t)rows, (uint64_t)ldz * 2, lora::kTok, lora::kRows, 128, "tokens");
+      st = make_tmap3(&p.tm_v, which ? more.as<uint16_t>() : terms.as<uint16_t>(), (uint64_t)rs, (uint64_t)T,
+                      (uint64_t)planes, (uint64_t)rs * 2, (uint64_t)(T * rs) * 2, box, lora::kTok,
+                      box == 64 ? 128 : box == 32 ? 64 : box == 16 ? 32 : 0, "adapter terms");
     if (st != NM_OK) return st;
     p.rows = rows;
-    p.out = out;
+    p.out = which ? dA : dB;
+    p.early = which && want[0];
     e = launch_lora_outer(p, which != 0, s);
     if (e != cudaSuccess) return cuda_fail(e, "adapter gradient launch");
   }

@@ -42,6 +42,8 @@ struct LoraShrink {
   int32_t* inv;
   uint32_t* status;
   int cluster;         // CTAs that share a tile's reduction
+  int stages;          // of its ring
+  int early;           // runs beside its predecessor (pdl_enter)
 };
 cudaError_t launch_lora_shrink(LoraShrink& p, bool trans, cudaStream_t s);
 
@@ -63,8 +65,10 @@ struct LoraExpand {
   void* Y;
   int64_t ldy;
   int out_f32;
+  int batch;          // adapters' tiles in flight (set by the launcher, like base_off)
+  uint32_t base_off;  // splits > 1: the summed base in shared memory
 };
-cudaError_t launch_lora_expand(const LoraExpand& p, bool trans, cudaStream_t s);
+cudaError_t launch_lora_expand(LoraExpand& p, bool trans, cudaStream_t s);
 
 // The adapters' second factors as one matrix, for the projection's own reduction: cat[row][a * rank + j] = B_a[row][j]
 // (rows x cat, zero past n * rank; by_rank = false) or cat[a * rank + j][k] = A_a[j][idx[k]] (n * rank x ldc;
@@ -119,6 +123,7 @@ struct LoraOuter {
   int out_f32;
   uint32_t* status;
   int cluster;
+  int early;  // runs beside its predecessor (pdl_enter)
 };
 cudaError_t launch_lora_plan(const int32_t* adapter, int64_t T, int64_t n, int32_t* tiles, int32_t* counts,
                              cudaStream_t s);

@@ -84,6 +84,7 @@ struct SpmmParams {
   int ext_planes;
   int64_t ext_cat;
   float* ws;
+  int early;          // skinny kernel: runs beside its predecessor (pdl_enter)
   int keep_partials;  // leave the ranges' sums in ws (no reduction launch)
   // fused prune + compress + GEMM: optional outputs of the compressed operand
   uint16_t* out_vals;

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(skinny::kThreads, 1) spmm_skinny_kernel(const 
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   bool ok = true;
-  pdl_gate();  // no global memory touched before this point
+  pdl_enter(p.early);  // no global memory touched before this point
 
   auto unit_range = [&](int u, int& tm, int64_t& kt0, int64_t& kt1) {
     tm = u % p.tiles_m;
@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(skinny::kThreads, 1) spmm_skinny_kernel(const 
     tc_fence_after();
     tmem_dealloc(tmem_base, kCols);
   }
+  pdl_leave(p.early);
 }
 
 // Y[r][t] = sum over K ranges s (in order) of ws[s][r][t], t < T.  Launched as
