@@ -37,13 +37,17 @@ namespace nmk {
 namespace lora {
 constexpr int kThreads = 256;
 constexpr int kDepth = 128;      // reduction steps of a shrink stage
-constexpr int kRankBlock = 32;   // rank rows of a shrink work item
 constexpr int kMaxStages = 6;
 constexpr uint32_t kZBytes = kDepth * kTok * 2;
-constexpr uint32_t kMBytes = kRankBlock * kDepth * 2;
-constexpr uint32_t kShrinkPart = 2 * kTok * (kRankBlock + 1) * 4;  // the wider of the two layouts of the joined sums
-__host__ __device__ constexpr uint32_t shrink_smem(int stages) { return (uint32_t)stages * (kZBytes + kMBytes) + 1024; }
-static_assert(kShrinkPart <= kZBytes + kMBytes, "the joined sums reuse the first stage");
+// A shrink work item takes 32 rank rows, or 64 of a rank above 32 (one reading of Z for them instead of two).
+__host__ __device__ constexpr int rank_block(int rank) { return rank > 32 ? 64 : 32; }
+__host__ __device__ constexpr uint32_t m_bytes(int rb) { return (uint32_t)(rb * kDepth * 2); }
+__host__ __device__ constexpr uint32_t sum_words(int rb) { return (uint32_t)(kTok * (rb + 1) + rb); }  // either layout
+__host__ __device__ constexpr uint32_t shrink_smem(int stages, int rb) {
+  return (uint32_t)stages * (kZBytes + m_bytes(rb)) + 1024;
+}
+static_assert(sum_words(32) * 4 <= kZBytes + m_bytes(32) && sum_words(64) * 4 <= kZBytes + m_bytes(64),
+              "the sums reuse the first stage");
 constexpr int kRows = 128;       // rows of an expand or outer tile
 constexpr uint32_t kExpandBatch = 96 * 1024;  // bytes of adapters' tiles in flight
 constexpr int kOuterRank = 64;   // rank columns of an outer work item
@@ -148,9 +152,12 @@ __device__ __forceinline__ void split_terms(float v, uint16_t (&term)[P]) {
 }
 }  // namespace lora
 
-template <bool TRANS, int OUT, int P>
-__global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __grid_constant__ LoraShrink p) {
+template <bool TRANS, int OUT, int P, int RB>
+__global__ void __launch_bounds__(lora::kThreads, RB == 32 ? 3 : 2) lora_shrink_kernel(const __grid_constant__ LoraShrink p) {
   using namespace lora;
+  constexpr int kRankBlock = RB;
+  constexpr int kMT = RB / 16;
+  constexpr uint32_t kMBytes = m_bytes(RB);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ int32_t s_id[kTok], s_list[kTok];
@@ -212,9 +219,9 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
             stage16(m + (c >> 3) * (kMBytes / 2) + j * 128 + (((c & 7) ^ (j & 7)) << 4),
                     p.M + ((int64_t)a * p.rank + j0 + j) * p.D + d0 + 8 * c, valid, 0);
           } else {
-            const int row = u >> 2, c = u & 3;
+            const int row = u / (RB / 8), c = u % (RB / 8);
             const int64_t valid = d0 + row < p.D ? p.rank - (j0 + 8 * c) : 0;
-            stage16(m + row * 64 + ((c ^ ((row >> 1) & 3)) << 4),
+            stage16(RB == 32 ? m + row * 64 + ((c ^ ((row >> 1) & 3)) << 4) : m + row * 128 + ((c ^ (row & 7)) << 4),
                     p.M + ((int64_t)a * p.D + d0 + row) * p.rank + j0 + 8 * c, valid, 0);
           }
         }
@@ -225,7 +232,7 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
       const unsigned lo = __ballot_sync(0xFFFFFFFFu, s_id[lane] == a), hi = __ballot_sync(0xFFFFFFFFu, s_id[32 + lane] == a);
       serves = ((group & 2 ? hi : lo) >> (16 * (group & 1))) & 0xFFFFu;
     }
-    float sum[2][2][4] = {};
+    float sum[kMT][2][4] = {};
     for (int i = 0; i < stages - 1 && i < mine; ++i) load(i);
     for (int i = 0; i < mine; ++i) {
       mbar_wait(&s_full[slot], phase, &s_abort, p.status, kWaitNs);
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
         phase ^= 1u;
       }
       if (!serves) continue;
-      float acc[2][2][4] = {};
+      float acc[kMT][2][4] = {};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int ks = 4 * half + q, mi = lane >> 3, l8 = lane & 7;
@@ -245,74 +252,64 @@ __global__ void __launch_bounds__(lora::kThreads) lora_shrink_kernel(const __gri
         const int zr = 16 * ks + 8 * (mi & 1) + l8;
         ldmatrix_x4_trans(b, z + zr * 128 + (((2 * group + (mi >> 1)) ^ (zr & 7)) << 4));
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < kMT; ++mt) {
           if (16 * mt >= live) continue;
           if (!TRANS) {
             const int j = 16 * mt + 8 * (mi & 1) + l8;
             ldmatrix_x4(w, m + half * (kMBytes / 2) + j * 128 + (((2 * q + (mi >> 1)) ^ (j & 7)) << 4));
           } else {
             const int row = 16 * ks + 8 * (mi >> 1) + l8;
-            ldmatrix_x4_trans(w, m + row * 64 + (((2 * mt + (mi & 1)) ^ ((row >> 1) & 3)) << 4));
+            ldmatrix_x4_trans(w, RB == 32 ? m + row * 64 + (((2 * mt + (mi & 1)) ^ ((row >> 1) & 3)) << 4)
+                                           : m + row * 128 + (((2 * mt + (mi & 1)) ^ (row & 7)) << 4));
           }
           mma_bf16(acc[mt][0], w, b[0], b[1]);
           mma_bf16(acc[mt][1], w, b[2], b[3]);
         }
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sum[e >> 3][(e >> 2) & 1][e & 3] += acc[e >> 3][(e >> 2) & 1][e & 3];
+      for (int e = 0; e < 8 * kMT; ++e) sum[e >> 3][(e >> 2) & 1][e & 3] += acc[e >> 3][(e >> 2) & 1][e & 3];
     }
     __syncthreads();  // every warp is done with the stages
-    // The sums of both K halves, in the order of the output (ranks of a token, or tokens of a rank row, side by side):
-    // lanes that read another CTA's shared memory at neighbouring addresses share a transfer (reading it across rows
-    // took 14 us of a 25 us item).
+    // The sums, in the order of the output (ranks of a token, or tokens of a rank row, side by side): lanes that read
+    // another CTA's shared memory at neighbouring addresses share a transfer (reading it across rows took 14 us of a
+    // 25 us item).  The second K half's warps leave theirs, the first half's add them to their own.
     auto part_at = [](int j, int t) { return OUT == SHRINK_BLOCKS ? j * (kTok + 1) + t : t * (kRankBlock + 1) + j; };
-    constexpr int kHalf = kShrinkPart / 8;
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int h = 1; h >= 0; --h) {
+      if (half == h) {
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 16 * mt + (lane >> 2) + 8 * (e >> 1), t = 16 * group + 8 * nb + 2 * (lane & 3) + (e & 1);
-          s_part[half * kHalf + part_at(j, t)] = sum[mt][nb][e];
+        for (int e = 0; e < 8 * kMT; ++e) {
+          const int mt = e >> 3, nb = (e >> 2) & 1, f = e & 3;
+          const int at = part_at(16 * mt + (lane >> 2) + 8 * (f >> 1), 16 * group + 8 * nb + 2 * (lane & 3) + (f & 1));
+          s_part[at] = h == 1 ? sum[mt][nb][f] : sum[mt][nb][f] + s_part[at];
         }
-    __syncthreads();
-    if (C > 1) cluster_sync();  // every CTA's sums are written
-    constexpr int kOwn = kRankBlock * kTok / kThreads;  // outputs of a thread when it is alone
-    float v[kOwn];
-#pragma unroll
-    for (int o = 0; o < kOwn; ++o) {
-      const int e = tid + kThreads * ((int)rank + o * C);
-      v[o] = 0.f;
-      if (e >= kRankBlock * kTok) continue;
-      const int j = OUT == SHRINK_BLOCKS ? e / kTok : e % kRankBlock, t = OUT == SHRINK_BLOCKS ? e % kTok : e / kRankBlock;
-      const uint32_t mine_at = smem_u32(s_part + part_at(j, t));
-      float part[8][2];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        if (c >= C) continue;
-        const uint32_t there = map_to_cta(mine_at, c);
-        part[c][0] = ld_cluster_f32(there);
-        part[c][1] = ld_cluster_f32(there + kHalf * 4);
       }
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (c < C) v[o] += part[c][0] + part[c][1];
+      __syncthreads();
     }
-    if (C > 1) cluster_arrive();  // done with the other CTAs' sums; the stores below need not be waited for
+    if (C > 1) cluster_sync();  // every CTA's sums are written
+    // Output e belongs to one CTA of the cluster: nobody else reads its place in that CTA's own sums, so the joined
+    // value goes back there and leaves after the others have been told that their sums are done with.
+    for (int e = tid + kThreads * (int)rank; C > 1 && e < kRankBlock * kTok; e += kThreads * C) {
+      const int j = OUT == SHRINK_BLOCKS ? e / kTok : e % kRankBlock, t = OUT == SHRINK_BLOCKS ? e % kTok : e / kRankBlock;
+      float* place = s_part + part_at(j, t);
+      const uint32_t mine_at = smem_u32(place);
+      float part[8];
 #pragma unroll
-    for (int o = 0; o < kOwn; ++o) {
-      const int e = tid + kThreads * ((int)rank + o * C);
-      if (e >= kRankBlock * kTok) continue;
+      for (int c = 0; c < 8; ++c) part[c] = c < C ? ld_cluster_f32(map_to_cta(mine_at, c)) : 0.f;
+      *place = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
+    }
+    if (C > 1) cluster_arrive();  // the stores below need not be waited for
+    for (int e = tid + kThreads * (int)rank; e < kRankBlock * kTok; e += kThreads * C) {
       const int j = OUT == SHRINK_BLOCKS ? e / kTok : e % kRankBlock, t = OUT == SHRINK_BLOCKS ? e % kTok : e / kRankBlock;
       const bool own = s_id[t] == a;
       if (OUT == SHRINK_BLOCKS ? (j >= live || t0 + t >= p.ldp) : (!own || j0 + j >= rs)) continue;
+      float v = s_part[part_at(j, t)];
       if (OUT == SHRINK_F32) {
-        p.S[(t0 + t) * rs + j0 + j] = v[o];
+        p.S[(t0 + t) * rs + j0 + j] = v;
       } else {
-        if (OUT == SHRINK_BLOCKS && p.scale) v[o] *= __ldg(p.scale + a);
+        if (OUT == SHRINK_BLOCKS && p.scale) v *= __ldg(p.scale + a);
         uint16_t term[P];
-        split_terms<P>(v[o], term);
+        split_terms<P>(v, term);
 #pragma unroll
         for (int q = 0; q < P; ++q) {
           if (OUT == SHRINK_TERMS)
@@ -878,16 +875,17 @@ static cudaError_t launch_clustered(Kern kernel, dim3 grid, int cluster, uint32_
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <bool TRANS>
+template <bool TRANS, int RB>
 static cudaError_t launch_shrink_out(const LoraShrink& p, dim3 grid, cudaStream_t s) {
   using namespace lora;
-  const uint32_t b = shrink_smem(p.stages), most = shrink_smem(kMaxStages);
-  if (p.out == SHRINK_F32) return launch_clustered(lora_shrink_kernel<TRANS, SHRINK_F32, 1>, grid, p.cluster, b, most, p, s);
+  const uint32_t b = shrink_smem(p.stages, RB), most = shrink_smem(kMaxStages, RB);
+  const int c = p.cluster;
+  if (p.out == SHRINK_F32) return launch_clustered(lora_shrink_kernel<TRANS, SHRINK_F32, 1, RB>, grid, c, b, most, p, s);
   if (p.out == SHRINK_TERMS)
-    return p.planes == 3 ? launch_clustered(lora_shrink_kernel<TRANS, SHRINK_TERMS, 3>, grid, p.cluster, b, most, p, s)
-                         : launch_clustered(lora_shrink_kernel<TRANS, SHRINK_TERMS, 2>, grid, p.cluster, b, most, p, s);
-  return p.planes == 3 ? launch_clustered(lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 3>, grid, p.cluster, b, most, p, s)
-                       : launch_clustered(lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 2>, grid, p.cluster, b, most, p, s);
+    return p.planes == 3 ? launch_clustered(lora_shrink_kernel<TRANS, SHRINK_TERMS, 3, RB>, grid, c, b, most, p, s)
+                         : launch_clustered(lora_shrink_kernel<TRANS, SHRINK_TERMS, 2, RB>, grid, c, b, most, p, s);
+  return p.planes == 3 ? launch_clustered(lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 3, RB>, grid, c, b, most, p, s)
+                       : launch_clustered(lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 2, RB>, grid, c, b, most, p, s);
 }
 
 cudaError_t launch_lora_shrink(LoraShrink& p, bool trans, cudaStream_t s) {
@@ -898,16 +896,18 @@ cudaError_t launch_lora_shrink(LoraShrink& p, bool trans, cudaStream_t s) {
   p.cluster = 1;
   while (p.cluster < 8 && tiles * p.cluster < target && chunks / (2 * p.cluster) >= 2) p.cluster <<= 1;
   // ... and further CTAs take the tile's adapters side by side when the tiles are few
-  const int64_t items = (p.n < kTok ? p.n : kTok) * ((p.rank + kRankBlock - 1) / kRankBlock);
-  const int64_t rblocks = (p.rank + kRankBlock - 1) / kRankBlock;
+  const int64_t rblocks = (p.rank + rank_block(p.rank) - 1) / rank_block(p.rank);
+  const int64_t items = (p.n < kTok ? p.n : kTok) * rblocks;
   int64_t y = (target + tiles * p.cluster - 1) / (tiles * p.cluster);
   if (y < rblocks) y = rblocks;
   if (y > items) y = items;
   if (tiles * p.cluster >= (1ll << 31)) return cudaErrorInvalidValue;
-  // Three CTAs to an SM in a full grid (three stages); with an SM to itself a CTA has all its chunks in flight.
+  // Two or three CTAs to an SM in a full grid (three stages); with an SM to itself a CTA has all its chunks in flight.
   p.stages = tiles * p.cluster * y <= sm_count_current() ? kMaxStages : 3;
   const dim3 grid((unsigned)(tiles * p.cluster), (unsigned)y);
-  return trans ? launch_shrink_out<true>(p, grid, s) : launch_shrink_out<false>(p, grid, s);
+  if (rank_block(p.rank) == 64)
+    return trans ? launch_shrink_out<true, 64>(p, grid, s) : launch_shrink_out<false, 64>(p, grid, s);
+  return trans ? launch_shrink_out<true, 32>(p, grid, s) : launch_shrink_out<false, 32>(p, grid, s);
 }
 
 cudaError_t launch_lora_expand(LoraExpand& p, bool trans, cudaStream_t s) {
@@ -964,7 +964,7 @@ cudaError_t launch_lora_outer(LoraOuter& p, bool by_rank, cudaStream_t s) {
   if (items > 65535) return cudaErrorInvalidValue;
   // CTAs that share an adapter's tokens, until the grid fills the SMs
   p.cluster = 1;
-  while (p.cluster < 8 && blocks * items * p.cluster < 2 * (int64_t)sm_count_current() && tiles / (2 * p.cluster) >= 2)
+  while (p.cluster < 8 && blocks * items * p.cluster < 3 * (int64_t)sm_count_current() && tiles / (2 * p.cluster) >= 2)
     p.cluster <<= 1;
   if (blocks * p.cluster >= (1ll << 31)) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(blocks * p.cluster), (unsigned)items);
@@ -1027,9 +1027,10 @@ nm_status shrink(const Adapters& ad, bool trans, int64_t D, const uint16_t* Z, i
   nm_status st = NM_OK;
   if (D > 0) st = make_tmap(&p.tm_z, Z, (uint64_t)T, (uint64_t)D, (uint64_t)ldz * 2, kTok, kDepth, 128, "tokens");
   if (st == NM_OK && p.vec) {
+    const int rb = rank_block(ad.rank);
     const uint64_t inner = trans ? (uint64_t)ad.rank : (uint64_t)D, rows = trans ? (uint64_t)D : (uint64_t)ad.rank;
-    st = make_tmap3(&p.tm_m, p.M, inner, rows, (uint64_t)ad.n, inner * 2, inner * rows * 2, trans ? kRankBlock : 64,
-                    trans ? kDepth : kRankBlock, trans ? 64 : 128, "adapters");
+    st = make_tmap3(&p.tm_m, p.M, inner, rows, (uint64_t)ad.n, inner * 2, inner * rows * 2, trans ? (uint32_t)rb : 64u,
+                    trans ? (uint32_t)kDepth : (uint32_t)rb, trans && rb == 32 ? 64 : 128, "adapters");
   }
   if (st != NM_OK) return st;
   cudaError_t e = launch_lora_shrink(p, trans, s);
