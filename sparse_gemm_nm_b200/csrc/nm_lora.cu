@@ -53,12 +53,14 @@ constexpr uint32_t kExpandBatch = 96 * 1024;  // bytes of adapters' tiles in fli
 constexpr int kOuterRank = 64;   // rank columns of an outer work item
 constexpr uint32_t kOuterM = kRows * kTok * 2;
 constexpr uint32_t kOuterV = kTok * kOuterRank * 2;  // one bf16 term
-// Two CTAs to an SM: their warps cover for one another's MMA latency (one CTA left the issue slots 59 % idle).
-__host__ __device__ constexpr int outer_stages(int planes) { return planes == 3 ? 2 : 3; }
+// Two CTAs to an SM: their warps cover for one another's MMA latency (one CTA left the issue slots 59 % idle).  Z comes
+// from HBM and has a ring of three stages; three terms leave room for two stages of V, which the L2 holds.
+constexpr int kOuterZ = 3;
+__host__ __device__ constexpr int outer_v(int planes) { return planes == 3 ? 2 : 3; }
 __host__ __device__ constexpr uint32_t outer_smem(int planes) {
-  return outer_stages(planes) * (kOuterM + (uint32_t)planes * kOuterV) + 1024;
+  return kOuterZ * kOuterM + (uint32_t)(outer_v(planes) * planes) * kOuterV + 1024;
 }
-static_assert(kRows * (kOuterRank + 1) * 4 <= 2 * (kOuterM + 2 * kOuterV), "the joined sums reuse the stages");
+static_assert(kRows * (kOuterRank + 1) * 4 <= kOuterZ * kOuterM, "the joined sums reuse the stages");
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
@@ -374,13 +376,60 @@ __global__ void __launch_bounds__(lora::kThreads) lora_expand_kernel(const LoraE
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t r0 = (int64_t)blockIdx.x * kRows, t0 = (int64_t)blockIdx.y * kTok;
 
-  // The base first: it needs nothing else, and its loads are in flight behind the rest.  Several K ranges' sums are
-  // added on the way into shared memory, four ranges in flight for every 16 bytes.
-  float acc[8][4];
   const int tokens = p.T - t0 < kTok ? (int)(p.T - t0) : kTok;
+  const int distinct = tile_adapters(p.adapter, p.n, t0, p.T, s_id, s_list, &s_count);
+
+  const int unit_bits = rs <= 16 ? 1 : rs <= 32 ? 2 : rs <= 64 ? 3 : 4;  // 16-byte units of a row, to a power of two
+  auto load = [&](int i, int at) {
+    uint8_t* m = s_m + at * m_bytes;
+    const int64_t a = s_list[i];
+    if (!TRANS) {
+      for (int u = tid; u < kRows << unit_bits; u += kThreads) {
+        const int row = u >> unit_bits, c = u & ((1 << unit_bits) - 1);
+        if (8 * c >= rs) continue;
+        const int64_t valid = r0 + row < p.rows ? p.rank - 8 * c : 0;
+        stage16(m + row * pitch + c * 16, valid > 0 ? p.M + (a * p.rows + r0 + row) * p.rank + 8 * c : p.M, valid, p.vec);
+      }
+    } else {
+      for (int u = tid; u < rs * 16; u += kThreads) {
+        const int j = u >> 4, c = u & 15;
+        const int64_t valid = j < p.rank ? p.rows - (r0 + 8 * c) : 0;
+        stage16(m + j * 256 + ((c ^ (j & 7)) << 4), valid > 0 ? p.M + (a * p.rank + j) * p.rows + r0 + 8 * c : p.M, valid,
+                p.vec);
+      }
+    }
+  };
+  for (int i = 0; i < p.batch && i < distinct; ++i) load(i, i);
+  cp_commit();
+  // s_a S of the tile's tokens as P bf16 terms (0 for a token without an adapter, whose S is not written)
+  for (int u = tid; u < tokens * (rs / 4); u += kThreads) {
+    const int t = u / (rs / 4), j = 4 * (u - t * (rs / 4));
+    const int32_t id = s_id[t];
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (id >= 0) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(p.S + (t0 + t) * rs + j));
+      const float sc = p.scale ? __ldg(p.scale + id) : 1.f;
+      v[0] = x.x * sc;
+      v[1] = x.y * sc;
+      v[2] = x.z * sc;
+      v[3] = x.w * sc;
+    }
+    uint16_t term[4][P];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_terms<P>(v[e], term[e]);
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+      *reinterpret_cast<uint2*>(s_s + ((uint32_t)q * kTok + t) * pitch + 2 * j) =
+          make_uint2((uint32_t)term[0][q] | (uint32_t)term[1][q] << 16, (uint32_t)term[2][q] | (uint32_t)term[3][q] << 16);
+  }
+
+  // The base, while the adapters' tiles are on their way.  Several K ranges' sums are added on the way into shared
+  // memory, four ranges in flight for every 16 bytes.
+  float acc[8][4];
   if (p.splits > 1) {
     float* s_base = reinterpret_cast<float*>(smem + p.base_off);
     const int quads = (int)p.ldb / 4;  // rows of a K range's sums: 16, 32 or 64 columns (one tile of tokens)
+#pragma unroll 2
     for (int u = tid; u < kRows * quads; u += kThreads) {
       const int row = u / quads, c = u - row * quads;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -431,58 +480,14 @@ __global__ void __launch_bounds__(lora::kThreads) lora_expand_kernel(const LoraE
       acc[nb][2 * h + 1] = v.y;
     }
   }
-  const int distinct = tile_adapters(p.adapter, p.n, t0, p.T, s_id, s_list, &s_count);
-
-  auto load = [&](int i, int at) {
-    uint8_t* m = s_m + at * m_bytes;
-    const int64_t a = s_list[i];
-    if (!TRANS) {
-      const int units = rs / 8;
-      for (int u = tid; u < kRows * units; u += kThreads) {
-        const int row = u / units, c = u - row * units;
-        const int64_t valid = r0 + row < p.rows ? p.rank - 8 * c : 0;
-        stage16(m + row * pitch + c * 16, valid > 0 ? p.M + (a * p.rows + r0 + row) * p.rank + 8 * c : p.M, valid, p.vec);
-      }
-    } else {
-      for (int u = tid; u < rs * 16; u += kThreads) {
-        const int j = u >> 4, c = u & 15;
-        const int64_t valid = j < p.rank ? p.rows - (r0 + 8 * c) : 0;
-        stage16(m + j * 256 + ((c ^ (j & 7)) << 4), valid > 0 ? p.M + (a * p.rank + j) * p.rows + r0 + 8 * c : p.M, valid,
-                p.vec);
-      }
-    }
-  };
-  for (int i = 0; i < p.batch && i < distinct; ++i) load(i, i);
-  // s_a S of the tile's tokens as P bf16 terms (0 for a token without an adapter, whose S is not written)
-  for (int u = tid; u < tokens * (rs / 4); u += kThreads) {
-    const int t = u / (rs / 4), j = 4 * (u - t * (rs / 4));
-    const int32_t id = s_id[t];
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (id >= 0) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(p.S + (t0 + t) * rs + j));
-      const float sc = p.scale ? __ldg(p.scale + id) : 1.f;
-      v[0] = x.x * sc;
-      v[1] = x.y * sc;
-      v[2] = x.z * sc;
-      v[3] = x.w * sc;
-    }
-    uint16_t term[4][P];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) split_terms<P>(v[e], term[e]);
-#pragma unroll
-    for (int q = 0; q < P; ++q)
-      *reinterpret_cast<uint2*>(s_s + ((uint32_t)q * kTok + t) * pitch + 2 * j) =
-          make_uint2((uint32_t)term[0][q] | (uint32_t)term[1][q] << 16, (uint32_t)term[2][q] | (uint32_t)term[3][q] << 16);
-  }
-
   for (int i = 0, at = 0; i < distinct; ++i, ++at) {
     if (at == p.batch) {  // the next batch of adapters' tiles, all in flight together
       __syncthreads();
       at = 0;
       for (int u = 0; u < p.batch && i + u < distinct; ++u) load(i + u, u);
+      cp_commit();
     }
     if (at == 0) {
-      cp_commit();
       cp_wait<0>();
       __syncthreads();  // the batch has landed (and S, at first)
     }
@@ -675,14 +680,16 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
   using namespace lora;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int kOuterStages = outer_stages(P);
-  constexpr uint32_t kStage = kOuterM + P * kOuterV;  // Z tile, then P terms of [64 tokens][up to 64 ranks]
-  __shared__ int32_t s_id[kOuterStages][kTok];
-  __shared__ uint64_t s_full[kOuterStages];
+  constexpr int kV = outer_v(P);                  // stages of V: P terms of [64 tokens][up to 64 ranks]
+  constexpr uint32_t kVStage = P * kOuterV;
+  uint8_t* s_v = smem + kOuterZ * kOuterM;
+  __shared__ int32_t s_id[kOuterZ][kTok];
+  __shared__ uint64_t s_fz[kOuterZ], s_fv[kV];
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    for (int i = 0; i < kOuterStages; ++i) mbar_init(&s_full[i], 1);
+    for (int i = 0; i < kOuterZ; ++i) mbar_init(&s_fz[i], 1);
+    for (int i = 0; i < kV; ++i) mbar_init(&s_fv[i], 1);
     s_abort = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -701,30 +708,47 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
   const int cols = rs - j0 < kOuterRank ? rs - j0 : kOuterRank;  // of which this item has (a multiple of 16)
   const int32_t* list = p.tiles + (int64_t)a * ((p.T + kTok - 1) / kTok);
   const int count = __ldcg(p.counts + a);
+  int32_t first[kOuterZ];  // read beside the count (places past it hold no tile and are not used)
+#pragma unroll
+  for (int d = 0; d < kOuterZ; ++d) {
+    const int64_t at = rank + (int64_t)d * C;
+    first[d] = at < (p.T + kTok - 1) / kTok ? __ldcg(list + at) : 0;
+  }
   const int mine = count > (int)rank ? (count - (int)rank + C - 1) / C : 0;  // tiles rank, rank + C, ... of the list
   __syncthreads();
 
-  // Ring slot i % kOuterStages: the tile's boxes by one thread, its tokens' adapters by 64 others.  `tile` comes from
-  // the list one turn earlier, so that no load waits for the list.
-  auto load = [&](int i, int32_t tile) {
-    const int slot = i % kOuterStages;
+  // Tile i of this CTA: Z and its tokens' adapters into ring slot i % kOuterZ, V into slot i % kV.  The tile numbers come
+  // from the list two turns earlier, so that no load waits for the list.
+  auto load_z = [&](int i, int32_t tile) {
+    const int slot = i % kOuterZ;
     const int64_t t0 = (int64_t)tile * kTok;
     if (tid == 0) {
-      mbar_arrive_expect_tx(&s_full[slot], kOuterM + (uint32_t)(P * kTok * box * 2));
-      uint8_t* m = smem + slot * kStage;
-      tma_load_2d(m, &p.tm_z, &s_full[slot], (int32_t)t0, (int32_t)r0);
-#pragma unroll
-      for (int q = 0; q < P; ++q) tma_load_3d(m + kOuterM + q * kOuterV, &p.tm_v, &s_full[slot], j0, (int32_t)t0, q);
+      mbar_arrive_expect_tx(&s_fz[slot], kOuterM);
+      tma_load_2d(smem + slot * kOuterM, &p.tm_z, &s_fz[slot], (int32_t)t0, (int32_t)r0);
     } else if (tid >= 64 && tid < 64 + kTok) {
       const int t = tid - 64;
       s_id[slot][t] = t0 + t < p.T ? __ldg(p.adapter + t0 + t) : -1;
     }
   };
-  auto tile_at = [&](int i) { return i < mine ? __ldcg(list + rank + (int64_t)i * C) : 0; };
+  auto load_v = [&](int i, int32_t tile) {
+    if (tid != 32) return;
+    const int slot = i % kV;
+    mbar_arrive_expect_tx(&s_fv[slot], (uint32_t)(P * kTok * box * 2));
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+      tma_load_3d(s_v + slot * kVStage + q * kOuterV, &p.tm_v, &s_fv[slot], j0, tile * kTok, q);
+  };
   float sum[8][4] = {};
-  for (int i = 0; i < kOuterStages - 1; ++i)
-    if (i < mine) load(i, tile_at(i));
-  int32_t next = tile_at(kOuterStages - 1);
+  // next[d]: the tile that is d turns ahead
+  int32_t next[kOuterZ];
+#pragma unroll
+  for (int d = 0; d < kOuterZ; ++d) next[d] = d < mine ? first[d] : 0;
+#pragma unroll
+  for (int d = 0; d < kOuterZ - 1; ++d)
+    if (d < mine) load_z(d, next[d]);
+#pragma unroll
+  for (int d = 0; d < kV - 1; ++d)
+    if (d < mine) load_v(d, next[d]);
   // Addresses within a stage.  The swizzles XOR row bits that a step of 16 rows leaves alone, so a lane's offsets are
   // the same in every step: Z in units of the K step, the terms' four 16-rank blocks (rows of 32, 64 or 128 bytes
   // swizzled within themselves, rows of 96 bytes not).
@@ -737,11 +761,11 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
   for (int b = 0; b < 4; ++b) {
     const uint32_t unit = (uint32_t)(2 * b + (mi >> 1));
     const uint32_t sw = box == 64 ? (uint32_t)l8 : box == 32 ? (uint32_t)(l8 >> 1) & 3u : box == 16 ? (uint32_t)(l8 >> 2) : 0u;
-    v_off[b] = kOuterM + (uint32_t)(8 * (mi & 1) + l8) * (uint32_t)box * 2u + ((unit ^ sw) << 4);
+    v_off[b] = (uint32_t)(8 * (mi & 1) + l8) * (uint32_t)box * 2u + ((unit ^ sw) << 4);
   }
   // One tile's products.  MASKED: some of its tokens are not the adapter's and leave both operands: their Inf or NaN in
   // one would survive a 0 in the other, and S of a token without an adapter is not written at all.
-  auto products = [&](uint32_t m, unsigned lo, unsigned hi, float (&acc)[8][4], auto masked) {
+  auto products = [&](uint32_t m, uint32_t v, unsigned lo, unsigned hi, float (&acc)[8][4], auto masked) {
     constexpr bool MASKED = decltype(masked)::value;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
@@ -764,7 +788,7 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
 #pragma unroll
         for (int q = 0; q < P; ++q) {
           uint32_t f[4];
-          ldmatrix_x4_trans(f, m + q * kOuterV + ks * v_step + v_off[b]);
+          ldmatrix_x4_trans(f, v + q * kOuterV + ks * v_step + v_off[b]);
           if (MASKED) {
             f[0] &= keep[0];
             f[1] &= keep[1];
@@ -778,19 +802,23 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
     }
   };
   for (int i = 0; i < mine; ++i) {
-    const int slot = i % kOuterStages;
-    mbar_wait(&s_full[slot], (uint32_t)(i / kOuterStages) & 1u, &s_abort, p.status, kWaitNs);
-    __syncthreads();  // the ids are there, and the slot of tile i - 1 is free
-    if (i + kOuterStages - 1 < mine) load(i + kOuterStages - 1, next);
-    next = tile_at(i + kOuterStages);
-    const uint32_t m = smem_u32(smem + slot * kStage);
+    const int slot = i % kOuterZ;
+    mbar_wait(&s_fz[slot], (uint32_t)(i / kOuterZ) & 1u, &s_abort, p.status, kWaitNs);
+    mbar_wait(&s_fv[i % kV], (uint32_t)(i / kV) & 1u, &s_abort, p.status, kWaitNs);
+    __syncthreads();  // the ids are there, and the slots of tile i - 1 are free
+    if (i + kOuterZ - 1 < mine) load_z(i + kOuterZ - 1, next[kOuterZ - 1]);
+    if (i + kV - 1 < mine) load_v(i + kV - 1, next[kV - 1]);
+#pragma unroll
+    for (int d = 0; d + 1 < kOuterZ; ++d) next[d] = next[d + 1];
+    next[kOuterZ - 1] = i + kOuterZ < mine ? __ldcg(list + rank + (int64_t)(i + kOuterZ) * C) : 0;
+    const uint32_t m = smem_u32(smem + slot * kOuterM), v = smem_u32(s_v + (i % kV) * kVStage);
     const unsigned lo = __ballot_sync(0xFFFFFFFFu, s_id[slot][lane] == a);
     const unsigned hi = __ballot_sync(0xFFFFFFFFu, s_id[slot][32 + lane] == a);
     float acc[8][4] = {};
     if ((lo & hi) == 0xFFFFFFFFu)
-      products(m, lo, hi, acc, std::false_type());
+      products(m, v, lo, hi, acc, std::false_type());
     else
-      products(m, lo, hi, acc, std::true_type());
+      products(m, v, lo, hi, acc, std::true_type());
 #pragma unroll
     for (int e = 0; e < 32; ++e) sum[e >> 2][e & 3] += acc[e >> 2][e & 3];
   }
