@@ -60,7 +60,8 @@ __host__ __device__ constexpr int outer_v(int planes) { return planes == 3 ? 2 :
 __host__ __device__ constexpr uint32_t outer_smem(int planes) {
   return kOuterZ * kOuterM + (uint32_t)(outer_v(planes) * planes) * kOuterV + 1024;
 }
-static_assert(kRows * (kOuterRank + 1) * 4 <= kOuterZ * kOuterM, "the joined sums reuse the stages");
+constexpr int kOuterPitch = kOuterRank + 4;  // floats of a row of joined sums
+static_assert(kRows * kOuterPitch * 4 <= kOuterZ * kOuterM, "the joined sums reuse the stages");
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
@@ -89,6 +90,14 @@ __device__ __forceinline__ void cp_wait() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -823,43 +832,77 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
     for (int e = 0; e < 32; ++e) sum[e >> 2][e & 3] += acc[e >> 2][e & 3];
   }
   __syncthreads();
-  float* s_sum = reinterpret_cast<float*>(smem);  // [128 rows][65], over the stages
+  float* s_sum = reinterpret_cast<float*>(smem);  // [128 rows][kOuterPitch], over the stages
 #pragma unroll
   for (int nb = 0; nb < 8; ++nb)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      s_sum[(16 * warp + (lane >> 2) + 8 * (e >> 1)) * (kOuterRank + 1) + 8 * nb + 2 * (lane & 3) + (e & 1)] = sum[nb][e];
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<float2*>(s_sum + (16 * warp + (lane >> 2) + 8 * h) * kOuterPitch + 8 * nb + 2 * (lane & 3)) =
+          make_float2(sum[nb][2 * h], sum[nb][2 * h + 1]);
   __syncthreads();
   if (C > 1) cluster_sync();
   const float scale = p.scale ? __ldg(p.scale + a) : 1.f;
   const int part = kRows / C;  // rows that this CTA joins and stores
   const int live = p.rank - j0 < kOuterRank ? p.rank - j0 : kOuterRank;
-  // Neighbouring lanes take neighbouring ranks of a row, for the reads across the cluster; this CTA's rows of its own
-  // sums are read by nobody else, so the joined values go back there and leave in the order of the output.
-  float* own = s_sum + (int)rank * part * (kOuterRank + 1);
-  for (int e = tid; e < part * kOuterRank; e += kThreads) {
-    const int at = (e / kOuterRank) * (kOuterRank + 1) + e % kOuterRank;
-    float got[8], v = 0.f;
+  // Four neighbouring ranks of a row at a time.  Rank-contiguous outputs leave from here.  For row-contiguous ones the
+  // joined values go back to this CTA's own sums (whose rows nobody else reads) and leave row by row.
+  float* own = s_sum + (int)rank * part * kOuterPitch;
+  const int64_t out0 = (int64_t)a * p.rows * p.rank;
+  const bool vec = !BY_RANK && p.out_f32 && p.rank % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0;
+#pragma unroll 2
+  for (int e = tid; e < part * (kOuterRank / 4); e += kThreads) {
+    const int row = e / (kOuterRank / 4), j = 4 * (e % (kOuterRank / 4));
+    float* place = own + row * kOuterPitch + j;
+    const uint32_t at = smem_u32(place);
+    float4 got[8], v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-      if (c < C) got[c] = ld_cluster_f32(map_to_cta(smem_u32(own + at), c));
+      if (c < C) got[c] = ld_cluster_f32x4(map_to_cta(at, c));
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      if (c < C) v += got[c];
-    own[at] = v * scale;
+    for (int c = 0; c < 8; ++c) {
+      if (c >= C) continue;
+      v.x += got[c].x;
+      v.y += got[c].y;
+      v.z += got[c].z;
+      v.w += got[c].w;
+    }
+    v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+    const int64_t r = r0 + (int)rank * part + row;
+    if (BY_RANK) {
+      *reinterpret_cast<float4*>(place) = v;
+    } else if (r < p.rows && j < live) {
+      const int64_t to = out0 + r * p.rank + j0 + j;
+      if (vec) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = v;
+      } else {
+        const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (j + u >= live) continue;
+          if (p.out_f32)
+            static_cast<float*>(p.out)[to + u] = f[u];
+          else
+            static_cast<uint16_t*>(p.out)[to + u] = (uint16_t)(pack_bf16x2(f[u], 0.f) & 0xFFFFu);
+        }
+      }
+    }
   }
   if (C > 1) cluster_arrive();  // done with the other CTAs' sums
-  __syncthreads();
-  for (int e = tid; e < part * live; e += kThreads) {
-    const int row = BY_RANK ? e % part : e / live, j = BY_RANK ? e / part : e % live;
-    const int64_t r = r0 + (int)rank * part + row;
-    if (r >= p.rows) continue;
-    const float v = own[row * (kOuterRank + 1) + j];
-    const int64_t at = BY_RANK ? ((int64_t)a * p.rank + j0 + j) * p.rows + r : ((int64_t)a * p.rows + r) * p.rank + j0 + j;
-    if (p.out_f32)
-      static_cast<float*>(p.out)[at] = v;
-    else
-      static_cast<uint16_t*>(p.out)[at] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
+  if (BY_RANK) {
+    __syncthreads();
+    const int bits = 31 - __clz(part);  // a power of two
+#pragma unroll 4
+    for (int e = tid; e < part * live; e += kThreads) {
+      const int row = e & (part - 1), j = e >> bits;
+      const int64_t r = r0 + (int)rank * part + row;
+      if (r >= p.rows) continue;
+      const float v = own[row * kOuterPitch + j];
+      const int64_t to = out0 + (int64_t)(j0 + j) * p.rows + r;
+      if (p.out_f32)
+        static_cast<float*>(p.out)[to] = v;
+      else
+        static_cast<uint16_t*>(p.out)[to] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
+    }
   }
   if (C > 1) cluster_wait();  // no CTA leaves while another still reads its sums
   pdl_leave(p.early != 0);
