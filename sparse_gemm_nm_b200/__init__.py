@@ -16,7 +16,6 @@ the same bits).  Matrices are row-major: W is R x K, X is K x T, Y is R x T.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -325,28 +324,43 @@ def _require_cuda(*ts):
 
 def _same_device(first, *others):
     """Every tensor is on first's CUDA device."""
-    _require_cuda(first, *others)
+    at = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != at:
+            _require_cuda(first, *others)
             raise ValueError(f"tensors must share one device, got {first.device} and {t.device}")
+    if at < 0:
+        _require_cuda(first)
 
 
-@contextlib.contextmanager
-def _on(X, stream):
+class _On:
     """X's device made current and, when given, `stream` too (outputs are then allocated in that stream's order);
-    yields the stream handle for the call."""
-    import torch
-    if stream is None:
-        at = X.device.index
-        if at == torch.cuda.current_device():
-            yield torch.cuda.current_stream(at).cuda_stream
-        else:
-            with torch.cuda.device(at):
-                yield torch.cuda.current_stream(at).cuda_stream
-        return
-    s = torch.cuda.ExternalStream(stream, device=X.device) if isinstance(stream, int) else stream
-    with torch.cuda.device(X.device), torch.cuda.stream(s):
-        yield s.cuda_stream
+    enters as the stream handle for the call."""
+    __slots__ = ("at", "stream", "held")
+
+    def __init__(self, X, stream):
+        self.at, self.stream, self.held = X.get_device(), stream, ()
+
+    def __enter__(self):
+        import torch
+        if self.stream is None:
+            if self.at != torch.cuda.current_device():
+                self._hold(torch.cuda.device(self.at))
+            return torch.cuda.current_stream(self.at).cuda_stream
+        s = self.stream
+        if isinstance(s, int):
+            s = torch.cuda.ExternalStream(s, device=self.at)
+        self._hold(torch.cuda.device(self.at))
+        self._hold(torch.cuda.stream(s))
+        return s.cuda_stream
+
+    def _hold(self, manager):
+        manager.__enter__()
+        self.held = (manager,) + self.held
+
+    def __exit__(self, *what):
+        for manager in self.held:
+            manager.__exit__(*what)
 
 
 def _rows(X, name: str, *dtypes):
@@ -354,29 +368,32 @@ def _rows(X, name: str, *dtypes):
     if X.dim() != 2 or X.dtype not in dtypes:
         raise ValueError(f"{name} must be a matrix of {' or '.join(str(d) for d in dtypes)}, got {X.dim()}-d {X.dtype}")
     rows, cols = X.shape
-    if cols > 1 and X.stride(1) != 1:
-        raise ValueError(f"{name}: the columns of a row must be adjacent (stride 1), got {X.stride(1)}")
-    return X.stride(0) if rows > 1 else (cols + 7) // 8 * 8
+    ld, step = X.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name}: the columns of a row must be adjacent (stride 1), got {step}")
+    return ld if rows > 1 else (cols + 7) // 8 * 8
 
 
 def _vector(v, name: str, size: int, dtype):
-    if v is not None and (tuple(v.shape) != (size,) or v.dtype != dtype or not v.is_contiguous()):
+    if v is not None and (v.shape != (size,) or v.dtype != dtype or not v.is_contiguous()):
         raise ValueError(f"{name} must be {size} contiguous values of {dtype}, got {tuple(v.shape)} {v.dtype}")
 
 
-def _out_rows(rows: int, cols: int, dtype, device):
-    """rows x cols with rows padded to 16 bytes: (the view, its row stride)."""
-    import torch
-    per = 4 if dtype == torch.float32 else 8
+def _out_rows(like, rows: int, cols: int, dtype, yt: int):
+    """rows x cols on like's device with rows padded to 16 bytes: (the view, its row stride)."""
+    per = 4 if yt == NM_OUT_F32 else 8
     ld = max((cols + per - 1) // per * per, per)
-    return torch.empty((rows, ld), dtype=dtype, device=device)[:, :cols], ld
+    out = like.new_empty((rows, ld), dtype=dtype)
+    return (out if ld == cols else out[:, :cols]), ld
 
 
 def _out_type(dtype):
     import torch
-    if dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"output type must be bfloat16 or float32, got {dtype}")
-    return NM_OUT_F32 if dtype == torch.float32 else NM_OUT_BF16
+    if dtype == torch.bfloat16:
+        return NM_OUT_BF16
+    if dtype == torch.float32:
+        return NM_OUT_F32
+    raise ValueError(f"output type must be bfloat16 or float32, got {dtype}")
 
 
 def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, out_dtype=None, stream=None):
@@ -393,11 +410,12 @@ def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, out_dtype=None, stre
     _vector(beta, "beta", K, torch.float32)
     out_dtype = out_dtype or X.dtype
     yt = _out_type(out_dtype)
-    with _on(X, stream) as s:
-        Y, ldy = _out_rows(K, T, out_dtype, X.device)
-        stats = torch.empty((2, T), dtype=torch.float32, device=X.device)
-        nm_layer_norm(X, ldx, _out_type(X.dtype), K, T, gamma, beta, eps, Y, ldy, yt, stats[0], stats[1], s)
-    return Y, stats[0], stats[1]
+    with _On(X, stream) as s:
+        Y, ldy = _out_rows(X, K, T, out_dtype, yt)
+        stats = X.new_empty((2, T), dtype=torch.float32)
+        at = stats.data_ptr()
+        nm_layer_norm(X, ldx, _out_type(X.dtype), K, T, gamma, beta, eps, Y, ldy, yt, at, at + 4 * T if at else at, s)
+    return (Y, *stats.unbind(0))
 
 
 def layer_norm_grad(dY, X, mean, rstd, gamma=None, stream=None):
@@ -409,14 +427,16 @@ def layer_norm_grad(dY, X, mean, rstd, gamma=None, stream=None):
     if dY.shape != X.shape:
         raise ValueError(f"dY {tuple(dY.shape)} and X {tuple(X.shape)} differ in shape")
     K, T = X.shape
-    for v, name, size in ((mean, "mean", T), (rstd, "rstd", T), (gamma, "gamma", K)):
-        _vector(v, name, size, torch.float32)
-    with _on(X, stream) as s:
-        dX, lddx = _out_rows(K, T, X.dtype, X.device)
-        sums = torch.empty((2, K), dtype=torch.float32, device=X.device)
-        nm_layer_norm_grad(dY, lddy, _out_type(dY.dtype), X, ldx, _out_type(X.dtype), K, T, gamma, mean, rstd, dX,
-                           lddx, sums[0], sums[1], s)
-    return dX, sums[0], sums[1]
+    _vector(mean, "mean", T, torch.float32)
+    _vector(rstd, "rstd", T, torch.float32)
+    _vector(gamma, "gamma", K, torch.float32)
+    xt = _out_type(X.dtype)
+    with _On(X, stream) as s:
+        dX, lddx = _out_rows(X, K, T, X.dtype, xt)
+        sums = X.new_empty((2, K), dtype=torch.float32)
+        at = sums.data_ptr()
+        nm_layer_norm_grad(dY, lddy, _out_type(dY.dtype), X, ldx, xt, K, T, gamma, mean, rstd, dX, lddx, at, at + 4 * K, s)
+    return (dX, *sums.unbind(0))
 
 
 def _compressed(values, meta, n: int, m: int, K: int, idx=None) -> int:
@@ -450,9 +470,8 @@ def spmm_xent(values, meta, n: int, m: int, K: int, X, target, idx=None, stream=
     if X.shape[0] != K:
         raise ValueError(f"X has {X.shape[0]} rows, K is {K}")
     _vector(target, "target", T, torch.int32)
-    with _on(X, stream) as s:
-        out = torch.empty((2, T), dtype=torch.float32, device=X.device)
-        loss, lse = out[0], out[1]
+    with _On(X, stream) as s:
+        loss, lse = X.new_empty((2, T), dtype=torch.float32).unbind(0)
         nm_spmm_xent(values, meta, n, m, R, K, idx, X, ldx, T, target, loss, lse, s)
     return loss, lse
 
@@ -471,11 +490,11 @@ def spmm_xent_grad(values, meta, n: int, m: int, K: int, X, target, lse, dloss, 
     _vector(lse, "lse", T, torch.float32)
     _vector(dloss, "dloss", T, torch.float32)
     dX, dV, lddx = None, None, 0
-    with _on(X, stream) as s:
+    with _On(X, stream) as s:
         if need_dx:
-            dX, lddx = _out_rows(K, T, torch.bfloat16, X.device)
+            dX, lddx = _out_rows(X, K, T, torch.bfloat16, NM_OUT_BF16)
         if need_dv:
-            dV = torch.empty((R, nm_value_cols(K, n, m)), dtype=torch.bfloat16, device=X.device)
+            dV = X.new_empty((R, values.shape[1]))
         nm_spmm_xent_grad(values, meta, n, m, R, K, idx, X, ldx, T, target, lse, dloss, dX, lddx, dV, s)
     return dX, dV
 
@@ -511,8 +530,8 @@ def spmm_lora(values, meta, n: int, m: int, K: int, X, A, B, adapter, scale=None
     num, rank = _adapters(A, B, R, K, T, adapter, scale)
     out_dtype = out_dtype or torch.bfloat16
     yt = _out_type(out_dtype)
-    with _on(X, stream) as s:
-        Y, ldy = _out_rows(R, T, out_dtype, X.device)
+    with _On(X, stream) as s:
+        Y, ldy = _out_rows(X, R, T, out_dtype, yt)
         nm_spmm_lora(values, meta, n, m, R, K, idx, X, ldx, T, A, B, rank, num, scale, adapter, Y, ldy, yt, s)
     return Y
 
@@ -530,8 +549,8 @@ def spmm_lora_t(values, meta, n: int, m: int, K: int, dY, A, B, adapter, scale=N
     num, rank = _adapters(A, B, R, K, T, adapter, scale)
     out_dtype = out_dtype or torch.bfloat16
     yt = _out_type(out_dtype)
-    with _on(dY, stream) as s:
-        dX, lddx = _out_rows(K, T, out_dtype, dY.device)
+    with _On(dY, stream) as s:
+        dX, lddx = _out_rows(dY, K, T, out_dtype, yt)
         nm_spmm_lora_t(values, meta, n, m, R, K, idx, dY, lddy, T, A, B, rank, num, scale, adapter, dX, lddx, yt, s)
     return dX
 
@@ -547,9 +566,9 @@ def lora_grad(dY, X, A, B, adapter, scale=None, out_dtype=None, stream=None):
     num, rank = _adapters(A, B, R, K, T, adapter, scale)
     out_dtype = out_dtype or torch.bfloat16
     yt = _out_type(out_dtype)
-    with _on(X, stream) as s:
-        dA = torch.empty((num, rank, K), dtype=out_dtype, device=X.device)
-        dB = torch.empty((num, R, rank), dtype=out_dtype, device=X.device)
+    with _On(X, stream) as s:
+        dA = X.new_empty((num, rank, K), dtype=out_dtype)
+        dB = X.new_empty((num, R, rank), dtype=out_dtype)
         nm_lora_grad(R, K, dY, lddy, X, ldx, T, A, B, rank, num, scale, adapter, dA, dB, yt, s)
     return dA, dB
 

@@ -2,6 +2,7 @@
 // (internal): error reporting, the staging pool, tensor maps, argument checks
 // and the GEMM routines that other entry points build on.  Defined in nm_api.cu.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -93,6 +94,20 @@ inline nm_status check_matrix(const void* p, int64_t ld, int64_t T, int64_t esiz
   return NM_OK;
 }
 
+// Parts of one staging buffer, each on 256 bytes: take() returns a part's offset.
+class Parts {
+ public:
+  int64_t take(int64_t bytes) {
+    const int64_t at = size_;
+    size_ += (bytes + 255) / 256 * 256;
+    return at;
+  }
+  size_t size() const { return (size_t)size_; }
+
+ private:
+  int64_t size_ = 0;
+};
+
 // A staging buffer from the library's pool, handed back on its stream when it goes out of scope.
 class Staged {
  public:
@@ -112,13 +127,29 @@ class Staged {
     p_ = nullptr;
   }
   template <typename T>
-  T* as() const {
-    return static_cast<T*>(p_);
+  T* as(int64_t offset_bytes = 0) const {
+    return reinterpret_cast<T*>(static_cast<uint8_t*>(p_) + offset_bytes);
   }
 
  private:
   cudaStream_t stream_;
   void* p_ = nullptr;
+};
+
+// Raises a kernel's shared-memory limit once per device (always to the same value, its largest request).
+struct SmemLimit {
+  std::atomic<bool> done[64];  // static storage: false
+  template <typename Kern>
+  cudaError_t raise(Kern kernel, uint32_t bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < 64;
+    if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+  }
 };
 
 }  // namespace nmk

@@ -921,11 +921,11 @@ __global__ void __launch_bounds__(256) invert_map_kernel(const int32_t* idx, int
   if (j >= 0 && (int64_t)j < K) atomicMax(inv + j, (int32_t)k);
 }
 
-template <typename Kern, typename Params>
-static cudaError_t launch_clustered(Kern kernel, dim3 grid, int cluster, uint32_t smem, uint32_t smem_limit,
-                                    const Params& p, cudaStream_t s) {
-  // Always the kernel's largest request: calls from several host threads set no smaller limit meanwhile.
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_limit);
+template <auto Kern, typename Params>
+static cudaError_t launch_clustered(dim3 grid, int cluster, uint32_t smem, uint32_t smem_limit, const Params& p,
+                                    cudaStream_t s) {
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(Kern, smem_limit);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -941,7 +941,7 @@ static cudaError_t launch_clustered(Kern kernel, dim3 grid, int cluster, uint32_
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  e = cudaLaunchKernelEx(&cfg, Kern, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -951,12 +951,12 @@ static cudaError_t launch_shrink_out(const LoraShrink& p, dim3 grid, cudaStream_
   using namespace lora;
   const uint32_t b = shrink_smem(p.stages, RB), most = shrink_smem(kMaxStages, RB);
   const int c = p.cluster;
-  if (p.out == SHRINK_F32) return launch_clustered(lora_shrink_kernel<TRANS, SHRINK_F32, 1, RB>, grid, c, b, most, p, s);
+  if (p.out == SHRINK_F32) return launch_clustered<&lora_shrink_kernel<TRANS, SHRINK_F32, 1, RB>>(grid, c, b, most, p, s);
   if (p.out == SHRINK_TERMS)
-    return p.planes == 3 ? launch_clustered(lora_shrink_kernel<TRANS, SHRINK_TERMS, 3, RB>, grid, c, b, most, p, s)
-                         : launch_clustered(lora_shrink_kernel<TRANS, SHRINK_TERMS, 2, RB>, grid, c, b, most, p, s);
-  return p.planes == 3 ? launch_clustered(lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 3, RB>, grid, c, b, most, p, s)
-                       : launch_clustered(lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 2, RB>, grid, c, b, most, p, s);
+    return p.planes == 3 ? launch_clustered<&lora_shrink_kernel<TRANS, SHRINK_TERMS, 3, RB>>(grid, c, b, most, p, s)
+                         : launch_clustered<&lora_shrink_kernel<TRANS, SHRINK_TERMS, 2, RB>>(grid, c, b, most, p, s);
+  return p.planes == 3 ? launch_clustered<&lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 3, RB>>(grid, c, b, most, p, s)
+                       : launch_clustered<&lora_shrink_kernel<TRANS, SHRINK_BLOCKS, 2, RB>>(grid, c, b, most, p, s);
 }
 
 cudaError_t launch_lora_shrink(LoraShrink& p, bool trans, cudaStream_t s) {
@@ -996,10 +996,10 @@ cudaError_t launch_lora_expand(LoraExpand& p, bool trans, cudaStream_t s) {
   const uint32_t b = p.base_off + (p.splits > 1 ? (uint32_t)(kRows * (p.ldb + 4) * 4) : 0u);
   const uint32_t most = kExpandBatch + 3 * kTok * (kMaxRank * 2 + 16) + kRows * (kTok + 4) * 4;
   if (trans)
-    return p.out_f32 ? launch_clustered(lora_expand_kernel<true, 3>, grid, 1, b, most, p, s)
-                     : launch_clustered(lora_expand_kernel<true, 2>, grid, 1, b, most, p, s);
-  return p.out_f32 ? launch_clustered(lora_expand_kernel<false, 3>, grid, 1, b, most, p, s)
-                   : launch_clustered(lora_expand_kernel<false, 2>, grid, 1, b, most, p, s);
+    return p.out_f32 ? launch_clustered<&lora_expand_kernel<true, 3>>(grid, 1, b, most, p, s)
+                     : launch_clustered<&lora_expand_kernel<true, 2>>(grid, 1, b, most, p, s);
+  return p.out_f32 ? launch_clustered<&lora_expand_kernel<false, 3>>(grid, 1, b, most, p, s)
+                   : launch_clustered<&lora_expand_kernel<false, 2>>(grid, 1, b, most, p, s);
 }
 
 int lora_cat_blocks() { return 2 * sm_count_current(); }
@@ -1041,10 +1041,10 @@ cudaError_t launch_lora_outer(LoraOuter& p, bool by_rank, cudaStream_t s) {
   const dim3 grid((unsigned)(blocks * p.cluster), (unsigned)items);
   const uint32_t b = outer_smem(p.out_f32 ? 3 : 2);
   if (by_rank)
-    return p.out_f32 ? launch_clustered(lora_outer_kernel<true, 3>, grid, p.cluster, b, b, p, s)
-                     : launch_clustered(lora_outer_kernel<true, 2>, grid, p.cluster, b, b, p, s);
-  return p.out_f32 ? launch_clustered(lora_outer_kernel<false, 3>, grid, p.cluster, b, b, p, s)
-                   : launch_clustered(lora_outer_kernel<false, 2>, grid, p.cluster, b, b, p, s);
+    return p.out_f32 ? launch_clustered<&lora_outer_kernel<true, 3>>(grid, p.cluster, b, b, p, s)
+                     : launch_clustered<&lora_outer_kernel<true, 2>>(grid, p.cluster, b, b, p, s);
+  return p.out_f32 ? launch_clustered<&lora_outer_kernel<false, 3>>(grid, p.cluster, b, b, p, s)
+                   : launch_clustered<&lora_outer_kernel<false, 2>>(grid, p.cluster, b, b, p, s);
 }
 
 cudaError_t launch_invert_map(const int32_t* idx, int64_t K, int32_t* inv, cudaStream_t s) {
@@ -1111,10 +1111,10 @@ nm_status shrink(const Adapters& ad, bool trans, int64_t D, const uint16_t* Z, i
 // The adapters in the projection's own reduction: a GEMM that serves the shape takes, after its own steps, the blocks
 // of 64 rank rows that a column tile's tokens use.  Returns what that GEMM and the mending pass need.
 struct InGemm {
-  Staged cat, blocks, small;
+  Staged buf;
   GemmExt ext{};
   LoraMend mend{};
-  InGemm(cudaStream_t s) : cat(s), blocks(s), small(s) {}
+  InGemm(cudaStream_t s) : buf(s) {}
 };
 bool adapters_fit_gemm(const Adapters& ad) { return ad.n > 0 && ad.n * ad.rank <= lora::kMaxCat; }
 nm_status adapters_for_gemm(const Adapters& ad, bool trans, int64_t D, int64_t rows, const uint16_t* Z, int64_t ldz,
@@ -1122,13 +1122,15 @@ nm_status adapters_for_gemm(const Adapters& ad, bool trans, int64_t D, int64_t r
   using namespace lora;
   const int64_t cat = (ad.n * ad.rank + 63) / 64 * 64, ldp = (T + 7) / 8 * 8, ldc = trans ? (rows + 7) / 8 * 8 : cat;
   const int planes = f32 ? 3 : 2, nflags = lora_cat_blocks();
-  cudaError_t e = g.cat.get((size_t)((trans ? ad.n * ad.rank : rows) * ldc * 2));
-  if (e == cudaSuccess) e = g.blocks.get((size_t)(planes * cat * ldp * 2));
-  if (e == cudaSuccess) e = g.small.get((size_t)(nflags + tiles_of(T) + (idx ? rows : 0)) * 4);
+  Parts parts;
+  const int64_t at_cat = parts.take((trans ? ad.n * ad.rank : rows) * ldc * 2), at_blocks = parts.take(planes * cat * ldp * 2);
+  const int64_t at_flags = parts.take(nflags * 4), at_masks = parts.take(tiles_of(T) * 4);
+  const int64_t at_inv = parts.take(idx ? rows * 4 : 0);
+  cudaError_t e = g.buf.get(parts.size());
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the adapters");
-  uint32_t* flags = g.small.as<uint32_t>();
-  uint32_t* masks = flags + nflags;
-  int32_t* inv = idx ? reinterpret_cast<int32_t*>(masks + tiles_of(T)) : nullptr;
+  uint32_t* flags = g.buf.as<uint32_t>(at_flags);
+  uint32_t* masks = g.buf.as<uint32_t>(at_masks);
+  int32_t* inv = idx ? g.buf.as<int32_t>(at_inv) : nullptr;
   LoraCat c = {};
   c.M = trans ? ad.A : ad.B;
   c.n = ad.n;
@@ -1137,7 +1139,7 @@ nm_status adapters_for_gemm(const Adapters& ad, bool trans, int64_t D, int64_t r
   c.cat = cat;
   c.ldc = ldc;
   c.idx = idx;
-  c.out = g.cat.as<uint16_t>();
+  c.out = g.buf.as<uint16_t>(at_cat);
   c.flags = flags;
   c.inv = inv;
   e = launch_lora_cat(c, trans, s);
@@ -1145,7 +1147,7 @@ nm_status adapters_for_gemm(const Adapters& ad, bool trans, int64_t D, int64_t r
   LoraShrink p = {};
   p.out = SHRINK_BLOCKS;
   p.planes = planes;
-  p.terms = g.blocks.as<uint16_t>();
+  p.terms = g.buf.as<uint16_t>(at_blocks);
   p.cat = cat;
   p.ldp = ldp;
   p.masks = masks;
@@ -1155,8 +1157,7 @@ nm_status adapters_for_gemm(const Adapters& ad, bool trans, int64_t D, int64_t r
   p.early = 1;  // reads nothing of the layout launch (inv is taken at its end)
   nm_status st = shrink(ad, trans, D, Z, ldz, T, p, s);
   if (st != NM_OK) return st;
-  g.ext = GemmExt{g.cat.as<uint16_t>(), trans ? ad.n * ad.rank : rows, trans ? rows : cat, ldc, g.blocks.as<uint16_t>(), cat,
-                  ldp, planes, masks};
+  g.ext = GemmExt{c.out, trans ? ad.n * ad.rank : rows, trans ? rows : cat, ldc, p.terms, cat, ldp, planes, masks};
   LoraMend& m = g.mend;
   m.M = c.M;
   m.adapter = ad.adapter;
@@ -1328,12 +1329,13 @@ nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t lddy, c
   if (st == NM_OK && K > 0) st = check_matrix(X, ldx, T, 2, "X");
   if (st == NM_OK) st = require_device();
   if (st != NM_OK) return st;
-  Staged terms(s), more(s), plan(s);
+  Staged buf(s);
   const int planes = dtype == NM_OUT_F32 ? 3 : 2;
   const int64_t rs = lora::rank_stride(rank), tiles = lora::tiles_of(T);
-  cudaError_t e = plan.get((size_t)((tiles + 1) * num_adapters * 4));
-  if (e == cudaSuccess) e = terms.get((size_t)(planes * T * rs * 2));
-  if (e == cudaSuccess) e = more.get((size_t)(planes * T * rs * 2));
+  Parts parts;
+  const int64_t at_plan = parts.take((tiles + 1) * num_adapters * 4);
+  const int64_t at_terms[2] = {parts.take(planes * T * rs * 2), parts.take(planes * T * rs * 2)};
+  cudaError_t e = buf.get(parts.size());
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the adapter gradients");
   LoraOuter p = {};
   p.adapter = adapter;
@@ -1341,12 +1343,13 @@ nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t lddy, c
   p.n = num_adapters;
   p.T = T;
   p.rank = rank;
-  p.counts = plan.as<int32_t>();
-  p.tiles = plan.as<int32_t>() + num_adapters;
+  int32_t* counts = buf.as<int32_t>(at_plan);
+  p.counts = counts;
+  p.tiles = counts + num_adapters;
   p.out_f32 = dtype == NM_OUT_F32;
   p.status = status_word_ptr();
   if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
-  e = launch_lora_plan(adapter, T, num_adapters, plan.as<int32_t>() + num_adapters, plan.as<int32_t>(), s);
+  e = launch_lora_plan(adapter, T, num_adapters, counts + num_adapters, counts, s);
   if (e != cudaSuccess) return cuda_fail(e, "adapter plan launch");
   const uint32_t box = (uint32_t)(rs < lora::kOuterRank ? rs : lora::kOuterRank);
   // S = A X for dB and U = B^T dY for dA, then the two gradients: within each pair the second launch needs nothing of
@@ -1357,7 +1360,7 @@ nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t lddy, c
     LoraShrink sh = {};
     sh.out = SHRINK_TERMS;
     sh.planes = planes;
-    sh.terms = which ? more.as<uint16_t>() : terms.as<uint16_t>();
+    sh.terms = buf.as<uint16_t>(at_terms[which]);
     sh.early = 1;
     st = which ? shrink(ad, true, R, dY, lddy, T, sh, s) : shrink(ad, false, K, X, ldx, T, sh, s);
     if (st != NM_OK) return st;
@@ -1368,7 +1371,7 @@ nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t lddy, c
     st = make_tmap(&p.tm_z, which ? X : dY, (uint64_t)T, (uint64_t)rows, (uint64_t)(which ? ldx : lddy) * 2, lora::kTok,
                    lora::kRows, 128, "tokens");
     if (st == NM_OK)
-      st = make_tmap3(&p.tm_v, which ? more.as<uint16_t>() : terms.as<uint16_t>(), (uint64_t)rs, (uint64_t)T,
+      st = make_tmap3(&p.tm_v, buf.as<uint16_t>(at_terms[which]), (uint64_t)rs, (uint64_t)T,
                       (uint64_t)planes, (uint64_t)rs * 2, (uint64_t)(T * rs) * 2, box, lora::kTok,
                       box == 64 ? 128 : box == 32 ? 64 : box == 16 ? 32 : 0, "adapter terms");
     if (st != NM_OK) return st;

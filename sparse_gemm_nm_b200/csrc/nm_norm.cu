@@ -461,14 +461,12 @@ void norm_shape(NormParams& p, int64_t bytes) {
   p.smem = p.cached ? (uint32_t)slab(lpr, c) : 0;
 }
 
-template <typename Kern>
-static cudaError_t launch_norm_grid(Kern kernel, const NormParams& p, cudaStream_t s) {
+template <auto Kern>
+static cudaError_t launch_norm_grid(const NormParams& p, cudaStream_t s) {
   if (p.tiles * p.cluster >= (1ll << 31)) return cudaErrorInvalidValue;
-  if (p.smem > 32 * 1024) {  // always the same limit: calls from several host threads set no smaller one meanwhile
-    cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)norm::kMaxSlabBytes);
-    if (e != cudaSuccess) return e;
-  }
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(Kern, (uint32_t)norm::kMaxSlabBytes);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.tiles * p.cluster));
   cfg.blockDim = dim3(norm::kThreads);
@@ -483,21 +481,21 @@ static cudaError_t launch_norm_grid(Kern kernel, const NormParams& p, cudaStream
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  e = cudaLaunchKernelEx(&cfg, Kern, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
   if (p.x_f32)
-    return p.cached ? launch_norm_grid(norm_kernel<true, true>, p, s) : launch_norm_grid(norm_kernel<true, false>, p, s);
-  return p.cached ? launch_norm_grid(norm_kernel<false, true>, p, s) : launch_norm_grid(norm_kernel<false, false>, p, s);
+    return p.cached ? launch_norm_grid<&norm_kernel<true, true>>(p, s) : launch_norm_grid<&norm_kernel<true, false>>(p, s);
+  return p.cached ? launch_norm_grid<&norm_kernel<false, true>>(p, s) : launch_norm_grid<&norm_kernel<false, false>>(p, s);
 }
 
 template <bool XF32, bool DF32>
 static cudaError_t launch_norm_grad_types(const NormParams& p, cudaStream_t s) {
-  return p.cached ? launch_norm_grid(norm_grad_kernel<XF32, DF32, true>, p, s)
-                  : launch_norm_grid(norm_grad_kernel<XF32, DF32, false>, p, s);
+  return p.cached ? launch_norm_grid<&norm_grad_kernel<XF32, DF32, true>>(p, s)
+                  : launch_norm_grid<&norm_grad_kernel<XF32, DF32, false>>(p, s);
 }
 
 cudaError_t launch_norm_grad(const NormParams& p, cudaStream_t s) {

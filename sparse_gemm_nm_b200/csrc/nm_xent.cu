@@ -297,7 +297,7 @@ nm_status run_xent(Head h, const int32_t* idx, const int32_t* target, float* los
 
 nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const float* lse, const float* dloss,
                         uint16_t* dX, int64_t lddx, uint16_t* dV, cudaStream_t s) {
-  Staged xp(s), z(s), g(s), wd(s), acc(s), cols(s);
+  Staged xp(s), buf(s), cols(s);
   nm_status st = gather_input(h, idx, xp, s);
   if (st != NM_OK) return st;
   const bool fused = spmm_pair_serves(h.values, h.meta, h.n, h.m, h.K, h.T);
@@ -307,35 +307,39 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
   epi.mode = PAIR_EPI_XGRAD;
   if (fused) st = column_data(h, target, lse, dloss, epi, cols, s);
   if (st != NM_OK) return st;
-  cudaError_t e = g.get((size_t)(rows * ldg * 2));
-  if (e == cudaSuccess && !fused) e = z.get((size_t)(rows * ldz * 4));
-  if (e == cudaSuccess && dX) e = wd.get((size_t)(rows * ldk * 2));
-  if (e == cudaSuccess && dX) e = acc.get((size_t)(h.K * ldz * 4));
+  Parts parts;
+  const int64_t at_g = parts.take(rows * ldg * 2), at_z = parts.take(fused ? 0 : rows * ldz * 4);
+  const int64_t at_wd = parts.take(dX ? rows * ldk * 2 : 0), at_acc = parts.take(dX ? h.K * ldz * 4 : 0);
+  cudaError_t e = buf.get(parts.size());
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gradient piece");
+  uint16_t* g = buf.as<uint16_t>(at_g);
+  uint16_t* wd = buf.as<uint16_t>(at_wd);
+  float* z = buf.as<float>(at_z);
+  float* acc = buf.as<float>(at_acc);
   for (int64_t v0 = 0; v0 < h.R; v0 += rows) {
     const int64_t n = h.R - v0 < rows ? h.R - v0 : rows;
     if (fused) {  // the GEMM's epilogue turns the logits into G
       epi.row0 = v0;
-      st = run_spmm_epilogue(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, g.as<uint16_t>(), ldg,
+      st = run_spmm_epilogue(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, g, ldg,
                              epi, s);
       if (st != NM_OK) return st;
     } else {
-      st = spmm_rows(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, z.as<float>(), ldz, NM_OUT_F32,
+      st = spmm_rows(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, z, ldz, NM_OUT_F32,
                      s);
       if (st != NM_OK) return st;
       e = launch_pdl(xent_g_kernel, dim3((unsigned)((ldg / 2 + 31) / 32), (unsigned)((n + 63) / 64)), dim3(256), 0, s,
-                     (const float*)z.as<float>(), ldz, n, h.T, h.R, v0, target, lse, dloss, g.as<uint16_t>(), ldg);
+                     (const float*)z, ldz, n, h.T, h.R, v0, target, lse, dloss, g, ldg);
       count_launch();
       if (e != cudaSuccess) return cuda_fail(e, "cross-entropy gradient launch");
     }
     if (dX) {
-      e = launch_decompress(h.row_values(v0), h.row_meta(v0), n, h.K, h.n, h.m, wd.as<uint16_t>(), ldk, s);
+      e = launch_decompress(h.row_values(v0), h.row_meta(v0), n, h.K, h.n, h.m, wd, ldk, s);
       if (e != cudaSuccess) return cuda_fail(e, "decompress launch");
-      st = dense_t_accumulate(wd.as<uint16_t>(), ldk, n, h.K, g.as<uint16_t>(), ldg, h.T, acc.as<float>(), ldz, v0 > 0, s);
+      st = dense_t_accumulate(wd, ldk, n, h.K, g, ldg, h.T, acc, ldz, v0 > 0, s);
       if (st != NM_OK) return st;
     }
     if (dV) {
-      st = run_sddmm(h.row_meta(v0), h.n, h.m, n, h.K, nullptr, g.as<uint16_t>(), ldg, h.X, h.ldx, h.T,
+      st = run_sddmm(h.row_meta(v0), h.n, h.m, n, h.K, nullptr, g, ldg, h.X, h.ldx, h.T,
                      dV + v0 * value_cols(h.K, h.n, h.m), NM_OUT_BF16, s);
       if (st != NM_OK) return st;
     }
@@ -343,7 +347,7 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
   if (dX) {
     const int64_t want = (h.K * ((h.T + 7) / 8) + 255) / 256, cap = (int64_t)sm_count_current() * 16;
     e = launch_pdl(xent_round_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, s,
-                   (const float*)acc.as<float>(), ldz, h.K, h.T, idx, dX, lddx);
+                   (const float*)acc, ldz, h.K, h.T, idx, dX, lddx);
     count_launch();
     if (e != cudaSuccess) return cuda_fail(e, "gradient rounding launch");
   }
