@@ -39,75 +39,95 @@ namespace nmk {
 namespace norm {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCols = 64;  // tokens of a strip: eight lanes of eight
+constexpr int kMaxCols = 64;  // tokens of a strip, at most (eight lanes of eight)
 constexpr int kMaxCluster = 8;
 constexpr int kBoxRows = 32;                     // rows of a TMA box (slabs are whole boxes)
 constexpr int64_t kSlabBytes = 52 * 1024;        // four CTAs of an SM
 constexpr int64_t kMaxSlabBytes = 216 * 1024;    // one CTA
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// Eight consecutive tokens of one row as held in registers.
-template <bool F32>
-struct Piece {
-  uint4 v[F32 ? 2 : 1];
+// Two float32 values, worked on by the packed float32 instructions (one issue for both).
+struct F2 {
+  unsigned long long v;
 };
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
 
+// Eight consecutive tokens of a row, as four pairs.
 template <bool F32>
-__device__ __forceinline__ Piece<F32> load_piece(const void* base, int64_t off, int valid) {
-  Piece<F32> p;
+__device__ __forceinline__ void load_global(const void* base, int64_t off, int valid, F2 (&f)[4]) {
   if (F32) {
     const float* s = static_cast<const float*>(base) + off;
     if (valid >= 8) {
-      p.v[0] = __ldg(reinterpret_cast<const uint4*>(s));
-      p.v[F32 ? 1 : 0] = __ldg(reinterpret_cast<const uint4*>(s) + 1);
+      const float4 a = __ldg(reinterpret_cast<const float4*>(s)), b = __ldg(reinterpret_cast<const float4*>(s) + 1);
+      f[0] = f2(a.x, a.y);
+      f[1] = f2(a.z, a.w);
+      f[2] = f2(b.x, b.y);
+      f[3] = f2(b.z, b.w);
     } else {  // the row's last tokens one by one, zeros after them
-      uint32_t w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = j < valid ? __float_as_uint(__ldg(s + j)) : 0u;
-      p.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      p.v[F32 ? 1 : 0] = make_uint4(w[4], w[5], w[6], w[7]);
+      for (int j = 0; j < 4; ++j)
+        f[j] = f2(2 * j < valid ? __ldg(s + 2 * j) : 0.f, 2 * j + 1 < valid ? __ldg(s + 2 * j + 1) : 0.f);
     }
   } else {
     const uint16_t* s = static_cast<const uint16_t*>(base) + off;
+    uint32_t w[4] = {0, 0, 0, 0};
     if (valid >= 8) {
-      p.v[0] = __ldg(reinterpret_cast<const uint4*>(s));
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(s));
+      w[0] = a.x;
+      w[1] = a.y;
+      w[2] = a.z;
+      w[3] = a.w;
     } else {
-      uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j < valid) w[j >> 1] |= (uint32_t)__ldg(s + j) << (16 * (j & 1));
-      p.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = f2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
   }
-  return p;
 }
 
+// The same from shared memory (whole pieces; zeros past T and K were filled in).
 template <bool F32>
-__device__ __forceinline__ void unpack(const Piece<F32>& p, float (&f)[8]) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(p.v);
+__device__ __forceinline__ void load_shared(const uint8_t* at, F2 (&f)[4]) {
   if (F32) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[F32 ? j : 0]);
+    const float4 a = *reinterpret_cast<const float4*>(at), b = *(reinterpret_cast<const float4*>(at) + 1);
+    f[0] = f2(a.x, a.y);
+    f[1] = f2(a.z, a.w);
+    f[2] = f2(b.x, b.y);
+    f[3] = f2(b.z, b.w);
   } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(at);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(w[j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
+    for (int j = 0; j < 4; ++j) f[j] = f2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
   }
 }
 
-// The same from shared memory (off in elements; whole pieces only).
-template <bool F32>
-__device__ __forceinline__ Piece<F32> shared_piece(const uint8_t* base, int64_t off) {
-  Piece<F32> p;
-  const uint4* s = reinterpret_cast<const uint4*>(base + off * (F32 ? 4 : 2));
-  p.v[0] = s[0];
-  if (F32) p.v[F32 ? 1 : 0] = s[1];
-  return p;
-}
-
-__device__ __forceinline__ void store_piece(void* base, int64_t off, bool f32, int valid, const float (&f)[8]) {
+__device__ __forceinline__ void store_piece(void* base, int64_t off, bool f32, int valid, const F2 (&p)[4]) {
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) split(p[j], f[2 * j], f[2 * j + 1]);
   if (f32) {
     float* d = static_cast<float*>(base) + off;
     if (valid >= 8) {
@@ -133,25 +153,35 @@ __device__ __forceinline__ void store_piece(void* base, int64_t off, bool f32, i
   }
 }
 
-// Sums of f over the threads of the CTA that hold the same eight tokens, left in out[token] (lpr * 8 values).
-// All threads call it; out and scratch are shared memory, scratch kWarps x kMaxCols floats.
-__device__ __forceinline__ void column_sums(float (&f)[8], int lpr, float* scratch, float* out) {
+// Sums of N quantities over the threads of the CTA that hold the same eight tokens, left in out[n][token].
+// All threads call it; out and scratch are shared memory, scratch N x kWarps x kMaxCols floats.
+template <int N>
+__device__ __forceinline__ void column_sums(F2 (&q)[N][4], int lpr, float* scratch, float (*out)[kMaxCols]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float f[N][8];
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split(q[n][j], f[n][2 * j], f[n][2 * j + 1]);
   for (int o = lpr; o < 32; o <<= 1) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] += __shfl_xor_sync(0xFFFFFFFFu, f[j], o);
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[n][j] += __shfl_xor_sync(0xFFFFFFFFu, f[n][j], o);
   }
-  __syncthreads();  // earlier readers of scratch and out are done
   if (lane < lpr) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) scratch[warp * kMaxCols + lane * 8 + j] = f[j];
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) scratch[(n * kWarps + warp) * kMaxCols + lane * 8 + j] = f[n][j];
   }
   __syncthreads();
-  if ((int)threadIdx.x < lpr * 8) {
+  const int n = threadIdx.x / kMaxCols, t = threadIdx.x % kMaxCols;
+  if (n < N && t < lpr * 8) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += scratch[w * kMaxCols + threadIdx.x];
-    out[threadIdx.x] = s;
+    for (int w = 0; w < kWarps; ++w) s += scratch[(n * kWarps + w) * kMaxCols + t];
+    out[n][t] = s;
   }
   __syncthreads();
 }
@@ -161,6 +191,12 @@ __device__ __forceinline__ float ld_cluster(const float* local, uint32_t rank) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to_cta(smem_u32(local), rank)) : "memory");
   return v;
 }
+// The same place of every CTA of the cluster (0 past C): all reads in flight together.
+__device__ __forceinline__ void ld_cluster_all(const float* local, int C, float (&v)[kMaxCluster]) {
+#pragma unroll
+  for (int c = 0; c < kMaxCluster; ++c) v[c] = c < C ? ld_cluster(local, c) : 0.f;
+}
+
 // Brings `rows` rows from row r0 of a K x T tensor, columns t .. t + 8 lpr, into shared memory as rows of
 // 8 lpr elements (boxes of kBoxRows rows; the last box may reach into rows of the next slab or past K).  The first
 // lane of every warp calls it and issues its share of the boxes.
@@ -172,21 +208,21 @@ __device__ __forceinline__ void load_slab(uint8_t* dst, const CUtensorMap* tm, u
 }  // namespace norm
 
 template <bool XF32, bool CACHED>
-__global__ void __launch_bounds__(norm::kThreads) norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(norm::kThreads, 4) norm_kernel(const __grid_constant__ NormParams p) {
   using namespace norm;
   extern __shared__ __align__(128) uint8_t slab[];
   __shared__ float scratch[kWarps * kMaxCols];
-  __shared__ float s_mean[kMaxCols], s_m2[kMaxCols], s_rstd[kMaxCols], t_mean[kMaxCols];
+  __shared__ float s_mean[1][kMaxCols], s_m2[1][kMaxCols], s_rstd[kMaxCols], t_mean[kMaxCols];
   __shared__ uint64_t bar;
   __shared__ int abort_flag;
   const uint32_t rank = cluster_ctarank();
   const int C = p.cluster, lpr = p.lpr;
   const int64_t tile = blockIdx.x / C;
-  const int64_t r0 = rank * p.rows, r1 = r0 + p.rows < p.K ? r0 + p.rows : p.K;
-  const int64_t mine = r1 > r0 ? r1 - r0 : 0;
+  const int64_t r0 = rank * p.rows;
+  const int mine = (int)(r0 < p.K ? (p.K - r0 < p.rows ? p.K - r0 : p.rows) : 0);  // rows of this CTA
   const int col8 = threadIdx.x % lpr;
   const int step = kThreads / lpr;
-  const int64_t first = r0 + threadIdx.x / lpr;
+  const int first = threadIdx.x / lpr;
   const int64_t t0 = tile * (8 * lpr) + 8 * col8;
   const int valid = t0 >= p.T ? 0 : (p.T - t0 < 8 ? (int)(p.T - t0) : 8);
   if (CACHED && threadIdx.x == 0) {
@@ -198,59 +234,72 @@ __global__ void __launch_bounds__(norm::kThreads) norm_kernel(const __grid_const
   if (CACHED) __syncthreads();
   pdl_gate();
   bool ok = true;
+  const int piece = XF32 ? 32 : 16;  // bytes of eight tokens
+  const uint8_t* mine_at = slab + (first * lpr + col8) * piece;
+  const int stride = step * lpr * piece;  // bytes between this thread's rows
   if (CACHED) {
     const int64_t boxes = (mine + kBoxRows - 1) / kBoxRows;
-    const uint32_t box_bytes = (uint32_t)(kBoxRows * 8 * lpr) * (XF32 ? 4u : 2u);
+    const uint32_t box_bytes = (uint32_t)(kBoxRows * lpr * piece);
     if (threadIdx.x % 32 == 0 && boxes > 0) {
       if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar, (uint32_t)boxes * box_bytes);
       load_slab(slab, &p.tm_x, &bar, tile * (8 * lpr), r0, boxes, box_bytes);
     }
     if (boxes > 0) ok = mbar_wait(&bar, 0, &abort_flag, p.status, kWaitNs);
   }
-  // Row k's piece of this thread's eight tokens (zeros past T).
-  auto row = [&](int64_t k) {
-    if (CACHED) return shared_piece<XF32>(slab, (k - r0) * (8 * lpr) + 8 * col8);
-    return load_piece<XF32>(p.X, k * p.ldx + t0, valid);
+  // Row `k` of the slab, the i-th of this thread: its eight tokens (zeros past T).
+  auto row = [&](int k, int i, F2 (&f)[4]) {
+    if (CACHED)
+      load_shared<XF32>(mine_at + (int64_t)i * stride, f);
+    else
+      load_global<XF32>(p.X, (r0 + k) * p.ldx + t0, valid, f);
   };
 
-  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  const F2 zero = f2(0.f, 0.f);
+  F2 sum[1][4] = {{zero, zero, zero, zero}};
 #pragma unroll 4
-  for (int64_t k = first; k < r1; k += step) {
-    float f[8];
-    unpack<XF32>(row(k), f);
+  for (int k = first, i = 0; k < mine; k += step, ++i) {
+    F2 f[4];
+    row(k, i, f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += f[j];
+    for (int j = 0; j < 4; ++j) sum[0][j] = add2(sum[0][j], f[j]);
   }
-  column_sums(sum, lpr, scratch, s_mean);
-  if ((int)threadIdx.x < lpr * 8) s_mean[threadIdx.x] = mine > 0 ? s_mean[threadIdx.x] / (float)mine : 0.f;
-  __syncthreads();
-  float m[8], sq[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  column_sums<1>(sum, lpr, scratch, s_mean);
+  // this CTA's own mean, negated: the squares are taken about it
+  const float per = mine > 0 ? 1.0f / (float)mine : 0.f;
+  F2 m[4], sq[1][4] = {{zero, zero, zero, zero}};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m[j] = s_mean[8 * col8 + j];
+  for (int j = 0; j < 4; ++j) m[j] = f2(-(s_mean[0][8 * col8 + 2 * j] * per), -(s_mean[0][8 * col8 + 2 * j + 1] * per));
 #pragma unroll 4
-  for (int64_t k = first; k < r1; k += step) {
-    float f[8];
-    unpack<XF32>(row(k), f);
+  for (int k = first, i = 0; k < mine; k += step, ++i) {
+    F2 f[4];
+    row(k, i, f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sq[j] += (f[j] - m[j]) * (f[j] - m[j]);
+    for (int j = 0; j < 4; ++j) {
+      const F2 d = add2(f[j], m[j]);
+      sq[0][j] = fma2(d, d, sq[0][j]);
+    }
   }
-  column_sums(sq, lpr, scratch, s_m2);
-  if (C > 1) cluster_sync();  // every CTA's s_mean and s_m2 are written
+  column_sums<1>(sq, lpr, scratch, s_m2);
+  if (C > 1) cluster_sync();  // every CTA's s_mean (sums) and s_m2 are written
   if ((int)threadIdx.x < lpr * 8) {
-    float mean = 0.f, m2 = 0.f;
+    float mean = s_mean[0][threadIdx.x] / (float)p.K, m2 = s_m2[0][threadIdx.x];
     if (C > 1) {
-      for (int c = 0; c < C; ++c) {
-        const int64_t a = c * p.rows, n = a + p.rows < p.K ? p.rows : (p.K > a ? p.K - a : 0);
-        mean += ld_cluster(s_mean + threadIdx.x, c) * ((float)n / (float)p.K);
+      float a[kMaxCluster], q[kMaxCluster];
+      ld_cluster_all(&s_mean[0][threadIdx.x], C, a);
+      ld_cluster_all(&s_m2[0][threadIdx.x], C, q);
+      float total = 0.f;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) total += a[c];
+      mean = total / (float)p.K;
+      m2 = 0.f;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        if (c >= C) continue;
+        const int64_t at = c * p.rows;
+        const float n = (float)(at < p.K ? (p.K - at < p.rows ? p.K - at : p.rows) : 0);
+        const float d = n > 0.f ? a[c] * (1.0f / n) - mean : 0.f;
+        m2 += q[c] + n * d * d;
       }
-      for (int c = 0; c < C; ++c) {
-        const int64_t a = c * p.rows, n = a + p.rows < p.K ? p.rows : (p.K > a ? p.K - a : 0);
-        const float d = ld_cluster(s_mean + threadIdx.x, c) - mean;
-        m2 += ld_cluster(s_m2 + threadIdx.x, c) + (float)n * d * d;
-      }
-    } else {
-      mean = s_mean[threadIdx.x];
-      m2 = s_m2[threadIdx.x];
     }
     const float rstd = 1.0f / sqrtf(m2 / (float)p.K + p.eps);
     t_mean[threadIdx.x] = mean;
@@ -261,43 +310,46 @@ __global__ void __launch_bounds__(norm::kThreads) norm_kernel(const __grid_const
       if (p.rstd) p.rstd[t] = rstd;
     }
   }
+  if (C > 1) cluster_arrive();  // done with the other CTAs' sums
   __syncthreads();
-  float rs[8];
+  F2 rs[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    m[j] = t_mean[8 * col8 + j];
-    rs[j] = s_rstd[8 * col8 + j];
+  for (int j = 0; j < 4; ++j) {
+    m[j] = f2(-t_mean[8 * col8 + 2 * j], -t_mean[8 * col8 + 2 * j + 1]);
+    rs[j] = f2(s_rstd[8 * col8 + 2 * j], s_rstd[8 * col8 + 2 * j + 1]);
   }
   if (ok && valid > 0) {
+    int64_t out = (r0 + first) * p.ldy + t0;
 #pragma unroll 4
-    for (int64_t k = first; k < r1; k += step) {
-      float f[8];
-      unpack<XF32>(row(k), f);
-      const float g = p.gamma ? __ldg(p.gamma + k) : 1.f, b = p.beta ? __ldg(p.beta + k) : 0.f;
+    for (int k = first, i = 0; k < mine; k += step, ++i, out += step * p.ldy) {
+      F2 f[4];
+      const float g = p.gamma ? __ldg(p.gamma + r0 + k) : 1.f, b = p.beta ? __ldg(p.beta + r0 + k) : 0.f;
+      const F2 g2 = f2(g, g), b2 = f2(b, b);
+      row(k, i, f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = (f[j] - m[j]) * rs[j] * g + b;
-      store_piece(p.Y, k * p.ldy + t0, p.y_f32 != 0, valid, f);
+      for (int j = 0; j < 4; ++j) f[j] = fma2(mul2(add2(f[j], m[j]), rs[j]), g2, b2);
+      store_piece(p.Y, out, p.y_f32 != 0, valid, f);
     }
   }
-  if (C > 1) cluster_sync();  // no CTA leaves while another still reads its shared memory
+  if (C > 1) cluster_wait();  // no CTA leaves while another still reads its shared memory
 }
 
 template <bool XF32, bool DF32, bool CACHED>
-__global__ void __launch_bounds__(norm::kThreads) norm_grad_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(norm::kThreads, 3) norm_grad_kernel(const __grid_constant__ NormParams p) {
   using namespace norm;
   extern __shared__ __align__(128) uint8_t slab[];  // X's rows, then dY's
-  __shared__ float scratch[kWarps * kMaxCols];
-  __shared__ float s_c1[kMaxCols], s_c2[kMaxCols], t_c1[kMaxCols], t_c2[kMaxCols];
+  __shared__ float scratch[2 * kWarps * kMaxCols];
+  __shared__ float s_c[2][kMaxCols], t_c[2][kMaxCols];
   __shared__ uint64_t bar;
   __shared__ int abort_flag;
   const uint32_t rank = cluster_ctarank();
   const int C = p.cluster, lpr = p.lpr;
   const int64_t tile = blockIdx.x / C;
-  const int64_t r0 = rank * p.rows, r1 = r0 + p.rows < p.K ? r0 + p.rows : p.K;
-  const int64_t mine = r1 > r0 ? r1 - r0 : 0;
+  const int64_t r0 = rank * p.rows;
+  const int mine = (int)(r0 < p.K ? (p.K - r0 < p.rows ? p.K - r0 : p.rows) : 0);  // rows of this CTA
   const int col8 = threadIdx.x % lpr;
   const int step = kThreads / lpr;
-  const int64_t first = r0 + threadIdx.x / lpr;
+  const int first = threadIdx.x / lpr;
   const int64_t t0 = tile * (8 * lpr) + 8 * col8;
   const int valid = t0 >= p.T ? 0 : (p.T - t0 < 8 ? (int)(p.T - t0) : 8);
   if (CACHED && threadIdx.x == 0) {
@@ -308,102 +360,120 @@ __global__ void __launch_bounds__(norm::kThreads) norm_grad_kernel(const __grid_
   }
   if (CACHED) __syncthreads();
   pdl_gate();
+  const int x_piece = XF32 ? 32 : 16, d_piece = DF32 ? 32 : 16;  // bytes of eight tokens
   const int64_t boxes = (mine + kBoxRows - 1) / kBoxRows;
-  const uint32_t x_box = (uint32_t)(kBoxRows * 8 * lpr) * (XF32 ? 4u : 2u);
-  const uint32_t d_box = (uint32_t)(kBoxRows * 8 * lpr) * (DF32 ? 4u : 2u);
-  const uint8_t* d_slab = slab + boxes * x_box;
+  const uint32_t x_box = (uint32_t)(kBoxRows * lpr * x_piece), d_box = (uint32_t)(kBoxRows * lpr * d_piece);
+  uint8_t* d_slab = slab + boxes * x_box;
+  const uint8_t* x_at = slab + (first * lpr + col8) * x_piece;
+  const uint8_t* d_at = d_slab + (first * lpr + col8) * d_piece;
+  const int stride = step * lpr;  // pieces between this thread's rows
   bool ok = true;
   if (CACHED && threadIdx.x % 32 == 0 && boxes > 0) {
     if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar, (uint32_t)boxes * (x_box + d_box));
     load_slab(slab, &p.tm_x, &bar, tile * (8 * lpr), r0, boxes, x_box);
-    load_slab(slab + boxes * x_box, &p.tm_d, &bar, tile * (8 * lpr), r0, boxes, d_box);
+    load_slab(d_slab, &p.tm_d, &bar, tile * (8 * lpr), r0, boxes, d_box);
   }
-  float mean[8], rs[8];
+  F2 mean[4], rs[4];  // the mean negated
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    mean[j] = j < valid ? __ldg(p.mean + t0 + j) : 0.f;
-    rs[j] = j < valid ? __ldg(p.rstd + t0 + j) : 0.f;
+  for (int j = 0; j < 4; ++j) {
+    const bool a = 2 * j < valid, b = 2 * j + 1 < valid;
+    mean[j] = f2(a ? -__ldg(p.mean + t0 + 2 * j) : 0.f, b ? -__ldg(p.mean + t0 + 2 * j + 1) : 0.f);
+    rs[j] = f2(a ? __ldg(p.rstd + t0 + 2 * j) : 0.f, b ? __ldg(p.rstd + t0 + 2 * j + 1) : 0.f);
   }
   if (CACHED && boxes > 0) ok = mbar_wait(&bar, 0, &abort_flag, p.status, kWaitNs);
-  auto x_row = [&](int64_t k) {
-    if (CACHED) return shared_piece<XF32>(slab, (k - r0) * (8 * lpr) + 8 * col8);
-    return load_piece<XF32>(p.X, k * p.ldx + t0, valid);
+  auto x_row = [&](int k, int i, F2 (&f)[4]) {
+    if (CACHED)
+      load_shared<XF32>(x_at + (int64_t)i * stride * x_piece, f);
+    else
+      load_global<XF32>(p.X, (r0 + k) * p.ldx + t0, valid, f);
   };
-  auto d_row = [&](int64_t k) {
-    if (CACHED) return shared_piece<DF32>(d_slab, (k - r0) * (8 * lpr) + 8 * col8);
-    return load_piece<DF32>(p.dY, k * p.ldy + t0, valid);
+  auto d_row = [&](int k, int i, F2 (&f)[4]) {
+    if (CACHED)
+      load_shared<DF32>(d_at + (int64_t)i * stride * d_piece, f);
+    else
+      load_global<DF32>(p.dY, (r0 + k) * p.ldy + t0, valid, f);
   };
 
-  float c1[8] = {0, 0, 0, 0, 0, 0, 0, 0}, c2[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  const int64_t trips = (mine + step - 1) / step;  // the same for every thread: the row sums shuffle
+  const F2 zero = f2(0.f, 0.f);
+  F2 c[2][4] = {{zero, zero, zero, zero}, {zero, zero, zero, zero}};
+  const int trips = (mine + step - 1) / step;  // the same for every thread: the row sums shuffle
+  float* part = p.part + tile * 2 * p.K + r0;
 #pragma unroll 2
-  for (int64_t i = 0; i < trips; ++i) {
-    const int64_t k = first + i * step;
-    float dg = 0.f, db = 0.f;
-    if (k < r1) {
-      float f[8], e[8];
-      unpack<XF32>(x_row(k), f);
-      unpack<DF32>(d_row(k), e);
-      const float g = p.gamma ? __ldg(p.gamma + k) : 1.f;
+  for (int i = 0; i < trips; ++i) {
+    const int k = first + i * step;
+    F2 dg = zero, db = zero;
+    if (k < mine) {
+      F2 f[4], e[4];
+      const float g = p.gamma ? __ldg(p.gamma + r0 + k) : 1.f;
+      const F2 g2 = f2(g, g);
+      x_row(k, i, f);
+      d_row(k, i, e);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float h = (f[j] - mean[j]) * rs[j];  // 0 past T: rs is 0 there
-        c1[j] += g * e[j];
-        c2[j] += g * e[j] * h;
-        dg += e[j] * h;
-        db += e[j];
+      for (int j = 0; j < 4; ++j) {
+        const F2 h = mul2(add2(f[j], mean[j]), rs[j]);  // 0 past T: rs is 0 there
+        const F2 ge = mul2(g2, e[j]);
+        c[0][j] = add2(c[0][j], ge);
+        c[1][j] = fma2(ge, h, c[1][j]);
+        dg = fma2(e[j], h, dg);
+        db = add2(db, e[j]);
       }
     }
     if (p.part) {
+      float a, b, u, v;
+      split(dg, a, b);
+      split(db, u, v);
+      a += b;
+      u += v;
       for (int o = lpr >> 1; o > 0; o >>= 1) {
-        dg += __shfl_xor_sync(0xFFFFFFFFu, dg, o);
-        db += __shfl_xor_sync(0xFFFFFFFFu, db, o);
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
       }
-      if (ok && col8 == 0 && k < r1) {
-        p.part[tile * 2 * p.K + k] = dg;
-        p.part[tile * 2 * p.K + p.K + k] = db;
+      if (ok && col8 == 0 && k < mine) {
+        part[k] = a;
+        part[p.K + k] = u;
       }
     }
   }
-  column_sums(c1, lpr, scratch, s_c1);
-  column_sums(c2, lpr, scratch, s_c2);
+  column_sums<2>(c, lpr, scratch, s_c);
   if (C > 1) cluster_sync();
-  if ((int)threadIdx.x < lpr * 8) {
-    float a = 0.f, b = 0.f;
-    if (C > 1) {
-      for (int c = 0; c < C; ++c) {
-        a += ld_cluster(s_c1 + threadIdx.x, c);
-        b += ld_cluster(s_c2 + threadIdx.x, c);
+  {
+    const int n = threadIdx.x / kMaxCols, t = threadIdx.x % kMaxCols;
+    if (n < 2 && t < lpr * 8) {
+      float total = s_c[n][t];
+      if (C > 1) {
+        float a[kMaxCluster];
+        ld_cluster_all(&s_c[n][t], C, a);
+        total = 0.f;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) total += a[q];
       }
-    } else {
-      a = s_c1[threadIdx.x];
-      b = s_c2[threadIdx.x];
+      t_c[n][t] = -total / (float)p.K;
     }
-    t_c1[threadIdx.x] = a / (float)p.K;
-    t_c2[threadIdx.x] = b / (float)p.K;
   }
+  if (C > 1) cluster_arrive();  // done with the other CTAs' sums
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    c1[j] = t_c1[8 * col8 + j];
-    c2[j] = t_c2[8 * col8 + j];
-  }
-  if (ok && valid > 0) {
-#pragma unroll 2
-    for (int64_t k = first; k < r1; k += step) {
-      float f[8], e[8];
-      unpack<XF32>(x_row(k), f);
-      unpack<DF32>(d_row(k), e);
-      const float g = p.gamma ? __ldg(p.gamma + k) : 1.f;
+  for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float h = (f[j] - mean[j]) * rs[j];
-        f[j] = rs[j] * (g * e[j] - (c1[j] + h * c2[j]));
+    for (int j = 0; j < 4; ++j) c[n][j] = f2(t_c[n][8 * col8 + 2 * j], t_c[n][8 * col8 + 2 * j + 1]);
+  if (ok && valid > 0) {
+    int64_t out = (r0 + first) * p.ldo + t0;
+#pragma unroll 2
+    for (int k = first, i = 0; k < mine; k += step, ++i, out += step * p.ldo) {
+      F2 f[4], e[4];
+      const float g = p.gamma ? __ldg(p.gamma + r0 + k) : 1.f;
+      const F2 g2 = f2(g, g);
+      x_row(k, i, f);
+      d_row(k, i, e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const F2 h = mul2(add2(f[j], mean[j]), rs[j]);
+        f[j] = mul2(rs[j], add2(mul2(g2, e[j]), fma2(h, c[1][j], c[0][j])));
       }
-      store_piece(p.Y, k * p.ldo + t0, XF32, valid, f);
+      store_piece(p.Y, out, XF32, valid, f);
     }
   }
-  if (C > 1) cluster_sync();
+  if (C > 1) cluster_wait();
 }
 
 // dgamma[k] and dbeta[k]: the strips' partials added in strip order (a fixed
@@ -433,19 +503,19 @@ __global__ void __launch_bounds__(1024) norm_grad_reduce_kernel(const float* par
   }
 }
 
-// Strip width, cluster size and rows per CTA, from the bytes of one row element (X, and dY in the backward
-// pass).  The widest strip (64 tokens: whole 128-byte lines of bf16) whose slab fits a quarter of an SM in a cluster of
-// eight; for larger K strips of 16 tokens (whole 32-byte sectors) that fit at all, then of 8; past that nothing is cached.  Then
-// the smallest cluster that keeps the slab there, enlarged while the grid leaves SMs idle.
+// Strip width, cluster size and rows per CTA, from the bytes of one element (X's type, and dY's in the backward pass).
+// Strips of 32 tokens (64 bytes of bf16: whole DRAM bursts; 64-token strips need twice the cluster, whose
+// synchronisation cost more than their wider rows gained), narrower for few tokens and for a K whose slab leaves a
+// quarter of an SM in a cluster of eight; for larger K strips of 16 tokens that fit at all, then of 8; past that nothing
+// is cached.  Then the smallest cluster that keeps the slab there, enlarged while the grid leaves SMs idle.
 void norm_shape(NormParams& p, int64_t bytes) {
   using namespace norm;
   auto slab = [&](int l, int c) {
     const int64_t rows = (p.K + c - 1) / c;
     return (rows + kBoxRows - 1) / kBoxRows * kBoxRows * 8 * l * bytes;
   };
-  int widest = 8;
-  while (widest > 1 && (int64_t)(widest / 2) * 8 >= p.T) widest >>= 1;
-  int lpr = widest;
+  int lpr = 4;
+  while (lpr > 1 && (int64_t)(lpr / 2) * 8 >= p.T) lpr >>= 1;
   int64_t limit = kSlabBytes;
   while (lpr > 2 && slab(lpr, kMaxCluster) > limit) lpr >>= 1;
   if (slab(lpr, kMaxCluster) > limit) limit = kMaxSlabBytes;
