@@ -13,11 +13,14 @@
 // operations per byte the kernels are bound by memory, so the strip is read
 // from HBM once: a CTA's slab comes into shared memory by TMA boxes, issued
 // before anything else (past T and K they fill zeros, so ragged edges need no
-// element loads), and the passes over it read shared memory.  The slab is kept
-// to a quarter of the SM's shared memory where a cluster of eight allows it:
-// the four CTAs of an SM are then in different phases, and loads, sums and
-// stores overlap.  (Holding the rows in registers instead left one CTA per SM,
-// 160 registers a thread: 105 us against the floor of 24 us on 768 x 50432.)
+// element loads), and the passes over it read shared memory.  A slab takes at
+// most half of the SM's shared memory where a cluster of eight allows it, so
+// that one CTA loads while the other computes.  Arithmetic is in packed float32
+// pairs.  768 x 50432 takes 35 us forward (floor 24 us) and 78 us backward
+// (36 us), bound by instruction issue: three passes over a piece of eight
+// tokens unpack it each time.  Tried and slower: persistent clusters that fetch
+// the next strip while they work on one (57 and 93 us), 512 threads a CTA (40
+// and 90 us), rows held in registers with one CTA to an SM (105 us forward).
 // Column sums go lanes -> warps -> CTA, and across the cluster through
 // distributed shared memory, every addition in a fixed order.  The forward
 // pass takes each CTA's own mean first and the squares about that, and joins
@@ -27,6 +30,7 @@
 // A K too large for a cluster's shared memory reads the strip from global
 // memory in every pass (CACHED = false).
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "nm_host.h"
@@ -41,9 +45,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCols = 64;  // tokens of a strip, at most (eight lanes of eight)
 constexpr int kMaxCluster = 8;
-constexpr int kBoxRows = 32;                     // rows of a TMA box (slabs are whole boxes)
-constexpr int64_t kSlabBytes = 52 * 1024;        // four CTAs of an SM
-constexpr int64_t kMaxSlabBytes = 216 * 1024;    // one CTA
+constexpr int64_t kSlabBytes = 104 * 1024;     // with gamma and beta: two CTAs to an SM
+constexpr int64_t kMaxSlabBytes = 216 * 1024;  // one
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Two float32 values, worked on by the packed float32 instructions (one issue for both).
@@ -124,13 +127,15 @@ __device__ __forceinline__ void load_shared(const uint8_t* at, F2 (&f)[4]) {
   }
 }
 
-__device__ __forceinline__ void store_piece(void* base, int64_t off, bool f32, int valid, const F2 (&p)[4]) {
+// Eight tokens to global memory: WHOLE, or the first `valid` of them one by one.
+template <bool F32, bool WHOLE>
+__device__ __forceinline__ void store_piece(uint8_t* at, int valid, const F2 (&p)[4]) {
   float f[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) split(p[j], f[2 * j], f[2 * j + 1]);
-  if (f32) {
-    float* d = static_cast<float*>(base) + off;
-    if (valid >= 8) {
+  if (F32) {
+    float* d = reinterpret_cast<float*>(at);
+    if (WHOLE) {
       reinterpret_cast<float4*>(d)[0] = make_float4(f[0], f[1], f[2], f[3]);
       reinterpret_cast<float4*>(d)[1] = make_float4(f[4], f[5], f[6], f[7]);
     } else {
@@ -139,11 +144,11 @@ __device__ __forceinline__ void store_piece(void* base, int64_t off, bool f32, i
         if (j < valid) d[j] = f[j];
     }
   } else {
-    uint16_t* d = static_cast<uint16_t*>(base) + off;
+    uint16_t* d = reinterpret_cast<uint16_t*>(at);
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
-    if (valid >= 8) {
+    if (WHOLE) {
       *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
@@ -197,88 +202,111 @@ __device__ __forceinline__ void ld_cluster_all(const float* local, int C, float 
   for (int c = 0; c < kMaxCluster; ++c) v[c] = c < C ? ld_cluster(local, c) : 0.f;
 }
 
+// n rows, U of them at a time with nothing between their loads, then one by one: body(index of the first,
+// integral_constant U or 1).
+template <int U, typename Body>
+__device__ __forceinline__ void each_row(int n, Body body) {
+  int i = 0;
+  for (; i + U <= n; i += U) body(i, std::integral_constant<int, U>());
+  for (; i < n; ++i) body(i, std::integral_constant<int, 1>());
+}
+
 // Brings `rows` rows from row r0 of a K x T tensor, columns t .. t + 8 lpr, into shared memory as rows of
-// 8 lpr elements (boxes of kBoxRows rows; the last box may reach into rows of the next slab or past K).  The first
+// 8 lpr elements (boxes of box_rows rows; the last box may reach into rows of the next slab or past K).  The first
 // lane of every warp calls it and issues its share of the boxes.
 __device__ __forceinline__ void load_slab(uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int64_t t, int64_t r0,
-                                          int64_t boxes, uint32_t box_bytes) {
+                                          int64_t boxes, int box_rows, uint32_t box_bytes) {
   for (int64_t b = threadIdx.x >> 5; b < boxes; b += kWarps)
-    tma_load_2d(dst + b * box_bytes, tm, bar, (int32_t)t, (int32_t)(r0 + b * kBoxRows));
+    tma_load_2d(dst + b * box_bytes, tm, bar, (int32_t)t, (int32_t)(r0 + b * box_rows));
 }
 }  // namespace norm
 
-template <bool XF32, bool CACHED>
-__global__ void __launch_bounds__(norm::kThreads, 4) norm_kernel(const __grid_constant__ NormParams p) {
+template <bool XF32, bool YF32, bool CACHED>
+__global__ void __launch_bounds__(norm::kThreads, 2) norm_kernel(const __grid_constant__ NormParams p) {
   using namespace norm;
-  extern __shared__ __align__(128) uint8_t slab[];
+  extern __shared__ __align__(128) uint8_t smem[];  // the slab, then (gamma, beta) of every row
   __shared__ float scratch[kWarps * kMaxCols];
   __shared__ float s_mean[1][kMaxCols], s_m2[1][kMaxCols], s_rstd[kMaxCols], t_mean[kMaxCols];
   __shared__ uint64_t bar;
   __shared__ int abort_flag;
   const uint32_t rank = cluster_ctarank();
   const int C = p.cluster, lpr = p.lpr;
-  const int64_t tile = blockIdx.x / C;
   const int64_t r0 = rank * p.rows;
   const int mine = (int)(r0 < p.K ? (p.K - r0 < p.rows ? p.K - r0 : p.rows) : 0);  // rows of this CTA
   const int col8 = threadIdx.x % lpr;
   const int step = kThreads / lpr;
   const int first = threadIdx.x / lpr;
-  const int64_t t0 = tile * (8 * lpr) + 8 * col8;
-  const int valid = t0 >= p.T ? 0 : (p.T - t0 < 8 ? (int)(p.T - t0) : 8);
+  const int n = first < mine ? (mine - first + step - 1) / step : 0;  // rows of this thread: first, + step, ...
   if (CACHED && threadIdx.x == 0) {
     mbar_init(&bar, 1);
     abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
   }
-  if (CACHED) __syncthreads();
+  __syncthreads();
   pdl_gate();
   bool ok = true;
-  const int piece = XF32 ? 32 : 16;  // bytes of eight tokens
-  const uint8_t* mine_at = slab + (first * lpr + col8) * piece;
-  const int stride = step * lpr * piece;  // bytes between this thread's rows
-  if (CACHED) {
-    const int64_t boxes = (mine + kBoxRows - 1) / kBoxRows;
-    const uint32_t box_bytes = (uint32_t)(kBoxRows * lpr * piece);
-    if (threadIdx.x % 32 == 0 && boxes > 0) {
-      if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar, (uint32_t)boxes * box_bytes);
-      load_slab(slab, &p.tm_x, &bar, tile * (8 * lpr), r0, boxes, box_bytes);
-    }
-    if (boxes > 0) ok = mbar_wait(&bar, 0, &abort_flag, p.status, kWaitNs);
+  constexpr int kX = XF32 ? 32 : 16, kY = YF32 ? 32 : 16;  // bytes of eight tokens
+  const int boxes = (mine + p.box_rows - 1) / p.box_rows;
+  const uint32_t box_bytes = (uint32_t)(p.box_rows * lpr * kX);
+  const int64_t tile = blockIdx.x / C;
+  const int64_t t0 = tile * (8 * lpr) + 8 * col8;
+  const int valid = t0 >= p.T ? 0 : (p.T - t0 < 8 ? (int)(p.T - t0) : 8);
+  if (CACHED && threadIdx.x % 32 == 0 && boxes > 0) {
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar, (uint32_t)boxes * box_bytes);
+    load_slab(smem, &p.tm_x, &bar, tile * (8 * lpr), r0, boxes, p.box_rows, box_bytes);
   }
-  // Row `k` of the slab, the i-th of this thread: its eight tokens (zeros past T).
-  auto row = [&](int k, int i, F2 (&f)[4]) {
+  float2* s_affine = reinterpret_cast<float2*>(smem + p.slab);
+  auto affine = [&](int k) {
+    const float g = p.gamma ? __ldg(p.gamma + r0 + k) : 1.f, b = p.beta ? __ldg(p.beta + r0 + k) : 0.f;
+    return make_float2(g, b);
+  };
+  if (CACHED)
+    for (int k = threadIdx.x; k < mine; k += kThreads) s_affine[k] = affine(k);  // read after the first __syncthreads
+
+  if (CACHED && boxes > 0) ok = mbar_wait(&bar, 0, &abort_flag, p.status, kWaitNs);
+  const uint8_t* x_at = smem + (first * lpr + col8) * kX;
+  constexpr int kXStep = kThreads * kX;  // bytes between this thread's rows
+  // The i-th row of this thread: its eight tokens (zeros past T).
+  auto row = [&](int i, F2 (&f)[4]) {
     if (CACHED)
-      load_shared<XF32>(mine_at + (int64_t)i * stride, f);
+      load_shared<XF32>(x_at + i * kXStep, f);
     else
-      load_global<XF32>(p.X, (r0 + k) * p.ldx + t0, valid, f);
+      load_global<XF32>(p.X, (r0 + first + (int64_t)i * step) * p.ldx + t0, valid, f);
   };
 
   const F2 zero = f2(0.f, 0.f);
   F2 sum[1][4] = {{zero, zero, zero, zero}};
-#pragma unroll 4
-  for (int k = first, i = 0; k < mine; k += step, ++i) {
-    F2 f[4];
-    row(k, i, f);
+  each_row<4>(n, [&](int i, auto u) {
+    constexpr int U = decltype(u)::value;
+    F2 f[U][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sum[0][j] = add2(sum[0][j], f[j]);
-  }
+    for (int r = 0; r < U; ++r) row(i + r, f[r]);
+#pragma unroll
+    for (int r = 0; r < U; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[0][j] = add2(sum[0][j], f[r][j]);
+  });
   column_sums<1>(sum, lpr, scratch, s_mean);
   // this CTA's own mean, negated: the squares are taken about it
   const float per = mine > 0 ? 1.0f / (float)mine : 0.f;
   F2 m[4], sq[1][4] = {{zero, zero, zero, zero}};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) m[j] = f2(-(s_mean[0][8 * col8 + 2 * j] * per), -(s_mean[0][8 * col8 + 2 * j + 1] * per));
-#pragma unroll 4
-  for (int k = first, i = 0; k < mine; k += step, ++i) {
-    F2 f[4];
-    row(k, i, f);
+  for (int j = 0; j < 4; ++j)
+    m[j] = f2(-(s_mean[0][8 * col8 + 2 * j] * per), -(s_mean[0][8 * col8 + 2 * j + 1] * per));
+  each_row<4>(n, [&](int i, auto u) {
+    constexpr int U = decltype(u)::value;
+    F2 f[U][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const F2 d = add2(f[j], m[j]);
-      sq[0][j] = fma2(d, d, sq[0][j]);
-    }
-  }
+    for (int r = 0; r < U; ++r) row(i + r, f[r]);
+#pragma unroll
+    for (int r = 0; r < U; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const F2 d = add2(f[r][j], m[j]);
+        sq[0][j] = fma2(d, d, sq[0][j]);
+      }
+  });
   column_sums<1>(sq, lpr, scratch, s_m2);
   if (C > 1) cluster_sync();  // every CTA's s_mean (sums) and s_m2 are written
   if ((int)threadIdx.x < lpr * 8) {
@@ -296,9 +324,9 @@ __global__ void __launch_bounds__(norm::kThreads, 4) norm_kernel(const __grid_co
       for (int c = 0; c < kMaxCluster; ++c) {
         if (c >= C) continue;
         const int64_t at = c * p.rows;
-        const float n = (float)(at < p.K ? (p.K - at < p.rows ? p.K - at : p.rows) : 0);
-        const float d = n > 0.f ? a[c] * (1.0f / n) - mean : 0.f;
-        m2 += q[c] + n * d * d;
+        const float rows = (float)(at < p.K ? (p.K - at < p.rows ? p.K - at : p.rows) : 0);
+        const float d = rows > 0.f ? a[c] * (1.0f / rows) - mean : 0.f;
+        m2 += q[c] + rows * d * d;
       }
     }
     const float rstd = 1.0f / sqrtf(m2 / (float)p.K + p.eps);
@@ -318,61 +346,78 @@ __global__ void __launch_bounds__(norm::kThreads, 4) norm_kernel(const __grid_co
     m[j] = f2(-t_mean[8 * col8 + 2 * j], -t_mean[8 * col8 + 2 * j + 1]);
     rs[j] = f2(s_rstd[8 * col8 + 2 * j], s_rstd[8 * col8 + 2 * j + 1]);
   }
-  if (ok && valid > 0) {
-    int64_t out = (r0 + first) * p.ldy + t0;
-#pragma unroll 4
-    for (int k = first, i = 0; k < mine; k += step, ++i, out += step * p.ldy) {
-      F2 f[4];
-      const float g = p.gamma ? __ldg(p.gamma + r0 + k) : 1.f, b = p.beta ? __ldg(p.beta + r0 + k) : 0.f;
-      const F2 g2 = f2(g, g), b2 = f2(b, b);
-      row(k, i, f);
+  uint8_t* out = static_cast<uint8_t*>(p.Y) + ((r0 + first) * p.ldy + t0) * (kY / 8);
+  const int64_t out_step = step * p.ldy * (kY / 8);
+  auto write = [&](auto whole) {
+    each_row<2>(n, [&](int i, auto u) {
+      constexpr int U = decltype(u)::value;
+      F2 f[U][4];
+      float2 a[U];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = fma2(mul2(add2(f[j], m[j]), rs[j]), g2, b2);
-      store_piece(p.Y, out, p.y_f32 != 0, valid, f);
-    }
-  }
-  if (C > 1) cluster_wait();  // no CTA leaves while another still reads its shared memory
+      for (int r = 0; r < U; ++r) {
+        a[r] = CACHED ? s_affine[first + (i + r) * step] : affine(first + (i + r) * step);
+        row(i + r, f[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < U; ++r) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          f[r][j] = fma2(mul2(add2(f[r][j], m[j]), rs[j]), f2(a[r].x, a[r].x), f2(a[r].y, a[r].y));
+        store_piece<YF32, decltype(whole)::value>(out, valid, f[r]);
+        out += out_step;
+      }
+    });
+  };
+  if (ok && valid == 8)
+    write(std::true_type());
+  else if (ok && valid > 0)
+    write(std::false_type());
+  if (C > 1) cluster_wait();  // the other CTAs have read this one's sums
 }
 
 template <bool XF32, bool DF32, bool CACHED>
-__global__ void __launch_bounds__(norm::kThreads, 3) norm_grad_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(norm::kThreads, 2) norm_grad_kernel(const __grid_constant__ NormParams p) {
   using namespace norm;
-  extern __shared__ __align__(128) uint8_t slab[];  // X's rows, then dY's
+  extern __shared__ __align__(128) uint8_t smem[];  // X's slab, dY's, then gamma of every row
   __shared__ float scratch[2 * kWarps * kMaxCols];
   __shared__ float s_c[2][kMaxCols], t_c[2][kMaxCols];
   __shared__ uint64_t bar;
   __shared__ int abort_flag;
   const uint32_t rank = cluster_ctarank();
   const int C = p.cluster, lpr = p.lpr;
-  const int64_t tile = blockIdx.x / C;
   const int64_t r0 = rank * p.rows;
   const int mine = (int)(r0 < p.K ? (p.K - r0 < p.rows ? p.K - r0 : p.rows) : 0);  // rows of this CTA
   const int col8 = threadIdx.x % lpr;
   const int step = kThreads / lpr;
   const int first = threadIdx.x / lpr;
-  const int64_t t0 = tile * (8 * lpr) + 8 * col8;
-  const int valid = t0 >= p.T ? 0 : (p.T - t0 < 8 ? (int)(p.T - t0) : 8);
+  const int n = first < mine ? (mine - first + step - 1) / step : 0;  // rows of this thread: first, + step, ...
+  const int turns = (mine + step - 1) / step;                         // of any thread, at most
   if (CACHED && threadIdx.x == 0) {
     mbar_init(&bar, 1);
     abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
   }
-  if (CACHED) __syncthreads();
+  __syncthreads();
   pdl_gate();
-  const int x_piece = XF32 ? 32 : 16, d_piece = DF32 ? 32 : 16;  // bytes of eight tokens
-  const int64_t boxes = (mine + kBoxRows - 1) / kBoxRows;
-  const uint32_t x_box = (uint32_t)(kBoxRows * lpr * x_piece), d_box = (uint32_t)(kBoxRows * lpr * d_piece);
-  uint8_t* d_slab = slab + boxes * x_box;
-  const uint8_t* x_at = slab + (first * lpr + col8) * x_piece;
-  const uint8_t* d_at = d_slab + (first * lpr + col8) * d_piece;
-  const int stride = step * lpr;  // pieces between this thread's rows
+  constexpr int kX = XF32 ? 32 : 16, kD = DF32 ? 32 : 16;  // bytes of eight tokens
+  const int boxes = (mine + p.box_rows - 1) / p.box_rows;
+  const uint32_t x_box = (uint32_t)(p.box_rows * lpr * kX), d_box = (uint32_t)(p.box_rows * lpr * kD);
   bool ok = true;
+  const int64_t tile = blockIdx.x / C;
+  const int64_t t0 = tile * (8 * lpr) + 8 * col8;
+  const int valid = t0 >= p.T ? 0 : (p.T - t0 < 8 ? (int)(p.T - t0) : 8);
   if (CACHED && threadIdx.x % 32 == 0 && boxes > 0) {
     if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar, (uint32_t)boxes * (x_box + d_box));
-    load_slab(slab, &p.tm_x, &bar, tile * (8 * lpr), r0, boxes, x_box);
-    load_slab(d_slab, &p.tm_d, &bar, tile * (8 * lpr), r0, boxes, d_box);
+    load_slab(smem, &p.tm_x, &bar, tile * (8 * lpr), r0, boxes, p.box_rows, x_box);
+    load_slab(smem + boxes * x_box, &p.tm_d, &bar, tile * (8 * lpr), r0, boxes, p.box_rows, d_box);
   }
+  float* s_gamma = reinterpret_cast<float*>(smem + p.slab);
+  auto gamma = [&](int k) { return p.gamma ? __ldg(p.gamma + r0 + k) : 1.f; };
+  if (CACHED)
+    for (int k = threadIdx.x; k < mine; k += kThreads) s_gamma[k] = gamma(k);
+  __syncthreads();
+
   F2 mean[4], rs[4];  // the mean negated
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -381,99 +426,127 @@ __global__ void __launch_bounds__(norm::kThreads, 3) norm_grad_kernel(const __gr
     rs[j] = f2(a ? __ldg(p.rstd + t0 + 2 * j) : 0.f, b ? __ldg(p.rstd + t0 + 2 * j + 1) : 0.f);
   }
   if (CACHED && boxes > 0) ok = mbar_wait(&bar, 0, &abort_flag, p.status, kWaitNs);
-  auto x_row = [&](int k, int i, F2 (&f)[4]) {
-    if (CACHED)
-      load_shared<XF32>(x_at + (int64_t)i * stride * x_piece, f);
-    else
-      load_global<XF32>(p.X, (r0 + k) * p.ldx + t0, valid, f);
-  };
-  auto d_row = [&](int k, int i, F2 (&f)[4]) {
-    if (CACHED)
-      load_shared<DF32>(d_at + (int64_t)i * stride * d_piece, f);
-    else
-      load_global<DF32>(p.dY, (r0 + k) * p.ldy + t0, valid, f);
+  const uint8_t* x_at = smem + (first * lpr + col8) * kX;
+  const uint8_t* d_at = smem + boxes * x_box + (first * lpr + col8) * kD;
+  auto rows = [&](int i, F2 (&f)[4], F2 (&e)[4]) {
+    if (CACHED) {
+      load_shared<XF32>(x_at + i * (kThreads * kX), f);
+      load_shared<DF32>(d_at + i * (kThreads * kD), e);
+    } else {
+      const int64_t k = r0 + first + (int64_t)i * step;
+      load_global<XF32>(p.X, k * p.ldx + t0, valid, f);
+      load_global<DF32>(p.dY, k * p.ldy + t0, valid, e);
+    }
   };
 
   const F2 zero = f2(0.f, 0.f);
   F2 c[2][4] = {{zero, zero, zero, zero}, {zero, zero, zero, zero}};
-  const int trips = (mine + step - 1) / step;  // the same for every thread: the row sums shuffle
-  float* part = p.part + tile * 2 * p.K + r0;
-#pragma unroll 2
-  for (int i = 0; i < trips; ++i) {
-    const int k = first + i * step;
-    F2 dg = zero, db = zero;
-    if (k < mine) {
-      F2 f[4], e[4];
-      const float g = p.gamma ? __ldg(p.gamma + r0 + k) : 1.f;
-      const F2 g2 = f2(g, g);
-      x_row(k, i, f);
-      d_row(k, i, e);
+  // One row's terms of the column sums, and its own sums over the eight tokens.
+  auto take = [&](const F2 (&f)[4], const F2 (&e)[4], float g, float& dg, float& db) {
+    const F2 g2 = f2(g, g);
+    F2 a = zero, b = zero;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const F2 h = mul2(add2(f[j], mean[j]), rs[j]);  // 0 past T: rs is 0 there
-        const F2 ge = mul2(g2, e[j]);
-        c[0][j] = add2(c[0][j], ge);
-        c[1][j] = fma2(ge, h, c[1][j]);
-        dg = fma2(e[j], h, dg);
-        db = add2(db, e[j]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const F2 h = mul2(add2(f[j], mean[j]), rs[j]);  // 0 past T: rs is 0 there
+      const F2 ge = mul2(g2, e[j]);
+      c[0][j] = add2(c[0][j], ge);
+      c[1][j] = fma2(ge, h, c[1][j]);
+      a = fma2(e[j], h, a);
+      b = add2(b, e[j]);
     }
-    if (p.part) {
-      float a, b, u, v;
-      split(dg, a, b);
-      split(db, u, v);
-      a += b;
-      u += v;
-      for (int o = lpr >> 1; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
-      }
-      if (ok && col8 == 0 && k < mine) {
-        part[k] = a;
-        part[p.K + k] = u;
-      }
+    float lo, hi;
+    split(a, lo, hi);
+    dg = lo + hi;
+    split(b, lo, hi);
+    db = lo + hi;
+  };
+  float* part = p.part + tile * 2 * p.K + r0;
+  auto keep = [&](int i, float dg, float db) {  // the sums of row first + i * step; every lane takes part
+    for (int o = lpr >> 1; o > 0; o >>= 1) {
+      dg += __shfl_xor_sync(0xFFFFFFFFu, dg, o);
+      db += __shfl_xor_sync(0xFFFFFFFFu, db, o);
     }
+    if (col8 != 0 || i >= n) return;
+    const int k = first + i * step;
+    part[k] = dg;
+    part[p.K + k] = db;
+  };
+  const bool sums = p.part != nullptr;
+  // Turns taken two at a time: those in which every lane of the warp has its rows.
+  const int both = CACHED && __all_sync(0xFFFFFFFFu, n == turns) ? turns / 2 * 2 : 0;
+  for (int i = 0; i < both; i += 2) {
+    F2 f[2][4], e[2][4];
+    float dg[2], db[2];
+    rows(i, f[0], e[0]);
+    rows(i + 1, f[1], e[1]);
+    take(f[0], e[0], s_gamma[first + i * step], dg[0], db[0]);
+    take(f[1], e[1], s_gamma[first + (i + 1) * step], dg[1], db[1]);
+    if (sums) {
+      keep(i, dg[0], db[0]);
+      keep(i + 1, dg[1], db[1]);
+    }
+  }
+  for (int i = both; i < turns; ++i) {
+    float dg = 0.f, db = 0.f;
+    if (i < n) {
+      F2 f[4], e[4];
+      rows(i, f, e);
+      take(f, e, gamma(first + i * step), dg, db);
+    }
+    if (sums) keep(i, dg, db);
   }
   column_sums<2>(c, lpr, scratch, s_c);
   if (C > 1) cluster_sync();
   {
-    const int n = threadIdx.x / kMaxCols, t = threadIdx.x % kMaxCols;
-    if (n < 2 && t < lpr * 8) {
-      float total = s_c[n][t];
+    const int q = threadIdx.x / kMaxCols, t = threadIdx.x % kMaxCols;
+    if (q < 2 && t < lpr * 8) {
+      float total = s_c[q][t];
       if (C > 1) {
         float a[kMaxCluster];
-        ld_cluster_all(&s_c[n][t], C, a);
+        ld_cluster_all(&s_c[q][t], C, a);
         total = 0.f;
 #pragma unroll
-        for (int q = 0; q < kMaxCluster; ++q) total += a[q];
+        for (int u = 0; u < kMaxCluster; ++u) total += a[u];
       }
-      t_c[n][t] = -total / (float)p.K;
+      t_c[q][t] = -total / (float)p.K;
     }
   }
   if (C > 1) cluster_arrive();  // done with the other CTAs' sums
   __syncthreads();
 #pragma unroll
-  for (int n = 0; n < 2; ++n)
+  for (int q = 0; q < 2; ++q)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c[n][j] = f2(t_c[n][8 * col8 + 2 * j], t_c[n][8 * col8 + 2 * j + 1]);
-  if (ok && valid > 0) {
-    int64_t out = (r0 + first) * p.ldo + t0;
-#pragma unroll 2
-    for (int k = first, i = 0; k < mine; k += step, ++i, out += step * p.ldo) {
-      F2 f[4], e[4];
-      const float g = p.gamma ? __ldg(p.gamma + r0 + k) : 1.f;
-      const F2 g2 = f2(g, g);
-      x_row(k, i, f);
-      d_row(k, i, e);
+    for (int j = 0; j < 4; ++j) c[q][j] = f2(t_c[q][8 * col8 + 2 * j], t_c[q][8 * col8 + 2 * j + 1]);
+  uint8_t* out = static_cast<uint8_t*>(p.Y) + ((r0 + first) * p.ldo + t0) * (kX / 8);
+  const int64_t out_step = step * p.ldo * (kX / 8);
+  auto write = [&](auto whole) {
+    each_row<2>(n, [&](int i, auto u) {
+      constexpr int U = decltype(u)::value;
+      F2 f[U][4], e[U][4];
+      float g[U];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const F2 h = mul2(add2(f[j], mean[j]), rs[j]);
-        f[j] = mul2(rs[j], add2(mul2(g2, e[j]), fma2(h, c[1][j], c[0][j])));
+      for (int r = 0; r < U; ++r) {
+        g[r] = CACHED ? s_gamma[first + (i + r) * step] : gamma(first + (i + r) * step);
+        rows(i + r, f[r], e[r]);
       }
-      store_piece(p.Y, out, XF32, valid, f);
-    }
-  }
-  if (C > 1) cluster_wait();
+#pragma unroll
+      for (int r = 0; r < U; ++r) {
+        const F2 g2 = f2(g[r], g[r]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const F2 h = mul2(add2(f[r][j], mean[j]), rs[j]);
+          f[r][j] = mul2(rs[j], fma2(g2, e[r][j], fma2(h, c[1][j], c[0][j])));
+        }
+        store_piece<XF32, decltype(whole)::value>(out, valid, f[r]);
+        out += out_step;
+      }
+    });
+  };
+  if (ok && valid == 8)
+    write(std::true_type());
+  else if (ok && valid > 0)
+    write(std::false_type());
+  if (C > 1) cluster_wait();  // the other CTAs have read this one's sums
 }
 
 // dgamma[k] and dbeta[k]: the strips' partials added in strip order (a fixed
@@ -504,36 +577,41 @@ __global__ void __launch_bounds__(1024) norm_grad_reduce_kernel(const float* par
 }
 
 // Strip width, cluster size and rows per CTA, from the bytes of one element (X's type, and dY's in the backward pass).
-// Strips of 32 tokens (64 bytes of bf16: whole DRAM bursts; 64-token strips need twice the cluster, whose
-// synchronisation cost more than their wider rows gained), narrower for few tokens and for a K whose slab leaves a
-// quarter of an SM in a cluster of eight; for larger K strips of 16 tokens that fit at all, then of 8; past that nothing
-// is cached.  Then the smallest cluster that keeps the slab there, enlarged while the grid leaves SMs idle.
+// Strips of 64 tokens (128 bytes of bf16 a row; strips of 32 tokens: 40 us instead of 36 forward, 111 instead of 85
+// backward, 768 x 50432), narrower for few tokens and for a K whose slab does not leave half an SM in a cluster of
+// eight; for larger K strips of 16 tokens that fit at all, then of 8; past that nothing is cached.  Then the smallest
+// cluster that keeps the slab there (a cluster's synchronisation cost more than smaller slabs and more CTAs to an SM
+// gained: 51 and 106 us with slabs of 52 KB), enlarged while the grid leaves SMs idle.
 void norm_shape(NormParams& p, int64_t bytes) {
   using namespace norm;
+  auto box_of = [](int64_t rows) { return rows >= 512 ? 128 : 32; };  // whole boxes; few of them to issue
   auto slab = [&](int l, int c) {
     const int64_t rows = (p.K + c - 1) / c;
-    return (rows + kBoxRows - 1) / kBoxRows * kBoxRows * 8 * l * bytes;
+    const int64_t box = box_of(rows);
+    return (rows + box - 1) / box * box * 8 * l * bytes;
   };
-  int lpr = 4;
+  auto total = [&](int l, int c) { return slab(l, c) + (p.K + c - 1) / c * 8; };  // gamma and beta behind it
+  int lpr = kMaxCols / 8;
   while (lpr > 1 && (int64_t)(lpr / 2) * 8 >= p.T) lpr >>= 1;
   int64_t limit = kSlabBytes;
-  while (lpr > 2 && slab(lpr, kMaxCluster) > limit) lpr >>= 1;
-  if (slab(lpr, kMaxCluster) > limit) limit = kMaxSlabBytes;
-  if (slab(lpr, kMaxCluster) > limit) lpr = 1;
-  p.cached = slab(lpr, kMaxCluster) <= limit;
+  while (lpr > 2 && total(lpr, kMaxCluster) > limit) lpr >>= 1;
+  if (total(lpr, kMaxCluster) > limit) limit = kMaxSlabBytes;
+  if (total(lpr, kMaxCluster) > limit) lpr = 1;
+  p.cached = total(lpr, kMaxCluster) <= limit;
   int c = 1;
-  while (c < kMaxCluster && slab(lpr, c) > limit) c <<= 1;
+  while (c < kMaxCluster && total(lpr, c) > limit) c <<= 1;
   p.tiles = (p.T + 8 * lpr - 1) / (8 * lpr);
   while (c < kMaxCluster && p.tiles * c < 2 * (int64_t)sm_count_current() && p.K / c > kThreads / lpr) c <<= 1;
   p.lpr = lpr;
   p.cluster = c;
   p.rows = (p.K + c - 1) / c;
-  p.smem = p.cached ? (uint32_t)slab(lpr, c) : 0;
+  p.box_rows = box_of(p.rows);
+  p.slab = p.cached ? (uint32_t)slab(lpr, c) : 0;
+  p.smem = p.cached ? (uint32_t)total(lpr, c) : 0;
 }
 
 template <auto Kern>
 static cudaError_t launch_norm_grid(const NormParams& p, cudaStream_t s) {
-  if (p.tiles * p.cluster >= (1ll << 31)) return cudaErrorInvalidValue;
   static SmemLimit limit;
   cudaError_t e = limit.raise(Kern, (uint32_t)norm::kMaxSlabBytes);
   if (e != cudaSuccess) return e;
@@ -556,10 +634,15 @@ static cudaError_t launch_norm_grid(const NormParams& p, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <bool XF32, bool YF32>
+static cudaError_t launch_norm_types(const NormParams& p, cudaStream_t s) {
+  return p.cached ? launch_norm_grid<&norm_kernel<XF32, YF32, true>>(p, s)
+                  : launch_norm_grid<&norm_kernel<XF32, YF32, false>>(p, s);
+}
+
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
-  if (p.x_f32)
-    return p.cached ? launch_norm_grid<&norm_kernel<true, true>>(p, s) : launch_norm_grid<&norm_kernel<true, false>>(p, s);
-  return p.cached ? launch_norm_grid<&norm_kernel<false, true>>(p, s) : launch_norm_grid<&norm_kernel<false, false>>(p, s);
+  if (p.x_f32) return p.y_f32 ? launch_norm_types<true, true>(p, s) : launch_norm_types<true, false>(p, s);
+  return p.y_f32 ? launch_norm_types<false, true>(p, s) : launch_norm_types<false, false>(p, s);
 }
 
 template <bool XF32, bool DF32>
@@ -585,12 +668,12 @@ cudaError_t launch_norm_grad_reduce(const float* part, int64_t tiles, int64_t K,
 
 using namespace nmk;
 
-// Map of a K x T tensor in boxes of kBoxRows rows of one strip.
+// Map of a K x T tensor in boxes of box_rows rows of one strip.
 static nm_status norm_map(CUtensorMap* tm, const void* base, int64_t K, int64_t T, int64_t ld, nm_out_dtype dtype,
-                          int lpr, const char* what) {
+                          const NormParams& p, const char* what) {
   const bool f32 = dtype == NM_OUT_F32;
-  return make_tmap(tm, base, (uint64_t)T, (uint64_t)K, (uint64_t)(ld * dtype_bytes(dtype)), 8u * (uint32_t)lpr,
-                   (uint32_t)norm::kBoxRows, 0, what,
+  return make_tmap(tm, base, (uint64_t)T, (uint64_t)K, (uint64_t)(ld * dtype_bytes(dtype)), 8u * (uint32_t)p.lpr,
+                   (uint32_t)p.box_rows, 0, what,
                    f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
@@ -625,7 +708,7 @@ nm_status nm_layer_norm(const void* X, int64_t ldx, nm_out_dtype x_dtype, int64_
   p.mean = mean;
   p.rstd = rstd;
   norm_shape(p, dtype_bytes(x_dtype));
-  if (p.cached) st = norm_map(&p.tm_x, X, K, T, ldx, x_dtype, p.lpr, "X");
+  if (p.cached) st = norm_map(&p.tm_x, X, K, T, ldx, x_dtype, p, "X");
   if (st != NM_OK) return st;
   p.status = status_word_ptr();
   if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
@@ -670,8 +753,8 @@ nm_status nm_layer_norm_grad(const void* dY, int64_t lddy, nm_out_dtype dy_dtype
   p.mean = const_cast<float*>(mean);
   p.rstd = const_cast<float*>(rstd);
   norm_shape(p, dtype_bytes(x_dtype) + dtype_bytes(dy_dtype));
-  if (p.cached) st = norm_map(&p.tm_x, X, K, T, ldx, x_dtype, p.lpr, "X");
-  if (p.cached && st == NM_OK) st = norm_map(&p.tm_d, dY, K, T, lddy, dy_dtype, p.lpr, "dY");
+  if (p.cached) st = norm_map(&p.tm_x, X, K, T, ldx, x_dtype, p, "X");
+  if (p.cached && st == NM_OK) st = norm_map(&p.tm_d, dY, K, T, lddy, dy_dtype, p, "dY");
   if (st != NM_OK) return st;
   p.status = status_word_ptr();
   if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");

@@ -23,8 +23,9 @@ struct NormParams {
   int x_f32, y_f32;    // type of X (and dX), type of Y (forward) or dY (backward)
   // set by norm_shape
   int lpr, cluster, cached;
+  int box_rows;         // of a TMA box
   int64_t tiles, rows;  // strips; rows of a CTA's slab
-  uint32_t smem;
+  uint32_t slab, smem;  // bytes
 };
 
 void norm_shape(NormParams& p, int64_t bytes);
