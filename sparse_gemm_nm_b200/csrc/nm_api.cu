@@ -348,7 +348,8 @@ static void choose_splits(SpmmParams& p, int sms) {
 
 // The same when the caller reads the ranges' sums itself: every range then costs R * bn fp32 written and read, which
 // for many rows is more than an idle tail (32000 rows at bn = 64: 16 MB a range, against 148 MB of weights).  Takes
-// the least sum of weight bytes over the balance and bytes of sums.
+// the least sum of weight bytes over the balance and bytes of sums, these counted twice (the reader waits for them:
+// cross entropy of 32000 x 4096, T = 16, 52 us in four ranges and 37 us in one).
 static void choose_splits_partials(SpmmParams& p, int sms) {
   const int64_t kt = p.k_tiles;
   const double weights = (double)p.R * (double)p.K * 1.125;
@@ -359,7 +360,7 @@ static void choose_splits_partials(SpmmParams& p, int sms) {
     const int64_t se = (kt + kps - 1) / kps;
     const int64_t units = (int64_t)p.tiles_m * se;
     const int64_t waves = (units + sms - 1) / sms;
-    const double cost = weights * (double)(waves * sms) / (double)units + (double)se * (double)p.R * p.bn * 8.0;
+    const double cost = weights * (double)(waves * sms) / (double)units + (double)se * (double)p.R * p.bn * 16.0;
     if (s == 1 || cost < best) {
       best = cost;
       p.splits = (int)se;
@@ -560,8 +561,16 @@ static nm_status run_gemm(const GemmRequest& q, cudaStream_t stream) {
       if (staged) cudaFreeAsync(staged, stream);
       if (staged_a) cudaFreeAsync(staged_a, stream);
     };
-    if (p.permuted) {
-      const int64_t ldp = (q.T + 7) / 8 * 8;
+    // The skinny kernel's boxes of X arrive slowly when T ends inside the first 16 columns or the third (cross entropy
+    // of 32000 x 4096: T = 8 45 us, T = 16 37 us; T = 37 62 us, T = 48 45 us), so where partial sums are the result (the
+    // reader takes T columns of them) X is first copied to rows of 16 or 48 (T = 8 39 us, T = 37 47 us), whose last
+    // columns hold anything: each feeds its own column of sums only.  Below 16 stages an SM the copy costs as much.
+    const bool slow = use_skinny && q.partials && (q.T < 16 || (q.T > 32 && q.T < 48));
+    const bool pad = slow && (q.R + 127) / 128 * (q.K / 128) >= 16 * (int64_t)sm_count_current();
+    int64_t cols = q.T;  // of the GEMM's X
+    if (p.permuted || pad) {
+      if (slow) cols = q.T < 16 ? 16 : 48;
+      const int64_t ldp = (cols + 7) / 8 * 8;
       if (!pool) e = staging_pool(&pool);
       if (e != cudaSuccess) {
         release();
@@ -573,7 +582,8 @@ static nm_status run_gemm(const GemmRequest& q, cudaStream_t stream) {
         release();
         return cuda_fail(e, "staging buffer for the permuted input");
       }
-      e = launch_gather_rows(q.X, q.ldx, q.idx, q.K, q.T, static_cast<uint16_t*>(staged), ldp, stream, nullptr, q.beside);
+      e = launch_gather_rows(q.X, q.ldx, p.permuted ? q.idx : nullptr, q.K, q.T, static_cast<uint16_t*>(staged), ldp,
+                             stream, nullptr, q.beside);
       if (e != cudaSuccess) {
         release();
         return cuda_fail(e, "gather launch");
@@ -621,7 +631,7 @@ static nm_status run_gemm(const GemmRequest& q, cudaStream_t stream) {
           q.partials->ld = p.bn;
         }
       }
-      st = make_tmap(&p.tm_x, xsrc, (uint64_t)q.T, (uint64_t)q.K, (uint64_t)ldsrc * 2, (uint32_t)p.bn,
+      st = make_tmap(&p.tm_x, xsrc, (uint64_t)cols, (uint64_t)q.K, (uint64_t)ldsrc * 2, (uint32_t)p.bn,
                      (uint32_t)p.kd, p.bn * 2, "X");
     } else {
       p.tiles_m = (int)((q.R + 255) / 256);

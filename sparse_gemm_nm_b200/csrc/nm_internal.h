@@ -40,7 +40,7 @@ inline bool fits_2of4(int n, int m) { return (m == 2 && n == 1) || ((m == 4 || m
 struct GatherJob {
   const uint16_t* X;
   int64_t ldx;
-  const int32_t* idx;
+  const int32_t* idx;  // null: rows in order
   int64_t K, T;
   uint16_t* Xp;
   int64_t ldp;
@@ -75,7 +75,7 @@ __device__ __forceinline__ void gather_rows_items(const GatherJob& g, int64_t wa
   const int64_t items = g.K * chunks;
   for (int64_t it = warp; it < items; it += nwarps) {
     const int64_t k = it / chunks, c0 = (it - k * chunks) * 256;
-    const int32_t src = __ldg(g.idx + k);
+    const int32_t src = g.idx ? __ldg(g.idx + k) : (int32_t)k;
     const bool valid = src >= 0 && (int64_t)src < g.K;
     const uint16_t* row = g.X + (valid ? (int64_t)src : 0) * g.ldx;
     const uint4* in = reinterpret_cast<const uint4*>(row);

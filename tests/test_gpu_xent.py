@@ -131,6 +131,15 @@ def test_other_patterns(n, m, R, K, T):
     c.check_grad(lse, dX, dV)
 
 
+# 32-deep tiles enough for every SM, where a token count inside the first or third 16 is padded before the skinny GEMM
+@pytest.mark.parametrize("T,permuted", [(1, False), (13, True), (16, False), (33, True), (47, False)])
+def test_loss_of_few_tokens_over_a_large_vocabulary(T, permuted):
+    c = Case(20000, 2048, T, permuted=permuted, seed=21)
+    loss, lse = nm.spmm_xent(*c.args(), idx=c.idx)
+    nm.nm_device_status()
+    c.check_loss(loss, lse)
+
+
 @pytest.mark.parametrize("K,T", [(256, 256), (256, 20), (40, 70)])
 def test_large_logits_neither_overflow_nor_vanish(K, T):
     """Logits of several hundred: exp of them overflows unless the column's largest is taken off first."""
