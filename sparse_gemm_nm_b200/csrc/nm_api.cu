@@ -1009,7 +1009,7 @@ nm_status run_spmm(const uint16_t* values, const uint32_t* meta, int n, int m, i
   GemmRequest q = gemm_request(values, meta, n, m, R, K, idx, X, ldx, T, Y, ldy, y_dtype);
   q.partials = partials;
   q.ext = ext;
-  q.beside = ext || partials;
+  q.beside = ext || (partials && partials->beside);
   return run_gemm(q, stream);
 }
 

@@ -45,6 +45,7 @@ struct GemmExt {
 // is in Y as usual), `split_stride` elements apart, rows of `ld`.
 struct GemmPartials {
   Staged* ws;
+  bool beside;  // the call's launches before this GEMM began with pdl_gate(): its first may run beside the last of them
   int splits;
   int64_t split_stride, ld;
 };

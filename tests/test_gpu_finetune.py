@@ -216,3 +216,30 @@ def test_a_process_may_capture_its_first_step():
     r = subprocess.run([sys.executable, "-c", FIRST_CALL_UNDER_CAPTURE], capture_output=True, text=True, timeout=300,
                        cwd=wl.__file__.rsplit("/", 2)[0])
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("T", [1, 13, 16, 37, 48])
+def test_the_loss_waits_for_the_launch_before_it(T):
+    """Each call reads what the one before it in the stream writes last, with nothing in between; several K ranges and
+    pieces of the vocabulary in the loss, its input copied to wider rows (T = 1, 13, 37) and not."""
+    K, V = 2048, 20000
+    vals, meta = oracle.compress(wl.normal_bf16((V, K), 0.02, 31), 2, 4)
+    head = to_dev(vals), torch.from_numpy(meta.view(np.int32)).to(DEV), 2, 4, K
+    xs = [padded((K, T), 1.0, 32 + i) for i in range(4)]
+    target = torch.arange(T, dtype=torch.int32, device=DEV)
+    calm = []
+    for x in xs:
+        Y = nm.layer_norm(x)[0]
+        torch.cuda.synchronize()
+        calm.append(nm.spmm_xent(*head, Y, target))
+        torch.cuda.synchronize()
+    out = padded((K, T), 1.0, 40)  # every layer norm writes here, and every loss reads it
+    ld = out.stride(0)
+    hurried = []
+    for x in xs * 3:
+        nm.nm_layer_norm(x, x.stride(0), nm.NM_OUT_BF16, K, T, None, None, 1e-5, out, ld, nm.NM_OUT_BF16, None, None)
+        hurried.append(nm.spmm_xent(*head, out, target))
+    torch.cuda.synchronize()
+    nm.nm_device_status()
+    for i, got in enumerate(hurried):
+        assert all(torch.equal(a, b) for a, b in zip(got, calm[i % 4]))
