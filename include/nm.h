@@ -3,8 +3,10 @@
  * (sm_100a): magnitude prune + push-left compression, decompression, and the
  * sparse x dense GEMM y = (W Pi) x in plain, column-permuted and PATCH-style
  * hybrid forms; further down, the one-call prune + GEMM, the two backward
- * products, INT8 2:4, TF32 1:2 (float32 data) and the diagonal pattern, each
- * with its own conventions where they differ from the ones below.
+ * products, INT8 2:4, TF32 1:2 (float32 data) and the diagonal pattern, and
+ * around a pruned projection layer norm, low-rank adapters and the cross
+ * entropy of a pruned output head, with their gradients, each with its own
+ * conventions where they differ from the ones below.
  *
  * Conventions shared by every call
  *  - bf16 data is passed as its 16-bit pattern (uint16_t).  All matrices are
@@ -31,12 +33,14 @@
  *  - Every pointer is DEVICE memory owned by the caller (none is freed or
  *    retained).  The library allocates no device memory, except stream-ordered
  *    staging buffers from its own pool in the calls that document them (the
- *    GEMMs on the two-SM path, the backward, INT8, TF32 and diagonal calls).
+ *    GEMMs on the two-SM path, the backward, INT8, TF32 and diagonal calls,
+ *    layer norm's gradient, the adapter and the cross-entropy calls).
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy
  *    default stream).  Argument errors are detected on the host and returned
  *    before anything is launched.  Each successful call launches one kernel
  *    (none when the output is empty), except the GEMM calls that stage an
- *    operand first (a re-encoding and/or a gather pass; see nm_spmm).
+ *    operand first (a re-encoding and/or a gather pass; see nm_spmm) and the
+ *    adapter and cross-entropy calls, which are several passes.
  *  - Device pointers given to the GEMMs must be 16-byte aligned, and leading
  *    dimensions of X and Y must keep every row 16-byte aligned
  *    (NM_ERR_MISALIGNED otherwise).
@@ -433,8 +437,8 @@ NM_API nm_status nm_layer_norm(const void* X, int64_t ldx, nm_out_dtype x_dtype,
  *   dX     [out] K x T of X's type, row stride lddx >= T, 16-byte rows; must
  *          not overlap dY or X
  *   dgamma, dbeta [out, optional] K fp32 each, overwritten (zeros when T = 0)
- * With dgamma or dbeta, ceil(T/w)*2*K*4 bytes of row sums (one pair per strip
- * of w = 8 to 64 tokens) are staged from the library's pool, and a second
+ * With dgamma or dbeta, ceil(T/w)*2*K*4 bytes of row sums (one pair per row and
+ * strip of w = 8 to 64 tokens) are staged from the library's pool, and a second
  * launch adds them in a fixed order, so that results repeat bit for bit.
  * Errors: as nm_layer_norm.
  */
@@ -450,16 +454,20 @@ NM_API nm_status nm_layer_norm_grad(const void* dY, int64_t lddy, nm_out_dtype d
  *   lse[t]  = log sum_v exp(z[v][t]),
  *   loss[t] = lse[t] - z[target[t]][t], and 0 where target[t] is outside
  *             [0, R) (a token without a loss; its lse is still written).
- * The logits are never all in memory: the vocabulary is taken in pieces of
- * rows, and every 256 rows leave one (max, sum of exponentials) pair per token.
+ * The logits are never all in memory.  Where the two-SM GEMM serves the shape
+ * (K % 128 == 0, T >= 192, T % 8 == 0, a pattern it takes) none is written at
+ * all: its epilogue leaves one (max, sum of exponentials) pair per token and 32
+ * rows.  Elsewhere the vocabulary is taken in pieces of rows, and every 256 rows
+ * of a piece leave one pair per token.
  * The pages train and fine-tune pruned networks without giving this step; it
  * is the loss behind the last projection.  Logits, exponentials and sums are fp32.
  *   values, meta, n, m, idx, X  as nm_spmm_permuted (idx may be NULL); R, K >= 1
  *   target    [in]  T int32
  *   loss, lse [out] T fp32 each
- * Staged from the library's pool: 8 bytes per token and 256 rows of W, and a
- * piece of fp32 logits (at most 8192 rows, about 64 MB; 256 rows at least),
- * Xp with idx, and what nm_spmm stages for a piece.
+ * Results repeat bit for bit.  Staged from the library's pool: the pairs (8 bytes
+ * per token and 32 or 256 rows of W), Xp with idx, what nm_spmm stages, and
+ * outside the two-SM GEMM a piece of fp32 logits (at most 8192 rows, about 64
+ * MB; 256 rows at least).
  * Errors: as nm_spmm_permuted.
  */
 NM_API nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
@@ -471,16 +479,17 @@ NM_API nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int 
  *   G[v][t] = dloss[t] (exp(z[v][t] - lse[t]) - [v == target[t]])
  * (0 for a token without a loss), dX = (W' Pi)^T G as nm_spmm_t gives it and
  * dV = the survivors' entries of G Xp^T as nm_sddmm gives them.  The logits
- * of a piece of the vocabulary are computed again; G is rounded to bf16, as
- * the dY of those calls is; dX adds up in fp32 over the pieces.
+ * of a piece of the vocabulary are computed again (on the two-SM GEMM its
+ * epilogue writes G and no logits); G is rounded to bf16, as the dY of those
+ * calls is; dX adds up in fp32 over the pieces.
  *   target, lse, dloss [in] T each (int32, fp32, fp32); lse from nm_spmm_xent
  *   dX  [out] K x T bf16, row stride lddx >= T, 16-byte rows, or NULL.  With
  *       idx, rows as in nm_spmm_t (repeated entries are not supported, rows
  *       that no entry names are not written)
  *   dV  [out] R x nm_value_cols(K,n,m) bf16, or NULL (a frozen head); not both
- * Results repeat bit for bit.  Staged from the library's pool: a piece of
- * logits and of G, and with dX the piece's decompressed weights and a K x T
- * fp32 accumulator.
+ * Results repeat bit for bit.  Staged from the library's pool: a piece of G (and
+ * of fp32 logits, outside the two-SM GEMM), 12 bytes per token, with dX the
+ * piece's decompressed weights and a K x T fp32 accumulator, and Xp with idx.
  * Errors: as nm_spmm_t.
  */
 NM_API nm_status nm_spmm_xent_grad(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
@@ -505,26 +514,34 @@ NM_API nm_status nm_spmm_xent_grad(const uint16_t* values, const uint32_t* meta,
  *   adapter T int32
  * A and B are aligned to their elements; rows that start on 16 bytes (K % 8 ==
  * 0, rank % 8 == 0) are read faster.  A_a x_t and B_a^T dy_t stay fp32 between
- * the products (read by the tensor cores as two or three bf16 terms), and the
+ * the products (read by the tensor cores as two bf16 terms, three for fp32 results), and the
  * projection's fp32 sum takes the adapter's before the one rounding to the
  * output.  No column depends on another column's data: an Inf or NaN in one
  * request's tokens or adapter stays in its columns.  Results repeat bit for
  * bit.  At most 4194240 tokens a call (NM_ERR_UNSUPPORTED).
+ * Where a two-SM GEMM serves the projection (nm_spmm_lora: as for nm_spmm_xent;
+ * nm_spmm_lora_t: always) and num_adapters * rank <= 2048, the adapters are
+ * further reduction steps of that GEMM ("inside" below): their second factors
+ * are laid side by side first, and a last pass redoes the columns of tokens
+ * that met an Inf or NaN of another adapter there.  Otherwise the adapters'
+ * product is a pass of its own after the projection.
  *
  * nm_spmm_lora: Y as above; other arguments as nm_spmm_permuted (idx may be
- *   NULL).  Staged from the library's pool: T x rank (padded to 16) fp32, the
- *   projection's R x T fp32 sum, and what nm_spmm_permuted stages.
+ *   NULL).  Staged from the library's pool, besides what nm_spmm_permuted
+ *   stages: inside, R x num_adapters*rank (padded to 64) and two or three terms
+ *   of num_adapters*rank x T, bf16; otherwise T x rank (padded to 16) and the
+ *   projection's R x T sum, fp32.
  * nm_spmm_lora_t: the input gradient dX = (W' Pi)^T dY + s_a A_a^T (B_a^T dY).
  *   Arguments as nm_spmm_t, but with idx every row of dX is written: rows that
- *   no entry names get the adapters' part alone.  Staged: T x rank fp32, a K x T
- *   fp32 sum, with idx K*4 bytes, and what nm_spmm_t stages.
+ *   no entry names get the adapters' part alone.  Staged as by nm_spmm_lora
+ *   with K for R, with idx K*4 bytes more, and what nm_spmm_t stages.
  * nm_lora_grad: the adapters' gradients, summed over each adapter's tokens,
  *     dA_a = s_a sum_t (B_a^T dy_t) x_t^T   (num_adapters x rank x K),
  *     dB_a = s_a sum_t dy_t (A_a x_t)^T     (num_adapters x R x rank),
  *   both bf16 or both fp32 (dtype), contiguous, either may be NULL (not
  *   both); zeros for an adapter without tokens.  dY R x T and X K x T as in
- *   nm_sddmm.  Staged: T x rank fp32 for each of the two, and 4 bytes per
- *   adapter and 64 tokens.
+ *   nm_sddmm.  Staged: two or three bf16 terms of T x rank for each of the two,
+ *   and 4 bytes per adapter and 64 tokens.
  * Errors: as nm_spmm_permuted, nm_spmm_t and nm_sddmm.
  */
 NM_API nm_status nm_spmm_lora(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,

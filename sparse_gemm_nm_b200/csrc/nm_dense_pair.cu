@@ -26,6 +26,10 @@
 // with K = 32 and K = 8 per MMA.  The plain store epilogue sends whole
 // 128-byte row chunks through a swizzled staging tile and TMA stores; with a
 // row map (dX under an index map) rows are stored one per lane.
+// `add` adds the fp32 tile to what C holds (TMA reductions, no read in the
+// kernel; one writer per element and launch, so results repeat): the pieces of
+// the vocabulary in nm_xent.cu.  EXT appends half-stages of 64 reduction steps
+// for the adapters of nm_lora.cu, as in nm_spmm_pair.cu.
 #include <atomic>
 #include <cstdint>
 #include <cuda.h>
