@@ -489,7 +489,8 @@ NM_API nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int 
  *   dV  [out] R x nm_value_cols(K,n,m) bf16, or NULL (a frozen head); not both
  * Results repeat bit for bit.  Staged from the library's pool: a piece of G (and
  * of fp32 logits, outside the two-SM GEMM), 12 bytes per token, with dX the
- * piece's decompressed weights and a K x T fp32 accumulator, and Xp with idx.
+ * piece's decompressed weights and one to eight K x T fp32 accumulators, and Xp
+ * with idx.
  * Errors: as nm_spmm_t.
  */
 NM_API nm_status nm_spmm_xent_grad(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,

@@ -131,7 +131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_gate();  // no global memory touched before this point
+  pdl_enter(p.early != 0);  // no global memory touched before this point
 
   const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
   const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
@@ -451,6 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, dpair::kTmemCols);
   }
+  pdl_leave(p.early != 0);
 }
 
 template <bool A_MN, bool B_MN, int EPI, bool I8 = false, bool TF32 = false, bool EXT = false>

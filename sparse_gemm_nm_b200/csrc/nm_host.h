@@ -75,11 +75,13 @@ nm_status run_spmm_epilogue(const uint16_t* values, const uint32_t* meta, int n,
 // nm_sddmm.
 nm_status run_sddmm(const uint32_t* meta, int n, int m, int64_t R, int64_t K, const int32_t* idx, const uint16_t* dY,
                     int64_t lddy, const uint16_t* X, int64_t ldx, int64_t T, void* dV, nm_out_dtype dtype,
-                    cudaStream_t stream);
+                    cudaStream_t stream, bool beside = false);  // beside: as GemmPartials' (without idx)
 // C (K x T fp32, row stride ldc) = or += W^T D for a dense R x K bf16 W (row stride ldw) and an R x T bf16 D, by
 // the SM-pair GEMM; every element takes one addition.
+// With ranges > 1 the rows of W and D are taken in that many ranges side by side, range i's sum in C + i K ldc.
+int dense_t_ranges(int64_t R, int64_t K, int64_t T);  // that fill the SMs
 nm_status dense_t_accumulate(const uint16_t* W, int64_t ldw, int64_t R, int64_t K, const uint16_t* D, int64_t ldd,
-                             int64_t T, float* C, int64_t ldc, bool add, cudaStream_t stream);
+                             int64_t T, float* C, int64_t ldc, int ranges, bool add, cudaStream_t stream);
 
 inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -116,6 +116,7 @@ struct DenseParams {
   int64_t ldo;
   int out_f32;
   int add;  // epilogue 0 with tma_store and out_f32: C += (a TMA reduction per chunk) instead of C =
+  int early;  // runs beside its predecessor (pdl_enter)
   const int32_t* row_map;
   int64_t rows_out;
   const uint32_t* meta;

@@ -16,13 +16,15 @@
 // the SM-pair GEMM's epilogue where that serves; G meets the decompressed piece
 // of W' in a product that adds to a K x T fp32 accumulator, and Xp in the
 // survivor-sampled product for dV.  The accumulator takes one addition per
-// piece, in the order of the pieces; it is rounded to dX at the end.
+// piece, in the order of the pieces; with few tiles of dX there are several, for
+// ranges of a piece's rows side by side.  Their sum is rounded to dX at the end.
+// Launches that need nothing of the one before them start beside it.
 //
 // Measured: 32000 x 4096 x 2048 forward 264 us (floor 160 us of sparse products;
 // the GEMM itself sets the time: its MMA issue and, in a loop, the power cap),
 // backward 1113 us (two dense products of 0.54 TFLOP beside the sparse one);
 // 37 tokens 47 us (floor 23 us of weights; 250 row tiles on 148 SMs, and every
-// tile reads X again); 1000 x 768 x 256 backward 41 us, launches and their
+// tile reads X again); 1000 x 768 x 256 backward 31 us, launches and their
 // latency.
 #include <cstdint>
 #include <cstring>
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(256) xent_g_kernel(const float* Z, int64_t ldz
 }
 
 // dX[idx[k]] (dX[k] without idx) = the accumulator's row k, rounded to bf16; rows mapped outside [0, K) are dropped.
-__global__ void __launch_bounds__(256) xent_round_kernel(const float* acc, int64_t lda, int64_t K, int64_t T,
+__global__ void __launch_bounds__(256) xent_round_kernel(const float* acc, int ranges, int64_t lda, int64_t K, int64_t T,
                                                          const int32_t* idx, uint16_t* dX, int64_t lddx) {
   pdl_gate();
   const int64_t pieces = (T + 7) / 8, total = K * pieces;
@@ -184,11 +186,27 @@ __global__ void __launch_bounds__(256) xent_round_kernel(const float* acc, int64
     const float* a = acc + k * lda + t;
     uint16_t* d = dX + row * lddx + t;
     if (t + 8 <= T) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(a)), y = __ldcg(reinterpret_cast<const float4*>(a) + 1);
+      float4 x = __ldcg(reinterpret_cast<const float4*>(a)), y = __ldcg(reinterpret_cast<const float4*>(a) + 1);
+      for (int i = 1; i < ranges; ++i) {
+        const float4* b = reinterpret_cast<const float4*>(a + i * K * lda);
+        const float4 u = __ldcg(b), v = __ldcg(b + 1);
+        x.x += u.x;
+        x.y += u.y;
+        x.z += u.z;
+        x.w += u.w;
+        y.x += v.x;
+        y.y += v.y;
+        y.z += v.z;
+        y.w += v.w;
+      }
       *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
                                                 pack_bf16x2(y.z, y.w));
     } else {
-      for (int j = 0; t + j < T; ++j) d[j] = (uint16_t)(pack_bf16x2(__ldcg(a + j), 0.f) & 0xFFFFu);
+      for (int j = 0; t + j < T; ++j) {
+        float x = __ldcg(a + j);
+        for (int i = 1; i < ranges; ++i) x += __ldcg(a + i * K * lda + j);
+        d[j] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xFFFFu);
+      }
     }
   }
 }
@@ -311,13 +329,14 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
   const bool fused = spmm_pair_serves(h.values, h.meta, h.n, h.m, h.K, h.T);
   const int64_t rows = piece_rows(h.R, h.T, fused ? 2 : 4), ldz = (h.T + 3) / 4 * 4, ldg = (h.T + 7) / 8 * 8;
   const int64_t ldk = (h.K + 7) / 8 * 8;
+  const int ranges = dense_t_ranges(rows < h.R ? rows : h.R, h.K, h.T);
   PairEpiData epi = {};
   epi.mode = PAIR_EPI_XGRAD;
   if (fused) st = column_data(h, target, lse, dloss, epi, cols, s);
   if (st != NM_OK) return st;
   Parts parts;
   const int64_t at_g = parts.take(rows * ldg * 2), at_z = parts.take(fused ? 0 : rows * ldz * 4);
-  const int64_t at_wd = parts.take(dX ? rows * ldk * 2 : 0), at_acc = parts.take(dX ? h.K * ldz * 4 : 0);
+  const int64_t at_wd = parts.take(dX ? rows * ldk * 2 : 0), at_acc = parts.take(dX ? ranges * h.K * ldz * 4 : 0);
   cudaError_t e = buf.get(parts.size());
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gradient piece");
   uint16_t* g = buf.as<uint16_t>(at_g);
@@ -341,21 +360,22 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
       if (e != cudaSuccess) return cuda_fail(e, "cross-entropy gradient launch");
     }
     if (dX) {
-      e = launch_decompress(h.row_values(v0), h.row_meta(v0), n, h.K, h.n, h.m, wd, ldk, s);
+      // beside the launch that makes G
+      e = launch_decompress(h.row_values(v0), h.row_meta(v0), n, h.K, h.n, h.m, wd, ldk, s, true);
       if (e != cudaSuccess) return cuda_fail(e, "decompress launch");
-      st = dense_t_accumulate(wd, ldk, n, h.K, g, ldg, h.T, acc, ldz, v0 > 0, s);
+      st = dense_t_accumulate(wd, ldk, n, h.K, g, ldg, h.T, acc, ldz, ranges, v0 > 0, s);
       if (st != NM_OK) return st;
     }
     if (dV) {
       st = run_sddmm(h.row_meta(v0), h.n, h.m, n, h.K, nullptr, g, ldg, h.X, h.ldx, h.T,
-                     dV + v0 * value_cols(h.K, h.n, h.m), NM_OUT_BF16, s);
+                     dV + v0 * value_cols(h.K, h.n, h.m), NM_OUT_BF16, s, dX != nullptr);
       if (st != NM_OK) return st;
     }
   }
   if (dX) {
     const int64_t want = (h.K * ((h.T + 7) / 8) + 255) / 256, cap = (int64_t)sm_count_current() * 16;
     e = launch_pdl(xent_round_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, s,
-                   (const float*)acc, ldz, h.K, h.T, idx, dX, lddx);
+                   (const float*)acc, ranges, ldz, h.K, h.T, idx, dX, lddx);
     count_launch();
     if (e != cudaSuccess) return cuda_fail(e, "gradient rounding launch");
   }

@@ -274,3 +274,13 @@ def test_refusals():
     with pytest.raises(nm.NmError) as e:
         nm.spmm_xent(c.values, c.meta, 2, 5, 64, c.X, t)
     assert e.value.status == nm.NM_ERR_INVALID_ARG
+
+
+# one SM pair's tile of dX over thousands of rows, taken in several ranges; with several pieces, the last too small for all
+@pytest.mark.parametrize("R,K,T", [(9000, 136, 14), (5000, 256, 200), (4500, 128, 300)])
+def test_gradients_of_a_large_vocabulary_and_few_features(R, K, T):
+    c = Case(R, K, T, seed=23)
+    loss, lse, dX, dV = c.run()
+    nm.nm_device_status()
+    c.check_loss(loss, lse)
+    c.check_grad(lse, dX, dV)
