@@ -3,12 +3,15 @@
 Python binding of the C ABI in ``include/nm.h`` (library ``libnm_b200.so``).
 The functions named like the C entry points (``nm_prune_compress``,
 ``nm_decompress``, ``nm_spmm``, ``nm_spmm_permuted``, ``nm_hybrid_spmm``,
-``nm_spmm_algo``, ``nm_prune_spmm``, ``nm_spmm_t``, ``nm_sddmm``) only marshal arguments: tensors become device pointers, the
+``nm_spmm_algo``, ``nm_prune_spmm``, ``nm_spmm_t``, ``nm_sddmm``,
+``nm_layer_norm``, ``nm_spmm_lora``, ``nm_spmm_xent``, their gradients and the
+calls of the other formats) only marshal arguments: tensors become device pointers, the
 stream defaults to torch's current stream, and a non-zero status raises
 :class:`NmError`.  Every step of the computation runs in the library's CUDA
 kernels; there is no fallback of any kind.  The convenience wrappers
 (``prune_compress``, ``decompress``, ``spmm``, ``hybrid_spmm``, ``prune_spmm``, ``spmm_t``,
-``sddmm``) also allocate
+``sddmm``; around a projection ``layer_norm``, ``layer_norm_grad``, ``spmm_lora``,
+``spmm_lora_t``, ``lora_grad``, ``spmm_xent``, ``spmm_xent_grad``) also allocate
 the outputs with torch.
 
 bf16 data is accepted as ``torch.bfloat16`` tensors (or int16/uint16 views of
