@@ -1,12 +1,16 @@
 // nm_lora.cu -- low-rank adapters of many requests beside the shared pruned
 // projection: y_t = (W' Pi) x_t + s_a B_a (A_a x_t), a the adapter of token t.
 //
-// Three products, each over tiles of 64 tokens, on the warp-level bf16 MMA
-// (m16n8k16): with ranks of 8 to 128 they move far more bytes than they
-// multiply, so operand streaming bounds them and not the tensor pipe.
+// Three products, each over tiles of 64 tokens:
 //   shrink   S[t] = A_a x_t          (and U[t] = B_a^T dy_t in the backward pass)
 //   expand   Y = base + s_a B_a S    (and dX = base + s_a A_a^T U)
 //   outer    dB_a = s_a sum_t dy_t S[t]^T,  dA_a = s_a sum_t U[t] x_t^T
+// With ranks of 8 to 128 they move far more bytes than they multiply.  Shrink and
+// expand, whose tiles hold several adapters' tokens in any order, run on the
+// warp-level bf16 MMA (m16n8k16), which takes blocks of 16 ranks and 8 tokens;
+// outer, whose reduction is the adapter's tokens, on tcgen05 with both operands
+// as TMA brings them (128 rows x the terms side by side, up to 3 x 64 columns, so
+// that the rows are read from shared memory once for all terms).
 // A tile lists the distinct adapters of its tokens and takes them one after the
 // other; a product for adapter a is kept only in the columns of a's tokens (a
 // select, not a multiplication by 0), so an Inf or NaN of one request reaches no
@@ -28,8 +32,10 @@
 // of weights; shrink 9 us beside the GEMM's 18, expand 8); 4096 x 4096 x 2048, 8 of
 // rank 16 57 us (the sparse product alone 35); input gradient 4096 x 11008 x 2048, 2
 // of rank 32 169 us (the dense product alone 110, decompression beside the
-// shrink); gradients 11008 x 4096 x 2048, 4 of rank 64 95 us (13 us of bytes;
-// the warp-level MMA with its fragment loads sets the outer products' 42 and 26 us).
+// shrink); gradients 11008 x 4096 x 2048, 4 of rank 64 74 us (13 us of bytes;
+// latency of the copies: a CTA has 9 tiles between its first load and its join.
+// The outer product on warp-level MMAs, whose fragment loads and thirds of the rate
+// of three terms set its time: 95 us).
 #include <cstdint>
 #include <type_traits>
 #include <cuda_runtime.h>
@@ -60,14 +66,18 @@ constexpr uint32_t kExpandBatch = 96 * 1024;  // bytes of adapters' tiles in fli
 constexpr int kOuterRank = 64;   // rank columns of an outer work item
 constexpr uint32_t kOuterM = kRows * kTok * 2;
 constexpr uint32_t kOuterV = kTok * kOuterRank * 2;  // one bf16 term
-// Two CTAs to an SM: their warps cover for one another's MMA latency (one CTA left the issue slots 59 % idle).  Z comes
-// from HBM and has a ring of three stages; three terms leave room for two stages of V, which the L2 holds.
+// Two CTAs to an SM, one working while the other waits for copies or joins (tiles of 256 rows, one CTA to an SM with
+// four stages: 11008 x 4096 x 2048, 4 of rank 64 took 90 us instead of 74).  Z comes from HBM and has a ring of three
+// stages; three terms leave room for two stages of V, which the L2 holds.
 constexpr int kOuterZ = 3;
 __host__ __device__ constexpr int outer_v(int planes) { return planes == 3 ? 2 : 3; }
 __host__ __device__ constexpr uint32_t outer_smem(int planes) {
   return kOuterZ * kOuterM + (uint32_t)(outer_v(planes) * planes) * kOuterV + 1024;
 }
 constexpr int kOuterPitch = kOuterRank + 4;  // floats of a row of joined sums
+constexpr int kOuterGroup = 3;  // tiles whose products one accumulator takes (it truncates): 192 tokens
+// Rank columns of a work item as an MMA's N and a box: 16, 32 or 64 (a swizzle's width).
+__host__ __device__ constexpr int outer_box(int rank) { return rank > 32 ? 64 : rank > 16 ? 32 : 16; }
 static_assert(kRows * kOuterPitch * 4 <= kOuterZ * kOuterM, "the joined sums reuse the stages");
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -696,19 +706,28 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int kV = outer_v(P);                  // stages of V: P terms of [64 tokens][up to 64 ranks]
   constexpr uint32_t kVStage = P * kOuterV;
+  constexpr uint32_t kCols = P == 3 ? 256 : 128;  // TMEM columns: the terms' products side by side, 64 each at most
   uint8_t* s_v = smem + kOuterZ * kOuterM;
   __shared__ int32_t s_id[kOuterZ][kTok];
-  __shared__ uint64_t s_fz[kOuterZ], s_fv[kV];
+  __shared__ uint64_t s_fz[kOuterZ], s_fv[kV], s_done[kOuterZ];
+  __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    for (int i = 0; i < kOuterZ; ++i) mbar_init(&s_fz[i], 1);
+    for (int i = 0; i < kOuterZ; ++i) {
+      mbar_init(&s_fz[i], 1);
+      mbar_init(&s_done[i], 1);
+    }
     for (int i = 0; i < kV; ++i) mbar_init(&s_fv[i], 1);
     s_abort = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
     tma_prefetch_desc(&p.tm_z);
     tma_prefetch_desc(&p.tm_v);
+  }
+  if (warp == 4) {
+    tmem_alloc(&s_tmem, kCols);
+    tmem_relinquish();
   }
   pdl_enter(p.early != 0);
   const uint32_t rank = cluster_ctarank();
@@ -717,9 +736,7 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
   const int rblocks = (p.rank + kOuterRank - 1) / kOuterRank;
   const int32_t a = (int32_t)(blockIdx.y / rblocks);
   const int j0 = (int)(blockIdx.y % rblocks) * kOuterRank;
-  const int rs = (p.rank + 15) / 16 * 16;
-  const int box = rs < kOuterRank ? rs : kOuterRank;            // rank columns that a box brings
-  const int cols = rs - j0 < kOuterRank ? rs - j0 : kOuterRank;  // of which this item has (a multiple of 16)
+  const int box = outer_box(p.rank);  // rank columns that a box brings, N of the MMAs (past the rank: zeros)
   const int32_t* list = p.tiles + (int64_t)a * ((p.T + kTok - 1) / kTok);
   const int count = __ldcg(p.counts + a);
   int32_t first[kOuterZ];  // read beside the count (places past it hold no tile and are not used)
@@ -729,7 +746,10 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
     first[d] = at < (p.T + kTok - 1) / kTok ? __ldcg(list + at) : 0;
   }
   const int mine = count > (int)rank ? (count - (int)rank + C - 1) / C : 0;  // tiles rank, rank + C, ... of the list
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
 
   // Tile i of this CTA: Z and its tokens' adapters into ring slot i % kOuterZ, V into slot i % kV.  The tile numbers come
   // from the list two turns earlier, so that no load waits for the list.
@@ -752,7 +772,10 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
     for (int q = 0; q < P; ++q)
       tma_load_3d(s_v + slot * kVStage + q * kOuterV, &p.tm_v, &s_fv[slot], j0, tile * kTok, q);
   };
-  float sum[8][4] = {};
+  // The products of tile i are complete (its slots are free, its accumulator may be read).
+  auto done = [&](int i) {
+    return mbar_wait(&s_done[i % kOuterZ], (uint32_t)(i / kOuterZ) & 1u, &s_abort, p.status, kWaitNs);
+  };
   // next[d]: the tile that is d turns ahead
   int32_t next[kOuterZ];
 #pragma unroll
@@ -763,88 +786,96 @@ __global__ void __launch_bounds__(lora::kThreads, 2) lora_outer_kernel(const __g
 #pragma unroll
   for (int d = 0; d < kV - 1; ++d)
     if (d < mine) load_v(d, next[d]);
-  // Addresses within a stage.  The swizzles XOR row bits that a step of 16 rows leaves alone, so a lane's offsets are
-  // the same in every step: Z in units of the K step, the terms' four 16-rank blocks (rows of 32, 64 or 128 bytes
-  // swizzled within themselves, rows of 96 bytes not).
-  const int mi = lane >> 3, l8 = lane & 7;
-  const uint32_t z_row = (uint32_t)(16 * warp + 8 * (mi & 1) + l8);
-  const uint32_t z_off = z_row * 128, z_sw = z_row & 7u, z_unit = (uint32_t)(mi >> 1);
-  const uint32_t v_step = 16u * (uint32_t)box * 2u;
-  uint32_t v_off[4];
+  const uint32_t idesc = idesc_bf16_major((uint32_t)(P * box), (uint32_t)kRows, false, true);
+  const uint32_t v_row = (uint32_t)box * 2u;  // bytes of a token's ranks, the swizzle's width
+  const uint32_t v_swz = box == 64 ? SWZ_128B : box == 32 ? SWZ_64B : SWZ_32B;
+  // This thread's part of the sums: row 32 (warp % 4) + lane, 32 ranks from 32 (warp / 4).
+  const uint32_t my_tmem = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 32u * (uint32_t)(warp >> 2);
+  float sum[32] = {};
+  auto flush = [&] {  // adds the accumulators of a group of tiles, whose products are complete
+    tc_fence_after();
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const uint32_t unit = (uint32_t)(2 * b + (mi >> 1));
-    const uint32_t sw = box == 64 ? (uint32_t)l8 : box == 32 ? (uint32_t)(l8 >> 1) & 3u : box == 16 ? (uint32_t)(l8 >> 2) : 0u;
-    v_off[b] = (uint32_t)(8 * (mi & 1) + l8) * (uint32_t)box * 2u + ((unit ^ sw) << 4);
-  }
-  // One tile's products.  MASKED: some of its tokens are not the adapter's and leave both operands: their Inf or NaN in
-  // one would survive a 0 in the other, and S of a token without an adapter is not written at all.
-  auto products = [&](uint32_t m, uint32_t v, unsigned lo, unsigned hi, float (&acc)[8][4], auto masked) {
-    constexpr bool MASKED = decltype(masked)::value;
+    for (int q = 0; q < P; ++q) {
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(my_tmem + (uint32_t)(q * box), v);
+      tc_wait_ld();
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      const unsigned used = ((ks & 2 ? hi : lo) >> (16 * (ks & 1))) & 0xFFFFu;  // this step's tokens of the adapter
-      if (MASKED && !used) continue;
-      uint32_t z[4], keep[2] = {~0u, ~0u};
-      ldmatrix_x4(z, m + z_off + (((2 * ks + z_unit) ^ z_sw) << 4));
-      if (MASKED) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const unsigned two = used >> (8 * h + 2 * (lane & 3));
-          keep[h] = (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
-          z[2 * h] &= keep[h];
-          z[2 * h + 1] &= keep[h];
-        }
-      }
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (16 * b >= cols) continue;
-#pragma unroll
-        for (int q = 0; q < P; ++q) {
-          uint32_t f[4];
-          ldmatrix_x4_trans(f, v + q * kOuterV + ks * v_step + v_off[b]);
-          if (MASKED) {
-            f[0] &= keep[0];
-            f[1] &= keep[1];
-            f[2] &= keep[0];
-            f[3] &= keep[1];
-          }
-          mma_bf16(acc[2 * b], z, f[0], f[1]);
-          mma_bf16(acc[2 * b + 1], z, f[2], f[3]);
-        }
-      }
+      for (int e = 0; e < 32; ++e) sum[e] += __uint_as_float(v[e]);
     }
+    tc_fence_before();  // the next __syncthreads lets the next group overwrite them
   };
-  for (int i = 0; i < mine; ++i) {
+  __syncthreads();  // the first tiles' adapters are there
+  bool ok = true;
+  for (int i = 0; i < mine && ok; ++i) {
     const int slot = i % kOuterZ;
-    mbar_wait(&s_fz[slot], (uint32_t)(i / kOuterZ) & 1u, &s_abort, p.status, kWaitNs);
-    mbar_wait(&s_fv[i % kV], (uint32_t)(i / kV) & 1u, &s_abort, p.status, kWaitNs);
-    __syncthreads();  // the ids are there, and the slots of tile i - 1 are free
+    uint8_t* z = smem + slot * kOuterM;
+    uint8_t* v = s_v + (i % kV) * kVStage;
+    ok = mbar_wait(&s_fz[slot], (uint32_t)(i / kOuterZ) & 1u, &s_abort, p.status, kWaitNs) &&
+         mbar_wait(&s_fv[i % kV], (uint32_t)(i / kV) & 1u, &s_abort, p.status, kWaitNs);
+    const unsigned lo = __ballot_sync(0xFFFFFFFFu, s_id[slot][lane] == a);
+    const unsigned hi = __ballot_sync(0xFFFFFFFFu, s_id[slot][32 + lane] == a);
+    if ((lo & hi) != 0xFFFFFFFFu) {
+      // Tokens that are not the adapter's leave both operands: their Inf or NaN in one would survive a 0 in the other, and
+      // S of a token without an adapter is not written at all.
+#pragma unroll
+      for (int u = 0; u < kRows * 8 / kThreads; ++u) {
+        const int e = tid + u * kThreads, row = e >> 3, c = e & 7;  // tokens 8 c ..
+        const unsigned used = ((c & 4 ? hi : lo) >> (8 * (c & 3))) & 0xFFu;
+        if (used == 0xFFu) continue;
+        uint4* at = reinterpret_cast<uint4*>(z + row * 128 + ((c ^ (row & 7)) << 4));
+        uint4 w = *at;
+        auto keep = [&](int j) { return (used >> j & 1u ? 0xFFFFu : 0u) | (used >> j & 2u ? 0xFFFF0000u : 0u); };
+        w.x &= keep(0);
+        w.y &= keep(2);
+        w.z &= keep(4);
+        w.w &= keep(6);
+        *at = w;
+      }
+      const int units = box / 8;  // 16-byte units of a token, swizzled within it
+      for (int e = tid; e < P * kTok * units; e += kThreads) {
+        const int q = e / (kTok * units), t = (e - q * kTok * units) / units, c = e % units;
+        if (((t & 32 ? hi : lo) >> (t & 31)) & 1u) continue;
+        *reinterpret_cast<uint4*>(v + q * kOuterV + t * v_row + c * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+    }
+    if (i > 0 && i % kOuterGroup == 0) {
+      const bool complete = __all_sync(0xFFFFFFFFu, done(i - 1));
+      if (complete) flush();
+      ok = ok && complete;
+    }
+    ok = !__syncthreads_or(!ok);  // every thread leaves together when a copy did not come
+    if (tid == 0 && ok) {
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < kTok / 16; ++ks)  // the terms are P atoms of the second operand: Z is read once for all
+        tc_mma(tmem, smem_desc(smem_u32(z) + 32 * ks, 16, 1024, SWZ_128B),
+               smem_desc(smem_u32(v) + ks * 16 * v_row, kOuterV, 8 * v_row, v_swz), idesc,
+               i % kOuterGroup > 0 || ks > 0 ? 1u : 0u);
+      tc_commit(&s_done[slot]);
+    }
+    if (!ok) break;
+    if (i >= 1 && (tid == 0 || tid == 32)) done(i - 1);  // the slots of tile i - 1 are free
     if (i + kOuterZ - 1 < mine) load_z(i + kOuterZ - 1, next[kOuterZ - 1]);
     if (i + kV - 1 < mine) load_v(i + kV - 1, next[kV - 1]);
 #pragma unroll
     for (int d = 0; d + 1 < kOuterZ; ++d) next[d] = next[d + 1];
     next[kOuterZ - 1] = i + kOuterZ < mine ? __ldcg(list + rank + (int64_t)(i + kOuterZ) * C) : 0;
-    const uint32_t m = smem_u32(smem + slot * kOuterM), v = smem_u32(s_v + (i % kV) * kVStage);
-    const unsigned lo = __ballot_sync(0xFFFFFFFFu, s_id[slot][lane] == a);
-    const unsigned hi = __ballot_sync(0xFFFFFFFFu, s_id[slot][32 + lane] == a);
-    float acc[8][4] = {};
-    if ((lo & hi) == 0xFFFFFFFFu)
-      products(m, v, lo, hi, acc, std::false_type());
-    else
-      products(m, v, lo, hi, acc, std::true_type());
-#pragma unroll
-    for (int e = 0; e < 32; ++e) sum[e >> 2][e & 3] += acc[e >> 2][e & 3];
   }
+  if (mine > 0 && ok && __all_sync(0xFFFFFFFFu, done(mine - 1))) flush();
+  if (*static_cast<volatile int*>(&s_abort)) sleep_about_ns(200000ull);  // what is in flight lands before its place is reused
   __syncthreads();
   float* s_sum = reinterpret_cast<float*>(smem);  // [128 rows][kOuterPitch], over the stages
 #pragma unroll
-  for (int nb = 0; nb < 8; ++nb)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<float2*>(s_sum + (16 * warp + (lane >> 2) + 8 * h) * kOuterPitch + 8 * nb + 2 * (lane & 3)) =
-          make_float2(sum[nb][2 * h], sum[nb][2 * h + 1]);
+  for (int e = 0; e < 32; e += 4)
+    *reinterpret_cast<float4*>(s_sum + (32 * (warp & 3) + lane) * kOuterPitch + 32 * (warp >> 2) + e) =
+        make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
   __syncthreads();
+  if (warp == 4) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
   if (C > 1) cluster_sync();
   const float scale = p.scale ? __ldg(p.scale + a) : 1.f;
   const int part = kRows / C;  // rows that this CTA joins and stores
@@ -1038,9 +1069,9 @@ cudaError_t launch_lora_outer(LoraOuter& p, bool by_rank, cudaStream_t s) {
   const int64_t items = p.n * ((p.rank + kOuterRank - 1) / kOuterRank);
   if (blocks == 0 || items == 0) return cudaSuccess;
   if (items > 65535) return cudaErrorInvalidValue;
-  // CTAs that share an adapter's tokens, until the grid fills the SMs
+  // CTAs that share an adapter's tokens, until every SM has one (until it has three: 8 us more of the 74 above)
   p.cluster = 1;
-  while (p.cluster < 8 && blocks * items * p.cluster < 3 * (int64_t)sm_count_current() && tiles / (2 * p.cluster) >= 2)
+  while (p.cluster < 8 && blocks * items * p.cluster < (int64_t)sm_count_current() && tiles / (2 * p.cluster) >= 2)
     p.cluster <<= 1;
   if (blocks * p.cluster >= (1ll << 31)) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(blocks * p.cluster), (unsigned)items);
@@ -1356,7 +1387,7 @@ nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t lddy, c
   if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
   e = launch_lora_plan(adapter, T, num_adapters, counts + num_adapters, counts, s);
   if (e != cudaSuccess) return cuda_fail(e, "adapter plan launch");
-  const uint32_t box = (uint32_t)(rs < lora::kOuterRank ? rs : lora::kOuterRank);
+  const uint32_t box = (uint32_t)lora::outer_box(rank);
   // S = A X for dB and U = B^T dY for dA, then the two gradients: within each pair the second launch needs nothing of
   // the first and runs beside it.
   const bool want[2] = {dB && R > 0, dA && K > 0};
@@ -1378,7 +1409,7 @@ nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t lddy, c
     if (st == NM_OK)
       st = make_tmap3(&p.tm_v, buf.as<uint16_t>(at_terms[which]), (uint64_t)rs, (uint64_t)T,
                       (uint64_t)planes, (uint64_t)rs * 2, (uint64_t)(T * rs) * 2, box, lora::kTok,
-                      box == 64 ? 128 : box == 32 ? 64 : box == 16 ? 32 : 0, "adapter terms");
+                      box == 64 ? 128 : box == 32 ? 64 : 32, "adapter terms");
     if (st != NM_OK) return st;
     p.rows = rows;
     p.out = which ? dA : dB;

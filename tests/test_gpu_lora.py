@@ -342,3 +342,11 @@ def test_refusals():
     with pytest.raises(nm.NmError) as e:
         nm.spmm_lora(*ok[:6], big_a, big_b, c.adapter)
     assert e.value.status == nm.NM_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kind", ["mixed", "runs"])
+@pytest.mark.parametrize("rank,dtype", [(20, F32), (40, BF), (100, F32)])
+def test_adapter_gradients_of_many_tokens(rank, kind, dtype):
+    """A dozen token tiles and more to every CTA of a cluster: several groups of products, ring slots taken again."""
+    c = Case(200, 96, 7003, 2, rank, kind, scaled=True, seed=rank)
+    c.check_grads(*c.grads(dtype))
