@@ -17,10 +17,11 @@
 // most half of the SM's shared memory where a cluster of eight allows it, so
 // that one CTA loads while the other computes.  Arithmetic is in packed float32
 // pairs.  768 x 50432 takes 35 us forward (floor 24 us) and 78 us backward
-// (36 us), bound by instruction issue: three passes over a piece of eight
-// tokens unpack it each time.  Tried and slower: persistent clusters that fetch
-// the next strip while they work on one (57 and 93 us), 512 threads a CTA (40
-// and 90 us), rows held in registers with one CTA to an SM (105 us forward).
+// (36 us), bound by a CTA's own phases (load, passes between barriers, store),
+// which one other CTA of the SM covers: 39 and 45 % of the cycles issue.  Tried
+// and slower: persistent clusters that fetch the next strip while they work on
+// one (57 and 93 us), 512 threads a CTA (40 and 90 us), rows held in registers
+// with one CTA to an SM (105 us forward).
 // Column sums go lanes -> warps -> CTA, and across the cluster through
 // distributed shared memory, every addition in a fixed order.  The forward
 // pass takes each CTA's own mean first and the squares about that, and joins
