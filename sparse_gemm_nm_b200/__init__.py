@@ -481,7 +481,10 @@ def spmm_xent(values, meta, n: int, m: int, K: int, X, target, idx=None, stream=
 
 def spmm_xent_grad(values, meta, n: int, m: int, K: int, X, target, lse, dloss, idx=None, need_dx: bool = True,
                    need_dv: bool = True, stream=None):
-    """(dX K x T, dV like values), bf16: gradients of sum(dloss * loss) of spmm_xent; None for one not needed."""
+    """(dX K x T, dV like values), bf16: gradients of sum(dloss * loss) of spmm_xent; None for one not needed.
+
+    As in spmm_t, rows of dX that idx never names are not written (a permutation names all).
+    """
     import torch
     _same_device(X, values, meta, target, lse, dloss, idx)
     R = _compressed(values, meta, n, m, K, idx)
