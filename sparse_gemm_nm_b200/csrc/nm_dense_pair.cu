@@ -295,6 +295,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
       const int tn = p.n_major ? tile % p.tiles_n : tile / p.tiles_m;
       const int64_t row = (int64_t)tm * 256 + 128 * rank + quarter * 32 + lane;
       const int64_t n0 = (int64_t)tn * 256;
+      // The positions of this row's survivors, on their way while the products are (asked for by each chunk of columns,
+      // they made the epilogue of 32000 x 4096 x 256 take 9 us a tile).
+      uint32_t word[2][8];
+      if (EPI == EPI_SURVIVORS && p.vec_out) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t* mb = p.meta + ((row >> 4) * p.meta_cblocks + (n0 >> 7) + c / 4) * 64 + 4 * (row & 7) + (c & 3);
+          const bool in = row < p.M && n0 + 32 * c < p.N;
+          word[0][c] = in ? __ldg(mb) : 0u;
+          word[1][c] = in ? __ldg(mb + 32) : 0u;
+        }
+      }
       ok = mbar_wait(&acc_full[ab], (uint32_t)(i >> 1) & 1u, abort_flag, p.status, kWaitNs);
       if (!ok) break;
       tc_fence_after();
@@ -395,9 +407,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
           // 2:4: the chunk's eight groups take their nibbles from two tiled metadata words (column
           // halves h = 0, 1 of the chunk's 32-column quarter q); the sixteen survivors are picked from
           // registers and stored as 32 (bf16) or 64 (fp32) contiguous bytes of the row.
-          const uint32_t* mb =
-              p.meta + ((row >> 4) * p.meta_cblocks + (col0 >> 7)) * 64 + 4 * (row & 7) + ((col0 >> 5) & 3);
-          const uint32_t wh[2] = {__ldg(mb), __ldg(mb + 32)};
+          uint32_t wh[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // (c runs in a loop: a choice, not an index)
+            const uint32_t a = c & 1 ? word[h][1] : word[h][0], b = c & 1 ? word[h][3] : word[h][2];
+            const uint32_t d = c & 1 ? word[h][5] : word[h][4], e = c & 1 ? word[h][7] : word[h][6];
+            wh[h] = c & 4 ? (c & 2 ? e : d) : (c & 2 ? b : a);
+          }
           const int sh = 16 * (int)((row >> 3) & 1);
           float o[16];
 #pragma unroll
