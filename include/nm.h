@@ -521,7 +521,7 @@ NM_API nm_status nm_spmm_xent_grad(const uint16_t* values, const uint32_t* meta,
  * request's tokens or adapter stays in its columns.  Results repeat bit for
  * bit.  At most 4194240 tokens a call (NM_ERR_UNSUPPORTED).
  * Where a two-SM GEMM serves the projection (nm_spmm_lora: as for nm_spmm_xent;
- * nm_spmm_lora_t: always) and num_adapters * rank <= 2048, the adapters are
+ * nm_spmm_lora_t: always) and num_adapters * rank <= 512, the adapters are
  * further reduction steps of that GEMM ("inside" below): their second factors
  * are laid side by side first, and a last pass redoes the columns of tokens
  * that met an Inf or NaN of another adapter there.  Otherwise the adapters'

@@ -350,3 +350,14 @@ def test_adapter_gradients_of_many_tokens(rank, kind, dtype):
     """A dozen token tiles and more to every CTA of a cluster: several groups of products, ring slots taken again."""
     c = Case(200, 96, 7003, 2, rank, kind, scaled=True, seed=rank)
     c.check_grads(*c.grads(dtype))
+
+
+@pytest.mark.parametrize("T,permuted", [(1, False), (5, True), (37, False)])
+def test_few_tokens_of_a_large_projection(T, permuted):
+    """Stages enough for every SM: X goes through rows of 16 or 48 tokens before the skinny GEMM."""
+    c = Case(13824, 2816, T, 3, 8, "mixed", permuted=permuted, scaled=True, seed=61)
+    for dtype in (BF, F32):
+        y = c.forward(dtype)
+        torch.cuda.synchronize()
+        nm.nm_device_status()
+        c.check_forward(y)
