@@ -12,7 +12,8 @@
 // logits would be 262 MB written and read); elsewhere the vocabulary is taken in
 // pieces of rows whose logits xent_pairs_kernel reads, 256 rows to a pair.
 // Backward: the logits of a piece are computed again and become G (bf16, rounded
-// once: it is an operand of the tensor cores like the dY of nm_spmm_t), again in
+// once: it is an operand of the tensor cores like the dY of nm_spmm_t; two terms
+// for up to 128 tokens, see run_xent_grad), again in
 // the SM-pair GEMM's epilogue where that serves; G meets the decompressed piece
 // of W' in a product that adds to a K x T fp32 accumulator, and Xp in the
 // survivor-sampled product for dV.  The accumulator takes one addition per
@@ -147,14 +148,16 @@ __global__ void __launch_bounds__(256) xent_columns_kernel(const int32_t* target
 }
 
 // G = dloss (exp(z - lse) - [row == target]) of a logits piece, bf16; 0 where the target is outside [0, R).
-// Columns T .. ldg - 1 (padding to whole 16-byte pieces) are written as 0.
+// Columns T .. width - 1 (padding to whole 16-byte pieces) are written as 0.  TWO: what the rounding left over follows, as
+// a second bf16 term, in columns width .. 2 width - 1.
+template <bool TWO>
 __global__ void __launch_bounds__(256) xent_g_kernel(const float* Z, int64_t ldz, int64_t rows, int64_t T, int64_t R,
                                                      int64_t v0, const int32_t* target, const float* lse,
-                                                     const float* dloss, uint16_t* G, int64_t ldg) {
+                                                     const float* dloss, uint16_t* G, int64_t ldg, int64_t width) {
   using namespace xent;
   pdl_gate();
   const int64_t t = ((int64_t)blockIdx.x * 32 + (threadIdx.x & 31)) * 2;
-  if (t >= ldg) return;
+  if (t >= width) return;
   float l[2], d[2];
   int64_t want[2];
   for (int j = 0; j < 2; ++j) {
@@ -170,13 +173,21 @@ __global__ void __launch_bounds__(256) xent_g_kernel(const float* Z, int64_t ldz
     float g[2] = {0.f, 0.f};
     if (has0) g[0] = d[0] * (exp2f((__ldcg(Z + r * ldz + t) - l[0]) * kLog2e) - (r == want[0] ? 1.f : 0.f));
     if (has1) g[1] = d[1] * (exp2f((__ldcg(Z + r * ldz + t + 1) - l[1]) * kLog2e) - (r == want[1] ? 1.f : 0.f));
-    *reinterpret_cast<uint32_t*>(G + r * ldg + t) = pack_bf16x2(g[0], g[1]);
+    const uint32_t hi = pack_bf16x2(g[0], g[1]);
+    *reinterpret_cast<uint32_t*>(G + r * ldg + t) = hi;
+    if (TWO) {  // nothing is left over of an Inf or NaN
+      const float lo0 = (hi & 0x7F80u) == 0x7F80u ? 0.f : g[0] - __uint_as_float(hi << 16);
+      const float lo1 = (hi & 0x7F800000u) == 0x7F800000u ? 0.f : g[1] - __uint_as_float(hi & 0xFFFF0000u);
+      *reinterpret_cast<uint32_t*>(G + r * ldg + width + t) = pack_bf16x2(lo0, lo1);
+    }
   }
 }
 
-// dX[idx[k]] (dX[k] without idx) = the accumulator's row k, rounded to bf16; rows mapped outside [0, K) are dropped.
-__global__ void __launch_bounds__(256) xent_round_kernel(const float* acc, int ranges, int64_t lda, int64_t K, int64_t T,
-                                                         const int32_t* idx, uint16_t* dX, int64_t lddx) {
+// dX[idx[k]] (dX[k] without idx) = the accumulators' rows k, rounded to bf16; rows mapped outside [0, K) are dropped.
+// `parts` sums are added in order: `terms` column blocks of `width` columns in each of the ranges' accumulators.
+__global__ void __launch_bounds__(256) xent_round_kernel(const float* acc, int parts, int terms, int64_t width,
+                                                         int64_t lda, int64_t K, int64_t T, const int32_t* idx,
+                                                         uint16_t* dX, int64_t lddx) {
   pdl_gate();
   const int64_t pieces = (T + 7) / 8, total = K * pieces;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
@@ -185,10 +196,11 @@ __global__ void __launch_bounds__(256) xent_round_kernel(const float* acc, int r
     if (row < 0 || row >= K) continue;
     const float* a = acc + k * lda + t;
     uint16_t* d = dX + row * lddx + t;
+    auto part = [&](int q) { return a + q / terms * K * lda + q % terms * width; };
     if (t + 8 <= T) {
       float4 x = __ldcg(reinterpret_cast<const float4*>(a)), y = __ldcg(reinterpret_cast<const float4*>(a) + 1);
-      for (int i = 1; i < ranges; ++i) {
-        const float4* b = reinterpret_cast<const float4*>(a + i * K * lda);
+      for (int q = 1; q < parts; ++q) {
+        const float4* b = reinterpret_cast<const float4*>(part(q));
         const float4 u = __ldcg(b), v = __ldcg(b + 1);
         x.x += u.x;
         x.y += u.y;
@@ -204,7 +216,7 @@ __global__ void __launch_bounds__(256) xent_round_kernel(const float* acc, int r
     } else {
       for (int j = 0; t + j < T; ++j) {
         float x = __ldcg(a + j);
-        for (int i = 1; i < ranges; ++i) x += __ldcg(a + i * K * lda + j);
+        for (int q = 1; q < parts; ++q) x += __ldcg(part(q) + j);
         d[j] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xFFFFu);
       }
     }
@@ -327,22 +339,40 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
   nm_status st = gather_input(h, idx, xp, s);
   if (st != NM_OK) return st;
   const bool fused = spmm_pair_serves(h.values, h.meta, h.n, h.m, h.K, h.T);
-  const int64_t rows = piece_rows(h.R, h.T, fused ? 2 : 4), ldz = (h.T + 3) / 4 * 4, ldg = (h.T + 7) / 8 * 8;
+  const int64_t rows = piece_rows(h.R, h.T, fused ? 2 : 4), ldz = (h.T + 3) / 4 * 4, width = (h.T + 7) / 8 * 8;
   const int64_t ldk = (h.K + 7) / 8 * 8;
   const int ranges = dense_t_ranges(rows < h.R ? rows : h.R, h.K, h.T);
+  // With few tokens a sum has few terms, and the rounding of G to bf16 can be half again the rounding of the result
+  // (149 x 3224 x 28: 2.5e-3 of the gradients instead of 1.7e-3).  Up to 128 tokens G's two terms fit the one column tile
+  // of dX and its 128-deep reduction steps nearly so, and cost next to nothing; above, errors average out.
+  const bool two = !fused && h.T <= 128;
+  const int terms = two ? 2 : 1;
+  const int64_t ldg = terms * width, lda = two ? ldg : ldz, tokens = two ? ldg : h.T;  // of the products
   PairEpiData epi = {};
   epi.mode = PAIR_EPI_XGRAD;
   if (fused) st = column_data(h, target, lse, dloss, epi, cols, s);
   if (st != NM_OK) return st;
   Parts parts;
   const int64_t at_g = parts.take(rows * ldg * 2), at_z = parts.take(fused ? 0 : rows * ldz * 4);
-  const int64_t at_wd = parts.take(dX ? rows * ldk * 2 : 0), at_acc = parts.take(dX ? ranges * h.K * ldz * 4 : 0);
+  const int64_t at_wd = parts.take(dX ? rows * ldk * 2 : 0), at_acc = parts.take(dX ? ranges * h.K * lda * 4 : 0);
+  const int64_t at_x2 = parts.take(two && dV ? h.K * ldg * 2 : 0);
   cudaError_t e = buf.get(parts.size());
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gradient piece");
   uint16_t* g = buf.as<uint16_t>(at_g);
   uint16_t* wd = buf.as<uint16_t>(at_wd);
   float* z = buf.as<float>(at_z);
   float* acc = buf.as<float>(at_acc);
+  const uint16_t* x = h.X;  // of the value gradient: once for each term of G
+  int64_t ldx = h.ldx;
+  if (two && dV) {
+    uint16_t* x2 = buf.as<uint16_t>(at_x2);
+    for (int q = 0; q < 2; ++q) {
+      e = launch_gather_rows(h.X, h.ldx, nullptr, h.K, h.T, x2 + q * width, ldg, s, nullptr, q > 0);
+      if (e != cudaSuccess) return cuda_fail(e, "input copy launch");
+    }
+    x = x2;
+    ldx = ldg;
+  }
   for (int64_t v0 = 0; v0 < h.R; v0 += rows) {
     const int64_t n = h.R - v0 < rows ? h.R - v0 : rows;
     if (fused) {  // the GEMM's epilogue turns the logits into G
@@ -354,8 +384,9 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
       st = spmm_rows(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, z, ldz, NM_OUT_F32,
                      s);
       if (st != NM_OK) return st;
-      e = launch_pdl(xent_g_kernel, dim3((unsigned)((ldg / 2 + 31) / 32), (unsigned)((n + 63) / 64)), dim3(256), 0, s,
-                     (const float*)z, ldz, n, h.T, h.R, v0, target, lse, dloss, g, ldg);
+      const dim3 grid((unsigned)((width / 2 + 31) / 32), (unsigned)((n + 63) / 64));
+      e = launch_pdl(two ? xent_g_kernel<true> : xent_g_kernel<false>, grid, dim3(256), 0, s, (const float*)z, ldz, n, h.T,
+                     h.R, v0, target, lse, dloss, g, ldg, width);
       count_launch();
       if (e != cudaSuccess) return cuda_fail(e, "cross-entropy gradient launch");
     }
@@ -363,11 +394,11 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
       // beside the launch that makes G
       e = launch_decompress(h.row_values(v0), h.row_meta(v0), n, h.K, h.n, h.m, wd, ldk, s, true);
       if (e != cudaSuccess) return cuda_fail(e, "decompress launch");
-      st = dense_t_accumulate(wd, ldk, n, h.K, g, ldg, h.T, acc, ldz, ranges, v0 > 0, s);
+      st = dense_t_accumulate(wd, ldk, n, h.K, g, ldg, tokens, acc, lda, ranges, v0 > 0, s);
       if (st != NM_OK) return st;
     }
     if (dV) {
-      st = run_sddmm(h.row_meta(v0), h.n, h.m, n, h.K, nullptr, g, ldg, h.X, h.ldx, h.T,
+      st = run_sddmm(h.row_meta(v0), h.n, h.m, n, h.K, nullptr, g, ldg, x, ldx, tokens,
                      dV + v0 * value_cols(h.K, h.n, h.m), NM_OUT_BF16, s, dX != nullptr);
       if (st != NM_OK) return st;
     }
@@ -375,7 +406,7 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
   if (dX) {
     const int64_t want = (h.K * ((h.T + 7) / 8) + 255) / 256, cap = (int64_t)sm_count_current() * 16;
     e = launch_pdl(xent_round_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, s,
-                   (const float*)acc, ranges, ldz, h.K, h.T, idx, dX, lddx);
+                   (const float*)acc, ranges * terms, terms, width, lda, h.K, h.T, idx, dX, lddx);
     count_launch();
     if (e != cudaSuccess) return cuda_fail(e, "gradient rounding launch");
   }
