@@ -481,7 +481,7 @@ NM_API nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int 
  * dV = the survivors' entries of G Xp^T as nm_sddmm gives them.  The logits
  * of a piece of the vocabulary are computed again (on the two-SM GEMM its
  * epilogue writes G and no logits); G is rounded to bf16, as the dY of those
- * calls is (up to 128 tokens: two bf16 terms); dX adds up in fp32 over the pieces.
+ * calls is (up to 256 tokens outside the two-SM GEMM: two bf16 terms); dX adds up in fp32 over the pieces.
  *   target, lse, dloss [in] T each (int32, fp32, fp32); lse from nm_spmm_xent
  *   dX  [out] K x T bf16, row stride lddx >= T, 16-byte rows, or NULL.  With
  *       idx, rows as in nm_spmm_t (repeated entries are not supported, rows

@@ -13,7 +13,7 @@
 // pieces of rows whose logits xent_pairs_kernel reads, 256 rows to a pair.
 // Backward: the logits of a piece are computed again and become G (bf16, rounded
 // once: it is an operand of the tensor cores like the dY of nm_spmm_t; two terms
-// for up to 128 tokens, see run_xent_grad), again in
+// for up to 256 tokens, see run_xent_grad), again in
 // the SM-pair GEMM's epilogue where that serves; G meets the decompressed piece
 // of W' in a product that adds to a K x T fp32 accumulator, and Xp in the
 // survivor-sampled product for dV.  The accumulator takes one addition per
@@ -341,13 +341,13 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
   const bool fused = spmm_pair_serves(h.values, h.meta, h.n, h.m, h.K, h.T);
   const int64_t rows = piece_rows(h.R, h.T, fused ? 2 : 4), ldz = (h.T + 3) / 4 * 4, width = (h.T + 7) / 8 * 8;
   const int64_t ldk = (h.K + 7) / 8 * 8;
-  const int ranges = dense_t_ranges(rows < h.R ? rows : h.R, h.K, h.T);
   // With few tokens a sum has few terms, and the rounding of G to bf16 can be half again the rounding of the result
   // (149 x 3224 x 28: 2.5e-3 of the gradients instead of 1.7e-3).  Up to 128 tokens G's two terms fit the one column tile
-  // of dX and its 128-deep reduction steps nearly so, and cost next to nothing; above, errors average out.
-  const bool two = !fused && h.T <= 128;
+  // of dX, up to 256 two, and the steps of dV hide behind its epilogue, so they cost little; above, errors average out.
+  const bool two = !fused && h.T <= 256;
   const int terms = two ? 2 : 1;
   const int64_t ldg = terms * width, lda = two ? ldg : ldz, tokens = two ? ldg : h.T;  // of the products
+  const int ranges = dense_t_ranges(rows, h.K, tokens);
   PairEpiData epi = {};
   epi.mode = PAIR_EPI_XGRAD;
   if (fused) st = column_data(h, target, lse, dloss, epi, cols, s);
