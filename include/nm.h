@@ -466,8 +466,9 @@ NM_API nm_status nm_layer_norm_grad(const void* dY, int64_t lddy, nm_out_dtype d
  *   loss, lse [out] T fp32 each
  * Results repeat bit for bit.  Staged from the library's pool: the pairs (8 bytes
  * per token and 32 or 256 rows of W), Xp with idx, what nm_spmm stages, and
- * outside the two-SM GEMM a piece of fp32 logits (at most 8192 rows, about 64
- * MB; 256 rows at least).
+ * outside the two-SM GEMM a piece of fp32 logits (about 64 MB; 256 rows at
+ * least) and, for K % 128 != 0 or T >= 192, the piece's decompressed weights (at
+ * most 256 MB, or 256 rows).
  * Errors: as nm_spmm_permuted.
  */
 NM_API nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
@@ -488,9 +489,9 @@ NM_API nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int 
  *       that no entry names are not written)
  *   dV  [out] R x nm_value_cols(K,n,m) bf16, or NULL (a frozen head); not both
  * Results repeat bit for bit.  Staged from the library's pool: a piece of G (and
- * of fp32 logits, outside the two-SM GEMM), 12 bytes per token, with dX the
- * piece's decompressed weights and one to eight K x T fp32 accumulators, and Xp
- * with idx.
+ * of fp32 logits, outside the two-SM GEMM), 12 bytes per token, with dX (and
+ * there) the piece's decompressed weights, one to eight K x T fp32 accumulators, X
+ * twice where G has two terms, and Xp with idx.
  * Errors: as nm_spmm_t.
  */
 NM_API nm_status nm_spmm_xent_grad(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,

@@ -1075,6 +1075,31 @@ nm_status dense_t_accumulate(const uint16_t* W, int64_t ldw, int64_t R, int64_t 
   return NM_OK;
 }
 
+nm_status dense_product(const uint16_t* W, int64_t ldw, int64_t R, int64_t K, const uint16_t* X, int64_t ldx, int64_t T,
+                        float* C, int64_t ldc, cudaStream_t stream) {
+  DenseParams p;
+  std::memset(&p, 0, sizeof p);
+  p.M = R;
+  p.N = T;
+  p.Kr = K;
+  p.k_tiles = (K + 127) / 128;
+  p.tiles_m = (int)((R + 255) / 256);
+  p.tiles_n = (int)((T + 255) / 256);
+  if ((int64_t)p.tiles_m * p.tiles_n >= (1ll << 31)) return fail(NM_ERR_UNSUPPORTED, "too many tiles");
+  p.num_tiles = p.tiles_m * p.tiles_n;
+  p.status = status_word_ptr();
+  if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
+  p.out = C;
+  p.ldo = ldc;
+  p.out_f32 = 1;
+  nm_status st = make_tmap(&p.tm_a, W, (uint64_t)K, (uint64_t)R, (uint64_t)ldw * 2, 64, 64, 128, "W' (dense)");
+  if (st == NM_OK) st = make_tmap(&p.tm_b, X, (uint64_t)T, (uint64_t)K, (uint64_t)ldx * 2, 64, 64, 128, "X");
+  if (st == NM_OK) st = set_store_map(p, C, R, ldc, ldc, true);  // ldc % 4 == 0; columns past T get zeros
+  if (st != NM_OK) return st;
+  cudaError_t e = launch_dense_pair(p, false, true, EPI_STORE, stream);
+  return e == cudaSuccess ? NM_OK : cuda_fail(e, "dense GEMM launch");
+}
+
 nm_status check_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,
                        const uint16_t* dY, int64_t lddy, int64_t T, void* dX, int64_t lddx, nm_out_dtype dtype) {
   nm_status st = check_bwd_common(n, m, R, K, T, dtype);

@@ -78,6 +78,9 @@ nm_status run_sddmm(const uint32_t* meta, int n, int m, int64_t R, int64_t K, co
                     cudaStream_t stream, bool beside = false);  // beside: as GemmPartials' (without idx)
 // C (K x T fp32, row stride ldc) = or += W^T D for a dense R x K bf16 W (row stride ldw) and an R x T bf16 D, by
 // the SM-pair GEMM; every element takes one addition.
+// dense_product: C (R x T fp32, row stride ldc) = W X, X K x T.
+nm_status dense_product(const uint16_t* W, int64_t ldw, int64_t R, int64_t K, const uint16_t* X, int64_t ldx, int64_t T,
+                        float* C, int64_t ldc, cudaStream_t stream);
 // With ranges > 1 the rows of W and D are taken in that many ranges side by side, range i's sum in C + i K ldc.
 int dense_t_ranges(int64_t R, int64_t K, int64_t T);  // that fill the SMs
 nm_status dense_t_accumulate(const uint16_t* W, int64_t ldw, int64_t R, int64_t K, const uint16_t* D, int64_t ldd,

@@ -249,12 +249,20 @@ nm_status check_head(int n, int m, int64_t R, int64_t K, int64_t T) {
 
 // Rows of one piece: a multiple of 256 that takes about 64 MB (fp32 logits, or bf16 gradients where no logits are
 // written), so that it stays in L2.
-int64_t piece_rows(int64_t R, int64_t T, int64_t bytes = 4) {
+int64_t piece_rows(int64_t R, int64_t K, int64_t T, int64_t bytes = 4) {
   int64_t rows = (64ll << 20) / bytes / (T > 0 ? T : 1) / 256 * 256;
+  const int64_t weights = (256ll << 20) / (2 * K) / 256 * 256;  // of a piece, where they are decompressed
+  if (rows > weights) rows = weights;
   if (rows < 256) rows = 256;
   if (rows > (1 << 21)) rows = 1 << 21;  // the element-wise kernels' grids: 64 rows a block, 65535 blocks
   return rows < R ? rows : R;
 }
+
+// Where only the one-SM GEMM serves a shape, a piece's logits are the dense product of its decompressed weights, except
+// for whole 128-deep stages and few tokens, whose weights that GEMM streams by TMA (forward of 15 x 3592 x 876 175 us with
+// the one-SM GEMM and 30 dense, 8980 x 216 x 8192 474 and 221, 20482 x 128 x 5443 344 and 308; 32000 x 4096 x 100 100 and
+// 161; gradients of 149 x 3224 x 28 245 and 80).
+bool dense_logits(int64_t K, int64_t T) { return K % 128 != 0 || T >= 192; }
 
 // Xp[k] = X[idx[k]] when there is an index map.
 nm_status gather_input(Head& h, const int32_t* idx, Staged& staged, cudaStream_t s) {
@@ -288,7 +296,7 @@ nm_status column_data(const Head& h, const int32_t* target, const float* lse, co
 }
 
 nm_status run_xent(Head h, const int32_t* idx, const int32_t* target, float* loss, float* lse, cudaStream_t s) {
-  Staged xp(s), work(s), z(s), ws(s), cols(s);
+  Staged xp(s), work(s), buf(s), ws(s), cols(s);
   nm_status st = gather_input(h, idx, xp, s);
   if (st != NM_OK) return st;
   const bool fused = spmm_pair_serves(h.values, h.meta, h.n, h.m, h.K, h.T);
@@ -309,19 +317,30 @@ nm_status run_xent(Head h, const int32_t* idx, const int32_t* target, float* los
       st = run_spmm_epilogue(h.values, h.meta, h.n, h.m, h.R, h.K, h.X, h.ldx, h.T, nullptr, 0, epi, s);
     if (st != NM_OK) return st;
   } else {
-    const int64_t rows = piece_rows(h.R, h.T), ldz = (h.T + 3) / 4 * 4;
-    e = z.get((size_t)(rows * ldz * 4));
+    const bool dense = dense_logits(h.K, h.T);
+    const int64_t rows = piece_rows(h.R, h.K, h.T), ldz = (h.T + 3) / 4 * 4, ldk = (h.K + 7) / 8 * 8;
+    Parts parts;
+    const int64_t at_z = parts.take(rows * ldz * 4), at_wd = parts.take(dense ? rows * ldk * 2 : 0);
+    e = buf.get(parts.size());
     if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the logits piece");
+    float* z = buf.as<float>(at_z);
+    uint16_t* wd = buf.as<uint16_t>(at_wd);
     for (int64_t v0 = 0; v0 < h.R; v0 += rows) {
       const int64_t n = h.R - v0 < rows ? h.R - v0 : rows;
       ws.release();
       GemmPartials raw{&ws, false, 1, 0, 0};
-      st = run_spmm(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, nullptr, h.X, h.ldx, h.T, z.as<float>(), ldz,
-                    NM_OUT_F32, &raw, s);
+      if (dense) {
+        e = launch_decompress(h.row_values(v0), h.row_meta(v0), n, h.K, h.n, h.m, wd, ldk, s);
+        if (e != cudaSuccess) return cuda_fail(e, "decompress launch");
+        st = dense_product(wd, ldk, n, h.K, h.X, h.ldx, h.T, z, ldz, s);
+      } else {
+        st = run_spmm(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, nullptr, h.X, h.ldx, h.T, z, ldz, NM_OUT_F32,
+                      &raw, s);
+      }
       if (st != NM_OK) return st;
       const bool split = raw.splits > 1;
       e = launch_pdl(xent_pairs_kernel, dim3(tb, (unsigned)((n + per - 1) / per)), dim3(256), 0, s,
-                     (const float*)(split ? ws.as<float>() : z.as<float>()), raw.splits, raw.split_stride,
+                     (const float*)(split ? ws.as<float>() : z), raw.splits, raw.split_stride,
                      split ? raw.ld : ldz, n, h.T, v0, target, part, z_target);
       count_launch();
       if (e != cudaSuccess) return cuda_fail(e, "cross-entropy launch");
@@ -339,7 +358,8 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
   nm_status st = gather_input(h, idx, xp, s);
   if (st != NM_OK) return st;
   const bool fused = spmm_pair_serves(h.values, h.meta, h.n, h.m, h.K, h.T);
-  const int64_t rows = piece_rows(h.R, h.T, fused ? 2 : 4), ldz = (h.T + 3) / 4 * 4, width = (h.T + 7) / 8 * 8;
+  const bool dense = !fused && dense_logits(h.K, h.T);
+  const int64_t rows = piece_rows(h.R, h.K, h.T, fused ? 2 : 4), ldz = (h.T + 3) / 4 * 4, width = (h.T + 7) / 8 * 8;
   const int64_t ldk = (h.K + 7) / 8 * 8;
   // With few tokens a sum has few terms, and the rounding of G to bf16 can be half again the rounding of the result
   // (149 x 3224 x 28: 2.5e-3 of the gradients instead of 1.7e-3).  Up to 128 tokens G's two terms fit the one column tile
@@ -354,7 +374,7 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
   if (st != NM_OK) return st;
   Parts parts;
   const int64_t at_g = parts.take(rows * ldg * 2), at_z = parts.take(fused ? 0 : rows * ldz * 4);
-  const int64_t at_wd = parts.take(dX ? rows * ldk * 2 : 0), at_acc = parts.take(dX ? ranges * h.K * lda * 4 : 0);
+  const int64_t at_wd = parts.take(dX || dense ? rows * ldk * 2 : 0), at_acc = parts.take(dX ? ranges * h.K * lda * 4 : 0);
   const int64_t at_x2 = parts.take(two && dV ? h.K * ldg * 2 : 0);
   cudaError_t e = buf.get(parts.size());
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gradient piece");
@@ -381,8 +401,13 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
                              epi, s);
       if (st != NM_OK) return st;
     } else {
-      st = spmm_rows(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, z, ldz, NM_OUT_F32,
-                     s);
+      if (dense) {
+        e = launch_decompress(h.row_values(v0), h.row_meta(v0), n, h.K, h.n, h.m, wd, ldk, s);
+        if (e != cudaSuccess) return cuda_fail(e, "decompress launch");
+        st = dense_product(wd, ldk, n, h.K, h.X, h.ldx, h.T, z, ldz, s);
+      } else {
+        st = spmm_rows(h.row_values(v0), h.row_meta(v0), h.n, h.m, n, h.K, h.X, h.ldx, h.T, z, ldz, NM_OUT_F32, s);
+      }
       if (st != NM_OK) return st;
       const dim3 grid((unsigned)((width / 2 + 31) / 32), (unsigned)((n + 63) / 64));
       e = launch_pdl(two ? xent_g_kernel<true> : xent_g_kernel<false>, grid, dim3(256), 0, s, (const float*)z, ldz, n, h.T,
@@ -391,8 +416,7 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
       if (e != cudaSuccess) return cuda_fail(e, "cross-entropy gradient launch");
     }
     if (dX) {
-      // beside the launch that makes G
-      e = launch_decompress(h.row_values(v0), h.row_meta(v0), n, h.K, h.n, h.m, wd, ldk, s, true);
+      if (!dense) e = launch_decompress(h.row_values(v0), h.row_meta(v0), n, h.K, h.n, h.m, wd, ldk, s, true);  // beside G's launch
       if (e != cudaSuccess) return cuda_fail(e, "decompress launch");
       st = dense_t_accumulate(wd, ldk, n, h.K, g, ldg, tokens, acc, lda, ranges, v0 > 0, s);
       if (st != NM_OK) return st;
