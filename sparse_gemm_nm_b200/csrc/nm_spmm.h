@@ -30,10 +30,10 @@ enum PairEpi : int {
 // Per-column data of the last two, each padded with anything to a whole number of tiles and on 16 bytes.
 struct PairEpiData {
   int mode;
-  float2* part;         // LSE: [ceil(R / 32)][T], (max, sum 2^(y log2 e - max)), the max times log2 e
+  float2* part;         // LSE: [ceil(R / 32)][T], (max, sum exp(y - max))
   float* z_target;      // LSE: y[target] of the columns whose target lies in the rows
   const int32_t* target;  // the column's row (relative to the whole vocabulary), negative for none
-  const float* lse2;    // XGRAD: lse times log2 e
+  const float* lse;     // XGRAD
   const float* d;       // XGRAD: the column's factor, 0 for a column without a target
   int64_t row0;         // row 0 of Y within the vocabulary
 };

@@ -64,7 +64,8 @@
 // the sum of exponentials of each 32 rows (a warp's, joined between lanes) and
 // the target's logit; no Y is written.
 // XGRAD turns the logits into G = dloss (exp(z - lse) - [target]) and stores it
-// as a bf16 Y.  Exponentials are of base 2, one multiplication and one ex2 each.
+// as a bf16 Y.  Differences are taken before they are scaled for ex2, so that a
+// dominant logit's exponential is exactly 1.
 //
 // Further reduction steps (EXT).  Adapters side by side (nm_lora.cu) are dense
 // products: after a tile's sparse stages, half-stages of 64 rank rows follow for
@@ -126,10 +127,11 @@ struct Cfg {
 };
 }  // namespace pair
 
-// (max, sum) of two sets of terms as one; maxima and exponents in powers of two.
+// (max, sum of exponentials) of two sets of terms as one.
+constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ void join_pair(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
-  s = s * exp2_fast(m - top) + s2 * exp2_fast(m2 - top);
+  s = s * exp2_fast((m - top) * kLog2e) + s2 * exp2_fast((m2 - top) * kLog2e);
   m = top;
 }
 
@@ -140,7 +142,6 @@ __device__ __forceinline__ void join_pair(float& m, float& s, float m2, float s2
 template <int NB, typename Release>
 __device__ __forceinline__ void lse_epilogue(const SpmmParams& p, uint32_t t_addr, int64_t wrow0, int64_t n0, int lane,
                                              Release release) {
-  constexpr float kLog2e = 1.4426950408889634f;
   const bool ragged = wrow0 + 32 > p.R;
 #pragma unroll 1
   for (int c = 0; c < NB; ++c) {
@@ -178,10 +179,9 @@ __device__ __forceinline__ void lse_epilogue(const SpmmParams& p, uint32_t t_add
       const int i = 4 * (v >> 1) + (v & 1);
       const float z0 = __uint_as_float(lo[i]), z1 = __uint_as_float(lo[i + 2]);
       const float z2 = __uint_as_float(hi[i]), z3 = __uint_as_float(hi[i + 2]);
-      m[v] = fmaxf(fmaxf(fmaxf(z0, z1), fmaxf(z2, z3)), -3.0e38f) * kLog2e;
-      m[v] = fmaxf(m[v], -3.0e38f);  // finite: (-inf) - (-inf) must not arise
-      s[v] = (exp2_fast(fmaf(z0, kLog2e, -m[v])) + exp2_fast(fmaf(z1, kLog2e, -m[v]))) +
-             (exp2_fast(fmaf(z2, kLog2e, -m[v])) + exp2_fast(fmaf(z3, kLog2e, -m[v])));
+      m[v] = fmaxf(fmaxf(fmaxf(z0, z1), fmaxf(z2, z3)), -3.0e38f);  // finite: (-inf) - (-inf) must not arise
+      s[v] = (exp2_fast((z0 - m[v]) * kLog2e) + exp2_fast((z1 - m[v]) * kLog2e)) +
+             (exp2_fast((z2 - m[v]) * kLog2e) + exp2_fast((z3 - m[v]) * kLog2e));
     }
 #pragma unroll
     for (int half = 4; half > 0; half >>= 1) {
@@ -205,18 +205,17 @@ __device__ __forceinline__ void lse_epilogue(const SpmmParams& p, uint32_t t_add
 
 // The gradient of 32 columns of one logits row per lane: v becomes d (exp(v - lse) - [row == target]).
 __device__ __forceinline__ void xgrad_block(const SpmmParams& p, uint32_t (&v)[32], int64_t wrow0, int64_t t0, int lane) {
-  constexpr float kLog2e = 1.4426950408889634f;
   const int32_t want = __ldg(p.epi.target + t0 + lane);
   const uint32_t at = (uint32_t)(want - p.epi.row0 - wrow0);
-  const float4* l4 = reinterpret_cast<const float4*>(p.epi.lse2 + t0);
+  const float4* l4 = reinterpret_cast<const float4*>(p.epi.lse + t0);
   const float4* d4 = reinterpret_cast<const float4*>(p.epi.d + t0);
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     const float4 l = __ldg(l4 + q);
-    v[4 * q] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(v[4 * q]), kLog2e, -l.x)));
-    v[4 * q + 1] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(v[4 * q + 1]), kLog2e, -l.y)));
-    v[4 * q + 2] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(v[4 * q + 2]), kLog2e, -l.z)));
-    v[4 * q + 3] = __float_as_uint(exp2_fast(fmaf(__uint_as_float(v[4 * q + 3]), kLog2e, -l.w)));
+    v[4 * q] = __float_as_uint(exp2_fast((__uint_as_float(v[4 * q]) - l.x) * kLog2e));
+    v[4 * q + 1] = __float_as_uint(exp2_fast((__uint_as_float(v[4 * q + 1]) - l.y) * kLog2e));
+    v[4 * q + 2] = __float_as_uint(exp2_fast((__uint_as_float(v[4 * q + 2]) - l.z) * kLog2e));
+    v[4 * q + 3] = __float_as_uint(exp2_fast((__uint_as_float(v[4 * q + 3]) - l.w) * kLog2e));
   }
   if (__ballot_sync(0xFFFFFFFFu, want >= 0 && at < 32u)) {
 #pragma unroll

@@ -7,7 +7,11 @@
 //   dX = (W' Pi)^T G,  dV = the survivors' entries of G Xp^T.
 // Forward: every group of rows leaves a pair (max, sum of exp(z - max)) per
 // token, and the token's target row its logit; one last pass joins the pairs in
-// order.  On shapes of the SM-pair GEMM its epilogue makes the pairs of 32 rows
+// order.  The maxima are logits as they are, and differences are taken before
+// anything is scaled: the largest term of a sum is then exactly 1, and
+// loss = (max - z[target]) + log(sum) has no rounding of the size of the logits
+// and is never negative (lse - z[target] of scaled sums was off by 1.5e-5, and
+// below 0, for logits of 200).  On shapes of the SM-pair GEMM its epilogue makes the pairs of 32 rows
 // from the accumulator in TMEM, and no logit is written (32000 x 4096 x 2048
 // logits would be 262 MB written and read); elsewhere the vocabulary is taken in
 // pieces of rows whose logits xent_pairs_kernel reads, 256 rows to a pair.
@@ -43,8 +47,8 @@ constexpr int kPairRows = 256;  // logits rows joined into one (max, sum) pair b
 constexpr float kLog2e = 1.4426950408889634f;
 }  // namespace xent
 
-// part[pair][t] = (max, sum 2^(z log2 e - max)) over one pair's kPairRows rows of the logits piece, the max times log2 e;
-// the rows of targets write their logit.  Z is the sum of `splits` matrices.  One block: 32 tokens, one pair.
+// part[pair][t] = (max, sum exp(z - max)) over one pair's kPairRows rows of the logits piece; the rows of targets write
+// their logit.  Z is the sum of `splits` matrices.  One block: 32 tokens, one pair.
 __global__ void __launch_bounds__(256) xent_pairs_kernel(const float* Z, int splits, int64_t split_stride, int64_t ldz,
                                                          int64_t rows, int64_t T, int64_t v0, const int32_t* target,
                                                          float2* part, float* z_target) {
@@ -67,15 +71,14 @@ __global__ void __launch_bounds__(256) xent_pairs_kernel(const float* Z, int spl
       if (t < T && r0 + 8 * i < rows) z[i] += __ldcg(Z + q * split_stride + (r0 + 8 * i) * ldz + t);
   }
   const int64_t want = t < T ? (int64_t)__ldg(target + t) - v0 - r0 : -1;
-  float top = -3.0e38f, sum = 0.f;
+  float top = -3.0e38f, sum = 0.f;  // finite: (-inf) - (-inf) must not arise
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     top = fmaxf(top, z[i]);
     if (want == 8 * i) z_target[t] = z[i];
   }
-  top = fmaxf(top * kLog2e, -3.0e38f);
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) sum += exp2_fast(fmaf(z[i], kLog2e, -top));
+  for (int i = 0; i < kEach; ++i) sum += exp2_fast((z[i] - top) * kLog2e);
   s_max[warp][lane] = top;
   s_sum[warp][lane] = sum;
   __syncthreads();
@@ -83,12 +86,13 @@ __global__ void __launch_bounds__(256) xent_pairs_kernel(const float* Z, int spl
     float m = s_max[0][lane];
     for (int w = 1; w < 8; ++w) m = fmaxf(m, s_max[w][lane]);
     float s = 0.f;
-    for (int w = 0; w < 8; ++w) s += s_sum[w][lane] * exp2_fast(s_max[w][lane] - m);
+    for (int w = 0; w < 8; ++w) s += s_sum[w][lane] * exp2_fast((s_max[w][lane] - m) * kLog2e);
     part[(v0 / kPairRows + blockIdx.y) * T + t] = make_float2(m, s);
   }
 }
 
-// Joins a token's pairs: lse = (M + log2 sum_p s_p 2^(m_p - M)) log 2, M the largest max.
+// Joins a token's pairs: with M the largest max and S = sum_p s_p exp(m_p - M), lse = M + log S and
+// loss = (M - z[target]) + log S.
 __global__ void __launch_bounds__(1024) xent_join_kernel(const float2* part, int64_t pairs, int64_t R, int64_t T,
                                                          const int32_t* target, const float* z_target, float* loss,
                                                          float* lse) {
@@ -107,9 +111,9 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const float2* part, int
       float top = m;
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = fmaxf(top, q[i].x);
-      s *= exp2_fast(m - top);
+      s *= exp2_fast((m - top) * kLog2e);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += q[i].y * exp2_fast(q[i].x - top);
+      for (int i = 0; i < 8; ++i) s += q[i].y * exp2_fast((q[i].x - top) * kLog2e);
       m = top;
     }
   }
@@ -122,19 +126,18 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const float2* part, int
     for (int w = 1; w < 32; ++w) top = fmaxf(top, s_max[w][lane]);
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < 32; ++w) sum += s_sum[w][lane] * exp2_fast(s_max[w][lane] - top);
-    const float l = (top + log2f(sum)) * 0.6931471805599453f;
+    for (int w = 0; w < 32; ++w) sum += s_sum[w][lane] * exp2_fast((s_max[w][lane] - top) * kLog2e);
+    const float l = logf(sum);
     const int32_t want = __ldg(target + t);
-    lse[t] = l;
-    loss[t] = want >= 0 && (int64_t)want < R ? l - __ldcg(z_target + t) : 0.f;
+    lse[t] = top + l;
+    loss[t] = want >= 0 && (int64_t)want < R ? (top - __ldcg(z_target + t)) + l : 0.f;
   }
 }
 
 // The SM-pair epilogues' per-token data, on 16 bytes and padded to `padded` tokens (no target, factor 0).
 __global__ void __launch_bounds__(256) xent_columns_kernel(const int32_t* target, const float* lse, const float* dloss,
                                                            int64_t R, int64_t T, int64_t padded, int32_t* tgt,
-                                                           float* lse2, float* d) {
-  using namespace xent;
+                                                           float* lse_out, float* d) {
   pdl_gate();
   const int64_t t = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
   if (t >= padded) return;
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(256) xent_columns_kernel(const int32_t* target
   const bool has = w >= 0 && (int64_t)w < R;
   tgt[t] = has ? w : -1;
   if (lse) {
-    lse2[t] = has ? __ldg(lse + t) * kLog2e : 0.f;
+    lse_out[t] = has ? __ldg(lse + t) : 0.f;
     d[t] = has ? __ldg(dloss + t) : 0.f;
   }
 }
@@ -277,7 +280,7 @@ nm_status gather_input(Head& h, const int32_t* idx, Staged& staged, cudaStream_t
   return NM_OK;
 }
 
-// Per-token data of the SM-pair epilogues: [target | lse2 | d], each padded to whole tiles (256 and 224 columns).
+// Per-token data of the SM-pair epilogues: [target | lse | d], each padded to whole tiles (256 and 224 columns).
 int64_t padded_tokens(int64_t T) { return (T + 255) / 256 * 256 + 256; }
 nm_status column_data(const Head& h, const int32_t* target, const float* lse, const float* dloss, PairEpiData& epi,
                       Staged& staged, cudaStream_t s) {
@@ -285,13 +288,13 @@ nm_status column_data(const Head& h, const int32_t* target, const float* lse, co
   cudaError_t e = staged.get((size_t)(n * 4 * (lse ? 3 : 1)));
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the token data");
   int32_t* tgt = staged.as<int32_t>();
-  float* lse2 = staged.as<float>() + n;
+  float* lse_to = staged.as<float>() + n;
   e = launch_pdl(xent_columns_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, target, lse, dloss, h.R, h.T, n,
-                 tgt, lse2, lse2 + n);
+                 tgt, lse_to, lse_to + n);
   count_launch();
   epi.target = tgt;
-  epi.lse2 = lse2;
-  epi.d = lse2 + n;
+  epi.lse = lse_to;
+  epi.d = lse_to + n;
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "token data launch");
 }
 

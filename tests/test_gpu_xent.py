@@ -284,3 +284,35 @@ def test_gradients_of_a_large_vocabulary_and_few_features(R, K, T):
     nm.nm_device_status()
     c.check_loss(loss, lse)
     c.check_grad(lse, dX, dV)
+
+
+# The SM-pair epilogue; the one-SM, skinny (whole and split) and dense GEMMs, whose logits the pair kernel reads
+@pytest.mark.parametrize("R,K,T", [(600, 128, 256), (300, 1280, 200), (600, 256, 100), (700, 2048, 24), (500, 136, 80)])
+@pytest.mark.parametrize("above", [20.0, 60.0, 200.0])
+def test_loss_of_a_confident_token_is_small_and_not_negative(R, K, T, above):
+    """Target logits far above the rest, where the loss is far below the logits' own roundings.
+
+    The target has the largest logit, so the loss is log(1 + sum of exp(z - z_target)): no term of the size of the logits
+    is left in it.  An error e in every logit changes a term by a factor of exp(2 e); the exponentials add 2^-19 (their
+    arguments are below 128 where a term counts); every addition to a sum between 1 and 2 rounds by 2^-24, and a sum takes
+    at most 32 + 8 + 8 + 32 of them on its way (fewer in the SM-pair epilogue).
+    """
+    c = Case(R, K, T, seed=31, scale=0.3)
+    rng = np.random.Generator(np.random.PCG64(32))
+    target = rng.integers(0, R, T)
+    w = c.w[torch.from_numpy(target)]
+    x = (above * rng.uniform(0.9, 1.1, T))[:, None] * (w / (w * w).sum(1, keepdim=True)).numpy() + 0.02 * rng.standard_normal((T, K))
+    X = wl.bf16_bits(x.T.astype(np.float32))
+    c.X, c.x = padded(X), torch.from_numpy(wl.bf16_to_f32(X).astype(np.float64))
+    c.target = torch.from_numpy(target.astype(np.int32))
+    loss, lse = nm.spmm_xent(*c.args())
+    z = c.w @ c.x
+    top = z.gather(0, c.target.long()[None, :])[0]
+    rest = (z - top).exp().scatter_(0, c.target.long()[None, :], 0.0)
+    assert (rest < 1).all()  # the target leads everywhere
+    want = torch.log1p(rest.sum(0))
+    e = 2 * c.logit_error().max(0).values
+    got = f64(loss)
+    assert (got >= 0).all(), f"{int((got < 0).sum())} negative losses, down to {float(got.min()):.2e}"
+    assert (got - want).abs().le(want * (2 * e + 2.0 ** -19) + 80 * 2.0 ** -24).all()
+    c.check_loss(loss, lse)
