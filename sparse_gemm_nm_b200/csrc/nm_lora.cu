@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(lora::kThreads, RB == 32 ? 3 : 2) lora_shrink_
       }
     }
     if (C > 1) cluster_wait();  // the sums may be overwritten, and a CTA may leave
+    fence_proxy_async_smem();   // ... by the next item's copies, which take their place: ordinary accesses come first
     __syncthreads();
   }
 

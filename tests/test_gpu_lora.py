@@ -361,3 +361,13 @@ def test_few_tokens_of_a_large_projection(T, permuted):
         torch.cuda.synchronize()
         nm.nm_device_status()
         c.check_forward(y)
+
+
+@pytest.mark.parametrize("rank,dtype", [(8, BF), (48, F32), (100, BF)])
+def test_tiles_of_many_adapters_share_a_ring(rank, dtype):
+    """A CTA of the shrink takes dozens of adapters one after the other, each through the ring that held the sums of the last."""
+    c = Case(130, 1000, 4500, 40, rank, "mixed", seed=rank)
+    c.check_grads(*c.grads(dtype))
+    first = c.grads(dtype)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(c.grads(dtype), first))
