@@ -214,17 +214,17 @@ nm_status make_tmap3(CUtensorMap* tm, const void* base, uint64_t d0, uint64_t d1
   return NM_OK;
 }
 
-// Maps of a GEMM's further reduction steps (boxes of 64 x 64).
+// Maps of a GEMM's further reduction steps (boxes of box_rows rows of 64).
 template <typename Params>
-static nm_status set_ext(Params& p, const GemmExt& x, int64_t T) {
+static nm_status set_ext(Params& p, const GemmExt& x, int64_t T, uint32_t box_rows) {
   p.ext_planes = x.planes;
   p.ext_cat = x.cat;
   p.ext_masks = x.masks;
-  nm_status st = make_tmap(&p.tm_xa, x.left, (uint64_t)x.cols, (uint64_t)x.rows, (uint64_t)x.ldl * 2, 64, 64, 128,
-                           "adapter matrix");
+  nm_status st = make_tmap(&p.tm_xa, x.left, (uint64_t)x.cols, (uint64_t)x.rows, (uint64_t)x.ldl * 2, 64, box_rows,
+                           128, "adapter matrix");
   if (st == NM_OK)
-    st = make_tmap(&p.tm_xs, x.terms, (uint64_t)T, (uint64_t)(x.planes * x.cat), (uint64_t)x.ldp * 2, 64, 64, 128,
-                   "adapter blocks");
+    st = make_tmap(&p.tm_xs, x.terms, (uint64_t)T, (uint64_t)(x.planes * x.cat), (uint64_t)x.ldp * 2, 64,
+                   box_rows, 128, "adapter blocks");
   return st;
 }
 
@@ -651,7 +651,7 @@ static nm_status run_gemm(const GemmRequest& q, cudaStream_t stream) {
                      128, "values");
     if (st == NM_OK && !dense_pair) st = make_meta_tmap(&p.tm_meta, meta, p.meta_rblocks, p.meta_cblocks);
     if (q.epi) p.epi = *q.epi;
-    if (st == NM_OK && q.ext) st = set_ext(p, *q.ext, q.T);
+    if (st == NM_OK && q.ext) st = set_ext(p, *q.ext, q.T, kPairExtBoxRows);
     if (st == NM_OK && !use_skinny && p.epi.mode != PAIR_EPI_LSE)
       st = make_pair_store_maps(p, q.Y, q.R, q.T, q.ldy, p.out_f32 != 0);
     if (!use_skinny && !dense_pair) p.n_major = pair_n_major(q.R, p.vcols, q.K, q.T);
@@ -1158,7 +1158,7 @@ nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m,
   if (e == cudaSuccess && st == NM_OK)
     st = make_tmap(&p.tm_b, dY, (uint64_t)T, (uint64_t)R, (uint64_t)lddy * 2, 64, 64, 128, "dY");
   if (e == cudaSuccess && st == NM_OK && !idx) st = set_store_map(p, dX, K, T, lddx, p.out_f32 != 0);
-  if (e == cudaSuccess && st == NM_OK && ext) st = set_ext(p, *ext, T);
+  if (e == cudaSuccess && st == NM_OK && ext) st = set_ext(p, *ext, T, 64);
   if (e == cudaSuccess && st == NM_OK) e = launch_dense_pair(p, true, true, EPI_STORE, stream);
   cudaFreeAsync(wd, stream);
   if (st != NM_OK) return st;

@@ -18,6 +18,7 @@ enum AMode : int {
 // Height of the A and B boxes of the SM-pair kernel: each stage's 128 rows
 // of values and 128 rows of X arrive as 64-row boxes from separate warps.
 constexpr uint32_t kPairBoxRows = 64;
+constexpr uint32_t kPairExtBoxRows = 32;  // of the further reduction steps: seven warps share their eight boxes
 
 enum Pattern : int { PAT_2_4 = 0, PAT_1_2 = 1, PAT_1_4 = 2, PAT_1_8 = 3, PAT_2_8 = 4, PAT_OTHER = 5 };
 

@@ -125,6 +125,25 @@ struct Cfg {
   static_assert(kN <= 256 && (kN / 2) % 16 == 0, "each CTA supplies a multiple of 16 columns of X");
   static_assert(kECol >= 256u * (kAcc - 1) + kN && kECol + kECols * kStages <= kTmemCols, "TMEM columns");
 };
+
+// The boxes of a half stage of the further reduction steps (kPairExtBoxRows rows each; four of A, two for each strip of
+// B) by copying warp.  Every copying warp brings at least one: a warp that only waited for the slot and moved on could
+// fall behind the others by more than a turn of the ring, where the slot's parity no longer tells it which turn it
+// sees, and its next box would never come.
+__host__ __device__ constexpr int ext_a_boxes(int warp) { return warp == 0 ? 2 : warp == 10 || warp == 11 ? 1 : 0; }
+__host__ __device__ constexpr int ext_a_first(int warp) { return warp == 0 ? 0 : warp - 8; }
+__host__ __device__ constexpr int ext_b_boxes(int warp) { return warp >= 2 && warp <= 5 ? 1 : 0; }
+constexpr bool ext_boxes_shared() {
+  int a = 0, b = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const bool copies = w < 6 ? w != 1 : w >= 10;
+    if (copies != (ext_a_boxes(w) + ext_b_boxes(w) > 0)) return false;
+    a += ext_a_boxes(w);
+    b += ext_b_boxes(w);
+  }
+  return a * kPairExtBoxRows == 128 && b * kPairExtBoxRows == 128;
+}
+static_assert(ext_boxes_shared(), "every copying warp has a part of every half stage");
 }  // namespace pair
 
 // (max, sum of exponentials) of two sets of terms as one.
@@ -464,14 +483,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                 ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
                 if (!ok) break;
                 const uint32_t lead_full = lead_full0 + 8u * s;
-                if (warp == 0 || warp == 10) {
-                  const int h = warp == 10;
-                  if (rank == 0 && h == 0) mbar_arrive_expect_tx(&full[s], 2u * (16384u + 16384u));
-                  tma_load_2d_pair(smem + L.a + s * kA + h * 8192, &p.tm_xa, lead_full, k0, row0 + 64 * h);
-                } else if (warp == 2 || warp == 4) {
-                  const int j = (warp - 2) >> 1;
-                  tma_load_2d_pair(smem + L.b + s * kB + j * 16384, &p.tm_xs, lead_full, col0 + 64 * j,
-                                   (int32_t)(pl * p.ext_cat) + k0);
+                constexpr int kRows = (int)kPairExtBoxRows;
+                if (rank == 0 && warp == 0) mbar_arrive_expect_tx(&full[s], 2u * (16384u + 16384u));
+                for (int i = 0; i < ext_a_boxes(warp); ++i) {
+                  const int r = (ext_a_first(warp) + i) * kRows;
+                  tma_load_2d_pair(smem + L.a + s * kA + r * 128, &p.tm_xa, lead_full, k0, row0 + r);
+                }
+                if (ext_b_boxes(warp)) {
+                  const int j = (warp - 2) >> 1, r = ((warp - 2) & 1) * kRows;
+                  tma_load_2d_pair(smem + L.b + s * kB + j * 16384 + r * 128, &p.tm_xs, lead_full, col0 + 64 * j,
+                                   (int32_t)(pl * p.ext_cat) + k0 + r);
                 }
                 if (++s == kStages) { s = 0; ph ^= 1u; }
               }

@@ -371,3 +371,42 @@ def test_tiles_of_many_adapters_share_a_ring(rank, dtype):
     first = c.grads(dtype)
     for _ in range(5):
         assert all(torch.equal(a, b) for a, b in zip(c.grads(dtype), first))
+
+
+# More than eight 128-deep stages: the adapters inside the 256 x 256 form of the SM-pair GEMM.  Token counts before, at and
+# behind a column tile; up to the eight blocks of 64 rank rows that fit; several tiles to an SM pair; many rows to few tokens
+# (column tiles go fastest)
+LONG = [(520, 1152, 200, 3, 20), (520, 1152, 256, 8, 64), (300, 2048, 264, 16, 32), (1600, 1152, 264, 4, 16),
+        (2600, 1152, 2056, 5, 16), (8000, 1280, 640, 2, 64)]
+
+
+@pytest.mark.parametrize("R,K,T,N,rank", LONG)
+@pytest.mark.parametrize("kind", ["mixed", "runs"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_forward_of_a_long_reduction(R, K, T, N, rank, kind, dtype):
+    c = Case(R, K, T, N, rank, kind, permuted=kind == "runs", scaled=kind == "mixed", seed=R + T)
+    y = c.forward(dtype)
+    torch.cuda.synchronize()
+    nm.nm_device_status()
+    c.check_forward(y)
+
+
+@pytest.mark.parametrize("T", [200, 264])
+def test_requests_do_not_reach_each_other_in_a_long_reduction(T):
+    def case():
+        c = Case(300, 1152, T, 3, 40, "mixed", seed=44)
+        c.adapter[:6] = torch.tensor([0, 1, 2, 0, 1, 2], dtype=torch.int32)
+        return c
+
+    c = case()
+    y = c.forward()
+    c.X[5, 1] = float("nan")  # token 1 belongs to adapter 1
+    keep = torch.arange(T, device=DEV) != 1
+    y2 = c.forward()
+    assert y2[:, 1].isnan().any() and torch.equal(y2[:, keep], y[:, keep])
+    c = case()
+    c.A[1, 3, 9] = float("inf")
+    c.B[1, 4, 5] = float("nan")
+    keep = c.adapter != 1
+    y2 = c.forward()
+    assert torch.equal(y2[:, keep], y[:, keep]) and y2[4, ~keep].isnan().all()
