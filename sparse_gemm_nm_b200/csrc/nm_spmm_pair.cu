@@ -126,24 +126,28 @@ struct Cfg {
   static_assert(kECol >= 256u * (kAcc - 1) + kN && kECol + kECols * kStages <= kTmemCols, "TMEM columns");
 };
 
-// The boxes of a half stage of the further reduction steps (kPairExtBoxRows rows each; four of A, two for each strip of
-// B) by copying warp.  Every copying warp brings at least one: a warp that only waited for the slot and moved on could
-// fall behind the others by more than a turn of the ring, where the slot's parity no longer tells it which turn it
-// sees, and its next box would never come.
+// Who copies what.  Every copying warp brings a box in every kind of stage: a warp that only waited for the slot and
+// moved on could fall behind the others by more than a turn of the ring, where the slot's parity no longer tells it
+// which turn it sees, and its next box would never come.  Sparse stages: a box of A or B, or the metadata, each.
+// Dense tiles of the hybrid: A is four boxes (K half + 2 x row half); the B warps as in sparse stages.
+__host__ __device__ constexpr int dense_boxes(int warp) { return warp == 0 ? 2 : warp == 10 || warp == 11 ? 1 : 0; }
+__host__ __device__ constexpr int dense_first(int warp) { return warp == 0 ? 0 : warp - 8; }
+// Half stages of the further reduction steps: boxes of kPairExtBoxRows rows, four of A and two for each strip of B.
 __host__ __device__ constexpr int ext_a_boxes(int warp) { return warp == 0 ? 2 : warp == 10 || warp == 11 ? 1 : 0; }
 __host__ __device__ constexpr int ext_a_first(int warp) { return warp == 0 ? 0 : warp - 8; }
 __host__ __device__ constexpr int ext_b_boxes(int warp) { return warp >= 2 && warp <= 5 ? 1 : 0; }
-constexpr bool ext_boxes_shared() {
-  int a = 0, b = 0;
+constexpr bool boxes_shared() {
+  int dense = 0, a = 0, b = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
-    const bool copies = w < 6 ? w != 1 : w >= 10;
-    if (copies != (ext_a_boxes(w) + ext_b_boxes(w) > 0)) return false;
+    const bool copies = w < 6 ? w != 1 : w >= 10, copies_b = w >= 2 && w <= 5;
+    if (copies != (ext_a_boxes(w) + ext_b_boxes(w) > 0) || copies != (dense_boxes(w) + copies_b > 0)) return false;
+    dense += dense_boxes(w);
     a += ext_a_boxes(w);
     b += ext_b_boxes(w);
   }
-  return a * kPairExtBoxRows == 128 && b * kPairExtBoxRows == 128;
+  return dense == 4 && a * kPairExtBoxRows == 128 && b * kPairExtBoxRows == 128;
 }
-static_assert(ext_boxes_shared(), "every copying warp has a part of every half stage");
+static_assert(boxes_shared(), "every copying warp has a part of every stage");
 }  // namespace pair
 
 // (max, sum of exponentials) of two sets of terms as one.
@@ -446,12 +450,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
               if (sparse) {
                 tma_load_2d_pair(smem + L.a + s * kA + h * 8192, &p.tm_vals, lead_full,
                                  (int32_t)(kt * (I8 ? 128 : TF32 ? 32 : 64)), row0 + 64 * h);
-              } else if (HYB) {  // this CTA's dense tile: W, or W under the 2:4 mask if the tile is 2:4
-                const CUtensorMap* src = tile_sparse(tm, kt, (int)rank) ? &p.tm_wm : &p.tm_w;
-#pragma unroll
-                for (int kh = 0; kh < 2; ++kh)
-                  tma_load_2d_pair(smem + L.a + s * kA + kh * 16384 + h * 8192, src, lead_full,
-                                   (int32_t)(kt * 128 + 64 * kh), row0 + 64 * h);
               }
             } else if (warp <= 5) {
               if (I8) {  // box K quarter q: 128 int8 columns x 64 rows of X
@@ -472,6 +470,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                                (int32_t)(((int64_t)(row0 / 128) * p.meta_cblocks + kt) * 16));
             } else if (sparse) {  // eight 16-row metadata blocks of column block kt
               tma_load_3d_pair(smem + L.e + s * kE, &p.tm_meta, lead_full, 0, (int32_t)kt, row0 / 16);
+            }
+            if (HYB && !sparse) {  // this CTA's dense tile: W, or W under the 2:4 mask if the tile is 2:4
+              const CUtensorMap* src = tile_sparse(tm, kt, (int)rank) ? &p.tm_wm : &p.tm_w;
+              for (int i = 0; i < dense_boxes(warp); ++i) {
+                const int kh = (dense_first(warp) + i) & 1, h = (dense_first(warp) + i) >> 1;
+                tma_load_2d_pair(smem + L.a + s * kA + kh * 16384 + h * 8192, src, lead_full,
+                                 (int32_t)(kt * 128 + 64 * kh), row0 + 64 * h);
+              }
             }
             if (++s == kStages) { s = 0; ph ^= 1u; }
           }

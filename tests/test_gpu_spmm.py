@@ -585,3 +585,20 @@ def test_pair_repeatable():
         a = run_spmm(W, X, 2, 4)
         b = run_spmm(W, X, 2, 4)
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dense_first", [True, False])
+def test_hybrid_pair_long_runs_of_dense_tiles(dense_first):
+    """Many turns of the ring of dense stages, where no metadata is copied, before and after sparse ones."""
+    R, K, T = 600, 4096, 1032
+    W = wl.integer_bf16((R, K), -4, 4, seed=201)
+    X = wl.integer_bf16((K, T), -4, 4, seed=202)
+    tm = np.zeros((5, 32), np.uint8)
+    tm[:, 28:] = 1
+    if not dense_first:
+        tm = np.ascontiguousarray(tm[:, ::-1])
+    tm[2, 5:9] = 1  # 2:4 tiles whose partner is dense
+    Y = run_hybrid(W, X, tm)
+    nm.nm_device_status()
+    ref = oracle.hybrid_spmm(W, tm, X, 128)
+    assert np.array_equal(bits(Y), bf16_rne_of(ref))
