@@ -266,7 +266,10 @@ __global__ void __launch_bounds__(256) compress_generic_kernel(const uint16_t* _
   }
 }
 
-// 2:4 decompress from tiled metadata: one thread per word -> 2 x 16 weights.
+// 2:4 decompress from tiled metadata: one thread per word -> 2 x 16 weights.  WORDS: pairs of values and of weights as
+// 32-bit words (and eight weights at once with vec); otherwise, where values, W or W's rows start off 4 bytes, elements
+// one by one.
+template <bool WORDS>
 __device__ __forceinline__ void decompress_half16(const uint16_t* __restrict__ vrow, uint16_t* __restrict__ wrow,
                                                   uint32_t nibs, uint32_t k0, uint32_t K, bool vec) {
   uint32_t out[8];
@@ -275,7 +278,10 @@ __device__ __forceinline__ void decompress_half16(const uint16_t* __restrict__ v
     const uint32_t nib = (nibs >> (4 * t)) & 0xFu;
     const uint32_t p0 = nib & 3u, p1 = nib >> 2;
     uint32_t v = 0;
-    if (k0 + 4 * t < K) v = *reinterpret_cast<const uint32_t*>(vrow + k0 / 2 + 2 * t);
+    if (k0 + 4 * t < K) {
+      const uint16_t* at = vrow + k0 / 2 + 2 * t;
+      v = WORDS ? *reinterpret_cast<const uint32_t*>(at) : (uint32_t)at[0] | (uint32_t)at[1] << 16;
+    }
     const uint32_t v0 = v & 0xFFFFu, v1 = v >> 16;
     uint32_t e[4];
 #pragma unroll
@@ -283,20 +289,25 @@ __device__ __forceinline__ void decompress_half16(const uint16_t* __restrict__ v
     out[2 * t] = e[0] | (e[1] << 16);
     out[2 * t + 1] = e[2] | (e[3] << 16);
   }
-  if (vec && k0 + 16 <= K) {
+  if (WORDS && vec && k0 + 16 <= K) {
     uint4* dst = reinterpret_cast<uint4*>(wrow + k0);
     dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
     dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
-  } else {
+  } else if (WORDS) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
       if (k0 + 4 * t < K) {
         *reinterpret_cast<uint32_t*>(wrow + k0 + 4 * t) = out[2 * t];
         *reinterpret_cast<uint32_t*>(wrow + k0 + 4 * t + 2) = out[2 * t + 1];
       }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (k0 + i < K) wrow[k0 + i] = (uint16_t)(out[i >> 1] >> (16 * (i & 1)));
   }
 }
 
+template <bool WORDS>
 __global__ void __launch_bounds__(256) decompress_2of4_tiled_kernel(const uint16_t* __restrict__ V,
                                                                     const uint32_t* __restrict__ meta, uint32_t R,
                                                                     uint32_t K, uint16_t* __restrict__ W,
@@ -324,9 +335,9 @@ __global__ void __launch_bounds__(256) decompress_2of4_tiled_kernel(const uint16
     }
     const uint32_t word = __ldg(meta + w);
     if (r_lo < R)
-      decompress_half16(V + (int64_t)r_lo * (K >> 1), W + (int64_t)r_lo * ldw, word & 0xFFFFu, k0, K, vec);
+      decompress_half16<WORDS>(V + (int64_t)r_lo * (K >> 1), W + (int64_t)r_lo * ldw, word & 0xFFFFu, k0, K, vec);
     if (r_lo + 8 < R)
-      decompress_half16(V + (int64_t)(r_lo + 8) * (K >> 1), W + (int64_t)(r_lo + 8) * ldw, word >> 16, k0, K, vec);
+      decompress_half16<WORDS>(V + (int64_t)(r_lo + 8) * (K >> 1), W + (int64_t)(r_lo + 8) * ldw, word >> 16, k0, K, vec);
   }
   pdl_leave(early);
 }
@@ -514,8 +525,9 @@ cudaError_t launch_decompress(const uint16_t* values, const uint32_t* meta, int6
   if (tiled_meta(n, m)) {
     const int64_t total = meta_words(R, K, n, m);
     const bool vec = K % 16 == 0 && ldw % 8 == 0 && aligned16(W_out) && aligned16(values);
-    launch_pdl(decompress_2of4_tiled_kernel, grid_for(total, threads), threads, 0, s,
-        values, meta, (uint32_t)R, (uint32_t)K, W_out, ldw, (uint32_t)meta_col_blocks(K), (uint32_t)total, vec,
+    const bool words = ((reinterpret_cast<uintptr_t>(values) | reinterpret_cast<uintptr_t>(W_out)) & 3u) == 0 && ldw % 2 == 0;
+    launch_pdl(words ? decompress_2of4_tiled_kernel<true> : decompress_2of4_tiled_kernel<false>,
+        grid_for(total, threads), threads, 0, s, values, meta, (uint32_t)R, (uint32_t)K, W_out, ldw, (uint32_t)meta_col_blocks(K), (uint32_t)total, vec,
         nullptr, 0u, early);
   } else {
     const int64_t work = R * (K / m);
@@ -536,7 +548,7 @@ cudaError_t launch_decompress_tiles(const uint16_t* values, const uint32_t* meta
   const int threads = 256;
   const int64_t total = meta_words(R, K, 2, 4);
   const bool vec = K % 16 == 0 && ldw % 8 == 0 && aligned16(W_out) && aligned16(values);
-  launch_pdl(decompress_2of4_tiled_kernel, grid_for(total, threads), threads, 0, s,
+  launch_pdl(decompress_2of4_tiled_kernel<true>, grid_for(total, threads), threads, 0, s,
       values, meta, (uint32_t)R, (uint32_t)K, W_out, ldw, (uint32_t)meta_col_blocks(K), (uint32_t)total, vec,
       tile_map, (uint32_t)((R + 127) / 128), false);
   count_launch();

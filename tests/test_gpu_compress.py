@@ -182,3 +182,21 @@ def test_compress_1of8_large_weight():
     ov, om = oracle.compress(W, 1, 8)
     v, mt = gpu_compress(W, 1, 8)
     assert np.array_equal(v, ov) and np.array_equal(mt, om)
+
+
+@pytest.mark.parametrize("R,K", [(20, 24), (33, 256), (17, 132)])
+@pytest.mark.parametrize("off,extra,w_off", [(1, 0, 0), (0, 1, 0), (0, 2, 1), (1, 3, 1), (2, 8, 0)])
+def test_decompress_2of4_of_any_alignment(R, K, off, extra, w_off):
+    """Values and W that start on any element, and odd row strides; elements behind a row's last weight stay."""
+    W = wl.normal_bf16((R, K), 1.0, seed=R + K)
+    ov, om = oracle.compress(W, 2, 4)
+    buf = torch.zeros(ov.size + off, dtype=torch.bfloat16, device=DEV)
+    buf[off:] = to_dev(ov).flatten()
+    meta = torch.from_numpy(om.view(np.int32)).to(DEV)
+    ld = K + extra
+    out = torch.full((w_off + R * ld,), 5.0, dtype=torch.bfloat16, device=DEV)
+    nm.nm_decompress(buf[off:], meta, R, K, 2, 4, out[w_off:], ld)
+    torch.cuda.synchronize()
+    got = bits(out[w_off:]).reshape(R, ld)
+    assert np.array_equal(got[:, :K], oracle.decompress(ov, om, K, 2, 4))
+    assert (got[:, K:] == 0x40A0).all() and (out[:w_off] == 5).all()

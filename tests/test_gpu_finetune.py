@@ -243,3 +243,33 @@ def test_the_loss_waits_for_the_launch_before_it(T):
     nm.nm_device_status()
     for i, got in enumerate(hurried):
         assert all(torch.equal(a, b) for a, b in zip(got, calm[i % 4]))
+
+
+@pytest.mark.parametrize("R,K,T", [(130, 256, 200), (70, 72, 37), (300, 128, 24)])
+@pytest.mark.parametrize("off", [1, 2, 4])
+def test_weights_that_start_on_any_element(R, K, T, off):
+    """Views of a larger buffer as the 2:4 values: every call gives what aligned values give, up to the order of sums."""
+    g = torch.Generator().manual_seed(R + off)
+    vals, meta = oracle.compress(wl.normal_bf16((R, K), 0.05, 71), 2, 4)
+    aligned, meta = to_dev(vals), torch.from_numpy(meta.view(np.int32)).to(DEV)
+    buf = torch.zeros(aligned.numel() + off, dtype=torch.bfloat16, device=DEV)
+    values = buf[off:].view(aligned.shape)
+    values.copy_(aligned)
+    X, dY = (torch.zeros((r, -(-T // 8) * 8), dtype=torch.bfloat16, device=DEV)[:, :T] for r in (K, R))
+    X.copy_(torch.randn((K, T), generator=g))
+    dY.copy_(torch.randn((R, T), generator=g))
+    A, B = (torch.randn(s, generator=g).to(DEV, torch.bfloat16) for s in ((2, 4, K), (2, R, 4)))
+    ids = torch.randint(0, 2, (T,), generator=g, dtype=torch.int32).to(DEV)
+    target = torch.randint(0, R, (T,), generator=g, dtype=torch.int32).to(DEV)
+    dloss = torch.rand(T, generator=g).to(DEV)
+
+    def calls(v):
+        loss, lse = nm.spmm_xent(v, meta, 2, 4, K, X, target)
+        return (loss, lse, *nm.spmm_xent_grad(v, meta, 2, 4, K, X, target, lse, dloss),
+                nm.spmm_lora(v, meta, 2, 4, K, X, A, B, ids), nm.spmm_lora_t(v, meta, 2, 4, K, dY, A, B, ids),
+                nm.spmm_t(v, meta, 2, 4, K, dY), nm.decompress(v, meta, K, 2, 4))
+
+    for got, want in zip(calls(values), calls(aligned)):
+        # float32 sums in another order; each side rounds its result to bf16 once, and G before it
+        assert (got.double() - want.double()).norm() <= GRAD_TOL * want.double().norm()
+    nm.nm_device_status()
