@@ -44,6 +44,9 @@
  *  - Device pointers given to the GEMMs must be 16-byte aligned, and leading
  *    dimensions of X and Y must keep every row 16-byte aligned
  *    (NM_ERR_MISALIGNED otherwise).
+ *    Layer norm, the adapter and the cross-entropy calls also refuse vectors
+ *    and words of 32 bits that start off 4 bytes; the values of theirs may
+ *    start on any element.
  *  - Waits inside the GEMM kernels are bounded (about 2 s); a kernel that gives
  *    up records it in a device status word read by nm_device_status().
  *  - Inputs are expected to be finite.  With an Inf or NaN in X the result may

@@ -4,6 +4,7 @@
 #pragma once
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -97,6 +98,13 @@ inline nm_status check_matrix(const void* p, int64_t ld, int64_t T, int64_t esiz
   if (!p) return fail(NM_ERR_INVALID_ARG, "%s is null", name);
   if (ld < T) return fail(NM_ERR_INVALID_ARG, "ld of %s < T", name);
   if (!al16(p) || (ld * esize) % 16 != 0) return fail(NM_ERR_MISALIGNED, "%s rows must be 16-byte aligned", name);
+  return NM_OK;
+}
+
+// 32-bit vectors and words, each on 4 bytes (null where the argument is optional).
+inline nm_status check_words(std::initializer_list<const void*> ps, const char* names) {
+  for (const void* p : ps)
+    if (!aligned_to(p, 4)) return fail(NM_ERR_MISALIGNED, "%s must be 4-byte aligned", names);
   return NM_OK;
 }
 

@@ -1109,7 +1109,11 @@ nm_status check_adapters(const Adapters& ad) {
   if (ad.n < 0 || ad.rank < 1) return fail(NM_ERR_INVALID_ARG, "num_adapters must be >= 0 and rank >= 1");
   if (ad.rank > lora::kMaxRank) return fail(NM_ERR_UNSUPPORTED, "rank %d is above %d", ad.rank, lora::kMaxRank);
   if (ad.n > 65535 / 2) return fail(NM_ERR_UNSUPPORTED, "more than 32767 adapters in a call");
-  return NM_OK;
+  return check_words({ad.scale, ad.adapter}, "scale and adapter");
+}
+nm_status check_operand(const uint16_t* values, const uint32_t* meta, const int32_t* idx) {
+  if (!aligned_to(values, 2)) return fail(NM_ERR_MISALIGNED, "values misaligned");
+  return check_words({meta, idx}, "meta and idx");
 }
 nm_status check_adapter_pointers(const Adapters& ad, int64_t R, int64_t K, int64_t T) {
   if ((!ad.A && K > 0) || (!ad.B && R > 0) || !ad.adapter) return fail(NM_ERR_INVALID_ARG, "A, B or adapter is null");
@@ -1228,6 +1232,7 @@ nm_status nm_spmm_lora(const uint16_t* values, const uint32_t* meta, int n, int 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const Adapters ad{A, B, num_adapters, rank, scale, adapter};
   nm_status st = check_adapters(ad);
+  if (st == NM_OK) st = check_operand(values, meta, idx);
   if (st == NM_OK) st = check_spmm(values, meta, n, m, R, K, X, ldx, T, Y, ldy, y_dtype);
   if (st != NM_OK || R == 0 || T == 0) return st;
   if (num_adapters == 0 || K == 0)
@@ -1285,6 +1290,7 @@ nm_status nm_spmm_lora_t(const uint16_t* values, const uint32_t* meta, int n, in
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const Adapters ad{A, B, num_adapters, rank, scale, adapter};
   nm_status st = check_adapters(ad);
+  if (st == NM_OK) st = check_operand(values, meta, idx);
   if (st == NM_OK) st = check_spmm_t(values, meta, n, m, R, K, dY, lddy, T, dX, lddx, dtype);
   if (st != NM_OK || K == 0 || T == 0) return st;
   if (R == 0) return run_spmm_t(values, meta, n, m, R, K, nullptr, dY, lddy, T, dX, lddx, dtype, s);

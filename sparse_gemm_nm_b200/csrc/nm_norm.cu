@@ -692,6 +692,7 @@ nm_status nm_layer_norm(const void* X, int64_t ldx, nm_out_dtype x_dtype, int64_
   if (T == 0) return NM_OK;
   nm_status st = check_matrix(X, ldx, T, dtype_bytes(x_dtype), "X");
   if (st == NM_OK) st = check_matrix(Y, ldy, T, dtype_bytes(y_dtype), "Y");
+  if (st == NM_OK) st = check_words({gamma, beta, mean, rstd}, "gamma, beta, mean and rstd");
   if (st == NM_OK) st = require_device();
   if (st != NM_OK) return st;
   NormParams p = {};
@@ -726,14 +727,16 @@ nm_status nm_layer_norm_grad(const void* dY, int64_t lddy, nm_out_dtype dy_dtype
   if (K == 0) return fail(NM_ERR_INVALID_ARG, "K is 0: the mean of no features is undefined");
   if (!dtype_ok(x_dtype) || !dtype_ok(dy_dtype)) return fail(NM_ERR_INVALID_ARG, "bad dtype");
   if (K >= kMaxDim || T >= kMaxDim) return fail(NM_ERR_UNSUPPORTED, "dimensions must stay below 2^31");
+  nm_status st = check_words({gamma, mean, rstd, dgamma, dbeta}, "gamma, mean, rstd, dgamma and dbeta");
+  if (st != NM_OK) return st;
   if (T == 0) {  // empty sums
     if (!dgamma && !dbeta) return NM_OK;
-    nm_status st = require_device();
+    st = require_device();
     if (st != NM_OK) return st;
     cudaError_t e = launch_norm_grad_reduce(nullptr, 0, K, dgamma, dbeta, s);
     return e == cudaSuccess ? NM_OK : cuda_fail(e, "layer norm gradient reduction launch");
   }
-  nm_status st = check_matrix(dY, lddy, T, dtype_bytes(dy_dtype), "dY");
+  st = check_matrix(dY, lddy, T, dtype_bytes(dy_dtype), "dY");
   if (st == NM_OK) st = check_matrix(X, ldx, T, dtype_bytes(x_dtype), "X");
   if (st == NM_OK) st = check_matrix(dX, lddx, T, dtype_bytes(x_dtype), "dX");
   if (st == NM_OK && (!mean || !rstd)) st = fail(NM_ERR_INVALID_ARG, "mean or rstd is null");

@@ -454,7 +454,9 @@ nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int n, int 
   nm_status st = check_head(n, m, R, K, T);
   if (st != NM_OK || T == 0) return st;
   if (!values || !meta || !target || !loss || !lse) return fail(NM_ERR_INVALID_ARG, "null operand");
-  st = check_matrix(X, ldx, T, 2, "X");
+  if (!aligned_to(values, 2)) return fail(NM_ERR_MISALIGNED, "values misaligned");
+  st = check_words({meta, idx, target, loss, lse}, "meta, idx, target, loss and lse");
+  if (st == NM_OK) st = check_matrix(X, ldx, T, 2, "X");
   if (st == NM_OK) st = require_device();
   if (st != NM_OK) return st;
   return run_xent(Head{values, meta, n, m, R, K, T, X, ldx}, idx, target, loss, lse,
@@ -480,7 +482,9 @@ nm_status nm_spmm_xent_grad(const uint16_t* values, const uint32_t* meta, int n,
     return e == cudaSuccess ? NM_OK : cuda_fail(e, "zero fill");
   }
   if (!values || !meta || !target || !lse || !dloss) return fail(NM_ERR_INVALID_ARG, "null operand");
-  st = check_matrix(X, ldx, T, 2, "X");
+  if (!aligned_to(values, 2)) return fail(NM_ERR_MISALIGNED, "values misaligned");
+  st = check_words({meta, idx, target, lse, dloss}, "meta, idx, target, lse and dloss");
+  if (st == NM_OK) st = check_matrix(X, ldx, T, 2, "X");
   if (st == NM_OK && dX) st = check_matrix(dX, lddx, T, 2, "dX");
   if (st == NM_OK) st = require_device();
   if (st != NM_OK) return st;

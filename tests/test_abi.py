@@ -190,3 +190,30 @@ def test_host_argument_checks_of_the_adapters(lib):
     assert grad(rank=129) == grad(num=32768) == grad(T=1 << 31) == U
     assert grad(dA=17) == grad(dt=1, dB=18) == grad(X=8) == grad(lddy=12) == grad(A=17) == A16
     assert grad(num=0) == nm.NM_OK
+
+
+def test_host_checks_of_element_alignment(lib):
+    """Vectors and words that start off 4 bytes, and values off 2, are refused: the kernels' loads of them would fault."""
+    A = nm.NM_ERR_MISALIGNED
+    for i in range(4):  # gamma, beta, mean, rstd
+        p = [16] * 4
+        p[i] = 18
+        assert lib.nm_layer_norm(16, 8, 0, 4, 8, p[0], p[1], 1e-5, 16, 8, 0, p[2], p[3], None) == A
+    for i in range(5):  # gamma, mean, rstd, dgamma, dbeta
+        p = [16] * 5
+        p[i] = 18
+        for T in (8, 0):
+            assert lib.nm_layer_norm_grad(16, 8, 0, 16, 8, 0, 4, T, p[0], p[1], p[2], 16, 8, p[3], p[4], None) == A
+    for i in range(6):  # values, meta, idx, target, loss, lse
+        p = [16] * 6
+        p[i] = 17 if i == 0 else 18
+        assert lib.nm_spmm_xent(p[0], p[1], 2, 4, 8, 32, p[2], 16, 8, 8, p[3], p[4], p[5], None) == A
+        # values, meta, idx, target, lse, dloss
+        assert lib.nm_spmm_xent_grad(p[0], p[1], 2, 4, 8, 32, p[2], 16, 8, 8, p[3], p[4], p[5], 16, 8, 16, None) == A
+    for fn in (lib.nm_spmm_lora, lib.nm_spmm_lora_t):
+        for i in range(5):  # values, meta, idx, scale, adapter
+            p = [16] * 5
+            p[i] = 17 if i == 0 else 18
+            assert fn(p[0], p[1], 2, 4, 8, 32, p[2], 16, 8, 8, 16, 16, 4, 2, p[3], p[4], 16, 8, 0, None) == A
+    for p in ((18, 16), (16, 18)):  # scale, adapter
+        assert lib.nm_lora_grad(8, 32, 16, 8, 16, 8, 8, 16, 16, 4, 2, *p, 16, 16, 0, None) == A
