@@ -485,7 +485,8 @@ NM_API nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int 
  * dV = the survivors' entries of G Xp^T as nm_sddmm gives them.  The logits
  * of a piece of the vocabulary are computed again (on the two-SM GEMM its
  * epilogue writes G and no logits); G is rounded to bf16, as the dY of those
- * calls is (up to 256 tokens outside the two-SM GEMM: two bf16 terms); dX adds up in fp32 over the pieces.
+ * calls is (for up to 256 tokens: two bf16 terms, so that dX and dV carry little more
+ * than their own rounding); dX adds up in fp32 over the pieces.
  *   target, lse, dloss [in] T each (int32, fp32, fp32); lse from nm_spmm_xent
  *   dX  [out] K x T bf16, row stride lddx >= T, 16-byte rows, or NULL.  With
  *       idx, rows as in nm_spmm_t (repeated entries are not supported, rows
@@ -493,8 +494,8 @@ NM_API nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int 
  *   dV  [out] R x nm_value_cols(K,n,m) bf16, or NULL (a frozen head); not both
  * Results repeat bit for bit.  Staged from the library's pool: a piece of G (and
  * of fp32 logits, outside the two-SM GEMM), 12 bytes per token, with dX (and
- * there) the piece's decompressed weights, one to eight K x T fp32 accumulators, X
- * twice where G has two terms, and Xp with idx.
+ * there) the piece's decompressed weights, one to eight K x T fp32 accumulators
+ * (twice the columns where G has two terms), and Xp with idx.
  * Errors: as nm_spmm_t.
  */
 NM_API nm_status nm_spmm_xent_grad(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,

@@ -654,6 +654,14 @@ static nm_status run_gemm(const GemmRequest& q, cudaStream_t stream) {
     if (st == NM_OK && q.ext) st = set_ext(p, *q.ext, q.T, kPairExtBoxRows);
     if (st == NM_OK && !use_skinny && p.epi.mode != PAIR_EPI_LSE)
       st = make_pair_store_maps(p, q.Y, q.R, q.T, q.ldy, p.out_f32 != 0);
+    if (st == NM_OK && p.epi.mode == PAIR_EPI_XGRAD2) {  // two matrices of half of Y's columns each, zeros past T
+      p.T = q.ldy / 2;
+      SpmmParams lo;
+      st = make_pair_store_maps(p, q.Y, q.R, p.T, q.ldy, false);
+      if (st == NM_OK) st = make_pair_store_maps(lo, static_cast<uint16_t*>(q.Y) + p.T, q.R, p.T, q.ldy, false);
+      p.tm_y_lo = lo.tm_y;
+      p.tm_y32_lo = lo.tm_y32;
+    }
     if (!use_skinny && !dense_pair) p.n_major = pair_n_major(q.R, p.vcols, q.K, q.T);
     if (st == NM_OK)
       e = use_skinny   ? launch_spmm_skinny(p, stream)
@@ -1167,7 +1175,7 @@ nm_status run_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m,
 
 nm_status run_sddmm(const uint32_t* meta, int n, int m, int64_t R, int64_t K, const int32_t* idx,
                            const uint16_t* dY, int64_t lddy, const uint16_t* X, int64_t ldx, int64_t T, void* dV,
-                           nm_out_dtype dtype, cudaStream_t stream, bool beside) {
+                           nm_out_dtype dtype, cudaStream_t stream, bool beside, int64_t x_tokens) {
   t_last_error.clear();
   nm_status st = check_bwd_common(n, m, R, K, T, dtype);
   if (st != NM_OK) return st;
@@ -1183,7 +1191,8 @@ nm_status run_sddmm(const uint32_t* meta, int n, int m, int64_t R, int64_t K, co
     return e == cudaSuccess ? NM_OK : cuda_fail(e, "zero fill");
   }
   if (!dY || !X) return fail(NM_ERR_INVALID_ARG, "null operand");
-  if (lddy < T || ldx < T) return fail(NM_ERR_INVALID_ARG, "leading dimension < T");
+  if (x_tokens <= 0) x_tokens = T;
+  if (lddy < T || ldx < x_tokens) return fail(NM_ERR_INVALID_ARG, "leading dimension < T");
   if (!al16(dY) || lddy % 8 != 0 || !al16(X) || ldx % 8 != 0)
     return fail(NM_ERR_MISALIGNED, "dY and X rows must be 16-byte aligned");
   cudaError_t e = cudaSuccess;
@@ -1222,12 +1231,13 @@ nm_status run_sddmm(const uint32_t* meta, int n, int m, int64_t R, int64_t K, co
   p.meta_cblocks = meta_col_blocks(K);
   p.vec_out = n == 2 && m == 4 && K % 16 == 0 && al16(dV);
   p.early = beside && !idx;
+  p.b_again = x_tokens < T ? (int32_t)(T / 2) : 0;
   if (e == cudaSuccess && !p.status) e = cudaErrorInvalidSymbol;
   if ((int64_t)p.tiles_m * p.tiles_n >= (1ll << 31)) st = fail(NM_ERR_UNSUPPORTED, "too many tiles");
   if (e == cudaSuccess && st == NM_OK)
     st = make_tmap(&p.tm_a, dY, (uint64_t)T, (uint64_t)R, (uint64_t)lddy * 2, 64, 64, 128, "dY");
   if (e == cudaSuccess && st == NM_OK)
-    st = make_tmap(&p.tm_b, xsrc, (uint64_t)T, (uint64_t)K, (uint64_t)ldsrc * 2, 64, 64, 128, "X");
+    st = make_tmap(&p.tm_b, xsrc, (uint64_t)x_tokens, (uint64_t)K, (uint64_t)ldsrc * 2, 64, 64, 128, "X");
   if (e == cudaSuccess && st == NM_OK) e = launch_dense_pair(p, false, false, EPI_SURVIVORS, stream);
   if (staged) cudaFreeAsync(staged, stream);
   if (st != NM_OK) return st;

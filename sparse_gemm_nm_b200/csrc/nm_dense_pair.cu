@@ -200,7 +200,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
               if (B_MN)
                 tma_load_2d_pair(b + i * 16384 + h * 8192, tmb, bar, n0 + 64 * i, k0 + 64 * h);
               else
-                tma_load_2d_pair(b + i * 16384 + h * 8192, tmb, bar, k0 + 64 * i, n0 + 64 * h);
+                tma_load_2d_pair(b + i * 16384 + h * 8192, tmb, bar,
+                                 k0 + 64 * i - (EPI == EPI_SURVIVORS && p.b_again && k0 + 64 * i >= p.b_again ? p.b_again : 0),
+                                 n0 + 64 * h);
             }
           }
           if (++s == kStages) { s = 0; ph ^= 1u; }

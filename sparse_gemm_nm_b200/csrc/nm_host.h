@@ -76,7 +76,9 @@ nm_status run_spmm_epilogue(const uint16_t* values, const uint32_t* meta, int n,
 // nm_sddmm.
 nm_status run_sddmm(const uint32_t* meta, int n, int m, int64_t R, int64_t K, const int32_t* idx, const uint16_t* dY,
                     int64_t lddy, const uint16_t* X, int64_t ldx, int64_t T, void* dV, nm_out_dtype dtype,
-                    cudaStream_t stream, bool beside = false);  // beside: as GemmPartials' (without idx)
+                    cudaStream_t stream, bool beside = false, int64_t x_tokens = 0);
+// beside: as GemmPartials' (without idx).  x_tokens below T: X has that many columns, and dY is two terms of T / 2 columns
+// (a multiple of 64), each of which meets X (zeros past x_tokens).
 // C (K x T fp32, row stride ldc) = or += W^T D for a dense R x K bf16 W (row stride ldw) and an R x T bf16 D, by
 // the SM-pair GEMM; every element takes one addition.
 // dense_product: C (R x T fp32, row stride ldc) = W X, X K x T.

@@ -482,5 +482,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// What that rounding left over, rounded in turn (nothing is left over of an Inf or NaN).
+__device__ __forceinline__ uint32_t bf16x2_rest(float lo, float hi, uint32_t rounded) {
+  const float r0 = (rounded & 0x7F80u) == 0x7F80u ? 0.f : lo - __uint_as_float(rounded << 16);
+  const float r1 = (rounded & 0x7F800000u) == 0x7F800000u ? 0.f : hi - __uint_as_float(rounded & 0xFFFF0000u);
+  return pack_bf16x2(r0, r1);
+}
 
 }  // namespace nmk

@@ -26,9 +26,10 @@ enum Pattern : int { PAT_2_4 = 0, PAT_1_2 = 1, PAT_1_4 = 2, PAT_1_8 = 3, PAT_2_8
 enum PairEpi : int {
   PAIR_EPI_Y = 0,      // stores it
   PAIR_EPI_LSE = 1,    // Y are logits (rows: the vocabulary): one (max, sum of exponentials) pair per 32 rows and column
-  PAIR_EPI_XGRAD = 2   // Y are logits: stores the gradient d (exp(y - lse) - [row == target]) as bf16
+  PAIR_EPI_XGRAD = 2,  // Y are logits: stores the gradient d (exp(y - lse) - [row == target]) as bf16
+  PAIR_EPI_XGRAD2 = 3  // ... and what that rounding left over as a second bf16 matrix, behind Y's columns
 };
-// Per-column data of the last two, each padded with anything to a whole number of tiles and on 16 bytes.
+// Per-column data of the last three, each padded with anything to a whole number of tiles and on 16 bytes.
 struct PairEpiData {
   int mode;
   float2* part;         // LSE: [ceil(R / 32)][T], (max, sum exp(y - max))
@@ -46,6 +47,7 @@ struct SpmmParams {
   CUtensorMap tm_wm;    // W under the 2:4 mask (staged), box {64, 64}, 128B swizzle (SM-pair hybrid)
   CUtensorMap tm_y;     // Y R x T bf16, box {64, 32}, 128B swizzle (SM-pair epilogue stores)
   CUtensorMap tm_y32;   // Y R x T bf16, box {32, 32}, no swizzle (last 32 columns of a 224-column SM-pair tile)
+  CUtensorMap tm_y_lo, tm_y32_lo;  // the same of the second matrix (PAIR_EPI_XGRAD2), T (padded) columns to the right
   CUtensorMap tm_meta;  // tiled 2:4 metadata {64 words, col blocks, row blocks}, box {64, 1, 8} (SM pair)
   const uint16_t* vals;
   const uint32_t* meta;
@@ -118,6 +120,7 @@ struct DenseParams {
   int out_f32;
   int add;  // epilogue 0 with tma_store and out_f32: C += (a TMA reduction per chunk) instead of C =
   int early;  // runs beside its predecessor (pdl_enter)
+  int32_t b_again;  // epilogue 1, a multiple of 64: B's reduction axis starts over at this step of A's (0: nowhere)
   const int32_t* row_map;
   int64_t rows_out;
   const uint32_t* meta;

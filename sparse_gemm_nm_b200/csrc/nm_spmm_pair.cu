@@ -64,7 +64,8 @@
 // the sum of exponentials of each 32 rows (a warp's, joined between lanes) and
 // the target's logit; no Y is written.
 // XGRAD turns the logits into G = dloss (exp(z - lse) - [target]) and stores it
-// as a bf16 Y.  Differences are taken before they are scaled for ex2, so that a
+// as a bf16 Y; XGRAD2 (few tokens) stores the rounding's remainder too, as a
+// second bf16 term.  Differences are taken before they are scaled for ex2, so that a
 // dominant logit's exponential is exactly 1.
 //
 // Further reduction steps (EXT).  Adapters side by side (nm_lora.cu) are dense
@@ -527,28 +528,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(lead_acc_empty);
         });
-      } else if constexpr (EPI == PAIR_EPI_XGRAD) {
+      } else if constexpr (EPI == PAIR_EPI_XGRAD || EPI == PAIR_EPI_XGRAD2) {
         // Chunks of 64 columns (a last one of 32 in the 224-column form) become gradients in registers and leave
         // through the staging buffer.  The last two stay packed in registers until the accumulator is released,
         // so that only one earlier store's read of the buffer is waited for before that.
         constexpr int kChunks = (int)((C::kN + 63) / 64);
         const int32_t wrow0 = (int32_t)(tm * 256 + 128 * rank + quarter * 32);
         uint8_t* ebuf = smem + L.epi + quarter * (C::kEpiBufs * kEpi);
-        uint32_t w[2][32];
-        auto take = [&](int c, uint32_t (&out)[32]) {
+        constexpr bool kTwo = EPI == PAIR_EPI_XGRAD2;
+        uint32_t w[2][32];  // XGRAD2: a chunk's two terms
+        auto take = [&](int c, uint32_t (&out)[32], uint32_t* rest) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (C::kN == 224u && c == kChunks - 1 && h == 1) break;
+            if (C::kN == 224u && c == kChunks - 1 && h == 1) break;  // no second half
             uint32_t v[32];
             tmem_ld_32x32b_x32(t_addr + c * 64 + 32 * h, v);
             tc_wait_ld();
             if (n0 + 64 * c + 32 * h < p.T) xgrad_block(p, v, wrow0, n0 + 64 * c + 32 * h, lane);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              out[16 * h + j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t hi = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+              out[16 * h + j] = hi;
+              if (kTwo) rest[16 * h + j] = bf16x2_rest(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), hi);
+            }
           }
         };
-        auto put = [&](int c, const uint32_t (&out)[32]) {
+        auto put = [&](int c, const uint32_t (&out)[32], const CUtensorMap* wide, const CUtensorMap* slim) {
           if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the buffer
           __syncwarp();
           const bool narrow = C::kN == 224u && c == kChunks - 1;  // 32 columns: 64-byte rows, unswizzled
@@ -561,22 +566,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && n0 + 64 * c < p.T && wrow0 < p.R) {
-            tma_store_2d(narrow ? &p.tm_y32 : &p.tm_y, ebuf, (int32_t)(n0 + 64 * c), wrow0);
+            tma_store_2d(narrow ? slim : wide, ebuf, (int32_t)(n0 + 64 * c), wrow0);
             bulk_commit_group();
           }
         };
+        auto release = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead_acc_empty);
+        };
+        if (kTwo) {  // at most two column tiles: nothing to gain from an early release
+#pragma unroll 1
+          for (int c = 0; c < kChunks; ++c) {
+            take(c, w[0], w[1]);
+            if (c == kChunks - 1) release();
+            put(c, w[0], &p.tm_y, &p.tm_y32);
+            put(c, w[1], &p.tm_y_lo, &p.tm_y32_lo);
+          }
+        } else {
 #pragma unroll
-        for (int c = 0; c < kChunks - 2; ++c) {
-          take(c, w[0]);
-          put(c, w[0]);
+          for (int c = 0; c < kChunks - 2; ++c) {
+            take(c, w[0], nullptr);
+            put(c, w[0], &p.tm_y, &p.tm_y32);
+          }
+          take(kChunks - 2, w[0], nullptr);
+          take(kChunks - 1, w[1], nullptr);
+          release();
+          put(kChunks - 2, w[0], &p.tm_y, &p.tm_y32);
+          put(kChunks - 1, w[1], &p.tm_y, &p.tm_y32);
         }
-        take(kChunks - 2, w[0]);
-        take(kChunks - 1, w[1]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_acc_empty);
-        put(kChunks - 2, w[0]);
-        put(kChunks - 1, w[1]);
       } else if (DB && !p.out_f32) {
         // Column chunks of 64, 64, 64 and 32 through the warp's staging buffer,
         // one TMA store each (the last through the 32-column map tm_y32).  The
@@ -761,6 +779,7 @@ cudaError_t launch_spmm_pair(SpmmParams& p, cudaStream_t stream) {
     p.num_tiles = p.tiles_m * p.tiles_n;
     if (p.epi.mode == PAIR_EPI_LSE) return launch_pair<false, true, false, false, PAIR_EPI_LSE>(p, stream);
     if (p.epi.mode == PAIR_EPI_XGRAD) return launch_pair<false, true, false, false, PAIR_EPI_XGRAD>(p, stream);
+    if (p.epi.mode == PAIR_EPI_XGRAD2) return launch_pair<false, true, false, false, PAIR_EPI_XGRAD2>(p, stream);
     if (p.ext_planes) return launch_pair<false, true, false, false, PAIR_EPI_Y, true>(p, stream);
     return launch_pair<false, true>(p, stream);
   }

@@ -316,3 +316,21 @@ def test_loss_of_a_confident_token_is_small_and_not_negative(R, K, T, above):
     assert (got >= 0).all(), f"{int((got < 0).sum())} negative losses, down to {float(got.min()):.2e}"
     assert (got - want).abs().le(want * (2 * e + 2.0 ** -19) + 80 * 2.0 ** -24).all()
     c.check_loss(loss, lse)
+
+
+@pytest.mark.parametrize("K,T", [(768, 192), (768, 248), (768, 255), (768, 256), (776, 256), (768, 100), (768, 16)])
+def test_gradients_of_few_tokens_carry_two_terms_on_every_gemm(K, T):
+    """Up to 256 tokens dX and dV are the 64-bit gradients but for their own rounding, on whichever GEMM the shape takes.
+
+    A value off by a relative d before it is rounded lands on the other side of a rounding boundary with a probability of
+    at most d x / ulp(x), and is then off by ulp(x) <= 2^-7 x from the rounded exact value: a relative Frobenius distance of
+    sqrt(d 2^-7).  G's second term loses 2^-17; d = 2^-13 leaves 16 times that for the float32 logits and sums: 2^-10.  One
+    term alone (errors of 1.5e-3) would give 2.4e-3.
+    """
+    c = Case(1000, K, T, permuted=True, seed=41)
+    loss, lse, dX, dV = c.run()
+    c.check_grad(lse, dX, dV)
+    G, dXp, dW = ref.cross_entropy_grad(c.w, c.x, c.target.long(), c.dloss.double())
+    want = torch.empty_like(dXp).index_copy_(0, torch.from_numpy(c.perm).long(), dXp), dW.gather(1, c.cols)
+    for got, exact in zip((dX, dV), want):
+        assert (f64(got) - f64(exact.to(BF))).norm() <= 2.0 ** -10 * exact.norm()
