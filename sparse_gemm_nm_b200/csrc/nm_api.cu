@@ -269,7 +269,10 @@ static int pair_n_major(int64_t R, int64_t vcols, int64_t K, int64_t T) {
 // or int32 accumulator bits) in 32 x 32 boxes; both 128-byte rows with the 128-byte swizzle.
 // Store maps of the SM-pair epilogues: p.tm_y, and for bf16 Y also p.tm_y32
 // (the last 32 columns of the double-buffered form's 224-column tiles).
+// Rows that end inside a 16-byte unit leave their last elements to the epilogue (32-bit Y: int8 and TF32 GEMMs of any T).
 static nm_status make_pair_store_maps(SpmmParams& p, void* Y, int64_t R, int64_t T, int64_t ldy, bool out32) {
+  T -= T % (out32 ? 4 : 8);
+  p.tma_cols = T;
   if (out32)
     return make_tmap(&p.tm_y, Y, (uint64_t)T, (uint64_t)R, (uint64_t)ldy * 4, 32, 32, 128, "Y (32-bit)",
                      CU_TENSOR_MAP_DATA_TYPE_FLOAT32);

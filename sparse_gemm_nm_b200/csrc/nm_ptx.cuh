@@ -482,6 +482,17 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// The last `bytes` (below 16, even) of a row that ends inside a 16-byte unit, for an output whose rows leave by TMA: a TMA
+// store writes whole units, and what lies behind the row's last element is the caller's.  `unit` is the unit's number in
+// this lane's row of the warp's 128-byte-swizzled staging tile, which the lane itself has filled.
+__device__ __forceinline__ void store_row_tail(const uint8_t* tile, int lane, int unit, void* dst, int bytes) {
+  const uint4 u = *reinterpret_cast<const uint4*>(tile + lane * 128 + ((unit ^ (lane & 7)) << 4));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint16_t* d = static_cast<uint16_t*>(dst);
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (2 * e < bytes) d[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+}
 // What that rounding left over, rounded in turn (nothing is left over of an Inf or NaN).
 __device__ __forceinline__ uint32_t bf16x2_rest(float lo, float hi, uint32_t rounded) {
   const float r0 = (rounded & 0x7F80u) == 0x7F80u ? 0.f : lo - __uint_as_float(rounded << 16);

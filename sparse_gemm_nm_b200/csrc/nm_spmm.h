@@ -56,6 +56,7 @@ struct SpmmParams {
   int64_t ldx;
   const uint8_t* tile_map;
   void* Y;
+  int64_t tma_cols;  // SM pair: leading columns of Y that TMA stores, whole 16-byte units; the rest element by element
   uint32_t* status;
   int64_t ldy;
   int64_t R, K, T;

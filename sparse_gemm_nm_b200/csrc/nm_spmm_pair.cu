@@ -677,9 +677,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                 make_uint4(pk[32 * c + 4 * j], pk[32 * c + 4 * j + 1], pk[32 * c + 4 * j + 2], pk[32 * c + 4 * j + 3]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && n0 + 64 * c < p.T && wrow0 < p.R) {
+          if (lane == 0 && n0 + 64 * c < p.tma_cols && wrow0 < p.R) {
             tma_store_2d(&p.tm_y, ebuf, (int32_t)(n0 + 64 * c), wrow0);
             bulk_commit_group();
+          }
+          if constexpr (TF32) {
+            const int64_t at = p.tma_cols - (n0 + 64 * c);
+            if (p.tma_cols < p.T && at >= 0 && at < 64 && wrow0 + lane < p.R)
+              store_row_tail(ebuf, lane, (int)at >> 3, static_cast<uint16_t*>(p.Y) + (int64_t)(wrow0 + lane) * p.ldy + p.tma_cols,
+                             (int)(p.T - p.tma_cols) * 2);
           }
         }
       } else {
@@ -705,9 +711,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
                 make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && n0 + 32 * c < p.T && wrow0 < p.R) {
+          if (lane == 0 && n0 + 32 * c < p.tma_cols && wrow0 < p.R) {
             tma_store_2d(&p.tm_y, ebuf, (int32_t)(n0 + 32 * c), wrow0);
             bulk_commit_group();
+          }
+          if constexpr (I8 || TF32) {
+            const int64_t at = p.tma_cols - (n0 + 32 * c);
+            if (p.tma_cols < p.T && at >= 0 && at < 32 && wrow0 + lane < p.R)
+              store_row_tail(ebuf, lane, (int)at >> 2, static_cast<uint32_t*>(p.Y) + (int64_t)(wrow0 + lane) * p.ldy + p.tma_cols,
+                             (int)(p.T - p.tma_cols) * 4);
           }
           if (c + 1 < kChunks) {
             tmem_ld_32x32b_x32(t_addr + (c + 1) * 32, v);

@@ -42,3 +42,20 @@ def test_int8_and_tf32_outputs_stop_at_the_last_token(T):
     Yf = torch.full((R, ld), 5.0, device=DEV)
     nm.nm_spmm_tf32(vf, mf, R, K, Xf, ld, T, Yf, ld)
     assert torch.equal(Yf[:, :T], nm.spmm_tf32(vf, mf, K, Xf)[:, :T]) and (Yf[:, T:] == 5).all()
+
+
+@pytest.mark.parametrize("T", [193, 194, 227, 256, 513, 1001, 1030])
+def test_int8_and_tf32_outputs_of_many_tokens_stop_at_the_last_token(T):
+    """The sparse SM-pair GEMM (192 tokens and more): each tail of a 16-byte unit, in its own chunk of columns or not."""
+    R, K, ld = 300, 512, -(-T // 16) * 16 + 16
+    v8, m8 = nm.prune_compress_i8(torch.from_numpy(wl.integer_i8((R, K), -9, 9, 3)).to(DEV))
+    X8 = torch.from_numpy(wl.integer_i8((K, ld), -9, 9, 4)).to(DEV)
+    Y8 = torch.full((R, ld), 5, dtype=torch.int32, device=DEV)
+    nm.nm_spmm_i8(v8, m8, R, K, X8, ld, T, Y8, ld)
+    assert torch.equal(Y8[:, :T], nm.spmm_i8(v8, m8, K, X8)[:, :T]) and (Y8[:, T:] == 5).all()
+    vf, mf = nm.prune_compress_tf32(torch.from_numpy(wl.normal_f32((R, K), 1.0, 5)).to(DEV))
+    Xf = torch.from_numpy(wl.normal_f32((K, ld), 1.0, 6)).to(DEV)
+    for dtype, yt in ((torch.float32, nm.NM_OUT_F32), (torch.bfloat16, nm.NM_OUT_BF16)):
+        Yf = torch.full((R, ld), 5.0, dtype=dtype, device=DEV)
+        nm.nm_spmm_tf32(vf, mf, R, K, Xf, ld, T, Yf, ld, yt)
+        assert torch.equal(Yf[:, :T], nm.spmm_tf32(vf, mf, K, Xf, out_dtype=dtype)[:, :T]) and (Yf[:, T:] == 5).all()
