@@ -230,10 +230,14 @@ static nm_status set_ext(Params& p, const GemmExt& x, int64_t T, uint32_t box_ro
 
 // Whole-line TMA stores for the dense pair kernel's plain epilogue: C is rows x cols with row stride ldo
 // elements (bf16, or four-byte values when wide); the caller has checked 16-byte rows.  A TMA store writes whole
-// 16-byte units, so rows that end inside one would lose what the caller keeps behind their last column: those are
-// stored element by element from registers.
+// 16-byte units, so where rows end inside one the map ends before it, and the epilogue stores what is left element by
+// element (rows shorter than one unit leave from registers altogether).
 static nm_status set_store_map(DenseParams& p, void* out, int64_t rows, int64_t cols, int64_t ldo, bool wide) {
-  p.tma_store = cols % (wide ? 4 : 8) == 0 ? 1 : 0;
+  const int64_t unit = wide ? 4 : 8;
+  p.row_tail = (int)(cols % unit);
+  cols -= p.row_tail;
+  p.tma_cols = cols;
+  p.tma_store = cols > 0 ? 1 : 0;
   if (!p.tma_store) return NM_OK;
   return wide ? make_tmap(&p.tm_out, out, (uint64_t)cols, (uint64_t)rows, (uint64_t)ldo * 4, 32, 32, 128,
                           "C (four-byte)", CU_TENSOR_MAP_DATA_TYPE_FLOAT32)

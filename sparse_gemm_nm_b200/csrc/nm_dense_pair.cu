@@ -24,8 +24,10 @@
 // two accumulators (512 TMEM columns) let the next tile's MMAs run meanwhile.
 // The int8 and tf32 forms keep the stage bytes (256 and 64 reduction steps),
 // with K = 32 and K = 8 per MMA.  The plain store epilogue sends whole
-// 128-byte row chunks through a swizzled staging tile and TMA stores; with a
-// row map (dX under an index map) rows are stored one per lane.
+// 128-byte row chunks through a swizzled staging tile and TMA stores, and a
+// row's last elements inside a 16-byte unit one by one (4096 x 4096 x 2047: 70
+// us like 2048; every row from registers: 76); with a row map (dX under an index
+// map) rows are stored one per lane.
 // `add` adds the fp32 tile to what C holds (TMA reductions, no read in the
 // kernel; one writer per element and launch, so results repeat): the pieces of
 // the vocabulary in nm_xent.cu.  EXT appends half-stages of 64 reduction steps
@@ -353,12 +355,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
                 make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && col0 < p.N && (int64_t)wrow0 < p.M) {
+          if (lane == 0 && col0 < p.N && col0 < p.tma_cols && (int64_t)wrow0 < p.M) {
             if (p.add)
               tma_reduce_add_2d(&p.tm_out, sbuf, (int32_t)col0, wrow0);
             else
               tma_store_2d(&p.tm_out, sbuf, (int32_t)col0, wrow0);
             bulk_commit_group();
+          }
+          const int64_t at = p.tma_cols - col0;  // of the row's tail in this chunk
+          if (p.row_tail && at >= 0 && at < (wide ? 32 : 64) && row < p.M) {
+            const int size = wide ? 4 : 2;
+            store_row_tail(sbuf, lane, (int)at * size >> 4, static_cast<uint8_t*>(p.out) + (row * p.ldo + p.tma_cols) * size,
+                           p.row_tail * size);
           }
         }
         continue;

@@ -111,6 +111,8 @@ struct DenseParams {
   CUtensorMap tm_out;       // epilogue 0 with tma_store: C (M x N), box {64 bf16 | 32 four-byte, 32 rows}, 128B swizzle
   const uint32_t* use_alt;
   int tma_store;            // epilogue 0 without row_map: whole-line TMA stores through tm_out
+  int64_t tma_cols;         // ... of the leading columns, a whole number of 16-byte units
+  int row_tail;             // ... and this many elements behind them, one by one
   int64_t M, N, Kr;
   int64_t k_tiles;
   int tiles_m, tiles_n, num_tiles;

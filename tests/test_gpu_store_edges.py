@@ -59,3 +59,30 @@ def test_int8_and_tf32_outputs_of_many_tokens_stop_at_the_last_token(T):
         Yf = torch.full((R, ld), 5.0, dtype=dtype, device=DEV)
         nm.nm_spmm_tf32(vf, mf, R, K, Xf, ld, T, Yf, ld, yt)
         assert torch.equal(Yf[:, :T], nm.spmm_tf32(vf, mf, K, Xf, out_dtype=dtype)[:, :T]) and (Yf[:, T:] == 5).all()
+
+
+@pytest.mark.parametrize("T", [7, 9, 63, 65, 71, 129, 255, 260, 513, 1031])
+def test_every_tail_of_a_row_in_the_dense_gemms(T):
+    """Rows of the input gradient, INT8, TF32 and diagonal products that end anywhere in a chunk of columns."""
+    R, K, ld = 300, 264, -(-T // 16) * 16 + 16
+    vals, meta = oracle.compress(wl.normal_bf16((R, K), 0.1, 11), 2, 4)
+    dY = to_dev(wl.normal_bf16((R, ld), 1.0, 12))
+    values, meta = to_dev(vals), torch.from_numpy(meta.view(np.int32)).to(DEV)
+    for dtype, yt in ((torch.bfloat16, nm.NM_OUT_BF16), (torch.float32, nm.NM_OUT_F32)):
+        dX = torch.full((K, ld), 5.0, dtype=dtype, device=DEV)
+        nm.nm_spmm_t(values, meta, 2, 4, R, K, None, dY, ld, T, dX, ld, yt)
+        full = nm.spmm_t(values, meta, 2, 4, K, dY, out_dtype=dtype)
+        assert torch.equal(dX[:, :T], full[:, :T]) and (dX[:, T:] == 5).all()
+    W = to_dev(wl.normal_bf16((K, R), 1.0, 13))  # K rows of R columns
+    off, dv = nm.diag_prune_compress(W, 17)
+    for dtype, yt in ((torch.bfloat16, nm.NM_OUT_BF16), (torch.float32, nm.NM_OUT_F32)):
+        Y = torch.full((K, ld), 5.0, dtype=dtype, device=DEV)
+        nm.nm_diag_spmm(dv, off, 17, K, R, None, dY, ld, T, Y, ld, yt)
+        full = torch.full((K, ld), 5.0, dtype=dtype, device=DEV)
+        nm.nm_diag_spmm(dv, off, 17, K, R, None, dY, ld, ld, full, ld, yt)
+        assert torch.equal(Y[:, :T], full[:, :T]) and (Y[:, T:] == 5).all()
+    v8, m8 = nm.prune_compress_i8(torch.from_numpy(wl.integer_i8((R, 80), -9, 9, 3)).to(DEV))  # K % 32 != 0: the dense GEMM
+    X8 = torch.from_numpy(wl.integer_i8((80, ld), -9, 9, 4)).to(DEV)
+    Y8 = torch.full((R, ld), 5, dtype=torch.int32, device=DEV)
+    nm.nm_spmm_i8(v8, m8, R, 80, X8, ld, T, Y8, ld)
+    assert torch.equal(Y8[:, :T], nm.spmm_i8(v8, m8, 80, X8)[:, :T]) and (Y8[:, T:] == 5).all()
