@@ -481,12 +481,14 @@ NM_API nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int 
 /*
  * nm_spmm_xent_grad -- gradients of sum_t dloss[t] loss[t]: with
  *   G[v][t] = dloss[t] (exp(z[v][t] - lse[t]) - [v == target[t]])
- * (0 for a token without a loss), dX = (W' Pi)^T G as nm_spmm_t gives it and
- * dV = the survivors' entries of G Xp^T as nm_sddmm gives them.  The logits
- * of a piece of the vocabulary are computed again (on the two-SM GEMM its
- * epilogue writes G and no logits); G is rounded to bf16, as the dY of those
- * calls is (for up to 256 tokens: two bf16 terms, so that dX and dV carry little more
- * than their own rounding); dX adds up in fp32 over the pieces.
+ * (0 for a token without a loss or with dloss[t] = 0, whatever its logits are; its
+ * features still meet that 0 in dV, so they have to be finite),
+ * dX = (W' Pi)^T G as nm_spmm_t gives it and dV = the survivors' entries of
+ * G Xp^T as nm_sddmm gives them.  The logits of a piece of the vocabulary are
+ * computed again (on the two-SM GEMM its epilogue writes G and no logits); G is
+ * rounded to bf16, as the dY of those calls is (for up to 256 tokens: two bf16
+ * terms, so that dX and dV carry little more than their own rounding); dX adds
+ * up in fp32 over the pieces.
  *   target, lse, dloss [in] T each (int32, fp32, fp32); lse from nm_spmm_xent
  *   dX  [out] K x T bf16, row stride lddx >= T, 16-byte rows, or NULL.  With
  *       idx, rows as in nm_spmm_t (repeated entries are not supported, rows

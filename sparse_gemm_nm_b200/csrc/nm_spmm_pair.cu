@@ -251,7 +251,7 @@ __device__ __forceinline__ void xgrad_block(const SpmmParams& p, uint32_t (&v)[3
   }
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const float4 d = __ldg(d4 + q);  // 0 for a column without a target, whatever its logits are
+    const float4 d = __ldg(d4 + q);  // 0: a column without a target or a gradient, whatever its logits are
     v[4 * q] = d.x == 0.f ? 0u : __float_as_uint(__uint_as_float(v[4 * q]) * d.x);
     v[4 * q + 1] = d.y == 0.f ? 0u : __float_as_uint(__uint_as_float(v[4 * q + 1]) * d.y);
     v[4 * q + 2] = d.z == 0.f ? 0u : __float_as_uint(__uint_as_float(v[4 * q + 2]) * d.z);

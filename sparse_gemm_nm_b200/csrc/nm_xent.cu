@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(256) xent_columns_kernel(const int32_t* target
   }
 }
 
-// G = dloss (exp(z - lse) - [row == target]) of a logits piece, bf16; 0 where the target is outside [0, R).
+// G = dloss (exp(z - lse) - [row == target]) of a logits piece, bf16; 0 where the target is outside [0, R) or dloss is 0,
+// whatever the logits are.
 // Columns T .. width - 1 (padding to whole 16-byte pieces) are written as 0.  TWO: what the rounding left over follows, as
 // a second bf16 term, in columns width .. 2 width - 1.
 template <bool TWO>
@@ -163,6 +164,7 @@ __global__ void __launch_bounds__(256) xent_g_kernel(const float* Z, int64_t ldz
   if (t >= width) return;
   float l[2], d[2];
   int64_t want[2];
+  bool live[2];
   for (int j = 0; j < 2; ++j) {
     const int64_t tj = t + j;
     const int32_t w = tj < T ? __ldg(target + tj) : -1;
@@ -170,12 +172,12 @@ __global__ void __launch_bounds__(256) xent_g_kernel(const float* Z, int64_t ldz
     want[j] = (int64_t)w - v0;
     l[j] = has ? __ldg(lse + tj) : 0.f;
     d[j] = has ? __ldg(dloss + tj) : 0.f;
+    live[j] = d[j] != 0.f;  // a NaN is
   }
-  const bool has0 = t < T && want[0] + v0 >= 0 && want[0] + v0 < R, has1 = t + 1 < T && want[1] + v0 >= 0 && want[1] + v0 < R;
   for (int64_t r = (int64_t)blockIdx.y * 64 + (threadIdx.x >> 5); r < rows && r < ((int64_t)blockIdx.y + 1) * 64; r += 8) {
     float g[2] = {0.f, 0.f};
-    if (has0) g[0] = d[0] * (exp2f((__ldcg(Z + r * ldz + t) - l[0]) * kLog2e) - (r == want[0] ? 1.f : 0.f));
-    if (has1) g[1] = d[1] * (exp2f((__ldcg(Z + r * ldz + t + 1) - l[1]) * kLog2e) - (r == want[1] ? 1.f : 0.f));
+    if (live[0]) g[0] = d[0] * (exp2f((__ldcg(Z + r * ldz + t) - l[0]) * kLog2e) - (r == want[0] ? 1.f : 0.f));
+    if (live[1]) g[1] = d[1] * (exp2f((__ldcg(Z + r * ldz + t + 1) - l[1]) * kLog2e) - (r == want[1] ? 1.f : 0.f));
     const uint32_t hi = pack_bf16x2(g[0], g[1]);
     *reinterpret_cast<uint32_t*>(G + r * ldg + t) = hi;
     if (TWO) *reinterpret_cast<uint32_t*>(G + r * ldg + width + t) = bf16x2_rest(g[0], g[1], hi);

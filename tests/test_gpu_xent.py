@@ -334,3 +334,19 @@ def test_gradients_of_few_tokens_carry_two_terms_on_every_gemm(K, T):
     want = torch.empty_like(dXp).index_copy_(0, torch.from_numpy(c.perm).long(), dXp), dW.gather(1, c.cols)
     for got, exact in zip((dX, dV), want):
         assert (f64(got) - f64(exact.to(BF))).norm() <= 2.0 ** -10 * exact.norm()
+
+
+# Each source of G: both SM-pair epilogues, and the pass over the logits of the one-SM, skinny and dense GEMMs
+@pytest.mark.parametrize("K,T", [(256, 200), (256, 264), (256, 100), (256, 24), (40, 300)])
+def test_a_token_with_no_weight_in_the_loss_has_no_gradient(K, T):
+    """dloss = 0 masks a token as a target outside does: its column of dX is 0 although its logits are not finite."""
+    c = Case(600, K, T, seed=51)
+    c.target.copy_(torch.arange(T) % 600)
+    masked = [0, 3, 17, T - 1]
+    c.dloss[masked] = 0.0
+    dX, dV = c.run()[2:]
+    assert not dX[:, masked].any()
+    c.X[5, masked[:2]] = float("nan")
+    c.X[5, masked[2:]] = float("inf")
+    dX2 = c.run()[2]
+    assert torch.equal(dX2, dX)
