@@ -497,7 +497,8 @@ NM_API nm_status nm_spmm_xent(const uint16_t* values, const uint32_t* meta, int 
  * Results repeat bit for bit.  Staged from the library's pool: a piece of G (and
  * of fp32 logits, outside the two-SM GEMM), 12 bytes per token, with dX (and
  * there) the piece's decompressed weights, one to eight K x T fp32 accumulators
- * (twice the columns where G has two terms), and Xp with idx.
+ * (twice the columns where G has two terms), with dV up to 32 tokens X twice,
+ * and Xp with idx.
  * Errors: as nm_spmm_t.
  */
 NM_API nm_status nm_spmm_xent_grad(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t R, int64_t K,

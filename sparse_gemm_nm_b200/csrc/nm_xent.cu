@@ -360,7 +360,7 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
   if (st != NM_OK) return st;
   const bool fused = spmm_pair_serves(h.values, h.meta, h.n, h.m, h.K, h.T);
   const bool dense = !fused && dense_logits(h.K, h.T);
-  const int64_t rows = piece_rows(h.R, h.K, h.T, fused ? 2 : 4), ldz = (h.T + 3) / 4 * 4, ldk = (h.K + 7) / 8 * 8;
+  const int64_t ldz = (h.T + 3) / 4 * 4, ldk = (h.K + 7) / 8 * 8;
   // With few tokens a sum has few terms, and the rounding of G to bf16 can be half again the rounding of the result
   // (149 x 3224 x 28: 2.5e-3 of the gradients instead of 1.7e-3).  Up to 128 tokens G's two terms fit the one column tile
   // of dX, up to 256 two, and the steps of dV hide behind its epilogue, so they cost little; above, the products do, and
@@ -368,8 +368,12 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
   // the SM-pair GEMM 32000 x 4096 x 256 takes 412 us with two terms and 361 with one, 1000 x 768 x 256 38 and 34).
   const bool two = h.T <= 256;
   const int terms = two ? 2 : 1;
-  // Columns of one term: whole boxes of the value gradient's product with two, which reads X again for the second.
-  const int64_t width = two ? (h.T + 63) / 64 * 64 : (h.T + 7) / 8 * 8;
+  // The value gradient's product takes X once for each term.  Up to 32 tokens both terms fit one 64-column box and meet a
+  // copy of X twice side by side (32000 x 512 x 8 97 us, in two boxes 107); above, a term has whole boxes of its own and
+  // the product reads X again (1000 x 768 x 256 38 us, with the copies 44).
+  const bool twice = two && h.T <= 32;
+  const int64_t per = two && !twice ? 64 : 8, width = (h.T + per - 1) / per * per;  // columns of one term
+  const int64_t rows = piece_rows(h.R, h.K, two ? width : h.T, fused && !two ? 2 : 4);  // by G's or the logits' bytes
   const int64_t ldg = terms * width, lda = two ? ldg : ldz, tokens = two ? ldg : h.T;  // of the products
   const int ranges = dense_t_ranges(rows, h.K, tokens);
   PairEpiData epi = {};
@@ -379,12 +383,24 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
   Parts parts;
   const int64_t at_g = parts.take(rows * ldg * 2), at_z = parts.take(fused ? 0 : rows * ldz * 4);
   const int64_t at_wd = parts.take(dX || dense ? rows * ldk * 2 : 0), at_acc = parts.take(dX ? ranges * h.K * lda * 4 : 0);
+  const int64_t at_x2 = parts.take(twice && dV ? h.K * ldg * 2 : 0);
   cudaError_t e = buf.get(parts.size());
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gradient piece");
   uint16_t* g = buf.as<uint16_t>(at_g);
   uint16_t* wd = buf.as<uint16_t>(at_wd);
   float* z = buf.as<float>(at_z);
   float* acc = buf.as<float>(at_acc);
+  const uint16_t* x = h.X;  // of the value gradient
+  int64_t ldx = h.ldx, x_tokens = h.T;
+  if (twice && dV) {
+    uint16_t* x2 = buf.as<uint16_t>(at_x2);
+    for (int q = 0; q < 2; ++q) {
+      e = launch_gather_rows(h.X, h.ldx, nullptr, h.K, h.T, x2 + q * width, ldg, s, nullptr, q > 0);
+      if (e != cudaSuccess) return cuda_fail(e, "input copy launch");
+    }
+    x = x2;
+    ldx = x_tokens = ldg;
+  }
   for (int64_t v0 = 0; v0 < h.R; v0 += rows) {
     const int64_t n = h.R - v0 < rows ? h.R - v0 : rows;
     if (fused) {  // the GEMM's epilogue turns the logits into G
@@ -414,8 +430,8 @@ nm_status run_xent_grad(Head h, const int32_t* idx, const int32_t* target, const
       if (st != NM_OK) return st;
     }
     if (dV) {
-      st = run_sddmm(h.row_meta(v0), h.n, h.m, n, h.K, nullptr, g, ldg, h.X, h.ldx, tokens,
-                     dV + v0 * value_cols(h.K, h.n, h.m), NM_OUT_BF16, s, dX != nullptr, h.T);
+      st = run_sddmm(h.row_meta(v0), h.n, h.m, n, h.K, nullptr, g, ldg, x, ldx, tokens,
+                     dV + v0 * value_cols(h.K, h.n, h.m), NM_OUT_BF16, s, dX != nullptr, x_tokens);
       if (st != NM_OK) return st;
     }
   }

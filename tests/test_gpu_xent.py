@@ -350,3 +350,44 @@ def test_a_token_with_no_weight_in_the_loss_has_no_gradient(K, T):
     c.X[5, masked[2:]] = float("inf")
     dX2 = c.run()[2]
     assert torch.equal(dX2, dX)
+
+
+def test_pieces_of_a_large_vocabulary_of_few_tokens():
+    """Several pieces whose G has two terms, the last one ragged: one token of eight features, half a million rows."""
+    c = Case(530_001, 16, 1, seed=61)
+    c.target.fill_(300_000)
+    loss, lse, dX, dV = c.run()
+    nm.nm_device_status()
+    c.check_loss(loss, lse)
+    c.check_grad(lse, dX, dV)
+
+
+def test_two_terms_repeat_bit_for_bit_on_streams_and_in_graphs():
+    cases = [Case(1500, 256, T, permuted=True, seed=62 + T) for T in (200, 256, 37)]
+    data = [(c.args(), c.dloss.to(DEV), c.idx) for c in cases]
+
+    def once(stream=None):
+        out = []
+        for args, dl, idx in data:
+            loss, lse = nm.spmm_xent(*args, idx=idx, stream=stream)
+            out += [loss, lse, *nm.spmm_xent_grad(*args, lse, dl, idx=idx, stream=stream)]
+        return out
+
+    first = once()
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(3)]
+    runs = [once(s) for s in side * 2]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(once())
+        graphs.append(g)
+    for s, g in zip(side * 2, graphs * 3):
+        with torch.cuda.stream(s):
+            g.replay()
+    torch.cuda.synchronize()
+    nm.nm_device_status()
+    for got in runs + outs:
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
