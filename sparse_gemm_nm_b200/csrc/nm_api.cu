@@ -571,7 +571,9 @@ static nm_status run_gemm(const GemmRequest& q, cudaStream_t stream) {
     // The skinny kernel's boxes of X arrive slowly when T ends inside the first 16 columns or the third (cross entropy
     // of 32000 x 4096: T = 8 45 us, T = 16 37 us; T = 37 62 us, T = 48 45 us), so where partial sums are the result (the
     // reader takes T columns of them) X is first copied to rows of 16 or 48 (T = 8 39 us, T = 37 47 us), whose last
-    // columns hold anything: each feeds its own column of sums only.  Below 16 stages an SM the copy costs as much.
+    // columns hold anything: each feeds its own column of sums only.  Below 16 stages an SM the copy costs as much, and so it
+    // does between 16 and 32 and behind 48 columns, where the boxes lose less (T = 17 to 31 2 to 4 us against 32, T = 49 to
+    // 63 2 to 6 us against 64; the copy takes 2 to 4 us).
     const bool slow = use_skinny && q.partials && (q.T < 16 || (q.T > 32 && q.T < 48));
     const bool pad = slow && (q.R + 127) / 128 * (q.K / 128) >= 16 * (int64_t)sm_count_current();
     int64_t cols = q.T;  // of the GEMM's X

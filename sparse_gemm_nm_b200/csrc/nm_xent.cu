@@ -26,11 +26,11 @@
 // Launches that need nothing of the one before them start beside it.
 //
 // Measured: 32000 x 4096 x 2048 forward 264 us (floor 160 us of sparse products;
-// the GEMM itself sets the time: its MMA issue and, in a loop, the power cap),
-// backward 1135 us (two dense products of 0.54 TFLOP beside the sparse one);
-// 37 tokens 47 us (floor 23 us of weights; 250 row tiles on 148 SMs, and every
-// tile reads X again); 1000 x 768 x 256 backward 28 us, launches and their
-// latency.
+// the GEMM itself sets the time: its MMA issue and, in a loop, the power cap, 305
+// us), backward 1135 us (two dense products of 0.54 TFLOP beside the sparse one;
+// 1265 us in a loop); 37 tokens 47 us (floor 23 us of weights; 250 row tiles on
+// 148 SMs, and every tile reads X again); 1000 x 768 x 256 backward 33 us,
+// launches and their latency.
 #include <cstdint>
 #include <cstring>
 #include <cuda_runtime.h>
