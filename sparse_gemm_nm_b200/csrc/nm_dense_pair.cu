@@ -124,6 +124,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
     tma_prefetch_desc(&p.tm_b);
     if (p.use_alt) tma_prefetch_desc(&p.tm_b_alt);
   }
+  cluster_sync();  // the allocation takes columns in both SMs: the peer has started
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
@@ -486,6 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, dpair::kTmemCols);
   }
+  cluster_sync();  // ... and so does the deallocation: neither CTA leaves before both are through it
   pdl_leave(p.early != 0);
 }
 

@@ -313,6 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     tma_prefetch_desc(&p.tm_x);
     tma_prefetch_desc(&p.tm_meta);
   }
+  cluster_sync();  // the allocation takes columns in both SMs: the peer has started
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
@@ -749,6 +750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);
   }
+  cluster_sync();  // ... and so does the deallocation: neither CTA leaves before both are through it
 }
 
 bool pair_kernel_fits(const SpmmParams& p) {
