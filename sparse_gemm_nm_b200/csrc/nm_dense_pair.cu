@@ -312,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
           word[1][c] = in ? __ldg(mb + 32) : 0u;
         }
       }
-      ok = mbar_wait(&acc_full[ab], (uint32_t)(i >> 1) & 1u, abort_flag, p.status, kWaitNs);
+      ok = mbar_wait_warp(&acc_full[ab], (uint32_t)(i >> 1) & 1u, abort_flag, p.status, kWaitNs);
       if (!ok) break;
       tc_fence_after();
       const uint32_t t_addr = tmem_base + ((uint32_t)(quarter * 32) << 16) + 256u * (uint32_t)ab;

@@ -524,6 +524,7 @@ __global__ void __launch_bounds__(lora::kThreads) lora_expand_kernel(const LoraE
     for (int b = 0; b < 4; ++b) {
       const unsigned used = ((b & 2 ? hi : lo) >> (16 * (b & 1))) & 0xFFFFu;  // this block's tokens of the adapter
       if (!used) continue;
+      __syncwarp();  // lanes kept other columns of the last block
       float d[2][4] = {};
       for (int ks = 0; ks < rs / 16; ++ks) {
         uint32_t w[4];

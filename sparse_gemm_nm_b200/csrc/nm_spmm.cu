@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) spmm_kernel(const __grid_constant
       const int tm = tile % p.tiles_m, tn = tile / p.tiles_m;
       const int64_t row = (int64_t)tm * 128 + quarter * 32 + lane;
       const int64_t n0 = (int64_t)tn * BN;
-      ok = mbar_wait(&acc_full[acc], aph, abort_flag, p.status, kWaitLimitNs);
+      ok = mbar_wait_warp(&acc_full[acc], aph, abort_flag, p.status, kWaitLimitNs);
       if (!ok) break;
       tc_fence_after();
       const uint32_t t_addr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN);

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(fused::kThreads, 1) prune_spmm_skinny_kernel(c
       unit_range(u, tm, kt0, kt1);
       const int sp = u / p.tiles_m;
       const int a = i % kAcc;
-      ok = mbar_wait(&acc_full[a], (uint32_t)(i / kAcc) & 1u, abort_flag, p.status, kWaitNs);
+      ok = mbar_wait_warp(&acc_full[a], (uint32_t)(i / kAcc) & 1u, abort_flag, p.status, kWaitNs);
       if (!ok) break;
       tc_fence_after();
       const int64_t row = (int64_t)tm * 128 + quarter * 32 + lane;

@@ -518,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair::kThreads, 1)
       const int tm = p.n_major ? tile / p.tiles_n : tile % p.tiles_m;
       const int tn = p.n_major ? tile % p.tiles_n : tile / p.tiles_m;
       const int64_t n0 = (int64_t)tn * C::kN;
-      ok = mbar_wait(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
+      ok = mbar_wait_warp(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
       if (!ok) break;
       tc_fence_after();
       const uint32_t t_addr = tmem_base + 256u * (uint32_t)acc + ((uint32_t)(quarter * 32) << 16);
