@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(lora::kThreads) lora_expand_kernel(const LoraE
     if (p.splits > 1) break;
     const int64_t row = r0 + 16 * warp + (lane >> 2) + 8 * h;
     int64_t brow = row < p.rows ? row : -1;
-    if (p.base_row && brow >= 0) brow = __ldg(p.base_row + row);
+    if (p.base_row && brow >= 0) brow = __ldcg(p.base_row + row);
     const float* src = p.base + brow * p.ldb + t0 + 2 * (lane & 3);
 #pragma unroll
     for (int nb = 0; nb < 8; ++nb) {

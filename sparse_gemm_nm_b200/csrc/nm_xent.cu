@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(256) xent_columns_kernel(const int32_t* target
   const bool has = w >= 0 && (int64_t)w < R;
   tgt[t] = has ? w : -1;
   if (lse) {
-    lse_out[t] = has ? __ldg(lse + t) : 0.f;
+    lse_out[t] = has ? __ldcg(lse + t) : 0.f;
     d[t] = has ? __ldg(dloss + t) : 0.f;
   }
 }
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(256) xent_g_kernel(const float* Z, int64_t ldz
     const int32_t w = tj < T ? __ldg(target + tj) : -1;
     const bool has = w >= 0 && (int64_t)w < R;
     want[j] = (int64_t)w - v0;
-    l[j] = has ? __ldg(lse + tj) : 0.f;
+    l[j] = has ? __ldcg(lse + tj) : 0.f;
     d[j] = has ? __ldg(dloss + tj) : 0.f;
     live[j] = d[j] != 0.f;  // a NaN is
   }
