@@ -63,14 +63,29 @@ def entropy(g, R, K, T):
     return call
 
 
-def test_threads_on_streams_of_their_own():
-    g = torch.Generator(device=DEV)
-    g.manual_seed(3)
-    calls = [norm(g, 1893, 97, F32), norm(g, 23, 3528, F32), norm(g, 10, 15, F32), norm(g, 768, 5001, BF),
-             norm(g, 5120, 13, BF), adapters(g, 309, 5888, 1006, 3, 49), adapters(g, 267, 512, 2308, 13, 8),
-             adapters(g, 330, 1152, 4096, 6, 12), adapters(g, 2602, 5096, 53, 3, 1), adapters(g, 24, 72, 6, 2, 8),
-             adapters(g, 2000, 1024, 16, 8, 16), entropy(g, 9492, 88, 4099), entropy(g, 3, 152, 8192), entropy(g, 94, 240, 1),
-             entropy(g, 183, 2280, 618), entropy(g, 803, 128, 3), entropy(g, 3000, 768, 200), entropy(g, 2000, 512, 1000)]
+def projection(g, R, K, T):
+    """The library's other calls on one shape: forward, permuted, one-call, hybrid, both gradients, and the other formats."""
+    W = (torch.randn((R, K), generator=g, device=DEV) * 0.05).to(BF)
+    values, meta = nm.prune_compress(W, 2, 4)
+    v18, m18 = nm.prune_compress(W, 1, 8)
+    X, dY = rows(g, K, T), rows(g, R, T)
+    idx = torch.randperm(K, generator=g, device=DEV).int()
+    tiles = torch.randint(0, 2, (-(-R // 128), -(-K // 128)), generator=g, device=DEV, dtype=torch.uint8)
+    W8 = torch.randint(-9, 10, (R, K), generator=g, device=DEV, dtype=torch.int8)
+    X8 = torch.randint(-9, 10, (K, -(-T // 16) * 16), generator=g, device=DEV, dtype=torch.int8)
+    v8, m8 = nm.prune_compress_i8(W8)
+    vf, mf = nm.prune_compress_tf32(W.float())
+    Xf = rows(g, K, T, F32)
+
+    def call():
+        return (nm.spmm(values, meta, 2, 4, K, X), nm.spmm(values, meta, 2, 4, K, X, idx=idx, out_dtype=F32),
+                nm.spmm(v18, m18, 1, 8, K, X), nm.prune_spmm(W, 2, 4, X), nm.hybrid_spmm(W, values, meta, tiles, X),
+                nm.spmm_t(values, meta, 2, 4, K, dY), nm.sddmm(meta, 2, 4, R, K, dY, X), nm.spmm_i8(v8, m8, K, X8),
+                nm.spmm_tf32(vf, mf, K, Xf), nm.decompress(values, meta, K, 2, 4))
+    return call
+
+
+def run_together(calls, seconds=10):
     alone = []
     for call in calls:
         alone.append(call())
@@ -81,7 +96,7 @@ def test_threads_on_streams_of_their_own():
     def work(k):
         pick, stream = random.Random(k), torch.cuda.Stream()
         with torch.cuda.stream(stream):
-            while time.monotonic() - start < 10:
+            while time.monotonic() - start < seconds:
                 got = [(i, calls[i]()) for i in (pick.randrange(len(calls)) for _ in range(pick.randint(3, 15)))]
                 done = torch.cuda.Event()
                 done.record()
@@ -105,3 +120,21 @@ def test_threads_on_streams_of_their_own():
     assert not wrong, wrong
     assert all(ended)
     nm.nm_device_status()
+
+
+def test_threads_on_streams_of_their_own():
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    calls = [norm(g, 1893, 97, F32), norm(g, 23, 3528, F32), norm(g, 10, 15, F32), norm(g, 768, 5001, BF),
+             norm(g, 5120, 13, BF), adapters(g, 309, 5888, 1006, 3, 49), adapters(g, 267, 512, 2308, 13, 8),
+             adapters(g, 330, 1152, 4096, 6, 12), adapters(g, 2602, 5096, 53, 3, 1), adapters(g, 24, 72, 6, 2, 8),
+             adapters(g, 2000, 1024, 16, 8, 16), entropy(g, 9492, 88, 4099), entropy(g, 3, 152, 8192), entropy(g, 94, 240, 1),
+             entropy(g, 183, 2280, 618), entropy(g, 803, 128, 3), entropy(g, 3000, 768, 200), entropy(g, 2000, 512, 1000)]
+    run_together(calls)
+
+
+def test_threads_on_streams_of_their_own_through_the_other_calls():
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    run_together([projection(g, 1000, 512, 264), projection(g, 300, 1152, 1000), projection(g, 520, 256, 24),
+                  projection(g, 260, 144, 200), norm(g, 768, 1001, BF), entropy(g, 9492, 88, 4099)])
