@@ -141,7 +141,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dpair::kThreads, 1)
   bool ok = true;
   auto ext_blocks = [&](int tn) -> uint32_t {  // the blocks that column tile tn's four 64-token tiles use
     uint32_t m = 0;
-    for (int64_t i = (int64_t)tn * 4; i < (int64_t)tn * 4 + 4 && i * 64 < p.N; ++i) m |= __ldcg(p.ext_masks + i);
+    for (int64_t i = (int64_t)tn * 4; i < (int64_t)tn * 4 + 4 && i * 64 < p.N; ++i) m |= p.ext_masks[i];
     return m;
   };
 

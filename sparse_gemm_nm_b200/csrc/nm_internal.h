@@ -49,8 +49,8 @@ struct GatherJob {
 };
 
 #ifdef __CUDACC__
-// What a launch before may still be writing while this kernel already runs up to its gate is read past L1 afterwards (TMA
-// or __ldcg): the read-only path (__ldg) is for data that does not change in a kernel's lifetime.
+// What a launch before may still be writing while this kernel already runs up to its gate is read by TMA or by ordinary
+// loads (or __ldcg) afterwards: the read-only path (__ldg) is for data that does not change in a kernel's lifetime.
 __device__ __forceinline__ void pdl_gate() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -86,10 +86,10 @@ __device__ __forceinline__ void gather_rows_items(const GatherJob& g, int64_t wa
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int64_t c = c0 + u * 32 + lane;
-      v[u] = (valid && c < whole) ? __ldcg(in + c) : make_uint4(0, 0, 0, 0);
+      v[u] = (valid && c < whole) ? in[c] : make_uint4(0, 0, 0, 0);
       if (valid && c == whole && c < pieces) {  // columns 8c .. T-1 one by one, zeros after them
         uint32_t w[4] = {0, 0, 0, 0};
-        for (int64_t j = 0; 8 * c + j < g.T; ++j) w[j >> 1] |= (uint32_t)__ldcg(row + 8 * c + j) << (16 * (j & 1));
+        for (int64_t j = 0; 8 * c + j < g.T; ++j) w[j >> 1] |= (uint32_t)row[8 * c + j] << (16 * (j & 1));
         v[u] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }

@@ -82,7 +82,7 @@ __device__ __forceinline__ void load_global(const void* base, int64_t off, int v
   if (F32) {
     const float* s = static_cast<const float*>(base) + off;
     if (valid >= 8) {
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(s)), b = __ldcg(reinterpret_cast<const float4*>(s) + 1);
+      const float4 a = *reinterpret_cast<const float4*>(s), b = *(reinterpret_cast<const float4*>(s) + 1);
       f[0] = f2(a.x, a.y);
       f[1] = f2(a.z, a.w);
       f[2] = f2(b.x, b.y);
@@ -90,13 +90,13 @@ __device__ __forceinline__ void load_global(const void* base, int64_t off, int v
     } else {  // the row's last tokens one by one, zeros after them
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        f[j] = f2(2 * j < valid ? __ldcg(s + 2 * j) : 0.f, 2 * j + 1 < valid ? __ldcg(s + 2 * j + 1) : 0.f);
+        f[j] = f2(2 * j < valid ? s[2 * j] : 0.f, 2 * j + 1 < valid ? s[2 * j + 1] : 0.f);
     }
   } else {
     const uint16_t* s = static_cast<const uint16_t*>(base) + off;
     uint32_t w[4] = {0, 0, 0, 0};
     if (valid >= 8) {
-      const uint4 a = __ldcg(reinterpret_cast<const uint4*>(s));
+      const uint4 a = *reinterpret_cast<const uint4*>(s);
       w[0] = a.x;
       w[1] = a.y;
       w[2] = a.z;
@@ -104,7 +104,7 @@ __device__ __forceinline__ void load_global(const void* base, int64_t off, int v
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < valid) w[j >> 1] |= (uint32_t)__ldcg(s + j) << (16 * (j & 1));
+        if (j < valid) w[j >> 1] |= (uint32_t)s[j] << (16 * (j & 1));
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[j] = f2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(norm::kThreads, 2) norm_grad_kernel(const __gr
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const bool a = 2 * j < valid, b = 2 * j + 1 < valid;
-    mean[j] = f2(a ? -__ldcg(p.mean + t0 + 2 * j) : 0.f, b ? -__ldcg(p.mean + t0 + 2 * j + 1) : 0.f);
-    rs[j] = f2(a ? __ldcg(p.rstd + t0 + 2 * j) : 0.f, b ? __ldcg(p.rstd + t0 + 2 * j + 1) : 0.f);
+    mean[j] = f2(a ? -p.mean[t0 + 2 * j] : 0.f, b ? -p.mean[t0 + 2 * j + 1] : 0.f);
+    rs[j] = f2(a ? p.rstd[t0 + 2 * j] : 0.f, b ? p.rstd[t0 + 2 * j + 1] : 0.f);
   }
   if (CACHED && boxes > 0) ok = mbar_wait(&bar, 0, &abort_flag, p.status, kWaitNs);
   const uint8_t* x_at = smem + (first * lpr + col8) * kX;

@@ -173,7 +173,7 @@ __device__ __forceinline__ void lse_epilogue(const SpmmParams& p, uint32_t t_add
     tmem_ld_16x256b_x4(t_addr + c * 32, lo);
     tmem_ld_16x256b_x4(t_addr + (16u << 16) + c * 32, hi);
     const int64_t t0 = n0 + 32 * c;
-    const int32_t want = t0 < p.T ? __ldcg(p.epi.target + t0 + lane) : -1;
+    const int32_t want = t0 < p.T ? p.epi.target[t0 + lane] : -1;
     tc_wait_ld();
     if (c == NB - 1) release();
     if (t0 >= p.T || wrow0 >= p.R) continue;
@@ -229,13 +229,13 @@ __device__ __forceinline__ void lse_epilogue(const SpmmParams& p, uint32_t t_add
 
 // The gradient of 32 columns of one logits row per lane: v becomes d (exp(v - lse) - [row == target]).
 __device__ __forceinline__ void xgrad_block(const SpmmParams& p, uint32_t (&v)[32], int64_t wrow0, int64_t t0, int lane) {
-  const int32_t want = __ldcg(p.epi.target + t0 + lane);
+  const int32_t want = p.epi.target[t0 + lane];
   const uint32_t at = (uint32_t)(want - p.epi.row0 - wrow0);
   const float4* l4 = reinterpret_cast<const float4*>(p.epi.lse + t0);
   const float4* d4 = reinterpret_cast<const float4*>(p.epi.d + t0);
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const float4 l = __ldcg(l4 + q);
+    const float4 l = l4[q];
     v[4 * q] = __float_as_uint(exp2_fast((__uint_as_float(v[4 * q]) - l.x) * kLog2e));
     v[4 * q + 1] = __float_as_uint(exp2_fast((__uint_as_float(v[4 * q + 1]) - l.y) * kLog2e));
     v[4 * q + 2] = __float_as_uint(exp2_fast((__uint_as_float(v[4 * q + 2]) - l.z) * kLog2e));
@@ -251,7 +251,7 @@ __device__ __forceinline__ void xgrad_block(const SpmmParams& p, uint32_t (&v)[3
   }
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const float4 d = __ldcg(d4 + q);  // 0: a column without a target or a gradient, whatever its logits are
+    const float4 d = d4[q];  // 0: a column without a target or a gradient, whatever its logits are
     v[4 * q] = d.x == 0.f ? 0u : __float_as_uint(__uint_as_float(v[4 * q]) * d.x);
     v[4 * q + 1] = d.y == 0.f ? 0u : __float_as_uint(__uint_as_float(v[4 * q + 1]) * d.y);
     v[4 * q + 2] = d.z == 0.f ? 0u : __float_as_uint(__uint_as_float(v[4 * q + 2]) * d.z);
@@ -263,7 +263,7 @@ __device__ __forceinline__ void xgrad_block(const SpmmParams& p, uint32_t (&v)[3
 __device__ __forceinline__ uint32_t ext_mask(const uint32_t* masks, int64_t n0, int64_t width, int64_t T) {
   const int64_t last = (n0 + width < T ? n0 + width : T) - 1;
   uint32_t m = 0;
-  for (int64_t i = n0 >> 6; i <= last >> 6; ++i) m |= __ldcg(masks + i);
+  for (int64_t i = n0 >> 6; i <= last >> 6; ++i) m |= masks[i];
   return m;
 }
 
