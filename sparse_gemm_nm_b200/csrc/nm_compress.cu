@@ -527,8 +527,8 @@ cudaError_t launch_decompress(const uint16_t* values, const uint32_t* meta, int6
     const bool vec = K % 16 == 0 && ldw % 8 == 0 && aligned16(W_out) && aligned16(values);
     const bool words = ((reinterpret_cast<uintptr_t>(values) | reinterpret_cast<uintptr_t>(W_out)) & 3u) == 0 && ldw % 2 == 0;
     launch_pdl(words ? decompress_2of4_tiled_kernel<true> : decompress_2of4_tiled_kernel<false>,
-        grid_for(total, threads), threads, 0, s, values, meta, (uint32_t)R, (uint32_t)K, W_out, ldw, (uint32_t)meta_col_blocks(K), (uint32_t)total, vec,
-        nullptr, 0u, early);
+        grid_for(total, threads), threads, 0, s, values, meta, (uint32_t)R, (uint32_t)K, W_out, ldw,
+        (uint32_t)meta_col_blocks(K), (uint32_t)total, vec, nullptr, 0u, early);
   } else {
     const int64_t work = R * (K / m);
     const int grid = grid_for(work, threads);

@@ -11,10 +11,11 @@
 // anything is scaled: the largest term of a sum is then exactly 1, and
 // loss = (max - z[target]) + log(sum) has no rounding of the size of the logits
 // and is never negative (lse - z[target] of scaled sums was off by 1.5e-5, and
-// below 0, for logits of 200).  On shapes of the SM-pair GEMM its epilogue makes the pairs of 32 rows
-// from the accumulator in TMEM, and no logit is written (32000 x 4096 x 2048
-// logits would be 262 MB written and read); elsewhere the vocabulary is taken in
-// pieces of rows whose logits xent_pairs_kernel reads, 256 rows to a pair.
+// below 0, for logits of 200).  On shapes of the SM-pair GEMM its epilogue makes
+// the pairs of 32 rows from the accumulator in TMEM, and no logit is written
+// (32000 x 4096 x 2048 logits would be 262 MB written and read); elsewhere the
+// vocabulary is taken in pieces of rows whose logits xent_pairs_kernel reads, 256
+// rows to a pair.
 // Backward: the logits of a piece are computed again and become G (bf16, rounded
 // once: it is an operand of the tensor cores like the dY of nm_spmm_t; two terms
 // for up to 256 tokens, see run_xent_grad), again in
