@@ -113,7 +113,9 @@ NM_API int64_t nm_meta_words(int64_t R, int64_t K, int n, int m);
  *   meta    [out] nm_meta_words(R,K,n,m) uint32, every word written
  * Magnitudes are compared on the bf16 value: +0 and -0 tie, a NaN ranks above
  * every number.  Exactly n survivors are stored per group, zeros included.
- * Errors: NM_ERR_INVALID_ARG (bad pattern, K % m, ldw < K, null pointer).
+ * 2:4 writes pairs: values 4-byte and meta 8-byte aligned.
+ * Errors: NM_ERR_INVALID_ARG (bad pattern, K % m, ldw < K, null pointer),
+ * NM_ERR_MISALIGNED.
  */
 NM_API nm_status nm_prune_compress(const uint16_t* W, int64_t R, int64_t K, int64_t ldw, int n, int m,
                             uint16_t* values, uint32_t* meta, void* stream);

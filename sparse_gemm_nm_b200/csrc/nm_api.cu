@@ -1704,6 +1704,8 @@ nm_status nm_prune_compress(const uint16_t* W, int64_t R, int64_t K, int64_t ldw
   if (!W || !values || !meta) return fail(NM_ERR_INVALID_ARG, "null pointer");
   if (R >= (1ll << 31) || K >= (1ll << 31) || meta_words(R, K, n, m) >= (1ll << 31))
     return fail(NM_ERR_UNSUPPORTED, "matrix too large for one call");
+  if (tiled_meta(n, m) && (!aligned_to(values, 4) || !aligned_to(meta, 8)))
+    return fail(NM_ERR_MISALIGNED, "2:4 compress: values must be 4-byte and meta 8-byte aligned");
   nm_status st = require_device();
   if (st != NM_OK) return st;
   cudaError_t e;

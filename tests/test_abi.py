@@ -217,3 +217,9 @@ def test_host_checks_of_element_alignment(lib):
             assert fn(p[0], p[1], 2, 4, 8, 32, p[2], 16, 8, 8, 16, 16, 4, 2, p[3], p[4], 16, 8, 0, None) == A
     for p in ((18, 16), (16, 18)):  # scale, adapter
         assert lib.nm_lora_grad(8, 32, 16, 8, 16, 8, 8, 16, 16, 4, 2, *p, 16, 16, 0, None) == A
+
+
+def test_compress_refuses_outputs_that_its_stores_cannot_take(lib):
+    """2:4 stores pairs of values and of metadata words; a pointer off their size would fault."""
+    assert lib.nm_prune_compress(16, 4, 8, 8, 2, 4, 18, 16, None) == nm.NM_ERR_MISALIGNED
+    assert lib.nm_prune_compress(16, 4, 8, 8, 2, 4, 16, 20, None) == nm.NM_ERR_MISALIGNED
