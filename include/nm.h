@@ -568,6 +568,48 @@ NM_API nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t 
                               const float* scale, const int32_t* adapter, void* dA, void* dB, nm_out_dtype dtype,
                               void* stream);
 
+/* -------------------------------------------------------------- experts */
+/*
+ * A layer of pruned experts (mixture of experts): every token passes through a
+ * few of E pruned projections of one shape.  The pages prune one projection;
+ * these calls run many side by side without a count on the host.  Columns are
+ * grouped by expert: expert e has the columns offsets[e] .. offsets[e+1]-1 of
+ * an activation matrix, in any numbers (none included) and starting anywhere.
+ * Arguments shared by the three products:
+ *   values  E x R x K/2 bf16, meta E x nm_meta_words(R, K, 2, 4) words: every
+ *           expert's 2:4 compressed form, one behind the other, 16-byte aligned
+ *           (nm_prune_compress of the E*R x K matrix where R % 16 == 0, else of
+ *           each expert into its place)
+ *   n, m    2:4 (NM_ERR_UNSUPPORTED for other patterns), K % 16 == 0
+ *   E       0..1024 (NM_ERR_UNSUPPORTED above)
+ *   S       columns of the activations; 16-byte rows as everywhere
+ *   offsets E + 1 int32, ascending, within [0, S] (read on the device; entries
+ *           outside are clamped, and columns that two experts claim hold either
+ *           one's result).  Columns before offsets[0] and from offsets[E] on
+ *           belong to no expert: they are not read into any result, and results
+ *           leave them as they were.
+ * No column depends on another column's data, and results repeat bit for bit.
+ * One launch each; nothing is staged.
+ *
+ * nm_experts_spmm: Y[:, s] = W'_e X[:, s] (R x S, bf16 or fp32), as nm_spmm.
+ * nm_experts_spmm_t: dX[:, s] = W'_e^T dY[:, s] (K x S, bf16 or fp32), as
+ *   nm_spmm_t; the weights are expanded on their way to the tensor cores.
+ * nm_experts_sddmm: dV_e = the survivors' entries of the sum over expert e's
+ *   columns of dY[:, s] X[:, s]^T (E x R x K/2, bf16 or fp32), as nm_sddmm;
+ *   zeros for an expert without columns.
+ * Sums are fp32, rounded once.
+ * Errors: as nm_spmm, nm_spmm_t and nm_sddmm.
+ */
+NM_API nm_status nm_experts_spmm(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t E, int64_t R,
+                                 int64_t K, const uint16_t* X, int64_t ldx, int64_t S, const int32_t* offsets, void* Y,
+                                 int64_t ldy, nm_out_dtype y_dtype, void* stream);
+NM_API nm_status nm_experts_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t E, int64_t R,
+                                   int64_t K, const uint16_t* dY, int64_t lddy, int64_t S, const int32_t* offsets,
+                                   void* dX, int64_t lddx, nm_out_dtype dtype, void* stream);
+NM_API nm_status nm_experts_sddmm(const uint32_t* meta, int n, int m, int64_t E, int64_t R, int64_t K,
+                                  const uint16_t* dY, int64_t lddy, const uint16_t* X, int64_t ldx, int64_t S,
+                                  const int32_t* offsets, void* dV, nm_out_dtype dtype, void* stream);
+
 /*
  * nm_spmm_algo --nm_spmm / nm_spmm_permuted (idx may be NULL) with the kernel
  * design chosen explicitly, to compare the sparse tensor-core path with the

@@ -71,6 +71,9 @@ SIGNATURES = {
     "nm_spmm_lora": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I, _I64, _P, _P, _P, _I64, _I, _P], _I),
     "nm_spmm_lora_t": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I, _I64, _P, _P, _P, _I64, _I, _P], _I),
     "nm_lora_grad": ([_I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I, _I64, _P, _P, _P, _P, _I, _P], _I),
+    "nm_experts_spmm": ([_P, _P, _I, _I, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I, _P], _I),
+    "nm_experts_spmm_t": ([_P, _P, _I, _I, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I, _P], _I),
+    "nm_experts_sddmm": ([_P, _I, _I, _I64, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I, _P], _I),
     "nm_spmm_algo": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I, _I, _P], _I),
     "nm_spmm_permuted_noalloc": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I, _P], _I),
     "nm_release_staging": ([], _I),
@@ -282,6 +285,22 @@ def nm_lora_grad(R, K, dY, lddy, X, ldx, T, A, B, rank, num_adapters, scale, ada
                  stream=None) -> None:
     _check(lib().nm_lora_grad(R, K, _ptr(dY), lddy, _ptr(X), ldx, T, _ptr(A), _ptr(B), rank, num_adapters, _ptr(scale),
                               _ptr(adapter), _ptr(dA), _ptr(dB), dtype, _stream(stream)), "nm_lora_grad")
+
+
+def nm_experts_spmm(values, meta, n, m, E, R, K, X, ldx, S, offsets, Y, ldy, y_dtype=NM_OUT_BF16, stream=None) -> None:
+    _check(lib().nm_experts_spmm(_ptr(values), _ptr(meta), n, m, E, R, K, _ptr(X), ldx, S, _ptr(offsets), _ptr(Y), ldy,
+                                 y_dtype, _stream(stream)), "nm_experts_spmm")
+
+
+def nm_experts_spmm_t(values, meta, n, m, E, R, K, dY, lddy, S, offsets, dX, lddx, dtype=NM_OUT_BF16,
+                      stream=None) -> None:
+    _check(lib().nm_experts_spmm_t(_ptr(values), _ptr(meta), n, m, E, R, K, _ptr(dY), lddy, S, _ptr(offsets), _ptr(dX),
+                                   lddx, dtype, _stream(stream)), "nm_experts_spmm_t")
+
+
+def nm_experts_sddmm(meta, n, m, E, R, K, dY, lddy, X, ldx, S, offsets, dV, dtype=NM_OUT_BF16, stream=None) -> None:
+    _check(lib().nm_experts_sddmm(_ptr(meta), n, m, E, R, K, _ptr(dY), lddy, _ptr(X), ldx, S, _ptr(offsets), _ptr(dV),
+                                  dtype, _stream(stream)), "nm_experts_sddmm")
 
 
 def nm_spmm_algo(values, meta, n, m, R, K, idx, X, ldx, T, Y, ldy, y_dtype=NM_OUT_BF16, algo=NM_ALGO_AUTO,
@@ -577,6 +596,89 @@ def lora_grad(dY, X, A, B, adapter, scale=None, out_dtype=None, stream=None):
         dB = X.new_empty((num, R, rank), dtype=out_dtype)
         nm_lora_grad(R, K, dY, lddy, X, ldx, T, A, B, rank, num, scale, adapter, dA, dB, yt, s)
     return dA, dB
+
+
+def _experts(values, meta, n: int, m: int, K: int, offsets):
+    """Checks the compressed operands of E experts and their columns' offsets; returns (E, R)."""
+    import torch
+    if values.dim() != 3 or values.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise ValueError(f"values must be three dimensions of bfloat16, got {values.dim()}-d {values.dtype}")
+    E, R = values.shape[:2]
+    cols = nm_value_cols(K, n, m)
+    if cols < 0:  # let the library name the bad argument
+        _check(lib().nm_prune_compress(None, R, K, K, n, m, None, None, None), "nm_prune_compress")
+    if values.shape[2] != cols or not values.is_contiguous():
+        raise ValueError(f"values must be {E} x {R} x {cols} contiguous for K={K} at {n}:{m}, got {tuple(values.shape)}")
+    _expert_words(meta, n, m, E, R, K, offsets)
+    return E, R
+
+
+def _expert_words(meta, n: int, m: int, E: int, R: int, K: int, offsets):
+    import torch
+    words = E * max(nm_meta_words(R, K, n, m), 0)
+    if meta.numel() != words or meta.element_size() != 4 or not meta.is_contiguous():
+        raise ValueError(f"meta must be {words} contiguous 32-bit words, got {meta.numel()} of {meta.dtype}")
+    _vector(offsets, "offsets", E + 1, torch.int32)
+
+
+def experts_spmm(values, meta, n: int, m: int, K: int, X, offsets, out_dtype=None, stream=None):
+    """Y[:, s] = W'_e X[:, s] for the columns s = offsets[e] .. offsets[e + 1] - 1 of every expert e.
+
+    values E x R x K*n/m bf16 and meta (E x nm_meta_words) hold the experts' compressed weights one behind the other, X
+    is K x S bf16, offsets E + 1 int32 on the device.  Y (R x S, rows padded to 16 bytes) is not written in columns
+    that belong to no expert.
+    """
+    import torch
+    _same_device(X, values, meta, offsets)
+    E, R = _experts(values, meta, n, m, K, offsets)
+    ldx = _rows(X, "X", torch.bfloat16)
+    S = X.shape[1]
+    if X.shape[0] != K:
+        raise ValueError(f"X has {X.shape[0]} rows, K is {K}")
+    out_dtype = out_dtype or torch.bfloat16
+    yt = _out_type(out_dtype)
+    with _On(X, stream) as s:
+        Y, ldy = _out_rows(X, R, S, out_dtype, yt)
+        nm_experts_spmm(values, meta, n, m, E, R, K, X, ldx, S, offsets, Y, ldy, yt, s)
+    return Y
+
+
+def experts_spmm_t(values, meta, n: int, m: int, K: int, dY, offsets, out_dtype=None, stream=None):
+    """dX[:, s] = W'_e^T dY[:, s] (K x S), the input gradient of experts_spmm; columns of no expert are not written."""
+    import torch
+    _same_device(dY, values, meta, offsets)
+    E, R = _experts(values, meta, n, m, K, offsets)
+    lddy = _rows(dY, "dY", torch.bfloat16)
+    S = dY.shape[1]
+    if dY.shape[0] != R:
+        raise ValueError(f"dY has {dY.shape[0]} rows, the experts {R}")
+    out_dtype = out_dtype or torch.bfloat16
+    yt = _out_type(out_dtype)
+    with _On(dY, stream) as s:
+        dX, lddx = _out_rows(dY, K, S, out_dtype, yt)
+        nm_experts_spmm_t(values, meta, n, m, E, R, K, dY, lddy, S, offsets, dX, lddx, yt, s)
+    return dX
+
+
+def experts_sddmm(meta, n: int, m: int, R: int, K: int, dY, X, offsets, out_dtype=None, stream=None):
+    """dV (E x R x K*n/m), the gradients of the experts' stored values; zeros for an expert without columns."""
+    import torch
+    _same_device(X, meta, dY, offsets)
+    E = offsets.numel() - 1
+    cols = nm_value_cols(K, n, m)
+    if cols < 0:  # let the library name the bad argument
+        _check(lib().nm_prune_compress(None, R, K, K, n, m, None, None, None), "nm_prune_compress")
+    _expert_words(meta, n, m, E, R, K, offsets)
+    ldx, lddy = _rows(X, "X", torch.bfloat16), _rows(dY, "dY", torch.bfloat16)
+    S = X.shape[1]
+    if X.shape[0] != K or dY.shape[0] != R or dY.shape[1] != S:
+        raise ValueError(f"X must be {K} x S and dY {R} x S, got {tuple(X.shape)} and {tuple(dY.shape)}")
+    out_dtype = out_dtype or torch.bfloat16
+    yt = _out_type(out_dtype)
+    with _On(X, stream) as s:
+        dV = X.new_empty((E, R, cols), dtype=out_dtype)
+        nm_experts_sddmm(meta, n, m, E, R, K, dY, lddy, X, ldx, S, offsets, dV, yt, s)
+    return dV
 
 
 def prune_compress(W, n: int, m: int, stream=None):

@@ -245,15 +245,15 @@ static nm_status set_store_map(DenseParams& p, void* out, int64_t rows, int64_t 
 }
 
 // 3-D map of the tiled 2:4 metadata: {64 words of a block, column blocks, row blocks}.
-static nm_status make_meta_tmap(CUtensorMap* tm, const void* meta, int64_t rblocks, int64_t cblocks) {
-  const TmapKey key{meta, 64, (uint64_t)cblocks, (uint64_t)rblocks, 256, (uint64_t)cblocks * 256, 64, 1, 8, 0,
+nm_status make_meta_tmap(CUtensorMap* tm, const void* meta, int64_t rblocks, int64_t cblocks, uint32_t box_rblocks) {
+  const TmapKey key{meta, 64, (uint64_t)cblocks, (uint64_t)rblocks, 256, (uint64_t)cblocks * 256, 64, 1, box_rblocks, 0,
                     (int)CU_TENSOR_MAP_DATA_TYPE_UINT32, 3};
   if (t_tmaps.find(key, tm)) return NM_OK;
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(NM_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   cuuint64_t dims[3] = {64, (cuuint64_t)cblocks, (cuuint64_t)rblocks};
   cuuint64_t strides[2] = {256, (cuuint64_t)cblocks * 256};
-  cuuint32_t box[3] = {64, 1, 8};
+  cuuint32_t box[3] = {64, 1, box_rblocks};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(meta), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -1,0 +1,326 @@
+// nm_experts.cu -- products grouped by expert: Y[:, s] = W'_e X[:, s] for the columns s of expert e, W'_e the expert's 2:4
+// weight, from the compressed operand on the sparse tensor cores of SM pairs.
+//
+// One persistent launch covers all experts.  The pairs derive the list of tiles from the device's offsets
+// (nm_experts.cuh), so no count is needed on the host.  A tile is 256 rows of one expert by up to 256 of its columns; its
+// width is a run-time operand of the MMA, in steps of 32, so that an expert with few columns costs few MMA cycles, and its
+// X copies only the 64-column strips that the width reaches.
+//
+// Per CTA and stage of 128 logical K (as in nm_spmm_pair.cu, whose layouts these are): A 128 rows of compressed values
+// (16 KB), E their metadata (2 KB), B 128 rows of X by this CTA's half of the columns, in strips of 64 (16 KB each).  The
+// boxes of values come from a map of three axes, so rows past an expert's last read as zeros and not as the next expert's.
+// K may end inside a stage: values and X read as zeros there, and the padded metadata is valid.
+//
+// Forms (MAXN columns a tile, ACC accumulators):
+//   256, 1  many columns.  As in nm_spmm_pair.cu the whole accumulator leaves TMEM for registers before it is stored.
+//   224, 2  the same for short K, where the hand-over of the accumulator is a large part of a tile.
+//   128, 2  few columns per expert: bound by reading the weights once, so six stages of 34 KB instead of four of 50 KB.
+//
+// Stores: 64-column boxes that lie inside the expert's columns leave as TMA stores; in the boxes that hold an expert's
+// first and last columns, lanes store 16-byte units, and the units that two experts share element by element.
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "nm_experts.cuh"
+#include "nm_experts.h"
+#include "nm_host.h"
+#include "nm_internal.h"
+#include "nm_ptx.cuh"
+
+namespace nmk {
+
+namespace grp {
+constexpr int kThreads = 320;  // warps 0, 2 values; 3, 4 X; 5 metadata; 1 MMA; 6-9 epilogue
+constexpr uint32_t kA = 16384, kE = 2048;
+constexpr uint32_t kStrip = 16384;  // 128 rows x 64 columns of X
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+template <int MAXN, int ACC>
+struct Cfg {
+  static constexpr int kStrips = MAXN > 128 ? 2 : 1;  // of one CTA
+  static constexpr int kStages = kStrips == 2 ? 4 : 6;
+  static constexpr uint32_t kB = kStrips * kStrip;
+  static constexpr uint32_t kECol = ACC == 1 ? 256u : 256u + (MAXN + 31) / 32 * 32;  // TMEM column of the metadata
+  static constexpr uint32_t kOffB = kStages * kA, kOffE = kOffB + kStages * kB, kOffEpi = kOffE + kStages * kE;
+  static constexpr uint32_t kOffBar = kOffEpi + 4 * kBoxBytes;
+  static constexpr uint32_t kOffFirst = kOffBar + (2 * kStages + 5) * 8 + 8;
+  static constexpr uint32_t bytes(int E) { return kOffFirst + 4u * (uint32_t)(E + 1) + 1024u; }
+  static_assert(kECol + 4 * kStages <= kTmemCols, "TMEM columns");
+  static_assert(kOffFirst + 4 * (kMaxExperts + 1) + 1024 <= 232448, "shared memory");
+};
+
+}  // namespace grp
+
+template <int MAXN, int ACC>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
+    experts_pair_kernel(const __grid_constant__ ExpertsParams p) {
+  using namespace grp;
+  using C = Cfg<MAXN, ACC>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;    // [2]
+  uint64_t* spare = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(spare + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* first = reinterpret_cast<int32_t*>(smem + C::kOffFirst);
+
+  const uint32_t rank = cluster_ctarank();  // 0: leader (issues the MMAs)
+  const int pair_id = blockIdx.x >> 1;
+  const int npairs = gridDim.x >> 1;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], 8);
+    }
+    mbar_init(spare, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 2 && lane == 0) {
+    tma_prefetch_desc(&p.tm_vals);
+    tma_prefetch_desc(&p.tm_x);
+    tma_prefetch_desc(&p.tm_meta);
+  }
+  cluster_sync();  // the allocation takes columns in both SMs: the peer has started
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  pdl_gate();  // no global memory touched before this point
+  if (warp == 0) list_tiles(p.offsets, p.E, p.S, MAXN, p.tiles_m, first, lane);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
+  const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
+  bool ok = true;
+  TileWalk w;
+
+  if (warp == 1) {
+    // ---------------------------------------------------------- MMA (leader)
+    if (rank == 0 && lane == 0) {
+      int s = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;  // aph bit a: phase of accumulator a
+      for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, MAXN); tile += npairs) {
+        ok = mbar_wait(&acc_empty[acc], ((aph >> acc) & 1u) ^ 1u, abort_flag, p.status, kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + 256u * (uint32_t)acc;
+        const uint32_t idesc = idesc_bf16((uint32_t)w.n, true, 256);
+        for (int kt = 0; kt < p.k_tiles; ++kt) {
+          ok = mbar_wait(&full[s], ph, abort_flag, p.status, kWaitNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + s * kA);
+          const uint32_t b_addr = smem_u32(smem + C::kOffB + s * C::kB);
+          const uint32_t e_tmem = tmem_base + C::kECol + 4u * (uint32_t)s;
+          tc_cp_128x128b_pair(e_tmem, smem_desc(smem_u32(smem + C::kOffE + s * kE), 2048, 128, SWZ_NONE));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t ad = smem_desc(a_addr + kk * 32, 16, 1024, SWZ_128B);
+            const uint64_t bd = smem_desc(b_addr + kk * 4096, kStrip, 1024, SWZ_128B);
+            tc_mma_sp_pair(d_tmem, ad, bd, e_tmem + (uint32_t)(kk & 2), idesc | (uint32_t)(kk & 1),
+                           (kt > 0 || kk > 0) ? 1u : 0u);
+          }
+          tc_commit_pair(&empty[s], 0x3);
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+        if (!ok) break;
+        tc_commit_pair(&acc_full[acc], 0x3);
+        aph ^= 1u << acc;
+        if (ACC == 2) acc ^= 1;
+      }
+      if (!ok) {
+        tc_commit_pair(spare, 0x1);
+        volatile int dummy = 0;
+        mbar_wait(spare, 0, &dummy, p.status, 100000000ull);
+      }
+    }
+  } else if (warp < 6) {
+    // ------ copies, each warp a part of every stage: 0, 2 halves of the values, 3, 4 K halves of X, 5 the metadata
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, MAXN); tile += npairs) {
+        const int32_t row0 = w.tm * 256 + 128 * (int)rank;
+        const int32_t col0 = w.x0 + (w.n >> 1) * (int32_t)rank;
+        const int strips = C::kStrips == 2 && w.n > 128 ? 2 : 1;
+        for (int kt = 0; kt < p.k_tiles; ++kt) {
+          ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
+          if (!ok) break;
+          const uint32_t bar = lead_full0 + 8u * s;
+          if (warp == 0 || warp == 2) {
+            const int h = warp >> 1;
+            if (rank == 0 && h == 0)
+              mbar_arrive_expect_tx(&full[s], 2u * (kA + kE + (uint32_t)strips * kStrip));
+            tma_load_3d_pair(smem + s * kA + h * 8192, &p.tm_vals, bar, kt * 64, row0 + 64 * h, w.e);
+          } else if (warp <= 4) {
+            const int h = warp - 3;
+            uint8_t* b = smem + C::kOffB + s * C::kB + h * 8192;
+            tma_load_2d_pair(b, &p.tm_x, bar, col0, kt * 128 + 64 * h);
+            if (strips == 2) tma_load_2d_pair(b + kStrip, &p.tm_x, bar, col0 + 64, kt * 128 + 64 * h);
+          } else {
+            tma_load_3d_pair(smem + C::kOffE + s * kE, &p.tm_meta, bar, 0, kt, w.e * p.meta_rblocks + row0 / 16);
+          }
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int quarter = warp & 3;
+    uint8_t* box = smem + C::kOffEpi + quarter * kBoxBytes;
+    uint32_t aph = 0;
+    int acc = 0;
+    for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, MAXN); tile += npairs) {
+      ok = mbar_wait_warp(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t_addr = tmem_base + 256u * (uint32_t)acc + ((uint32_t)(quarter * 32) << 16);
+      const int32_t wrow0 = w.tm * 256 + 128 * (int)rank + quarter * 32;
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
+      };
+      if (ACC == 2 || p.out_f32) {
+        store_tile(p, w, t_addr, box, wrow0, lane, release);
+      } else {
+        const int32_t end = min(w.c1, w.x0 + w.n);
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (64 * c < w.n) {
+            take_bf16(t_addr + c * 64, v[c]);
+            take_bf16(t_addr + c * 64 + 32, v[c] + 16);
+          }
+        }
+        release();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (64 * c < w.n) store_chunk<uint16_t>(p, v[c], box, w.x0 + 64 * c, w.c0, end, wrow0, lane);
+      }
+      aph ^= 1u << acc;
+      if (ACC == 2) acc ^= 1;
+    }
+    if (lane == 0) bulk_wait_group<0>();  // every store of this warp has landed
+  }
+
+  // -------------------------------------------------------------- teardown
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) sleep_about_ns(200000ull);
+  cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+  cluster_sync();  // ... and so does the deallocation: neither CTA leaves before both are through it
+}
+
+template <int MAXN, int ACC>
+static cudaError_t launch_experts(const ExpertsParams& p, cudaStream_t stream) {
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(experts_pair_kernel<MAXN, ACC>, grp::Cfg<MAXN, ACC>::bytes(kMaxExperts));
+  if (e != cudaSuccess) return e;
+  const int pairs = experts_pairs(p, MAXN);
+  e = launch_pdl(experts_pair_kernel<MAXN, ACC>, dim3(2 * pairs), dim3(grp::kThreads), grp::Cfg<MAXN, ACC>::bytes(p.E), stream,
+                 p);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+int experts_pairs(const ExpertsParams& p, int max_n) {
+  const int64_t most = (int64_t)p.tiles_m * (p.S / max_n + (p.E < p.S ? p.E : p.S) + 1);
+  const int pairs = sm_count_current() / 2;
+  return most < pairs ? (int)most : pairs;
+}
+
+nm_status make_experts_store_map(ExpertsParams& p, void* Y, int64_t M, int64_t S, int64_t ldy) {
+  return p.out_f32 ? make_tmap(&p.tm_y, Y, (uint64_t)S, (uint64_t)M, (uint64_t)ldy * 4, 32, 32, 128, "Y (fp32)",
+                               CU_TENSOR_MAP_DATA_TYPE_FLOAT32)
+                   : make_tmap(&p.tm_y, Y, (uint64_t)S, (uint64_t)M, (uint64_t)ldy * 2, 64, 32, 128, "Y");
+}
+
+nm_status check_experts(int n, int m, int64_t E, int64_t R, int64_t K, int64_t S, const int32_t* offsets) {
+  if (E < 0 || R < 0 || K < 0 || S < 0) return fail(NM_ERR_INVALID_ARG, "negative dimension");
+  if (!pattern_ok(n, m)) return fail(NM_ERR_INVALID_ARG, "pattern %d:%d not supported", n, m);
+  if (K < 1 || K % m != 0) return fail(NM_ERR_INVALID_ARG, "K=%lld is not a positive multiple of M=%d", (long long)K, m);
+  if (n != 2 || m != 4) return fail(NM_ERR_UNSUPPORTED, "products grouped by expert take 2:4, not %d:%d", n, m);
+  if (K % 16 != 0) return fail(NM_ERR_UNSUPPORTED, "K=%lld is not a multiple of 16", (long long)K);
+  if (E > kMaxExperts) return fail(NM_ERR_UNSUPPORTED, "more than %d experts", kMaxExperts);
+  const int64_t lim = kMaxDim - 4096;  // tile corners are 32-bit
+  if (R >= lim || K >= lim || S >= lim || E * ((R + 15) / 16) >= lim ||
+      (S / 128 + E + 1) * ((R > K ? R : K) / 256 + 1) >= lim)
+    return fail(NM_ERR_UNSUPPORTED, "dimensions too large");
+  if (E > 0 && S > 0 && !offsets) return fail(NM_ERR_INVALID_ARG, "offsets is null");
+  return check_words({offsets}, "offsets");
+}
+
+}  // namespace nmk
+
+using namespace nmk;
+
+extern "C" nm_status nm_experts_spmm(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t E, int64_t R,
+                                     int64_t K, const uint16_t* X, int64_t ldx, int64_t S, const int32_t* offsets, void* Y,
+                                     int64_t ldy, nm_out_dtype y_dtype, void* stream) {
+  set_last_error("");
+  nm_status st = check_experts(n, m, E, R, K, S, offsets);
+  if (st != NM_OK) return st;
+  if (!dtype_ok(y_dtype)) return fail(NM_ERR_INVALID_ARG, "bad output dtype");
+  if (E == 0 || R == 0 || S == 0) return NM_OK;
+  if (!values || !meta) return fail(NM_ERR_INVALID_ARG, "values or meta is null");
+  st = check_matrix(X, ldx, S, 2, "X");
+  if (st == NM_OK) st = check_matrix(Y, ldy, S, dtype_bytes(y_dtype), "Y");
+  if (st != NM_OK) return st;
+  if (!al16(values) || !al16(meta)) return fail(NM_ERR_MISALIGNED, "values and meta must be 16-byte aligned");
+  st = require_device();
+  if (st != NM_OK) return st;
+  ExpertsParams p;
+  std::memset(&p, 0, sizeof p);
+  p.offsets = offsets;
+  p.Y = Y;
+  p.ldy = ldy;
+  p.M = (int32_t)R;
+  p.S = (int32_t)S;
+  p.E = (int32_t)E;
+  p.k_tiles = (int32_t)((K + 127) / 128);
+  p.tiles_m = (int32_t)((R + 255) / 256);
+  p.meta_rblocks = (int32_t)meta_row_blocks(R);
+  p.out_f32 = y_dtype == NM_OUT_F32;
+  p.status = status_word_ptr();
+  if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
+  st = make_tmap3(&p.tm_vals, values, (uint64_t)(K / 2), (uint64_t)R, (uint64_t)E, (uint64_t)K, (uint64_t)(R * K), 64, 64, 128,
+                  "values");
+  if (st == NM_OK) st = make_meta_tmap(&p.tm_meta, meta, E * meta_row_blocks(R), meta_col_blocks(K));
+  if (st == NM_OK) st = make_tmap(&p.tm_x, X, (uint64_t)S, (uint64_t)K, (uint64_t)ldx * 2, 64, 64, 128, "X");
+  if (st == NM_OK) st = make_experts_store_map(p, Y, R, S, ldy);
+  if (st != NM_OK) return st;
+  cudaError_t e;
+  if (S <= 96 * E)
+    e = launch_experts<128, 2>(p, (cudaStream_t)stream);
+  else if (p.k_tiles <= 8)
+    e = launch_experts<224, 2>(p, (cudaStream_t)stream);
+  else
+    e = launch_experts<256, 1>(p, (cudaStream_t)stream);
+  return e == cudaSuccess ? NM_OK : cuda_fail(e, "grouped product launch");
+}

@@ -1,0 +1,177 @@
+// nm_experts.cuh -- the columns of a product grouped by expert as tiles (internal).
+//
+// Columns [offsets[e], offsets[e + 1]) of the activations belong to expert e.  The counts are known on the device alone,
+// so every CTA derives the same list of tiles from the offsets when it starts: expert e has row_tiles * nt tiles, nt column
+// tiles of at most max_n columns.  A column tile starts on a 16-byte unit of the rows (TMA loads from no other place): an
+// expert's first tile begins at its first column rounded down to a multiple of 8, and the columns of its neighbours that a
+// tile takes along are computed and not stored.
+#pragma once
+#include <cstdint>
+
+#include "nm_experts.h"
+#include "nm_ptx.cuh"
+
+namespace nmk {
+
+
+struct ExpertCols {
+  int32_t c0, c1;  // the expert's columns
+  int32_t a0;      // its first tile's first column
+  int32_t nt;      // column tiles
+  int32_t step;    // columns of a tile, a multiple of 32
+};
+
+// Offsets are clamped to the matrix, whatever they hold.
+__device__ __forceinline__ ExpertCols expert_cols(const int32_t* offsets, int e, int32_t S, int max_n) {
+  ExpertCols x;
+  x.c0 = min(max(__ldcg(offsets + e), 0), S);
+  x.c1 = min(max(__ldcg(offsets + e + 1), x.c0), S);
+  x.a0 = x.c0 & ~7;
+  const int32_t w = x.c1 > x.c0 ? x.c1 - x.a0 : 0;
+  x.nt = (w + max_n - 1) / max_n;
+  x.step = x.nt ? ((w + x.nt - 1) / x.nt + 31) & ~31 : 0;  // even widths: 260 columns are 160 + 100, not 256 + 4
+  return x;
+}
+
+// first[e] = number of the first tile of expert e, first[E] = number of tiles.  One warp; `first` is shared memory.
+__device__ __forceinline__ void list_tiles(const int32_t* offsets, int E, int32_t S, int max_n, int row_tiles, int32_t* first,
+                                           int lane) {
+  int32_t base = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    int32_t n = e0 + lane < E ? expert_cols(offsets, e0 + lane, S, max_n).nt * row_tiles : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t up = __shfl_up_sync(0xFFFFFFFFu, n, o);
+      if (lane >= o) n += up;
+    }
+    if (e0 + lane < E) first[e0 + lane + 1] = base + n;
+    base += __shfl_sync(0xFFFFFFFFu, n, 31);
+  }
+  if (lane == 0) first[0] = 0;
+}
+
+// Walks the tiles id, id + stride, ... in ascending order.  Column tiles go fastest, so that the pairs running together
+// share a block of weights, which streams from HBM once.
+struct TileWalk {
+  int e, tm;       // expert, row tile
+  int32_t x0, n;   // first column, columns (a multiple of 32)
+  int32_t c0, c1;  // the expert's columns
+  ExpertCols cols;
+  int known;
+
+  __device__ __forceinline__ TileWalk() : e(0), known(-1) {}
+  // Sets the members for tile `id` (at least the last call's); false behind the last tile.
+  __device__ __forceinline__ bool at(int id, const int32_t* first, const int32_t* offsets, int E, int32_t S, int max_n) {
+    if (id >= first[E]) return false;
+    while (id >= first[e + 1]) ++e;
+    if (e != known) {
+      cols = expert_cols(offsets, e, S, max_n);
+      known = e;
+    }
+    const int at = id - first[e];
+    tm = at / cols.nt;
+    const int32_t tn = at - tm * cols.nt;
+    c0 = cols.c0;
+    c1 = cols.c1;
+    x0 = cols.a0 + tn * cols.step;
+    const int32_t left = (cols.c1 - x0 + 31) & ~31;
+    n = left < cols.step ? left : cols.step;
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------ stores
+constexpr uint32_t kBoxBytes = 4096;  // an epilogue warp's staging tile: 32 rows x 128 bytes, 128-byte swizzle
+
+// Elements [from, to) of a 16-byte unit, one by one.
+template <typename T>
+__device__ __forceinline__ void store_unit_part(const uint4& u, T* dst, int from, int to) {
+  constexpr int kPer = 16 / (int)sizeof(T);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (i >= from && i < to) dst[i] = sizeof(T) == 2 ? (T)(w[i >> 1] >> (16 * (i & 1))) : (T)w[i & 3];
+}
+
+// A warp's staged box (32 rows of 128 bytes, swizzled), columns x .. of rows wrow0 ..: whole by TMA, or its part inside
+// [c0, c1) by the lanes.
+template <typename T>
+__device__ __forceinline__ void store_box(const ExpertsParams& p, const uint8_t* box, int32_t x, int32_t c0, int32_t c1,
+                                          int32_t wrow0, int lane) {
+  constexpr int kPer = 16 / (int)sizeof(T), kCols = 8 * kPer;
+  if (wrow0 >= p.M || x >= c1 || x + kCols <= c0) return;
+  if (x >= c0 && x + kCols <= c1) {
+    if (lane == 0) {
+      tma_store_2d(&p.tm_y, box, x, wrow0);
+      bulk_commit_group();
+    }
+    return;
+  }
+  const int unit = lane & 7;
+  const int32_t u0 = x + unit * kPer;
+  const int from = max(c0 - u0, 0), to = min(c1 - u0, kPer);
+  if (from >= to) return;
+  T* col = static_cast<T*>(p.Y) + u0;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    if (wrow0 + r >= p.M) break;
+    const uint4 u = *reinterpret_cast<const uint4*>(box + r * 128 + ((unit ^ (r & 7)) << 4));
+    T* dst = col + (int64_t)(wrow0 + r) * p.ldy;
+    if (from == 0 && to == kPer)
+      *reinterpret_cast<uint4*>(dst) = u;
+    else
+      store_unit_part<T>(u, dst, from, to);
+  }
+}
+
+// 32 accumulator columns of the warp's 32 rows as bf16 pairs.
+__device__ __forceinline__ void take_bf16(uint32_t t_addr, uint32_t* out) {
+  uint32_t v[32];
+  tmem_ld_32x32b_x32(t_addr, v);
+  tc_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) out[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+}
+
+// One chunk (128 bytes of each of the warp's 32 rows, a row a lane) through the warp's staging tile.
+template <typename T>
+__device__ __forceinline__ void store_chunk(const ExpertsParams& p, const uint32_t (&v)[32], uint8_t* box, int32_t x,
+                                            int32_t c0, int32_t c1, int32_t wrow0, int lane) {
+  if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read it
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+        make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  store_box<T>(p, box, x, c0, c1, wrow0, lane);
+}
+
+// The warp's 32 rows of a tile, chunk by chunk; `release` is called after the last TMEM load.  Accumulator columns behind
+// the tile's hold what an earlier tile left there: they lie behind `end`.
+template <typename Release>
+__device__ __forceinline__ void store_tile(const ExpertsParams& p, const TileWalk& w, uint32_t t_addr, uint8_t* box,
+                                           int32_t wrow0, int lane, Release release) {
+  const int32_t end = min(w.c1, w.x0 + w.n);
+  const int step = p.out_f32 ? 32 : 64;
+#pragma unroll 1
+  for (int c = 0; c < w.n; c += step) {
+    uint32_t v[32];
+    if (p.out_f32) {
+      tmem_ld_32x32b_x32(t_addr + c, v);
+      tc_wait_ld();
+    } else {
+      take_bf16(t_addr + c, v);
+      take_bf16(t_addr + c + 32, v + 16);
+    }
+    if (c + step >= w.n) release();
+    if (p.out_f32)
+      store_chunk<uint32_t>(p, v, box, w.x0 + c, w.c0, end, wrow0, lane);
+    else
+      store_chunk<uint16_t>(p, v, box, w.x0 + c, w.c0, end, wrow0, lane);
+  }
+}
+
+}  // namespace nmk

@@ -1,0 +1,48 @@
+// nm_experts.h -- parameter blocks and shared checks of the products grouped by expert (internal).
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "nm_host.h"
+
+namespace nmk {
+
+constexpr int kMaxExperts = 1024;
+
+// Y[:, s] = W'_e X[:, s], or its transpose's: M rows of Y.
+struct ExpertsParams {
+  CUtensorMap tm_vals;  // compressed values {K / 2, R, E}, box {64, 64, 1}, 128B swizzle
+  CUtensorMap tm_meta;  // tiled metadata {64 words, column blocks, E x row blocks}, box {64, 1, 8} (transposed: 4)
+  CUtensorMap tm_x;     // X K x S (transposed: dY R x S), box {64, 64}, 128B swizzle
+  CUtensorMap tm_y;     // Y M x S, box {64 bf16 | 32 fp32, 32 rows}, 128B swizzle
+  const int32_t* offsets;
+  void* Y;
+  int64_t ldy;
+  int32_t M, S, E;
+  int32_t k_tiles, tiles_m, meta_rblocks;  // stages of a tile, row tiles, row blocks of one expert's metadata
+  int out_f32;
+  uint32_t* status;
+};
+
+// Gradient of the survivors: dV_e[r][j] = sum over expert e's columns s of dY[r][s] X[k_j][s].
+struct ExpertsGradParams {
+  CUtensorMap tm_a, tm_b;  // dY R x S and X K x S, box {64, 64}, 128B swizzle
+  const int32_t* offsets;
+  const uint32_t* meta;
+  void* dV;
+  int64_t R, K;
+  int32_t S, E;
+  int32_t tiles_m, tiles_n, meta_cblocks;
+  int64_t meta_words;  // of one expert
+  int out_f32;
+  uint32_t* status;
+};
+
+// What the grouped products check alike.
+nm_status check_experts(int n, int m, int64_t E, int64_t R, int64_t K, int64_t S, const int32_t* offsets);
+// SM pairs for as many tiles as there can be.
+int experts_pairs(const ExpertsParams& p, int max_n);
+nm_status make_experts_store_map(ExpertsParams& p, void* Y, int64_t M, int64_t S, int64_t ldy);
+
+}  // namespace nmk

@@ -1,0 +1,680 @@
+// nm_experts_grad.cu -- the two gradients of products grouped by expert (nm_experts.cu), with expert e's columns s:
+//   dX[:, s] = W'_e^T dY[:, s]          (experts_t_kernel), and
+//   dV_e = the survivors' entries of sum_s dY[:, s] X[:, s]^T   (experts_dv_kernel).
+// W'^T is 2:4 along its output axis and the product for dV has no sparse operand, so both are dense MMAs on SM pairs
+// (M = 256, N up to 256, two accumulators).
+//
+// experts_t_kernel reads the compressed weights and expands them on the way to the tensor core: a dense copy of all experts
+// would be staged at 16 bits a weight and written and read again, 4.6 times the bytes of the compressed operand (721 MB
+// staged for eight experts of 11008 x 4096).  Per CTA and stage of 64 reduction rows (R), TMA brings 64 x 64 stored values
+// (8 KB) and their metadata (1 KB) into a ring of their own; eight warps expand them into the MN-major operand tile (two
+// strips of 64 columns, 64 rows of 128 bytes each, 128-byte swizzle): a group of four is two byte permutations of its pair
+// of values, whose selector comes from the group's nibble.  Lanes are assigned so that loads and stores meet every bank
+// once: eight lanes take the eight 16-byte units of a row of values, and the lanes of the second strip store their two
+// units in the other order.  dY's rows arrive by TMA beside it.
+//
+// experts_dv_kernel reduces over an expert's columns, which start and end anywhere.  Its stages of 128 columns start on a
+// 16-byte unit; in a tile's first and last stage a warp of each CTA zeroes the columns outside the expert (of both
+// operands: a zero times a neighbour's Inf would be NaN) before the MMA may read them, and the last stage issues only the
+// MMAs that its columns need.  An expert without columns has a gradient of zeros.
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "nm_experts.cuh"
+#include "nm_experts.h"
+#include "nm_host.h"
+#include "nm_internal.h"
+#include "nm_ptx.cuh"
+
+namespace nmk {
+
+namespace grpt {
+constexpr int kThreads = 512;  // warps 0 raw copies, 1 MMA, 2 copies of dY, 4-7 epilogue, 8-15 expansion
+constexpr int kRaw = 4, kStages = 5;
+constexpr uint32_t kVals = 8192, kMeta = 1024;
+constexpr uint32_t kA = 16384, kB = 16384;  // 64 reduction rows x 128 columns, in strips of 8 KB
+constexpr uint32_t kStrip = 8192;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxN = 256;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint32_t kOffB = kStages * kA, kOffVals = kOffB + kStages * kB, kOffMeta = kOffVals + kRaw * kVals;
+constexpr uint32_t kOffEpi = kOffMeta + kRaw * kMeta;
+constexpr uint32_t kOffBar = kOffEpi + 4 * kBoxBytes;
+constexpr uint32_t kOffFirst = kOffBar + (2 * kStages + 2 * kRaw + 5) * 8 + 8;
+constexpr uint32_t bytes(int E) { return kOffFirst + 4u * (uint32_t)(E + 1) + 1024u; }
+static_assert(kOffFirst + 4 * (kMaxExperts + 1) + 1024 <= 232448, "shared memory");
+}  // namespace grpt
+
+// Four weights, as two words, from their two stored values and positions (nib = p0 | p1 << 2, 8 times in s0 and s1).
+__device__ __forceinline__ void expand_group(uint32_t v, uint32_t s0, uint32_t s1, uint32_t& lo, uint32_t& hi) {
+  // A selector byte of the four halves: 0x44 picks zeros, 0x10 the first value, 0x32 the second.
+  const uint32_t sel = 0x44444444u ^ (0x54u << s0) ^ (0x76u << s1);
+  lo = __byte_perm(v, 0u, sel);
+  hi = __byte_perm(v, 0u, sel >> 16);
+}
+
+// One row's 16 weights: eight values and 16 bits of positions to two 16-byte units.
+__device__ __forceinline__ void expand_row(const uint4& v, uint32_t pos, uint4& a, uint4& b) {
+  const uint32_t p = pos << 3;  // group g: 8 p0 at bits 4g + 3, 8 p1 two bits above
+  expand_group(v.x, p & 24u, (p >> 2) & 24u, a.x, a.y);
+  expand_group(v.y, (p >> 4) & 24u, (p >> 6) & 24u, a.z, a.w);
+  expand_group(v.z, (p >> 8) & 24u, (p >> 10) & 24u, b.x, b.y);
+  expand_group(v.w, (p >> 12) & 24u, (p >> 14) & 24u, b.z, b.w);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
+    experts_t_kernel(const __grid_constant__ ExpertsParams p) {
+  using namespace grpt;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* empty = full + kStages;
+  uint64_t* raw_full = empty + kStages;
+  uint64_t* raw_empty = raw_full + kRaw;
+  uint64_t* acc_full = raw_empty + kRaw;  // [2]
+  uint64_t* acc_empty = acc_full + 2;     // [2]
+  uint64_t* spare = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(spare + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* first = reinterpret_cast<int32_t*>(smem + kOffFirst);
+
+  const uint32_t rank = cluster_ctarank();  // 0: leader (issues the MMAs)
+  const int pair_id = blockIdx.x >> 1;
+  const int npairs = gridDim.x >> 1;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1 + 16);  // dY's bytes, and the expanding warps of both CTAs
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kRaw; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], 8);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], 8);
+    }
+    mbar_init(spare, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 2 && lane == 0) {
+    tma_prefetch_desc(&p.tm_vals);
+    tma_prefetch_desc(&p.tm_x);
+    tma_prefetch_desc(&p.tm_meta);
+  }
+  cluster_sync();  // the allocation takes columns in both SMs: the peer has started
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  pdl_gate();  // no global memory touched before this point
+  if (warp == 0) list_tiles(p.offsets, p.E, p.S, kMaxN, p.tiles_m, first, lane);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
+  const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
+  bool ok = true;
+  TileWalk w;
+
+  if (warp == 0) {
+    // ------------------------------------------------- values and metadata
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, kMaxN); tile += npairs) {
+        const int32_t m0 = w.tm * 256 + 128 * (int)rank;
+        for (int kt = 0; kt < p.k_tiles; ++kt) {
+          ok = mbar_wait(&raw_empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&raw_full[s], kVals + kMeta);
+          tma_load_3d(smem + kOffVals + s * kVals, &p.tm_vals, &raw_full[s], m0 >> 1, kt * 64, w.e);
+          tma_load_3d(smem + kOffMeta + s * kMeta, &p.tm_meta, &raw_full[s], 0, m0 >> 7, w.e * p.meta_rblocks + kt * 4);
+          if (++s == kRaw) { s = 0; ph ^= 1u; }
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ dY
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, kMaxN); tile += npairs) {
+        const int32_t col0 = w.x0 + (w.n >> 1) * (int32_t)rank;
+        const int strips = w.n > 128 ? 2 : 1;
+        for (int kt = 0; kt < p.k_tiles; ++kt) {
+          ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
+          if (!ok) break;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)strips * kStrip);
+          for (int j = 0; j < strips; ++j)
+            tma_load_2d_pair(smem + kOffB + s * kB + j * kStrip, &p.tm_x, lead_full0 + 8u * s, col0 + 64 * j, kt * 64);
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA (leader)
+    if (rank == 0 && lane == 0) {
+      int s = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, kMaxN); tile += npairs) {
+        ok = mbar_wait(&acc_empty[acc], ((aph >> acc) & 1u) ^ 1u, abort_flag, p.status, kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + 256u * (uint32_t)acc;
+        const uint32_t idesc = idesc_bf16_major((uint32_t)w.n, 256, true, true);
+        for (int kt = 0; kt < p.k_tiles; ++kt) {
+          ok = mbar_wait_cluster(&full[s], ph, abort_flag, p.status, kWaitNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + s * kA);
+          const uint32_t b_addr = smem_u32(smem + kOffB + s * kB);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_pair(d_tmem, smem_desc(a_addr + kk * 2048, kStrip, 1024, SWZ_128B),
+                        smem_desc(b_addr + kk * 2048, kStrip, 1024, SWZ_128B), idesc, (kt > 0 || kk > 0) ? 1u : 0u);
+          tc_commit_pair(&empty[s], 0x3);
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+        if (!ok) break;
+        tc_commit_pair(&acc_full[acc], 0x3);
+        aph ^= 1u << acc;
+        acc ^= 1;
+      }
+      if (!ok) {
+        tc_commit_pair(spare, 0x1);
+        volatile int dummy = 0;
+        mbar_wait(spare, 0, &dummy, p.status, 100000000ull);
+      }
+    }
+  } else if (warp >= 8) {
+    // ----------------------------------------------------------- expansion
+    // Eight rows of a 16-row block and their partners eight below, every warp: a word of metadata a lane.
+    const int q = lane & 3, h = (lane >> 2) & 1;
+    const int rr = 4 * (warp & 1) + (lane >> 3), row = 16 * ((warp - 8) >> 1) + rr;
+    const uint32_t word_at = (uint32_t)((warp - 8) >> 1) * 256u + 4u * (uint32_t)(4 * (rr + 8 * h) + q);
+    const uint32_t val_at = (uint32_t)row * 128u + (uint32_t)(((2 * q + h) ^ rr) << 4);
+    const uint32_t u0 = (uint32_t)(4 * (q & 1) + 2 * h), swap = (uint32_t)(q >> 1);
+    const uint32_t out_at = (uint32_t)(q >> 1) * kStrip + (uint32_t)row * 128u;
+    const uint32_t first_at = out_at + (((u0 + swap) ^ (uint32_t)rr) << 4);
+    const uint32_t second_at = out_at + (((u0 + (swap ^ 1u)) ^ (uint32_t)rr) << 4);
+    int s = 0, r = 0;
+    uint32_t ph = 0, rph = 0;
+    for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, kMaxN); tile += npairs) {
+      for (int kt = 0; kt < p.k_tiles; ++kt) {
+        ok = mbar_wait_warp(&raw_full[r], rph, abort_flag, p.status, kWaitNs);
+        if (!ok) break;
+        const uint8_t* vals = smem + kOffVals + r * kVals + val_at;
+        const uint32_t word = *reinterpret_cast<const uint32_t*>(smem + kOffMeta + r * kMeta + word_at);
+        const uint4 v0 = *reinterpret_cast<const uint4*>(vals), v1 = *reinterpret_cast<const uint4*>(vals + 1024);
+        uint4 a0, b0, a1, b1;
+        expand_row(v0, word & 0xFFFFu, a0, b0);
+        expand_row(v1, word >> 16, a1, b1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&raw_empty[r]);
+        ok = mbar_wait_warp(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
+        if (!ok) break;
+        uint8_t* a = smem + s * kA;
+        *reinterpret_cast<uint4*>(a + first_at) = swap ? b0 : a0;
+        *reinterpret_cast<uint4*>(a + second_at) = swap ? a0 : b0;
+        *reinterpret_cast<uint4*>(a + first_at + 1024) = swap ? b1 : a1;
+        *reinterpret_cast<uint4*>(a + second_at + 1024) = swap ? a1 : b1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead_full0 + 8u * s);
+        if (++s == kStages) { s = 0; ph ^= 1u; }
+        if (++r == kRaw) { r = 0; rph ^= 1u; }
+      }
+    }
+  } else if (warp >= 4) {
+    // -------------------------------------------------------------- epilogue
+    const int quarter = warp & 3;
+    uint8_t* box = smem + kOffEpi + quarter * kBoxBytes;
+    uint32_t aph = 0;
+    int acc = 0;
+    for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, kMaxN); tile += npairs) {
+      ok = mbar_wait_warp(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t_addr = tmem_base + 256u * (uint32_t)acc + ((uint32_t)(quarter * 32) << 16);
+      store_tile(p, w, t_addr, box, w.tm * 256 + 128 * (int)rank + quarter * 32, lane, [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
+      });
+      aph ^= 1u << acc;
+      acc ^= 1;
+    }
+    if (lane == 0) bulk_wait_group<0>();  // every store of this warp has landed
+  }
+
+  // -------------------------------------------------------------- teardown
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) sleep_about_ns(200000ull);
+  cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+  cluster_sync();  // ... and so does the deallocation: neither CTA leaves before both are through it
+}
+
+// ------------------------------------------------------------ survivors' gradient
+namespace grpv {
+constexpr int kThreads = 256;  // warp 0 copies, 1 MMA, 2 columns outside the expert, 4-7 epilogue
+constexpr int kStages = 3;
+constexpr uint32_t kA = 32768, kB = 32768;  // 128 rows x 128 columns each, in halves of 64 columns
+constexpr uint32_t kHalf = 16384;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint32_t kOffBar = kStages * (kA + kB);
+constexpr uint32_t kSmemBytes = kOffBar + (3 * kStages + 5) * 8 + 8 + 1024;
+
+// The stages of one expert's reduction, from its first column rounded down.
+struct Reduction {
+  int e;
+  int32_t c0, c1, a0;
+  int stages;
+  __device__ __forceinline__ Reduction() : e(-1) {}
+  __device__ __forceinline__ void at(const ExpertsGradParams& p, int expert) {
+    if (expert == e) return;
+    const ExpertCols x = expert_cols(p.offsets, expert, p.S, 256);
+    e = expert;
+    c0 = x.c0;
+    c1 = x.c1;
+    a0 = x.a0;
+    stages = c1 > c0 ? (c1 - a0 + 127) / 128 : 0;
+  }
+  __device__ __forceinline__ int32_t columns(int kt) const { return min(c1 - a0 - 128 * kt, 128); }  // up to the last one
+  // Do the stage's MMAs meet columns of another expert (or behind the matrix)?
+  __device__ __forceinline__ bool ragged(int kt) const { return (kt == 0 && c0 > a0) || (columns(kt) & 15) != 0; }
+};
+}  // namespace grpv
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
+    experts_dv_kernel(const __grid_constant__ ExpertsGradParams p) {
+  using namespace grpv;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* empty = full + kStages;
+  uint64_t* landed = empty + kStages;  // a ragged stage's bytes, in each CTA
+  uint64_t* acc_full = landed + kStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;     // [2]
+  uint64_t* spare = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(spare + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const uint32_t rank = cluster_ctarank();  // 0: leader (issues the MMAs)
+  const int pair_id = blockIdx.x >> 1;
+  const int npairs = gridDim.x >> 1;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 2);  // one thread of each CTA
+      mbar_init(&empty[s], 1);
+      mbar_init(&landed[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], 8);
+    }
+    mbar_init(spare, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 2 && lane == 0) {
+    tma_prefetch_desc(&p.tm_a);
+    tma_prefetch_desc(&p.tm_b);
+  }
+  cluster_sync();  // the allocation takes columns in both SMs: the peer has started
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  pdl_gate();  // no global memory touched before this point
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
+  const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
+  const int per_expert = p.tiles_m * p.tiles_n, tiles = p.E * per_expert;
+  bool ok = true;
+  Reduction red;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- copies
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int tile = pair_id; tile < tiles && ok; tile += npairs) {
+        red.at(p, tile / per_expert);
+        const int in = tile % per_expert, tm = in / p.tiles_n, tn = in % p.tiles_n;
+        const int32_t m0 = tm * 256 + 128 * (int)rank, n0 = tn * 256 + 128 * (int)rank;
+        for (int kt = 0; kt < red.stages; ++kt) {
+          ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
+          if (!ok) break;
+          uint8_t* a = smem + s * (kA + kB);
+          const int halves = red.columns(kt) > 64 ? 2 : 1;
+          const uint32_t tx = (uint32_t)halves * 2u * kHalf;  // this CTA's bytes
+          const bool ragged = red.ragged(kt);
+          if (ragged)
+            mbar_arrive_expect_tx(&landed[s], tx);
+          else if (rank == 0)
+            mbar_arrive_expect_tx(&full[s], 2u * tx);
+          else
+            mbar_arrive_cluster(lead_full0 + 8u * s);
+          for (int i = 0; i < halves; ++i) {
+            const int32_t k0 = red.a0 + kt * 128 + 64 * i;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint8_t* to = a + i * kHalf + h * 8192;
+              if (ragged) {
+                tma_load_2d(to, &p.tm_a, &landed[s], k0, m0 + 64 * h);
+                tma_load_2d(to + kA, &p.tm_b, &landed[s], k0, n0 + 64 * h);
+              } else {
+                tma_load_2d_pair(to, &p.tm_a, lead_full0 + 8u * s, k0, m0 + 64 * h);
+                tma_load_2d_pair(to + kA, &p.tm_b, lead_full0 + 8u * s, k0, n0 + 64 * h);
+              }
+            }
+          }
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------- columns outside the expert
+    int s = 0;
+    uint32_t lph = 0;  // bit s: phase of landed[s]
+    for (int tile = pair_id; tile < tiles && ok; tile += npairs) {
+      red.at(p, tile / per_expert);
+      for (int kt = 0; kt < red.stages; ++kt) {
+        if (red.ragged(kt)) {
+          ok = mbar_wait_warp(&landed[s], (lph >> s) & 1u, abort_flag, p.status, kWaitNs);
+          if (!ok) break;
+          lph ^= 1u << s;
+          const int lo = kt == 0 ? red.c0 - red.a0 : 0;  // below 8
+          const int hi = red.columns(kt), end = (hi + 15) & ~15;
+          uint8_t* ab = smem + s * (kA + kB);
+#pragma unroll 1
+          for (int r = lane; r < 256; r += 32) {  // rows of A, then of B
+            uint8_t* row = ab + (r >> 7) * kA + (r & 127) * 128;
+            for (int c = 0; c < end; c = c == 0 ? max(8, hi & ~7) : c + 8) {  // the first unit and those past hi
+              if (c == 0 && lo == 0 && hi >= 8) continue;
+              uint4* unit = reinterpret_cast<uint4*>(row + (c >> 6) * kHalf + ((((c >> 3) & 7) ^ (r & 7)) << 4));
+              uint4 u = *unit;
+              uint32_t* wd = &u.x;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int k = c + 2 * i;
+                const uint32_t keep = (k >= lo && k < hi ? 0xFFFFu : 0u) | (k + 1 >= lo && k + 1 < hi ? 0xFFFF0000u : 0u);
+                wd[i] &= keep;
+              }
+              *unit = u;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead_full0 + 8u * s);
+        }
+        if (++s == kStages) s = 0;
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA (leader)
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t kIdesc = idesc_bf16_major(256, 256, false, false);
+      int s = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      for (int tile = pair_id; tile < tiles && ok; tile += npairs) {
+        red.at(p, tile / per_expert);
+        if (red.stages == 0) continue;
+        ok = mbar_wait(&acc_empty[acc], ((aph >> acc) & 1u) ^ 1u, abort_flag, p.status, kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + 256u * (uint32_t)acc;
+        for (int kt = 0; kt < red.stages; ++kt) {
+          ok = mbar_wait_cluster(&full[s], ph, abort_flag, p.status, kWaitNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + s * (kA + kB));
+          const uint32_t b_addr = a_addr + kA;
+          const int steps = (red.columns(kt) + 15) >> 4;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t at = (uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u;
+            if (kk < steps)
+              tc_mma_pair(d_tmem, smem_desc(a_addr + at, 16, 1024, SWZ_128B), smem_desc(b_addr + at, 16, 1024, SWZ_128B),
+                          kIdesc, (kt > 0 || kk > 0) ? 1u : 0u);
+          }
+          tc_commit_pair(&empty[s], 0x3);
+          if (++s == kStages) { s = 0; ph ^= 1u; }
+        }
+        if (!ok) break;
+        tc_commit_pair(&acc_full[acc], 0x3);
+        aph ^= 1u << acc;
+        acc ^= 1;
+      }
+      if (!ok) {
+        tc_commit_pair(spare, 0x1);
+        volatile int dummy = 0;
+        mbar_wait(spare, 0, &dummy, p.status, 100000000ull);
+      }
+    }
+  } else if (warp >= 4) {
+    // -------------------------------------------------------------- epilogue
+    const int quarter = warp & 3;
+    const int64_t vcols = p.K >> 1;
+    uint32_t aph = 0;
+    int acc = 0;
+    for (int tile = pair_id; tile < tiles && ok; tile += npairs) {
+      red.at(p, tile / per_expert);
+      const int in = tile % per_expert, tm = in / p.tiles_n, tn = in % p.tiles_n;
+      const int64_t row = (int64_t)tm * 256 + 128 * rank + quarter * 32 + lane;
+      const int64_t n0 = (int64_t)tn * 256;
+      // The positions of this row's survivors, on their way while the products are.
+      uint32_t word[2][8];
+      const uint32_t* mb = p.meta + red.e * p.meta_words + ((row >> 4) * p.meta_cblocks + (n0 >> 7)) * 64 + 4 * (row & 7);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const bool in_w = row < p.R && n0 + 32 * c < p.K;
+        word[0][c] = in_w ? __ldcg(mb + (c >> 2) * 64 + (c & 3)) : 0u;
+        word[1][c] = in_w ? __ldcg(mb + (c >> 2) * 64 + (c & 3) + 32) : 0u;
+      }
+      const bool some = red.stages > 0;
+      if (some) {
+        ok = mbar_wait_warp(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const uint32_t t_addr = tmem_base + 256u * (uint32_t)acc + ((uint32_t)(quarter * 32) << 16);
+      const int sh = 16 * (int)((row >> 3) & 1);
+      const int64_t out0 = ((int64_t)red.e * p.R + row) * vcols;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int64_t col0 = n0 + 32 * c;
+        if (col0 >= p.K) break;  // the same for all lanes
+        uint32_t v[32];
+        if (some) {
+          tmem_ld_32x32b_x32(t_addr + c * 32, v);
+          tc_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0u;
+        }
+        if (row >= p.R) continue;
+        const bool both = col0 + 32 <= p.K;  // or 16 of the columns
+        const int64_t at = out0 + (col0 >> 1);
+        if (p.out_f32) {
+          float o[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t nib = (word[i >> 2][c] >> (sh + 4 * (i & 3))) & 0xFu;
+            const uint32_t p0 = nib & 3u, p1 = nib >> 2;
+            const float a0 = __uint_as_float(v[4 * i]), a1 = __uint_as_float(v[4 * i + 1]);
+            const float a2 = __uint_as_float(v[4 * i + 2]), a3 = __uint_as_float(v[4 * i + 3]);
+            o[2 * i] = p0 == 0 ? a0 : (p0 == 1 ? a1 : a2);
+            o[2 * i + 1] = p1 == 3 ? a3 : (p1 == 2 ? a2 : a1);
+          }
+          float4* y = reinterpret_cast<float4*>(static_cast<float*>(p.dV) + at);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < 2 || both) y[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else {
+          // Rounded first: one byte permutation of a group's four values then picks both survivors (position q is the
+          // bytes 2q and 2q + 1).
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t nib = word[i >> 2][c] >> (sh + 4 * (i & 3));
+            const uint32_t pick = (nib & 3u) * 0x22u + (nib >> 2 & 3u) * 0x2200u + 0x1010u;
+            o[i] = __byte_perm(pack_bf16x2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
+                               pack_bf16x2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), pick);
+          }
+          uint4* y = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dV) + at);
+          y[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          if (both) y[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      }
+      if (some) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
+        aph ^= 1u << acc;
+        acc ^= 1;
+      }
+    }
+  }
+
+  // -------------------------------------------------------------- teardown
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) sleep_about_ns(200000ull);
+  cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+  cluster_sync();  // ... and so does the deallocation: neither CTA leaves before both are through it
+}
+
+}  // namespace nmk
+
+using namespace nmk;
+
+extern "C" nm_status nm_experts_spmm_t(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t E, int64_t R,
+                                       int64_t K, const uint16_t* dY, int64_t lddy, int64_t S, const int32_t* offsets,
+                                       void* dX, int64_t lddx, nm_out_dtype dtype, void* stream) {
+  set_last_error("");
+  nm_status st = check_experts(n, m, E, R, K, S, offsets);
+  if (st != NM_OK) return st;
+  if (!dtype_ok(dtype)) return fail(NM_ERR_INVALID_ARG, "bad output dtype");
+  if (R < 1) return fail(NM_ERR_INVALID_ARG, "R must be positive");
+  if (E == 0 || S == 0) return NM_OK;
+  if (!values || !meta) return fail(NM_ERR_INVALID_ARG, "values or meta is null");
+  st = check_matrix(dY, lddy, S, 2, "dY");
+  if (st == NM_OK) st = check_matrix(dX, lddx, S, dtype_bytes(dtype), "dX");
+  if (st != NM_OK) return st;
+  if (!al16(values) || !al16(meta)) return fail(NM_ERR_MISALIGNED, "values and meta must be 16-byte aligned");
+  st = require_device();
+  if (st != NM_OK) return st;
+  ExpertsParams p;
+  std::memset(&p, 0, sizeof p);
+  p.offsets = offsets;
+  p.Y = dX;
+  p.ldy = lddx;
+  p.M = (int32_t)K;
+  p.S = (int32_t)S;
+  p.E = (int32_t)E;
+  p.k_tiles = (int32_t)((R + 63) / 64);
+  p.tiles_m = (int32_t)((K + 255) / 256);
+  p.meta_rblocks = (int32_t)meta_row_blocks(R);
+  p.out_f32 = dtype == NM_OUT_F32;
+  p.status = status_word_ptr();
+  if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
+  st = make_tmap3(&p.tm_vals, values, (uint64_t)(K / 2), (uint64_t)R, (uint64_t)E, (uint64_t)K, (uint64_t)(R * K), 64, 64, 128,
+                  "values");
+  if (st == NM_OK) st = make_meta_tmap(&p.tm_meta, meta, E * meta_row_blocks(R), meta_col_blocks(K), 4);
+  if (st == NM_OK) st = make_tmap(&p.tm_x, dY, (uint64_t)S, (uint64_t)R, (uint64_t)lddy * 2, 64, 64, 128, "dY");
+  if (st == NM_OK) st = make_experts_store_map(p, dX, K, S, lddx);
+  if (st != NM_OK) return st;
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(experts_t_kernel, grpt::bytes(kMaxExperts));
+  if (e != cudaSuccess) return cuda_fail(e, "grouped input gradient");
+  const int pairs = experts_pairs(p, grpt::kMaxN);
+  e = launch_pdl(experts_t_kernel, dim3(2 * pairs), dim3(grpt::kThreads), grpt::bytes(p.E), (cudaStream_t)stream, p);
+  count_launch();
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? NM_OK : cuda_fail(e, "grouped input gradient launch");
+}
+
+extern "C" nm_status nm_experts_sddmm(const uint32_t* meta, int n, int m, int64_t E, int64_t R, int64_t K, const uint16_t* dY,
+                                      int64_t lddy, const uint16_t* X, int64_t ldx, int64_t S, const int32_t* offsets,
+                                      void* dV, nm_out_dtype dtype, void* stream) {
+  set_last_error("");
+  nm_status st = check_experts(n, m, E, R, K, S, offsets);
+  if (st != NM_OK) return st;
+  if (!dtype_ok(dtype)) return fail(NM_ERR_INVALID_ARG, "bad output dtype");
+  if (E == 0 || R == 0) return NM_OK;
+  if (!meta || !dV) return fail(NM_ERR_INVALID_ARG, "meta or dV is null");
+  if (!al16(dV)) return fail(NM_ERR_MISALIGNED, "dV must be 16-byte aligned");
+  st = check_words({meta}, "meta");
+  if (st == NM_OK && S > 0) st = check_matrix(dY, lddy, S, 2, "dY");
+  if (st == NM_OK && S > 0) st = check_matrix(X, ldx, S, 2, "X");
+  if (st != NM_OK) return st;
+  const int64_t tiles_m = (R + 255) / 256, tiles_n = (K + 255) / 256;
+  if (E * tiles_m * tiles_n >= kMaxDim - 1024) return fail(NM_ERR_UNSUPPORTED, "too many tiles");
+  st = require_device();
+  if (st != NM_OK) return st;
+  if (S == 0) {  // no columns: zeros (offsets may be null)
+    const cudaError_t e = cudaMemsetAsync(dV, 0, (size_t)(E * R * (K / 2) * dtype_bytes(dtype)), (cudaStream_t)stream);
+    return e == cudaSuccess ? NM_OK : cuda_fail(e, "zero gradient");
+  }
+  ExpertsGradParams p;
+  std::memset(&p, 0, sizeof p);
+  p.offsets = offsets;
+  p.meta = meta;
+  p.dV = dV;
+  p.R = R;
+  p.K = K;
+  p.S = (int32_t)S;
+  p.E = (int32_t)E;
+  p.tiles_m = (int32_t)tiles_m;
+  p.tiles_n = (int32_t)tiles_n;
+  p.meta_cblocks = (int32_t)meta_col_blocks(K);
+  p.meta_words = meta_words(R, K, 2, 4);
+  p.out_f32 = dtype == NM_OUT_F32;
+  p.status = status_word_ptr();
+  if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
+  st = make_tmap(&p.tm_a, dY, (uint64_t)S, (uint64_t)R, (uint64_t)lddy * 2, 64, 64, 128, "dY");
+  if (st == NM_OK) st = make_tmap(&p.tm_b, X, (uint64_t)S, (uint64_t)K, (uint64_t)ldx * 2, 64, 64, 128, "X");
+  if (st != NM_OK) return st;
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(experts_dv_kernel, grpv::kSmemBytes);
+  if (e != cudaSuccess) return cuda_fail(e, "grouped survivor gradient");
+  const int64_t tiles = E * tiles_m * tiles_n;
+  const int pairs_avail = sm_count_current() / 2;
+  const int pairs = tiles < pairs_avail ? (int)tiles : pairs_avail;
+  e = launch_pdl(experts_dv_kernel, dim3(2 * pairs), dim3(grpv::kThreads), (size_t)grpv::kSmemBytes, (cudaStream_t)stream, p);
+  count_launch();
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? NM_OK : cuda_fail(e, "grouped survivor gradient launch");
+}

@@ -27,6 +27,8 @@ nm_status make_tmap(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t 
 // 3-D map of {d0, d1, d2} bf16 with strides s1 and s2 bytes, boxes {b0, b1, 1}.
 nm_status make_tmap3(CUtensorMap* tm, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
                      uint32_t b0, uint32_t b1, int swizzle_bytes, const char* what);
+// 3-D map of the tiled 2:4 metadata (boxes of box_rblocks row blocks of one column block).
+nm_status make_meta_tmap(CUtensorMap* tm, const void* meta, int64_t rblocks, int64_t cblocks, uint32_t box_rblocks = 8);
 
 class Staged;
 
