@@ -611,6 +611,90 @@ NM_API nm_status nm_experts_sddmm(const uint32_t* meta, int n, int m, int64_t E,
                                   const int32_t* offsets, void* dV, nm_out_dtype dtype, void* stream);
 
 /*
+ * The router of such a layer.  Logits are E x T (experts x tokens, bf16 or fp32
+ * by dtype, row stride ld >= T, 16-byte rows), 1 <= k <= 16 (NM_ERR_UNSUPPORTED
+ * above), k <= E <= 1024, k * T < 2^31.
+ *
+ * nm_experts_route: every token's k experts of largest logits, in descending
+ *   order, ties to the lower expert, a NaN above every number.  A logit of -inf
+ *   is never chosen: a token with fewer than k others has expert -1, gate 0 and
+ *   slot -1 in the places left, and a token of -inf alone goes nowhere.
+ *     expert [out] k x T int32
+ *     gate   [out] k x T fp32: exp(l) over the sum of exp(l) of the chosen
+ *            (renorm != 0) or of all experts (renorm == 0)
+ *     offsets [out] E + 1 int32: the columns grouped by expert, as above
+ *     slot   [out] k x T int32: a token's column at its j-th expert (within an
+ *            expert the tokens ascend)
+ *     source [out] k T int32: j T + t for the column of token t at its j-th
+ *            expert; -1 from column offsets[E] on
+ *   One launch up to 32 tokens, else two, with E bytes staged for every 32
+ *   tokens.  Integers throughout, so the order does not vary.
+ * nm_experts_route_grad: dlogits (E x T, logits' type) of sum gate dgate, from
+ *   the logits and the expert and gate that nm_experts_route gave.  Nothing
+ *   flows through the choice.  Every element is written.
+ * Errors: NM_ERR_INVALID_ARG, NM_ERR_MISALIGNED, NM_ERR_UNSUPPORTED, NM_ERR_CUDA.
+ */
+NM_API nm_status nm_experts_route(const void* logits, int64_t ld, nm_out_dtype dtype, int64_t E, int64_t T, int k,
+                                  int renorm, int32_t* expert, float* gate, int32_t* slot, int32_t* source,
+                                  int32_t* offsets, void* stream);
+NM_API nm_status nm_experts_route_grad(const void* logits, int64_t ld, nm_out_dtype dtype, int64_t E, int64_t T, int k,
+                                       int renorm, const int32_t* expert, const float* gate, const float* dgate,
+                                       void* dlogits, int64_t lddl, void* stream);
+
+/*
+ * Tokens to their experts' columns and back; slot, source and gate as
+ * nm_experts_route gives them (k T < 2^31), bf16 rows of 16 bytes.
+ *
+ * nm_experts_gather: Xg[:, s] = X[:, source[s] mod T] (K x S), a column of zeros
+ *   where source[s] < 0.  One launch.
+ * nm_experts_combine: Y[:, t] = sum_j gate[j][t] Yg[:, slot[j][t]] (R x T, bf16
+ *   or fp32), j ascending in fp32, rounded once; a slot outside [0, S) adds
+ *   nothing; gate NULL for 1, which makes it the gather's gradient (dX from
+ *   dXg).  One launch.
+ * nm_experts_combine_grad: dYg[:, s] = gate[source[s]] dY[:, source[s] mod T]
+ *   (R x S bf16, zeros where source[s] is outside [0, k T)) and dgate[j][t] =
+ *   dY[:, t] . Yg[:, slot[j][t]] (k x T fp32; 0 where slot is outside [0, S)).
+ *   slot and source must name each other, as the router's do: dgate of a token
+ *   is read from the column that its slot names.  gate NULL for 1.  Two launches; 4 bytes a
+ *   column and group of rows (about two to an SM) staged.
+ * Results repeat bit for bit.
+ * Errors: as nm_experts_route.
+ */
+NM_API nm_status nm_experts_gather(const uint16_t* X, int64_t ldx, int64_t K, int64_t T, const int32_t* source,
+                                   int64_t S, uint16_t* Xg, int64_t ldg, void* stream);
+NM_API nm_status nm_experts_combine(const uint16_t* Yg, int64_t ldg, int64_t S, int64_t R, int64_t T, int k,
+                                    const int32_t* slot, const float* gate, void* Y, int64_t ldy, nm_out_dtype y_dtype,
+                                    void* stream);
+NM_API nm_status nm_experts_combine_grad(const uint16_t* dY, int64_t lddy, int64_t R, int64_t T, int k,
+                                         const uint16_t* Yg, int64_t ldg, int64_t S, const int32_t* slot,
+                                         const int32_t* source, const float* gate, uint16_t* dYg, int64_t lddg,
+                                         float* dgate, void* stream);
+
+/* ------------------------------------------------------------- clipping */
+/*
+ * nm_clip_grads -- the norm over many gradients and their scaling to it, between
+ * a backward pass and the optimiser:
+ *   norm = sqrt(sum over all elements of g^2),
+ *   out = g * (max_norm / norm) where norm > max_norm, else g.
+ * A norm that is Inf or NaN scales nothing (the caller sees it in *norm).
+ * The pages train pruned networks without giving this step.
+ *   grads, outs  [in] HOST arrays of `count` device pointers, each aligned to
+ *           its elements (16 bytes are read faster); outs[i] may be grads[i]
+ *           and must not overlap it otherwise; outs NULL: the norm alone
+ *   sizes, dtypes [in] HOST arrays: elements and nm_out_dtype of each
+ *   max_norm >= 0 (Inf: no scaling, a copy where outs differ)
+ *   norm    [out] one fp32 on the device
+ * The host arrays are read before the call returns.  Squares are added in 64
+ * bits (in fp32 over 32 elements where that is safe), so norms of any size up
+ * to the largest float come out; products are fp32, rounded once.  Two launches
+ * for every 640 gradients; 8 bytes staged for every CTA.  Results repeat bit
+ * for bit.
+ * Errors: NM_ERR_INVALID_ARG, NM_ERR_MISALIGNED, NM_ERR_UNSUPPORTED, NM_ERR_CUDA.
+ */
+NM_API nm_status nm_clip_grads(const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes,
+                               int64_t count, float max_norm, float* norm, void* stream);
+
+/*
  * nm_spmm_algo --nm_spmm / nm_spmm_permuted (idx may be NULL) with the kernel
  * design chosen explicitly, to compare the sparse tensor-core path with the
  * dense expansion on the same pattern.  NM_ERR_UNSUPPORTED when the pattern

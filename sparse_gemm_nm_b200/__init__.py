@@ -4,15 +4,17 @@ Python binding of the C ABI in ``include/nm.h`` (library ``libnm_b200.so``).
 The functions named like the C entry points (``nm_prune_compress``,
 ``nm_decompress``, ``nm_spmm``, ``nm_spmm_permuted``, ``nm_hybrid_spmm``,
 ``nm_spmm_algo``, ``nm_prune_spmm``, ``nm_spmm_t``, ``nm_sddmm``,
-``nm_layer_norm``, ``nm_spmm_lora``, ``nm_spmm_xent``, their gradients and the
-calls of the other formats) only marshal arguments: tensors become device pointers, the
+``nm_layer_norm``, ``nm_spmm_lora``, ``nm_spmm_xent``, ``nm_experts_*``, their
+gradients, ``nm_clip_grads`` and the calls of the other formats) only marshal arguments: tensors become device pointers, the
 stream defaults to torch's current stream, and a non-zero status raises
 :class:`NmError`.  Every step of the computation runs in the library's CUDA
 kernels; there is no fallback of any kind.  The convenience wrappers
 (``prune_compress``, ``decompress``, ``spmm``, ``hybrid_spmm``, ``prune_spmm``, ``spmm_t``,
 ``sddmm``; around a projection ``layer_norm``, ``layer_norm_grad``, ``spmm_lora``,
-``spmm_lora_t``, ``lora_grad``, ``spmm_xent``, ``spmm_xent_grad``) also allocate
-the outputs with torch.
+``spmm_lora_t``, ``lora_grad``, ``spmm_xent``, ``spmm_xent_grad``; for layers of
+pruned experts ``experts_route``, ``experts_gather``, ``experts_spmm``,
+``experts_combine``, their gradients, and ``clip_grads``) also allocate the
+outputs with torch.
 
 bf16 data is accepted as ``torch.bfloat16`` tensors (or int16/uint16 views of
 the same bits).  Matrices are row-major: W is R x K, X is K x T, Y is R x T.
@@ -74,6 +76,12 @@ SIGNATURES = {
     "nm_experts_spmm": ([_P, _P, _I, _I, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I, _P], _I),
     "nm_experts_spmm_t": ([_P, _P, _I, _I, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I, _P], _I),
     "nm_experts_sddmm": ([_P, _I, _I, _I64, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I, _P], _I),
+    "nm_experts_route": ([_P, _I64, _I, _I64, _I64, _I, _I, _P, _P, _P, _P, _P, _P], _I),
+    "nm_experts_route_grad": ([_P, _I64, _I, _I64, _I64, _I, _I, _P, _P, _P, _P, _I64, _P], _I),
+    "nm_experts_gather": ([_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P], _I),
+    "nm_experts_combine": ([_P, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _I64, _I, _P], _I),
+    "nm_experts_combine_grad": ([_P, _I64, _I64, _I64, _I, _P, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P], _I),
+    "nm_clip_grads": ([_P, _P, _P, _P, _I64, _F, _P, _P], _I),
     "nm_spmm_algo": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I, _I, _P], _I),
     "nm_spmm_permuted_noalloc": ([_P, _P, _I, _I, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I, _P], _I),
     "nm_release_staging": ([], _I),
@@ -301,6 +309,40 @@ def nm_experts_spmm_t(values, meta, n, m, E, R, K, dY, lddy, S, offsets, dX, ldd
 def nm_experts_sddmm(meta, n, m, E, R, K, dY, lddy, X, ldx, S, offsets, dV, dtype=NM_OUT_BF16, stream=None) -> None:
     _check(lib().nm_experts_sddmm(_ptr(meta), n, m, E, R, K, _ptr(dY), lddy, _ptr(X), ldx, S, _ptr(offsets), _ptr(dV),
                                   dtype, _stream(stream)), "nm_experts_sddmm")
+
+
+def nm_experts_route(logits, ld, dtype, E, T, k, renorm, expert, gate, slot, source, offsets, stream=None) -> None:
+    _check(lib().nm_experts_route(_ptr(logits), ld, dtype, E, T, k, int(renorm), _ptr(expert), _ptr(gate), _ptr(slot),
+                                  _ptr(source), _ptr(offsets), _stream(stream)), "nm_experts_route")
+
+
+def nm_experts_route_grad(logits, ld, dtype, E, T, k, renorm, expert, gate, dgate, dlogits, lddl, stream=None) -> None:
+    _check(lib().nm_experts_route_grad(_ptr(logits), ld, dtype, E, T, k, int(renorm), _ptr(expert), _ptr(gate),
+                                       _ptr(dgate), _ptr(dlogits), lddl, _stream(stream)), "nm_experts_route_grad")
+
+
+def nm_experts_gather(X, ldx, K, T, source, S, Xg, ldg, stream=None) -> None:
+    _check(lib().nm_experts_gather(_ptr(X), ldx, K, T, _ptr(source), S, _ptr(Xg), ldg, _stream(stream)),
+           "nm_experts_gather")
+
+
+def nm_experts_combine(Yg, ldg, S, R, T, k, slot, gate, Y, ldy, y_dtype=NM_OUT_BF16, stream=None) -> None:
+    _check(lib().nm_experts_combine(_ptr(Yg), ldg, S, R, T, k, _ptr(slot), _ptr(gate), _ptr(Y), ldy, y_dtype,
+                                    _stream(stream)), "nm_experts_combine")
+
+
+def nm_experts_combine_grad(dY, lddy, R, T, k, Yg, ldg, S, slot, source, gate, dYg, lddg, dgate, stream=None) -> None:
+    _check(lib().nm_experts_combine_grad(_ptr(dY), lddy, R, T, k, _ptr(Yg), ldg, S, _ptr(slot), _ptr(source), _ptr(gate),
+                                         _ptr(dYg), lddg, _ptr(dgate), _stream(stream)), "nm_experts_combine_grad")
+
+
+def nm_clip_grads(grads, outs, sizes, dtypes, max_norm, norm, stream=None) -> None:
+    """grads, outs (or None): sequences of device pointers or tensors; sizes, dtypes: sequences of numbers."""
+    n = len(grads)
+    g = (ctypes.c_void_p * n)(*[_ptr(t) for t in grads])
+    o = None if outs is None else (ctypes.c_void_p * n)(*[_ptr(t) for t in outs])
+    _check(lib().nm_clip_grads(g, o, (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*dtypes), n, max_norm, _ptr(norm),
+                               _stream(stream)), "nm_clip_grads")
 
 
 def nm_spmm_algo(values, meta, n, m, R, K, idx, X, ldx, T, Y, ldy, y_dtype=NM_OUT_BF16, algo=NM_ALGO_AUTO,
@@ -679,6 +721,131 @@ def experts_sddmm(meta, n: int, m: int, R: int, K: int, dY, X, offsets, out_dtyp
         dV = X.new_empty((E, R, cols), dtype=out_dtype)
         nm_experts_sddmm(meta, n, m, E, R, K, dY, lddy, X, ldx, S, offsets, dV, yt, s)
     return dV
+
+
+def experts_route(logits, k: int, renorm: bool = True, stream=None):
+    """(expert, gate, slot, source, offsets): every token's k experts and the tokens as columns grouped by expert.
+
+    logits are E x T (bf16 or float32).  expert (int32), gate (float32) and slot (int32, the token's column at its j-th
+    expert) are k x T, source (k T int32) holds j T + t for every column, offsets (E + 1 int32) every expert's first
+    column.  gate is the softmax over the chosen experts, or over all with renorm=False.  Logits of -inf are never
+    chosen: expert -1, gate 0, slot -1, and source -1 behind the last column.
+    """
+    import torch
+    _same_device(logits)
+    ld = _rows(logits, "logits", torch.bfloat16, torch.float32)
+    E, T = logits.shape
+    if not 1 <= k <= E:
+        raise ValueError(f"k must be 1..{E}, got {k}")
+    with _On(logits, stream) as s:
+        n = (k * T + 3) // 4 * 4  # each part on 16 bytes
+        words = logits.new_empty(3 * n + E + 1, dtype=torch.int32)
+        expert, slot = words[:k * T].view(k, T), words[n:n + k * T].view(k, T)
+        source, offsets = words[2 * n:2 * n + k * T], words[3 * n:]
+        gate = logits.new_empty((k, T), dtype=torch.float32)
+        nm_experts_route(logits, ld, _out_type(logits.dtype), E, T, k, renorm, expert, gate, slot, source, offsets, s)
+    return expert, gate, slot, source, offsets
+
+
+def _pairs(k: int, T: int, *named):
+    """Checks k x T arrays: (array, name, type), None where the array is optional."""
+    for v, name, dtype in named:
+        if v is not None and (tuple(v.shape) != (k, T) or v.dtype != dtype or not v.is_contiguous()):
+            raise ValueError(f"{name} must be {k} x {T} contiguous values of {dtype}, got {tuple(v.shape)} {v.dtype}")
+
+
+def experts_route_grad(logits, expert, gate, dgate, renorm: bool = True, stream=None):
+    """dlogits (like logits) of sum(gate * dgate), from the expert and gate that experts_route returned."""
+    import torch
+    _same_device(logits, expert, gate, dgate)
+    ld = _rows(logits, "logits", torch.bfloat16, torch.float32)
+    E, T = logits.shape
+    k = expert.shape[0]
+    _pairs(k, T, (expert, "expert", torch.int32), (gate, "gate", torch.float32), (dgate, "dgate", torch.float32))
+    lt = _out_type(logits.dtype)
+    with _On(logits, stream) as s:
+        dlogits, lddl = _out_rows(logits, E, T, logits.dtype, lt)
+        nm_experts_route_grad(logits, ld, lt, E, T, k, renorm, expert, gate, dgate, dlogits, lddl, s)
+    return dlogits
+
+
+def experts_gather(X, source, stream=None):
+    """Xg[:, s] = X[:, source[s] mod T] (K x S bf16, rows padded to 16 bytes); zeros where source[s] < 0."""
+    import torch
+    _same_device(X, source)
+    ldx = _rows(X, "X", torch.bfloat16)
+    K, T = X.shape
+    S = source.numel()
+    _vector(source, "source", S, torch.int32)
+    with _On(X, stream) as s:
+        Xg, ldg = _out_rows(X, K, S, torch.bfloat16, NM_OUT_BF16)
+        nm_experts_gather(X, ldx, K, T, source, S, Xg, ldg, s)
+    return Xg
+
+
+def experts_combine(Yg, slot, gate=None, out_dtype=None, stream=None):
+    """Y[:, t] = sum_j gate[j][t] Yg[:, slot[j][t]] (R x T); a slot outside the columns adds nothing.
+
+    Without gates it is the input gradient of experts_gather.
+    """
+    import torch
+    _same_device(Yg, slot, gate)
+    ldg = _rows(Yg, "Yg", torch.bfloat16)
+    R, S = Yg.shape
+    if slot.dim() != 2:
+        raise ValueError(f"slot must be k x T, got {tuple(slot.shape)}")
+    k, T = slot.shape
+    _pairs(k, T, (slot, "slot", torch.int32), (gate, "gate", torch.float32))
+    out_dtype = out_dtype or torch.bfloat16
+    yt = _out_type(out_dtype)
+    with _On(Yg, stream) as s:
+        Y, ldy = _out_rows(Yg, R, T, out_dtype, yt)
+        nm_experts_combine(Yg, ldg, S, R, T, k, slot, gate, Y, ldy, yt, s)
+    return Y
+
+
+def experts_combine_grad(dY, Yg, slot, source, gate=None, stream=None):
+    """(dYg like Yg, dgate k x T float32): the gradients of experts_combine."""
+    import torch
+    _same_device(dY, Yg, slot, source, gate)
+    lddy, ldg = _rows(dY, "dY", torch.bfloat16), _rows(Yg, "Yg", torch.bfloat16)
+    (R, T), S = dY.shape, Yg.shape[1]
+    if Yg.shape[0] != R:
+        raise ValueError(f"dY has {R} rows, Yg {Yg.shape[0]}")
+    k = slot.shape[0]
+    _pairs(k, T, (slot, "slot", torch.int32), (gate, "gate", torch.float32))
+    _vector(source, "source", S, torch.int32)
+    with _On(dY, stream) as s:
+        dYg, lddg = _out_rows(Yg, R, S, torch.bfloat16, NM_OUT_BF16)
+        dgate = dY.new_empty((k, T), dtype=torch.float32)
+        nm_experts_combine_grad(dY, lddy, R, T, k, Yg, ldg, S, slot, source, gate, dYg, lddg, dgate, s)
+    return dYg, dgate
+
+
+def clip_grads(grads, max_norm: float, out=None, stream=None):
+    """The norm over all gradients (a float32 tensor of no dimensions, on the device); scales them to max_norm if above.
+
+    grads are contiguous tensors (bf16 or float32) of one CUDA device, scaled in place, or into the tensors of `out`.
+    A norm that is Inf or NaN scales nothing.
+    """
+    import torch
+    grads = list(grads)
+    if not grads:
+        raise ValueError("no gradients")
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(grads)} gradients, {len(outs)} outputs")
+    _same_device(grads[0], *grads, *outs)
+    types = []
+    for g, o in zip(grads, outs):
+        types.append(_out_type(g.dtype))
+        if o.dtype != g.dtype or o.shape != g.shape or not g.is_contiguous() or not o.is_contiguous():
+            raise ValueError(f"gradients and outputs must be contiguous and alike, got {tuple(g.shape)} {g.dtype} and "
+                             f"{tuple(o.shape)} {o.dtype}")
+    with _On(grads[0], stream) as s:
+        norm = grads[0].new_empty((), dtype=torch.float32)
+        nm_clip_grads(grads, outs, [g.numel() for g in grads], types, max_norm, norm, s)
+    return norm
 
 
 def prune_compress(W, n: int, m: int, stream=None):

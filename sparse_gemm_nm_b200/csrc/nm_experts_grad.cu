@@ -13,10 +13,10 @@
 // once: eight lanes take the eight 16-byte units of a row of values, and the lanes of the second strip store their two
 // units in the other order.  dY's rows arrive by TMA beside it.
 //
-// experts_dv_kernel reduces over an expert's columns, which start and end anywhere.  Its stages of 128 columns start on a
-// 16-byte unit; in a tile's first and last stage a warp of each CTA zeroes the columns outside the expert (of both
-// operands: a zero times a neighbour's Inf would be NaN) before the MMA may read them, and the last stage issues only the
-// MMAs that its columns need.  An expert without columns has a gradient of zeros.
+// experts_dv_kernel reduces over an expert's columns, which start and end anywhere.  Its stages of 128 columns start as the
+// tiles of nm_experts.cuh do; in a tile's first and last stage a warp of each CTA zeroes the columns outside the expert (of both
+// operands: a zero times a neighbour's Inf would be NaN) before the MMA may read them, and these stages issue only the
+// MMAs (16 columns each) that hold columns of the expert.  An expert without columns has a gradient of zeros.
 #include <atomic>
 #include <cstdint>
 #include <cstring>
@@ -89,12 +89,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1 + 16);  // dY's bytes, and the expanding warps of both CTAs
+      mbar_init(&full[s], 1 + 8);  // dY's bytes, and the expanding warps of both CTAs
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kRaw; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], 8);
+      mbar_init(&raw_empty[s], 4);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
@@ -175,7 +175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
         const uint32_t d_tmem = tmem_base + 256u * (uint32_t)acc;
         const uint32_t idesc = idesc_bf16_major((uint32_t)w.n, 256, true, true);
         for (int kt = 0; kt < p.k_tiles; ++kt) {
-          ok = mbar_wait_cluster(&full[s], ph, abort_flag, p.status, kWaitNs);
+          ok = mbar_wait(&full[s], ph, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           tc_fence_after();
           const uint32_t a_addr = smem_u32(smem + s * kA);
@@ -200,39 +200,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     }
   } else if (warp >= 8) {
     // ----------------------------------------------------------- expansion
-    // Eight rows of a 16-row block and their partners eight below, every warp: a word of metadata a lane.
-    const int q = lane & 3, h = (lane >> 2) & 1;
-    const int rr = 4 * (warp & 1) + (lane >> 3), row = 16 * ((warp - 8) >> 1) + rr;
-    const uint32_t word_at = (uint32_t)((warp - 8) >> 1) * 256u + 4u * (uint32_t)(4 * (rr + 8 * h) + q);
-    const uint32_t val_at = (uint32_t)row * 128u + (uint32_t)(((2 * q + h) ^ rr) << 4);
+    // Four warps to a stage, two stages at a time (one warp's loads, permutations, stores and fence take longer than a
+    // stage's MMAs).  A warp takes 16 rows: two words of metadata a lane, each of a row and its partner eight below.
+    const int q = lane & 3, h = (lane >> 2) & 1, rb = warp & 3, mine = (warp - 8) >> 2;
+    const uint32_t word_at = (uint32_t)rb * 256u + 4u * (uint32_t)(4 * ((lane >> 3) + 8 * h) + q);
     const uint32_t u0 = (uint32_t)(4 * (q & 1) + 2 * h), swap = (uint32_t)(q >> 1);
-    const uint32_t out_at = (uint32_t)(q >> 1) * kStrip + (uint32_t)row * 128u;
-    const uint32_t first_at = out_at + (((u0 + swap) ^ (uint32_t)rr) << 4);
-    const uint32_t second_at = out_at + (((u0 + (swap ^ 1u)) ^ (uint32_t)rr) << 4);
-    int s = 0, r = 0;
+    const uint32_t out_at = (uint32_t)(q >> 1) * kStrip + (uint32_t)rb * 2048u;
+    int s = 0, r = 0, turn = 0;
     uint32_t ph = 0, rph = 0;
     for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, kMaxN); tile += npairs) {
       for (int kt = 0; kt < p.k_tiles; ++kt) {
-        ok = mbar_wait_warp(&raw_full[r], rph, abort_flag, p.status, kWaitNs);
-        if (!ok) break;
-        const uint8_t* vals = smem + kOffVals + r * kVals + val_at;
-        const uint32_t word = *reinterpret_cast<const uint32_t*>(smem + kOffMeta + r * kMeta + word_at);
-        const uint4 v0 = *reinterpret_cast<const uint4*>(vals), v1 = *reinterpret_cast<const uint4*>(vals + 1024);
-        uint4 a0, b0, a1, b1;
-        expand_row(v0, word & 0xFFFFu, a0, b0);
-        expand_row(v1, word >> 16, a1, b1);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&raw_empty[r]);
-        ok = mbar_wait_warp(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
-        if (!ok) break;
-        uint8_t* a = smem + s * kA;
-        *reinterpret_cast<uint4*>(a + first_at) = swap ? b0 : a0;
-        *reinterpret_cast<uint4*>(a + second_at) = swap ? a0 : b0;
-        *reinterpret_cast<uint4*>(a + first_at + 1024) = swap ? b1 : a1;
-        *reinterpret_cast<uint4*>(a + second_at + 1024) = swap ? a1 : b1;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_full0 + 8u * s);
+        if (turn == mine) {
+          ok = mbar_wait_warp(&raw_full[r], rph, abort_flag, p.status, kWaitNs);
+          if (!ok) break;
+          uint4 out[2][2][2];  // word, row, unit
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int rr = (lane >> 3) + 4 * i;
+            const uint8_t* vals = smem + kOffVals + r * kVals + rb * 2048 + rr * 128 + (((2 * q + h) ^ rr) << 4);
+            const uint32_t word = *reinterpret_cast<const uint32_t*>(smem + kOffMeta + r * kMeta + word_at + 64 * i);
+            const uint4 v0 = *reinterpret_cast<const uint4*>(vals), v1 = *reinterpret_cast<const uint4*>(vals + 1024);
+            expand_row(v0, word & 0xFFFFu, out[i][0][0], out[i][0][1]);
+            expand_row(v1, word >> 16, out[i][1][0], out[i][1][1]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&raw_empty[r]);
+          ok = mbar_wait_warp(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t rr = (uint32_t)(lane >> 3) + 4u * i;
+            uint8_t* a = smem + s * kA + out_at + rr * 128u;
+            const uint32_t at0 = ((u0 + swap) ^ rr) << 4, at1 = ((u0 + (swap ^ 1u)) ^ rr) << 4;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              *reinterpret_cast<uint4*>(a + at0 + 1024 * j) = swap ? out[i][j][1] : out[i][j][0];
+              *reinterpret_cast<uint4*>(a + at1 + 1024 * j) = swap ? out[i][j][0] : out[i][j][1];
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_peer(lead_full0 + 8u * s);
+        }
+        turn ^= 1;
         if (++s == kStages) { s = 0; ph ^= 1u; }
         if (++r == kRaw) { r = 0; rph ^= 1u; }
       }
@@ -273,14 +283,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
 
 // ------------------------------------------------------------ survivors' gradient
 namespace grpv {
-constexpr int kThreads = 256;  // warp 0 copies, 1 MMA, 2 columns outside the expert, 4-7 epilogue
+constexpr int kThreads = 256;  // warp 0 copies, 1 MMA, 2, 3 columns outside the expert, 4-7 epilogue
 constexpr int kStages = 3;
 constexpr uint32_t kA = 32768, kB = 32768;  // 128 rows x 128 columns each, in halves of 64 columns
 constexpr uint32_t kHalf = 16384;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kOffBar = kStages * (kA + kB);
-constexpr uint32_t kSmemBytes = kOffBar + (3 * kStages + 5) * 8 + 8 + 1024;
+constexpr uint32_t kSmemBytes = kOffBar + (4 * kStages + 5) * 8 + 8 + 1024;
 
 // The stages of one expert's reduction, from its first column rounded down.
 struct Reduction {
@@ -297,9 +307,11 @@ struct Reduction {
     a0 = x.a0;
     stages = c1 > c0 ? (c1 - a0 + 127) / 128 : 0;
   }
-  __device__ __forceinline__ int32_t columns(int kt) const { return min(c1 - a0 - 128 * kt, 128); }  // up to the last one
+  // The expert's columns of stage kt, from the stage's first; MMAs take 16 of them each.
+  __device__ __forceinline__ int32_t from(int kt) const { return kt == 0 ? c0 - a0 : 0; }  // below 64
+  __device__ __forceinline__ int32_t to(int kt) const { return min(c1 - a0 - 128 * kt, 128); }
   // Do the stage's MMAs meet columns of another expert (or behind the matrix)?
-  __device__ __forceinline__ bool ragged(int kt) const { return (kt == 0 && c0 > a0) || (columns(kt) & 15) != 0; }
+  __device__ __forceinline__ bool ragged(int kt) const { return ((from(kt) | to(kt)) & 15) != 0; }
 };
 }  // namespace grpv
 
@@ -310,8 +322,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* empty = full + kStages;
-  uint64_t* landed = empty + kStages;  // a ragged stage's bytes, in each CTA
-  uint64_t* acc_full = landed + kStages;  // [2]
+  uint64_t* landed = empty + kStages;   // a ragged stage's bytes, in each CTA
+  uint64_t* masked = landed + kStages;  // ... its columns, in both: stands in for full
+  uint64_t* acc_full = masked + kStages;  // [2]
   uint64_t* acc_empty = acc_full + 2;     // [2]
   uint64_t* spare = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(spare + 1);
@@ -325,9 +338,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 2);  // one thread of each CTA
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&landed[s], 1);
+      mbar_init(&masked[s], 4);  // two warps of each CTA
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
@@ -355,6 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
+  const uint32_t lead_masked0 = map_to_cta(smem_u32(&masked[0]), 0);
   const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
   const int per_expert = p.tiles_m * p.tiles_n, tiles = p.E * per_expert;
   bool ok = true;
@@ -373,15 +388,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
           ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           uint8_t* a = smem + s * (kA + kB);
-          const int halves = red.columns(kt) > 64 ? 2 : 1;
+          const int halves = red.to(kt) > 64 ? 2 : 1;
           const uint32_t tx = (uint32_t)halves * 2u * kHalf;  // this CTA's bytes
           const bool ragged = red.ragged(kt);
           if (ragged)
             mbar_arrive_expect_tx(&landed[s], tx);
           else if (rank == 0)
             mbar_arrive_expect_tx(&full[s], 2u * tx);
-          else
-            mbar_arrive_cluster(lead_full0 + 8u * s);
           for (int i = 0; i < halves; ++i) {
             const int32_t k0 = red.a0 + kt * 128 + 64 * i;
 #pragma unroll
@@ -400,8 +413,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
         }
       }
     }
-  } else if (warp == 2) {
-    // ------------------------------------------- columns outside the expert
+  } else if (warp == 2 || warp == 3) {
+    // ------------------------------------------- columns outside the expert (of A, of B)
     int s = 0;
     uint32_t lph = 0;  // bit s: phase of landed[s]
     for (int tile = pair_id; tile < tiles && ok; tile += npairs) {
@@ -411,29 +424,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
           ok = mbar_wait_warp(&landed[s], (lph >> s) & 1u, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           lph ^= 1u << s;
-          const int lo = kt == 0 ? red.c0 - red.a0 : 0;  // below 8
-          const int hi = red.columns(kt), end = (hi + 15) & ~15;
-          uint8_t* ab = smem + s * (kA + kB);
-#pragma unroll 1
-          for (int r = lane; r < 256; r += 32) {  // rows of A, then of B
-            uint8_t* row = ab + (r >> 7) * kA + (r & 127) * 128;
-            for (int c = 0; c < end; c = c == 0 ? max(8, hi & ~7) : c + 8) {  // the first unit and those past hi
-              if (c == 0 && lo == 0 && hi >= 8) continue;
-              uint4* unit = reinterpret_cast<uint4*>(row + (c >> 6) * kHalf + ((((c >> 3) & 7) ^ (r & 7)) << 4));
-              uint4 u = *unit;
-              uint32_t* wd = &u.x;
+          const int lo = red.from(kt), hi = red.to(kt);
+          uint8_t* operand = smem + s * (kA + kB) + (warp - 2) * kA;
+          // The two 16-byte units of the MMA step where the columns start, and of the one where they end.
+          const int unit = (lane >> 4 ? (hi - 1) >> 4 : lo >> 4) * 2;
+          const bool touch = (lane >> 4) == 0 ? (lo & 15) != 0 || (lo >> 4) == ((hi - 1) >> 4)
+                                              : (hi & 15) != 0 && (lo >> 4) != ((hi - 1) >> 4);
+          if (touch) {
+            uint32_t keep[2][4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int k = c + 2 * i;
-                const uint32_t keep = (k >= lo && k < hi ? 0xFFFFu : 0u) | (k + 1 >= lo && k + 1 < hi ? 0xFFFF0000u : 0u);
-                wd[i] &= keep;
+            for (int i = 0; i < 8; ++i) {
+              const int k = 8 * unit + 2 * i;
+              keep[i >> 2][i & 3] = (k >= lo && k < hi ? 0xFFFFu : 0u) | (k + 1 >= lo && k + 1 < hi ? 0xFFFF0000u : 0u);
+            }
+#pragma unroll 4
+            for (int r = lane & 15; r < 128; r += 16) {
+              uint8_t* row = operand + (unit >> 3) * kHalf + r * 128;
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                uint4* at = reinterpret_cast<uint4*>(row + ((((unit & 7) + j) ^ (r & 7)) << 4));
+                uint4 u = *at;
+                u.x &= keep[j][0];
+                u.y &= keep[j][1];
+                u.z &= keep[j][2];
+                u.w &= keep[j][3];
+                *at = u;
               }
-              *unit = u;
             }
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead_full0 + 8u * s);
+          if (lane == 0) mbar_arrive_peer(lead_masked0 + 8u * s);
         }
         if (++s == kStages) s = 0;
       }
@@ -443,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
     if (rank == 0 && lane == 0) {
       constexpr uint32_t kIdesc = idesc_bf16_major(256, 256, false, false);
       int s = 0, acc = 0;
-      uint32_t ph = 0, aph = 0;
+      uint32_t fph = 0, mph = 0, aph = 0;  // bit s: phase of full[s], of masked[s]
       for (int tile = pair_id; tile < tiles && ok; tile += npairs) {
         red.at(p, tile / per_expert);
         if (red.stages == 0) continue;
@@ -452,21 +473,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + 256u * (uint32_t)acc;
         for (int kt = 0; kt < red.stages; ++kt) {
-          ok = mbar_wait_cluster(&full[s], ph, abort_flag, p.status, kWaitNs);
+          const bool ragged = red.ragged(kt);
+          ok = mbar_wait(ragged ? &masked[s] : &full[s], ((ragged ? mph : fph) >> s) & 1u, abort_flag, p.status, kWaitNs);
           if (!ok) break;
+          (ragged ? mph : fph) ^= 1u << s;
           tc_fence_after();
           const uint32_t a_addr = smem_u32(smem + s * (kA + kB));
           const uint32_t b_addr = a_addr + kA;
-          const int steps = (red.columns(kt) + 15) >> 4;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
+          const int step0 = red.from(kt) >> 4, steps = (red.to(kt) + 15) >> 4;
+          auto step = [&](int kk) {
             const uint32_t at = (uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u;
-            if (kk < steps)
-              tc_mma_pair(d_tmem, smem_desc(a_addr + at, 16, 1024, SWZ_128B), smem_desc(b_addr + at, 16, 1024, SWZ_128B),
-                          kIdesc, (kt > 0 || kk > 0) ? 1u : 0u);
+            tc_mma_pair(d_tmem, smem_desc(a_addr + at, 16, 1024, SWZ_128B), smem_desc(b_addr + at, 16, 1024, SWZ_128B),
+                        kIdesc, (kt > 0 || kk > step0) ? 1u : 0u);
+          };
+          if (steps - step0 == 8) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) step(kk);
+          } else {
+#pragma unroll 1
+            for (int kk = step0; kk < steps; ++kk) step(kk);
           }
           tc_commit_pair(&empty[s], 0x3);
-          if (++s == kStages) { s = 0; ph ^= 1u; }
+          if (++s == kStages) s = 0;
         }
         if (!ok) break;
         tc_commit_pair(&acc_full[acc], 0x3);

@@ -116,23 +116,6 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort, status, limit_ns));
 }
 
-// The same for a barrier on which threads of the peer CTA arrive as well, after writing what is read behind it.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status,
-                                                  uint64_t limit_ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  if (__builtin_expect(ok != 0, 1)) return true;
-  if (!mbar_wait_slow(bar, parity, abort, status, limit_ns)) return false;
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  return true;
-}
-
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
@@ -211,6 +194,13 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t saddr, uint32_t rank) {
 // Arrive on an mbarrier given by its cluster shared-memory address.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// The same without the release at cluster scope, which holds the thread until all its writes are seen there (a full fence
+// a stage: three times the time of the products in nm_experts_grad.cu).  For arrivals that follow no writes but
+// those to its own CTA's shared memory that a proxy fence has handed to the tensor core.
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // TMA tile load by either CTA of a pair; the transaction bytes complete on the
