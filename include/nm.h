@@ -654,9 +654,10 @@ NM_API nm_status nm_experts_route_grad(const void* logits, int64_t ld, nm_out_dt
  * nm_experts_combine_grad: dYg[:, s] = gate[source[s]] dY[:, source[s] mod T]
  *   (R x S bf16, zeros where source[s] is outside [0, k T)) and dgate[j][t] =
  *   dY[:, t] . Yg[:, slot[j][t]] (k x T fp32; 0 where slot is outside [0, S)).
- *   slot and source must name each other, as the router's do: dgate of a token
- *   is read from the column that its slot names.  gate NULL for 1.  Two launches; 4 bytes a
- *   column and group of rows (about two to an SM) staged.
+ *   slot and source must name each other, as the router's do (a pair whose slot
+ *   is a column that another pair's source names gets no gradient written).
+ *   gate NULL for 1.  Two launches; 4 bytes staged for every column and CTA (one
+ *   or two to an SM).
  * Results repeat bit for bit.
  * Errors: as nm_experts_route.
  */

@@ -39,6 +39,8 @@ struct Params {
   int out_f32;
   int vec;                 // index (and gate) may be read 16 bytes at a time
   int groups;              // row groups of a CTA
+  int depth;               // long rows: groups of rows in the ring
+  uint32_t* status;
   // combine_grad
   const uint16_t* yg;
   int64_t ldyg;
@@ -330,26 +332,455 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_con
   }
 }
 
-// dgate[j][t] = the partial sums of column slot[j][t], in order; 0 without a column.
-__global__ void __launch_bounds__(256) dgate_kernel(const float* part, int32_t parts, int64_t pitch, const int32_t* slot,
-                                                    int64_t n, int32_t S, float* dgate) {
+// ------------------------------------------------------------ long rows
+// The same by persistent CTAs that keep every column's index (and gate) in shared memory, 16 and 32 bits each, and take
+// group after group of kRows rows: read again for every group, the indices are as many bytes as the rows themselves.
+// Rows arrive by bulk copies in a ring of groups, as they lie in memory, so that loads never stop for the threads (with rows
+// brought through registers between two barriers, the loads of a CTA waited for its picks and the other way round: combine
+// of 8192 tokens at two experts, 4096 rows, 65 to 82 us).  A column is one 2-byte access a row, of random banks: about half
+// the time that HBM takes for the same row.  The word behind a row's columns is zero and stands for no column.
+namespace lng {
+constexpr int kThreads = 1024;
+constexpr int64_t kMaxSmem = 226 * 1024;
+constexpr int kMaxDepth = 8;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kBarBytes = 2 * kMaxDepth * 8 + 16;
+
+__host__ __device__ inline int32_t row_bytes(int32_t cols) { return ((cols + 7) & ~7) * 2 + 16; }
+
+// The ring of a CTA's groups of rows: group i has the rows (blockIdx.x + i gridDim.x) ROWS ..
+template <int ROWS>
+struct Ring {
+  uint64_t *full, *empty;
+  volatile int* abort;
+  uint8_t* slots;
+  int32_t pitch, issued;
+  uint32_t slot, phase;  // of the group being read
+  bool ok;
+
+  // smem: kBarBytes, then depth x ROWS rows.  Every thread; followed by a barrier of the CTA.
+  __device__ __forceinline__ void init(const Params& p, uint8_t* smem) {
+    full = reinterpret_cast<uint64_t*>(smem);
+    empty = full + kMaxDepth;
+    abort = reinterpret_cast<volatile int*>(empty + kMaxDepth);
+    slots = smem + kBarBytes;
+    pitch = row_bytes(p.cols_in);
+    issued = 0;
+    slot = 0;
+    phase = 0;
+    ok = true;
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < p.depth; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&empty[i], kThreads / 32);
+      }
+      *abort = 0;
+      fence_barrier_init();
+      fence_proxy_async_smem();
+    }
+    for (int i = threadIdx.x; i < p.depth * ROWS; i += kThreads)
+      *reinterpret_cast<uint4*>(slots + (int64_t)(i + 1) * pitch - 16) = make_uint4(0, 0, 0, 0);
+  }
+  // Thread 0: the next group's copies, once its slot has been read.
+  __device__ __forceinline__ void issue(const Params& p) {
+    const int64_t row0 = ((int64_t)blockIdx.x + (int64_t)issued * gridDim.x) * ROWS;
+    if (row0 >= p.rows || !ok) return;
+    const int at = issued % p.depth;
+    const uint32_t turn = (uint32_t)(issued / p.depth);
+    ok = mbar_wait(&empty[at], (turn & 1u) ^ 1u, abort, p.status, kWaitNs);
+    if (!ok) return;
+    uint8_t* to = slots + (int64_t)at * ROWS * pitch;
+    const uint32_t whole = (uint32_t)((p.cols_in + 7) >> 3) * 16u, part = (uint32_t)(p.cols_in >> 3) * 16u;
+    uint32_t bytes = 0;
+    for (int r = 0; r < ROWS && row0 + r < p.rows; ++r) {
+      const bool last = row0 + r == p.rows - 1;  // memory may end with its last column
+      bytes += last ? part : whole;
+      if (last)
+        for (int c = p.cols_in & ~7; c < p.cols_in; ++c)
+          reinterpret_cast<uint16_t*>(to + r * pitch)[c] = p.in[(row0 + r) * p.ldin + c];
+    }
+    mbar_arrive_expect_tx(&full[at], bytes);
+    for (int r = 0; r < ROWS && row0 + r < p.rows; ++r) {
+      const uint32_t n = row0 + r == p.rows - 1 ? part : whole;
+      if (n) bulk_load(to + r * pitch, p.in + (row0 + r) * p.ldin, n, &full[at]);
+    }
+    ++issued;
+  }
+  // The rows of the group to be read, for a warp.
+  __device__ __forceinline__ const uint8_t* wait(const Params& p) {
+    ok = mbar_wait_warp(&full[slot], phase, abort, p.status, kWaitNs);
+    return slots + (int64_t)slot * ROWS * pitch;
+  }
+  __device__ __forceinline__ void done(const Params& p, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[slot]);
+    if (++slot == (uint32_t)p.depth) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  __device__ __forceinline__ void leave() {
+    __syncthreads();
+    if (*abort && threadIdx.x == 0) sleep_about_ns(200000ull);  // copies in flight
+  }
+};
+
+// Eight 16-bit indices from shared memory.
+__device__ __forceinline__ void indices(const uint16_t* at, int32_t (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(at);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = (int32_t)(w[i] & 0xFFFFu);
+    v[2 * i + 1] = (int32_t)(w[i] >> 16);
+  }
+}
+__device__ __forceinline__ void values(const float* at, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(at)[0], b = reinterpret_cast<const float4*>(at)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+constexpr int kCombineRows = 2, kGradRows = 2;
+constexpr int kGradUnits = 2;  // units of eight columns a thread holds the dot products of
+
+// The gather has room for two tiles of RB rows as words, and one access a column then serves RB rows: the next group's rows
+// are on their way to registers while this one's columns are picked, and go to the other tile (8192 tokens at two experts,
+// 4096 rows: 42 us, from the ring 50).
+template <int RB>
+struct Next {
+  static constexpr int kUnits = 4 / RB;  // units of eight columns a thread brings
+  uint4 v[kUnits][RB];
+
+  __device__ __forceinline__ void fetch(const Params& p, int64_t row0) {
+    const int32_t units = (p.cols_in + 7) >> 3;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int32_t u = (int32_t)threadIdx.x + i * kThreads;
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        v[i][r] = make_uint4(0, 0, 0, 0);
+        if (u >= units || row0 + r >= p.rows) continue;
+        const uint16_t* at = p.in + (row0 + r) * p.ldin + 8 * u;
+        if (8 * u + 8 <= p.cols_in) {
+          v[i][r] = __ldcg(reinterpret_cast<const uint4*>(at));
+        } else {  // the row's last columns one by one
+          uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (8 * u + c < p.cols_in) w[c >> 1] |= (uint32_t)__ldcg(at + c) << (16 * (c & 1));
+          v[i][r] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  }
+  // Into the tile, the RB elements of a column side by side.  Lanes store their 16-byte pieces in different orders, so that
+  // eight of them meet every bank once.
+  __device__ __forceinline__ void put(const Params& p, typename Word<RB>::type* tile) const {
+    const int32_t units = (p.cols_in + 7) >> 3;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int32_t u = (int32_t)threadIdx.x + i * kThreads;
+      if (u >= units) continue;
+      uint4* to = reinterpret_cast<uint4*>(tile + 8 * u);
+      if constexpr (RB == 1) {
+        to[0] = v[i][0];
+      } else if constexpr (RB == 2) {
+        const uint4 a = v[i][0], b = v[i][1];
+        const uint4 lo = make_uint4(__byte_perm(a.x, b.x, 0x5410), __byte_perm(a.x, b.x, 0x7632),
+                                    __byte_perm(a.y, b.y, 0x5410), __byte_perm(a.y, b.y, 0x7632));
+        const uint4 hi = make_uint4(__byte_perm(a.z, b.z, 0x5410), __byte_perm(a.z, b.z, 0x7632),
+                                    __byte_perm(a.w, b.w, 0x5410), __byte_perm(a.w, b.w, 0x7632));
+        const int second = (u >> 2) & 1;
+        to[second] = second ? hi : lo;
+        to[second ^ 1] = second ? lo : hi;
+      } else {
+        const uint4 a = v[i][0], b = v[i][1], c = v[i][2], d = v[i][3];
+        uint4 q[4];
+        q[0] = make_uint4(__byte_perm(a.x, b.x, 0x5410), __byte_perm(c.x, d.x, 0x5410), __byte_perm(a.x, b.x, 0x7632),
+                          __byte_perm(c.x, d.x, 0x7632));
+        q[1] = make_uint4(__byte_perm(a.y, b.y, 0x5410), __byte_perm(c.y, d.y, 0x5410), __byte_perm(a.y, b.y, 0x7632),
+                          __byte_perm(c.y, d.y, 0x7632));
+        q[2] = make_uint4(__byte_perm(a.z, b.z, 0x5410), __byte_perm(c.z, d.z, 0x5410), __byte_perm(a.z, b.z, 0x7632),
+                          __byte_perm(c.z, d.z, 0x7632));
+        q[3] = make_uint4(__byte_perm(a.w, b.w, 0x5410), __byte_perm(c.w, d.w, 0x5410), __byte_perm(a.w, b.w, 0x7632),
+                          __byte_perm(c.w, d.w, 0x7632));
+        const int turn = (u >> 1) & 3;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = j ^ turn;
+          to[k] = k & 2 ? (k & 1 ? q[3] : q[2]) : (k & 1 ? q[1] : q[0]);
+        }
+      }
+    }
+  }
+};
+
+template <int RB>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ Params p) {
+  using W = typename Word<RB>::type;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int32_t width = (p.cols_in + 7) & ~7, units = (p.cols_out + 7) >> 3;
+  uint16_t* index = reinterpret_cast<uint16_t*>(smem);
+  W* const tiles = reinterpret_cast<W*>(smem + (int64_t)units * 16);
   pdl_gate();
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  const int32_t s = __ldcg(slot + i);
+  Next<RB> next;
+  int64_t row = (int64_t)blockIdx.x * RB;
+  next.fetch(p, row);
+  for (int32_t s = threadIdx.x; s < units * 8; s += kThreads) {
+    const int32_t src = s < p.cols_out ? __ldcg(p.index + s) : -1;
+    index[s] = src < 0 ? (uint16_t)0xFFFFu : (uint16_t)token_of(src, p.T, p.inv_T);
+  }
+  for (int second = 0; row < p.rows; row += (int64_t)gridDim.x * RB, second ^= 1) {
+    W* tile = tiles + second * width;
+    next.put(p, tile);
+    __syncthreads();  // and all are through with the other tile
+    next.fetch(p, row + (int64_t)gridDim.x * RB);
+    for (int32_t u = threadIdx.x; u < units; u += kThreads) {
+      int32_t t[8];
+      indices(index + 8 * u, t);
+      uint32_t v[8][(RB + 1) / 2];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) pick<RB, false>(p, tile, row, t[c], v[c]);
+#pragma unroll
+      for (int r = 0; r < RB; ++r) {
+        if (row + r >= p.rows) break;
+        uint32_t w[4];
+        row_of<RB>(v, r, w);
+        store8(static_cast<uint16_t*>(p.out) + (row + r) * p.ldout + 8 * u, p.cols_out - 8 * u, w);
+      }
+    }
+  }
+}
+// Rows of its word (0: it does not fit).
+inline int gather_rows(int64_t cols, int64_t rows, int64_t beside) {
+  const int64_t units = (cols + 7) / 8;
+  for (int rb = 4; rb >= 1; rb >>= 1)
+    if (cols < 0xFFFF && units <= (int64_t)kThreads * (4 / rb) && 2 * units * 16 * rb + beside <= kMaxSmem &&
+        rows >= 3 * (int64_t)rb * sm_count_current())
+      return rb;
+  return 0;
+}
+template <int RB>
+static cudaError_t launch_gather(const Params& p, unsigned grid, size_t smem, cudaStream_t s) {
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(gather_kernel<RB>, (uint32_t)kMaxSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(gather_kernel<RB>, dim3(grid), dim3(kThreads), smem, s, p);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+__global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int32_t units = (p.cols_out + 7) >> 3, per = units * 8, none = (p.cols_in + 7) & ~7;
+  const int lane = threadIdx.x & 31;
+  float* gates = reinterpret_cast<float*>(smem);
+  uint16_t* index = reinterpret_cast<uint16_t*>(gates + (p.gate ? (int64_t)p.k * per : 0));
+  Ring<kCombineRows> ring;
+  ring.init(p, reinterpret_cast<uint8_t*>(index + (int64_t)p.k * per));
+  __syncthreads();
+  pdl_gate();
+  if (threadIdx.x == 0)
+    for (int i = 0; i < p.depth; ++i) ring.issue(p);
+  for (int j = 0; j < p.k; ++j)
+    for (int32_t t = threadIdx.x; t < per; t += kThreads) {
+      const int32_t s = t < p.T ? __ldcg(p.index + (int64_t)j * p.T + t) : -1;
+      const bool has = (uint32_t)s < (uint32_t)p.cols_in;
+      index[j * per + t] = has ? (uint16_t)s : (uint16_t)none;
+      if (p.gate) gates[j * per + t] = has ? __ldcg(p.gate + (int64_t)j * p.T + t) : 0.f;
+    }
+  __syncthreads();
+  for (int64_t row = (int64_t)blockIdx.x * kCombineRows; row < p.rows; row += (int64_t)gridDim.x * kCombineRows) {
+    const uint8_t* rows = ring.wait(p);
+    if (!ring.ok) break;
+    for (int32_t u = threadIdx.x; u < units; u += kThreads) {
+      float acc[kCombineRows][8];
+#pragma unroll
+      for (int r = 0; r < kCombineRows; ++r)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[r][c] = 0.f;
+      for (int j = 0; j < p.k; ++j) {
+        int32_t s[8];
+        float gate[8];
+        indices(index + j * per + 8 * u, s);
+        if (p.gate) {
+          values(gates + j * per + 8 * u, gate);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) gate[c] = 1.f;
+        }
+#pragma unroll
+        for (int r = 0; r < kCombineRows; ++r) {
+          const uint16_t* from = reinterpret_cast<const uint16_t*>(rows + r * ring.pitch);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) acc[r][c] = fmaf(gate[c], bf(from[s[c]]), acc[r][c]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kCombineRows; ++r) {
+        if (row + r >= p.rows) break;
+        if (p.out_f32) {
+          store8(static_cast<float*>(p.out) + (row + r) * p.ldout + 8 * u, p.cols_out - 8 * u, acc[r]);
+        } else {
+          uint32_t w[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) w[c] = pack_bf16x2(acc[r][2 * c], acc[r][2 * c + 1]);
+          store8(static_cast<uint16_t*>(p.out) + (row + r) * p.ldout + 8 * u, p.cols_out - 8 * u, w);
+        }
+      }
+    }
+    ring.done(p, lane);
+    if (threadIdx.x == 0) ring.issue(p);
+  }
+  ring.leave();
+}
+
+// Eight columns of Yg from column s on, zeros behind the last.
+__device__ __forceinline__ uint4 columns8(const Params& p, int64_t row, int32_t s) {
+  if (row >= p.rows) return make_uint4(0, 0, 0, 0);
+  const uint16_t* at = p.yg + row * p.ldyg + s;
+  if (s + 8 <= p.cols_out) return __ldcg(reinterpret_cast<const uint4*>(at));
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    if (s + c < p.cols_out) w[c >> 1] |= (uint32_t)__ldcg(at + c) << (16 * (c & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// gridDim.y ranges of kThreads * kGradUnits units of the columns at most; the dot products stay with the threads.
+__global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int32_t all = (p.cols_out + 7) >> 3, none = (p.cols_in + 7) & ~7;
+  const int32_t per = (all + (int32_t)gridDim.y - 1) / (int32_t)gridDim.y;
+  const int32_t u0 = (int32_t)blockIdx.y * per, units = min(per, all - u0);
+  const int lane = threadIdx.x & 31;
+  float* gates = reinterpret_cast<float*>(smem);
+  uint16_t* index = reinterpret_cast<uint16_t*>(gates + per * 8);
+  Ring<kGradRows> ring;
+  ring.init(p, reinterpret_cast<uint8_t*>(index + per * 8));
+  __syncthreads();
+  pdl_gate();
+  if (threadIdx.x == 0)
+    for (int i = 0; i < p.depth; ++i) ring.issue(p);
+  uint4 y[kGradUnits][kGradRows];  // the next group's columns of Yg
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < kGradUnits; ++i)
+#pragma unroll
+      for (int r = 0; r < kGradRows; ++r) {
+        const int32_t u = (int32_t)threadIdx.x + i * kThreads;
+        if (u < units) y[i][r] = columns8(p, row + r, 8 * (u0 + u));
+      }
+  };
+  int64_t row = (int64_t)blockIdx.x * kGradRows;
+  fetch(row);
+  for (int32_t i = threadIdx.x; i < units * 8; i += kThreads) {
+    const int32_t s = 8 * u0 + i, src = s < p.cols_out ? __ldcg(p.index + s) : -1;
+    const bool has = src >= 0 && src < p.k * p.T;
+    index[i] = has ? (uint16_t)token_of(src, p.T, p.inv_T) : (uint16_t)none;
+    gates[i] = !has ? 0.f : p.gate ? __ldcg(p.gate + src) : 1.f;
+  }
+  __syncthreads();
+  float dot[kGradUnits][8];
+#pragma unroll
+  for (int i = 0; i < kGradUnits; ++i)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) dot[i][c] = 0.f;
+  for (; row < p.rows; row += (int64_t)gridDim.x * kGradRows) {
+    const uint8_t* rows = ring.wait(p);
+    if (!ring.ok) break;
+#pragma unroll
+    for (int i = 0; i < kGradUnits; ++i) {
+      const int32_t u = (int32_t)threadIdx.x + i * kThreads;
+      if (u >= units) break;
+      const int32_t s = 8 * (u0 + u);
+      const uint4 packed = *reinterpret_cast<const uint4*>(index + 8 * u);
+      uint32_t w[kGradRows][4];
+#pragma unroll
+      for (int c = 0; c < 8; c += 2) {
+        const uint32_t pair = c < 2 ? packed.x : c < 4 ? packed.y : c < 6 ? packed.z : packed.w;
+        const int32_t t0 = (int32_t)(pair & 0xFFFFu), t1 = (int32_t)(pair >> 16);
+        const float2 gate = *reinterpret_cast<const float2*>(gates + 8 * u + c);
+#pragma unroll
+        for (int r = 0; r < kGradRows; ++r) {
+          const uint16_t* from = reinterpret_cast<const uint16_t*>(rows + r * ring.pitch);
+          const uint32_t yw = c < 2 ? y[i][r].x : c < 4 ? y[i][r].y : c < 6 ? y[i][r].z : y[i][r].w;
+          const float d0 = bf(from[t0]), d1 = bf(from[t1]);
+          // a column of no token may hold anything, and so may the rows behind the last
+          if (t0 != none && row + r < p.rows) dot[i][c] = fmaf(d0, bf_lo(yw), dot[i][c]);
+          if (t1 != none && row + r < p.rows) dot[i][c + 1] = fmaf(d1, bf_hi(yw), dot[i][c + 1]);
+          w[r][c >> 1] = pack_bf16x2(gate.x * d0, gate.y * d1);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kGradRows; ++r) {
+        if (row + r < p.rows)
+          store8(static_cast<uint16_t*>(p.out) + (row + r) * p.ldout + s, p.cols_out - s, w[r]);
+        y[i][r] = columns8(p, row + (int64_t)gridDim.x * kGradRows + r, s);  // while the other units are at work
+      }
+    }
+    ring.done(p, lane);
+    if (threadIdx.x == 0) ring.issue(p);
+  }
+#pragma unroll
+  for (int i = 0; i < kGradUnits; ++i) {
+    const int32_t u = (int32_t)threadIdx.x + i * kThreads;
+    if (u >= units) break;
+    float4* to = reinterpret_cast<float4*>(p.part + (int64_t)blockIdx.x * (all * 8) + 8 * (u0 + u));
+    to[0] = make_float4(dot[i][0], dot[i][1], dot[i][2], dot[i][3]);
+    to[1] = make_float4(dot[i][4], dot[i][5], dot[i][6], dot[i][7]);
+  }
+  ring.leave();
+}
+
+// Groups of `group` rows in the ring for rows of `cols` elements, `beside` bytes of indices and gates with them: 0 where the
+// form does not fit (16-bit indices, two groups in shared memory) or would have too few groups to be worth its start.
+inline int depth_of(int64_t cols, int64_t rows, int64_t beside, int group) {
+  if (cols > 65000 || rows < 3 * (int64_t)group * sm_count_current()) return 0;
+  const int64_t depth = (kMaxSmem - beside - kBarBytes) / ((int64_t)row_bytes((int32_t)cols) * group);
+  return depth < 2 ? 0 : depth < kMaxDepth ? (int)depth : kMaxDepth;
+}
+inline size_t smem_of(const Params& p, int64_t beside, int group) {
+  return (size_t)(beside + kBarBytes + (int64_t)p.depth * group * row_bytes(p.cols_in));
+}
+inline unsigned grid_of(int64_t rows, int group) {
+  const int64_t groups = (rows + group - 1) / group, sms = sm_count_current();
+  return (unsigned)(groups < sms ? groups : sms);
+}
+}  // namespace lng
+
+// dgate[source[s]] = the partial sums of column s, in order; 0 for a pair without a column.  32 columns a CTA, whose warps
+// take the partial sums in eight ranges.
+__global__ void __launch_bounds__(256) dgate_kernel(const float* part, int32_t parts, int64_t pitch, const int32_t* source,
+                                                    const int32_t* slot, int64_t n, int32_t S, float* dgate) {
+  __shared__ float sums[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t s = (int64_t)blockIdx.x * 32 + lane;
+  const int32_t b0 = parts * warp / 8, b1 = parts * (warp + 1) / 8;
+  pdl_gate();
   float sum = 0.f;
-  if ((uint32_t)s < (uint32_t)S) {
-    int32_t b = 0;
-    for (; b + 8 <= parts; b += 8) {
+  if (s < S) {
+    int32_t b = b0;
+    for (; b + 8 <= b1; b += 8) {
       float f[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) f[q] = __ldcg(part + (b + q) * pitch + s);
 #pragma unroll
       for (int q = 0; q < 8; ++q) sum += f[q];
     }
-    for (; b < parts; ++b) sum += __ldcg(part + b * pitch + s);
+    for (; b < b1; ++b) sum += __ldcg(part + b * pitch + s);
   }
-  dgate[i] = sum;
+  sums[warp][lane] = sum;
+  __syncthreads();
+  if (warp) return;
+  if (s < S) {
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += sums[w][lane];
+    const int32_t src = __ldcg(source + s);
+    if (src >= 0 && src < n) dgate[src] = sum;
+  }
+  if (s < n && (uint32_t)__ldcg(slot + s) >= (uint32_t)S) dgate[s] = 0.f;
 }
 
 static uint32_t inverse(int64_t T) {
@@ -377,10 +808,11 @@ static cudaError_t dispatch(int rb, A&&... a) {
   }
 }
 template <typename Kernel>
-static cudaError_t start(Kernel kernel, SmemLimit& limit, dim3 grid, size_t smem, const Params& p, cudaStream_t s) {
-  cudaError_t e = limit.raise(kernel, (uint32_t)(208 * 1024));
+static cudaError_t start(Kernel kernel, SmemLimit& limit, dim3 grid, size_t smem, const Params& p, cudaStream_t s,
+                         int threads = kThreads) {
+  cudaError_t e = limit.raise(kernel, (uint32_t)lng::kMaxSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kernel, grid, dim3(kThreads), smem, s, p);
+  e = launch_pdl(kernel, grid, dim3((unsigned)threads), smem, s, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -450,6 +882,16 @@ extern "C" nm_status nm_experts_gather(const uint16_t* X, int64_t ldx, int64_t K
   p.rows = (int32_t)K, p.T = (int32_t)T, p.k = 1, p.inv_T = mv::inverse(T);
   p.index = source;
   p.vec = al16(source);
+  const int64_t beside = (S + 7) / 8 * 16;
+  const int lrb = mv::lng::gather_rows(T, K, beside);
+  if (lrb) {
+    const size_t smem = (size_t)(2 * ((T + 7) / 8 * 16 * lrb) + beside);
+    const unsigned grid = mv::lng::grid_of(K, lrb);
+    const cudaError_t e = lrb == 4   ? mv::lng::launch_gather<4>(p, grid, smem, (cudaStream_t)stream)
+                          : lrb == 2 ? mv::lng::launch_gather<2>(p, grid, smem, (cudaStream_t)stream)
+                                     : mv::lng::launch_gather<1>(p, grid, smem, (cudaStream_t)stream);
+    return e == cudaSuccess ? NM_OK : cuda_fail(e, "gather launch");
+  }
   const int rb = mv::rows_of_word(T, K, 0), step = rb ? rb : 1;
   p.groups = mv::groups_of(rb, K, T, S);
   const int64_t ctas = (K + (int64_t)p.groups * step - 1) / ((int64_t)p.groups * step);
@@ -479,6 +921,17 @@ extern "C" nm_status nm_experts_combine(const uint16_t* Yg, int64_t ldg, int64_t
   p.index = slot, p.gate = gate;
   p.out_f32 = y_dtype == NM_OUT_F32;
   p.vec = al16(slot) && al16(gate) && (T % 4 == 0 || k == 1);
+  const int64_t beside = (T + 7) / 8 * 8 * (gate ? 6 : 2) * k;
+  p.depth = mv::lng::depth_of(S, R, beside, mv::lng::kCombineRows);
+  if (p.depth) {
+    p.status = status_word_ptr();
+    if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
+    static SmemLimit limit;
+    const cudaError_t e = mv::start(mv::lng::combine_kernel, limit, dim3(mv::lng::grid_of(R, mv::lng::kCombineRows)),
+                                    mv::lng::smem_of(p, beside, mv::lng::kCombineRows), p, (cudaStream_t)stream,
+                                    mv::lng::kThreads);
+    return e == cudaSuccess ? NM_OK : cuda_fail(e, "combine launch");
+  }
   const int rb = mv::rows_of_word(S, R, 0), step = rb ? rb : 1;
   p.groups = mv::groups_of(rb, R, S, T);
   const int64_t ctas = (R + (int64_t)p.groups * step - 1) / ((int64_t)p.groups * step);
@@ -517,26 +970,46 @@ extern "C" nm_status nm_experts_combine_grad(const uint16_t* dY, int64_t lddy, i
   p.index = source, p.gate = gate;
   p.vec = al16(source);
   p.yg = Yg, p.ldyg = ldg;
-  // Columns in ranges whose sums take at most 64 KB.
-  const int64_t units = (S + 7) / 8, ranges = (units + 2047) / 2048, per = (units + ranges - 1) / ranges;
-  const int rb = mv::rows_of_word(T, R, 32 * per), step = rb ? rb : 1;
-  const int64_t row_groups = (R + step - 1) / step;
-  // Two CTAs to an SM, each with as many row groups as that leaves; more CTAs only write more partial sums.
-  int64_t ctas = 2 * (int64_t)sm_count_current() / ranges;
-  if (ctas < 1) ctas = 1;
-  if (ctas > row_groups) ctas = row_groups;
-  p.groups = (int)((row_groups + ctas - 1) / ctas);
-  ctas = (row_groups + p.groups - 1) / p.groups;
+  const int64_t units = (S + 7) / 8;
+  // Long rows: ranges of the columns that a CTA's threads hold.
+  const int64_t most = (int64_t)mv::lng::kThreads * mv::lng::kGradUnits;
+  int64_t ranges = (units + most - 1) / most, per = (units + ranges - 1) / ranges;
   Staged part(s);
-  cudaError_t e = part.get((size_t)ctas * units * 32);
-  if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gates' sums");
-  p.part = part.as<float>();
-  e = mv::dispatch<mv::CombineGrad>(rb, p, dim3((unsigned)ctas, (unsigned)ranges),
-                                    (size_t)(32 * per + (T + 1) / 2 * 4 * rb), s);
+  cudaError_t e;
+  int64_t ctas;
+  p.depth = mv::lng::depth_of(T, R, 48 * per, mv::lng::kGradRows);
+  if (p.depth) {
+    p.status = status_word_ptr();
+    if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
+    ctas = (int64_t)mv::lng::grid_of(R, mv::lng::kGradRows) / ranges;
+    if (ctas < 1) ctas = 1;
+    e = part.get((size_t)ctas * units * 32);
+    if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gates' sums");
+    p.part = part.as<float>();
+    static SmemLimit limit;
+    e = mv::start(mv::lng::combine_grad_kernel, limit, dim3((unsigned)ctas, (unsigned)ranges),
+                  mv::lng::smem_of(p, 48 * per, mv::lng::kGradRows), p, s, mv::lng::kThreads);
+  } else {
+    ranges = (units + 2047) / 2048;  // whose sums take at most 64 KB
+    per = (units + ranges - 1) / ranges;
+    const int rb = mv::rows_of_word(T, R, 32 * per), step = rb ? rb : 1;
+    const int64_t row_groups = (R + step - 1) / step;
+    // Two CTAs to an SM, each with as many row groups as that leaves; more CTAs only write more partial sums.
+    ctas = 2 * (int64_t)sm_count_current() / ranges;
+    if (ctas < 1) ctas = 1;
+    if (ctas > row_groups) ctas = row_groups;
+    p.groups = (int)((row_groups + ctas - 1) / ctas);
+    ctas = (row_groups + p.groups - 1) / p.groups;
+    e = part.get((size_t)ctas * units * 32);
+    if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gates' sums");
+    p.part = part.as<float>();
+    e = mv::dispatch<mv::CombineGrad>(rb, p, dim3((unsigned)ctas, (unsigned)ranges),
+                                      (size_t)(32 * per + (T + 1) / 2 * 4 * rb), s);
+  }
   if (e == cudaSuccess) {
-    const int64_t n = (int64_t)k * T;
-    e = launch_pdl(mv::dgate_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, (const float*)p.part, (int32_t)ctas,
-                   units * 8, slot, n, (int32_t)S, dgate);
+    const int64_t n = (int64_t)k * T, most_of = n > S ? n : S;
+    e = launch_pdl(mv::dgate_kernel, dim3((unsigned)((most_of + 31) / 32)), dim3(256), 0, s, (const float*)p.part, (int32_t)ctas,
+                   units * 8, source, slot, n, (int32_t)S, dgate);
     count_launch();
     if (e == cudaSuccess) e = cudaGetLastError();
   }
