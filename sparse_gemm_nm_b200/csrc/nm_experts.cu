@@ -55,7 +55,7 @@ struct Cfg {
 
 }  // namespace grp
 
-template <int MAXN, int ACC>
+template <int MAXN, int ACC, bool FEW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
     experts_pair_kernel(const __grid_constant__ ExpertsParams p) {
   using namespace grp;
@@ -102,8 +102,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
-  pdl_gate();  // no global memory touched before this point
-  if (warp == 0) list_tiles(p.offsets, p.E, p.S, MAXN, p.tiles_m, first, lane);
+  pdl_enter(FEW);  // no global memory touched before this point; few columns: nothing that the launch before writes
+  if (warp == 0) list_tiles<!FEW>(p.offsets, p.E, p.S, MAXN, p.tiles_m, first, lane);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -113,20 +113,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
   const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
   const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
   bool ok = true;
-  TileWalk w;
+  TileWalk<FEW, !FEW> w(first, p.offsets, p.E, p.S, MAXN, p.k_tiles, pair_id, npairs);
 
   if (warp == 1) {
     // ---------------------------------------------------------- MMA (leader)
     if (rank == 0 && lane == 0) {
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;  // aph bit a: phase of accumulator a
-      for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, MAXN); tile += npairs) {
+      while (ok && w.next()) {
         ok = mbar_wait(&acc_empty[acc], ((aph >> acc) & 1u) ^ 1u, abort_flag, p.status, kWaitNs);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + 256u * (uint32_t)acc;
-        const uint32_t idesc = idesc_bf16((uint32_t)w.n, true, 256);
-        for (int kt = 0; kt < p.k_tiles; ++kt) {
+        const uint32_t idesc = idesc_bf16((uint32_t)w.n, true, 256) & ~(FEW ? 1u << 16 : 0u);  // B's major axis
+        for (int kt = w.k0; kt < w.k1; ++kt) {
           ok = mbar_wait(&full[s], ph, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           tc_fence_after();
@@ -137,9 +137,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint64_t ad = smem_desc(a_addr + kk * 32, 16, 1024, SWZ_128B);
-            const uint64_t bd = smem_desc(b_addr + kk * 4096, kStrip, 1024, SWZ_128B);
+            const uint64_t bd = FEW ? smem_desc(b_addr + (kk >> 1) * 8192 + (kk & 1) * 64, 16, 1024, SWZ_128B)
+                                    : smem_desc(b_addr + kk * 4096, kStrip, 1024, SWZ_128B);
             tc_mma_sp_pair(d_tmem, ad, bd, e_tmem + (uint32_t)(kk & 2), idesc | (uint32_t)(kk & 1),
-                           (kt > 0 || kk > 0) ? 1u : 0u);
+                           (kt > w.k0 || kk > 0) ? 1u : 0u);
           }
           tc_commit_pair(&empty[s], 0x3);
           if (++s == kStages) { s = 0; ph ^= 1u; }
@@ -158,24 +159,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
   } else if (warp < 6) {
     // ------ copies, each warp a part of every stage: 0, 2 halves of the values, 3, 4 K halves of X, 5 the metadata
     if (lane == 0) {
+      if (FEW && (warp == 3 || warp == 4)) pdl_wait();  // the columns laid out by the launch before
       int s = 0;
       uint32_t ph = 0;
-      for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, MAXN); tile += npairs) {
+      while (ok && w.next()) {
         const int32_t row0 = w.tm * 256 + 128 * (int)rank;
         const int32_t col0 = w.x0 + (w.n >> 1) * (int32_t)rank;
         const int strips = C::kStrips == 2 && w.n > 128 ? 2 : 1;
-        for (int kt = 0; kt < p.k_tiles; ++kt) {
+        for (int kt = w.k0; kt < w.k1; ++kt) {
           ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           const uint32_t bar = lead_full0 + 8u * s;
           if (warp == 0 || warp == 2) {
             const int h = warp >> 1;
             if (rank == 0 && h == 0)
-              mbar_arrive_expect_tx(&full[s], 2u * (kA + kE + (uint32_t)strips * kStrip));
+              mbar_arrive_expect_tx(&full[s], 2u * (kA + kE + (FEW ? 128u * (uint32_t)w.n : (uint32_t)strips * kStrip)));
             tma_load_3d_pair(smem + s * kA + h * 8192, &p.tm_vals, bar, kt * 64, row0 + 64 * h, w.e);
           } else if (warp <= 4) {
             const int h = warp - 3;
             uint8_t* b = smem + C::kOffB + s * C::kB + h * 8192;
+            if constexpr (FEW) {  // K half h of this CTA's columns, 16 of them a box
+              for (int i = 0; i < (w.n >> 1); i += 16)
+                tma_load_2d_pair(b + i * 128, &p.tm_x, bar, kt * 128 + 64 * h, col0 + i);
+              if (++s == kStages) { s = 0; ph ^= 1u; }
+              continue;
+            }
             tma_load_2d_pair(b, &p.tm_x, bar, col0, kt * 128 + 64 * h);
             if (strips == 2) tma_load_2d_pair(b + kStrip, &p.tm_x, bar, col0 + 64, kt * 128 + 64 * h);
           } else {
@@ -191,7 +199,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
     uint8_t* box = smem + C::kOffEpi + quarter * kBoxBytes;
     uint32_t aph = 0;
     int acc = 0;
-    for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, MAXN); tile += npairs) {
+    while (ok && w.next()) {
       ok = mbar_wait_warp(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
       if (!ok) break;
       tc_fence_after();
@@ -202,6 +210,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
       };
+      if constexpr (FEW) {
+        if (!w.whole()) {
+          store_part(p.parts + (int64_t)(2 * pair_id + w.slot) * kSlotFloats, w, t_addr, wrow0 & 255, lane, release);
+          aph ^= 1u << acc;
+          if (ACC == 2) acc ^= 1;
+          continue;
+        }
+      }
       if (ACC == 2 || p.out_f32) {
         store_tile(p, w, t_addr, box, wrow0, lane, release);
       } else {
@@ -235,18 +251,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
     tmem_dealloc_pair(tmem_base, kTmemCols);
   }
   cluster_sync();  // ... and so does the deallocation: neither CTA leaves before both are through it
+  pdl_leave(FEW);
 }
 
-template <int MAXN, int ACC>
-static cudaError_t launch_experts(const ExpertsParams& p, cudaStream_t stream) {
+// Tiles that several pairs have parts of: their sums in the order of the stages, rounded and stored.  CTA (boundary, slab):
+// the tile that the share behind pair `boundary` starts inside (if it is the first such share of that tile), some of its
+// rows, all parts of an element on their way at once.
+constexpr int kJoinRows = 16;
+__global__ void __launch_bounds__(256) experts_join_kernel(const __grid_constant__ ExpertsParams p, int max_n, int pairs) {
+  extern __shared__ int32_t first[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_gate();
+  if (warp == 0) list_tiles<false>(p.offsets, p.E, p.S, max_n, p.tiles_m, first, lane);
+  __syncthreads();
+  const Shares sh(first[p.E], p.k_tiles, pairs);
+  const int pair = blockIdx.x;
+  if (pair + 1 >= sh.parts) return;
+  const int64_t from = sh.start(pair), cut = sh.start(pair + 1);
+  const int64_t id = cut / p.k_tiles, begin = id * p.k_tiles;
+  if (cut == begin || from > begin) return;  // whole tiles only; or an earlier share has cut this one
+  TileWalk<false, false> w(first, p.offsets, p.E, p.S, max_n, p.k_tiles, 0, 1);
+  w.tile((int)id);
+  const int32_t end = min(w.c1, w.x0 + w.n);
+  int last = pair + 1;
+  while (last + 1 < sh.parts && sh.start(last + 1) < begin + p.k_tiles) ++last;
+  const float* head = p.parts + (int64_t)(2 * pair + (from < begin ? 1 : 0)) * kSlotFloats;
+  for (int i = threadIdx.x; i < kJoinRows * w.n; i += 256) {
+    const int r = (int)blockIdx.y * kJoinRows + i / w.n, c = i % w.n;
+    const int64_t row = (int64_t)w.tm * 256 + r;
+    const int32_t col = w.x0 + c;
+    if (row >= p.M || col < w.c0 || col >= end) continue;
+    const int64_t at = (int64_t)r * w.n + c;
+    float sum = __ldcg(head + at);
+    const float* part = p.parts + (int64_t)(2 * (pair + 1)) * kSlotFloats + at;
+    int q = pair + 1;
+    for (; q + 4 <= last + 1; q += 4, part += 8 * kSlotFloats) {
+      const float f0 = __ldcg(part), f1 = __ldcg(part + 2 * kSlotFloats), f2 = __ldcg(part + 4 * kSlotFloats),
+                  f3 = __ldcg(part + 6 * kSlotFloats);
+      sum = (((sum + f0) + f1) + f2) + f3;
+    }
+    for (; q <= last; ++q, part += 2 * kSlotFloats) sum += __ldcg(part);
+    if (p.out_f32)
+      static_cast<float*>(p.Y)[row * p.ldy + col] = sum;
+    else
+      static_cast<uint16_t*>(p.Y)[row * p.ldy + col] = (uint16_t)(pack_bf16x2(sum, 0.f) & 0xFFFFu);
+  }
+}
+
+// XT (S x K) = X^T (K x S), 64 x 64 a CTA.
+__global__ void __launch_bounds__(256) columns_kernel(const uint16_t* X, int64_t ldx, int32_t K, int32_t S, uint16_t* XT) {
+  __shared__ uint16_t tile[64][66];
+  const int32_t k0 = (int32_t)blockIdx.x * 64, s0 = (int32_t)blockIdx.y * 64;
+  const int wide = min(64, S - s0);
+  pdl_gate();
+  for (int i = threadIdx.x; i < 64 * 32; i += 256) {
+    const int k = i >> 5, s = (i & 31) * 2;
+    if (k0 + k >= K || s >= wide) continue;
+    const uint16_t* at = X + (int64_t)(k0 + k) * ldx + s0 + s;
+    const uint32_t v = s + 1 < wide ? __ldcg(reinterpret_cast<const uint32_t*>(at)) : (uint32_t)__ldcg(at);
+    tile[s][k] = (uint16_t)v;
+    tile[s + 1][k] = (uint16_t)(v >> 16);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < wide * 32; i += 256) {
+    const int s = i >> 5, k = (i & 31) * 2;
+    if (k0 + k < K)
+      *reinterpret_cast<uint32_t*>(XT + (int64_t)(s0 + s) * K + k0 + k) = *reinterpret_cast<const uint32_t*>(&tile[s][k]);
+  }
+}
+
+template <int MAXN, int ACC, bool FEW>
+static cudaError_t launch_experts(const ExpertsParams& p, int pairs, cudaStream_t stream) {
   static SmemLimit limit;
-  cudaError_t e = limit.raise(experts_pair_kernel<MAXN, ACC>, grp::Cfg<MAXN, ACC>::bytes(kMaxExperts));
+  cudaError_t e = limit.raise(experts_pair_kernel<MAXN, ACC, FEW>, grp::Cfg<MAXN, ACC>::bytes(kMaxExperts));
   if (e != cudaSuccess) return e;
-  const int pairs = experts_pairs(p, MAXN);
-  e = launch_pdl(experts_pair_kernel<MAXN, ACC>, dim3(2 * pairs), dim3(grp::kThreads), grp::Cfg<MAXN, ACC>::bytes(p.E), stream,
-                 p);
+  e = launch_pdl(experts_pair_kernel<MAXN, ACC, FEW>, dim3(2 * pairs), dim3(grp::kThreads), grp::Cfg<MAXN, ACC>::bytes(p.E),
+                 stream, p);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Few columns: laid out with K contiguous first, then every pair an equal share of the stages, then the tiles cut by the
+// shares joined.
+static nm_status run_few(ExpertsParams& p, const uint16_t* X, int64_t ldx, int64_t K, cudaStream_t stream) {
+  const int pairs = sm_count_current() / 2;
+  Parts parts;
+  const int64_t at_parts = parts.take((int64_t)pairs * 2 * kSlotFloats * 4), at_x = parts.take(K * p.S * 2);
+  Staged staged(stream);
+  cudaError_t e = staged.get(parts.size());
+  if (e != cudaSuccess) return cuda_fail(e, "staging buffer of a grouped product");
+  p.parts = staged.as<float>(at_parts);
+  uint16_t* XT = staged.as<uint16_t>(at_x);
+  nm_status st = make_tmap(&p.tm_x, XT, (uint64_t)K, (uint64_t)p.S, (uint64_t)K * 2, 64, 16, 128, "X (K contiguous)");
+  if (st != NM_OK) return st;
+  e = launch_pdl(columns_kernel, dim3((unsigned)((K + 63) / 64), (unsigned)((p.S + 63) / 64)), dim3(256), 0, stream, X, ldx,
+                 (int32_t)K, p.S, XT);
+  count_launch();
+  if (e == cudaSuccess) e = launch_experts<128, 2, true>(p, pairs, stream);
+  if (e == cudaSuccess) {
+    e = launch_pdl(experts_join_kernel, dim3((unsigned)pairs, 256 / kJoinRows), dim3(256), (size_t)(p.E + 1) * 4, stream, p,
+                   128, pairs);
+    count_launch();
+    if (e == cudaSuccess) e = cudaGetLastError();
+  }
+  return e == cudaSuccess ? NM_OK : cuda_fail(e, "grouped product launch");
 }
 
 int experts_pairs(const ExpertsParams& p, int max_n) {
@@ -312,15 +420,13 @@ extern "C" nm_status nm_experts_spmm(const uint16_t* values, const uint32_t* met
   st = make_tmap3(&p.tm_vals, values, (uint64_t)(K / 2), (uint64_t)R, (uint64_t)E, (uint64_t)K, (uint64_t)(R * K), 64, 64, 128,
                   "values");
   if (st == NM_OK) st = make_meta_tmap(&p.tm_meta, meta, E * meta_row_blocks(R), meta_col_blocks(K));
-  if (st == NM_OK) st = make_tmap(&p.tm_x, X, (uint64_t)S, (uint64_t)K, (uint64_t)ldx * 2, 64, 64, 128, "X");
   if (st == NM_OK) st = make_experts_store_map(p, Y, R, S, ldy);
   if (st != NM_OK) return st;
-  cudaError_t e;
-  if (S <= 96 * E)
-    e = launch_experts<128, 2>(p, (cudaStream_t)stream);
-  else if (p.k_tiles <= 8)
-    e = launch_experts<224, 2>(p, (cudaStream_t)stream);
-  else
-    e = launch_experts<256, 1>(p, (cudaStream_t)stream);
+  // Few columns an expert (the weights' bytes decide), and few beside the rows: laying X out anew is little then.
+  if (S <= 96 * E && S <= R / 16 * E && (S + 63) / 64 < 65536) return run_few(p, X, ldx, K, (cudaStream_t)stream);
+  st = make_tmap(&p.tm_x, X, (uint64_t)S, (uint64_t)K, (uint64_t)ldx * 2, 64, 64, 128, "X");
+  if (st != NM_OK) return st;
+  const cudaError_t e = p.k_tiles <= 8 ? launch_experts<224, 2, false>(p, experts_pairs(p, 224), (cudaStream_t)stream)
+                                       : launch_experts<256, 1, false>(p, experts_pairs(p, 256), (cudaStream_t)stream);
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "grouped product launch");
 }

@@ -22,23 +22,25 @@ struct ExpertCols {
   int32_t nt;      // column tiles
 };
 
-// Offsets are clamped to the matrix, whatever they hold.
+// Offsets are clamped to the matrix, whatever they hold.  LINES: start on 128-byte lines of the activations (above).
+template <bool LINES = true>
 __device__ __forceinline__ ExpertCols expert_cols(const int32_t* offsets, int e, int32_t S, int max_n) {
   ExpertCols x;
   x.c0 = min(max(__ldcg(offsets + e), 0), S);
   x.c1 = min(max(__ldcg(offsets + e + 1), x.c0), S);
-  x.a0 = x.c0 & (x.c1 - x.c0 > 64 ? ~63 : ~7);
+  x.a0 = x.c0 & (LINES && x.c1 - x.c0 > 64 ? ~63 : ~7);
   const int32_t w = x.c1 > x.c0 ? x.c1 - x.a0 : 0;
   x.nt = (w + max_n - 1) / max_n;
   return x;
 }
 
 // first[e] = number of the first tile of expert e, first[E] = number of tiles.  One warp; `first` is shared memory.
+template <bool LINES = true>
 __device__ __forceinline__ void list_tiles(const int32_t* offsets, int E, int32_t S, int max_n, int row_tiles, int32_t* first,
                                            int lane) {
   int32_t base = 0;
   for (int e0 = 0; e0 < E; e0 += 32) {
-    int32_t n = e0 + lane < E ? expert_cols(offsets, e0 + lane, S, max_n).nt * row_tiles : 0;
+    int32_t n = e0 + lane < E ? expert_cols<LINES>(offsets, e0 + lane, S, max_n).nt * row_tiles : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int32_t up = __shfl_up_sync(0xFFFFFFFFu, n, o);
@@ -50,32 +52,82 @@ __device__ __forceinline__ void list_tiles(const int32_t* offsets, int E, int32_
   if (lane == 0) first[0] = 0;
 }
 
-// Walks the tiles id, id + stride, ... in ascending order.  Column tiles go fastest, so that the pairs running together
-// share a block of weights, which streams from HBM once.
+// What a pair works on: tiles pair, pair + pairs, ... whole, or (STREAM) an equal share of all tiles' stages, in one piece: a
+// share may start and end inside a tile, whose other stages the neighbouring pairs have.  Column tiles go fastest, so that
+// the pairs running together share a block of weights, which streams from HBM once.
+constexpr int kLeastStages = 4;  // of a share
+struct Shares {
+  int64_t total;  // stages of all tiles
+  int parts;      // shares
+  __device__ __forceinline__ Shares(int64_t tiles, int k_tiles, int pairs) {
+    total = tiles * k_tiles;
+    const int64_t most = total / kLeastStages;
+    parts = most < pairs ? (most < 1 ? 1 : (int)most) : pairs;
+  }
+  __device__ __forceinline__ int64_t start(int part) const { return total * part / parts; }
+};
+
+template <bool STREAM, bool LINES = true>
 struct TileWalk {
   int e, tm;       // expert, row tile
   int32_t x0, n;   // first column, columns (a multiple of 32)
   int32_t c0, c1;  // the expert's columns
+  int k0, k1;      // stages
+  int slot;        // of partial sums, for a part of a tile: 0 for the pair's first, 1 for its last
+  int64_t at, end;  // tile number, or (STREAM) stage number
+  const int32_t *first, *offsets;
+  int32_t S;
+  int E, max_n, k_tiles, step;
   ExpertCols cols;
   int known;
 
-  __device__ __forceinline__ TileWalk() : e(0), known(-1) {}
-  // Sets the members for tile `id` (at least the last call's); false behind the last tile.
-  __device__ __forceinline__ bool at(int id, const int32_t* first, const int32_t* offsets, int E, int32_t S, int max_n) {
-    if (id >= first[E]) return false;
+  __device__ __forceinline__ TileWalk(const int32_t* first_, const int32_t* offsets_, int E_, int32_t S_, int max_n_,
+                                      int k_tiles_, int pair, int pairs)
+      : e(0), slot(-1), first(first_), offsets(offsets_), S(S_), E(E_), max_n(max_n_), k_tiles(k_tiles_), step(pairs), known(-1) {
+    if (STREAM) {
+      const Shares sh(first[E], k_tiles, pairs);
+      at = pair < sh.parts ? sh.start(pair) : 0;
+      end = pair < sh.parts ? sh.start(pair + 1) : 0;
+    } else {
+      at = pair - pairs;
+      end = first[E];
+    }
+  }
+  // The next tile, or part of one; false behind the last.
+  __device__ __forceinline__ bool next() {
+    int id;
+    if (STREAM) {
+      if (slot >= 0) at += k1 - k0;
+      if (at >= end) return false;
+      id = (int)(at / k_tiles);
+      k0 = (int)(at - (int64_t)id * k_tiles);
+      k1 = end - at < k_tiles - k0 ? k0 + (int)(end - at) : k_tiles;
+      slot = slot < 0 ? 0 : 1;
+    } else {
+      at += step;
+      if (at >= end) return false;
+      id = (int)at;
+      k0 = 0;
+      k1 = k_tiles;
+    }
+    tile(id);
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return !STREAM || (k0 == 0 && k1 == k_tiles); }
+  // Sets the members for tile `id` (at least the last one).
+  __device__ __forceinline__ void tile(int id) {
     while (id >= first[e + 1]) ++e;
     if (e != known) {
-      cols = expert_cols(offsets, e, S, max_n);
+      cols = expert_cols<LINES>(offsets, e, S, max_n);
       known = e;
     }
-    const int at = id - first[e];
-    tm = at / cols.nt;
-    const int32_t tn = at - tm * cols.nt;
+    const int in = id - first[e];
+    tm = in / cols.nt;
+    const int32_t tn = in - tm * cols.nt;
     c0 = cols.c0;
     c1 = cols.c1;
     x0 = cols.a0 + tn * max_n;
     n = min((cols.c1 - x0 + 31) & ~31, max_n);
-    return true;
   }
 };
 
@@ -150,8 +202,8 @@ __device__ __forceinline__ void store_chunk(const ExpertsParams& p, const uint32
 
 // The warp's 32 rows of a tile, chunk by chunk; `release` is called after the last TMEM load.  Accumulator columns behind
 // the tile's hold what an earlier tile left there: they lie behind `end`.
-template <typename Release>
-__device__ __forceinline__ void store_tile(const ExpertsParams& p, const TileWalk& w, uint32_t t_addr, uint8_t* box,
+template <typename Walk, typename Release>
+__device__ __forceinline__ void store_tile(const ExpertsParams& p, const Walk& w, uint32_t t_addr, uint8_t* box,
                                            int32_t wrow0, int lane, Release release) {
   const int32_t end = min(w.c1, w.x0 + w.n);
   const int step = p.out_f32 ? 32 : 64;
@@ -170,6 +222,24 @@ __device__ __forceinline__ void store_tile(const ExpertsParams& p, const TileWal
       store_chunk<uint32_t>(p, v, box, w.x0 + c, w.c0, end, wrow0, lane);
     else
       store_chunk<uint16_t>(p, v, box, w.x0 + c, w.c0, end, wrow0, lane);
+  }
+}
+
+// Partial sums: the warp's 32 rows (row `row` of the tile on) into the slot's rows of w.n fp32.
+template <typename Walk, typename Release>
+__device__ __forceinline__ void store_part(float* slot, const Walk& w, uint32_t t_addr, int row, int lane,
+                                           Release release) {
+  float4* to = reinterpret_cast<float4*>(slot + (int64_t)(row + lane) * w.n);
+#pragma unroll 1
+  for (int c = 0; c < w.n; c += 32) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(t_addr + c, v);
+    tc_wait_ld();
+    if (c + 32 >= w.n) release();
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      to[c / 4 + q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]), __uint_as_float(v[4 * q + 2]),
+                                  __uint_as_float(v[4 * q + 3]));
   }
 }
 

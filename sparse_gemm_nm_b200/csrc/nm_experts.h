@@ -22,8 +22,11 @@ struct ExpertsParams {
   int32_t M, S, E;
   int32_t k_tiles, tiles_m, meta_rblocks;  // stages of a tile, row tiles, row blocks of one expert's metadata
   int out_f32;
+  float* parts;  // two slots of partial sums a pair
   uint32_t* status;
 };
+constexpr int kSlotCols = 128;
+constexpr int64_t kSlotFloats = 256 * kSlotCols;
 
 // Gradient of the survivors: dV_e[r][j] = sum over expert e's columns s of dY[r][s] X[k_j][s].
 struct ExpertsGradParams {

@@ -126,16 +126,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
   const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
   const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
   bool ok = true;
-  TileWalk w;
+  TileWalk<false> w(first, p.offsets, p.E, p.S, kMaxN, p.k_tiles, pair_id, npairs);
 
   if (warp == 0) {
     // ------------------------------------------------- values and metadata
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 0;
-      for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, kMaxN); tile += npairs) {
+      while (ok && w.next()) {
         const int32_t m0 = w.tm * 256 + 128 * (int)rank;
-        for (int kt = 0; kt < p.k_tiles; ++kt) {
+        for (int kt = w.k0; kt < w.k1; ++kt) {
           ok = mbar_wait(&raw_empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           mbar_arrive_expect_tx(&raw_full[s], kVals + kMeta);
@@ -150,10 +150,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 0;
-      for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, kMaxN); tile += npairs) {
+      while (ok && w.next()) {
         const int32_t col0 = w.x0 + (w.n >> 1) * (int32_t)rank;
         const int strips = w.n > 128 ? 2 : 1;
-        for (int kt = 0; kt < p.k_tiles; ++kt) {
+        for (int kt = w.k0; kt < w.k1; ++kt) {
           ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)strips * kStrip);
@@ -168,13 +168,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     if (rank == 0 && lane == 0) {
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
-      for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, kMaxN); tile += npairs) {
+      while (ok && w.next()) {
         ok = mbar_wait(&acc_empty[acc], ((aph >> acc) & 1u) ^ 1u, abort_flag, p.status, kWaitNs);
         if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + 256u * (uint32_t)acc;
         const uint32_t idesc = idesc_bf16_major((uint32_t)w.n, 256, true, true);
-        for (int kt = 0; kt < p.k_tiles; ++kt) {
+        for (int kt = w.k0; kt < w.k1; ++kt) {
           ok = mbar_wait(&full[s], ph, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           tc_fence_after();
@@ -183,7 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc_mma_pair(d_tmem, smem_desc(a_addr + kk * 2048, kStrip, 1024, SWZ_128B),
-                        smem_desc(b_addr + kk * 2048, kStrip, 1024, SWZ_128B), idesc, (kt > 0 || kk > 0) ? 1u : 0u);
+                        smem_desc(b_addr + kk * 2048, kStrip, 1024, SWZ_128B), idesc, (kt > w.k0 || kk > 0) ? 1u : 0u);
           tc_commit_pair(&empty[s], 0x3);
           if (++s == kStages) { s = 0; ph ^= 1u; }
         }
@@ -208,8 +208,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     const uint32_t out_at = (uint32_t)(q >> 1) * kStrip + (uint32_t)rb * 2048u;
     int s = 0, r = 0, turn = 0;
     uint32_t ph = 0, rph = 0;
-    for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, kMaxN); tile += npairs) {
-      for (int kt = 0; kt < p.k_tiles; ++kt) {
+    while (ok && w.next()) {
+      for (int kt = w.k0; kt < w.k1; ++kt) {
         if (turn == mine) {
           ok = mbar_wait_warp(&raw_full[r], rph, abort_flag, p.status, kWaitNs);
           if (!ok) break;
@@ -253,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     uint8_t* box = smem + kOffEpi + quarter * kBoxBytes;
     uint32_t aph = 0;
     int acc = 0;
-    for (int tile = pair_id; ok && w.at(tile, first, p.offsets, p.E, p.S, kMaxN); tile += npairs) {
+    while (ok && w.next()) {
       ok = mbar_wait_warp(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
       if (!ok) break;
       tc_fence_after();

@@ -63,6 +63,8 @@ __device__ __forceinline__ void pdl_enter(bool early) {
   if (!early) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// One thread of a kernel that pdl_enter() let run beside its predecessor: what that wrote may be read from here on.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_leave(bool early) {
   if (early) asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -61,6 +61,10 @@ CASES = [
     (300, 8, 32, [(i * 7) % 3 for i in range(300)], 0, 0),
     (1, 1030, 128, [2000], 0, 0),
     (6, 16, 4096, [700, 0, 129, 128, 127, 4], 6, 0),
+    (2, 300, 6000, [5, 40], 0, 0),
+    (1, 70, 11008, [1], 0, 7),
+    (9, 1300, 1024, [30, 0, 128, 127, 1, 64, 65, 2, 90], 5, 3),
+    (1, 4096, 912, [61], 3, 0),
 ]
 
 
