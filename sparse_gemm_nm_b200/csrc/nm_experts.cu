@@ -199,7 +199,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
     uint8_t* box = smem + C::kOffEpi + quarter * kBoxBytes;
     uint32_t aph = 0;
     int acc = 0;
+    const bool notes = FEW && rank == 0 && quarter == 0 && lane == 0;
+    bool noted = false;
     while (ok && w.next()) {
+      if (FEW && notes && w.k0 == 0 && w.k1 < p.k_tiles) {
+        const Shares sh(first[p.E], p.k_tiles, npairs);
+        const int last = sh.of(w.at + p.k_tiles - 1);
+        p.cuts[pair_id] = ExpertsCut{last - pair_id + 1, w.slot, w.tm * 256, w.x0, w.n, w.c0, min(w.c1, w.x0 + w.n), 0};
+        noted = true;
+      }
       ok = mbar_wait_warp(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
       if (!ok) break;
       tc_fence_after();
@@ -238,6 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
       aph ^= 1u << acc;
       if (ACC == 2) acc ^= 1;
     }
+    if (FEW && notes && !noted) p.cuts[pair_id].pairs = 0;
     if (lane == 0) bulk_wait_group<0>();  // every store of this warp has landed
   }
 
@@ -254,43 +263,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
   pdl_leave(FEW);
 }
 
-// Tiles that several pairs have parts of: their sums in the order of the stages, rounded and stored.  CTA (boundary, slab):
-// the tile that the share behind pair `boundary` starts inside (if it is the first such share of that tile), some of its
-// rows, all parts of an element on their way at once.
+// Tiles that several pairs have parts of: their sums in the order of the stages, rounded and stored.  CTA (pair, slab): the
+// tile that this pair has noted, some of its rows, several parts of an element on their way at once.
 constexpr int kJoinRows = 16;
-__global__ void __launch_bounds__(256) experts_join_kernel(const __grid_constant__ ExpertsParams p, int max_n, int pairs) {
-  extern __shared__ int32_t first[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(256) experts_join_kernel(const __grid_constant__ ExpertsParams p) {
   pdl_gate();
-  if (warp == 0) list_tiles<false>(p.offsets, p.E, p.S, max_n, p.tiles_m, first, lane);
-  __syncthreads();
-  const Shares sh(first[p.E], p.k_tiles, pairs);
-  const int pair = blockIdx.x;
-  if (pair + 1 >= sh.parts) return;
-  const int64_t from = sh.start(pair), cut = sh.start(pair + 1);
-  const int64_t id = cut / p.k_tiles, begin = id * p.k_tiles;
-  if (cut == begin || from > begin) return;  // whole tiles only; or an earlier share has cut this one
-  TileWalk<false, false> w(first, p.offsets, p.E, p.S, max_n, p.k_tiles, 0, 1);
-  w.tile((int)id);
-  const int32_t end = min(w.c1, w.x0 + w.n);
-  int last = pair + 1;
-  while (last + 1 < sh.parts && sh.start(last + 1) < begin + p.k_tiles) ++last;
-  const float* head = p.parts + (int64_t)(2 * pair + (from < begin ? 1 : 0)) * kSlotFloats;
-  for (int i = threadIdx.x; i < kJoinRows * w.n; i += 256) {
-    const int r = (int)blockIdx.y * kJoinRows + i / w.n, c = i % w.n;
-    const int64_t row = (int64_t)w.tm * 256 + r;
-    const int32_t col = w.x0 + c;
-    if (row >= p.M || col < w.c0 || col >= end) continue;
-    const int64_t at = (int64_t)r * w.n + c;
+  const int4* at_cut = reinterpret_cast<const int4*>(p.cuts + blockIdx.x);
+  const int4 a = __ldcg(at_cut), b = __ldcg(at_cut + 1);
+  const int pairs = a.x, slot = a.y, row0 = a.z, x0 = a.w, n = b.x, c0 = b.y, c1 = b.z;
+  if (pairs == 0) return;
+  const float* head = p.parts + (int64_t)(2 * (int)blockIdx.x + slot) * kSlotFloats;
+  const float* rest = p.parts + (int64_t)(2 * (int)blockIdx.x + 2) * kSlotFloats;
+  for (int i = threadIdx.x; i < kJoinRows * n; i += 256) {
+    const int r = (int)blockIdx.y * kJoinRows + i / n, c = i % n;
+    const int64_t row = row0 + r;
+    const int32_t col = x0 + c;
+    if (row >= p.M || col < c0 || col >= c1) continue;
+    const int64_t at = (int64_t)r * n + c;
     float sum = __ldcg(head + at);
-    const float* part = p.parts + (int64_t)(2 * (pair + 1)) * kSlotFloats + at;
-    int q = pair + 1;
-    for (; q + 4 <= last + 1; q += 4, part += 8 * kSlotFloats) {
+    const float* part = rest + at;
+    int q = 1;
+    for (; q + 4 <= pairs; q += 4, part += 8 * kSlotFloats) {
       const float f0 = __ldcg(part), f1 = __ldcg(part + 2 * kSlotFloats), f2 = __ldcg(part + 4 * kSlotFloats),
                   f3 = __ldcg(part + 6 * kSlotFloats);
       sum = (((sum + f0) + f1) + f2) + f3;
     }
-    for (; q <= last; ++q, part += 2 * kSlotFloats) sum += __ldcg(part);
+    for (; q < pairs; ++q, part += 2 * kSlotFloats) sum += __ldcg(part);
     if (p.out_f32)
       static_cast<float*>(p.Y)[row * p.ldy + col] = sum;
     else
@@ -302,20 +300,21 @@ __global__ void __launch_bounds__(256) experts_join_kernel(const __grid_constant
 __global__ void __launch_bounds__(256) columns_kernel(const uint16_t* X, int64_t ldx, int32_t K, int32_t S, uint16_t* XT) {
   __shared__ uint16_t tile[64][66];
   const int32_t k0 = (int32_t)blockIdx.x * 64, s0 = (int32_t)blockIdx.y * 64;
-  const int wide = min(64, S - s0);
+  const int wide = min(64, S - s0), deep = min(64, K - k0), two = (wide + 1) >> 1;
   pdl_gate();
-  for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-    const int k = i >> 5, s = (i & 31) * 2;
-    if (k0 + k >= K || s >= wide) continue;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < deep * two; i += 256) {
+    const int k = i / two, s = (i - k * two) * 2;
     const uint16_t* at = X + (int64_t)(k0 + k) * ldx + s0 + s;
     const uint32_t v = s + 1 < wide ? __ldcg(reinterpret_cast<const uint32_t*>(at)) : (uint32_t)__ldcg(at);
     tile[s][k] = (uint16_t)v;
     tile[s + 1][k] = (uint16_t)(v >> 16);
   }
   __syncthreads();
+#pragma unroll 4
   for (int i = threadIdx.x; i < wide * 32; i += 256) {
     const int s = i >> 5, k = (i & 31) * 2;
-    if (k0 + k < K)
+    if (k < deep)
       *reinterpret_cast<uint32_t*>(XT + (int64_t)(s0 + s) * K + k0 + k) = *reinterpret_cast<const uint32_t*>(&tile[s][k]);
   }
 }
@@ -336,11 +335,13 @@ static cudaError_t launch_experts(const ExpertsParams& p, int pairs, cudaStream_
 static nm_status run_few(ExpertsParams& p, const uint16_t* X, int64_t ldx, int64_t K, cudaStream_t stream) {
   const int pairs = sm_count_current() / 2;
   Parts parts;
-  const int64_t at_parts = parts.take((int64_t)pairs * 2 * kSlotFloats * 4), at_x = parts.take(K * p.S * 2);
+  const int64_t at_parts = parts.take((int64_t)pairs * 2 * kSlotFloats * 4), at_x = parts.take(K * p.S * 2),
+                at_cuts = parts.take((int64_t)pairs * sizeof(ExpertsCut));
   Staged staged(stream);
   cudaError_t e = staged.get(parts.size());
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer of a grouped product");
   p.parts = staged.as<float>(at_parts);
+  p.cuts = staged.as<ExpertsCut>(at_cuts);
   uint16_t* XT = staged.as<uint16_t>(at_x);
   nm_status st = make_tmap(&p.tm_x, XT, (uint64_t)K, (uint64_t)p.S, (uint64_t)K * 2, 64, 16, 128, "X (K contiguous)");
   if (st != NM_OK) return st;
@@ -349,8 +350,7 @@ static nm_status run_few(ExpertsParams& p, const uint16_t* X, int64_t ldx, int64
   count_launch();
   if (e == cudaSuccess) e = launch_experts<128, 2, true>(p, pairs, stream);
   if (e == cudaSuccess) {
-    e = launch_pdl(experts_join_kernel, dim3((unsigned)pairs, 256 / kJoinRows), dim3(256), (size_t)(p.E + 1) * 4, stream, p,
-                   128, pairs);
+    e = launch_pdl(experts_join_kernel, dim3((unsigned)pairs, 256 / kJoinRows), dim3(256), 0, stream, p);
     count_launch();
     if (e == cudaSuccess) e = cudaGetLastError();
   }

@@ -65,6 +65,12 @@ struct Shares {
     parts = most < pairs ? (most < 1 ? 1 : (int)most) : pairs;
   }
   __device__ __forceinline__ int64_t start(int part) const { return total * part / parts; }
+  // The share that has stage `at`.
+  __device__ __forceinline__ int of(int64_t at) const {
+    int part = (int)(at * parts / total);
+    while (part + 1 < parts && start(part + 1) <= at) ++part;
+    return part;
+  }
 };
 
 template <bool STREAM, bool LINES = true>

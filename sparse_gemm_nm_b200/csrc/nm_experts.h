@@ -23,7 +23,16 @@ struct ExpertsParams {
   int32_t k_tiles, tiles_m, meta_rblocks;  // stages of a tile, row tiles, row blocks of one expert's metadata
   int out_f32;
   float* parts;  // two slots of partial sums a pair
+  struct ExpertsCut* cuts;  // one a pair
   uint32_t* status;
+};
+// A tile whose stages several pairs have: the first of them notes it, for the kernel that joins their sums.
+struct ExpertsCut {
+  int32_t pairs;             // 0: this pair is not the first of one
+  int32_t slot;              // of the first pair's sums; the others' are their first
+  int32_t row0, x0, n;       // the tile
+  int32_t c0, c1;            // the columns of it that are the expert's
+  int32_t pad;
 };
 constexpr int kSlotCols = 128;
 constexpr int64_t kSlotFloats = 256 * kSlotCols;
