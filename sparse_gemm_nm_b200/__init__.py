@@ -339,8 +339,9 @@ def nm_experts_combine_grad(dY, lddy, R, T, k, Yg, ldg, S, slot, source, gate, d
 def nm_clip_grads(grads, outs, sizes, dtypes, max_norm, norm, stream=None) -> None:
     """grads, outs (or None): sequences of device pointers or tensors; sizes, dtypes: sequences of numbers."""
     n = len(grads)
-    g = (ctypes.c_void_p * n)(*[_ptr(t) for t in grads])
-    o = None if outs is None else (ctypes.c_void_p * n)(*[_ptr(t) for t in outs])
+    pointer = ctypes.c_void_p * n
+    g = pointer(*[x if type(x) is int else _ptr(x) for x in grads])
+    o = g if outs is grads else None if outs is None else pointer(*[x if type(x) is int else _ptr(x) for x in outs])
     _check(lib().nm_clip_grads(g, o, (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*dtypes), n, max_norm, _ptr(norm),
                                _stream(stream)), "nm_clip_grads")
 
@@ -738,13 +739,11 @@ def experts_route(logits, k: int, renorm: bool = True, stream=None):
     if not 1 <= k <= E:
         raise ValueError(f"k must be 1..{E}, got {k}")
     with _On(logits, stream) as s:
-        n = (k * T + 3) // 4 * 4  # each part on 16 bytes
-        words = logits.new_empty(3 * n + E + 1, dtype=torch.int32)
-        expert, slot = words[:k * T].view(k, T), words[n:n + k * T].view(k, T)
-        source, offsets = words[2 * n:2 * n + k * T], words[3 * n:]
+        expert, slot, source = logits.new_empty((3, k, T), dtype=torch.int32).unbind(0)
+        offsets = logits.new_empty(E + 1, dtype=torch.int32)
         gate = logits.new_empty((k, T), dtype=torch.float32)
         nm_experts_route(logits, ld, _out_type(logits.dtype), E, T, k, renorm, expert, gate, slot, source, offsets, s)
-    return expert, gate, slot, source, offsets
+    return expert, gate, slot, source.view(-1), offsets
 
 
 def _pairs(k: int, T: int, *named):
@@ -832,19 +831,28 @@ def clip_grads(grads, max_norm: float, out=None, stream=None):
     grads = list(grads)
     if not grads:
         raise ValueError("no gradients")
-    outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
-        raise ValueError(f"{len(grads)} gradients, {len(outs)} outputs")
-    _same_device(grads[0], *grads, *outs)
-    types = []
-    for g, o in zip(grads, outs):
-        types.append(_out_type(g.dtype))
-        if o.dtype != g.dtype or o.shape != g.shape or not g.is_contiguous() or not o.is_contiguous():
-            raise ValueError(f"gradients and outputs must be contiguous and alike, got {tuple(g.shape)} {g.dtype} and "
-                             f"{tuple(o.shape)} {o.dtype}")
+    at, types = grads[0].get_device(), {torch.bfloat16: NM_OUT_BF16, torch.float32: NM_OUT_F32}
+    sizes = [g.numel() for g in grads]
+    kinds = [g.dtype for g in grads]
+    every = [grads]
+    if out is not None:
+        every.append(list(out))
+        if len(every[1]) != len(grads):
+            raise ValueError(f"{len(grads)} gradients, {len(every[1])} outputs")
+        if [o.numel() for o in every[1]] != sizes or [o.dtype for o in every[1]] != kinds:
+            raise ValueError("outputs must have their gradients' sizes and types")
+    for ts in every:  # (lists of one question each: a step has hundreds of gradients)
+        if not all([t.is_contiguous() for t in ts]):
+            raise ValueError("gradients and outputs must be contiguous")
+        if at < 0 or [t.get_device() for t in ts] != [at] * len(ts):
+            _require_cuda(*ts)
+            raise ValueError("gradients and outputs must share one device")
+    if not set(kinds) <= types.keys():
+        raise ValueError(f"gradients must be bfloat16 or float32, got {set(kinds) - types.keys()}")
+    pointers = [[t.data_ptr() for t in ts] for ts in every]
     with _On(grads[0], stream) as s:
         norm = grads[0].new_empty((), dtype=torch.float32)
-        nm_clip_grads(grads, outs, [g.numel() for g in grads], types, max_norm, norm, s)
+        nm_clip_grads(pointers[0], pointers[-1], sizes, [types[k] for k in kinds], max_norm, norm, s)
     return norm
 
 

@@ -227,7 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
         }
       }
       if (ACC == 2 || p.out_f32) {
-        store_tile(p, w, t_addr, box, wrow0, lane, release);
+        store_tile(p, w.x0, w.n, w.c0, w.c1, t_addr, box, wrow0, lane, release);
       } else {
         const int32_t end = min(w.c1, w.x0 + w.n);
         uint32_t v[4][32];

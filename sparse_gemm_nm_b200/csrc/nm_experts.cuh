@@ -137,6 +137,67 @@ struct TileWalk {
   }
 };
 
+// Tiles of up to WIDE columns, the whole ones of all experts first and the experts' last, narrower ones behind them: tiles
+// are few then, and what is left for the pairs that come through early is small.  first has 2 E + 1 numbers.
+template <int WIDE>
+__device__ __forceinline__ int32_t wide_tiles(const int32_t* offsets, int v, int E, int32_t S, int row_tiles) {
+  const ExpertCols x = expert_cols(offsets, v < E ? v : v - E, S, WIDE);
+  const int32_t w = x.c1 > x.c0 ? x.c1 - x.a0 : 0;
+  return (v < E ? w / WIDE : (w % WIDE != 0)) * row_tiles;
+}
+template <int WIDE>
+__device__ __forceinline__ void list_wide_tiles(const int32_t* offsets, int E, int32_t S, int row_tiles, int32_t* first, int lane) {
+  int32_t base = 0;
+  for (int v0 = 0; v0 < 2 * E; v0 += 32) {
+    int32_t n = v0 + lane < 2 * E ? wide_tiles<WIDE>(offsets, v0 + lane, E, S, row_tiles) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t up = __shfl_up_sync(0xFFFFFFFFu, n, o);
+      if (lane >= o) n += up;
+    }
+    if (v0 + lane < 2 * E) first[v0 + lane + 1] = base + n;
+    base += __shfl_sync(0xFFFFFFFFu, n, 31);
+  }
+  if (lane == 0) first[0] = 0;
+}
+
+template <int WIDE>
+struct WideWalk {
+  int e, tm;       // expert, row tile
+  int32_t x0, n;   // first column, columns (a multiple of 32)
+  int32_t c0, c1;  // the expert's columns
+  const int32_t *first, *offsets;
+  int32_t S;
+  int E, v, id, step, known;
+  ExpertCols cols;
+
+  __device__ __forceinline__ WideWalk(const int32_t* first_, const int32_t* offsets_, int E_, int32_t S_, int pair, int pairs)
+      : first(first_), offsets(offsets_), S(S_), E(E_), v(0), id(pair - pairs), step(pairs), known(-1) {}
+  __device__ __forceinline__ bool next() {
+    id += step;
+    if (id >= first[2 * E]) return false;
+    while (id >= first[v + 1]) ++v;
+    e = v < E ? v : v - E;
+    if (e != known) {
+      cols = expert_cols(offsets, e, S, WIDE);
+      known = e;
+    }
+    const int in = id - first[v], whole = (cols.c1 - cols.a0) / WIDE;
+    c0 = cols.c0;
+    c1 = cols.c1;
+    if (v < E) {
+      tm = in / whole;
+      x0 = cols.a0 + (in - tm * whole) * WIDE;
+      n = WIDE;
+    } else {
+      tm = in;
+      x0 = cols.a0 + whole * WIDE;
+      n = (cols.c1 - x0 + 31) & ~31;
+    }
+    return true;
+  }
+};
+
 // ------------------------------------------------------------------ stores
 constexpr uint32_t kBoxBytes = 4096;  // an epilogue warp's staging tile: 32 rows x 128 bytes, 128-byte swizzle
 
@@ -208,13 +269,13 @@ __device__ __forceinline__ void store_chunk(const ExpertsParams& p, const uint32
 
 // The warp's 32 rows of a tile, chunk by chunk; `release` is called after the last TMEM load.  Accumulator columns behind
 // the tile's hold what an earlier tile left there: they lie behind `end`.
-template <typename Walk, typename Release>
-__device__ __forceinline__ void store_tile(const ExpertsParams& p, const Walk& w, uint32_t t_addr, uint8_t* box,
-                                           int32_t wrow0, int lane, Release release) {
-  const int32_t end = min(w.c1, w.x0 + w.n);
+template <typename Release>
+__device__ __forceinline__ void store_tile(const ExpertsParams& p, int32_t x0, int32_t n, int32_t c0, int32_t c1, uint32_t t_addr,
+                                           uint8_t* box, int32_t wrow0, int lane, Release release) {
+  const int32_t end = min(c1, x0 + n);
   const int step = p.out_f32 ? 32 : 64;
 #pragma unroll 1
-  for (int c = 0; c < w.n; c += step) {
+  for (int c = 0; c < n; c += step) {
     uint32_t v[32];
     if (p.out_f32) {
       tmem_ld_32x32b_x32(t_addr + c, v);
@@ -223,11 +284,11 @@ __device__ __forceinline__ void store_tile(const ExpertsParams& p, const Walk& w
       take_bf16(t_addr + c, v);
       take_bf16(t_addr + c + 32, v + 16);
     }
-    if (c + step >= w.n) release();
+    if (c + step >= n) release();
     if (p.out_f32)
-      store_chunk<uint32_t>(p, v, box, w.x0 + c, w.c0, end, wrow0, lane);
+      store_chunk<uint32_t>(p, v, box, x0 + c, c0, end, wrow0, lane);
     else
-      store_chunk<uint16_t>(p, v, box, w.x0 + c, w.c0, end, wrow0, lane);
+      store_chunk<uint16_t>(p, v, box, x0 + c, c0, end, wrow0, lane);
   }
 }
 

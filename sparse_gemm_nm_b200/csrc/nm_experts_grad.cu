@@ -33,19 +33,19 @@ namespace nmk {
 
 namespace grpt {
 constexpr int kThreads = 512;  // warps 0 raw copies, 1 MMA, 2 copies of dY, 4-7 epilogue, 8-15 expansion
-constexpr int kRaw = 4, kStages = 5;
+constexpr int kRaw = 4, kStages = 3;
 constexpr uint32_t kVals = 8192, kMeta = 1024;
-constexpr uint32_t kA = 16384, kB = 16384;  // 64 reduction rows x 128 columns, in strips of 8 KB
+constexpr uint32_t kA = 16384, kB = 32768;  // 64 reduction rows x 128 and 256 columns, in strips of 8 KB
 constexpr uint32_t kStrip = 8192;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxN = 256;
+constexpr int kMaxN = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kOffB = kStages * kA, kOffVals = kOffB + kStages * kB, kOffMeta = kOffVals + kRaw * kVals;
 constexpr uint32_t kOffEpi = kOffMeta + kRaw * kMeta;
 constexpr uint32_t kOffBar = kOffEpi + 4 * kBoxBytes;
 constexpr uint32_t kOffFirst = kOffBar + (2 * kStages + 2 * kRaw + 5) * 8 + 8;
-constexpr uint32_t bytes(int E) { return kOffFirst + 4u * (uint32_t)(E + 1) + 1024u; }
-static_assert(kOffFirst + 4 * (kMaxExperts + 1) + 1024 <= 232448, "shared memory");
+constexpr uint32_t bytes(int E) { return kOffFirst + 4u * (uint32_t)(2 * E + 1) + 1024u; }
+static_assert(kOffFirst + 4 * (2 * kMaxExperts + 1) + 1024 <= 232448, "shared memory");
 }  // namespace grpt
 
 // Four weights, as two words, from their two stored values and positions (nib = p0 | p1 << 2, 8 times in s0 and s1).
@@ -116,7 +116,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     tmem_relinquish_pair();
   }
   pdl_gate();  // no global memory touched before this point
-  if (warp == 0) list_tiles(p.offsets, p.E, p.S, kMaxN, p.tiles_m, first, lane);
+  if (warp == 0) list_wide_tiles<kMaxN>(p.offsets, p.E, p.S, p.tiles_m, first, lane);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -126,7 +126,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
   const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
   const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
   bool ok = true;
-  TileWalk<false> w(first, p.offsets, p.E, p.S, kMaxN, p.k_tiles, pair_id, npairs);
+  WideWalk<kMaxN> w(first, p.offsets, p.E, p.S, pair_id, npairs);
 
   if (warp == 0) {
     // ------------------------------------------------- values and metadata
@@ -135,7 +135,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
       uint32_t ph = 0;
       while (ok && w.next()) {
         const int32_t m0 = w.tm * 256 + 128 * (int)rank;
-        for (int kt = w.k0; kt < w.k1; ++kt) {
+        for (int kt = 0; kt < p.k_tiles; ++kt) {
           ok = mbar_wait(&raw_empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           mbar_arrive_expect_tx(&raw_full[s], kVals + kMeta);
@@ -151,14 +151,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
       int s = 0;
       uint32_t ph = 0;
       while (ok && w.next()) {
-        const int32_t col0 = w.x0 + (w.n >> 1) * (int32_t)rank;
-        const int strips = w.n > 128 ? 2 : 1;
-        for (int kt = w.k0; kt < w.k1; ++kt) {
+        // Columns in parts of 256, each half to a CTA, in strips of 64.
+        const int32_t n0 = min(w.n, 256), n1 = w.n - n0;
+        const int32_t col0 = w.x0 + (n0 >> 1) * (int32_t)rank, col1 = w.x0 + 256 + (n1 >> 1) * (int32_t)rank;
+        const int s0 = n0 > 128 ? 2 : 1, s1 = (n1 + 127) >> 7;
+        for (int kt = 0; kt < p.k_tiles; ++kt) {
           ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
           if (!ok) break;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)strips * kStrip);
-          for (int j = 0; j < strips; ++j)
-            tma_load_2d_pair(smem + kOffB + s * kB + j * kStrip, &p.tm_x, lead_full0 + 8u * s, col0 + 64 * j, kt * 64);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)(s0 + s1) * kStrip);
+          uint8_t* b = smem + kOffB + s * kB;
+          for (int j = 0; j < s0; ++j) tma_load_2d_pair(b + j * kStrip, &p.tm_x, lead_full0 + 8u * s, col0 + 64 * j, kt * 64);
+          for (int j = 0; j < s1; ++j)
+            tma_load_2d_pair(b + (2 + j) * kStrip, &p.tm_x, lead_full0 + 8u * s, col1 + 64 * j, kt * 64);
           if (++s == kStages) { s = 0; ph ^= 1u; }
         }
       }
@@ -169,12 +173,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       while (ok && w.next()) {
-        ok = mbar_wait(&acc_empty[acc], ((aph >> acc) & 1u) ^ 1u, abort_flag, p.status, kWaitNs);
+        const int parts = w.n > 256 ? 2 : 1;
+        for (int j = 0; j < parts && ok; ++j)
+          ok = mbar_wait(&acc_empty[acc ^ j], ((aph >> (acc ^ j)) & 1u) ^ 1u, abort_flag, p.status, kWaitNs);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + 256u * (uint32_t)acc;
-        const uint32_t idesc = idesc_bf16_major((uint32_t)w.n, 256, true, true);
-        for (int kt = w.k0; kt < w.k1; ++kt) {
+        const uint32_t d0 = tmem_base + 256u * (uint32_t)acc, d1 = tmem_base + 256u * (uint32_t)(acc ^ 1);
+        const uint32_t idesc0 = idesc_bf16_major((uint32_t)min(w.n, 256), 256, true, true);
+        const uint32_t idesc1 = idesc_bf16_major((uint32_t)max(w.n - 256, 32), 256, true, true);
+        for (int kt = 0; kt < p.k_tiles; ++kt) {
           ok = mbar_wait(&full[s], ph, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           tc_fence_after();
@@ -182,15 +189,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
           const uint32_t b_addr = smem_u32(smem + kOffB + s * kB);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_pair(d_tmem, smem_desc(a_addr + kk * 2048, kStrip, 1024, SWZ_128B),
-                        smem_desc(b_addr + kk * 2048, kStrip, 1024, SWZ_128B), idesc, (kt > w.k0 || kk > 0) ? 1u : 0u);
+            tc_mma_pair(d0, smem_desc(a_addr + kk * 2048, kStrip, 1024, SWZ_128B),
+                        smem_desc(b_addr + kk * 2048, kStrip, 1024, SWZ_128B), idesc0, (kt > 0 || kk > 0) ? 1u : 0u);
+          if (parts == 2) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_pair(d1, smem_desc(a_addr + kk * 2048, kStrip, 1024, SWZ_128B),
+                          smem_desc(b_addr + 2 * kStrip + kk * 2048, kStrip, 1024, SWZ_128B), idesc1,
+                          (kt > 0 || kk > 0) ? 1u : 0u);
+          }
           tc_commit_pair(&empty[s], 0x3);
           if (++s == kStages) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
-        tc_commit_pair(&acc_full[acc], 0x3);
-        aph ^= 1u << acc;
-        acc ^= 1;
+        for (int j = 0; j < parts; ++j) {
+          tc_commit_pair(&acc_full[acc], 0x3);
+          aph ^= 1u << acc;
+          acc ^= 1;
+        }
       }
       if (!ok) {
         tc_commit_pair(spare, 0x1);
@@ -209,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     int s = 0, r = 0, turn = 0;
     uint32_t ph = 0, rph = 0;
     while (ok && w.next()) {
-      for (int kt = w.k0; kt < w.k1; ++kt) {
+      for (int kt = 0; kt < p.k_tiles; ++kt) {
         if (turn == mine) {
           ok = mbar_wait_warp(&raw_full[r], rph, abort_flag, p.status, kWaitNs);
           if (!ok) break;
@@ -254,17 +270,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     uint32_t aph = 0;
     int acc = 0;
     while (ok && w.next()) {
-      ok = mbar_wait_warp(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t t_addr = tmem_base + 256u * (uint32_t)acc + ((uint32_t)(quarter * 32) << 16);
-      store_tile(p, w, t_addr, box, w.tm * 256 + 128 * (int)rank + quarter * 32, lane, [&] {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
-      });
-      aph ^= 1u << acc;
-      acc ^= 1;
+      for (int32_t x = 0; x < w.n; x += 256) {  // the parts
+        ok = mbar_wait_warp(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t t_addr = tmem_base + 256u * (uint32_t)acc + ((uint32_t)(quarter * 32) << 16);
+        store_tile(p, w.x0 + x, min(w.n - x, 256), w.c0, w.c1, t_addr, box, w.tm * 256 + 128 * (int)rank + quarter * 32, lane,
+                   [&] {
+                     tc_fence_before();
+                     __syncwarp();
+                     if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
+                   });
+        aph ^= 1u << acc;
+        acc ^= 1;
+      }
     }
     if (lane == 0) bulk_wait_group<0>();  // every store of this warp has landed
   }
