@@ -26,7 +26,7 @@ constexpr int kMaxK = 16;
 constexpr int kMaxE = 1024;
 constexpr int kWarps = 8;        // slices of the experts, at most
 constexpr int kPlaceThreads = 512;
-constexpr int kChunk = 16;       // groups of 32 tokens a CTA of place_kernel takes
+constexpr int kMaxChunk = 16;    // groups of 32 tokens a CTA of place_kernel takes, at most
 
 struct Params {
   const void* logits;
@@ -40,6 +40,7 @@ struct Params {
   int32_t* offsets; // E + 1
   uint8_t* counts;  // E x pitch: chosen pairs of every expert in every group of 32 tokens
   int32_t groups, pitch;
+  int32_t chunk;    // groups a CTA of place_kernel takes, a power of two
 };
 
 template <typename T>
@@ -225,55 +226,64 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constan
   }
 }
 
-// Columns of the pairs of `kChunk` groups of 32 tokens a CTA: every expert's pairs in the groups before, its first column,
+// Columns of the pairs of p.chunk groups of 32 tokens a CTA: every expert's pairs in the groups before, its first column,
 // and the chunk's own groups, each from the byte counts.
 __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const __grid_constant__ Params p) {
   extern __shared__ int32_t smem[];
   int32_t* start = smem;               // E + 1: total, then first column of the expert
-  int32_t* base = smem + p.E + 1;      // E x kChunk: column of the expert's first pair in the group
+  int32_t* base = smem + p.E + 1;      // E x chunk: column of the expert's first pair in the group
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g0 = (int)blockIdx.x * kChunk;
+  const int g0 = (int)blockIdx.x * p.chunk;
   pdl_gate();
+  const uint32_t part = (uint32_t)(g0 & 15);  // groups of the piece of 16 that the chunk starts in
+  uint32_t keep[4];                           // their bytes
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    keep[i] = part >= 4u * i + 4u ? 0xFFFFFFFFu : part <= 4u * i ? 0u : (1u << (8u * (part - 4u * i))) - 1u;
   for (int e = warp; e < p.E; e += kPlaceThreads / 32) {
-    const uint4* row = reinterpret_cast<const uint4*>(p.counts + (int64_t)e * p.pitch);
+    const uint8_t* row = p.counts + (int64_t)e * p.pitch;
     uint32_t all = 0, before = 0;
-    for (int i = lane; i < p.pitch / 16; i += 32) {  // bytes behind the last group are zero; g0 is a multiple of 16
-      const uint4 u = __ldcg(row + i);
+    for (int i = lane; i < p.pitch / 16; i += 32) {  // bytes behind the last group are zero
+      const uint4 u = __ldcg(reinterpret_cast<const uint4*>(row) + i);
       const uint32_t n = __dp4a(u.x, 0x01010101u, __dp4a(u.y, 0x01010101u, __dp4a(u.z, 0x01010101u, __dp4a(u.w, 0x01010101u, 0u))));
       all += n;
-      if (16 * i < g0) before += n;
+      if (i < g0 / 16)
+        before += n;
+      else if (i == g0 / 16)
+        before = __dp4a(u.x & keep[0], 0x01010101u, __dp4a(u.y & keep[1], 0x01010101u,
+                        __dp4a(u.z & keep[2], 0x01010101u, __dp4a(u.w & keep[3], 0x01010101u, before))));
     }
+    const int32_t own = lane < p.chunk && g0 + lane < p.groups ? (int32_t)__ldcg(row + g0 + lane) : 0;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
       before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
     }
-    // the chunk's groups: an exclusive sum over its 16 bytes
-    int32_t own = lane < kChunk && g0 + lane < p.groups ? (int32_t)__ldcg(p.counts + (int64_t)e * p.pitch + g0 + lane) : 0;
-    int32_t sum = own;
+    int32_t sum = own;  // of the chunk's groups up to the lane's
 #pragma unroll
-    for (int o = 1; o < kChunk; o <<= 1) {
+    for (int o = 1; o < kMaxChunk; o <<= 1) {
       const int32_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
       if (lane >= o) sum += up;
     }
-    if (lane < kChunk) base[e * kChunk + lane] = (int32_t)before + sum - own;
+    if (lane < p.chunk) base[e * p.chunk + lane] = (int32_t)before + sum - own;
     if (lane == 0) start[e] = (int32_t)all;
   }
   __syncthreads();
   if (warp == 0) scan_exclusive(start, p.E, lane);
   __syncthreads();
-  const int32_t t0 = g0 * 32, tokens = min(p.T - t0, kChunk * 32);
-  for (int i = threadIdx.x; i < tokens; i += kPlaceThreads) {
-    for (int j = 0; j < p.k; ++j) {
-      const int64_t at = (int64_t)j * p.T + t0 + i;
-      const int32_t e = __ldcg(p.expert + at);
-      int32_t s = -1;
-      if (e >= 0) {
-        s = start[e] + base[e * kChunk + (i >> 5)] + __ldcg(p.slot + at);
-        p.source[s] = j * p.T + t0 + i;
-      }
-      p.slot[at] = s;
+  const int32_t t0 = g0 * 32, tokens = min(p.T - t0, p.chunk * 32);
+  const int shift = 5 + (31 - __clz(p.chunk));  // a row of chunk x 32 tokens for every j
+  for (int i = threadIdx.x; i < p.k << shift; i += kPlaceThreads) {
+    const int j = i >> shift, t = i & ((1 << shift) - 1);
+    if (t >= tokens) continue;
+    const int64_t at = (int64_t)j * p.T + t0 + t;
+    const int32_t e = __ldcg(p.expert + at);
+    int32_t s = -1;
+    if (e >= 0) {
+      s = start[e] + base[e * p.chunk + (t >> 5)] + __ldcg(p.slot + at);
+      p.source[s] = j * p.T + t0 + t;
     }
+    p.slot[at] = s;
   }
   if (blockIdx.x == 0)
     for (int e = threadIdx.x; e <= p.E; e += kPlaceThreads) p.offsets[e] = start[e];
@@ -307,42 +317,32 @@ template <typename L>
 __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__ GradParams p) {
   __shared__ uint32_t mask[kMaxE];
   __shared__ int32_t who[kMaxK][32];
-  __shared__ float part[kMaxK][32];
-  __shared__ float scale[3][32];  // the best logit, its gate, sum_j gate_j dgate_j
+  __shared__ float gates[kMaxK][32], part[kMaxK][32];  // gate, gate dgate
+  __shared__ float best_of[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int32_t t = (int32_t)blockIdx.x * 32 + lane;
   const bool live = t < p.T;
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) mask[e] = 0u;
   pdl_gate();
   __syncthreads();
-  if (warp == 0 && live) {
-    float dot = 0.f, g0 = 0.f, best = 0.f;
-    for (int j = 0; j < p.k; ++j) {
+  if (live) {
+    for (int j = warp; j < p.k; j += warps) {
       const int64_t at = (int64_t)j * p.T + t;
       const int32_t e = __ldcg(p.expert + at);
+      const float gate = __ldcg(p.gate + at), d = __ldcg(p.dgate + at);
       const bool has = e >= 0 && e < p.E;  // (another number is no expert's)
-      const float g = has ? __ldcg(p.gate + at) : 0.f, d = has ? __ldcg(p.dgate + at) : 0.f;
       who[j][lane] = has ? e : -1;
-      part[j][lane] = g * d;
-      dot += g * d;
-      if (has) {
-        atomicOr(&mask[e], 1u << lane);
-        if (j == 0) {
-          g0 = g;
-          best = load_logit<L>(static_cast<const L*>(p.logits) + (int64_t)e * p.ld + t);
-        }
-      }
+      gates[j][lane] = has ? gate : 0.f;
+      part[j][lane] = has ? gate * d : 0.f;
+      if (has) atomicOr(&mask[e], 1u << lane);
+      if (j == 0) best_of[lane] = has ? load_logit<L>(static_cast<const L*>(p.logits) + (int64_t)e * p.ld + t) : 0.f;
     }
-    if (p.renorm)
-      for (int j = 0; j < p.k; ++j)
-        if (who[j][lane] >= 0) part[j][lane] -= __ldcg(p.gate + (int64_t)j * p.T + t) * dot;
-    scale[0][lane] = best;
-    scale[1][lane] = g0;
-    scale[2][lane] = dot;
   }
   __syncthreads();
   if (!live) return;
-  const float best = scale[0][lane], g0 = scale[1][lane], dot = scale[2][lane];
+  const float best = best_of[lane], g0 = gates[0][lane];
+  float dot = 0.f;
+  for (int j = 0; j < p.k; ++j) dot += part[j][lane];
   const bool some = who[0][lane] >= 0;  // a token without experts has no gradient
 #pragma unroll 4
   for (int e = warp; e < p.E; e += warps) {
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__
     if (!p.renorm && some) v = -g0 * expf(load_logit<L>(static_cast<const L*>(p.logits) + (int64_t)e * p.ld + t) - best) * dot;
     if (mask[e] >> lane & 1u) {
       for (int j = 0; j < p.k; ++j)
-        if (who[j][lane] == e) v += part[j][lane];
+        if (who[j][lane] == e) v += p.renorm ? part[j][lane] - gates[j][lane] * dot : part[j][lane];
     }
     static_cast<L*>(p.dlogits)[(int64_t)e * p.ldd + t] = round_to<L>(v);
   }
@@ -402,9 +402,12 @@ extern "C" nm_status nm_experts_route(const void* logits, int64_t ld, nm_out_dty
     const cudaError_t e = cudaMemsetAsync(offsets, 0, (size_t)(E + 1) * 4, s);
     return e == cudaSuccess ? NM_OK : cuda_fail(e, "offsets");
   }
-  route::Params p{logits, ld, (int32_t)E, (int32_t)T, k, renorm, expert, gate, slot, source, offsets, nullptr, 0, 0};
+  route::Params p{logits, ld, (int32_t)E, (int32_t)T, k, renorm, expert, gate, slot, source, offsets, nullptr, 0, 0, 1};
   p.groups = (int32_t)((T + 31) / 32);
   p.pitch = (p.groups + 15) / 16 * 16;
+  // A CTA reads all counts, so more of them only as long as there are SMs.
+  p.chunk = 1;
+  while (p.chunk < route::kMaxChunk && p.chunk * sm_count_current() < p.groups) p.chunk *= 2;
   const int warps = E >= 8 * route::kWarps ? route::kWarps : (int)((E + 7) / 8);  // eight experts a slice at least
   Staged counts(s);
   if (p.groups > 1) {
@@ -415,10 +418,10 @@ extern "C" nm_status nm_experts_route(const void* logits, int64_t ld, nm_out_dty
   cudaError_t e = dtype == NM_OUT_F32 ? route::launch_route<float>(p, k, warps, s) : route::launch_route<uint16_t>(p, k, warps, s);
   if (e == cudaSuccess && p.groups > 1) {
     static SmemLimit limit;
-    e = limit.raise(route::place_kernel, 4u * (route::kMaxE * (route::kChunk + 1) + 1));
+    e = limit.raise(route::place_kernel, 4u * (route::kMaxE * (route::kMaxChunk + 1) + 1));
     if (e == cudaSuccess) {
-      e = launch_pdl(route::place_kernel, dim3((unsigned)((p.groups + route::kChunk - 1) / route::kChunk)),
-                     dim3(route::kPlaceThreads), (size_t)4 * (E * (route::kChunk + 1) + 1), s, p);
+      e = launch_pdl(route::place_kernel, dim3((unsigned)((p.groups + p.chunk - 1) / p.chunk)), dim3(route::kPlaceThreads),
+                     (size_t)4 * (E * (p.chunk + 1) + 1), s, p);
       count_launch();
       if (e == cudaSuccess) e = cudaGetLastError();
     }
