@@ -64,17 +64,18 @@ __device__ __forceinline__ int32_t token_of(int32_t source, int32_t T, uint32_t 
   return r >= T ? r - T : r;
 }
 
-// Eight consecutive 32-bit values, `fill` behind the first `valid`.
+// Eight consecutive 32-bit values, `fill` behind the first `valid`.  Indices and gates are read by every CTA: ordinary loads,
+// which L1 holds (past it, a few lines of L2 that all SMs ask for at once: 4096 rows of 200 columns, combine_grad 25 us).
 template <typename V>
 __device__ __forceinline__ void load8(const V* p, int valid, bool vec, V fill, V (&v)[8]) {
   if (vec && valid >= 8) {
-    const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p)), b = __ldcg(reinterpret_cast<const uint4*>(p) + 1);
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const V*>(&w[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < valid ? __ldcg(p + i) : fill;
+    for (int i = 0; i < 8; ++i) v[i] = i < valid ? p[i] : fill;
   }
 }
 
@@ -105,19 +106,22 @@ __device__ __forceinline__ void load_rows(const Params& p, int64_t row0, typenam
   }
 }
 
-// The RB elements of column c (outside [0, cols_in): zeros), bf16 pairs.
+// The RB elements of column c (outside [0, cols_in): zeros), bf16 pairs.  Read in any case, from column 0 where there is
+// none, and masked: loads behind a condition would be waited for one by one.
 template <int RB, bool DIRECT>
 __device__ __forceinline__ void pick(const Params& p, const typename Word<RB>::type* tile, int64_t row, int32_t c,
                                      uint32_t (&w)[(RB + 1) / 2]) {
   const bool in = (uint32_t)c < (uint32_t)p.cols_in;
+  const uint32_t keep = in ? 0xFFFFFFFFu : 0u;
+  const int32_t at = in ? c : 0;
   if constexpr (DIRECT) {
-    w[0] = in ? (uint32_t)p.in[row * p.ldin + c] : 0u;
+    w[0] = (uint32_t)p.in[row * p.ldin + at] & keep;
   } else if constexpr (RB == 4) {
-    const uint2 v = in ? tile[c] : make_uint2(0u, 0u);
-    w[0] = v.x;
-    w[1] = v.y;
+    const uint2 v = tile[at];
+    w[0] = v.x & keep;
+    w[1] = v.y & keep;
   } else {
-    w[0] = in ? (uint32_t)tile[c] : 0u;
+    w[0] = (uint32_t)tile[at] & keep;
   }
 }
 
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   }
   const int32_t units = (p.cols_out + 7) >> 3;
   const int64_t items = (int64_t)p.groups * units;
-  for (int64_t i = threadIdx.x; i < items; i += blockDim.x) {
+  for (int64_t i = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; i < items; i += (int64_t)gridDim.y * blockDim.x) {
     const int g = p.groups == 1 ? 0 : (int)((uint32_t)i / (uint32_t)units);
     const int32_t s = (int32_t)(i - (int64_t)g * units) * 8;
     const int64_t row = row0 + (int64_t)g * RB;
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
   }
   const int32_t units = (p.cols_out + 7) >> 3;
   const int64_t items = (int64_t)p.groups * units;
-  for (int64_t i = threadIdx.x; i < items; i += blockDim.x) {
+  for (int64_t i = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; i < items; i += (int64_t)gridDim.y * blockDim.x) {
     const int g = p.groups == 1 ? 0 : (int)((uint32_t)i / (uint32_t)units);
     const int32_t t = (int32_t)(i - (int64_t)g * units) * 8;
     const int64_t row = row0 + (int64_t)g * RB;
@@ -212,6 +216,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
     for (int r = 0; r < RB; ++r)
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[r][c] = 0.f;
+#pragma unroll 2
     for (int j = 0; j < p.k; ++j) {
       int32_t slot[8];
       float gate[8];
@@ -303,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_con
         uint32_t v[(RB + 1) / 2];
         const bool live = src[c] >= 0 && src[c] < p.k * p.T;
         pick<RB, DIRECT>(p, tile, row, live ? token_of(src[c], p.T, p.inv_T) : -1, v);
-        const float gate = !live ? 0.f : p.gate ? __ldg(p.gate + src[c]) : 1.f;
+        const float gate = !live ? 0.f : p.gate ? p.gate[src[c]] : 1.f;
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
           const float dy = r & 1 ? bf_hi(v[r >> 1]) : bf_lo(v[r >> 1]);
@@ -332,6 +337,105 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_con
   }
 }
 
+// Few tokens: rows of Yg and dY are a few lines, picked from L1; a thread keeps its eight columns and takes row after row, the
+// CTA's threads side by side in rows.  gridDim.y ranges of kFewThreads units.
+constexpr int kFewThreads = 256;
+__global__ void __launch_bounds__(kFewThreads) combine_grad_few_kernel(const __grid_constant__ Params p) {
+  __shared__ float4 sums[kFewThreads][2];
+  const int32_t all = (p.cols_out + 7) >> 3, u0 = (int32_t)blockIdx.y * kFewThreads, units = min(all - u0, kFewThreads);
+  const int lanes = kFewThreads / units, rl = (int)threadIdx.x / units, u = u0 + (int)threadIdx.x - rl * units;
+  const int32_t s = 8 * u;
+  const int valid = p.cols_out - s;
+  pdl_gate();
+  float dot[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) dot[c] = 0.f;
+  if (rl < lanes) {
+    int32_t src[8];
+    float gate[8];
+    uint32_t live = 0;  // a bit a column
+    load8<int32_t>(p.index + s, valid, p.vec, -1, src);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const bool has = src[c] >= 0 && src[c] < p.k * p.T;
+      live |= (has ? 1u : 0u) << c;
+      src[c] = has ? src[c] : 0;  // (any token: what is read is not used)
+      gate[c] = 1.f;
+    }
+    if (p.gate) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) gate[c] = p.gate[src[c]];
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      gate[c] = live >> c & 1u ? gate[c] : 0.f;
+      src[c] = token_of(src[c], p.T, p.inv_T);
+    }
+    const int64_t end = min((int64_t)p.rows, ((int64_t)blockIdx.x + 1) * p.groups);
+    // A row's elements, the next row's on their way meanwhile (the stores hide from the compiler that they may be).
+    auto fetch = [&](int64_t row, uint32_t (&x)[8], uint32_t (&y)[4]) {
+      const uint16_t* from = p.in + row * p.ldin;
+      const uint16_t* at = p.yg + row * p.ldyg + s;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) x[c] = from[src[c]];
+      if (valid >= 8) {
+        const uint4 v = __ldcg(reinterpret_cast<const uint4*>(at));
+        y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+      } else {
+        y[0] = y[1] = y[2] = y[3] = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < valid) y[c >> 1] |= (uint32_t)__ldcg(at + c) << (16 * (c & 1));
+      }
+    };
+    uint32_t x[8], y[4];
+    int64_t row = (int64_t)blockIdx.x * p.groups + rl;
+    if (row < end) fetch(row, x, y);
+    for (; row < end; row += lanes) {
+      uint32_t nx[8] = {}, ny[4] = {};
+      if (row + lanes < end) fetch(row + lanes, nx, ny);
+      float d[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {  // a column of no token may hold anything
+        const uint32_t keep = 0u - (live >> c & 1u);
+        const float dy = bf(x[c] & keep), yv = __uint_as_float((c & 1 ? y[c >> 1] & 0xFFFF0000u : y[c >> 1] << 16) & keep);
+        dot[c] = fmaf(dy, yv, dot[c]);
+        d[c] = gate[c] * dy;
+      }
+      uint32_t w[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) w[c] = pack_bf16x2(d[2 * c], d[2 * c + 1]);
+      store8(static_cast<uint16_t*>(p.out) + row * p.ldout + s, valid, w);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) x[c] = nx[c];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c] = ny[c];
+    }
+  }
+  // The rows' lanes of a unit, two by two.
+  sums[threadIdx.x][0] = make_float4(dot[0], dot[1], dot[2], dot[3]);
+  sums[threadIdx.x][1] = make_float4(dot[4], dot[5], dot[6], dot[7]);
+  int half = 1;
+  while (2 * half < lanes) half *= 2;
+  for (; lanes > 1 && half > 0; half >>= 1) {
+    __syncthreads();
+    if (rl < half && rl + half < lanes) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float4 a = sums[threadIdx.x][i];
+        const float4 b = sums[threadIdx.x + half * units][i];
+        a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+        sums[threadIdx.x][i] = a;
+      }
+    }
+  }
+  if (rl == 0) {
+    float4* to = reinterpret_cast<float4*>(p.part + (int64_t)blockIdx.x * (all * 8) + s);
+    to[0] = sums[threadIdx.x][0];
+    to[1] = sums[threadIdx.x][1];
+  }
+}
+
 // ------------------------------------------------------------ long rows
 // The same by persistent CTAs that keep every column's index (and gate) in shared memory, 16 and 32 bits each, and take
 // group after group of kRows rows: read again for every group, the indices are as many bytes as the rows themselves.
@@ -343,6 +447,7 @@ namespace lng {
 constexpr int kThreads = 1024;
 constexpr int64_t kMaxSmem = 226 * 1024;
 constexpr int kMaxDepth = 8;
+constexpr int64_t kLeastOut = 4096;  // columns of the result, eight a thread: half the CTA's threads at least
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kBarBytes = 2 * kMaxDepth * 8 + 16;
 
@@ -440,7 +545,6 @@ __device__ __forceinline__ void values(const float* at, float (&v)[8]) {
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
-constexpr int kCombineRows = 2, kGradRows = 2;
 constexpr int kGradUnits = 2;  // units of eight columns a thread holds the dot products of
 
 // The gather has room for two tiles of RB rows as words, and one access a column then serves RB rows: the next group's rows
@@ -552,8 +656,9 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   }
 }
 // Rows of its word (0: it does not fit).
-inline int gather_rows(int64_t cols, int64_t rows, int64_t beside) {
+inline int gather_rows(int64_t cols, int64_t cols_out, int64_t rows, int64_t beside) {
   const int64_t units = (cols + 7) / 8;
+  if (cols_out < kLeastOut) return 0;
   for (int rb = 4; rb >= 1; rb >>= 1)
     if (cols < 0xFFFF && units <= (int64_t)kThreads * (4 / rb) && 2 * units * 16 * rb + beside <= kMaxSmem &&
         rows >= 3 * (int64_t)rb * sm_count_current())
@@ -570,33 +675,37 @@ static cudaError_t launch_gather(const Params& p, unsigned grid, size_t smem, cu
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// gridDim.y ranges of the tokens.
+template <int ROWS>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  const int32_t units = (p.cols_out + 7) >> 3, per = units * 8, none = (p.cols_in + 7) & ~7;
+  const int32_t all = (p.cols_out + 7) >> 3, none = (p.cols_in + 7) & ~7;
+  const int32_t most = (all + (int32_t)gridDim.y - 1) / (int32_t)gridDim.y, per = most * 8;
+  const int32_t u0 = (int32_t)blockIdx.y * most, units = min(most, all - u0);
   const int lane = threadIdx.x & 31;
   float* gates = reinterpret_cast<float*>(smem);
   uint16_t* index = reinterpret_cast<uint16_t*>(gates + (p.gate ? (int64_t)p.k * per : 0));
-  Ring<kCombineRows> ring;
+  Ring<ROWS> ring;
   ring.init(p, reinterpret_cast<uint8_t*>(index + (int64_t)p.k * per));
   __syncthreads();
   pdl_gate();
   if (threadIdx.x == 0)
     for (int i = 0; i < p.depth; ++i) ring.issue(p);
   for (int j = 0; j < p.k; ++j)
-    for (int32_t t = threadIdx.x; t < per; t += kThreads) {
-      const int32_t s = t < p.T ? __ldcg(p.index + (int64_t)j * p.T + t) : -1;
+    for (int32_t i = threadIdx.x; i < units * 8; i += kThreads) {
+      const int32_t t = 8 * u0 + i, s = t < p.T ? __ldcg(p.index + (int64_t)j * p.T + t) : -1;
       const bool has = (uint32_t)s < (uint32_t)p.cols_in;
-      index[j * per + t] = has ? (uint16_t)s : (uint16_t)none;
-      if (p.gate) gates[j * per + t] = has ? __ldcg(p.gate + (int64_t)j * p.T + t) : 0.f;
+      index[j * per + i] = has ? (uint16_t)s : (uint16_t)none;
+      if (p.gate) gates[j * per + i] = has ? __ldcg(p.gate + (int64_t)j * p.T + t) : 0.f;
     }
   __syncthreads();
-  for (int64_t row = (int64_t)blockIdx.x * kCombineRows; row < p.rows; row += (int64_t)gridDim.x * kCombineRows) {
+  for (int64_t row = (int64_t)blockIdx.x * ROWS; row < p.rows; row += (int64_t)gridDim.x * ROWS) {
     const uint8_t* rows = ring.wait(p);
     if (!ring.ok) break;
     for (int32_t u = threadIdx.x; u < units; u += kThreads) {
-      float acc[kCombineRows][8];
+      float acc[ROWS][8];
 #pragma unroll
-      for (int r = 0; r < kCombineRows; ++r)
+      for (int r = 0; r < ROWS; ++r)
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[r][c] = 0.f;
       for (int j = 0; j < p.k; ++j) {
@@ -610,22 +719,22 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
           for (int c = 0; c < 8; ++c) gate[c] = 1.f;
         }
 #pragma unroll
-        for (int r = 0; r < kCombineRows; ++r) {
+        for (int r = 0; r < ROWS; ++r) {
           const uint16_t* from = reinterpret_cast<const uint16_t*>(rows + r * ring.pitch);
 #pragma unroll
           for (int c = 0; c < 8; ++c) acc[r][c] = fmaf(gate[c], bf(from[s[c]]), acc[r][c]);
         }
       }
 #pragma unroll
-      for (int r = 0; r < kCombineRows; ++r) {
+      for (int r = 0; r < ROWS; ++r) {
         if (row + r >= p.rows) break;
         if (p.out_f32) {
-          store8(static_cast<float*>(p.out) + (row + r) * p.ldout + 8 * u, p.cols_out - 8 * u, acc[r]);
+          store8(static_cast<float*>(p.out) + (row + r) * p.ldout + 8 * (u0 + u), p.cols_out - 8 * (u0 + u), acc[r]);
         } else {
           uint32_t w[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) w[c] = pack_bf16x2(acc[r][2 * c], acc[r][2 * c + 1]);
-          store8(static_cast<uint16_t*>(p.out) + (row + r) * p.ldout + 8 * u, p.cols_out - 8 * u, w);
+          store8(static_cast<uint16_t*>(p.out) + (row + r) * p.ldout + 8 * (u0 + u), p.cols_out - 8 * (u0 + u), w);
         }
       }
     }
@@ -648,6 +757,7 @@ __device__ __forceinline__ uint4 columns8(const Params& p, int64_t row, int32_t 
 }
 
 // gridDim.y ranges of kThreads * kGradUnits units of the columns at most; the dot products stay with the threads.
+template <int ROWS>
 __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int32_t all = (p.cols_out + 7) >> 3, none = (p.cols_in + 7) & ~7;
@@ -656,23 +766,23 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_con
   const int lane = threadIdx.x & 31;
   float* gates = reinterpret_cast<float*>(smem);
   uint16_t* index = reinterpret_cast<uint16_t*>(gates + per * 8);
-  Ring<kGradRows> ring;
+  Ring<ROWS> ring;
   ring.init(p, reinterpret_cast<uint8_t*>(index + per * 8));
   __syncthreads();
   pdl_gate();
   if (threadIdx.x == 0)
     for (int i = 0; i < p.depth; ++i) ring.issue(p);
-  uint4 y[kGradUnits][kGradRows];  // the next group's columns of Yg
+  uint4 y[kGradUnits][ROWS];  // the next group's columns of Yg
   auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < kGradUnits; ++i)
 #pragma unroll
-      for (int r = 0; r < kGradRows; ++r) {
+      for (int r = 0; r < ROWS; ++r) {
         const int32_t u = (int32_t)threadIdx.x + i * kThreads;
         if (u < units) y[i][r] = columns8(p, row + r, 8 * (u0 + u));
       }
   };
-  int64_t row = (int64_t)blockIdx.x * kGradRows;
+  int64_t row = (int64_t)blockIdx.x * ROWS;
   fetch(row);
   for (int32_t i = threadIdx.x; i < units * 8; i += kThreads) {
     const int32_t s = 8 * u0 + i, src = s < p.cols_out ? __ldcg(p.index + s) : -1;
@@ -686,7 +796,7 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_con
   for (int i = 0; i < kGradUnits; ++i)
 #pragma unroll
     for (int c = 0; c < 8; ++c) dot[i][c] = 0.f;
-  for (; row < p.rows; row += (int64_t)gridDim.x * kGradRows) {
+  for (; row < p.rows; row += (int64_t)gridDim.x * ROWS) {
     const uint8_t* rows = ring.wait(p);
     if (!ring.ok) break;
 #pragma unroll
@@ -695,14 +805,14 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_con
       if (u >= units) break;
       const int32_t s = 8 * (u0 + u);
       const uint4 packed = *reinterpret_cast<const uint4*>(index + 8 * u);
-      uint32_t w[kGradRows][4];
+      uint32_t w[ROWS][4];
 #pragma unroll
       for (int c = 0; c < 8; c += 2) {
         const uint32_t pair = c < 2 ? packed.x : c < 4 ? packed.y : c < 6 ? packed.z : packed.w;
         const int32_t t0 = (int32_t)(pair & 0xFFFFu), t1 = (int32_t)(pair >> 16);
         const float2 gate = *reinterpret_cast<const float2*>(gates + 8 * u + c);
 #pragma unroll
-        for (int r = 0; r < kGradRows; ++r) {
+        for (int r = 0; r < ROWS; ++r) {
           const uint16_t* from = reinterpret_cast<const uint16_t*>(rows + r * ring.pitch);
           const uint32_t yw = c < 2 ? y[i][r].x : c < 4 ? y[i][r].y : c < 6 ? y[i][r].z : y[i][r].w;
           const float d0 = bf(from[t0]), d1 = bf(from[t1]);
@@ -713,10 +823,10 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_con
         }
       }
 #pragma unroll
-      for (int r = 0; r < kGradRows; ++r) {
+      for (int r = 0; r < ROWS; ++r) {
         if (row + r < p.rows)
           store8(static_cast<uint16_t*>(p.out) + (row + r) * p.ldout + s, p.cols_out - s, w[r]);
-        y[i][r] = columns8(p, row + (int64_t)gridDim.x * kGradRows + r, s);  // while the other units are at work
+        y[i][r] = columns8(p, row + (int64_t)gridDim.x * ROWS + r, s);  // while the other units are at work
       }
     }
     ring.done(p, lane);
@@ -733,15 +843,34 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(const __grid_con
   ring.leave();
 }
 
-// Groups of `group` rows in the ring for rows of `cols` elements, `beside` bytes of indices and gates with them: 0 where the
-// form does not fit (16-bit indices, two groups in shared memory) or would have too few groups to be worth its start.
-inline int depth_of(int64_t cols, int64_t rows, int64_t beside, int group) {
-  if (cols > 65000 || rows < 3 * (int64_t)group * sm_count_current()) return 0;
-  const int64_t depth = (kMaxSmem - beside - kBarBytes) / ((int64_t)row_bytes((int32_t)cols) * group);
-  return depth < 2 ? 0 : depth < kMaxDepth ? (int)depth : kMaxDepth;
+// How a ring form takes a call: groups of `rows` rows, `depth` of them in the ring, the columns of the result in `ranges`.
+struct Plan {
+  int rows, depth;
+  int64_t ranges, per;  // units a range
+};
+// For rows of `cols` elements and `units` units of the result, at most `most` a range, `beside` bytes of indices and gates
+// a unit.  rows = 0 where no form fits (16-bit indices, two groups in shared memory) or each CTA would have too little to be
+// worth its start.
+inline Plan plan_of(int64_t cols, int64_t units, int64_t most, int64_t rows, int64_t beside) {
+  if (cols > 65000) return Plan{0, 0, 0, 0};
+  for (int64_t ranges = (units + most - 1) / most; ranges <= 16; ++ranges) {
+    const int64_t per = (units + ranges - 1) / ranges;
+    if (per < (ranges == 1 ? kThreads / 2 : 128)) break;
+    for (int group = 2; group >= 1; --group) {
+      if (rows * ranges < 3 * (int64_t)group * sm_count_current()) continue;
+      const int64_t depth = (kMaxSmem - beside * per - kBarBytes) / ((int64_t)row_bytes((int32_t)cols) * group);
+      if (depth >= 2) return Plan{group, depth < kMaxDepth ? (int)depth : kMaxDepth, ranges, per};
+    }
+  }
+  return Plan{0, 0, 0, 0};
 }
-inline size_t smem_of(const Params& p, int64_t beside, int group) {
-  return (size_t)(beside + kBarBytes + (int64_t)p.depth * group * row_bytes(p.cols_in));
+inline size_t smem_of(const Params& p, const Plan& l, int64_t beside) {
+  return (size_t)(beside * l.per + kBarBytes + (int64_t)l.depth * l.rows * row_bytes(p.cols_in));
+}
+// CTAs for each range: one to an SM in all.
+inline unsigned ctas_of(int64_t rows, const Plan& l) {
+  const int64_t groups = (rows + l.rows - 1) / l.rows, ctas = sm_count_current() / l.ranges;
+  return (unsigned)(groups < ctas ? groups : ctas < 1 ? 1 : ctas);
 }
 inline unsigned grid_of(int64_t rows, int group) {
   const int64_t groups = (rows + group - 1) / group, sms = sm_count_current();
@@ -788,9 +917,11 @@ static uint32_t inverse(int64_t T) {
   return q > 0xFFFFFFFFull ? 0xFFFFFFFFu : (uint32_t)q;
 }
 
-// Rows a word holds for rows of `cols` elements (0: picked from global memory), beside `beside` bytes.
-static int rows_of_word(int64_t cols, int64_t rows, int64_t beside) {
+// Rows a word holds for rows of `cols` elements, beside `beside` bytes.  0: picked from global memory, where the row does not
+// fit, or where it is two lines of L1 and not worth a barrier, or gives a group of rows to few threads (13824 rows, one token at two experts: combine 61 -> 8 us).
+static int rows_of_word(int64_t cols, int64_t cols_out, int64_t rows, int64_t beside) {
   const int64_t one = (cols + 1) / 2 * 4;  // bytes of a row
+  if (cols <= 128 || cols_out <= 256) return 0;
   for (int rb = 4; rb > 1; rb >>= 1)
     if (one * rb + beside <= kTileBytes && rows >= rb) return rb;
   for (int rb = 2; rb >= 1; rb >>= 1)
@@ -818,26 +949,36 @@ static cudaError_t start(Kernel kernel, SmemLimit& limit, dim3 grid, size_t smem
 }
 template <int RB, bool DIRECT>
 struct Gather {
-  static cudaError_t go(const Params& p, dim3 grid, size_t smem, cudaStream_t s) {
+  static cudaError_t go(const Params& p, dim3 grid, size_t smem, cudaStream_t s, int threads = kThreads) {
     static SmemLimit limit;
-    return start(gather_kernel<RB, DIRECT>, limit, grid, smem, p, s);
+    return start(gather_kernel<RB, DIRECT>, limit, grid, smem, p, s, threads);
   }
 };
 template <int RB, bool DIRECT>
 struct Combine {
-  static cudaError_t go(const Params& p, dim3 grid, size_t smem, cudaStream_t s) {
+  static cudaError_t go(const Params& p, dim3 grid, size_t smem, cudaStream_t s, int threads = kThreads) {
     static SmemLimit limit;
-    return start(combine_kernel<RB, DIRECT>, limit, grid, smem, p, s);
+    return start(combine_kernel<RB, DIRECT>, limit, grid, smem, p, s, threads);
   }
 };
 template <int RB, bool DIRECT>
 struct CombineGrad {
-  static cudaError_t go(const Params& p, dim3 grid, size_t smem, cudaStream_t s) {
+  static cudaError_t go(const Params& p, dim3 grid, size_t smem, cudaStream_t s, int threads = kThreads) {
     static SmemLimit limit;
-    return start(combine_grad_kernel<RB, DIRECT>, limit, grid, smem, p, s);
+    return start(combine_grad_kernel<RB, DIRECT>, limit, grid, smem, p, s, threads);
   }
 };
 
+// Threads for the units of a CTA's groups.
+static int threads_of(int64_t cols_out, int groups) {
+  const int64_t t = (((cols_out + 7) / 8 * groups) + 63) / 64 * 64;
+  return t < 128 ? 128 : t < kThreads ? (int)t : kThreads;
+}
+// Few rows: CTAs that share a group of rows (each brings it), until every SM has one.
+static unsigned shares_of(int64_t ctas, int64_t cols_out, int groups, int threads) {
+  const int64_t most = ((cols_out + 7) / 8 * groups + threads - 1) / threads, want = sm_count_current() / ctas;
+  return (unsigned)(want < 1 ? 1 : want < most ? want : most);
+}
 // Row groups of a CTA: enough for its threads to have a unit of columns each, within the tile's bytes and the rows.
 static int groups_of(int rb, int64_t rows, int64_t cols_in, int64_t cols_out) {
   const int64_t units = (cols_out + 7) / 8, one = rb ? (cols_in + 1) / 2 * 4 * rb : 1;
@@ -883,7 +1024,7 @@ extern "C" nm_status nm_experts_gather(const uint16_t* X, int64_t ldx, int64_t K
   p.index = source;
   p.vec = al16(source);
   const int64_t beside = (S + 7) / 8 * 16;
-  const int lrb = mv::lng::gather_rows(T, K, beside);
+  const int lrb = mv::lng::gather_rows(T, S, K, beside);
   if (lrb) {
     const size_t smem = (size_t)(2 * ((T + 7) / 8 * 16 * lrb) + beside);
     const unsigned grid = mv::lng::grid_of(K, lrb);
@@ -892,11 +1033,12 @@ extern "C" nm_status nm_experts_gather(const uint16_t* X, int64_t ldx, int64_t K
                                      : mv::lng::launch_gather<1>(p, grid, smem, (cudaStream_t)stream);
     return e == cudaSuccess ? NM_OK : cuda_fail(e, "gather launch");
   }
-  const int rb = mv::rows_of_word(T, K, 0), step = rb ? rb : 1;
+  const int rb = mv::rows_of_word(T, S, K, 0), step = rb ? rb : 1;
   p.groups = mv::groups_of(rb, K, T, S);
   const int64_t ctas = (K + (int64_t)p.groups * step - 1) / ((int64_t)p.groups * step);
-  const cudaError_t e = mv::dispatch<mv::Gather>(rb, p, dim3((unsigned)ctas), (size_t)((T + 1) / 2 * 4 * rb * p.groups),
-                                                 (cudaStream_t)stream);
+  const int threads = mv::threads_of(S, p.groups);
+  const cudaError_t e = mv::dispatch<mv::Gather>(rb, p, dim3((unsigned)ctas, mv::shares_of(ctas, S, p.groups, threads)),
+                                                 (size_t)((T + 1) / 2 * 4 * rb * p.groups), (cudaStream_t)stream, threads);
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "gather launch");
 }
 
@@ -914,6 +1056,11 @@ extern "C" nm_status nm_experts_combine(const uint16_t* Yg, int64_t ldg, int64_t
   if (st == NM_OK) st = check_words({slot, gate}, "slot and gate");
   if (st == NM_OK) st = require_device();
   if (st != NM_OK) return st;
+  if (S == 0) {  // no columns: zeros
+    const int64_t size = dtype_bytes(y_dtype);
+    const cudaError_t e = cudaMemset2DAsync(Y, (size_t)(ldy * size), 0, (size_t)(T * size), (size_t)R, (cudaStream_t)stream);
+    return e == cudaSuccess ? NM_OK : cuda_fail(e, "zero result");
+  }
   mv::Params p{};
   p.in = Yg, p.ldin = ldg, p.cols_in = (int32_t)S;
   p.out = Y, p.ldout = ldy, p.cols_out = (int32_t)T;
@@ -921,22 +1068,27 @@ extern "C" nm_status nm_experts_combine(const uint16_t* Yg, int64_t ldg, int64_t
   p.index = slot, p.gate = gate;
   p.out_f32 = y_dtype == NM_OUT_F32;
   p.vec = al16(slot) && al16(gate) && (T % 4 == 0 || k == 1);
-  const int64_t beside = (T + 7) / 8 * 8 * (gate ? 6 : 2) * k;
-  p.depth = mv::lng::depth_of(S, R, beside, mv::lng::kCombineRows);
-  if (p.depth) {
+  const int64_t beside = 8 * (gate ? 6 : 2) * k;  // bytes a unit
+  const mv::lng::Plan plan = mv::lng::plan_of(S, (T + 7) / 8, INT32_MAX, R, beside);
+  if (plan.rows) {
     p.status = status_word_ptr();
     if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
-    static SmemLimit limit;
-    const cudaError_t e = mv::start(mv::lng::combine_kernel, limit, dim3(mv::lng::grid_of(R, mv::lng::kCombineRows)),
-                                    mv::lng::smem_of(p, beside, mv::lng::kCombineRows), p, (cudaStream_t)stream,
-                                    mv::lng::kThreads);
+    p.depth = plan.depth;
+    const dim3 grid(mv::lng::ctas_of(R, plan), (unsigned)plan.ranges);
+    const size_t smem = mv::lng::smem_of(p, plan, beside);
+    static SmemLimit one, two;
+    const cudaError_t e =
+        plan.rows == 2
+            ? mv::start(mv::lng::combine_kernel<2>, two, grid, smem, p, (cudaStream_t)stream, mv::lng::kThreads)
+            : mv::start(mv::lng::combine_kernel<1>, one, grid, smem, p, (cudaStream_t)stream, mv::lng::kThreads);
     return e == cudaSuccess ? NM_OK : cuda_fail(e, "combine launch");
   }
-  const int rb = mv::rows_of_word(S, R, 0), step = rb ? rb : 1;
+  const int rb = mv::rows_of_word(S, T, R, 0), step = rb ? rb : 1;
   p.groups = mv::groups_of(rb, R, S, T);
   const int64_t ctas = (R + (int64_t)p.groups * step - 1) / ((int64_t)p.groups * step);
-  const cudaError_t e = mv::dispatch<mv::Combine>(rb, p, dim3((unsigned)ctas), (size_t)((S + 1) / 2 * 4 * rb * p.groups),
-                                                  (cudaStream_t)stream);
+  const int threads = mv::threads_of(T, p.groups);
+  const cudaError_t e = mv::dispatch<mv::Combine>(rb, p, dim3((unsigned)ctas, mv::shares_of(ctas, T, p.groups, threads)),
+                                                  (size_t)((S + 1) / 2 * 4 * rb * p.groups), (cudaStream_t)stream, threads);
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "combine launch");
 }
 
@@ -972,30 +1124,44 @@ extern "C" nm_status nm_experts_combine_grad(const uint16_t* dY, int64_t lddy, i
   p.yg = Yg, p.ldyg = ldg;
   const int64_t units = (S + 7) / 8;
   // Long rows: ranges of the columns that a CTA's threads hold.
-  const int64_t most = (int64_t)mv::lng::kThreads * mv::lng::kGradUnits;
-  int64_t ranges = (units + most - 1) / most, per = (units + ranges - 1) / ranges;
   Staged part(s);
   cudaError_t e;
-  int64_t ctas;
-  p.depth = mv::lng::depth_of(T, R, 48 * per, mv::lng::kGradRows);
-  if (p.depth) {
+  int64_t ctas, ranges, per;
+  const mv::lng::Plan plan = mv::lng::plan_of(T, units, (int64_t)mv::lng::kThreads * mv::lng::kGradUnits, R, 48);
+  if (plan.rows) {
     p.status = status_word_ptr();
     if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
-    ctas = (int64_t)mv::lng::grid_of(R, mv::lng::kGradRows) / ranges;
-    if (ctas < 1) ctas = 1;
+    p.depth = plan.depth;
+    ctas = mv::lng::ctas_of(R, plan);
     e = part.get((size_t)ctas * units * 32);
     if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gates' sums");
     p.part = part.as<float>();
-    static SmemLimit limit;
-    e = mv::start(mv::lng::combine_grad_kernel, limit, dim3((unsigned)ctas, (unsigned)ranges),
-                  mv::lng::smem_of(p, 48 * per, mv::lng::kGradRows), p, s, mv::lng::kThreads);
+    const dim3 grid((unsigned)ctas, (unsigned)plan.ranges);
+    const size_t smem = mv::lng::smem_of(p, plan, 48);
+    static SmemLimit one, two;
+    e = plan.rows == 2 ? mv::start(mv::lng::combine_grad_kernel<2>, two, grid, smem, p, s, mv::lng::kThreads)
+                       : mv::start(mv::lng::combine_grad_kernel<1>, one, grid, smem, p, s, mv::lng::kThreads);
+  } else if (T <= 128 && units <= 65535ll * mv::kFewThreads) {
+    ranges = (units + mv::kFewThreads - 1) / mv::kFewThreads;
+    const int64_t lanes = mv::kFewThreads / (units < mv::kFewThreads ? units : mv::kFewThreads);
+    ctas = 2 * (int64_t)sm_count_current() / ranges;
+    if (ctas > (R + 2 * lanes - 1) / (2 * lanes)) ctas = (R + 2 * lanes - 1) / (2 * lanes);  // two rows a thread at least
+    if (ctas < 1) ctas = 1;
+    p.groups = (int)((R + ctas - 1) / ctas);
+    ctas = (R + p.groups - 1) / p.groups;
+    e = part.get((size_t)ctas * units * 32);
+    if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gates' sums");
+    p.part = part.as<float>();
+    e = launch_pdl(mv::combine_grad_few_kernel, dim3((unsigned)ctas, (unsigned)ranges), dim3(mv::kFewThreads), 0, s, p);
+    count_launch();
   } else {
     ranges = (units + 2047) / 2048;  // whose sums take at most 64 KB
     per = (units + ranges - 1) / ranges;
-    const int rb = mv::rows_of_word(T, R, 32 * per), step = rb ? rb : 1;
+    const int rb = mv::rows_of_word(T, kMaxDim, R, 32 * per), step = rb ? rb : 1;
     const int64_t row_groups = (R + step - 1) / step;
-    // Two CTAs to an SM, each with as many row groups as that leaves; more CTAs only write more partial sums.
-    ctas = 2 * (int64_t)sm_count_current() / ranges;
+    // A few CTAs to an SM (two with the largest tiles), each with as many row groups as that leaves; more of them only write
+    // more partial sums.
+    ctas = (units <= 256 ? 8 : units <= 512 ? 4 : 2) * (int64_t)sm_count_current() / ranges;
     if (ctas < 1) ctas = 1;
     if (ctas > row_groups) ctas = row_groups;
     p.groups = (int)((row_groups + ctas - 1) / ctas);
@@ -1004,7 +1170,7 @@ extern "C" nm_status nm_experts_combine_grad(const uint16_t* dY, int64_t lddy, i
     if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the gates' sums");
     p.part = part.as<float>();
     e = mv::dispatch<mv::CombineGrad>(rb, p, dim3((unsigned)ctas, (unsigned)ranges),
-                                      (size_t)(32 * per + (T + 1) / 2 * 4 * rb), s);
+                                      (size_t)(32 * per + (T + 1) / 2 * 4 * rb), s, units <= 256 ? 256 : mv::kThreads);
   }
   if (e == cudaSuccess) {
     const int64_t n = (int64_t)k * T, most_of = n > S ? n : S;

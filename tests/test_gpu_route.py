@@ -175,7 +175,7 @@ MOVES = [  # rows, T, k, experts
     (1, 1, 1, 1), (3, 5, 2, 4), (17, 16, 6, 64), (64, 33, 2, 8), (129, 1000, 3, 8), (6, 9001, 2, 16), (5, 30000, 1, 8),
     (2, 60001, 1, 4), (3, 110001, 2, 8), (640, 7, 1, 3), (4096, 2, 2, 8),
     (1800, 1001, 3, 8), (905, 5003, 3, 16), (449, 16001, 1, 8), (1337, 8200, 2, 64), (891, 20000, 1, 4), (450, 33000, 1, 8),
-    (470, 2100, 8, 32),
+    (470, 2100, 8, 32), (460, 16400, 2, 8), (300, 5000, 8, 64), (200, 16390, 8, 16), (5, 16001, 8, 16),
 ]
 
 
