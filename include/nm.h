@@ -612,8 +612,8 @@ NM_API nm_status nm_experts_sddmm(const uint32_t* meta, int n, int m, int64_t E,
 
 /*
  * The router of such a layer.  Logits are E x T (experts x tokens, bf16 or fp32
- * by dtype, row stride ld >= T, 16-byte rows), 1 <= k <= 16 (NM_ERR_UNSUPPORTED
- * above), k <= E <= 1024, k * T < 2^31.
+ * by dtype, any row stride ld >= T, aligned to their elements), 1 <= k <= 16
+ * (NM_ERR_UNSUPPORTED above), k <= E <= 1024, k * T < 2^31.
  *
  * nm_experts_route: every token's k experts of largest logits, in descending
  *   order, ties to the lower expert, a NaN above every number.  A logit of -inf

@@ -1108,8 +1108,9 @@ extern "C" nm_status nm_experts_combine_grad(const uint16_t* dY, int64_t lddy, i
     if (st == NM_OK) st = check_matrix(dYg, lddg, S, 2, "dYg");
   }
   if (st == NM_OK) st = check_words({slot, source, gate, dgate}, "slot, source, gate and dgate");
-  if (st == NM_OK) st = require_device();
   if (st != NM_OK || T == 0) return st;
+  st = require_device();
+  if (st != NM_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   if (S == 0 || R == 0) {
     const cudaError_t e = cudaMemsetAsync(dgate, 0, (size_t)k * T * 4, s);

@@ -368,6 +368,14 @@ static cudaError_t launch_route(const Params& p, int k, int warps, cudaStream_t 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Logits are read and written element by element: rows of any stride.
+static nm_status check_logits(const void* p, int64_t ld, int64_t T, int dtype, const char* name) {
+  if (!p) return fail(NM_ERR_INVALID_ARG, "%s is null", name);
+  if (ld < T) return fail(NM_ERR_INVALID_ARG, "ld of %s < T", name);
+  if (!aligned_to(p, (uintptr_t)dtype_bytes(dtype))) return fail(NM_ERR_MISALIGNED, "%s is not aligned to its elements", name);
+  return NM_OK;
+}
+
 static nm_status check(int64_t E, int64_t T, int64_t k) {
   if (E < 0 || T < 0) return fail(NM_ERR_INVALID_ARG, "negative dimension");
   if (E < 1) return fail(NM_ERR_INVALID_ARG, "no experts to choose from");
@@ -393,7 +401,7 @@ extern "C" nm_status nm_experts_route(const void* logits, int64_t ld, nm_out_dty
   if (!offsets) return fail(NM_ERR_INVALID_ARG, "offsets is null");
   if (T > 0 && (!expert || !gate || !slot || !source))
     return fail(NM_ERR_INVALID_ARG, "expert, gate, slot or source is null");
-  st = T > 0 ? check_matrix(logits, ld, T, dtype_bytes(dtype), "logits") : NM_OK;
+  st = T > 0 ? route::check_logits(logits, ld, T, dtype, "logits") : NM_OK;
   if (st == NM_OK) st = check_words({expert, gate, slot, source, offsets}, "expert, gate, slot, source and offsets");
   if (st == NM_OK) st = require_device();
   if (st != NM_OK) return st;
@@ -438,8 +446,8 @@ extern "C" nm_status nm_experts_route_grad(const void* logits, int64_t ld, nm_ou
   if (!dtype_ok(dtype)) return fail(NM_ERR_INVALID_ARG, "bad logits dtype");
   if (T == 0) return NM_OK;
   if (!expert || !gate || !dgate) return fail(NM_ERR_INVALID_ARG, "expert, gate or dgate is null");
-  st = check_matrix(logits, ld, T, dtype_bytes(dtype), "logits");
-  if (st == NM_OK) st = check_matrix(dlogits, lddl, T, dtype_bytes(dtype), "dlogits");
+  st = route::check_logits(logits, ld, T, dtype, "logits");
+  if (st == NM_OK) st = route::check_logits(dlogits, lddl, T, dtype, "dlogits");
   if (st == NM_OK) st = check_words({expert, gate, dgate}, "expert, gate and dgate");
   if (st == NM_OK) st = require_device();
   if (st != NM_OK) return st;

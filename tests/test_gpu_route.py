@@ -111,6 +111,17 @@ def test_route_nowhere():
     assert none[0].shape == (2, 0) and none[4].tolist() == [0] * 5
 
 
+def test_route_rows_of_any_stride():
+    g = torch.Generator(device=DEV).manual_seed(2)
+    wide = torch.randn((9, 51), generator=g, device=DEV)
+    for dtype in (BF, F32):
+        l = wide.to(dtype)[:, 1:46]
+        got, want = check_route(l, 3, False)
+        dgate = torch.randn((3, 45), generator=g, device=DEV)
+        a = nm.experts_route_grad(l, got[0], got[1], dgate, renorm=False)
+        assert torch.equal(a, nm.experts_route_grad(padded(l, dtype), got[0], got[1], dgate, renorm=False))
+
+
 def test_route_many_tokens():
     """More groups of tokens than one pass over the counts takes at a time: a permutation, sorted, with the right counts."""
     g = torch.Generator(device=DEV).manual_seed(3)
