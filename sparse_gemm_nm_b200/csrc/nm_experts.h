@@ -40,6 +40,7 @@ constexpr int64_t kSlotFloats = 256 * kSlotCols;
 // Gradient of the survivors: dV_e[r][j] = sum over expert e's columns s of dY[r][s] X[k_j][s].
 struct ExpertsGradParams {
   CUtensorMap tm_a, tm_b;  // dY R x S and X K x S, box {64, 64}, 128B swizzle
+  CUtensorMap tm_dv;       // dV {K / 2, R, E} in 16-bit units (fp32: K), box {64, 32, 1}, 128B swizzle
   const int32_t* offsets;
   const uint32_t* meta;
   void* dV;

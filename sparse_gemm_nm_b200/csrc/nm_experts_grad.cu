@@ -302,14 +302,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
 
 // ------------------------------------------------------------ survivors' gradient
 namespace grpv {
-constexpr int kThreads = 256;  // warp 0 copies, 1 MMA, 2, 3 columns outside the expert, 4-7 epilogue
+constexpr int kThreads = 384;  // warp 0 copies, 1 MMA, 2, 3 columns outside the expert, 4-11 epilogue
 constexpr int kStages = 3;
 constexpr uint32_t kA = 32768, kB = 32768;  // 128 rows x 128 columns each, in halves of 64 columns
 constexpr uint32_t kHalf = 16384;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr uint32_t kOffBar = kStages * (kA + kB);
+constexpr uint32_t kOffEpi = kStages * (kA + kB);
+constexpr uint32_t kOffBar = kOffEpi + 8 * kBoxBytes;
 constexpr uint32_t kSmemBytes = kOffBar + (4 * kStages + 5) * 8 + 8 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory");
 
 // The stages of one expert's reduction, from its first column rounded down.
 struct Reduction {
@@ -364,7 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], 8);
+      mbar_init(&acc_empty[a], 16);
     }
     mbar_init(spare, 1);
     *abort_flag = 0;
@@ -528,38 +530,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
     }
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
-    const int quarter = warp & 3;
-    const int64_t vcols = p.K >> 1;
+    // A warp takes 32 rows by half of the tile's columns: 64 survivors of every row, through its staging tile as one TMA
+    // store (stored by the lanes, a row each, every 16 bytes were a line of L1 of their own: 290 us of 11008 x 4096, eight
+    // experts of one column, by four warps).
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    uint8_t* box = smem + kOffEpi + (warp - 4) * kBoxBytes;
     uint32_t aph = 0;
     int acc = 0;
+    // The positions of a tile's survivors in this row: asked for a tile ahead.
+    uint32_t word[2][4], next[2][4];
+    auto positions = [&](int tile, uint32_t (&w)[2][4]) {
+      const int e = tile / per_expert, in = tile - e * per_expert, tm = in / p.tiles_n, tn = in - tm * p.tiles_n;
+      const int64_t row = (int64_t)tm * 256 + 128 * rank + quarter * 32 + lane, n0 = (int64_t)tn * 256 + 128 * half;
+      const uint32_t* mb = p.meta + e * p.meta_words + ((row >> 4) * p.meta_cblocks + (n0 >> 7)) * 64 + 4 * (row & 7);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool in_w = tile < tiles && row < p.R && n0 + 32 * c < p.K;
+        w[0][c] = in_w ? __ldcg(mb + c) : 0u;
+        w[1][c] = in_w ? __ldcg(mb + c + 32) : 0u;
+      }
+    };
+    positions(pair_id, next);
     for (int tile = pair_id; tile < tiles && ok; tile += npairs) {
       red.at(p, tile / per_expert);
       const int in = tile % per_expert, tm = in / p.tiles_n, tn = in % p.tiles_n;
-      const int64_t row = (int64_t)tm * 256 + 128 * rank + quarter * 32 + lane;
-      const int64_t n0 = (int64_t)tn * 256;
-      // The positions of this row's survivors, on their way while the products are.
-      uint32_t word[2][8];
-      const uint32_t* mb = p.meta + red.e * p.meta_words + ((row >> 4) * p.meta_cblocks + (n0 >> 7)) * 64 + 4 * (row & 7);
+      const int32_t wrow0 = tm * 256 + 128 * (int)rank + quarter * 32;
+      const int64_t row = wrow0 + lane, n0 = (int64_t)tn * 256 + 128 * half;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const bool in_w = row < p.R && n0 + 32 * c < p.K;
-        word[0][c] = in_w ? __ldcg(mb + (c >> 2) * 64 + (c & 3)) : 0u;
-        word[1][c] = in_w ? __ldcg(mb + (c >> 2) * 64 + (c & 3) + 32) : 0u;
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) word[i][c] = next[i][c];
+      positions(tile + npairs, next);
       const bool some = red.stages > 0;
       if (some) {
         ok = mbar_wait_warp(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
         if (!ok) break;
         tc_fence_after();
       }
-      const uint32_t t_addr = tmem_base + 256u * (uint32_t)acc + ((uint32_t)(quarter * 32) << 16);
+      const uint32_t t_addr = tmem_base + 256u * (uint32_t)acc + 128u * (uint32_t)half + ((uint32_t)(quarter * 32) << 16);
       const int sh = 16 * (int)((row >> 3) & 1);
-      const int64_t out0 = ((int64_t)red.e * p.R + row) * vcols;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int64_t col0 = n0 + 32 * c;
-        if (col0 >= p.K) break;  // the same for all lanes
-        uint32_t v[32];
+      auto take = [&](int c, uint32_t (&v)[32]) {
         if (some) {
           tmem_ld_32x32b_x32(t_addr + c * 32, v);
           tc_wait_ld();
@@ -567,25 +577,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = 0u;
         }
-        if (row >= p.R) continue;
-        const bool both = col0 + 32 <= p.K;  // or 16 of the columns
-        const int64_t at = out0 + (col0 >> 1);
-        if (p.out_f32) {
-          float o[16];
+      };
+      auto stage = [&](int unit, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
+        *reinterpret_cast<uint4*>(box + lane * 128 + ((unit ^ (lane & 7)) << 4)) = make_uint4(x, y, z, u);
+      };
+      auto free_box = [&] {
+        if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read it
+        __syncwarp();
+      };
+      auto send = [&](int32_t x) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && wrow0 < p.R && n0 < p.K) {
+          tma_store_3d(&p.tm_dv, box, x, wrow0, red.e);
+          bulk_commit_group();
+        }
+      };
+      auto release = [&] {
+        if (!some) return;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
+        aph ^= 1u << acc;
+        acc ^= 1;
+      };
+      if (p.out_f32) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t nib = (word[i >> 2][c] >> (sh + 4 * (i & 3))) & 0xFu;
-            const uint32_t p0 = nib & 3u, p1 = nib >> 2;
-            const float a0 = __uint_as_float(v[4 * i]), a1 = __uint_as_float(v[4 * i + 1]);
-            const float a2 = __uint_as_float(v[4 * i + 2]), a3 = __uint_as_float(v[4 * i + 3]);
-            o[2 * i] = p0 == 0 ? a0 : (p0 == 1 ? a1 : a2);
-            o[2 * i + 1] = p1 == 3 ? a3 : (p1 == 2 ? a2 : a1);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          take(c, v);
+          if (c == 3) release();
+          if (!(c & 1)) free_box();
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t nib = (word[i >> 2][c] >> (sh + 4 * ((i + j) & 3))) & 0xFu;
+              const uint32_t p0 = nib & 3u, p1 = nib >> 2;
+              const uint32_t* g = v + 4 * (i + j);
+              o[2 * j] = p0 == 0 ? g[0] : (p0 == 1 ? g[1] : g[2]);
+              o[2 * j + 1] = p1 == 3 ? g[3] : (p1 == 2 ? g[2] : g[1]);
+            }
+            stage(4 * (c & 1) + (i >> 1), o[0], o[1], o[2], o[3]);
           }
-          float4* y = reinterpret_cast<float4*>(static_cast<float*>(p.dV) + at);
+          if (c & 1) send((int32_t)n0 + 64 * (c >> 1));  // 32 survivors a box, two 16-bit units each
+        }
+      } else {
+        free_box();
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < 2 || both) y[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        } else {
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          take(c, v);
+          if (c == 3) release();
           // Rounded first: one byte permutation of a group's four values then picks both survivors (position q is the
           // bytes 2q and 2q + 1).
           uint32_t o[8];
@@ -596,19 +640,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
             o[i] = __byte_perm(pack_bf16x2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
                                pack_bf16x2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), pick);
           }
-          uint4* y = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dV) + at);
-          y[0] = make_uint4(o[0], o[1], o[2], o[3]);
-          if (both) y[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          stage(2 * c, o[0], o[1], o[2], o[3]);
+          stage(2 * c + 1, o[4], o[5], o[6], o[7]);
         }
-      }
-      if (some) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
-        aph ^= 1u << acc;
-        acc ^= 1;
+        send((int32_t)(n0 >> 1));
       }
     }
+    if (lane == 0) bulk_wait_group<0>();  // every store of this warp has landed
   }
 
   // -------------------------------------------------------------- teardown
@@ -713,6 +751,10 @@ extern "C" nm_status nm_experts_sddmm(const uint32_t* meta, int n, int m, int64_
   if (!p.status) return fail(NM_ERR_CUDA, "device status word is unavailable");
   st = make_tmap(&p.tm_a, dY, (uint64_t)S, (uint64_t)R, (uint64_t)lddy * 2, 64, 64, 128, "dY");
   if (st == NM_OK) st = make_tmap(&p.tm_b, X, (uint64_t)S, (uint64_t)K, (uint64_t)ldx * 2, 64, 64, 128, "X");
+  const int64_t units = p.out_f32 ? K : K / 2;  // 16-bit units of a row
+  if (st == NM_OK)
+    st = make_tmap3(&p.tm_dv, dV, (uint64_t)units, (uint64_t)R, (uint64_t)E, (uint64_t)units * 2, (uint64_t)(R * units) * 2, 64,
+                    32, 128, "dV");
   if (st != NM_OK) return st;
   static SmemLimit limit;
   cudaError_t e = limit.raise(experts_dv_kernel, grpv::kSmemBytes);
