@@ -202,11 +202,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
     const bool notes = FEW && rank == 0 && quarter == 0 && lane == 0;
     bool noted = false;
     while (ok && w.next()) {
-      if (FEW && notes && w.k0 == 0 && w.k1 < p.k_tiles) {
-        const Shares sh(first[p.E], p.k_tiles, npairs);
-        const int last = sh.of(w.at + p.k_tiles - 1);
-        p.cuts[pair_id] = ExpertsCut{last - pair_id + 1, w.slot, w.tm * 256, w.x0, w.n, w.c0, min(w.c1, w.x0 + w.n), 0};
-        noted = true;
+      if constexpr (FEW) {
+        if (notes && note_cut(p, w, pair_id, npairs)) noted = true;
       }
       ok = mbar_wait_warp(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
       if (!ok) break;
@@ -296,8 +293,9 @@ __global__ void __launch_bounds__(256) experts_join_kernel(const __grid_constant
   }
 }
 
-// XT (S x K) = X^T (K x S), 64 x 64 a CTA.
-__global__ void __launch_bounds__(256) columns_kernel(const uint16_t* X, int64_t ldx, int32_t K, int32_t S, uint16_t* XT) {
+// XT (S rows of `pitch`, an even number) = X^T (K x S), 64 x 64 a CTA.
+__global__ void __launch_bounds__(256) columns_kernel(const uint16_t* X, int64_t ldx, int32_t K, int32_t S, uint16_t* XT,
+                                                      int64_t pitch) {
   __shared__ uint16_t tile[64][66];
   const int32_t k0 = (int32_t)blockIdx.x * 64, s0 = (int32_t)blockIdx.y * 64;
   const int wide = min(64, S - s0), deep = min(64, K - k0), two = (wide + 1) >> 1;
@@ -315,7 +313,7 @@ __global__ void __launch_bounds__(256) columns_kernel(const uint16_t* X, int64_t
   for (int i = threadIdx.x; i < wide * 32; i += 256) {
     const int s = i >> 5, k = (i & 31) * 2;
     if (k < deep)
-      *reinterpret_cast<uint32_t*>(XT + (int64_t)(s0 + s) * K + k0 + k) = *reinterpret_cast<const uint32_t*>(&tile[s][k]);
+      *reinterpret_cast<uint32_t*>(XT + (s0 + s) * pitch + k0 + k) = *reinterpret_cast<const uint32_t*>(&tile[s][k]);
   }
 }
 
@@ -330,32 +328,33 @@ static cudaError_t launch_experts(const ExpertsParams& p, int pairs, cudaStream_
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Few columns: laid out with K contiguous first, then every pair an equal share of the stages, then the tiles cut by the
-// shares joined.
-static nm_status run_few(ExpertsParams& p, const uint16_t* X, int64_t ldx, int64_t K, cudaStream_t stream) {
-  const int pairs = sm_count_current() / 2;
+nm_status stage_few(ExpertsParams& p, const uint16_t* X, int64_t ldx, int64_t K, Staged& staged, cudaStream_t stream) {
+  const int64_t pairs = sm_count_current() / 2, pitch = (K + 7) / 8 * 8;
   Parts parts;
-  const int64_t at_parts = parts.take((int64_t)pairs * 2 * kSlotFloats * 4), at_x = parts.take(K * p.S * 2),
-                at_cuts = parts.take((int64_t)pairs * sizeof(ExpertsCut));
-  Staged staged(stream);
+  const int64_t at_parts = parts.take(pairs * 2 * kSlotFloats * 4), at_x = parts.take(pitch * p.S * 2),
+                at_cuts = parts.take(pairs * (int64_t)sizeof(ExpertsCut));
   cudaError_t e = staged.get(parts.size());
   if (e != cudaSuccess) return cuda_fail(e, "staging buffer of a grouped product");
   p.parts = staged.as<float>(at_parts);
   p.cuts = staged.as<ExpertsCut>(at_cuts);
   uint16_t* XT = staged.as<uint16_t>(at_x);
-  nm_status st = make_tmap(&p.tm_x, XT, (uint64_t)K, (uint64_t)p.S, (uint64_t)K * 2, 64, 16, 128, "X (K contiguous)");
+  nm_status st = make_tmap(&p.tm_x, XT, (uint64_t)K, (uint64_t)p.S, (uint64_t)pitch * 2, 64, 16, 128, "X (K contiguous)");
   if (st != NM_OK) return st;
   e = launch_pdl(columns_kernel, dim3((unsigned)((K + 63) / 64), (unsigned)((p.S + 63) / 64)), dim3(256), 0, stream, X, ldx,
-                 (int32_t)K, p.S, XT);
+                 (int32_t)K, p.S, XT, pitch);
   count_launch();
-  if (e == cudaSuccess) e = launch_experts<128, 2, true>(p, pairs, stream);
-  if (e == cudaSuccess) {
-    e = launch_pdl(experts_join_kernel, dim3((unsigned)pairs, 256 / kJoinRows), dim3(256), 0, stream, p);
-    count_launch();
-    if (e == cudaSuccess) e = cudaGetLastError();
-  }
+  if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "grouped product launch");
 }
+
+nm_status join_few(const ExpertsParams& p, cudaStream_t stream) {
+  cudaError_t e = launch_pdl(experts_join_kernel, dim3((unsigned)(sm_count_current() / 2), 256 / kJoinRows), dim3(256), 0, stream, p);
+  count_launch();
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? NM_OK : cuda_fail(e, "grouped product launch");
+}
+
+bool few_columns(int64_t E, int64_t M, int64_t S) { return S <= 96 * E && S <= M / 16 * E && (S + 63) / 64 < 65536; }
 
 int experts_pairs(const ExpertsParams& p, int max_n) {
   const int64_t most = (int64_t)p.tiles_m * (p.S / max_n + (p.E < p.S ? p.E : p.S) + 1);
@@ -422,8 +421,13 @@ extern "C" nm_status nm_experts_spmm(const uint16_t* values, const uint32_t* met
   if (st == NM_OK) st = make_meta_tmap(&p.tm_meta, meta, E * meta_row_blocks(R), meta_col_blocks(K));
   if (st == NM_OK) st = make_experts_store_map(p, Y, R, S, ldy);
   if (st != NM_OK) return st;
-  // Few columns an expert (the weights' bytes decide), and few beside the rows: laying X out anew is little then.
-  if (S <= 96 * E && S <= R / 16 * E && (S + 63) / 64 < 65536) return run_few(p, X, ldx, K, (cudaStream_t)stream);
+  if (few_columns(E, R, S)) {
+    Staged staged((cudaStream_t)stream);
+    st = stage_few(p, X, ldx, K, staged, (cudaStream_t)stream);
+    if (st != NM_OK) return st;
+    const cudaError_t e = launch_experts<128, 2, true>(p, sm_count_current() / 2, (cudaStream_t)stream);
+    return e == cudaSuccess ? join_few(p, (cudaStream_t)stream) : cuda_fail(e, "grouped product launch");
+  }
   st = make_tmap(&p.tm_x, X, (uint64_t)S, (uint64_t)K, (uint64_t)ldx * 2, 64, 64, 128, "X");
   if (st != NM_OK) return st;
   const cudaError_t e = p.k_tiles <= 8 ? launch_experts<224, 2, false>(p, experts_pairs(p, 224), (cudaStream_t)stream)

@@ -166,13 +166,15 @@ struct WideWalk {
   int e, tm;       // expert, row tile
   int32_t x0, n;   // first column, columns (a multiple of 32)
   int32_t c0, c1;  // the expert's columns
+  int k0, k1;      // stages
   const int32_t *first, *offsets;
   int32_t S;
   int E, v, id, step, known;
   ExpertCols cols;
 
-  __device__ __forceinline__ WideWalk(const int32_t* first_, const int32_t* offsets_, int E_, int32_t S_, int pair, int pairs)
-      : first(first_), offsets(offsets_), S(S_), E(E_), v(0), id(pair - pairs), step(pairs), known(-1) {}
+  __device__ __forceinline__ WideWalk(const int32_t* first_, const int32_t* offsets_, int E_, int32_t S_, int k_tiles, int pair,
+                                      int pairs)
+      : k0(0), k1(k_tiles), first(first_), offsets(offsets_), S(S_), E(E_), v(0), id(pair - pairs), step(pairs), known(-1) {}
   __device__ __forceinline__ bool next() {
     id += step;
     if (id >= first[2 * E]) return false;
@@ -290,6 +292,15 @@ __device__ __forceinline__ void store_tile(const ExpertsParams& p, int32_t x0, i
     else
       store_chunk<uint16_t>(p, v, box, x0 + c, c0, end, wrow0, lane);
   }
+}
+
+// A pair that starts a tile and does not finish it notes it for the join (one thread of the pair; false: not this one).
+__device__ __forceinline__ bool note_cut(const ExpertsParams& p, const TileWalk<true, false>& w, int pair, int pairs) {
+  if (w.k0 != 0 || w.k1 == w.k_tiles) return false;
+  const Shares sh(w.first[w.E], w.k_tiles, pairs);
+  const int last = sh.of(w.at + w.k_tiles - 1);
+  p.cuts[pair] = ExpertsCut{last - pair + 1, w.slot, w.tm * 256, w.x0, w.n, w.c0, min(w.c1, w.x0 + w.n), 0};
+  return true;
 }
 
 // Partial sums: the warp's 32 rows (row `row` of the tile on) into the slot's rows of w.n fp32.

@@ -54,6 +54,12 @@ struct ExpertsGradParams {
 
 // What the grouped products check alike.
 nm_status check_experts(int n, int m, int64_t E, int64_t R, int64_t K, int64_t S, const int32_t* offsets);
+// Few columns an expert (the weights' bytes decide), and few beside the M rows (laying them out anew is little then): the
+// columns with the reduction axis K contiguous (one launch), for a kernel that gives every SM pair an equal share of the
+// stages; then the tiles that several pairs have parts of joined.
+bool few_columns(int64_t E, int64_t M, int64_t S);
+nm_status stage_few(ExpertsParams& p, const uint16_t* X, int64_t ldx, int64_t K, Staged& staged, cudaStream_t stream);
+nm_status join_few(const ExpertsParams& p, cudaStream_t stream);
 // SM pairs for as many tiles as there can be.
 int experts_pairs(const ExpertsParams& p, int max_n);
 nm_status make_experts_store_map(ExpertsParams& p, void* Y, int64_t M, int64_t S, int64_t ldy);

@@ -33,19 +33,26 @@ namespace nmk {
 
 namespace grpt {
 constexpr int kThreads = 512;  // warps 0 raw copies, 1 MMA, 2 copies of dY, 4-7 epilogue, 8-15 expansion
-constexpr int kRaw = 4, kStages = 3;
 constexpr uint32_t kVals = 8192, kMeta = 1024;
-constexpr uint32_t kA = 16384, kB = 32768;  // 64 reduction rows x 128 and 256 columns, in strips of 8 KB
+constexpr uint32_t kA = 16384;  // 64 reduction rows x 128 columns, in strips of 8 KB
 constexpr uint32_t kStrip = 8192;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxN = 512;
+constexpr int kWide = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr uint32_t kOffB = kStages * kA, kOffVals = kOffB + kStages * kB, kOffMeta = kOffVals + kRaw * kVals;
-constexpr uint32_t kOffEpi = kOffMeta + kRaw * kMeta;
-constexpr uint32_t kOffBar = kOffEpi + 4 * kBoxBytes;
-constexpr uint32_t kOffFirst = kOffBar + (2 * kStages + 2 * kRaw + 5) * 8 + 8;
-constexpr uint32_t bytes(int E) { return kOffFirst + 4u * (uint32_t)(2 * E + 1) + 1024u; }
-static_assert(kOffFirst + 4 * (2 * kMaxExperts + 1) + 1024 <= 232448, "shared memory");
+// Many columns: up to 512 of them a tile, so that weights expanded once meet two accumulators: expansion, copies and operand
+// reads together fill shared memory's bandwidth (256 columns: 710 us for 8192 of 11008 x 4096, 512: 600 us).
+// FEW: up to 128, K-contiguous; the weights' bytes decide, so their ring is the deep one.
+template <bool FEW>
+struct Cfg {
+  static constexpr int kRaw = FEW ? 10 : 4, kStages = FEW ? 4 : 3;
+  static constexpr uint32_t kB = FEW ? 8192 : 32768;
+  static constexpr uint32_t kOffB = kStages * kA, kOffVals = kOffB + kStages * kB, kOffMeta = kOffVals + kRaw * kVals;
+  static constexpr uint32_t kOffEpi = kOffMeta + kRaw * kMeta;
+  static constexpr uint32_t kOffBar = kOffEpi + 4 * kBoxBytes;
+  static constexpr uint32_t kOffFirst = kOffBar + (2 * kStages + 2 * kRaw + 5) * 8 + 8;
+  static constexpr uint32_t bytes(int E) { return kOffFirst + 4u * (uint32_t)(2 * E + 1) + 1024u; }
+  static_assert(kOffFirst + 4 * (2 * kMaxExperts + 1) + 1024 <= 232448, "shared memory");
+};
 }  // namespace grpt
 
 // Four weights, as two words, from their two stored values and positions (nib = p0 | p1 << 2, 8 times in s0 and s1).
@@ -65,12 +72,16 @@ __device__ __forceinline__ void expand_row(const uint4& v, uint32_t pos, uint4& 
   expand_group(v.w, (p >> 12) & 24u, (p >> 14) & 24u, b.z, b.w);
 }
 
+template <bool FEW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     experts_t_kernel(const __grid_constant__ ExpertsParams p) {
   using namespace grpt;
+  using C = Cfg<FEW>;
+  constexpr int kRaw = C::kRaw, kStages = C::kStages;
+  constexpr uint32_t kB = C::kB, kOffB = C::kOffB, kOffVals = C::kOffVals, kOffMeta = C::kOffMeta;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* empty = full + kStages;
   uint64_t* raw_full = empty + kStages;
   uint64_t* raw_empty = raw_full + kRaw;
@@ -79,7 +90,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
   uint64_t* spare = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(spare + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* first = reinterpret_cast<int32_t*>(smem + kOffFirst);
+  int32_t* first = reinterpret_cast<int32_t*>(smem + C::kOffFirst);
 
   const uint32_t rank = cluster_ctarank();  // 0: leader (issues the MMAs)
   const int pair_id = blockIdx.x >> 1;
@@ -115,8 +126,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
-  pdl_gate();  // no global memory touched before this point
-  if (warp == 0) list_wide_tiles<kMaxN>(p.offsets, p.E, p.S, p.tiles_m, first, lane);
+  pdl_enter(FEW);  // no global memory touched before this point; few columns: nothing that the launch before writes
+  if (warp == 0) {
+    if (FEW)
+      list_tiles<false>(p.offsets, p.E, p.S, kSlotCols, p.tiles_m, first, lane);
+    else
+      list_wide_tiles<kWide>(p.offsets, p.E, p.S, p.tiles_m, first, lane);
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -126,7 +142,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
   const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
   const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
   bool ok = true;
-  WideWalk<kMaxN> w(first, p.offsets, p.E, p.S, pair_id, npairs);
+  auto w = [&] {
+    if constexpr (FEW)
+      return TileWalk<true, false>(first, p.offsets, p.E, p.S, kSlotCols, p.k_tiles, pair_id, npairs);
+    else
+      return WideWalk<kWide>(first, p.offsets, p.E, p.S, p.k_tiles, pair_id, npairs);
+  }();
 
   if (warp == 0) {
     // ------------------------------------------------- values and metadata
@@ -135,7 +156,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
       uint32_t ph = 0;
       while (ok && w.next()) {
         const int32_t m0 = w.tm * 256 + 128 * (int)rank;
-        for (int kt = 0; kt < p.k_tiles; ++kt) {
+        for (int kt = w.k0; kt < w.k1; ++kt) {
           ok = mbar_wait(&raw_empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           mbar_arrive_expect_tx(&raw_full[s], kVals + kMeta);
@@ -148,6 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
   } else if (warp == 2) {
     // ------------------------------------------------------------------ dY
     if (lane == 0) {
+      if (FEW) pdl_wait();  // the columns laid out by the launch before
       int s = 0;
       uint32_t ph = 0;
       while (ok && w.next()) {
@@ -155,14 +177,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
         const int32_t n0 = min(w.n, 256), n1 = w.n - n0;
         const int32_t col0 = w.x0 + (n0 >> 1) * (int32_t)rank, col1 = w.x0 + 256 + (n1 >> 1) * (int32_t)rank;
         const int s0 = n0 > 128 ? 2 : 1, s1 = (n1 + 127) >> 7;
-        for (int kt = 0; kt < p.k_tiles; ++kt) {
+        for (int kt = w.k0; kt < w.k1; ++kt) {
           ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
           if (!ok) break;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * (uint32_t)(s0 + s1) * kStrip);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], FEW ? 128u * (uint32_t)w.n : 2u * (uint32_t)(s0 + s1) * kStrip);
           uint8_t* b = smem + kOffB + s * kB;
-          for (int j = 0; j < s0; ++j) tma_load_2d_pair(b + j * kStrip, &p.tm_x, lead_full0 + 8u * s, col0 + 64 * j, kt * 64);
-          for (int j = 0; j < s1; ++j)
-            tma_load_2d_pair(b + (2 + j) * kStrip, &p.tm_x, lead_full0 + 8u * s, col1 + 64 * j, kt * 64);
+          if constexpr (FEW) {  // this CTA's columns, 16 of them a box
+            for (int i = 0; i < (n0 >> 1); i += 16)
+              tma_load_2d_pair(b + i * 128, &p.tm_x, lead_full0 + 8u * s, kt * 64, col0 + i);
+          } else {
+            for (int j = 0; j < s0; ++j)
+              tma_load_2d_pair(b + j * kStrip, &p.tm_x, lead_full0 + 8u * s, col0 + 64 * j, kt * 64);
+            for (int j = 0; j < s1; ++j)
+              tma_load_2d_pair(b + (2 + j) * kStrip, &p.tm_x, lead_full0 + 8u * s, col1 + 64 * j, kt * 64);
+          }
           if (++s == kStages) { s = 0; ph ^= 1u; }
         }
       }
@@ -179,9 +207,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t d0 = tmem_base + 256u * (uint32_t)acc, d1 = tmem_base + 256u * (uint32_t)(acc ^ 1);
-        const uint32_t idesc0 = idesc_bf16_major((uint32_t)min(w.n, 256), 256, true, true);
+        const uint32_t idesc0 = idesc_bf16_major((uint32_t)min(w.n, 256), 256, true, !FEW);
         const uint32_t idesc1 = idesc_bf16_major((uint32_t)max(w.n - 256, 32), 256, true, true);
-        for (int kt = 0; kt < p.k_tiles; ++kt) {
+        for (int kt = w.k0; kt < w.k1; ++kt) {
           ok = mbar_wait(&full[s], ph, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           tc_fence_after();
@@ -190,13 +218,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc_mma_pair(d0, smem_desc(a_addr + kk * 2048, kStrip, 1024, SWZ_128B),
-                        smem_desc(b_addr + kk * 2048, kStrip, 1024, SWZ_128B), idesc0, (kt > 0 || kk > 0) ? 1u : 0u);
+                        FEW ? smem_desc(b_addr + kk * 32, 16, 1024, SWZ_128B)
+                            : smem_desc(b_addr + kk * 2048, kStrip, 1024, SWZ_128B),
+                        idesc0, (kt > w.k0 || kk > 0) ? 1u : 0u);
           if (parts == 2) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               tc_mma_pair(d1, smem_desc(a_addr + kk * 2048, kStrip, 1024, SWZ_128B),
                           smem_desc(b_addr + 2 * kStrip + kk * 2048, kStrip, 1024, SWZ_128B), idesc1,
-                          (kt > 0 || kk > 0) ? 1u : 0u);
+                          (kt > w.k0 || kk > 0) ? 1u : 0u);
           }
           tc_commit_pair(&empty[s], 0x3);
           if (++s == kStages) { s = 0; ph ^= 1u; }
@@ -225,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     int s = 0, r = 0, turn = 0;
     uint32_t ph = 0, rph = 0;
     while (ok && w.next()) {
-      for (int kt = 0; kt < p.k_tiles; ++kt) {
+      for (int kt = w.k0; kt < w.k1; ++kt) {
         if (turn == mine) {
           ok = mbar_wait_warp(&raw_full[r], rph, abort_flag, p.status, kWaitNs);
           if (!ok) break;
@@ -266,25 +296,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
     const int quarter = warp & 3;
-    uint8_t* box = smem + kOffEpi + quarter * kBoxBytes;
+    uint8_t* box = smem + C::kOffEpi + quarter * kBoxBytes;
     uint32_t aph = 0;
     int acc = 0;
+    const bool notes = FEW && rank == 0 && quarter == 0 && lane == 0;
+    bool noted = false;
     while (ok && w.next()) {
+      if constexpr (FEW) {
+        if (notes && note_cut(p, w, pair_id, npairs)) noted = true;
+      }
       for (int32_t x = 0; x < w.n; x += 256) {  // the parts
         ok = mbar_wait_warp(&acc_full[acc], (aph >> acc) & 1u, abort_flag, p.status, kWaitNs);
         if (!ok) break;
         tc_fence_after();
         const uint32_t t_addr = tmem_base + 256u * (uint32_t)acc + ((uint32_t)(quarter * 32) << 16);
-        store_tile(p, w.x0 + x, min(w.n - x, 256), w.c0, w.c1, t_addr, box, w.tm * 256 + 128 * (int)rank + quarter * 32, lane,
-                   [&] {
-                     tc_fence_before();
-                     __syncwarp();
-                     if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
-                   });
+        const int row = 128 * (int)rank + quarter * 32;
+        auto release = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
+        };
+        bool whole = true;
+        if constexpr (FEW) {
+          whole = w.whole();
+          if (!whole) store_part(p.parts + (int64_t)(2 * pair_id + w.slot) * kSlotFloats, w, t_addr, row, lane, release);
+        }
+        if (whole)
+          store_tile(p, w.x0 + x, min(w.n - x, 256), w.c0, w.c1, t_addr, box, w.tm * 256 + row, lane, release);
         aph ^= 1u << acc;
         acc ^= 1;
       }
     }
+    if (FEW && notes && !noted) p.cuts[pair_id].pairs = 0;
     if (lane == 0) bulk_wait_group<0>();  // every store of this warp has landed
   }
 
@@ -298,6 +341,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     tmem_dealloc_pair(tmem_base, kTmemCols);
   }
   cluster_sync();  // ... and so does the deallocation: neither CTA leaves before both are through it
+  pdl_leave(FEW);
 }
 
 // ------------------------------------------------------------ survivors' gradient
@@ -698,14 +742,30 @@ extern "C" nm_status nm_experts_spmm_t(const uint16_t* values, const uint32_t* m
   st = make_tmap3(&p.tm_vals, values, (uint64_t)(K / 2), (uint64_t)R, (uint64_t)E, (uint64_t)K, (uint64_t)(R * K), 64, 64, 128,
                   "values");
   if (st == NM_OK) st = make_meta_tmap(&p.tm_meta, meta, E * meta_row_blocks(R), meta_col_blocks(K), 4);
-  if (st == NM_OK) st = make_tmap(&p.tm_x, dY, (uint64_t)S, (uint64_t)R, (uint64_t)lddy * 2, 64, 64, 128, "dY");
   if (st == NM_OK) st = make_experts_store_map(p, dX, K, S, lddx);
   if (st != NM_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  if (few_columns(E, K, S)) {
+    Staged staged(s);
+    st = stage_few(p, dY, lddy, R, staged, s);
+    if (st != NM_OK) return st;
+    static SmemLimit limit;
+    e = limit.raise(experts_t_kernel<true>, grpt::Cfg<true>::bytes(kMaxExperts));
+    if (e == cudaSuccess) {
+      e = launch_pdl(experts_t_kernel<true>, dim3(2 * (unsigned)(sm_count_current() / 2)), dim3(grpt::kThreads),
+                     grpt::Cfg<true>::bytes(p.E), s, p);
+      count_launch();
+    }
+    return e == cudaSuccess ? join_few(p, s) : cuda_fail(e, "grouped input gradient launch");
+  }
+  st = make_tmap(&p.tm_x, dY, (uint64_t)S, (uint64_t)R, (uint64_t)lddy * 2, 64, 64, 128, "dY");
+  if (st != NM_OK) return st;
   static SmemLimit limit;
-  cudaError_t e = limit.raise(experts_t_kernel, grpt::bytes(kMaxExperts));
+  e = limit.raise(experts_t_kernel<false>, grpt::Cfg<false>::bytes(kMaxExperts));
   if (e != cudaSuccess) return cuda_fail(e, "grouped input gradient");
-  const int pairs = experts_pairs(p, grpt::kMaxN);
-  e = launch_pdl(experts_t_kernel, dim3(2 * pairs), dim3(grpt::kThreads), grpt::bytes(p.E), (cudaStream_t)stream, p);
+  const int pairs = experts_pairs(p, grpt::kWide);
+  e = launch_pdl(experts_t_kernel<false>, dim3(2 * pairs), dim3(grpt::kThreads), grpt::Cfg<false>::bytes(p.E), s, p);
   count_launch();
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "grouped input gradient launch");
