@@ -9,9 +9,7 @@
 // staged for eight experts of 11008 x 4096).  Per CTA and stage of 64 reduction rows (R), TMA brings 64 x 64 stored values
 // (8 KB) and their metadata (1 KB) into a ring of their own; eight warps expand them into the MN-major operand tile (two
 // strips of 64 columns, 64 rows of 128 bytes each, 128-byte swizzle): a group of four is two byte permutations of its pair
-// of values, whose selector comes from the group's nibble.  Lanes are assigned so that loads and stores meet every bank
-// once: eight lanes take the eight 16-byte units of a row of values, and the lanes of the second strip store their two
-// units in the other order.  dY's rows arrive by TMA beside it.
+// of values, whose selectors come from a table by the group's nibble.  dY's rows arrive by TMA beside it.
 //
 // experts_dv_kernel reduces over an expert's columns, which start and end anywhere.  Its stages of 128 columns start as the
 // tiles of nm_experts.cuh do; in a tile's first and last stage a warp of each CTA zeroes the columns outside the expert (of both
@@ -49,27 +47,35 @@ struct Cfg {
   static constexpr uint32_t kOffB = kStages * kA, kOffVals = kOffB + kStages * kB, kOffMeta = kOffVals + kRaw * kVals;
   static constexpr uint32_t kOffEpi = kOffMeta + kRaw * kMeta;
   static constexpr uint32_t kOffBar = kOffEpi + 4 * kBoxBytes;
-  static constexpr uint32_t kOffFirst = kOffBar + (2 * kStages + 2 * kRaw + 5) * 8 + 8;
+  static constexpr uint32_t kOffTable = kOffBar + (2 * kStages + 2 * kRaw + 5) * 8 + 8;
+  static constexpr uint32_t kOffFirst = kOffTable + 128;
+  static_assert(kOffTable % 8 == 0, "eight bytes an entry");
   static constexpr uint32_t bytes(int E) { return kOffFirst + 4u * (uint32_t)(2 * E + 1) + 1024u; }
   static_assert(kOffFirst + 4 * (2 * kMaxExperts + 1) + 1024 <= 232448, "shared memory");
 };
 }  // namespace grpt
 
-// Four weights, as two words, from their two stored values and positions (nib = p0 | p1 << 2, 8 times in s0 and s1).
-__device__ __forceinline__ void expand_group(uint32_t v, uint32_t s0, uint32_t s1, uint32_t& lo, uint32_t& hi) {
-  // A selector byte of the four halves: 0x44 picks zeros, 0x10 the first value, 0x32 the second.
-  const uint32_t sel = 0x44444444u ^ (0x54u << s0) ^ (0x76u << s1);
-  lo = __byte_perm(v, 0u, sel);
-  hi = __byte_perm(v, 0u, sel >> 16);
+// Four weights from their two stored values, as two words, are two byte permutations; their selectors, by the group's nibble
+// p0 | p1 << 2: of a half's selector bytes 0x44 picks zeros, 0x10 the first value, 0x32 the second.
+__device__ __forceinline__ uint2 selectors(uint32_t nib) {
+  const uint32_t sel = 0x44444444u ^ (0x54u << (8u * (nib & 3u))) ^ (0x76u << (8u * (nib >> 2)));
+  return make_uint2(sel, sel >> 16);
 }
-
-// One row's 16 weights: eight values and 16 bits of positions to two 16-byte units.
-__device__ __forceinline__ void expand_row(const uint4& v, uint32_t pos, uint4& a, uint4& b) {
-  const uint32_t p = pos << 3;  // group g: 8 p0 at bits 4g + 3, 8 p1 two bits above
-  expand_group(v.x, p & 24u, (p >> 2) & 24u, a.x, a.y);
-  expand_group(v.y, (p >> 4) & 24u, (p >> 6) & 24u, a.z, a.w);
-  expand_group(v.z, (p >> 8) & 24u, (p >> 10) & 24u, b.x, b.y);
-  expand_group(v.w, (p >> 12) & 24u, (p >> 14) & 24u, b.z, b.w);
+// One row's 16 weights: eight values and, in the low 16 bits of `pos` shifted right by SHIFT, their positions, to two 16-byte
+// units.  The selectors come from a table in shared memory (16 entries: lanes meet different banks or the same word), half
+// the instructions of making them.
+template <int SHIFT>
+__device__ __forceinline__ void expand_row(const uint4& v, uint32_t pos, const uint8_t* table, uint4& a, uint4& b) {
+  auto group = [&](int g, uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const int right = SHIFT + 4 * g - 3;  // eight bytes an entry
+    const uint2 sel = *reinterpret_cast<const uint2*>(table + ((right < 0 ? pos << -right : pos >> right) & 0x78u));
+    lo = __byte_perm(w, 0u, sel.x);
+    hi = __byte_perm(w, 0u, sel.y);
+  };
+  group(0, v.x, a.x, a.y);
+  group(1, v.y, a.z, a.w);
+  group(2, v.z, b.x, b.y);
+  group(3, v.w, b.z, b.w);
 }
 
 template <bool FEW>
@@ -116,6 +122,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     fence_barrier_init();
     fence_proxy_async_smem();
   }
+  if (warp == 3 && lane < 16) reinterpret_cast<uint2*>(smem + C::kOffTable)[lane] = selectors((uint32_t)lane);
   if (warp == 2 && lane == 0) {
     tma_prefetch_desc(&p.tm_vals);
     tma_prefetch_desc(&p.tm_x);
@@ -246,11 +253,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     }
   } else if (warp >= 8) {
     // ----------------------------------------------------------- expansion
-    // Four warps to a stage, two stages at a time (one warp's loads, permutations, stores and fence take longer than a
-    // stage's MMAs).  A warp takes 16 rows: two words of metadata a lane, each of a row and its partner eight below.
-    const int q = lane & 3, h = (lane >> 2) & 1, rb = warp & 3, mine = (warp - 8) >> 2;
-    const uint32_t word_at = (uint32_t)rb * 256u + 4u * (uint32_t)(4 * ((lane >> 3) + 8 * h) + q);
-    const uint32_t u0 = (uint32_t)(4 * (q & 1) + 2 * h), swap = (uint32_t)(q >> 1);
+    // Four warps to a stage, two stages at a time (one warp's loads, permutations and stores take longer than a stage's
+    // MMAs).  A warp takes 16 rows: two words of metadata a lane, each of a row and its partner eight below.  Eight lanes
+    // take four 16-byte units of the values (a half of the columns) in two rows whose numbers differ by 5 in their bits: the
+    // swizzle then puts their units of values, and of weights (every other one of a strip), in different banks.
+    const int q = (lane & 1) + 2 * ((lane >> 3) & 1), h = (lane >> 1) & 1, rb = warp & 3, mine = (warp - 8) >> 2;
+    const int flip = (lane >> 2) & 1 ? 5 : 0, rlow = lane >> 4;
+    const uint8_t* table = smem + C::kOffTable;
+    const uint32_t u0 = (uint32_t)(4 * (q & 1) + 2 * h);
     const uint32_t out_at = (uint32_t)(q >> 1) * kStrip + (uint32_t)rb * 2048u;
     int s = 0, r = 0, turn = 0;
     uint32_t ph = 0, rph = 0;
@@ -262,12 +272,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
           uint4 out[2][2][2];  // word, row, unit
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int rr = (lane >> 3) + 4 * i;
+            const int rr = (rlow + 2 * i) ^ flip;
             const uint8_t* vals = smem + kOffVals + r * kVals + rb * 2048 + rr * 128 + (((2 * q + h) ^ rr) << 4);
-            const uint32_t word = *reinterpret_cast<const uint32_t*>(smem + kOffMeta + r * kMeta + word_at + 64 * i);
+            const uint32_t word =
+                *reinterpret_cast<const uint32_t*>(smem + kOffMeta + r * kMeta + rb * 256 + 4 * (4 * (rr + 8 * h) + q));
             const uint4 v0 = *reinterpret_cast<const uint4*>(vals), v1 = *reinterpret_cast<const uint4*>(vals + 1024);
-            expand_row(v0, word & 0xFFFFu, out[i][0][0], out[i][0][1]);
-            expand_row(v1, word >> 16, out[i][1][0], out[i][1][1]);
+            expand_row<0>(v0, word, table, out[i][0][0], out[i][0][1]);
+            expand_row<16>(v1, word, table, out[i][1][0], out[i][1][1]);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&raw_empty[r]);
@@ -275,13 +286,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
           if (!ok) break;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t rr = (uint32_t)(lane >> 3) + 4u * i;
+            const uint32_t rr = (uint32_t)((rlow + 2 * i) ^ flip);
             uint8_t* a = smem + s * kA + out_at + rr * 128u;
-            const uint32_t at0 = ((u0 + swap) ^ rr) << 4, at1 = ((u0 + (swap ^ 1u)) ^ rr) << 4;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              *reinterpret_cast<uint4*>(a + at0 + 1024 * j) = swap ? out[i][j][1] : out[i][j][0];
-              *reinterpret_cast<uint4*>(a + at1 + 1024 * j) = swap ? out[i][j][0] : out[i][j][1];
+              *reinterpret_cast<uint4*>(a + ((u0 ^ rr) << 4) + 1024 * j) = out[i][j][0];
+              *reinterpret_cast<uint4*>(a + (((u0 + 1u) ^ rr) << 4) + 1024 * j) = out[i][j][1];
             }
           }
           fence_proxy_async_smem();
