@@ -30,7 +30,7 @@
 namespace nmk {
 
 namespace grpt {
-constexpr int kThreads = 512;  // warps 0 raw copies, 1 MMA, 2 copies of dY, 4-7 epilogue, 8-15 expansion
+// Warps 0 raw copies, 1 MMA, 2 copies of dY, 4-7 epilogue, 8 on expansion.
 constexpr uint32_t kVals = 8192, kMeta = 1024;
 constexpr uint32_t kA = 16384;  // 64 reduction rows x 128 columns, in strips of 8 KB
 constexpr uint32_t kStrip = 8192;
@@ -42,7 +42,11 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // FEW: up to 128, K-contiguous; the weights' bytes decide, so their ring is the deep one.
 template <bool FEW>
 struct Cfg {
+  static constexpr int kGroups = 2;  // of four expanding warps, a stage each
+  static constexpr int kThreads = 256 + 128 * kGroups;
   static constexpr int kRaw = FEW ? 10 : 4, kStages = FEW ? 4 : 3;
+  // A group meets the same slots of the ring of values again and again, so that its parity tells it which turn it sees.
+  static_assert(kRaw % kGroups == 0, "whole turns");
   static constexpr uint32_t kB = FEW ? 8192 : 32768;
   static constexpr uint32_t kOffB = kStages * kA, kOffVals = kOffB + kStages * kB, kOffMeta = kOffVals + kRaw * kVals;
   static constexpr uint32_t kOffEpi = kOffMeta + kRaw * kMeta;
@@ -79,7 +83,7 @@ __device__ __forceinline__ void expand_row(const uint4& v, uint32_t pos, const u
 }
 
 template <bool FEW>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::Cfg<FEW>::kThreads, 1)
     experts_t_kernel(const __grid_constant__ ExpertsParams p) {
   using namespace grpt;
   using C = Cfg<FEW>;
@@ -253,8 +257,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
     }
   } else if (warp >= 8) {
     // ----------------------------------------------------------- expansion
-    // Four warps to a stage, two stages at a time (one warp's loads, permutations and stores take longer than a stage's
-    // MMAs).  A warp takes 16 rows: two words of metadata a lane, each of a row and its partner eight below.  Eight lanes
+    // Four warps to a stage, two stages at a time (one group alone takes longer than a stage's MMAs; three or four groups
+    // are no faster: 135 us with few columns, 145 and 140).  A warp takes 16 rows: two words of metadata a lane, each of a row and its partner eight below.  Eight lanes
     // take four 16-byte units of the values (a half of the columns) in two rows whose numbers differ by 5 in their bits: the
     // swizzle then puts their units of values, and of weights (every other one of a strip), in different banks.
     const int q = (lane & 1) + 2 * ((lane >> 3) & 1), h = (lane >> 1) & 1, rb = warp & 3, mine = (warp - 8) >> 2;
@@ -298,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_peer(lead_full0 + 8u * s);
         }
-        turn ^= 1;
+        if (++turn == C::kGroups) turn = 0;
         if (++s == kStages) { s = 0; ph ^= 1u; }
         if (++r == kRaw) { r = 0; rph ^= 1u; }
       }
@@ -763,7 +767,7 @@ extern "C" nm_status nm_experts_spmm_t(const uint16_t* values, const uint32_t* m
     static SmemLimit limit;
     e = limit.raise(experts_t_kernel<true>, grpt::Cfg<true>::bytes(kMaxExperts));
     if (e == cudaSuccess) {
-      e = launch_pdl(experts_t_kernel<true>, dim3(2 * (unsigned)(sm_count_current() / 2)), dim3(grpt::kThreads),
+      e = launch_pdl(experts_t_kernel<true>, dim3(2 * (unsigned)(sm_count_current() / 2)), dim3(grpt::Cfg<true>::kThreads),
                      grpt::Cfg<true>::bytes(p.E), s, p);
       count_launch();
     }
@@ -775,7 +779,7 @@ extern "C" nm_status nm_experts_spmm_t(const uint16_t* values, const uint32_t* m
   e = limit.raise(experts_t_kernel<false>, grpt::Cfg<false>::bytes(kMaxExperts));
   if (e != cudaSuccess) return cuda_fail(e, "grouped input gradient");
   const int pairs = experts_pairs(p, grpt::kWide);
-  e = launch_pdl(experts_t_kernel<false>, dim3(2 * pairs), dim3(grpt::kThreads), grpt::Cfg<false>::bytes(p.E), s, p);
+  e = launch_pdl(experts_t_kernel<false>, dim3(2 * pairs), dim3(grpt::Cfg<false>::kThreads), grpt::Cfg<false>::bytes(p.E), s, p);
   count_launch();
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "grouped input gradient launch");
