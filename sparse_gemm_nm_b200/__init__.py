@@ -23,6 +23,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
+from operator import attrgetter
 from typing import Optional, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -338,12 +340,21 @@ def nm_experts_combine_grad(dY, lddy, R, T, k, Yg, ldg, S, slot, source, gate, d
 
 def nm_clip_grads(grads, outs, sizes, dtypes, max_norm, norm, stream=None) -> None:
     """grads, outs (or None): sequences of device pointers or tensors; sizes, dtypes: sequences of numbers."""
-    n = len(grads)
-    pointer = ctypes.c_void_p * n
-    g = pointer(*[x if type(x) is int else _ptr(x) for x in grads])
-    o = g if outs is grads else None if outs is None else pointer(*[x if type(x) is int else _ptr(x) for x in outs])
-    _check(lib().nm_clip_grads(g, o, (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*dtypes), n, max_norm, _ptr(norm),
-                               _stream(stream)), "nm_clip_grads")
+    def pointers(ts):
+        return array("Q", [x if type(x) is int else _ptr(x) or 0 for x in ts])
+
+    g = pointers(grads)
+    o = g if outs is grads else None if outs is None else pointers(outs)
+    n, d = array("q", sizes), array("i", dtypes)
+    if not len(g) == len(n) == len(d) == len(g if o is None else o):
+        raise ValueError("grads, outs, sizes and dtypes must be as many")
+    _check(lib().nm_clip_grads(_at(g), _at(o), _at(n), _at(d), len(g), max_norm, _ptr(norm), _stream(stream)),
+           "nm_clip_grads")
+
+
+def _at(a) -> Optional[int]:
+    """Address of an array's elements."""
+    return None if a is None else a.buffer_info()[0]
 
 
 def nm_spmm_algo(values, meta, n, m, R, K, idx, X, ldx, T, Y, ldy, y_dtype=NM_OUT_BF16, algo=NM_ALGO_AUTO,
@@ -831,25 +842,26 @@ def clip_grads(grads, max_norm: float, out=None, stream=None):
     grads = list(grads)
     if not grads:
         raise ValueError("no gradients")
+    # One question to all tensors at a time: a step has hundreds of gradients.
+    Tensor, dtype = torch.Tensor, attrgetter("dtype")
     at, types = grads[0].get_device(), {torch.bfloat16: NM_OUT_BF16, torch.float32: NM_OUT_F32}
-    sizes = [g.numel() for g in grads]
-    kinds = [g.dtype for g in grads]
+    sizes, kinds = list(map(Tensor.numel, grads)), list(map(dtype, grads))
     every = [grads]
     if out is not None:
         every.append(list(out))
         if len(every[1]) != len(grads):
             raise ValueError(f"{len(grads)} gradients, {len(every[1])} outputs")
-        if [o.numel() for o in every[1]] != sizes or [o.dtype for o in every[1]] != kinds:
+        if list(map(Tensor.numel, every[1])) != sizes or list(map(dtype, every[1])) != kinds:
             raise ValueError("outputs must have their gradients' sizes and types")
-    for ts in every:  # (lists of one question each: a step has hundreds of gradients)
-        if not all([t.is_contiguous() for t in ts]):
+    for ts in every:
+        if not all(map(Tensor.is_contiguous, ts)):
             raise ValueError("gradients and outputs must be contiguous")
-        if at < 0 or [t.get_device() for t in ts] != [at] * len(ts):
+        if at < 0 or set(map(Tensor.get_device, ts)) != {at}:
             _require_cuda(*ts)
             raise ValueError("gradients and outputs must share one device")
     if not set(kinds) <= types.keys():
         raise ValueError(f"gradients must be bfloat16 or float32, got {set(kinds) - types.keys()}")
-    pointers = [[t.data_ptr() for t in ts] for ts in every]
+    pointers = [list(map(Tensor.data_ptr, ts)) for ts in every]
     with _On(grads[0], stream) as s:
         norm = grads[0].new_empty((), dtype=torch.float32)
         nm_clip_grads(pointers[0], pointers[-1], sizes, [types[k] for k in kinds], max_norm, norm, s)

@@ -118,6 +118,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
   if (warp == 1) {
     // ---------------------------------------------------------- MMA (leader)
     if (rank == 0 && lane == 0) {
+      // Descriptors of the first slots: their start address counts 16 bytes.
+      const uint64_t desc_a = smem_desc(smem_u32(smem), 16, 1024, SWZ_128B);
+      const uint64_t desc_b = smem_desc(smem_u32(smem + C::kOffB), FEW ? 16 : kStrip, 1024, SWZ_128B);
+      const uint64_t desc_e = smem_desc(smem_u32(smem + C::kOffE), 2048, 128, SWZ_NONE);
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;  // aph bit a: phase of accumulator a
       while (ok && w.next()) {
@@ -130,18 +134,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
           ok = mbar_wait(&full[s], ph, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + s * kA);
-          const uint32_t b_addr = smem_u32(smem + C::kOffB + s * C::kB);
+          const uint64_t ad = desc_a + (uint64_t)(s * (kA >> 4)), bd = desc_b + (uint64_t)(s * (C::kB >> 4));
           const uint32_t e_tmem = tmem_base + C::kECol + 4u * (uint32_t)s;
-          tc_cp_128x128b_pair(e_tmem, smem_desc(smem_u32(smem + C::kOffE + s * kE), 2048, 128, SWZ_NONE));
+          tc_cp_128x128b_pair(e_tmem, desc_e + (uint64_t)(s * (kE >> 4)));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ad = smem_desc(a_addr + kk * 32, 16, 1024, SWZ_128B);
-            const uint64_t bd = FEW ? smem_desc(b_addr + (kk >> 1) * 8192 + (kk & 1) * 64, 16, 1024, SWZ_128B)
-                                    : smem_desc(b_addr + kk * 4096, kStrip, 1024, SWZ_128B);
-            tc_mma_sp_pair(d_tmem, ad, bd, e_tmem + (uint32_t)(kk & 2), idesc | (uint32_t)(kk & 1),
-                           (kt > w.k0 || kk > 0) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_sp_pair(d_tmem, ad + 2u * kk, bd + (FEW ? (kk >> 1) * 512u + (kk & 1) * 4u : kk * 256u),
+                           e_tmem + (uint32_t)(kk & 2), idesc | (uint32_t)(kk & 1), (kt > w.k0 || kk > 0) ? 1u : 0u);
           tc_commit_pair(&empty[s], 0x3);
           if (++s == kStages) { s = 0; ph ^= 1u; }
         }

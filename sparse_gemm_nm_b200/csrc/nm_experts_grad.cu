@@ -209,6 +209,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::Cfg<FEW>::kThr
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA (leader)
     if (rank == 0 && lane == 0) {
+      // Descriptors of the first slots: their start address counts 16 bytes.
+      const uint64_t desc_a = smem_desc(smem_u32(smem), kStrip, 1024, SWZ_128B);
+      const uint64_t desc_b = smem_desc(smem_u32(smem + kOffB), FEW ? 16 : kStrip, 1024, SWZ_128B);
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       while (ok && w.next()) {
@@ -224,20 +227,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::Cfg<FEW>::kThr
           ok = mbar_wait(&full[s], ph, abort_flag, p.status, kWaitNs);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + s * kA);
-          const uint32_t b_addr = smem_u32(smem + kOffB + s * kB);
+          const uint64_t ad = desc_a + (uint64_t)(s * (kA >> 4)), bd = desc_b + (uint64_t)(s * (kB >> 4));
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_pair(d0, smem_desc(a_addr + kk * 2048, kStrip, 1024, SWZ_128B),
-                        FEW ? smem_desc(b_addr + kk * 32, 16, 1024, SWZ_128B)
-                            : smem_desc(b_addr + kk * 2048, kStrip, 1024, SWZ_128B),
-                        idesc0, (kt > w.k0 || kk > 0) ? 1u : 0u);
+            tc_mma_pair(d0, ad + 128u * kk, bd + (FEW ? 2u : 128u) * kk, idesc0, (kt > w.k0 || kk > 0) ? 1u : 0u);
           if (parts == 2) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_pair(d1, smem_desc(a_addr + kk * 2048, kStrip, 1024, SWZ_128B),
-                          smem_desc(b_addr + 2 * kStrip + kk * 2048, kStrip, 1024, SWZ_128B), idesc1,
-                          (kt > w.k0 || kk > 0) ? 1u : 0u);
+              tc_mma_pair(d1, ad + 128u * kk, bd + (2 * kStrip >> 4) + 128u * kk, idesc1, (kt > w.k0 || kk > 0) ? 1u : 0u);
           }
           tc_commit_pair(&empty[s], 0x3);
           if (++s == kStages) { s = 0; ph ^= 1u; }
@@ -542,6 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
     // ---------------------------------------------------------- MMA (leader)
     if (rank == 0 && lane == 0) {
       constexpr uint32_t kIdesc = idesc_bf16_major(256, 256, false, false);
+      const uint64_t desc = smem_desc(smem_u32(smem), 16, 1024, SWZ_128B);  // its start address counts 16 bytes
       int s = 0, acc = 0;
       uint32_t fph = 0, mph = 0, aph = 0;  // bit s: phase of full[s], of masked[s]
       for (int tile = pair_id; tile < tiles && ok; tile += npairs) {
@@ -557,13 +555,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
           if (!ok) break;
           (ragged ? mph : fph) ^= 1u << s;
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + s * (kA + kB));
-          const uint32_t b_addr = a_addr + kA;
+          const uint64_t ad = desc + (uint64_t)(s * ((kA + kB) >> 4)), bd = ad + (kA >> 4);
           const int step0 = red.from(kt) >> 4, steps = (red.to(kt) + 15) >> 4;
           auto step = [&](int kk) {
-            const uint32_t at = (uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u;
-            tc_mma_pair(d_tmem, smem_desc(a_addr + at, 16, 1024, SWZ_128B), smem_desc(b_addr + at, 16, 1024, SWZ_128B),
-                        kIdesc, (kt > 0 || kk > step0) ? 1u : 0u);
+            const uint32_t at = (uint32_t)(kk >> 2) * (kHalf >> 4) + (uint32_t)(kk & 3) * 2u;
+            tc_mma_pair(d_tmem, ad + at, bd + at, kIdesc, (kt > 0 || kk > step0) ? 1u : 0u);
           };
           if (steps - step0 == 8) {
 #pragma unroll
