@@ -103,7 +103,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
     tmem_relinquish_pair();
   }
   pdl_enter(FEW);  // no global memory touched before this point; few columns: nothing that the launch before writes
-  if (warp == 0) list_tiles<!FEW>(p.offsets, p.E, p.S, MAXN, p.tiles_m, first, lane);
+  if (warp == 0) list_tiles<FEW ? ON_UNITS : FEWEST_TILES>(p.offsets, p.E, p.S, MAXN, p.tiles_m, first, lane);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -113,7 +113,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
   const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
   const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
   bool ok = true;
-  TileWalk<FEW, !FEW> w(first, p.offsets, p.E, p.S, MAXN, p.k_tiles, pair_id, npairs);
+  TileWalk<FEW, FEW ? ON_UNITS : FEWEST_TILES> w(first, p.offsets, p.E, p.S, MAXN, p.k_tiles, pair_id, npairs);
 
   if (warp == 1) {
     // ---------------------------------------------------------- MMA (leader)
@@ -353,7 +353,11 @@ nm_status join_few(const ExpertsParams& p, cudaStream_t stream) {
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "grouped product launch");
 }
 
-bool few_columns(int64_t E, int64_t M, int64_t S) { return S <= 96 * E && S <= M / 16 * E && (S + 63) / 64 < 65536; }
+bool few_columns(const ExpertsParams& p, double few_us, double wide_us) {
+  if (p.S > 32 * (int64_t)p.E || p.S > (int64_t)p.M / 16 * p.E || (p.S + 63) / 64 >= 65536) return false;
+  const int64_t tiles = (int64_t)p.tiles_m * (p.E < p.S ? p.E : p.S), pairs = sm_count_current() / 2;
+  return 9. + few_us * (double)(tiles * p.k_tiles) / (double)pairs < wide_us * (double)((tiles + pairs - 1) / pairs * p.k_tiles);
+}
 
 int experts_pairs(const ExpertsParams& p, int max_n) {
   const int64_t most = (int64_t)p.tiles_m * (p.S / max_n + (p.E < p.S ? p.E : p.S) + 1);
@@ -420,7 +424,7 @@ extern "C" nm_status nm_experts_spmm(const uint16_t* values, const uint32_t* met
   if (st == NM_OK) st = make_meta_tmap(&p.tm_meta, meta, E * meta_row_blocks(R), meta_col_blocks(K));
   if (st == NM_OK) st = make_experts_store_map(p, Y, R, S, ldy);
   if (st != NM_OK) return st;
-  if (few_columns(E, R, S)) {
+  if (few_columns(p, 0.42, 0.56)) {
     Staged staged((cudaStream_t)stream);
     st = stage_few(p, X, ldx, K, staged, (cudaStream_t)stream);
     if (st != NM_OK) return st;

@@ -22,25 +22,32 @@ struct ExpertCols {
   int32_t nt;      // column tiles
 };
 
-// Offsets are clamped to the matrix, whatever they hold.  LINES: start on 128-byte lines of the activations (above).
-template <bool LINES = true>
+// Where an expert's first tile starts: on a 16-byte unit, on a 128-byte line (above), or on a line unless a unit saves
+// the second of two tiles (eight experts of 4096 x 4096, 250 columns each: 74 us, one tile from a unit 57)
+enum Start { ON_UNITS, ON_LINES, FEWEST_TILES };
+
+// Offsets are clamped to the matrix, whatever they hold.
+template <Start START = ON_LINES>
 __device__ __forceinline__ ExpertCols expert_cols(const int32_t* offsets, int e, int32_t S, int max_n) {
   ExpertCols x;
   x.c0 = min(max(__ldcg(offsets + e), 0), S);
   x.c1 = min(max(__ldcg(offsets + e + 1), x.c0), S);
-  x.a0 = x.c0 & (LINES && x.c1 - x.c0 > 64 ? ~63 : ~7);
-  const int32_t w = x.c1 > x.c0 ? x.c1 - x.a0 : 0;
-  x.nt = (w + max_n - 1) / max_n;
+  x.a0 = x.c0 & (START != ON_UNITS && x.c1 - x.c0 > 64 ? ~63 : ~7);
+  x.nt = x.c1 > x.c0 ? (x.c1 - x.a0 + max_n - 1) / max_n : 0;
+  if (START == FEWEST_TILES && x.nt == 2 && x.c1 - (x.c0 & ~7) <= max_n) {
+    x.a0 = x.c0 & ~7;
+    --x.nt;
+  }
   return x;
 }
 
 // first[e] = number of the first tile of expert e, first[E] = number of tiles.  One warp; `first` is shared memory.
-template <bool LINES = true>
+template <Start START = ON_LINES>
 __device__ __forceinline__ void list_tiles(const int32_t* offsets, int E, int32_t S, int max_n, int row_tiles, int32_t* first,
                                            int lane) {
   int32_t base = 0;
   for (int e0 = 0; e0 < E; e0 += 32) {
-    int32_t n = e0 + lane < E ? expert_cols<LINES>(offsets, e0 + lane, S, max_n).nt * row_tiles : 0;
+    int32_t n = e0 + lane < E ? expert_cols<START>(offsets, e0 + lane, S, max_n).nt * row_tiles : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int32_t up = __shfl_up_sync(0xFFFFFFFFu, n, o);
@@ -73,7 +80,7 @@ struct Shares {
   }
 };
 
-template <bool STREAM, bool LINES = true>
+template <bool STREAM, Start START = ON_LINES>
 struct TileWalk {
   int e, tm;       // expert, row tile
   int32_t x0, n;   // first column, columns (a multiple of 32)
@@ -124,7 +131,7 @@ struct TileWalk {
   __device__ __forceinline__ void tile(int id) {
     while (id >= first[e + 1]) ++e;
     if (e != known) {
-      cols = expert_cols<LINES>(offsets, e, S, max_n);
+      cols = expert_cols<START>(offsets, e, S, max_n);
       known = e;
     }
     const int in = id - first[e];
@@ -295,7 +302,7 @@ __device__ __forceinline__ void store_tile(const ExpertsParams& p, int32_t x0, i
 }
 
 // A pair that starts a tile and does not finish it notes it for the join (one thread of the pair; false: not this one).
-__device__ __forceinline__ bool note_cut(const ExpertsParams& p, const TileWalk<true, false>& w, int pair, int pairs) {
+__device__ __forceinline__ bool note_cut(const ExpertsParams& p, const TileWalk<true, ON_UNITS>& w, int pair, int pairs) {
   if (w.k0 != 0 || w.k1 == w.k_tiles) return false;
   const Shares sh(w.first[w.E], w.k_tiles, pairs);
   const int last = sh.of(w.at + w.k_tiles - 1);

@@ -54,10 +54,13 @@ struct ExpertsGradParams {
 
 // What the grouped products check alike.
 nm_status check_experts(int n, int m, int64_t E, int64_t R, int64_t K, int64_t S, const int32_t* offsets);
-// Few columns an expert (the weights' bytes decide), and few beside the M rows (laying them out anew is little then): the
-// columns with the reduction axis K contiguous (one launch), for a kernel that gives every SM pair an equal share of the
-// stages; then the tiles that several pairs have parts of joined.
-bool few_columns(int64_t E, int64_t M, int64_t S);
+// Few columns an expert: two forms.  Whole tiles of the general kernel, one launch, take wide_us a stage, and as long as the
+// pairs with the most tiles; equal shares of all stages, the columns laid out with the reduction axis K contiguous first and
+// the tiles that several pairs have parts of joined behind (three launches, 9 us more), take few_us.  Measured with one to
+// 32 columns an expert, forward / input gradient: 8 x 11008 x 4096 (tiles 4.6 / 1.7 to a pair) whole 92 to 115 / 150 us,
+// shares 79 to 87 / 138 to 147; 2 x 4096 x 11008 (0.4 / 1.2) 43 / 63 and 29 to 36 / 50 to 56; 8 x 4096 x 4096 (1.7) 41 to
+// 54 / 65 and 40 to 46 / 64 to 71; 16 x 1024 x 1024 (0.9) 17 and 23 to 28.  From 48 columns on whole tiles are faster.
+bool few_columns(const ExpertsParams& p, double few_us, double wide_us);
 nm_status stage_few(ExpertsParams& p, const uint16_t* X, int64_t ldx, int64_t K, Staged& staged, cudaStream_t stream);
 nm_status join_few(const ExpertsParams& p, cudaStream_t stream);
 // SM pairs for as many tiles as there can be.

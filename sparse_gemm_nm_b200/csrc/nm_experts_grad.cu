@@ -140,7 +140,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::Cfg<FEW>::kThr
   pdl_enter(FEW);  // no global memory touched before this point; few columns: nothing that the launch before writes
   if (warp == 0) {
     if (FEW)
-      list_tiles<false>(p.offsets, p.E, p.S, kSlotCols, p.tiles_m, first, lane);
+      list_tiles<ON_UNITS>(p.offsets, p.E, p.S, kSlotCols, p.tiles_m, first, lane);
     else
       list_wide_tiles<kWide>(p.offsets, p.E, p.S, p.tiles_m, first, lane);
   }
@@ -155,7 +155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::Cfg<FEW>::kThr
   bool ok = true;
   auto w = [&] {
     if constexpr (FEW)
-      return TileWalk<true, false>(first, p.offsets, p.E, p.S, kSlotCols, p.k_tiles, pair_id, npairs);
+      return TileWalk<true, ON_UNITS>(first, p.offsets, p.E, p.S, kSlotCols, p.k_tiles, pair_id, npairs);
     else
       return WideWalk<kWide>(first, p.offsets, p.E, p.S, p.k_tiles, pair_id, npairs);
   }();
@@ -756,7 +756,7 @@ extern "C" nm_status nm_experts_spmm_t(const uint16_t* values, const uint32_t* m
   if (st != NM_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
-  if (few_columns(E, K, S)) {
+  if (few_columns(p, 0.41, 0.44)) {
     Staged staged(s);
     st = stage_few(p, dY, lddy, R, staged, s);
     if (st != NM_OK) return st;

@@ -65,6 +65,10 @@ CASES = [
     (1, 70, 11008, [1], 0, 7),
     (9, 1300, 1024, [30, 0, 128, 127, 1, 64, 65, 2, 90], 5, 3),
     (1, 4096, 912, [61], 3, 0),
+    (2, 5000, 160, [7, 20], 1, 4),
+    (3, 700, 8192, [70, 1, 25], 0, 3),
+    (3, 6000, 704, [90, 1, 5], 9, 0),
+    (2, 333, 256, [257, 250], 7, 0),
 ]
 
 
