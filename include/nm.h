@@ -5,8 +5,9 @@
  * hybrid forms; further down, the one-call prune + GEMM, the two backward
  * products, INT8 2:4, TF32 1:2 (float32 data) and the diagonal pattern, and
  * around a pruned projection layer norm, low-rank adapters and the cross
- * entropy of a pruned output head, with their gradients, each with its own
- * conventions where they differ from the ones below.
+ * entropy of a pruned output head, and layers of pruned experts, with their
+ * gradients and the clipping of gradients, each with its own conventions where
+ * they differ from the ones below.
  *
  * Conventions shared by every call
  *  - bf16 data is passed as its 16-bit pattern (uint16_t).  All matrices are
@@ -34,19 +35,21 @@
  *    retained).  The library allocates no device memory, except stream-ordered
  *    staging buffers from its own pool in the calls that document them (the
  *    GEMMs on the two-SM path, the backward, INT8, TF32 and diagonal calls,
- *    layer norm's gradient, the adapter and the cross-entropy calls).
+ *    layer norm's gradient, the adapter, cross-entropy and expert calls, and
+ *    the clipping).
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy
  *    default stream).  Argument errors are detected on the host and returned
  *    before anything is launched.  Each successful call launches one kernel
  *    (none when the output is empty), except the GEMM calls that stage an
  *    operand first (a re-encoding and/or a gather pass; see nm_spmm) and the
- *    adapter and cross-entropy calls, which are several passes.
+ *    adapter, cross-entropy, expert and clipping calls, which may be several
+ *    passes.
  *  - Device pointers given to the GEMMs must be 16-byte aligned, and leading
  *    dimensions of X and Y must keep every row 16-byte aligned
  *    (NM_ERR_MISALIGNED otherwise).
- *    Layer norm, the adapter and the cross-entropy calls also refuse vectors
- *    and words of 32 bits that start off 4 bytes; the values of theirs may
- *    start on any element.
+ *    Layer norm, the adapter, cross-entropy, expert and clipping calls also
+ *    refuse vectors and words of 32 bits that start off 4 bytes; the values of
+ *    the adapter and cross-entropy calls may start on any element.
  *  - Waits inside the GEMM kernels are bounded (about 2 s); a kernel that gives
  *    up records it in a device status word read by nm_device_status().
  *  - Inputs are expected to be finite.  With an Inf or NaN in X the result may
@@ -589,15 +592,19 @@ NM_API nm_status nm_lora_grad(int64_t R, int64_t K, const uint16_t* dY, int64_t 
  *           belong to no expert: they are not read into any result, and results
  *           leave them as they were.
  * No column depends on another column's data, and results repeat bit for bit.
- * One launch each; nothing is staged.
+ * One launch each, nothing staged, except that nm_experts_spmm and
+ * nm_experts_spmm_t with few columns an expert (S <= 32 E at most) may give the
+ * SM pairs equal shares of the reduction instead of whole tiles: three launches,
+ * staging the columns once more, with the reduction axis contiguous, and 256 KB
+ * for every pair.
  *
  * nm_experts_spmm: Y[:, s] = W'_e X[:, s] (R x S, bf16 or fp32), as nm_spmm.
  * nm_experts_spmm_t: dX[:, s] = W'_e^T dY[:, s] (K x S, bf16 or fp32), as
  *   nm_spmm_t; the weights are expanded on their way to the tensor cores.
  * nm_experts_sddmm: dV_e = the survivors' entries of the sum over expert e's
- *   columns of dY[:, s] X[:, s]^T (E x R x K/2, bf16 or fp32), as nm_sddmm;
- *   zeros for an expert without columns.
- * Sums are fp32, rounded once.
+ *   columns of dY[:, s] X[:, s]^T (E x R x K/2, bf16 or fp32, contiguous,
+ *   16-byte aligned), as nm_sddmm; zeros for an expert without columns.
+ * Sums are fp32, rounded once; outputs must not overlap inputs.
  * Errors: as nm_spmm, nm_spmm_t and nm_sddmm.
  */
 NM_API nm_status nm_experts_spmm(const uint16_t* values, const uint32_t* meta, int n, int m, int64_t E, int64_t R,
