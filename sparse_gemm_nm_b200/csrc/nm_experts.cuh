@@ -15,7 +15,6 @@
 
 namespace nmk {
 
-
 struct ExpertCols {
   int32_t c0, c1;  // the expert's columns
   int32_t a0;      // its first tile's first column
@@ -59,9 +58,22 @@ __device__ __forceinline__ void list_tiles(const int32_t* offsets, int E, int32_
   if (lane == 0) first[0] = 0;
 }
 
+// An expert's tiles in strips of column tiles, equally wide and `most` at most; in a strip column tiles go fastest, then row
+// tiles.  The pairs running together then share a few row blocks of weights and a few column blocks: with all columns in
+// one strip 32 column tiles met two row tiles, and L2 gave the columns (one expert 11008 x 4096, 8192 columns: 359 us,
+// strips of 4, 8, 12 tiles 332, 326, 322; two of 4096 x 11008 with 8192 each 759 -> 674; input gradient in strips of 4
+// tiles of 512 columns 522 -> 501 and 1047 -> 998; experts of one strip as before).  A strip's weights come back from L2.
+__device__ __forceinline__ void tile_in_strip(int in, int row_tiles, int nt, int most, int& tm, int& tn) {
+  const int strips = (nt + most - 1) / most, wide = (nt + strips - 1) / strips;
+  const int strip = in / (row_tiles * wide);
+  in -= strip * row_tiles * wide;
+  const int across = min(nt - strip * wide, wide);
+  tm = in / across;
+  tn = strip * wide + in - tm * across;
+}
+
 // What a pair works on: tiles pair, pair + pairs, ... whole, or (STREAM) an equal share of all tiles' stages, in one piece: a
-// share may start and end inside a tile, whose other stages the neighbouring pairs have.  Column tiles go fastest, so that
-// the pairs running together share a block of weights, which streams from HBM once.
+// share may start and end inside a tile, whose other stages the neighbouring pairs have.
 constexpr int kLeastStages = 4;  // of a share
 struct Shares {
   int64_t total;  // stages of all tiles
@@ -134,9 +146,8 @@ struct TileWalk {
       cols = expert_cols<START>(offsets, e, S, max_n);
       known = e;
     }
-    const int in = id - first[e];
-    tm = in / cols.nt;
-    const int32_t tn = in - tm * cols.nt;
+    int tn;
+    tile_in_strip(id - first[e], (first[e + 1] - first[e]) / cols.nt, cols.nt, 12, tm, tn);
     c0 = cols.c0;
     c1 = cols.c1;
     x0 = cols.a0 + tn * max_n;
@@ -195,8 +206,9 @@ struct WideWalk {
     c0 = cols.c0;
     c1 = cols.c1;
     if (v < E) {
-      tm = in / whole;
-      x0 = cols.a0 + (in - tm * whole) * WIDE;
+      int tn;
+      tile_in_strip(in, (first[v + 1] - first[v]) / whole, whole, 4, tm, tn);
+      x0 = cols.a0 + tn * WIDE;
       n = WIDE;
     } else {
       tm = in;

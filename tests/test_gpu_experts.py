@@ -69,6 +69,9 @@ CASES = [
     (3, 700, 8192, [70, 1, 25], 0, 3),
     (3, 6000, 704, [90, 1, 5], 9, 0),
     (2, 333, 256, [257, 250], 7, 0),
+    # several strips of column tiles
+    (3, 300, 272, [3400, 100, 2900], 3, 5),
+    (2, 600, 1040, [6500, 2110], 0, 0),
 ]
 
 
