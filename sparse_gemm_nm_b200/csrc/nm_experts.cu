@@ -113,7 +113,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
   const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
   const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
   bool ok = true;
-  TileWalk<FEW, FEW ? ON_UNITS : FEWEST_TILES> w(first, p.offsets, p.E, p.S, MAXN, p.k_tiles, pair_id, npairs);
+  TileWalk<FEW, FEW ? ON_UNITS : FEWEST_TILES> w(first, p.offsets, p.E, p.S, MAXN, p.k_tiles, p.tiles_m, pair_id, npairs);
 
   if (warp == 1) {
     // ---------------------------------------------------------- MMA (leader)
@@ -212,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grp::kThreads, 1)
       auto release = [&] {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
+        if (lane == 0) mbar_arrive_peer(lead_acc_empty0 + 8u * (uint32_t)acc);
       };
       if constexpr (FEW) {
         if (!w.whole()) {

@@ -63,13 +63,21 @@ __device__ __forceinline__ void list_tiles(const int32_t* offsets, int E, int32_
 // one strip 32 column tiles met two row tiles, and L2 gave the columns (one expert 11008 x 4096, 8192 columns: 359 us,
 // strips of 4, 8, 12 tiles 332, 326, 322; two of 4096 x 11008 with 8192 each 759 -> 674; input gradient in strips of 4
 // tiles of 512 columns 522 -> 501 and 1047 -> 998; experts of one strip as before).  A strip's weights come back from L2.
-__device__ __forceinline__ void tile_in_strip(int in, int row_tiles, int nt, int most, int& tm, int& tn) {
-  const int strips = (nt + most - 1) / most, wide = (nt + strips - 1) / strips;
-  const int strip = in / (row_tiles * wide);
-  in -= strip * row_tiles * wide;
-  const int across = min(nt - strip * wide, wide);
+__host__ __device__ __forceinline__ int strip_width(int nt, int most) {  // nt > 0
+  if (nt <= most) return nt;
+  const int strips = (nt + most - 1) / most;
+  return (nt + strips - 1) / strips;
+}
+__device__ __forceinline__ void tile_in_strip(int in, int row_tiles, int nt, int wide, int& tm, int& tn) {
+  int first = 0, across = nt;
+  if (wide < nt) {
+    const int strip = in / (row_tiles * wide);
+    in -= strip * row_tiles * wide;
+    first = strip * wide;
+    across = min(nt - first, wide);
+  }
   tm = in / across;
-  tn = strip * wide + in - tm * across;
+  tn = first + in - tm * across;
 }
 
 // What a pair works on: tiles pair, pair + pairs, ... whole, or (STREAM) an equal share of all tiles' stages, in one piece: a
@@ -102,13 +110,14 @@ struct TileWalk {
   int64_t at, end;  // tile number, or (STREAM) stage number
   const int32_t *first, *offsets;
   int32_t S;
-  int E, max_n, k_tiles, step;
+  int E, max_n, k_tiles, step, row_tiles, wide;
   ExpertCols cols;
   int known;
 
   __device__ __forceinline__ TileWalk(const int32_t* first_, const int32_t* offsets_, int E_, int32_t S_, int max_n_,
-                                      int k_tiles_, int pair, int pairs)
-      : e(0), slot(-1), first(first_), offsets(offsets_), S(S_), E(E_), max_n(max_n_), k_tiles(k_tiles_), step(pairs), known(-1) {
+                                      int k_tiles_, int row_tiles_, int pair, int pairs)
+      : e(0), slot(-1), first(first_), offsets(offsets_), S(S_), E(E_), max_n(max_n_), k_tiles(k_tiles_), step(pairs),
+        row_tiles(row_tiles_), known(-1) {
     if (STREAM) {
       const Shares sh(first[E], k_tiles, pairs);
       at = pair < sh.parts ? sh.start(pair) : 0;
@@ -145,9 +154,10 @@ struct TileWalk {
     if (e != known) {
       cols = expert_cols<START>(offsets, e, S, max_n);
       known = e;
+      wide = strip_width(cols.nt, 12);
     }
     int tn;
-    tile_in_strip(id - first[e], (first[e + 1] - first[e]) / cols.nt, cols.nt, 12, tm, tn);
+    tile_in_strip(id - first[e], row_tiles, cols.nt, wide, tm, tn);
     c0 = cols.c0;
     c1 = cols.c1;
     x0 = cols.a0 + tn * max_n;
@@ -187,12 +197,13 @@ struct WideWalk {
   int k0, k1;      // stages
   const int32_t *first, *offsets;
   int32_t S;
-  int E, v, id, step, known;
+  int E, v, id, step, row_tiles, known;
   ExpertCols cols;
 
-  __device__ __forceinline__ WideWalk(const int32_t* first_, const int32_t* offsets_, int E_, int32_t S_, int k_tiles, int pair,
-                                      int pairs)
-      : k0(0), k1(k_tiles), first(first_), offsets(offsets_), S(S_), E(E_), v(0), id(pair - pairs), step(pairs), known(-1) {}
+  __device__ __forceinline__ WideWalk(const int32_t* first_, const int32_t* offsets_, int E_, int32_t S_, int k_tiles,
+                                      int row_tiles_, int pair, int pairs)
+      : k0(0), k1(k_tiles), first(first_), offsets(offsets_), S(S_), E(E_), v(0), id(pair - pairs), step(pairs),
+        row_tiles(row_tiles_), known(-1) {}
   __device__ __forceinline__ bool next() {
     id += step;
     if (id >= first[2 * E]) return false;
@@ -207,7 +218,7 @@ struct WideWalk {
     c1 = cols.c1;
     if (v < E) {
       int tn;
-      tile_in_strip(in, (first[v + 1] - first[v]) / whole, whole, 4, tm, tn);
+      tile_in_strip(in, row_tiles, whole, strip_width(whole, 4), tm, tn);
       x0 = cols.a0 + tn * WIDE;
       n = WIDE;
     } else {

@@ -155,9 +155,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::Cfg<FEW>::kThr
   bool ok = true;
   auto w = [&] {
     if constexpr (FEW)
-      return TileWalk<true, ON_UNITS>(first, p.offsets, p.E, p.S, kSlotCols, p.k_tiles, pair_id, npairs);
+      return TileWalk<true, ON_UNITS>(first, p.offsets, p.E, p.S, kSlotCols, p.k_tiles, p.tiles_m, pair_id, npairs);
     else
-      return WideWalk<kWide>(first, p.offsets, p.E, p.S, p.k_tiles, pair_id, npairs);
+      return WideWalk<kWide>(first, p.offsets, p.E, p.S, p.k_tiles, p.tiles_m, pair_id, npairs);
   }();
 
   if (warp == 0) {
@@ -197,10 +197,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::Cfg<FEW>::kThr
             for (int i = 0; i < (n0 >> 1); i += 16)
               tma_load_2d_pair(b + i * 128, &p.tm_x, lead_full0 + 8u * s, kt * 64, col0 + i);
           } else {
-            for (int j = 0; j < s0; ++j)
-              tma_load_2d_pair(b + j * kStrip, &p.tm_x, lead_full0 + 8u * s, col0 + 64 * j, kt * 64);
-            for (int j = 0; j < s1; ++j)
-              tma_load_2d_pair(b + (2 + j) * kStrip, &p.tm_x, lead_full0 + 8u * s, col1 + 64 * j, kt * 64);
+            const uint32_t bar = lead_full0 + 8u * s;
+            tma_load_2d_pair(b, &p.tm_x, bar, col0, kt * 64);
+            if (s0 == 2) tma_load_2d_pair(b + kStrip, &p.tm_x, bar, col0 + 64, kt * 64);
+            if (s1 >= 1) tma_load_2d_pair(b + 2 * kStrip, &p.tm_x, bar, col1, kt * 64);
+            if (s1 == 2) tma_load_2d_pair(b + 3 * kStrip, &p.tm_x, bar, col1 + 64, kt * 64);
           }
           if (++s == kStages) { s = 0; ph ^= 1u; }
         }
@@ -325,7 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::Cfg<FEW>::kThr
         auto release = [&] {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
+          if (lane == 0) mbar_arrive_peer(lead_acc_empty0 + 8u * (uint32_t)acc);
         };
         bool whole = true;
         if constexpr (FEW) {
@@ -361,6 +362,9 @@ constexpr int kThreads = 384;  // warp 0 copies, 1 MMA, 2, 3 columns outside the
 constexpr int kStages = 3;
 constexpr uint32_t kA = 32768, kB = 32768;  // 128 rows x 128 columns each, in halves of 64 columns
 constexpr uint32_t kHalf = 16384;
+// Column tiles of a strip, at most: 43 (two experts of 4096 x 11008, 8192 columns each) in strips of 8 993 us, in one
+// 1135; 16 (11008 x 4096, eight experts of 1024 columns) in strips of 8 581, in one 572.
+constexpr int kAcross = 16;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kOffEpi = kStages * (kA + kB);
@@ -447,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
   const uint32_t lead_full0 = map_to_cta(smem_u32(&full[0]), 0);
   const uint32_t lead_masked0 = map_to_cta(smem_u32(&masked[0]), 0);
   const uint32_t lead_acc_empty0 = map_to_cta(smem_u32(acc_empty), 0);
-  const int per_expert = p.tiles_m * p.tiles_n, tiles = p.E * per_expert;
+  const int per_expert = p.tiles_m * p.tiles_n, tiles = p.E * per_expert, wide = strip_width(p.tiles_n, kAcross);
   bool ok = true;
   Reduction red;
 
@@ -458,7 +462,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
       uint32_t ph = 0;
       for (int tile = pair_id; tile < tiles && ok; tile += npairs) {
         red.at(p, tile / per_expert);
-        const int in = tile % per_expert, tm = in / p.tiles_n, tn = in % p.tiles_n;
+        int tm, tn;
+        tile_in_strip(tile % per_expert, p.tiles_m, p.tiles_n, wide, tm, tn);
         const int32_t m0 = tm * 256 + 128 * (int)rank, n0 = tn * 256 + 128 * (int)rank;
         for (int kt = 0; kt < red.stages; ++kt) {
           ok = mbar_wait(&empty[s], ph ^ 1u, abort_flag, p.status, kWaitNs);
@@ -471,18 +476,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
             mbar_arrive_expect_tx(&landed[s], tx);
           else if (rank == 0)
             mbar_arrive_expect_tx(&full[s], 2u * tx);
-          for (int i = 0; i < halves; ++i) {
-            const int32_t k0 = red.a0 + kt * 128 + 64 * i;
+          const int32_t k0 = red.a0 + kt * 128;
+          // Written out for whole stages: by a loop of as many turns as there are halves, a stage's last copies were issued
+          // too late (8192 columns of 11008 x 4096 in experts of whole stages: 547 us, written out 503).
+          if (ragged) {
+            for (int i = 0; i < halves; ++i) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint8_t* to = a + i * kHalf + h * 8192;
-              if (ragged) {
-                tma_load_2d(to, &p.tm_a, &landed[s], k0, m0 + 64 * h);
-                tma_load_2d(to + kA, &p.tm_b, &landed[s], k0, n0 + 64 * h);
-              } else {
-                tma_load_2d_pair(to, &p.tm_a, lead_full0 + 8u * s, k0, m0 + 64 * h);
-                tma_load_2d_pair(to + kA, &p.tm_b, lead_full0 + 8u * s, k0, n0 + 64 * h);
+              for (int h = 0; h < 2; ++h) {
+                uint8_t* to = a + i * kHalf + h * 8192;
+                tma_load_2d(to, &p.tm_a, &landed[s], k0 + 64 * i, m0 + 64 * h);
+                tma_load_2d(to + kA, &p.tm_b, &landed[s], k0 + 64 * i, n0 + 64 * h);
               }
+            }
+          } else {
+            const uint32_t bar = lead_full0 + 8u * s;
+            auto load = [&](int i, int h) {
+              uint8_t* to = a + i * kHalf + h * 8192;
+              tma_load_2d_pair(to, &p.tm_a, bar, k0 + 64 * i, m0 + 64 * h);
+              tma_load_2d_pair(to + kA, &p.tm_b, bar, k0 + 64 * i, n0 + 64 * h);
+            };
+            load(0, 0);
+            load(0, 1);
+            if (halves == 2) {
+              load(1, 0);
+              load(1, 1);
             }
           }
           if (++s == kStages) { s = 0; ph ^= 1u; }
@@ -586,7 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
     // -------------------------------------------------------------- epilogue
     // A warp takes 32 rows by half of the tile's columns: 64 survivors of every row, through its staging tile as one TMA
     // store (stored by the lanes, a row each, every 16 bytes were a line of L1 of their own: 290 us of 11008 x 4096, eight
-    // experts of one column, by four warps).
+    // experts of one column, by four warps); with a release at cluster scope for each accumulator 174 us, without 133).
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     uint8_t* box = smem + kOffEpi + (warp - 4) * kBoxBytes;
     uint32_t aph = 0;
@@ -594,7 +611,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
     // The positions of a tile's survivors in this row: asked for a tile ahead.
     uint32_t word[2][4], next[2][4];
     auto positions = [&](int tile, uint32_t (&w)[2][4]) {
-      const int e = tile / per_expert, in = tile - e * per_expert, tm = in / p.tiles_n, tn = in - tm * p.tiles_n;
+      const int e = tile / per_expert;
+      int tm, tn;
+      tile_in_strip(tile - e * per_expert, p.tiles_m, p.tiles_n, wide, tm, tn);
       const int64_t row = (int64_t)tm * 256 + 128 * rank + quarter * 32 + lane, n0 = (int64_t)tn * 256 + 128 * half;
       const uint32_t* mb = p.meta + e * p.meta_words + ((row >> 4) * p.meta_cblocks + (n0 >> 7)) * 64 + 4 * (row & 7);
 #pragma unroll
@@ -607,7 +626,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
     positions(pair_id, next);
     for (int tile = pair_id; tile < tiles && ok; tile += npairs) {
       red.at(p, tile / per_expert);
-      const int in = tile % per_expert, tm = in / p.tiles_n, tn = in % p.tiles_n;
+      int tm, tn;
+      tile_in_strip(tile % per_expert, p.tiles_m, p.tiles_n, wide, tm, tn);
       const int32_t wrow0 = tm * 256 + 128 * (int)rank + quarter * 32;
       const int64_t row = wrow0 + lane, n0 = (int64_t)tn * 256 + 128 * half;
 #pragma unroll
@@ -651,7 +671,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpv::kThreads, 1)
         if (!some) return;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_acc_empty0 + 8u * (uint32_t)acc);
+        if (lane == 0) mbar_arrive_peer(lead_acc_empty0 + 8u * (uint32_t)acc);
         aph ^= 1u << acc;
         acc ^= 1;
       };
