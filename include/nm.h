@@ -688,7 +688,9 @@ NM_API nm_status nm_experts_combine_grad(const uint16_t* dY, int64_t lddy, int64
  * The pages train pruned networks without giving this step.
  *   grads, outs  [in] HOST arrays of `count` device pointers, each aligned to
  *           its elements (16 bytes are read faster); outs[i] may be grads[i]
- *           and must not overlap it otherwise; outs NULL: the norm alone
+ *           and overlaps no other gradient or output (NM_ERR_INVALID_ARG: one
+ *           listed twice would be scaled twice); outs NULL: the norm alone,
+ *           where a gradient listed twice counts twice
  *   sizes, dtypes [in] HOST arrays: elements and nm_out_dtype of each
  *   max_norm >= 0 (Inf: no scaling, a copy where outs differ)
  *   norm    [out] one fp32 on the device

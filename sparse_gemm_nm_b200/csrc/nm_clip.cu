@@ -7,12 +7,15 @@
 // Squares are added in fp32 over the 32 elements that a thread loads at a time and in 64 bits from there on; where those 32
 // leave the range in which that is exact enough (squares below 2^-126 or above 2^127), they are squared again in 64 bits.
 // Every CTA leaves one sum, and each CTA of the second pass adds them up in the same order, so results repeat bit for bit.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <memory>
+#include <new>
 
 #include "nm_host.h"
 #include "nm_internal.h"
@@ -254,6 +257,33 @@ static nm_status run(const void* const* grads, void* const* outs, const int64_t*
   }
   return NM_OK;
 }
+
+// An output that is also another gradient or its output would be scaled twice, or by two CTAs at once.
+static nm_status check_outs(const void* const* grads, void* const* outs, const int64_t* sizes, const int* dtypes,
+                            int64_t count) {
+  struct Range {
+    uintptr_t from, to;
+    bool out;
+  };
+  const std::unique_ptr<Range[]> r(new (std::nothrow) Range[2 * (size_t)count + 1]);
+  if (!r) return fail(NM_ERR_CUDA, "no host memory for %lld ranges", (long long)count);
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const uintptr_t g = (uintptr_t)grads[i], o = (uintptr_t)outs[i], bytes = (uintptr_t)(sizes[i] * dtype_bytes(dtypes[i]));
+    if (bytes == 0) continue;
+    r[n++] = Range{o, o + bytes, true};
+    if (g != o) r[n++] = Range{g, g + bytes, false};
+  }
+  const auto before = [](const Range& a, const Range& b) { return a.from < b.from; };
+  if (!std::is_sorted(r.get(), r.get() + n, before)) std::sort(r.get(), r.get() + n, before);
+  uintptr_t any = 0, out = 0;  // ends of the ranges so far
+  for (int64_t i = 0; i < n; ++i) {
+    if (r[i].from < (r[i].out ? any : out)) return fail(NM_ERR_INVALID_ARG, "an output overlaps another gradient or output");
+    any = std::max(any, r[i].to);
+    if (r[i].out) out = std::max(out, r[i].to);
+  }
+  return NM_OK;
+}
 }  // namespace clip
 
 }  // namespace nmk
@@ -279,7 +309,8 @@ extern "C" nm_status nm_clip_grads(const void* const* grads, void* const* outs, 
       return fail(NM_ERR_MISALIGNED, "gradient %lld is not aligned to its elements", (long long)i);
   }
   if (count >= kMaxDim / 64) return fail(NM_ERR_UNSUPPORTED, "too many gradients");
-  st = require_device();
+  if (outs) st = clip::check_outs(grads, outs, sizes, dtypes, count);
+  if (st == NM_OK) st = require_device();
   if (st != NM_OK) return st;
   return count <= 64 ? clip::run<64>(grads, outs, sizes, dtypes, count, max_norm, norm, (cudaStream_t)stream)
                      : clip::run<640>(grads, outs, sizes, dtypes, count, max_norm, norm, (cudaStream_t)stream);

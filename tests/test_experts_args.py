@@ -108,6 +108,27 @@ def test_clipping(L):
     assert L.nm_clip_grads(None, None, None, None, 2, 1.0, 16, None) == I
 
 
+def test_clipping_refuses_outputs_that_overlap(L):
+    def clip(grads, outs, sizes, types):
+        n = len(grads)
+        P = ctypes.c_void_p * n
+        return L.nm_clip_grads(P(*grads), P(*outs), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*types), n, 1.0, 16, None)
+
+    f32, bf = nm.NM_OUT_F32, nm.NM_OUT_BF16
+    for bad in (((64, 64), (64, 64), (4, 4), (f32, f32)),  # one gradient twice
+                ((64, 128), (256, 256), (4, 4), (f32, f32)),  # into one place
+                ((64, 76), (64, 76), (4, 4), (f32, f32)),  # the second starts in the first
+                ((76, 64), (76, 64), (4, 4), (f32, f32)),
+                ((64, 128), (128, 64), (1, 1), (bf, bf)),  # exchanged
+                ((64, 128), (70, 256), (4, 4), (bf, bf)),  # an output inside its own gradient
+                ((0x100000, 0x2000), (0x100000, 0x110000 - 2), (0x10000 // 4, 8), (f32, bf))):
+        assert clip(*bad) == I and b"overlap" in L.nm_last_error(), bad
+    if not torch.cuda.is_available():  # side by side, or of no elements: no refusal before the device is asked for
+        for good in (((80, 64), (80, 64), (4, 4), (f32, f32)), ((64, 64), (128, 256), (4, 4), (f32, f32)),
+                     ((64, 64), (64, 64), (4, 0), (f32, f32)), ((64, 72), (128, 136), (4, 4), (bf, bf))):
+            assert clip(*good) not in (I, A16, U, OK), good
+
+
 def test_wrappers_refuse():
     bf, i32 = torch.bfloat16, torch.int32
     X, off = torch.zeros((16, 8), dtype=bf), torch.zeros(3, dtype=i32)
