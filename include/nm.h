@@ -684,7 +684,8 @@ NM_API nm_status nm_experts_combine_grad(const uint16_t* dY, int64_t lddy, int64
  * a backward pass and the optimiser:
  *   norm = sqrt(sum over all elements of g^2),
  *   out = g * (max_norm / norm) where norm > max_norm, else g.
- * A norm that is Inf or NaN scales nothing (the caller sees it in *norm).
+ * A norm that is Inf or NaN as *norm holds it scales nothing, and so does the
+ * norm of finite gradients where it is above the largest float.
  * The pages train pruned networks without giving this step.
  *   grads, outs  [in] HOST arrays of `count` device pointers, each aligned to
  *           its elements (16 bytes are read faster); outs[i] may be grads[i]

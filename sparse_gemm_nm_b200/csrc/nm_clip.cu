@@ -203,8 +203,9 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
   for (int i = threadIdx.x; i < p.num_all; i += kThreads) d += __ldcg(p.all + i);
   const double norm = sqrt(cta_sum(d, scratch));
   if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = (float)norm;
-  // A norm that is no number (or infinite) scales nothing.
-  const float f = norm > (double)p.max_norm && norm <= DBL_MAX ? (float)((double)p.max_norm / norm) : 1.f;
+  // A norm that is no number or infinite, as the caller sees it in fp32, scales nothing.
+  const bool scales = norm > (double)p.max_norm && (float)norm <= FLT_MAX;
+  const float f = scales ? (float)((double)p.max_norm / norm) : 1.f;
   for (int32_t c = p.pieces - 1 - (int32_t)blockIdx.x; c >= 0; c -= gridDim.x) {
     const Tensor& t = p.t[tensor_of(p, c)];
     if (t.out == nullptr || (f == 1.f && t.out == t.in)) continue;
