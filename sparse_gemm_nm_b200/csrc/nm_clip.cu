@@ -108,6 +108,14 @@ __device__ __forceinline__ float element(const void* p, int64_t i) {
 }
 
 template <bool F32>
+__device__ __forceinline__ void store_element(void* p, int64_t i, float x) {
+  if (F32)
+    static_cast<float*>(p)[i] = x;
+  else
+    static_cast<uint16_t*>(p)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+
+template <bool F32>
 __device__ double piece_squares(const Tensor& t, int64_t a, int64_t b) {
   constexpr int kPer = F32 ? 4 : 8;
   double d = 0.;
@@ -186,13 +194,14 @@ __device__ void piece_scale(const Tensor& t, int64_t a, int64_t b, float f) {
     for (; k < end; k += kThreads) o[k] = scaled<F32>(v[k], f);
     i = end * kPer;
   }
-  for (i += threadIdx.x; i < b; i += kThreads) {
-    const float x = element<F32>(t.in, i) * f;
-    if (F32)
-      static_cast<float*>(t.out)[i] = x;
-    else
-      static_cast<uint16_t*>(t.out)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-  }
+  for (i += threadIdx.x; i < b; i += kThreads) store_element<F32>(t.out, i, element<F32>(t.in, i) * f);
+}
+
+// A factor below the smallest normal float, which fp32 holds in fewer bits or as zero: the product in 64 bits.
+template <bool F32>
+__device__ void piece_scale_tiny(const Tensor& t, int64_t a, int64_t b, double f) {
+  for (int64_t i = a + threadIdx.x; i < b; i += kThreads)
+    store_element<F32>(t.out, i, (float)((double)element<F32>(t.in, i) * f));
 }
 
 template <int N>
@@ -205,12 +214,16 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
   if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = (float)norm;
   // A norm that is no number or infinite, as the caller sees it in fp32, scales nothing.
   const bool scales = norm > (double)p.max_norm && (float)norm <= FLT_MAX;
-  const float f = scales ? (float)((double)p.max_norm / norm) : 1.f;
+  const double factor = scales ? (double)p.max_norm / norm : 1.;
+  const float f = (float)factor;
+  const bool tiny = f < FLT_MIN && factor > 0.;
   for (int32_t c = p.pieces - 1 - (int32_t)blockIdx.x; c >= 0; c -= gridDim.x) {
     const Tensor& t = p.t[tensor_of(p, c)];
     if (t.out == nullptr || (f == 1.f && t.out == t.in)) continue;
     const int64_t a = (int64_t)(c - t.piece) * kPiece, b = a + kPiece < t.n ? a + kPiece : t.n;
-    if (t.f32)
+    if (tiny)
+      t.f32 ? piece_scale_tiny<true>(t, a, b, factor) : piece_scale_tiny<false>(t, a, b, factor);
+    else if (t.f32)
       piece_scale<true>(t, a, b, f);
     else
       piece_scale<false>(t, a, b, f);
