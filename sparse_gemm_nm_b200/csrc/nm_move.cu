@@ -1156,7 +1156,8 @@ extern "C" nm_status nm_experts_combine_grad(const uint16_t* dY, int64_t lddy, i
     e = launch_pdl(mv::combine_grad_few_kernel, dim3((unsigned)ctas, (unsigned)ranges), dim3(mv::kFewThreads), 0, s, p);
     count_launch();
   } else {
-    ranges = (units + 2047) / 2048;  // whose sums take at most 64 KB
+    ranges = (units + 2047) / 2048;  // whose sums take at most 64 KB; up to 128 where the grid's axis ends
+    if (ranges > 65535) ranges = 65535;
     per = (units + ranges - 1) / ranges;
     const int rb = mv::rows_of_word(T, kMaxDim, R, 32 * per), step = rb ? rb : 1;
     const int64_t row_groups = (R + step - 1) / step;
