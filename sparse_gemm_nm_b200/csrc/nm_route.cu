@@ -26,7 +26,7 @@ constexpr int kMaxK = 16;
 constexpr int kMaxE = 1024;
 constexpr int kWarps = 8;        // slices of the experts, at most
 constexpr int kPlaceThreads = 512;
-constexpr int kMaxChunk = 16;    // groups of 32 tokens a CTA of place_kernel takes, at most
+constexpr int kMaxChunk = 16;    // groups of 32 tokens a CTA of place_kernel takes at a time, at most
 
 struct Params {
   const void* logits;
@@ -40,7 +40,8 @@ struct Params {
   int32_t* offsets; // E + 1
   uint8_t* counts;  // E x pitch: chosen pairs of every expert in every group of 32 tokens
   int32_t groups, pitch;
-  int32_t chunk;    // groups a CTA of place_kernel takes, a power of two
+  int32_t chunk;    // groups a CTA of place_kernel takes at a time, a power of two
+  int32_t turns;    // ... and how often
 };
 
 template <typename T>
@@ -226,17 +227,33 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constan
   }
 }
 
-// Columns of the pairs of p.chunk groups of 32 tokens a CTA: every expert's pairs in the groups before, its first column,
-// and the chunk's own groups, each from the byte counts.
-__global__ void __launch_bounds__(kPlaceThreads) place_kernel(const __grid_constant__ Params p) {
+// Columns of the pairs of p.chunk groups of 32 tokens at a time: every expert's pairs in the groups before, its first column,
+// and the chunk's own groups, each from the byte counts.  A CTA reads all counts once, so there are no more of them than run
+// together, four to an SM: beyond 16 groups for each (303104 tokens) a CTA takes p.turns chunks, one behind the other.  With
+// a CTA for every 16 groups the counts read grew with the square of the tokens: 2^26 tokens of two experts 138 ms.
+__global__ void __launch_bounds__(kPlaceThreads, 4) place_kernel(const __grid_constant__ Params p) {
   extern __shared__ int32_t smem[];
-  int32_t* start = smem;               // E + 1: total, then first column of the expert
-  int32_t* base = smem + p.E + 1;      // E x chunk: column of the expert's first pair in the group
+  int32_t* start = smem;                   // E + 1: total, then first column of the expert
+  int32_t* base = start + p.E + 1;         // E x chunk: pairs of the expert before the group
+  int32_t* so_far = base + p.E * p.chunk;  // E: before the next chunk
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g0 = (int)blockIdx.x * p.chunk;
+  const int first = (int)blockIdx.x * p.turns * p.chunk;
   pdl_gate();
-  const uint32_t part = (uint32_t)(g0 & 15);  // groups of the piece of 16 that the chunk starts in
-  uint32_t keep[4];                           // their bytes
+  // The pairs of the groups from g0 on, `before` of them before.  A warp an expert.
+  auto spread = [&](int e, int g0, int32_t before) {
+    const uint8_t* row = p.counts + (int64_t)e * p.pitch;
+    const int32_t own = lane < p.chunk && g0 + lane < p.groups ? (int32_t)__ldcg(row + g0 + lane) : 0;
+    int32_t sum = own;  // of the chunk's groups up to the lane's
+#pragma unroll
+    for (int o = 1; o < kMaxChunk; o <<= 1) {
+      const int32_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    if (lane < p.chunk) base[e * p.chunk + lane] = before + sum - own;
+    if (lane == p.chunk - 1) so_far[e] = before + sum;
+  };
+  const uint32_t part = (uint32_t)(first & 15);  // groups of the piece of 16 that the chunk starts in
+  uint32_t keep[4];                              // their bytes
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     keep[i] = part >= 4u * i + 4u ? 0xFFFFFFFFu : part <= 4u * i ? 0u : (1u << (8u * (part - 4u * i))) - 1u;
@@ -247,43 +264,47 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const __grid_const
       const uint4 u = __ldcg(reinterpret_cast<const uint4*>(row) + i);
       const uint32_t n = __dp4a(u.x, 0x01010101u, __dp4a(u.y, 0x01010101u, __dp4a(u.z, 0x01010101u, __dp4a(u.w, 0x01010101u, 0u))));
       all += n;
-      if (i < g0 / 16)
+      if (i < first / 16)
         before += n;
-      else if (i == g0 / 16)
+      else if (i == first / 16)
         before = __dp4a(u.x & keep[0], 0x01010101u, __dp4a(u.y & keep[1], 0x01010101u,
                         __dp4a(u.z & keep[2], 0x01010101u, __dp4a(u.w & keep[3], 0x01010101u, before))));
     }
-    const int32_t own = lane < p.chunk && g0 + lane < p.groups ? (int32_t)__ldcg(row + g0 + lane) : 0;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
       before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
     }
-    int32_t sum = own;  // of the chunk's groups up to the lane's
-#pragma unroll
-    for (int o = 1; o < kMaxChunk; o <<= 1) {
-      const int32_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-      if (lane >= o) sum += up;
-    }
-    if (lane < p.chunk) base[e * p.chunk + lane] = (int32_t)before + sum - own;
+    spread(e, first, (int32_t)before);
     if (lane == 0) start[e] = (int32_t)all;
   }
   __syncthreads();
   if (warp == 0) scan_exclusive(start, p.E, lane);
   __syncthreads();
-  const int32_t t0 = g0 * 32, tokens = min(p.T - t0, p.chunk * 32);
   const int shift = 5 + (31 - __clz(p.chunk));  // a row of chunk x 32 tokens for every j
-  for (int i = threadIdx.x; i < p.k << shift; i += kPlaceThreads) {
-    const int j = i >> shift, t = i & ((1 << shift) - 1);
-    if (t >= tokens) continue;
-    const int64_t at = (int64_t)j * p.T + t0 + t;
-    const int32_t e = __ldcg(p.expert + at);
-    int32_t s = -1;
-    if (e >= 0) {
-      s = start[e] + base[e * p.chunk + (t >> 5)] + __ldcg(p.slot + at);
-      p.source[s] = j * p.T + t0 + t;
+  for (int turn = 0;;) {
+    const int g0 = first + turn * p.chunk;
+    const int32_t t0 = g0 * 32, tokens = min(p.T - t0, p.chunk * 32);
+    for (int i = threadIdx.x; i < p.k << shift; i += kPlaceThreads) {
+      const int j = i >> shift, t = i & ((1 << shift) - 1);
+      if (t >= tokens) continue;
+      const int64_t at = (int64_t)j * p.T + t0 + t;
+      const int32_t e = __ldcg(p.expert + at);
+      int32_t s = -1;
+      if (e >= 0) {
+        s = start[e] + base[e * p.chunk + (t >> 5)] + __ldcg(p.slot + at);
+        p.source[s] = j * p.T + t0 + t;
+      }
+      p.slot[at] = s;
     }
-    p.slot[at] = s;
+    if (++turn == p.turns || g0 + p.chunk >= p.groups) break;
+    __syncthreads();  // all are through with this chunk's counts
+    for (int e = warp; e < p.E; e += kPlaceThreads / 32) {
+      const int32_t before = so_far[e];
+      __syncwarp();
+      spread(e, g0 + p.chunk, before);
+    }
+    __syncthreads();
   }
   if (blockIdx.x == 0)
     for (int e = threadIdx.x; e <= p.E; e += kPlaceThreads) p.offsets[e] = start[e];
@@ -410,12 +431,14 @@ extern "C" nm_status nm_experts_route(const void* logits, int64_t ld, nm_out_dty
     const cudaError_t e = cudaMemsetAsync(offsets, 0, (size_t)(E + 1) * 4, s);
     return e == cudaSuccess ? NM_OK : cuda_fail(e, "offsets");
   }
-  route::Params p{logits, ld, (int32_t)E, (int32_t)T, k, renorm, expert, gate, slot, source, offsets, nullptr, 0, 0, 1};
+  route::Params p{logits, ld, (int32_t)E, (int32_t)T, k, renorm, expert, gate, slot, source, offsets, nullptr, 0, 0, 1, 1};
   p.groups = (int32_t)((T + 31) / 32);
   p.pitch = (p.groups + 15) / 16 * 16;
   // A CTA reads all counts, so more of them only as long as there are SMs.
   p.chunk = 1;
   while (p.chunk < route::kMaxChunk && p.chunk * sm_count_current() < p.groups) p.chunk *= 2;
+  const int32_t chunks = (p.groups + p.chunk - 1) / p.chunk;
+  p.turns = (chunks + 4 * sm_count_current() - 1) / (4 * sm_count_current());
   const int warps = E >= 8 * route::kWarps ? route::kWarps : (int)((E + 7) / 8);  // eight experts a slice at least
   Staged counts(s);
   if (p.groups > 1) {
@@ -426,10 +449,10 @@ extern "C" nm_status nm_experts_route(const void* logits, int64_t ld, nm_out_dty
   cudaError_t e = dtype == NM_OUT_F32 ? route::launch_route<float>(p, k, warps, s) : route::launch_route<uint16_t>(p, k, warps, s);
   if (e == cudaSuccess && p.groups > 1) {
     static SmemLimit limit;
-    e = limit.raise(route::place_kernel, 4u * (route::kMaxE * (route::kMaxChunk + 1) + 1));
+    e = limit.raise(route::place_kernel, 4u * (route::kMaxE * (route::kMaxChunk + 2) + 1));
     if (e == cudaSuccess) {
-      e = launch_pdl(route::place_kernel, dim3((unsigned)((p.groups + p.chunk - 1) / p.chunk)), dim3(route::kPlaceThreads),
-                     (size_t)4 * (E * (p.chunk + 1) + 1), s, p);
+      e = launch_pdl(route::place_kernel, dim3((unsigned)((chunks + p.turns - 1) / p.turns)), dim3(route::kPlaceThreads),
+                     (size_t)4 * (E * (p.chunk + 2) + 1), s, p);
       count_launch();
       if (e == cudaSuccess) e = cudaGetLastError();
     }
