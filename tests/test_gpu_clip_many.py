@@ -28,3 +28,25 @@ def test_many(n, max_norm):
     keep = x.clone()
     nm.nm_clip_grads(at, at, sizes, [nm.NM_OUT_F32] * n, max_norm, norm)  # in place: the same bits
     assert torch.equal(x[mine], y[mine]) and torch.equal(x[~mine], keep[~mine])
+
+
+def test_the_norm_alone_takes_no_second_pass():
+    """One pass over the gradients, where clipping has two and writes them."""
+    x = torch.ones(1 << 28, device=DEV)
+    norm = torch.empty((), device=DEV)
+
+    def best(outs):
+        times = []
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            nm.nm_clip_grads([x], outs, [x.numel()], [nm.NM_OUT_F32], 1.0, norm)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    alone = best(None)
+    assert float(norm) == 2.0 ** 14
+    y = torch.empty_like(x)
+    assert alone < best([y]) and (y == 2.0 ** -14).all()
