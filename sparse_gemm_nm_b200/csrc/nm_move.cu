@@ -1068,7 +1068,7 @@ extern "C" nm_status nm_experts_combine(const uint16_t* Yg, int64_t ldg, int64_t
   p.index = slot, p.gate = gate;
   p.out_f32 = y_dtype == NM_OUT_F32;
   p.vec = al16(slot) && al16(gate) && (T % 4 == 0 || k == 1);
-  const int64_t beside = 8 * (gate ? 6 : 2) * k;  // bytes a unit
+  const int64_t beside = 8 * (gate ? 6 : 2) * (int64_t)k;  // bytes a unit
   const mv::lng::Plan plan = mv::lng::plan_of(S, (T + 7) / 8, INT32_MAX, R, beside);
   if (plan.rows) {
     p.status = status_word_ptr();
