@@ -664,8 +664,8 @@ NM_API nm_status nm_experts_route_grad(const void* logits, int64_t ld, nm_out_dt
  *   slot and source must name each other, as the router's do (a pair whose slot
  *   is a column that another pair's source names gets no gradient written).
  *   gate NULL for 1.  Two launches; 4 bytes staged for every column and CTA (one
- *   or two to an SM).
- * Results repeat bit for bit.
+ *   or two to an SM; up to four with 4096 columns or fewer, eight with 2048).
+ * Outputs must not overlap inputs.  Results repeat bit for bit.
  * Errors: as nm_experts_route.
  */
 NM_API nm_status nm_experts_gather(const uint16_t* X, int64_t ldx, int64_t K, int64_t T, const int32_t* source,
@@ -697,7 +697,8 @@ NM_API nm_status nm_experts_combine_grad(const uint16_t* dY, int64_t lddy, int64
  *   norm    [out] one fp32 on the device
  * The host arrays are read before the call returns.  Squares are added in 64
  * bits (in fp32 over 32 elements where that is safe), so norms of any size up
- * to the largest float come out; products are fp32, rounded once.  Two launches
+ * to the largest float come out; products are fp32, rounded once (in 64 bits
+ * where max_norm / norm is below the smallest normal float).  Two launches
  * for every 640 gradients; 8 bytes staged for every CTA.  Results repeat bit
  * for bit.
  * Errors: NM_ERR_INVALID_ARG, NM_ERR_MISALIGNED, NM_ERR_UNSUPPORTED, NM_ERR_CUDA.

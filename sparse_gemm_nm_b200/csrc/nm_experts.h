@@ -57,9 +57,13 @@ nm_status check_experts(int n, int m, int64_t E, int64_t R, int64_t K, int64_t S
 // Few columns an expert: two forms.  Whole tiles of the general kernel, one launch, take wide_us a stage, and as long as the
 // pairs with the most tiles; equal shares of all stages, the columns laid out with the reduction axis K contiguous first and
 // the tiles that several pairs have parts of joined behind (three launches, 9 us more), take few_us.  Measured with one to
-// 32 columns an expert, forward / input gradient: 8 x 11008 x 4096 (tiles 4.6 / 1.7 to a pair) whole 92 to 115 / 150 us,
-// shares 79 to 87 / 138 to 147; 2 x 4096 x 11008 (0.4 / 1.2) 43 / 63 and 29 to 36 / 50 to 56; 8 x 4096 x 4096 (1.7) 41 to
-// 54 / 65 and 40 to 46 / 64 to 71; 16 x 1024 x 1024 (0.9) 17 and 23 to 28.  From 48 columns on whole tiles are faster.
+// 32 columns an expert, forward / input gradient: 8 x 11008 x 4096 (tiles 4.6 / 1.7 to a pair) whole 84 to 107 / 147 to 149
+// us, shares 77 to 81 / 135 to 138; 2 x 4096 x 11008 (0.4 / 1.2) 41 / 61 to 63 and 29 to 30 / 47 to 48; 8 x 4096 x 4096
+// (1.7) 38 to 50 / 62 to 65 and 39 to 40 / 62 to 64; 16 x 1024 x 1024 (0.9) 9 to 13 / 15 and 16 to 17 / 22 to 23.
+// Two bounds come first, because the model knows nothing that grows with the columns (laying them out, partial sums, the
+// join): at most 32 columns an expert, and a 16th of the output's rows.  With many tiles they are right (8 x 4096 x 4096,
+// 64 columns each: whole 37 / 61, shares 45 / 68); with few tiles of long reductions they leave time behind (one expert of
+// 11008 x 4096, input gradient of 48, 128 columns: whole 77, 76 and shares 34, 41; 8000 x 144, of 16: 55 and 17).
 bool few_columns(const ExpertsParams& p, double few_us, double wide_us);
 nm_status stage_few(ExpertsParams& p, const uint16_t* X, int64_t ldx, int64_t K, Staged& staged, cudaStream_t stream);
 nm_status join_few(const ExpertsParams& p, cudaStream_t stream);
