@@ -836,7 +836,8 @@ def clip_grads(grads, max_norm: float, out=None, stream=None):
     """The norm over all gradients (a float32 tensor of no dimensions, on the device); scales them to max_norm if above.
 
     grads are contiguous tensors (bf16 or float32) of one CUDA device, scaled in place, or into the tensors of `out`;
-    an output shares no memory with another gradient or output (the same gradient twice is refused).  A norm that is Inf or NaN scales nothing.
+    an output shares no memory with another gradient or output (the same gradient twice is refused).  A norm that is Inf
+    or NaN scales nothing.
     """
     import torch
     grads = list(grads)

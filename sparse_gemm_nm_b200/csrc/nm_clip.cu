@@ -4,8 +4,9 @@
 // Bound by memory: every gradient is read twice and written once (the factor needs all of them).  The tensors' addresses and
 // sizes travel as kernel parameters, so a captured call holds no host memory and tables need no copy; both passes walk one
 // list of pieces of 16384 elements over a persistent grid, the second from its end, where the first has left what L2 holds.
-// Squares are added in fp32 over the 32 elements that a thread loads at a time and in 64 bits from there on; where those 32
-// leave the range in which that is exact enough (squares below 2^-126 or above 2^127), they are squared again in 64 bits.
+// Squares are added in fp32 over the 32 elements that a thread loads at a time and in 64 bits from there on.  Where the 32
+// add up to less than 1e-25 or more than 1e30 they are squared again in 64 bits: above 1e-25, squares below 2^-126 (1.2e-38),
+// which fp32 has in fewer bits or not at all, are 4e-12 of the sum together, and below 1e30 none has overflown.
 // Every CTA leaves one sum, and each CTA of the second pass adds them up in the same order, so results repeat bit for bit.
 #include <algorithm>
 #include <cfloat>
@@ -60,7 +61,9 @@ __device__ __forceinline__ int tensor_of(const Params<N>& p, int32_t piece) {
   return lo;
 }
 
-__device__ __forceinline__ float2 pair_of(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+__device__ __forceinline__ float2 pair_of(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
 
 // Sum of the squares of the elements in NV 16-byte units.
 template <bool F32, int NV>

@@ -347,7 +347,8 @@ nm_status stage_few(ExpertsParams& p, const uint16_t* X, int64_t ldx, int64_t K,
 }
 
 nm_status join_few(const ExpertsParams& p, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(experts_join_kernel, dim3((unsigned)(sm_count_current() / 2), 256 / kJoinRows), dim3(256), 0, stream, p);
+  const dim3 grid((unsigned)(sm_count_current() / 2), 256 / kJoinRows);
+  cudaError_t e = launch_pdl(experts_join_kernel, grid, dim3(256), 0, stream, p);
   count_launch();
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "grouped product launch");
@@ -356,7 +357,8 @@ nm_status join_few(const ExpertsParams& p, cudaStream_t stream) {
 bool few_columns(const ExpertsParams& p, double few_us, double wide_us) {
   if (p.S > 32 * (int64_t)p.E || p.S > (int64_t)p.M / 16 * p.E || (p.S + 63) / 64 >= 65536) return false;
   const int64_t tiles = (int64_t)p.tiles_m * (p.E < p.S ? p.E : p.S), pairs = sm_count_current() / 2;
-  return 9. + few_us * (double)(tiles * p.k_tiles) / (double)pairs < wide_us * (double)((tiles + pairs - 1) / pairs * p.k_tiles);
+  const double most_stages = (double)((tiles + pairs - 1) / pairs * p.k_tiles);  // of a pair's whole tiles
+  return 9. + few_us * (double)(tiles * p.k_tiles) / (double)pairs < wide_us * most_stages;
 }
 
 int experts_pairs(const ExpertsParams& p, int max_n) {

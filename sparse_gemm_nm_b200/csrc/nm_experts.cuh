@@ -174,7 +174,8 @@ __device__ __forceinline__ int32_t wide_tiles(const int32_t* offsets, int v, int
   return (v < E ? w / WIDE : (w % WIDE != 0)) * row_tiles;
 }
 template <int WIDE>
-__device__ __forceinline__ void list_wide_tiles(const int32_t* offsets, int E, int32_t S, int row_tiles, int32_t* first, int lane) {
+__device__ __forceinline__ void list_wide_tiles(const int32_t* offsets, int E, int32_t S, int row_tiles, int32_t* first,
+                                                int lane) {
   int32_t base = 0;
   for (int v0 = 0; v0 < 2 * E; v0 += 32) {
     int32_t n = v0 + lane < 2 * E ? wide_tiles<WIDE>(offsets, v0 + lane, E, S, row_tiles) : 0;
@@ -302,8 +303,8 @@ __device__ __forceinline__ void store_chunk(const ExpertsParams& p, const uint32
 // The warp's 32 rows of a tile, chunk by chunk; `release` is called after the last TMEM load.  Accumulator columns behind
 // the tile's hold what an earlier tile left there: they lie behind `end`.
 template <typename Release>
-__device__ __forceinline__ void store_tile(const ExpertsParams& p, int32_t x0, int32_t n, int32_t c0, int32_t c1, uint32_t t_addr,
-                                           uint8_t* box, int32_t wrow0, int lane, Release release) {
+__device__ __forceinline__ void store_tile(const ExpertsParams& p, int32_t x0, int32_t n, int32_t c0, int32_t c1,
+                                           uint32_t t_addr, uint8_t* box, int32_t wrow0, int lane, Release release) {
   const int32_t end = min(c1, x0 + n);
   const int step = p.out_f32 ? 32 : 64;
 #pragma unroll 1

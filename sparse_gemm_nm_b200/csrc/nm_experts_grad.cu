@@ -12,8 +12,8 @@
 // of values, whose selectors come from a table by the group's nibble.  dY's rows arrive by TMA beside it.
 //
 // experts_dv_kernel reduces over an expert's columns, which start and end anywhere.  Its stages of 128 columns start as the
-// tiles of nm_experts.cuh do; in a tile's first and last stage a warp of each CTA zeroes the columns outside the expert (of both
-// operands: a zero times a neighbour's Inf would be NaN) before the MMA may read them, and these stages issue only the
+// tiles of nm_experts.cuh do; in a tile's first and last stage two warps of each CTA zero the columns outside the expert (of
+// both operands: a zero times a neighbour's Inf would be NaN) before the MMA may read them, and these stages issue only the
 // MMAs (16 columns each) that hold columns of the expert.  An expert without columns has a gradient of zeros.
 #include <atomic>
 #include <cstdint>
@@ -256,9 +256,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(grpt::Cfg<FEW>::kThr
   } else if (warp >= 8) {
     // ----------------------------------------------------------- expansion
     // Four warps to a stage, two stages at a time (one group alone takes longer than a stage's MMAs; three or four groups
-    // are no faster: 135 us with few columns, 145 and 140).  A warp takes 16 rows: two words of metadata a lane, each of a row and its partner eight below.  Eight lanes
-    // take four 16-byte units of the values (a half of the columns) in two rows whose numbers differ by 5 in their bits: the
-    // swizzle then puts their units of values, and of weights (every other one of a strip), in different banks.
+    // are no faster: 135 us with few columns, 145 and 140).  A warp takes 16 rows: two words of metadata a lane, each of a
+    // row and its partner eight below.  Eight lanes take four 16-byte units of the values (a half of the columns) in two
+    // rows whose numbers differ by 5 in their bits: the swizzle then puts their units of values, and of weights (every other
+    // one of a strip), in different banks.
     const int q = (lane & 1) + 2 * ((lane >> 3) & 1), h = (lane >> 1) & 1, rb = warp & 3, mine = (warp - 8) >> 2;
     const int flip = (lane >> 2) & 1 ? 5 : 0, rlow = lane >> 4;
     const uint8_t* table = smem + C::kOffTable;
@@ -795,7 +796,8 @@ extern "C" nm_status nm_experts_spmm_t(const uint16_t* values, const uint32_t* m
   e = limit.raise(experts_t_kernel<false>, grpt::Cfg<false>::bytes(kMaxExperts));
   if (e != cudaSuccess) return cuda_fail(e, "grouped input gradient");
   const int pairs = experts_pairs(p, grpt::kWide);
-  e = launch_pdl(experts_t_kernel<false>, dim3(2 * pairs), dim3(grpt::Cfg<false>::kThreads), grpt::Cfg<false>::bytes(p.E), s, p);
+  e = launch_pdl(experts_t_kernel<false>, dim3(2 * pairs), dim3(grpt::Cfg<false>::kThreads),
+                 grpt::Cfg<false>::bytes(p.E), s, p);
   count_launch();
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "grouped input gradient launch");

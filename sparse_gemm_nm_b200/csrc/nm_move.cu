@@ -918,7 +918,8 @@ static uint32_t inverse(int64_t T) {
 }
 
 // Rows a word holds for rows of `cols` elements, beside `beside` bytes.  0: picked from global memory, where the row does not
-// fit, or where it is two lines of L1 and not worth a barrier, or gives a group of rows to few threads (13824 rows, one token at two experts: combine 61 -> 8 us).
+// fit, or where it is two lines of L1 and not worth a barrier, or gives a group of rows to few threads (13824 rows, one
+// token at two experts: combine 61 -> 8 us).
 static int rows_of_word(int64_t cols, int64_t cols_out, int64_t rows, int64_t beside) {
   const int64_t one = (cols + 1) / 2 * 4;  // bytes of a row
   if (cols <= 128 || cols_out <= 256) return 0;
@@ -1176,8 +1177,8 @@ extern "C" nm_status nm_experts_combine_grad(const uint16_t* dY, int64_t lddy, i
   }
   if (e == cudaSuccess) {
     const int64_t n = (int64_t)k * T, most_of = n > S ? n : S;
-    e = launch_pdl(mv::dgate_kernel, dim3((unsigned)((most_of + 31) / 32)), dim3(256), 0, s, (const float*)p.part, (int32_t)ctas,
-                   units * 8, source, slot, n, (int32_t)S, dgate);
+    e = launch_pdl(mv::dgate_kernel, dim3((unsigned)((most_of + 31) / 32)), dim3(256), 0, s, (const float*)p.part,
+                   (int32_t)ctas, units * 8, source, slot, n, (int32_t)S, dgate);
     count_launch();
     if (e == cudaSuccess) e = cudaGetLastError();
   }

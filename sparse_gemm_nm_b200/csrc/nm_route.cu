@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(kPlaceThreads, 4) place_kernel(const __grid_co
     uint32_t all = 0, before = 0;
     for (int i = lane; i < p.pitch / 16; i += 32) {  // bytes behind the last group are zero
       const uint4 u = __ldcg(reinterpret_cast<const uint4*>(row) + i);
-      const uint32_t n = __dp4a(u.x, 0x01010101u, __dp4a(u.y, 0x01010101u, __dp4a(u.z, 0x01010101u, __dp4a(u.w, 0x01010101u, 0u))));
+      const uint32_t n = __dp4a(u.x, 0x01010101u, __dp4a(u.y, 0x01010101u,
+                                __dp4a(u.z, 0x01010101u, __dp4a(u.w, 0x01010101u, 0u))));
       all += n;
       if (i < first / 16)
         before += n;
@@ -446,7 +447,8 @@ extern "C" nm_status nm_experts_route(const void* logits, int64_t ld, nm_out_dty
     if (e != cudaSuccess) return cuda_fail(e, "staging buffer for the experts' counts");
     p.counts = counts.as<uint8_t>();
   }
-  cudaError_t e = dtype == NM_OUT_F32 ? route::launch_route<float>(p, k, warps, s) : route::launch_route<uint16_t>(p, k, warps, s);
+  cudaError_t e = dtype == NM_OUT_F32 ? route::launch_route<float>(p, k, warps, s)
+                                      : route::launch_route<uint16_t>(p, k, warps, s);
   if (e == cudaSuccess && p.groups > 1) {
     static SmemLimit limit;
     e = limit.raise(route::place_kernel, 4u * (route::kMaxE * (route::kMaxChunk + 2) + 1));
